@@ -5,9 +5,10 @@ include/cpattn.h, with this thin PyTorch binding on top.
 The shared library is loaded on first use and must exist (built by
 ``__graft_entry__.build()``); there is no CPU fallback.
 """
-from .api import (CpattnError, grouped_as_bhsd, last_device_status, merge, partial,
-                  prepare_ring, prepare_ulysses_anything, prepare_unified, ring,
-                  ring_noalloc, ring_noalloc_max_workspace_bytes, ring_workspace_bytes,
+from .api import (CpattnError, cross_attention, cross_attention_backward,
+                  cross_backward_workspace_bytes, cross_workspace_bytes, grouped_as_bhsd, last_device_status,
+                  merge, partial, prepare_ring, prepare_ulysses_anything, prepare_unified, ring,
+                  ring_noalloc, ring_noalloc_max_workspace_bytes, ring_workspace_bytes, rotary,
                   set_wait_timeout_ns, ulysses_anything_attention, ulysses_anything_permute,
                   ulysses_anything_permute_batch, ulysses_attention, ulysses_permute,
                   ulysses_permute_batch, unified_attention)
@@ -19,4 +20,5 @@ __all__ = ["partial", "merge", "ring", "ring_workspace_bytes", "ring_noalloc", "
            "ulysses_attention", "ulysses_anything_permute", "ulysses_anything_attention",
            "ulysses_permute_batch", "ulysses_anything_permute_batch",
            "grouped_as_bhsd", "last_device_status", "set_wait_timeout_ns",
-           "CpattnError", "EXPORTS", "LIB_PATH", "load_library"]
+           "rotary", "cross_attention", "cross_attention_backward", "cross_workspace_bytes",
+           "cross_backward_workspace_bytes", "CpattnError", "EXPORTS", "LIB_PATH", "load_library"]

@@ -17,7 +17,7 @@ STATUS = {
     7: "CPATTN_ERR_WORKSPACE", 8: "CPATTN_ERR_CUDA", 9: "CPATTN_ERR_TIMEOUT",
     10: "CPATTN_ERR_BOUNDS",
 }
-F32, BF16 = 0, 1
+F32, BF16, I32 = 0, 1, 2
 
 # Every symbol include/cpattn.h declares.
 EXPORTS = (
@@ -27,6 +27,8 @@ EXPORTS = (
     "cpattn_set_fault_injection", "cpattn_ring_causal", "cpattn_ulysses_anything_permute",
     "cpattn_ulysses_anything_attention", "cpattn_ulysses_permute_batch",
     "cpattn_ulysses_anything_permute_batch", "cpattn_is_check_build", "cpattn_set_check_shrink",
+    "cpattn_rotary", "cpattn_cross_attention", "cpattn_cross_workspace_bytes",
+    "cpattn_cross_attention_backward", "cpattn_cross_backward_workspace_bytes",
 )
 
 
@@ -84,7 +86,17 @@ def bind(path: str):
     lib.cpattn_is_check_build.restype = ctypes.c_int
     lib.cpattn_set_check_shrink.argtypes = [ctypes.c_int64]
     lib.cpattn_set_check_shrink.restype = None
-    for name in ("cpattn_partial", "cpattn_merge", "cpattn_ring", "cpattn_ulysses_permute",
+    lib.cpattn_rotary.argtypes = [i32, P, P, i32, ctypes.POINTER(ctypes.c_int32), ctypes.c_double,
+                                  i32, i32, P, vp]
+    lib.cpattn_cross_attention.argtypes = [P, P, P, P, ctypes.c_float, P, P, vp, ctypes.c_size_t,
+                                           vp]
+    lib.cpattn_cross_attention_backward.argtypes = [P, P, P, P, P, P, P, ctypes.c_float, P, P, P,
+                                                    vp, ctypes.c_size_t, vp]
+    for name in ("cpattn_cross_workspace_bytes", "cpattn_cross_backward_workspace_bytes"):
+        getattr(lib, name).argtypes = [P, P]
+        getattr(lib, name).restype = ctypes.c_size_t
+    for name in ("cpattn_rotary", "cpattn_cross_attention", "cpattn_cross_attention_backward",
+                 "cpattn_partial", "cpattn_merge", "cpattn_ring", "cpattn_ulysses_permute",
                  "cpattn_last_device_status", "cpattn_ring_noalloc", "cpattn_ring_causal",
                  "cpattn_ulysses_anything_permute", "cpattn_ulysses_anything_attention",
                  "cpattn_ulysses_permute_batch", "cpattn_ulysses_anything_permute_batch"):

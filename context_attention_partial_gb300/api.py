@@ -8,7 +8,8 @@ kernels; CPU tensors are rejected (there is no CPU path).
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from contextlib import nullcontext
+from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -415,6 +416,160 @@ def prepare_ulysses_anything(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     return call
 
 
+def _on_device(ts, stream: Optional[torch.cuda.Stream]):
+    """Checks that a call's tensors share one CUDA device.  Returns (a context
+    in which that device is the current one, the stream to use, whether the
+    stream is another than the device's current one)."""
+    dev = ts[0].device
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("cpattn runs on CUDA tensors only (no CPU path)")
+        if t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device} in one call")
+    current = torch.cuda.current_stream(dev)
+    if stream is None:
+        stream = current
+    elif stream.device != dev:
+        raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
+    ctx = nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return ctx, stream, stream != current
+
+
+def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float = 10000.0,
+           interleaved: bool = True, inverse: bool = False, outs=None,
+           stream: Optional[torch.cuda.Stream] = None) -> Union[torch.Tensor, list]:
+    """Rotary positions with several axes (cpattn_rotary) on a tensor or up to
+    4 tensors [B,H_i,S,D] in one launch (q, and k with its own head count).
+    positions: f32 [S,A] or [B,S,A]; axes_dims: the features of each axis (even, sum
+    at most D, the rest is copied).  interleaved: pairs (2i, 2i+1) of an
+    axis' features, else (i, i + d/2).  inverse: turns back, which is also
+    the gradient.  outs may be xs (in place).  Returns a tensor for a tensor,
+    else a list."""
+    lib = _lib.load()
+    single = isinstance(xs, torch.Tensor)
+    if single:
+        xs, outs = [xs], None if outs is None else [outs]
+    ctx, s, other = _on_device([*xs, positions, *(o for o in outs or () if o is not None)], stream)
+    if positions.dtype != torch.float32:
+        raise TypeError(f"positions are float32, not {positions.dtype}")
+    outs = list(outs) if outs is not None else [None] * len(xs)
+    if len(outs) != len(xs):
+        raise ValueError(f"{len(xs)} tensors but {len(outs)} outputs")
+    made = []
+    for i, x in enumerate(xs):
+        if outs[i] is None:
+            outs[i] = torch.empty_like(x)   # (keeps a [B,S,H,D] tensor's order)
+            made.append(outs[i])
+    dims = (ctypes.c_int32 * max(1, len(axes_dims)))(*axes_dims)
+    with ctx:
+        check(lib.cpattn_rotary(len(xs), _descs(xs), _desc(positions), len(axes_dims), dims, float(theta),
+                                int(bool(interleaved)), int(bool(inverse)), _descs(outs),
+                                s.cuda_stream), "cpattn_rotary")
+    if other:
+        for t in made:
+            t.record_stream(s)
+    return outs[0] if single else outs
+
+
+def _desc_lengths(t: Optional[torch.Tensor]) -> Optional[_lib.CTensor]:
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise TypeError(f"kv_lengths are int32, not {t.dtype}")
+    return describe(t.data_ptr(), _lib.I32, t.shape, t.stride())
+
+
+def cross_workspace_bytes(q: torch.Tensor, k: torch.Tensor) -> int:
+    return int(_lib.load().cpattn_cross_workspace_bytes(describe(0, _code(q), q.shape, q.stride()),
+                                                        describe(0, _code(k), k.shape, k.stride())))
+
+
+def cross_backward_workspace_bytes(q: torch.Tensor, k: torch.Tensor) -> int:
+    return int(_lib.load().cpattn_cross_backward_workspace_bytes(
+        describe(0, _code(q), q.shape, q.stride()), describe(0, _code(k), k.shape, k.stride())))
+
+
+def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    kv_lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of q [B,H,S_q,D] to an encoder's states k, v [B,H_kv,S_kv,D]
+    (cpattn_cross_attention): H_kv divides H; kv_lengths (int32 [B]) gives each
+    sequence's valid keys, a sequence without any gives (0, -inf).
+    Returns (out [B,H,S_q,D] in q's dtype, lse f32 [B,H,S_q])."""
+    lib = _lib.load()
+    ctx, s, other = _on_device([t for t in (q, k, v, kv_lengths, out, lse, workspace) if t is not None],
+                               stream)
+    made = []
+    if out is None:
+        out = torch.empty_like(q)
+        made.append(out)
+    if lse is None:
+        lse = torch.empty(q.shape[:3], device=q.device, dtype=torch.float32)
+        made.append(lse)
+    dq, dk = _desc(q), _desc(k)
+    with ctx:
+        if workspace is None:
+            need = lib.cpattn_cross_workspace_bytes(dq, dk)
+            if need > 0:
+                workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+                made.append(workspace)
+        ws_ptr, ws_bytes = (None, 0) if workspace is None else (
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        check(lib.cpattn_cross_attention(dq, dk, _desc(v), _desc_lengths(kv_lengths), _scale(scale),
+                                         _desc(out), _desc(lse), ws_ptr, ws_bytes, s.cuda_stream),
+              "cpattn_cross_attention")
+    if other:
+        for t in made:
+            t.record_stream(s)
+    return out, lse
+
+
+def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                             lse: torch.Tensor, dout: torch.Tensor,
+                             kv_lengths: Optional[torch.Tensor] = None,
+                             scale: Optional[float] = None, dq: Optional[torch.Tensor] = None,
+                             dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None
+                             ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradient of ``cross_attention`` (cpattn_cross_attention_backward): out and
+    lse as it returned them, dout the gradient of out.  Returns (dq, dk, dv) in
+    the shapes and dtype of q, k, v; rows of dk and dv past a sequence's
+    length are 0."""
+    lib = _lib.load()
+    ctx, s, other = _on_device([t for t in (q, k, v, out, lse, dout, kv_lengths, dq, dk, dv, workspace)
+                                if t is not None], stream)
+    made = []
+    if dq is None:
+        dq = torch.empty_like(q)
+        made.append(dq)
+    if dk is None:
+        dk = torch.empty_like(k)
+        made.append(dk)
+    if dv is None:
+        dv = torch.empty_like(v)
+        made.append(dv)
+    tq, tk = _desc(q), _desc(k)
+    with ctx:
+        if workspace is None:
+            need = lib.cpattn_cross_backward_workspace_bytes(tq, tk)
+            if need > 0:
+                workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+                made.append(workspace)
+        ws_ptr, ws_bytes = (None, 0) if workspace is None else (
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        check(lib.cpattn_cross_attention_backward(
+            tq, tk, _desc(v), _desc(out), _desc(lse), _desc(dout), _desc_lengths(kv_lengths),
+            _scale(scale), _desc(dq), _desc(dk), _desc(dv), ws_ptr, ws_bytes, s.cuda_stream),
+            "cpattn_cross_attention_backward")
+    if other:
+        for t in made:
+            t.record_stream(s)
+    return dq, dk, dv
+
+
 def last_device_status(stream: Optional[torch.cuda.Stream] = None) -> int:
     """Synchronises the stream and returns (and clears) the device error word
     status: 0 = ok, 9 = a kernel-side wait timed out."""
@@ -429,4 +584,5 @@ __all__ = ["partial", "merge", "ring", "ring_workspace_bytes", "ring_noalloc", "
            "prepare_unified", "prepare_ulysses_anything",
            "ring_noalloc_max_workspace_bytes", "ulysses_permute", "unified_attention",
            "ulysses_attention", "grouped_as_bhsd", "last_device_status", "set_wait_timeout_ns",
-           "CpattnError"]
+           "rotary", "cross_attention", "cross_attention_backward", "cross_workspace_bytes",
+           "cross_backward_workspace_bytes", "CpattnError"]

@@ -16,6 +16,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "cross.cuh"
 #include "internal.h"
 
 namespace {
@@ -340,6 +341,121 @@ cpattn_status permute_batch(int n, const cpattn_tensor* x, int degree, int dir, 
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
+// layout_ok, and no extent above 1 walks on the spot (broadcast views).
+bool layout_distinct(const cpattn_tensor* t) {
+  if (!layout_ok(t)) return false;
+  for (int i = 0; i < t->ndim; ++i)
+    if (t->shape[i] > 1 && t->stride[i] <= 0) return false;
+  return true;
+}
+
+bool lse_layout_ok(const cpattn_tensor* t) {
+  if (reinterpret_cast<uintptr_t>(t->data) & 3u) return false;
+  for (int i = 0; i < 3; ++i)
+    if (t->shape[i] > 1 && t->stride[i] <= 0) return false;
+  return t->shape[2] <= 1 || t->stride[2] == 1;
+}
+
+bool same_shape(const cpattn_tensor* a, const cpattn_tensor* b, int ndim) {
+  for (int i = 0; i < ndim; ++i)
+    if (a->shape[i] != b->shape[i]) return false;
+  return true;
+}
+
+cpattn::CrossTensor cross_tensor(const cpattn_tensor* t, long long shrink = 0) {
+  return {t->data, {t->stride[0], t->stride[1], t->stride[2]}, {t->data, extent_bytes(t, shrink)}};
+}
+
+// q [B, H, S_q, D] against k [B, H_kv, S_kv, D]: types, shapes and sizes.
+cpattn_status cross_shape(const cpattn_tensor* q, const cpattn_tensor* k) {
+  if (!dtype_known(q->dtype) || k->dtype != q->dtype) return CPATTN_ERR_DTYPE;
+  if (!shape_ok(q, 4) || !shape_ok(k, 4)) return CPATTN_ERR_SHAPE;
+  if (q->shape[0] != k->shape[0] || q->shape[3] != k->shape[3]) return CPATTN_ERR_SHAPE;
+  const int64_t B = q->shape[0], H = q->shape[1], Hk = k->shape[1], D = q->shape[3];
+  if (H > 0 && Hk == 0) return CPATTN_ERR_SHAPE;
+  if (Hk > 0 && H % Hk != 0) return CPATTN_ERR_DIVISIBILITY;
+  if (D != 64 && D != 128) return CPATTN_ERR_UNSUPPORTED;
+  if (B > 65535 || H > 65535 || Hk > 65535 || q->shape[2] > (int64_t(1) << 30) ||
+      k->shape[2] > (int64_t(1) << 30))
+    return CPATTN_ERR_UNSUPPORTED;
+  return CPATTN_OK;
+}
+
+// Parts of the key axis of a forward call: 1 where the query rows fill the
+// GPU, else as many as give each SM a block, each with four key tiles or more.
+int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
+  const int64_t bh = q->shape[0] * q->shape[1], sm = cpattn::sm_count();
+  const int64_t blocks = ((q->shape[2] + 63) / 64) * bh >= sm ? sm : ((q->shape[2] + 1) / 2) * bh;
+  if (blocks >= sm || blocks == 0) return 1;
+  const int64_t most = (k->shape[2] + 511) / 512, want = (sm + blocks - 1) / blocks;
+  const int64_t s = want < most ? want : most;
+  return s > 1 ? static_cast<int>(s) : 1;
+}
+
+size_t cross_workspace(const cpattn_tensor* q, const cpattn_tensor* k) {
+  const int64_t rows = q->shape[0] * q->shape[1] * q->shape[2];
+  const int splits = cross_splits(q, k);
+  return splits > 1 && rows > 0 ? static_cast<size_t>(splits) * rows * (q->shape[3] + 1) * 4 : 0;
+}
+
+size_t cross_backward_workspace(const cpattn_tensor* q, const cpattn_tensor*) {
+  return static_cast<size_t>(q->shape[0] * q->shape[1] * q->shape[2]) * 4;
+}
+
+// What both directions check and fill in; *run stays false where q has no row.
+cpattn_status cross_common(const cpattn_tensor* q, const cpattn_tensor* k, const cpattn_tensor* v,
+                           const cpattn_tensor* out, const cpattn_tensor* lse,
+                           const cpattn_tensor* lengths, float scale, cpattn::CrossParams* p) {
+  if (!q || !k || !v || !out || !lse) return CPATTN_ERR_NULL;
+  if (v->dtype != q->dtype || out->dtype != q->dtype || lse->dtype != CPATTN_F32) return CPATTN_ERR_DTYPE;
+  if (lengths && lengths->dtype != CPATTN_I32) return CPATTN_ERR_DTYPE;
+  if (!shape_ok(v, 4) || !shape_ok(out, 4) || !shape_ok(lse, 3)) return CPATTN_ERR_SHAPE;
+  if (lengths && (!shape_ok(lengths, 1) || lengths->shape[0] != q->shape[0])) return CPATTN_ERR_SHAPE;
+  const cpattn_status st = cross_shape(q, k);
+  if (st != CPATTN_OK) return st;
+  if (!same_shape(v, k, 4) || !same_shape(out, q, 4) || !same_shape(lse, q, 3)) return CPATTN_ERR_SHAPE;
+  const bool rows = q->shape[0] * q->shape[1] * q->shape[2] > 0;
+  const bool keys = k->shape[0] * k->shape[1] * k->shape[2] > 0;
+  if (rows && (!q->data || !out->data || !lse->data)) return CPATTN_ERR_NULL;
+  if (keys && (!k->data || !v->data)) return CPATTN_ERR_NULL;
+  if (lengths && q->shape[0] > 0 && !lengths->data) return CPATTN_ERR_NULL;
+  if (rows && (!layout_distinct(q) || !layout_distinct(out) || !lse_layout_ok(lse))) return CPATTN_ERR_LAYOUT;
+  if (keys && (!layout_distinct(k) || !layout_distinct(v))) return CPATTN_ERR_LAYOUT;
+  if (lengths && ((lengths->shape[0] > 1 && lengths->stride[0] != 1) ||
+                  (reinterpret_cast<uintptr_t>(lengths->data) & 3u)))
+    return CPATTN_ERR_LAYOUT;
+  std::memset(p, 0, sizeof(*p));
+  p->q = cross_tensor(q);
+  p->k = cross_tensor(k);
+  p->v = cross_tensor(v);
+  p->out = cross_tensor(out);
+  p->lse = cross_tensor(lse);
+  if (lengths) {
+    p->lengths = static_cast<const int32_t*>(lengths->data);
+    p->lengths_span = {lengths->data, extent_bytes(lengths)};
+  }
+  p->batch = static_cast<int>(q->shape[0]);
+  p->heads = static_cast<int>(q->shape[1]);
+  p->kv_heads = static_cast<int>(k->shape[1]);
+  p->s_q = static_cast<int>(q->shape[2]);
+  p->s_kv = static_cast<int>(k->shape[2]);
+  if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt(static_cast<float>(q->shape[3]));
+  p->scale = scale;
+  p->scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p->timeout_ns = g_timeout_ns.load();
+  p->fault_skip_kv = g_fault_skip_kv.load();
+  p->err = cpattn::device_error_word();
+  return CPATTN_OK;
+}
+
+cpattn_status cross_workspace_ok(void* workspace, size_t bytes, size_t need, cpattn::CrossParams* p) {
+  if (need > 0 && (workspace == nullptr || bytes < need || !aligned16(workspace))) return CPATTN_ERR_WORKSPACE;
+  const size_t shrink = static_cast<size_t>(g_check_shrink.load());
+  p->ws = static_cast<float*>(workspace);
+  p->ws_span = {workspace, need > shrink ? need - shrink : 0};
+  return CPATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -485,6 +601,180 @@ cpattn_status cpattn_ulysses_anything_attention(const cpattn_tensor* q, const cp
   vl.shape[3] = vl.shape[4] = 0; vl.stride[3] = vl.stride[4] = 0;
   return run_attention(&vq, &vk, &vv, scale, 1, 0, &vo, &vl, nullptr, 0, false, is_causal != 0,
                        static_cast<cudaStream_t>(stream), static_cast<int>(G), heads);
+}
+
+cpattn_status cpattn_rotary(int n, const cpattn_tensor* x, const cpattn_tensor* positions, int axes,
+                            const int32_t* axis_dims, double theta, int interleaved, int inverse,
+                            cpattn_tensor* y, void* stream) {
+  if (n < 1 || n > cpattn::kMaxPermuteBatch) return CPATTN_ERR_SHAPE;
+  if (!x || !y || !positions || !axis_dims) return CPATTN_ERR_NULL;
+  if (positions->dtype != CPATTN_F32 || !dtype_known(x[0].dtype)) return CPATTN_ERR_DTYPE;
+  for (int i = 0; i < n; ++i)
+    if (x[i].dtype != x[0].dtype || y[i].dtype != x[0].dtype) return CPATTN_ERR_DTYPE;
+  if (axes < 1 || axes > CPATTN_MAX_ROTARY_AXES) return CPATTN_ERR_SHAPE;
+  for (int i = 0; i < n; ++i) {
+    if (!shape_ok(&x[i], 4) || !shape_ok(&y[i], 4) || !same_shape(&x[i], &y[i], 4)) return CPATTN_ERR_SHAPE;
+    if (x[i].shape[0] != x[0].shape[0] || x[i].shape[2] != x[0].shape[2] || x[i].shape[3] != x[0].shape[3])
+      return CPATTN_ERR_SHAPE;
+  }
+  const int64_t B = x[0].shape[0], S = x[0].shape[2], D = x[0].shape[3];
+  const bool per_batch = positions->ndim == 3;
+  if (!shape_ok(positions, per_batch ? 3 : 2)) return CPATTN_ERR_SHAPE;
+  const int pa = per_batch ? 2 : 1;   // the axis dimension of positions
+  if (positions->shape[pa] != axes || positions->shape[pa - 1] != S || (per_batch && positions->shape[0] != B))
+    return CPATTN_ERR_SHAPE;
+  int64_t turned = 0;
+  for (int a = 0; a < axes; ++a) {
+    if (axis_dims[a] < 2 || axis_dims[a] % 2 != 0) return CPATTN_ERR_SHAPE;
+    turned += axis_dims[a];
+  }
+  if (turned > D) return CPATTN_ERR_SHAPE;
+  if (D > CPATTN_MAX_ROTARY_DIM || (D * elem_bytes(x[0].dtype)) % 16 != 0) return CPATTN_ERR_UNSUPPORTED;
+  int64_t heads = 0;
+  for (int i = 0; i < n; ++i) {
+    if (x[i].shape[1] > 65535) return CPATTN_ERR_UNSUPPORTED;
+    heads += x[i].shape[1];
+  }
+  if (B > 65535 || S > (int64_t(1) << 30)) return CPATTN_ERR_UNSUPPORTED;
+  if (B * S * heads == 0) return CPATTN_OK;
+  if (!positions->data) return CPATTN_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(positions->data) & 3u) return CPATTN_ERR_LAYOUT;
+  for (int i = 0; i < positions->ndim; ++i)
+    if (positions->stride[i] < 0) return CPATTN_ERR_LAYOUT;
+
+  cpattn::RotaryParams p;
+  std::memset(&p, 0, sizeof(p));
+  const long long shrink = g_check_shrink.load();
+  bool token_inner = true;
+  for (int i = 0; i < n; ++i) {
+    const bool none = x[i].shape[1] == 0;
+    if (!none && (!x[i].data || !y[i].data)) return CPATTN_ERR_NULL;
+    if (!none && (!layout_ok(&x[i]) || !layout_distinct(&y[i]))) return CPATTN_ERR_LAYOUT;
+    if (!none && x[i].data == y[i].data)   // in place: element for element
+      for (int j = 0; j < 4; ++j)
+        if (x[i].shape[j] > 1 && x[i].stride[j] != y[i].stride[j]) return CPATTN_ERR_LAYOUT;
+    p.x[i] = x[i].data;
+    p.y[i] = y[i].data;
+    p.x_sb[i] = x[i].stride[0];
+    p.x_sh[i] = x[i].stride[1];
+    p.x_ss[i] = x[i].stride[2];
+    p.y_sb[i] = y[i].stride[0];
+    p.y_sh[i] = y[i].stride[1];
+    p.y_ss[i] = y[i].stride[2];
+    p.head_start[i + 1] = p.head_start[i] + static_cast<int>(x[i].shape[1]);
+    p.x_span[i] = {x[i].data, extent_bytes(&x[i])};
+    p.y_span[i] = {y[i].data, extent_bytes(&y[i], shrink)};
+    if (!none && x[i].shape[1] > 1 && x[i].stride[1] < x[i].stride[2]) token_inner = false;
+  }
+  p.n = n;
+  p.batch = static_cast<int>(B);
+  p.seq = static_cast<int>(S);
+  p.head_dim = static_cast<int>(D);
+  p.pos = static_cast<const float*>(positions->data);
+  p.pos_sb = per_batch ? positions->stride[0] : 0;
+  p.pos_ss = positions->stride[pa - 1];
+  p.pos_sa = positions->stride[pa];
+  p.pos_span = {positions->data, extent_bytes(positions)};
+  p.axes = axes;
+  p.interleaved = interleaved != 0;
+  p.inverse = inverse != 0;
+  p.token_inner = token_inner ? 1 : 0;
+  p.err = cpattn::device_error_word();
+  if (!(theta > 0.0) || !std::isfinite(theta)) theta = 10000.0;
+  int j = 0;
+  for (int a = 0; a < axes; ++a) {
+    p.axis_dim[a] = axis_dims[a];
+    p.pair_start[a] = j;
+    // theta^(-2i/d) / 2 pi by repeated products: relative error below
+    // 128 * 2^-53, far under the 2^-48 that hi + lo keep
+    const double step = std::exp(-2.0 / axis_dims[a] * std::log(theta));
+    double f = 0.15915494309189535;
+    for (int i = 0; i < axis_dims[a] / 2; ++i, f *= step) {
+      const float hi = static_cast<float>(f);
+      p.freq[j++] = make_float2(hi, static_cast<float>(f - hi));
+    }
+  }
+  p.rotary_pairs = j;
+  const InDtype dt = x[0].dtype == CPATTN_BF16 ? InDtype::BF16 : InDtype::F32;
+  return cpattn::launch_rotary(dt, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CPATTN_OK
+                                                                                       : CPATTN_ERR_CUDA;
+}
+
+size_t cpattn_cross_workspace_bytes(const cpattn_tensor* q, const cpattn_tensor* k) {
+  return q && k && cross_shape(q, k) == CPATTN_OK ? cross_workspace(q, k) : 0;
+}
+
+size_t cpattn_cross_backward_workspace_bytes(const cpattn_tensor* q, const cpattn_tensor* k) {
+  return q && k && cross_shape(q, k) == CPATTN_OK ? cross_backward_workspace(q, k) : 0;
+}
+
+cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor* k,
+                                     const cpattn_tensor* v, const cpattn_tensor* kv_lengths,
+                                     float scale, cpattn_tensor* out, cpattn_tensor* lse,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  cpattn::CrossParams p;
+  cpattn_status st = cross_common(q, k, v, out, lse, kv_lengths, scale, &p);
+  if (st != CPATTN_OK) return st;
+  if (q->shape[0] * q->shape[1] * q->shape[2] == 0) return CPATTN_OK;
+  const size_t need = cross_workspace(q, k);
+  if ((st = cross_workspace_ok(workspace, workspace_bytes, need, &p)) != CPATTN_OK) return st;
+  const long long shrink = g_check_shrink.load();
+  p.out = cross_tensor(out, shrink);
+  p.lse = cross_tensor(lse, shrink);
+  const InDtype dt = q->dtype == CPATTN_BF16 ? InDtype::BF16 : InDtype::F32;
+  const int D = static_cast<int>(q->shape[3]);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  p.splits = p.s_kv > 0 ? cross_splits(q, k) : 0;
+  if (p.splits > 0) e = cpattn::launch_cross_simt(dt, D, p, cs);
+  // (no parts: the join writes the empty result)
+  if (e == cudaSuccess && p.splits != 1) e = cpattn::launch_cross_join(dt, D, p, cs);
+  return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
+}
+
+cpattn_status cpattn_cross_attention_backward(const cpattn_tensor* q, const cpattn_tensor* k,
+                                              const cpattn_tensor* v, const cpattn_tensor* out,
+                                              const cpattn_tensor* lse, const cpattn_tensor* dout,
+                                              const cpattn_tensor* kv_lengths, float scale,
+                                              cpattn_tensor* dq, cpattn_tensor* dk,
+                                              cpattn_tensor* dv, void* workspace,
+                                              size_t workspace_bytes, void* stream) {
+  if (!dout || !dq || !dk || !dv) return CPATTN_ERR_NULL;
+  cpattn::CrossParams p;
+  cpattn_status st = cross_common(q, k, v, out, lse, kv_lengths, scale, &p);
+  if (st != CPATTN_OK) return st;
+  const cpattn_tensor* rows4[2] = {dout, dq};
+  const cpattn_tensor* keys4[2] = {dk, dv};
+  const bool rows = q->shape[0] * q->shape[1] * q->shape[2] > 0;
+  const bool keys = k->shape[0] * k->shape[1] * k->shape[2] > 0;
+  for (const cpattn_tensor* t : rows4) {
+    if (t->dtype != q->dtype) return CPATTN_ERR_DTYPE;
+    if (!shape_ok(t, 4) || !same_shape(t, q, 4)) return CPATTN_ERR_SHAPE;
+    if (rows && !t->data) return CPATTN_ERR_NULL;
+    if (rows && !layout_distinct(t)) return CPATTN_ERR_LAYOUT;
+  }
+  for (const cpattn_tensor* t : keys4) {
+    if (t->dtype != q->dtype) return CPATTN_ERR_DTYPE;
+    if (!shape_ok(t, 4) || !same_shape(t, k, 4)) return CPATTN_ERR_SHAPE;
+    if (keys && !t->data) return CPATTN_ERR_NULL;
+    if (keys && !layout_distinct(t)) return CPATTN_ERR_LAYOUT;
+  }
+  if (!rows && !keys) return CPATTN_OK;
+  const size_t need = cross_backward_workspace(q, k);
+  if ((st = cross_workspace_ok(workspace, workspace_bytes, need, &p)) != CPATTN_OK) return st;
+  const long long shrink = g_check_shrink.load();
+  p.dout = cross_tensor(dout);
+  p.dq = cross_tensor(dq, shrink);
+  p.dk = cross_tensor(dk, shrink);
+  p.dv = cross_tensor(dv, shrink);
+  p.splits = 1;
+  const InDtype dt = q->dtype == CPATTN_BF16 ? InDtype::BF16 : InDtype::F32;
+  const int D = static_cast<int>(q->shape[3]);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (rows) e = cpattn::launch_cross_delta(dt, D, p, cs);
+  if (e == cudaSuccess) e = cpattn::launch_cross_simt_backward(dt, D, p, cs);
+  return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 
 const char* cpattn_status_string(cpattn_status status) {

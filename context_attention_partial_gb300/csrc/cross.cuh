@@ -1,0 +1,48 @@
+// cross.cuh -- parameters of the cross-attention kernels and what they share
+// (not part of the public ABI).
+#pragma once
+#include "internal.h"
+
+namespace cpattn {
+
+// A [B, H, S, D] (or, for lse, [B, H, S]) tensor: strides (b, h, s) in elements.
+struct CrossTensor {
+  void* data;
+  int64_t s[3];
+  Span span;   // (CPATTN_CHECK builds)
+};
+
+struct CrossParams {
+  CrossTensor q, k, v, out, lse;
+  CrossTensor dout, dq, dk, dv;      // backward
+  const int32_t* lengths;            // [B] valid keys, or nullptr: s_kv everywhere
+  Span lengths_span;
+  float* ws;                         // workspace (see the launches)
+  Span ws_span;
+  int batch, heads, kv_heads, s_q, s_kv;
+  float scale, scale_log2;           // softmax scale, and times log2(e)
+  int splits;                        // forward: parts of the key axis (1: no join)
+                                     // backward: parts of the query axis for dk, dv
+  unsigned long long timeout_ns;
+  int fault_skip_kv;                 // testing: the producer issues no copies
+  unsigned int* err;                 // device error word
+};
+
+// Valid keys of batch b: the given length, brought into [0, s_kv].
+__device__ __forceinline__ int cross_length(const CrossParams& p, int b) {
+  if (p.lengths == nullptr) return p.s_kv;
+  const int32_t* at = p.lengths + b;
+  const int n = CPATTN_IN(p.lengths_span, at, 4, p.err) ? *at : 0;
+  return max(0, min(n, p.s_kv));
+}
+
+// fp32 inputs (D 64 or 128).
+cudaError_t launch_cross_simt(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream);
+cudaError_t launch_cross_simt_backward(InDtype dt, int head_dim, const CrossParams& p,
+                                       cudaStream_t stream);
+// ws_delta[b][h][i] = sum_d dout o (the row term of the softmax's gradient)
+cudaError_t launch_cross_delta(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream);
+// joins p.splits partial outputs of the workspace into out and lse
+cudaError_t launch_cross_join(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream);
+
+}  // namespace cpattn

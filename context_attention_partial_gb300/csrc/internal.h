@@ -87,6 +87,30 @@ cudaError_t launch_permute(const PermuteParams& p, cudaStream_t stream);
 // (heads = H; H need not divide by G).
 cudaError_t launch_permute_anything(const PermuteParams& p, cudaStream_t stream);
 
+// Rotary positions on up to kMaxPermuteBatch tensors x[i] -> y[i] of one
+// dtype, batch, sequence and head size (head counts may differ).
+struct RotaryParams {
+  int n;
+  const void* x[kMaxPermuteBatch];
+  void* y[kMaxPermuteBatch];
+  int64_t x_sb[kMaxPermuteBatch], x_sh[kMaxPermuteBatch], x_ss[kMaxPermuteBatch];   // elements
+  int64_t y_sb[kMaxPermuteBatch], y_sh[kMaxPermuteBatch], y_ss[kMaxPermuteBatch];
+  int head_start[kMaxPermuteBatch + 1];   // first head of tensor i in the count over all tensors
+  int batch, seq, head_dim;
+  const float* pos;
+  int64_t pos_sb, pos_ss, pos_sa;
+  int axes;
+  int axis_dim[CPATTN_MAX_ROTARY_AXES];
+  int pair_start[CPATTN_MAX_ROTARY_AXES];
+  int rotary_pairs;        // pairs that turn (the rest of the features is copied)
+  int interleaved, inverse;
+  int token_inner;         // walk order of a block's rows: tokens or heads innermost
+  float2 freq[CPATTN_MAX_ROTARY_DIM / 2];   // turns per position, hi + lo
+  Span x_span[kMaxPermuteBatch], y_span[kMaxPermuteBatch], pos_span;   // (CPATTN_CHECK builds)
+  unsigned int* err;
+};
+cudaError_t launch_rotary(InDtype dt, const RotaryParams& p, cudaStream_t stream);
+
 // Error word helpers (defined with the device symbol).
 cudaError_t read_and_clear_device_error(unsigned int* value, cudaStream_t stream);
 // Device address of the error word on the current device (nullptr on

@@ -65,7 +65,8 @@ typedef enum {
   CPATTN_ERR_BOUNDS = 10        /* a device-side bounds check failed (check builds only) */
 } cpattn_status;
 
-typedef enum { CPATTN_F32 = 0, CPATTN_BF16 = 1 } cpattn_dtype;
+/* CPATTN_I32 is the type of kv_lengths only. */
+typedef enum { CPATTN_F32 = 0, CPATTN_BF16 = 1, CPATTN_I32 = 2 } cpattn_dtype;
 
 #define CPATTN_MAX_DIMS 5
 #define CPATTN_MAX_RING_DEGREE 64
@@ -264,6 +265,87 @@ cpattn_status cpattn_ring_noalloc(const cpattn_tensor* q, const cpattn_tensor* k
 
 /* Size of the fixed workspace array of cpattn_ring_noalloc, in bytes. */
 size_t cpattn_ring_noalloc_max_workspace_bytes(void);
+
+#define CPATTN_MAX_ROTARY_AXES 4
+#define CPATTN_MAX_ROTARY_DIM 256
+
+/*
+ * cpattn_rotary -- rotary positions with several axes (time, height, width)
+ * on queries and keys, in one launch, before any of the attentions above; and
+ * its gradient.
+ *   x, y: arrays of n descriptors, 1 <= n <= CPATTN_MAX_PERMUTE_BATCH;
+ *     x[i], y[i] [B, H_i, S, D], bf16 or f32, of one dtype, B, S and D; head
+ *     counts may differ (queries, and keys of shared heads).  Any strides that
+ *     the conventions above allow, so a [B, S, H, D] tensor is given as its
+ *     [B, H, S, D] view.  D <= CPATTN_MAX_ROTARY_DIM, rows whole 16-byte
+ *     vectors (D % 8 == 0 for bf16, D % 4 for f32; else CPATTN_ERR_UNSUPPORTED).
+ *   positions f32 [S, axes] or [B, S, axes], any non-negative strides.
+ *   axes, axis_dims: 1 <= axes <= CPATTN_MAX_ROTARY_AXES; axis a owns the
+ *     next axis_dims[a] features (even, >= 2); their sum is at most D and
+ *     features past it are copied.  (Host array.)
+ *   theta: pair i of axis a turns by positions[.., a] * theta^(-2 i / axis_dims[a])
+ *     radians; theta <= 0 or NaN selects 10000.
+ *   interleaved: 1 pairs features (2i, 2i + 1) of the axis' block, 0 pairs
+ *     (i, i + axis_dims[a] / 2).
+ *   inverse: 0, or 1 for the turn by the negative angle: the gradient with
+ *     respect to x, and the way back.
+ * Angles are formed in two-float arithmetic: exact to fp32 at any position
+ * that fp32 holds exactly.  y[i] may be x[i] itself (same data and strides);
+ * otherwise no element of an output may be an element of another buffer of
+ * the call.  B, S or every H_i = 0 is a no-op.
+ */
+cpattn_status cpattn_rotary(int n, const cpattn_tensor* x, const cpattn_tensor* positions, int axes,
+                            const int32_t* axis_dims, double theta, int interleaved, int inverse,
+                            cpattn_tensor* y, void* stream);
+
+/*
+ * cpattn_cross_attention -- attention of q to an encoder's states of another
+ * length:
+ *   out = softmax(scale q k^T) v over the first kv_lengths[b] keys, lse its
+ *   natural log-sum-exp; a sequence without keys gives (0, -inf), the identity
+ *   of cpattn_merge.
+ *   q [B, H, S_q, D], k, v [B, H_kv, S_kv, D]: bf16 or f32, D = 64 or 128;
+ *     H % H_kv == 0 (else CPATTN_ERR_DIVISIBILITY): query heads h_kv * H / H_kv
+ *     and following share key head h_kv.  S_kv may be 0.
+ *   kv_lengths: NULL (every key is valid) or i32 [B] on the device, contiguous;
+ *     values are brought into [0, S_kv].  Keys and values past a length are not
+ *     used and may hold anything, NaN included.
+ *   out [B, H, S_q, D] same dtype as q; lse [B, H, S_q] f32.
+ *   workspace: at least cpattn_cross_workspace_bytes(q, k) bytes, 16-byte
+ *     aligned, NULL if that is 0: partial outputs of a key axis that is split
+ *     (few queries) and joined.  Calls that may overlap need their own.
+ * fp32 inputs are computed in fp32 (no tf32 rounding).  Strides of extents
+ * above 1 must be positive; outputs may not overlap any other buffer.
+ * B * H * S_q = 0 is a no-op.
+ */
+cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor* k,
+                                     const cpattn_tensor* v, const cpattn_tensor* kv_lengths,
+                                     float scale, cpattn_tensor* out, cpattn_tensor* lse,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+/* 0 also for a descriptor that the call would refuse. */
+size_t cpattn_cross_workspace_bytes(const cpattn_tensor* q, const cpattn_tensor* k);
+
+/*
+ * cpattn_cross_attention_backward -- the gradient of cpattn_cross_attention:
+ *   out, lse: what the forward call wrote for these q, k, v, kv_lengths, scale;
+ *   dout [B, H, S_q, D]: the gradient of out, q's dtype;
+ *   dq [B, H, S_q, D], dk, dv [B, H_kv, S_kv, D]: written, q's dtype.  dk and
+ *     dv sum over the query heads that share a key head; rows past a sequence's
+ *     length get 0, and dq is 0 for a sequence without keys.
+ * Every sum has one owner and a fixed order: equal calls give equal bits.
+ *   workspace: at least cpattn_cross_backward_workspace_bytes(q, k) bytes,
+ *     16-byte aligned.
+ * Other arguments, layouts and errors as cpattn_cross_attention.  S_q = 0
+ * writes zeros to dk and dv, S_kv = 0 zeros to dq.
+ */
+cpattn_status cpattn_cross_attention_backward(const cpattn_tensor* q, const cpattn_tensor* k,
+                                              const cpattn_tensor* v, const cpattn_tensor* out,
+                                              const cpattn_tensor* lse, const cpattn_tensor* dout,
+                                              const cpattn_tensor* kv_lengths, float scale,
+                                              cpattn_tensor* dq, cpattn_tensor* dk,
+                                              cpattn_tensor* dv, void* workspace,
+                                              size_t workspace_bytes, void* stream);
+size_t cpattn_cross_backward_workspace_bytes(const cpattn_tensor* q, const cpattn_tensor* k);
 
 /* Human-readable name of a status code (static storage). */
 const char* cpattn_status_string(cpattn_status status);
