@@ -382,12 +382,17 @@ cpattn_status cross_shape(const cpattn_tensor* q, const cpattn_tensor* k) {
 }
 
 // Parts of the key axis of a forward call: 1 where the query rows fill the
-// GPU, else as many as give each SM a block, each with four key tiles or more.
+// GPU, else as many as give each SM a unit of work (bf16: 256 query rows of a
+// head, parts of four 128-key tiles or more; fp32: 2 rows, 512 keys or more).
 int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
   const int64_t bh = q->shape[0] * q->shape[1], sm = cpattn::sm_count();
-  const int64_t blocks = ((q->shape[2] + 63) / 64) * bh >= sm ? sm : ((q->shape[2] + 1) / 2) * bh;
-  if (blocks >= sm || blocks == 0) return 1;
-  const int64_t most = (k->shape[2] + 511) / 512, want = (sm + blocks - 1) / blocks;
+  int64_t units;
+  if (q->dtype == CPATTN_BF16)
+    units = (q->shape[2] + 255) / 256 * bh;
+  else
+    units = (q->shape[2] + 63) / 64 * bh >= sm ? sm : (q->shape[2] + 1) / 2 * bh;
+  if (units >= sm || units == 0) return 1;
+  const int64_t most = (k->shape[2] + 511) / 512, want = sm / units;
   const int64_t s = want < most ? want : most;
   return s > 1 ? static_cast<int>(s) : 1;
 }
@@ -726,7 +731,15 @@ cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   p.splits = p.s_kv > 0 ? cross_splits(q, k) : 0;
-  if (p.splits > 0) e = cpattn::launch_cross_simt(dt, D, p, cs);
+  if (p.splits > 0 && dt == InDtype::BF16) {
+    CUtensorMap tm_q, tm_k, tm_v;
+    if ((st = make_tmap(&tm_q, q, 128)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&tm_k, k, 128)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&tm_v, v, 128)) != CPATTN_OK) return st;
+    e = cpattn::launch_cross_fwd(D, tm_q, tm_k, tm_v, p, cs);
+  } else if (p.splits > 0) {
+    e = cpattn::launch_cross_simt(dt, D, p, cs);
+  }
   // (no parts: the join writes the empty result)
   if (e == cudaSuccess && p.splits != 1) e = cpattn::launch_cross_join(dt, D, p, cs);
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;

@@ -36,6 +36,10 @@ __device__ __forceinline__ int cross_length(const CrossParams& p, int b) {
   return max(0, min(n, p.s_kv));
 }
 
+// bf16 inputs, D 64 or 128, on the tensor cores (s_kv >= 1; the maps' boxes
+// have 128 rows).
+cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                             const CUtensorMap& tm_v, const CrossParams& p, cudaStream_t stream);
 // fp32 inputs (D 64 or 128).
 cudaError_t launch_cross_simt(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream);
 cudaError_t launch_cross_simt_backward(InDtype dt, int head_dim, const CrossParams& p,

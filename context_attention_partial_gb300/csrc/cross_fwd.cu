@@ -1,0 +1,478 @@
+// cross_fwd.cu -- cross attention of bf16 inputs on the tensor cores.
+//
+// Mathematics: per query row, over the first n = length[b] keys,
+//     m = max_j scale s_j,  P_j = 2^(scale log2e s_j - m),  l = sum_j P_j,
+//     o = sum_j P_j v_j / l,  lse = m ln2 + ln l,
+// one pass over the keys with the running m and l (fp32).  P is rounded to
+// bf16 for its product with V (the tensor cores' operand type; l keeps the
+// fp32 values), and the output once.
+//
+// What bounds it: an encoder's states are short (some 64 to 512 keys), so a
+// unit of work -- 256 query rows of one head against its keys -- is only a
+// few 128-key tiles, 1024 tensor-core cycles per query tile each, and the
+// time to start and finish a unit weighs as much.  The kernel is therefore
+// persistent, one CTA per SM walking units u, u + gridDim.x, ...: the next
+// unit's queries and keys are fetched and its first Q K^T issued while this
+// unit's last softmax, P V and output are under way.
+//
+// Roles (12 warps): warps 0-7 softmax and output, a warpgroup per 128-row
+// query tile and one thread per row; warp 8 TMA producer; warp 9 MMA issuer;
+// warps 10-11 only give up their registers.  TMEM: S_0 | S_1 | O_0 | O_1,
+// P over S's first columns.  Shared memory: the two Q tiles, a ring of K / V
+// tiles, and an output staging area per softmax warp.
+//
+// Keys past a length share their tile with valid ones: their scores are
+// masked in registers, and their V rows are overwritten with zeros in shared
+// memory before P V reads them (0 * NaN would not be 0).
+// A unit may also be one part of the key axis (few queries): its normalised
+// fp32 output and lse go to the workspace and are joined by a second kernel.
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <cmath>
+
+#include "cross.cuh"
+#include "ptx.cuh"
+#include "tile_ops.cuh"
+#include "tmem_ops.cuh"
+
+namespace cpattn {
+namespace {
+
+constexpr int kBM = 128, kBN = 128;
+constexpr int kThreads = 384;
+constexpr int kWarpProducer = 8, kWarpMma = 9;
+constexpr int kLaunchRegs = 168;    // 65536 / 384, rounded down to 8
+constexpr int kSoftmaxRegs = 208, kControlRegs = 88;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr unsigned kErrProducer = 1u, kErrMma = 2u, kErrSoftmax = 4u;
+
+template <int D>
+struct Cfg {
+  static constexpr int ROW = D * 2;                       // bytes
+  static constexpr int NKB = ROW / 128;                   // 128-byte column blocks
+  static constexpr int TILE = kBM * ROW;                  // bytes of a Q, K or V tile
+  static constexpr int STAGES = D == 128 ? 4 : 8;
+  static constexpr int STAGING = 8 * 32 * 128;            // 32 rows x 64 columns bf16 per warp
+  static constexpr int BARS = 2 * STAGES + 11;
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + STAGING + BARS * 8 + 16;
+  static constexpr int QK = ROW / 32, PV = kBN / 16;      // MMAs of a tile product
+  static constexpr int O_COL = 2 * kBN;
+  static constexpr uint32_t IDESC_QK = make_idesc(1, false, kBM, kBN);
+  static constexpr uint32_t IDESC_PV = make_idesc(1, true, kBM, D);
+  static_assert(O_COL + 2 * D <= 512, "TMEM");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct Unit {
+  int b, h, q0, part;      // batch, head, first query row, part of the key axis
+  int k0, k1;              // its keys
+  int tiles, halves;       // key tiles, query tiles with rows
+};
+
+__device__ __forceinline__ Unit unit_at(const CrossParams& p, int64_t u) {
+  const int q_blocks = ceil_div(p.s_q, 2 * kBM);
+  Unit w;
+  w.q0 = static_cast<int>(u % q_blocks) * (2 * kBM);
+  u /= q_blocks;
+  w.part = static_cast<int>(u % p.splits);
+  u /= p.splits;
+  w.h = static_cast<int>(u % p.heads);
+  w.b = static_cast<int>(u / p.heads);
+  const int len = cross_length(p, w.b);
+  const int all = ceil_div(len, kBN), per = ceil_div(all, p.splits);
+  const int t0 = min(w.part * per, all), t1 = min(t0 + per, all);
+  w.k0 = t0 * kBN;
+  w.k1 = min(t1 * kBN, len);
+  w.tiles = t1 - t0;
+  w.halves = p.s_q - w.q0 > kBM ? 2 : 1;
+  return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CrossParams p,
+                     const int64_t units) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sQ = smem_addr(smem), sKV = sQ + 2 * C::TILE;
+  uint8_t* staging = smem + (2 + C::STAGES) * C::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::STAGING);
+  const uint32_t bar0 = smem_addr(bars);
+  auto bar_full = [&](int s) { return bar0 + 8u * s; };
+  auto bar_empty = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+  auto bar_q = [&](int i) { return bar0 + 8u * (2 * C::STAGES + i); };          // Q tile arrived
+  auto bar_qfree = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 2 + i); };  // its last Q K^T is done
+  auto bar_s = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 4 + i); };      // scores ready
+  auto bar_p = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 6 + i); };      // P written
+  auto bar_o = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 8 + i); };      // O of a unit ready
+  const uint32_t bar_drain = bar0 + 8u * (2 * C::STAGES + 10);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
+  const int lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_q(i), 1);
+      mbar_init(bar_qfree(i), 1);
+      mbar_init(bar_s(i), 1);
+      mbar_init(bar_p(i), 4);   // one arrival per softmax warp
+      mbar_init(bar_o(i), 1);
+    }
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(smem_addr(tmem_holder), 512);
+  if (warp == kWarpProducer && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  // every wait of a warp is voted on, so its lanes stay together
+  auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) {
+    const bool r = mbar_wait(bar, parity, abort_flag, p.timeout_ns, p.err, code);
+    return __all_sync(0xffffffffu, r) != 0;
+  };
+
+  if (warp >= 8) {
+    regs_decrease<kControlRegs>();
+    const bool leader = elect_one();
+    if (warp == kWarpProducer) {
+      // ---------------------------------------------------------- producer
+      const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
+      int ld = 0, nq[2] = {0, 0};
+      bool ok = p.fault_skip_kv == 0;
+      for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        const Unit w = unit_at(p, u);
+        const int hk = w.h / (p.heads / p.kv_heads);
+        for (int x = 0; x < 2 * w.tiles && ok; ++x) {
+          const int s = ld % C::STAGES;
+          ok = wait_all(bar_empty(s), ((ld / C::STAGES) & 1) ^ 1, kErrProducer);
+          if (!ok) break;
+          if (leader) {
+            mbar_arrive_expect_tx(bar_full(s), C::TILE);
+            for (int kb = 0; kb < C::NKB; ++kb)
+              tma_load_4d_hint(sKV + s * C::TILE + kb * kBN * 128, x % 2 ? &tm_v : &tm_k, bar_full(s), kb * 64,
+                               w.k0 + (x / 2) * kBN, hk, w.b, pol_kv);
+          }
+          __syncwarp();
+          ++ld;
+          // (the first K tile is requested before the Q tiles, which wait for
+          // the previous unit's last Q K^T)
+          for (int i = 0; x == 0 && i < w.halves && ok; ++i) {
+            ok = wait_all(bar_qfree(i), (nq[i] & 1) ^ 1, kErrProducer);
+            if (!ok) break;
+            if (leader) {
+              mbar_arrive_expect_tx(bar_q(i), C::TILE);
+              for (int kb = 0; kb < C::NKB; ++kb)
+                tma_load_4d_hint(sQ + i * C::TILE + kb * kBM * 128, &tm_q, bar_q(i), kb * 64, w.q0 + i * kBM, w.h,
+                                 w.b, pol_q);
+            }
+            __syncwarp();
+            ++nq[i];
+          }
+        }
+      }
+      if (!ok && leader) {
+        // leave no copy in flight into this CTA's shared memory
+        for (int x = ld > C::STAGES ? ld - C::STAGES : 0; x < ld; ++x)
+          mbar_drain(bar_full(x % C::STAGES), (x / C::STAGES) & 1, p.timeout_ns);
+        for (int i = 0; i < 2; ++i)
+          if (nq[i] > 0) mbar_drain(bar_q(i), (nq[i] - 1) & 1, p.timeout_ns);
+      }
+      __syncwarp();
+    } else if (warp == kWarpMma) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024), k_desc = smem_desc_sw128(sKV, 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(sKV, kBN * 128, 1024);
+      const uint32_t hi = static_cast<uint32_t>(q_desc >> 32);   // (shared by all: low words hold the address)
+      auto issue_qk = [&](int i, int stage) {
+        uint32_t a[C::QK], b[C::QK];
+#pragma unroll
+        for (int kk = 0; kk < C::QK; ++kk) {
+          const uint32_t off = ((kk / 4) * (kBM * 128) + (kk % 4) * 32) >> 4;
+          a[kk] = static_cast<uint32_t>(q_desc) + ((i * C::TILE) >> 4) + off;
+          b[kk] = static_cast<uint32_t>(k_desc) + ((stage * C::TILE) >> 4) + off;
+        }
+        mma_group<C::QK, true>(tmem + i * kBN, a, b, hi, C::IDESC_QK, 0u);
+      };
+      auto issue_pv = [&](int i, int stage, uint32_t acc) {
+        uint32_t a[C::PV], b[C::PV];
+#pragma unroll
+        for (int kk = 0; kk < C::PV; ++kk) {
+          a[kk] = tmem + i * kBN + kk * 8;
+          b[kk] = static_cast<uint32_t>(v_desc) + ((stage * C::TILE + kk * 16 * 128) >> 4);
+        }
+        mma_group<C::PV, false>(tmem + C::O_COL + i * D, a, b, hi, C::IDESC_PV, acc);
+      };
+      auto next_unit = [&](int64_t& u, Unit& w) {   // the next one with keys
+        for (; u < units; u += gridDim.x) {
+          w = unit_at(p, u);
+          if (w.tiles > 0) return true;
+        }
+        return false;
+      };
+      int ld = 0;                    // load index of the unit's first K tile
+      int nq[2] = {0, 0}, np[2] = {0, 0};
+      bool ok = true;
+      int64_t u = blockIdx.x;
+      Unit w;
+      bool have = next_unit(u, w);
+      // a unit's first scores, query tile by query tile
+      auto first_qk = [&](const Unit& x, int at) {
+        const int s = at % C::STAGES;
+        ok = ok && wait_all(bar_full(s), (at / C::STAGES) & 1, kErrMma);
+        for (int i = 0; i < x.halves && ok; ++i) {
+          ok = wait_all(bar_q(i), nq[i] & 1, kErrMma);
+          if (!ok) return;
+          ++nq[i];
+          tc_fence_after();
+          if (leader) {
+            issue_qk(i, s);
+            mma_commit(bar_s(i));
+            if (x.tiles == 1) mma_commit(bar_qfree(i));
+            if (i == x.halves - 1) mma_commit(bar_empty(s));
+          }
+          __syncwarp();
+        }
+      };
+      if (have) first_qk(w, ld);
+      while (have && ok) {
+        int64_t un = u + gridDim.x;
+        Unit wn;
+        const bool more_units = next_unit(un, wn);
+        for (int j = 0; j < w.tiles && ok; ++j) {
+          const int lv = ld + 2 * j + 1, sv = lv % C::STAGES;
+          const int lk = ld + 2 * j + 2, sk = lk % C::STAGES;
+          const bool more = j + 1 < w.tiles;
+          ok = wait_all(bar_full(sv), (lv / C::STAGES) & 1, kErrMma);
+          if (ok && more) ok = wait_all(bar_full(sk), (lk / C::STAGES) & 1, kErrMma);
+          if (!ok) break;
+          const int valid = w.k1 - (w.k0 + j * kBN);
+          if (valid < kBN) {
+            // V rows past the last valid key: zero (see above)
+            uint8_t* vt = smem + (2 + sv) * C::TILE;
+            for (int x = lane; x < (kBN - valid) * 8 * C::NKB; x += 32) {
+              const int kb = x / ((kBN - valid) * 8), y = x - kb * ((kBN - valid) * 8);
+              *reinterpret_cast<uint4*>(vt + kb * kBN * 128 + (valid * 8 + y) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          for (int i = 0; i < w.halves && ok; ++i) {
+            ok = wait_all(bar_p(i), np[i] & 1, kErrMma);
+            if (!ok) break;
+            ++np[i];
+            tc_fence_after();
+            if (leader) {
+              const bool last = i == w.halves - 1;
+              issue_pv(i, sv, j > 0);
+              if (last) mma_commit(bar_empty(sv));
+              if (more) {
+                issue_qk(i, sk);
+                mma_commit(bar_s(i));
+                if (j + 2 == w.tiles) mma_commit(bar_qfree(i));
+                if (last) mma_commit(bar_empty(sk));
+              } else {
+                mma_commit(bar_o(i));
+              }
+            }
+            __syncwarp();
+          }
+        }
+        ld += 2 * w.tiles;
+        if (ok && more_units) first_qk(wn, ld);
+        have = more_units;
+        u = un;
+        w = wn;
+      }
+      if (!ok && leader) {
+        // let every MMA already issued finish before TMEM is released
+        mma_commit(bar_drain);
+        mbar_drain(bar_drain, 0, p.timeout_ns);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------- softmax, output
+    regs_increase<kSoftmaxRegs>();
+    const int wg = warp / 4, quarter = warp % 4;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_base + wg * kBN;
+    const uint32_t tO = tmem + lane_base + C::O_COL + wg * D;
+    const float sl2 = p.scale_log2;
+    const uint64_t pol_out = l2_policy_evict_first();
+    uint8_t* stage = staging + warp * 4096;
+    int ns = 0, no = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const Unit w = unit_at(p, u);
+      if (wg >= w.halves) continue;
+      const int row0 = w.q0 + wg * kBM + quarter * 32, row = row0 + lane;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < w.tiles; ++j) {
+        ok = wait_all(bar_s(wg), ns & 1, kErrSoftmax);
+        if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        const int valid = w.k1 - (w.k0 + j * kBN);
+        uint32_t s[kBN];
+        float row_max;
+        if (valid >= kBN) {
+          tmem_ld_max_x128(tS, s, row_max);
+        } else {
+          tmem_ld_x128(tS, s);
+          row_max = masked_row_max<kBN>(s, valid);
+        }
+        const float top = row_max * sl2;
+        float factor = 1.f;
+        bool raise = false;
+        if (j == 0) {
+          m = top;
+        } else if (top > m + kRescaleThreshold) {
+          factor = ex2_approx(m - top);
+          m = top;
+          l *= factor;
+          raise = true;
+        }
+        // (the previous P V completed before these scores: one issue order)
+        if (__any_sync(0xffffffffu, raise)) rescale_o<D>(tO, factor);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kBN / 2; ++i) {
+          float x0, x1;
+          ffma2(x0, x1, u2f(s[2 * i]), u2f(s[2 * i + 1]), sl2, sl2, -m, -m);
+          const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+          const int a = 2 * (i & 1);
+          fadd2(acc[a], acc[a + 1], acc[a], acc[a + 1], e0, e1);
+          s[i] = pack_bf16x2(e0, e1);
+        }
+        tmem_st_x64(tS, *reinterpret_cast<uint32_t(*)[64]>(&s[0]));
+        l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p(wg));
+      }
+      if (!ok) break;
+      const bool none = w.tiles == 0;
+      const float inv = none ? 0.f : 1.f / l;
+      const float lse = none ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (!none) {
+        ok = wait_all(bar_o(wg), no & 1, kErrSoftmax);
+        if (!ok) break;
+        ++no;
+        tc_fence_after();
+      }
+      const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
+      const int64_t at = w.part * n + (static_cast<int64_t>(w.b) * p.heads + w.h) * p.s_q + row;
+      uint8_t* out = static_cast<uint8_t*>(p.out.data) + (w.b * p.out.s[0] + w.h * p.out.s[1]) * 2;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 64) {
+        uint32_t o[64];
+        __syncwarp();
+        if (none) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) o[i] = 0u;
+        } else {
+          tmem_ld_x64(tO + c0, o);
+        }
+        if (p.splits > 1) {
+          if (row < p.s_q && !none) {   // (a part without keys is not read)
+            float4* dst = reinterpret_cast<float4*>(p.ws + at * D + c0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (CPATTN_IN(p.ws_span, dst + i, 16, p.err))
+                dst[i] = make_float4(u2f(o[4 * i]) * inv, u2f(o[4 * i + 1]) * inv, u2f(o[4 * i + 2]) * inv,
+                                     u2f(o[4 * i + 3]) * inv);
+          }
+          continue;
+        }
+        // the warp's 32 rows pass through its staging area (16-byte chunks
+        // XOR-swizzled by row) and leave as whole 128-byte pieces
+        uint4* srow = reinterpret_cast<uint4*>(stage) + lane * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = pack_bf16x2(u2f(o[8 * i + 2 * e]) * inv, u2f(o[8 * i + 2 * e + 1]) * inv);
+          srow[i ^ (lane % 8)] = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const int r = it * 4 + lane / 8, c = lane % 8;
+          if (row0 + r < p.s_q) {
+            const uint4 val = reinterpret_cast<const uint4*>(stage)[r * 8 + (c ^ (r % 8))];
+            uint8_t* dst = out + (static_cast<int64_t>(row0 + r) * p.out.s[2] + c0) * 2 + c * 16;
+            if (CPATTN_IN(p.out.span, dst, 16, p.err)) st_global_v4_hint(dst, val, pol_out);
+          }
+        }
+      }
+      if (row < p.s_q) {
+        float* dst = p.splits > 1
+                         ? p.ws + p.splits * n * D + at
+                         : static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + row * p.lse.s[2];
+        if (CPATTN_IN(p.splits > 1 ? p.ws_span : p.lse.span, dst, 4, p.err)) *dst = lse;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                         const CrossParams& p, cudaStream_t stream) {
+  using C = Cfg<D>;
+  auto kernel = cross_fwd_kernel<D>;
+  // once per device: the register split needs exactly kLaunchRegs at launch
+  // (refused otherwise), and the shared-memory limit is raised
+  static std::atomic<unsigned long long> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit == 0 || (ready.load(std::memory_order_acquire) & bit) == 0) {
+    cudaFuncAttributes attr;
+    if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
+    if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess)
+      return e;
+    ready.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int64_t units = static_cast<int64_t>(p.batch) * p.heads * p.splits * ((p.s_q + 2 * kBM - 1) / (2 * kBM));
+  const int64_t sms = sm_count();
+  kernel<<<static_cast<unsigned>(units < sms ? units : sms), kThreads, C::SMEM, stream>>>(tm_q, tm_k, tm_v, p, units);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                             const CrossParams& p, cudaStream_t stream) {
+  return head_dim == 64 ? launch_typed<64>(tm_q, tm_k, tm_v, p, stream)
+                        : launch_typed<128>(tm_q, tm_k, tm_v, p, stream);
+}
+
+}  // namespace cpattn
