@@ -403,8 +403,23 @@ size_t cross_workspace(const cpattn_tensor* q, const cpattn_tensor* k) {
   return splits > 1 && rows > 0 ? static_cast<size_t>(splits) * rows * (q->shape[3] + 1) * 4 : 0;
 }
 
-size_t cross_backward_workspace(const cpattn_tensor* q, const cpattn_tensor*) {
-  return static_cast<size_t>(q->shape[0] * q->shape[1] * q->shape[2]) * 4;
+// Parts of the query axis for dk and dv (bf16; fp32: 1).
+int cross_parts(const cpattn_tensor* q, const cpattn_tensor* k) {
+  const int64_t rows = q->shape[0] * q->shape[1] * q->shape[2], keys = k->shape[0] * k->shape[1] * k->shape[2];
+  if (q->dtype != CPATTN_BF16 || rows == 0 || keys == 0) return 1;
+  return cpattn::cross_backward_parts(k->shape[0] * k->shape[1] * ((k->shape[2] + 127) / 128),
+                                      q->shape[1] / k->shape[1] * ((q->shape[2] + 127) / 128));
+}
+
+// Floats before the parts' sums: delta of every query row, whole 16-byte vectors.
+int64_t cross_delta_floats(const cpattn_tensor* q) {
+  return (q->shape[0] * q->shape[1] * q->shape[2] + 3) / 4 * 4;
+}
+
+size_t cross_backward_workspace(const cpattn_tensor* q, const cpattn_tensor* k) {
+  const int parts = cross_parts(q, k);
+  const int64_t keys = k->shape[0] * k->shape[1] * k->shape[2];
+  return static_cast<size_t>(cross_delta_floats(q) + (parts > 1 ? 2 * parts * keys * q->shape[3] : 0)) * 4;
 }
 
 // What both directions check and fill in; *run stays false where q has no row.
@@ -780,13 +795,23 @@ cpattn_status cpattn_cross_attention_backward(const cpattn_tensor* q, const cpat
   p.dq = cross_tensor(dq, shrink);
   p.dk = cross_tensor(dk, shrink);
   p.dv = cross_tensor(dv, shrink);
-  p.splits = 1;
+  p.splits = cross_parts(q, k);
   const InDtype dt = q->dtype == CPATTN_BF16 ? InDtype::BF16 : InDtype::F32;
   const int D = static_cast<int>(q->shape[3]);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  CUtensorMap tm_q, tm_k, tm_v, tm_g;
+  const bool tensor_cores = dt == InDtype::BF16 && rows && keys;
+  if (tensor_cores) {
+    if ((st = make_tmap(&tm_q, q, 128)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&tm_k, k, 128)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&tm_v, v, 128)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&tm_g, dout, 128)) != CPATTN_OK) return st;
+  }
   cudaError_t e = cudaSuccess;
   if (rows) e = cpattn::launch_cross_delta(dt, D, p, cs);
-  if (e == cudaSuccess) e = cpattn::launch_cross_simt_backward(dt, D, p, cs);
+  if (e == cudaSuccess)
+    e = tensor_cores ? cpattn::launch_cross_bwd(D, tm_q, tm_k, tm_v, tm_g, p, cross_delta_floats(q), cs)
+                     : cpattn::launch_cross_simt_backward(dt, D, p, cs);
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 

@@ -40,6 +40,14 @@ __device__ __forceinline__ int cross_length(const CrossParams& p, int b) {
 // have 128 rows).
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                              const CUtensorMap& tm_v, const CrossParams& p, cudaStream_t stream);
+// its gradient (s_q, s_kv >= 1; delta at the workspace's start, partial sums of
+// dk and dv `partials` floats into it when p.splits > 1)
+cudaError_t launch_cross_bwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                             const CUtensorMap& tm_v, const CUtensorMap& tm_g, const CrossParams& p,
+                             int64_t partials, cudaStream_t stream);
+// parts of the query axis for key_units 128-key tiles that walk `steps`
+// 128-row query tiles each
+int cross_backward_parts(int64_t key_units, int64_t steps);
 // fp32 inputs (D 64 or 128).
 cudaError_t launch_cross_simt(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream);
 cudaError_t launch_cross_simt_backward(InDtype dt, int head_dim, const CrossParams& p,
