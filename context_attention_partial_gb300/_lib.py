@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -119,15 +120,16 @@ def load():
         return _lib
 
 
+# CTensor's fields as one packed record, per rank (unused extents are zero):
+# setting the arrays element by element took most of a call's host time.
+_RECORD = [struct.Struct(f"@Pii{n}q{8 * (MAX_DIMS - n)}x{n}q{8 * (MAX_DIMS - n)}x") for n in range(MAX_DIMS + 1)]
+
+
 def describe(data_ptr: int, dtype_code: int, shape, stride) -> CTensor:
-    t = CTensor()
-    t.data = data_ptr or None
-    t.dtype = dtype_code
-    t.ndim = len(shape)
-    for i, (s, st) in enumerate(zip(shape, stride)):
-        t.shape[i] = int(s)
-        t.stride[i] = int(st)
-    return t
+    n = len(shape)
+    if n > MAX_DIMS:
+        raise IndexError(f"{n} dimensions: at most {MAX_DIMS}")
+    return CTensor.from_buffer_copy(_RECORD[n].pack(data_ptr, dtype_code, n, *shape, *stride))
 
 
 def check(status: int, what: str):

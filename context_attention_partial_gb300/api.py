@@ -420,19 +420,23 @@ def _on_device(ts, stream: Optional[torch.cuda.Stream]):
     """Checks that a call's tensors share one CUDA device.  Returns (a context
     in which that device is the current one, the stream to use, whether the
     stream is another than the device's current one)."""
-    dev = ts[0].device
+    index = ts[0].get_device()
     for t in ts:
-        if not t.is_cuda:
+        at = t.get_device()
+        if at < 0:
             raise ValueError("cpattn runs on CUDA tensors only (no CPU path)")
-        if t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device} in one call")
-    current = torch.cuda.current_stream(dev)
+        if at != index:
+            raise ValueError(f"tensors on cuda:{index} and cuda:{at} in one call")
+    ctx = _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
+    current = torch.cuda.current_stream(index)
     if stream is None:
-        stream = current
-    elif stream.device != dev:
-        raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
-    ctx = nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        return ctx, current, False
+    if stream.device_index != index:
+        raise ValueError(f"a stream of cuda:{stream.device_index} for tensors on cuda:{index}")
     return ctx, stream, stream != current
+
+
+_HERE = nullcontext()
 
 
 def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float = 10000.0,

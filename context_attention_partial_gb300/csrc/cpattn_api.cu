@@ -381,20 +381,34 @@ cpattn_status cross_shape(const cpattn_tensor* q, const cpattn_tensor* k) {
   return CPATTN_OK;
 }
 
+// Few query rows a key head: bf16 calls that the key and value read bounds.
+bool cross_few(const cpattn_tensor* q, const cpattn_tensor* k) {
+  return q->dtype == CPATTN_BF16 && k->shape[1] > 0 &&
+         q->shape[2] * (q->shape[1] / k->shape[1]) <= cpattn::kCrossFewRows;
+}
+
 // Parts of the key axis of a forward call: 1 where the query rows fill the
-// GPU, else as many as give each SM a unit of work (bf16: 256 query rows of a
-// head, parts of four 128-key tiles or more; fp32: 2 rows, 512 keys or more).
+// GPU, else as many as keep it full: for few rows four rounds of two CTAs per
+// SM, each with 256 keys or more; for 256-row units of the tensor-core kernel
+// one per SM, each with four 128-key tiles or more; for fp32's 2-row blocks
+// likewise, each with 512 keys or more.
 int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
   const int64_t bh = q->shape[0] * q->shape[1], sm = cpattn::sm_count();
-  int64_t units;
-  if (q->dtype == CPATTN_BF16)
-    units = (q->shape[2] + 255) / 256 * bh;
-  else
-    units = (q->shape[2] + 63) / 64 * bh >= sm ? sm : (q->shape[2] + 1) / 2 * bh;
-  if (units >= sm || units == 0) return 1;
-  const int64_t most = (k->shape[2] + 511) / 512, want = sm / units;
+  if (bh == 0 || q->shape[2] == 0 || k->shape[2] == 0) return 1;
+  int64_t most, want;
+  if (cross_few(q, k)) {
+    const int64_t units = q->shape[0] * k->shape[1];
+    most = (k->shape[2] + 255) / 256;
+    want = (8 * sm + units - 1) / units;
+  } else {
+    int64_t units = (q->shape[2] + 255) / 256 * bh;
+    if (q->dtype != CPATTN_BF16)
+      units = (q->shape[2] + 63) / 64 * bh >= sm ? sm : (q->shape[2] + 1) / 2 * bh;
+    most = (k->shape[2] + 511) / 512;
+    want = sm / units;
+  }
   const int64_t s = want < most ? want : most;
-  return s > 1 ? static_cast<int>(s) : 1;
+  return s > 1 ? static_cast<int>(s < 65535 ? s : 65535) : 1;
 }
 
 size_t cross_workspace(const cpattn_tensor* q, const cpattn_tensor* k) {
@@ -746,7 +760,9 @@ cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   p.splits = p.s_kv > 0 ? cross_splits(q, k) : 0;
-  if (p.splits > 0 && dt == InDtype::BF16) {
+  if (p.splits > 0 && cross_few(q, k)) {
+    e = cpattn::launch_cross_few(D, p, cs);
+  } else if (p.splits > 0 && dt == InDtype::BF16) {
     CUtensorMap tm_q, tm_k, tm_v;
     if ((st = make_tmap(&tm_q, q, 128)) != CPATTN_OK) return st;
     if ((st = make_tmap(&tm_k, k, 128)) != CPATTN_OK) return st;

@@ -40,6 +40,9 @@ __device__ __forceinline__ int cross_length(const CrossParams& p, int b) {
 // have 128 rows).
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                              const CUtensorMap& tm_v, const CrossParams& p, cudaStream_t stream);
+// the same for at most kCrossFewRows query rows a key head (s_q * H / H_kv)
+constexpr int kCrossFewRows = 64;
+cudaError_t launch_cross_few(int head_dim, const CrossParams& p, cudaStream_t stream);
 // its gradient (s_q, s_kv >= 1; delta at the workspace's start, partial sums of
 // dk and dv `partials` floats into it when p.splits > 1)
 cudaError_t launch_cross_bwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,

@@ -270,16 +270,22 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
   top = warp_max(top);
   float o[F] = {}, total = 0.f;
   const float base = top == -INFINITY ? 0.f : top;
-  for (int x = 0; x < p.splits; ++x) {
-    const float l = CPATTN_IN(p.ws_span, pl + x * n, 4, p.err) ? pl[x * n] : 0.f;
-    if (l == -INFINITY) continue;   // a part without keys
-    const float w = exp2f((l - base) * kLog2e);
-    const float* src = p.ws + (x * n + at) * D + lane * F;
-    float t[F] = {};
-    if (CPATTN_IN(p.ws_span, src, 4 * F, p.err)) load_lane<F>(src, t);
-    total += w;
+  for (int x0 = 0; x0 < p.splits; x0 += 32) {
+    // a lane's own part's weight, 0 for a part without keys (which is not read)
+    float mine = 0.f;
+    if (x0 + lane < p.splits && CPATTN_IN(p.ws_span, pl + (x0 + lane) * n, 4, p.err))
+      mine = exp2f((pl[(x0 + lane) * n] - base) * kLog2e);
+    const int count = min(32, p.splits - x0);
+#pragma unroll 8
+    for (int x = 0; x < count; ++x) {
+      const float w = __shfl_sync(0xffffffffu, mine, x);
+      const float* src = p.ws + ((x0 + x) * n + at) * D + lane * F;
+      float t[F] = {};
+      if (w != 0.f && CPATTN_IN(p.ws_span, src, 4 * F, p.err)) load_lane<F>(src, t);
+      total += w;
 #pragma unroll
-    for (int f = 0; f < F; ++f) o[f] = fmaf(w, t[f], o[f]);
+      for (int f = 0; f < F; ++f) o[f] = fmaf(w, t[f], o[f]);
+    }
   }
   const bool none = total == 0.f;
   const float inv = none ? 0.f : 1.f / total;
