@@ -93,6 +93,16 @@ def bind(path: str):
                                            vp]
     lib.cpattn_cross_attention_backward.argtypes = [P, P, P, P, P, P, P, ctypes.c_float, P, P, P,
                                                     vp, ctypes.c_size_t, vp]
+    # the same entry points taking descriptors as packed records (bytes): no
+    # ctypes object per tensor
+    b, f32, size = ctypes.c_char_p, ctypes.c_float, ctypes.c_size_t
+    for name, *args in (
+            ("cpattn_rotary", i32, b, b, i32, b, ctypes.c_double, i32, i32, b, vp),
+            ("cpattn_cross_attention", b, b, b, b, f32, b, b, vp, size, vp),
+            ("cpattn_cross_attention_backward", b, b, b, b, b, b, b, f32, b, b, b, vp, size, vp)):
+        setattr(lib, name + "_packed", ctypes.CFUNCTYPE(i32, *args)((name, lib)))
+    for name in ("cpattn_cross_workspace_bytes", "cpattn_cross_backward_workspace_bytes"):
+        setattr(lib, name + "_packed", ctypes.CFUNCTYPE(size, b, b)((name, lib)))
     for name in ("cpattn_cross_workspace_bytes", "cpattn_cross_backward_workspace_bytes"):
         getattr(lib, name).argtypes = [P, P]
         getattr(lib, name).restype = ctypes.c_size_t
@@ -122,14 +132,20 @@ def load():
 
 # CTensor's fields as one packed record, per rank (unused extents are zero):
 # setting the arrays element by element took most of a call's host time.
-_RECORD = [struct.Struct(f"@Pii{n}q{8 * (MAX_DIMS - n)}x{n}q{8 * (MAX_DIMS - n)}x") for n in range(MAX_DIMS + 1)]
+_RECORD = [struct.Struct(f"@Pii{n}q{8 * (MAX_DIMS - n)}x{n}q{8 * (MAX_DIMS - n)}x").pack
+           for n in range(MAX_DIMS + 1)]
 
 
-def describe(data_ptr: int, dtype_code: int, shape, stride) -> CTensor:
+def record(data_ptr: int, dtype_code: int, shape, stride) -> bytes:
+    """A tensor's descriptor as the bytes of a CTensor."""
     n = len(shape)
     if n > MAX_DIMS:
         raise IndexError(f"{n} dimensions: at most {MAX_DIMS}")
-    return CTensor.from_buffer_copy(_RECORD[n].pack(data_ptr, dtype_code, n, *shape, *stride))
+    return _RECORD[n](data_ptr, dtype_code, n, *shape, *stride)
+
+
+def describe(data_ptr: int, dtype_code: int, shape, stride) -> CTensor:
+    return CTensor.from_buffer_copy(record(data_ptr, dtype_code, shape, stride))
 
 
 def check(status: int, what: str):

@@ -8,6 +8,7 @@ kernels; CPU tensors are rejected (there is no CPU path).
 from __future__ import annotations
 
 import ctypes
+import struct
 from contextlib import nullcontext
 from typing import Optional, Sequence, Tuple, Union
 
@@ -418,8 +419,8 @@ def prepare_ulysses_anything(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
 
 def _on_device(ts, stream: Optional[torch.cuda.Stream]):
     """Checks that a call's tensors share one CUDA device.  Returns (a context
-    in which that device is the current one, the stream to use, whether the
-    stream is another than the device's current one)."""
+    in which that device is the current one, the handle of the stream to use,
+    the stream itself if it is another than the device's current one)."""
     index = ts[0].get_device()
     for t in ts:
         at = t.get_device()
@@ -430,13 +431,25 @@ def _on_device(ts, stream: Optional[torch.cuda.Stream]):
     ctx = _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
     current = torch.cuda.current_stream(index)
     if stream is None:
-        return ctx, current, False
+        return ctx, current.cuda_stream, None
     if stream.device_index != index:
         raise ValueError(f"a stream of cuda:{stream.device_index} for tensors on cuda:{index}")
-    return ctx, stream, stream != current
+    return ctx, stream.cuda_stream, stream if stream != current else None
 
 
 _HERE = nullcontext()
+
+
+def _record(t: torch.Tensor) -> bytes:
+    return _lib.record(t.data_ptr(), _code(t), t.shape, t.stride())
+
+
+def _lengths_record(t: Optional[torch.Tensor]) -> Optional[bytes]:
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise TypeError(f"kv_lengths are int32, not {t.dtype}")
+    return _lib.record(t.data_ptr(), _lib.I32, t.shape, t.stride())
 
 
 def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float = 10000.0,
@@ -453,44 +466,36 @@ def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float =
     single = isinstance(xs, torch.Tensor)
     if single:
         xs, outs = [xs], None if outs is None else [outs]
-    ctx, s, other = _on_device([*xs, positions, *(o for o in outs or () if o is not None)], stream)
-    if positions.dtype != torch.float32:
-        raise TypeError(f"positions are float32, not {positions.dtype}")
-    outs = list(outs) if outs is not None else [None] * len(xs)
-    if len(outs) != len(xs):
-        raise ValueError(f"{len(xs)} tensors but {len(outs)} outputs")
-    made = []
-    for i, x in enumerate(xs):
-        if outs[i] is None:
-            outs[i] = torch.empty_like(x)   # (keeps a [B,S,H,D] tensor's order)
-            made.append(outs[i])
-    dims = (ctypes.c_int32 * max(1, len(axes_dims)))(*axes_dims)
+    if outs is None:
+        given = (*xs, positions)
+        outs = made = [torch.empty_like(x) for x in xs]   # (keeps a [B,S,H,D] tensor's order)
+    else:
+        outs, made = list(outs), []
+        if len(outs) != len(xs):
+            raise ValueError(f"{len(xs)} tensors but {len(outs)} outputs")
+        given = (*xs, positions, *outs)
+    ctx, handle, other = _on_device(given, stream)
+    n = len(axes_dims)
     with ctx:
-        check(lib.cpattn_rotary(len(xs), _descs(xs), _desc(positions), len(axes_dims), dims, float(theta),
-                                int(bool(interleaved)), int(bool(inverse)), _descs(outs),
-                                s.cuda_stream), "cpattn_rotary")
-    if other:
+        check(lib.cpattn_rotary_packed(len(xs), b"".join(map(_record, xs)), _record(positions), n,
+                                       _INTS[min(n, 5)](*axes_dims[:5]), theta, interleaved, inverse,
+                                       b"".join(map(_record, outs)), handle), "cpattn_rotary")
+    if other is not None:
         for t in made:
-            t.record_stream(s)
+            t.record_stream(other)
     return outs[0] if single else outs
 
 
-def _desc_lengths(t: Optional[torch.Tensor]) -> Optional[_lib.CTensor]:
-    if t is None:
-        return None
-    if t.dtype != torch.int32:
-        raise TypeError(f"kv_lengths are int32, not {t.dtype}")
-    return describe(t.data_ptr(), _lib.I32, t.shape, t.stride())
+# int32 arrays as bytes, by length (five axes are refused by the library)
+_INTS = [struct.Struct(f"@{n}i").pack for n in range(6)]
 
 
 def cross_workspace_bytes(q: torch.Tensor, k: torch.Tensor) -> int:
-    return int(_lib.load().cpattn_cross_workspace_bytes(describe(0, _code(q), q.shape, q.stride()),
-                                                        describe(0, _code(k), k.shape, k.stride())))
+    return _lib.load().cpattn_cross_workspace_bytes_packed(_record(q), _record(k))
 
 
 def cross_backward_workspace_bytes(q: torch.Tensor, k: torch.Tensor) -> int:
-    return int(_lib.load().cpattn_cross_backward_workspace_bytes(
-        describe(0, _code(q), q.shape, q.stride()), describe(0, _code(k), k.shape, k.stride())))
+    return _lib.load().cpattn_cross_backward_workspace_bytes_packed(_record(q), _record(k))
 
 
 def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -503,8 +508,8 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     sequence's valid keys, a sequence without any gives (0, -inf).
     Returns (out [B,H,S_q,D] in q's dtype, lse f32 [B,H,S_q])."""
     lib = _lib.load()
-    ctx, s, other = _on_device([t for t in (q, k, v, kv_lengths, out, lse, workspace) if t is not None],
-                               stream)
+    ctx, handle, other = _on_device([t for t in (q, k, v, kv_lengths, out, lse, workspace) if t is not None],
+                                    stream)
     made = []
     if out is None:
         out = torch.empty_like(q)
@@ -512,21 +517,22 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if lse is None:
         lse = torch.empty(q.shape[:3], device=q.device, dtype=torch.float32)
         made.append(lse)
-    dq, dk = _desc(q), _desc(k)
+    rq, rk = _record(q), _record(k)
     with ctx:
+        ws_ptr, ws_bytes = None, 0
         if workspace is None:
-            need = lib.cpattn_cross_workspace_bytes(dq, dk)
+            need = lib.cpattn_cross_workspace_bytes_packed(rq, rk)
             if need > 0:
                 workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
                 made.append(workspace)
-        ws_ptr, ws_bytes = (None, 0) if workspace is None else (
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        check(lib.cpattn_cross_attention(dq, dk, _desc(v), _desc_lengths(kv_lengths), _scale(scale),
-                                         _desc(out), _desc(lse), ws_ptr, ws_bytes, s.cuda_stream),
-              "cpattn_cross_attention")
-    if other:
+        if workspace is not None:
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
+        check(lib.cpattn_cross_attention_packed(rq, rk, _record(v), _lengths_record(kv_lengths),
+                                                _scale(scale), _record(out), _record(lse), ws_ptr,
+                                                ws_bytes, handle), "cpattn_cross_attention")
+    if other is not None:
         for t in made:
-            t.record_stream(s)
+            t.record_stream(other)
     return out, lse
 
 
@@ -543,8 +549,8 @@ def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     the shapes and dtype of q, k, v; rows of dk and dv past a sequence's
     length are 0."""
     lib = _lib.load()
-    ctx, s, other = _on_device([t for t in (q, k, v, out, lse, dout, kv_lengths, dq, dk, dv, workspace)
-                                if t is not None], stream)
+    ctx, handle, other = _on_device([t for t in (q, k, v, out, lse, dout, kv_lengths, dq, dk, dv, workspace)
+                                     if t is not None], stream)
     made = []
     if dq is None:
         dq = torch.empty_like(q)
@@ -555,22 +561,23 @@ def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     if dv is None:
         dv = torch.empty_like(v)
         made.append(dv)
-    tq, tk = _desc(q), _desc(k)
+    rq, rk = _record(q), _record(k)
     with ctx:
+        ws_ptr, ws_bytes = None, 0
         if workspace is None:
-            need = lib.cpattn_cross_backward_workspace_bytes(tq, tk)
+            need = lib.cpattn_cross_backward_workspace_bytes_packed(rq, rk)
             if need > 0:
                 workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
                 made.append(workspace)
-        ws_ptr, ws_bytes = (None, 0) if workspace is None else (
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        check(lib.cpattn_cross_attention_backward(
-            tq, tk, _desc(v), _desc(out), _desc(lse), _desc(dout), _desc_lengths(kv_lengths),
-            _scale(scale), _desc(dq), _desc(dk), _desc(dv), ws_ptr, ws_bytes, s.cuda_stream),
+        if workspace is not None:
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
+        check(lib.cpattn_cross_attention_backward_packed(
+            rq, rk, _record(v), _record(out), _record(lse), _record(dout), _lengths_record(kv_lengths),
+            _scale(scale), _record(dq), _record(dk), _record(dv), ws_ptr, ws_bytes, handle),
             "cpattn_cross_attention_backward")
-    if other:
+    if other is not None:
         for t in made:
-            t.record_stream(s)
+            t.record_stream(other)
     return dq, dk, dv
 
 

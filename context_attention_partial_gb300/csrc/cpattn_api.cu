@@ -679,7 +679,6 @@ cpattn_status cpattn_rotary(int n, const cpattn_tensor* x, const cpattn_tensor* 
   cpattn::RotaryParams p;
   std::memset(&p, 0, sizeof(p));
   const long long shrink = g_check_shrink.load();
-  bool token_inner = true;
   for (int i = 0; i < n; ++i) {
     const bool none = x[i].shape[1] == 0;
     if (!none && (!x[i].data || !y[i].data)) return CPATTN_ERR_NULL;
@@ -698,7 +697,6 @@ cpattn_status cpattn_rotary(int n, const cpattn_tensor* x, const cpattn_tensor* 
     p.head_start[i + 1] = p.head_start[i] + static_cast<int>(x[i].shape[1]);
     p.x_span[i] = {x[i].data, extent_bytes(&x[i])};
     p.y_span[i] = {y[i].data, extent_bytes(&y[i], shrink)};
-    if (!none && x[i].shape[1] > 1 && x[i].stride[1] < x[i].stride[2]) token_inner = false;
   }
   p.n = n;
   p.batch = static_cast<int>(B);
@@ -712,7 +710,6 @@ cpattn_status cpattn_rotary(int n, const cpattn_tensor* x, const cpattn_tensor* 
   p.axes = axes;
   p.interleaved = interleaved != 0;
   p.inverse = inverse != 0;
-  p.token_inner = token_inner ? 1 : 0;
   p.err = cpattn::device_error_word();
   if (!(theta > 0.0) || !std::isfinite(theta)) theta = 10000.0;
   int j = 0;

@@ -1,6 +1,8 @@
 // cross.cuh -- parameters of the cross-attention kernels and what they share
 // (not part of the public ABI).
 #pragma once
+#include <atomic>
+
 #include "internal.h"
 
 namespace cpattn {
@@ -34,6 +36,20 @@ __device__ __forceinline__ int cross_length(const CrossParams& p, int b) {
   const int32_t* at = p.lengths + b;
   const int n = CPATTN_IN(p.lengths_span, at, 4, p.err) ? *at : 0;
   return max(0, min(n, p.s_kv));
+}
+
+// Raises a kernel's dynamic shared-memory limit once per device (bit d of
+// `ready`: device d is set up; the call costs about 5 us of host time).
+template <typename K>
+cudaError_t cross_set_up(K kernel, size_t smem, std::atomic<unsigned long long>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit != 0 && (ready.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
 }
 
 // bf16 inputs, D 64 or 128, on the tensor cores (s_kv >= 1; the maps' boxes

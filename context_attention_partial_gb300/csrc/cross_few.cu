@@ -271,7 +271,8 @@ template <int D, int MT>
 cudaError_t launch_tiles(const CrossParams& p, cudaStream_t stream) {
   using C = Few<D>;
   auto kernel = cross_few_kernel<D, MT>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<unsigned long long> ready{0};
+  const cudaError_t e = cross_set_up(kernel, C::SMEM, ready);
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(p.batch) * p.kv_heads;
   if (units > 0x7fffffff) return cudaErrorInvalidValue;

@@ -462,12 +462,12 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
   }
 }
 
-template <typename K>
-cudaError_t run(K kernel, int64_t blocks, int splits, int threads, size_t smem, const CrossParams& p,
-                cudaStream_t stream) {
+// (one instantiation, so one set-up record, per kernel)
+template <auto kernel>
+cudaError_t run(int64_t blocks, int splits, int threads, size_t smem, const CrossParams& p, cudaStream_t stream) {
+  static std::atomic<unsigned long long> ready{0};
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  // (repeated calls set the same limit; the attribute belongs to the device's copy of the kernel)
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const cudaError_t e = cross_set_up(kernel, smem, ready);
   if (e != cudaSuccess) return e;
   kernel<<<dim3(static_cast<unsigned>(blocks), splits), threads, smem, stream>>>(p);
   return cudaGetLastError();
@@ -482,9 +482,9 @@ cudaError_t forward_typed(const CrossParams& p, cudaStream_t stream) {
   // 64 rows a block where that fills the GPU, else 2 rows a block with its
   // four warps taking every fourth key tile
   if (tiles_of(p.s_q, 64) * bh >= sm_count())
-    return run(cross_simt_kernel<T, D, 8, 8, 1>, tiles_of(p.s_q, 64) * bh, p.splits, 256,
+    return run<cross_simt_kernel<T, D, 8, 8, 1>>(tiles_of(p.s_q, 64) * bh, p.splits, 256,
                sizeof(float) * (64 * D + 2 * 32 * PAD + 8 * 8 * 32), p, stream);
-  return run(cross_simt_kernel<T, D, 4, 2, 4>, tiles_of(p.s_q, 2) * bh, p.splits, 128,
+  return run<cross_simt_kernel<T, D, 4, 2, 4>>(tiles_of(p.s_q, 2) * bh, p.splits, 128,
              sizeof(float) * (2 * D + 2 * 128 * PAD + 4 * 2 * 32), p, stream);
 }
 
@@ -496,17 +496,17 @@ cudaError_t backward_typed(const CrossParams& p, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (p.s_q > 0) {
     if (tiles_of(p.s_q, 64) * bh >= sm_count())
-      e = run(cross_simt_dq_kernel<T, D, 8, 8>, tiles_of(p.s_q, 64) * bh, 1, 256,
+      e = run<cross_simt_dq_kernel<T, D, 8, 8>>(tiles_of(p.s_q, 64) * bh, 1, 256,
               sizeof(float) * (2 * 64 * D + 2 * 32 * PAD + 8 * 8 * 32), p, stream);
     else
-      e = run(cross_simt_dq_kernel<T, D, 4, 2>, tiles_of(p.s_q, 8) * bh, 1, 128,
+      e = run<cross_simt_dq_kernel<T, D, 4, 2>>(tiles_of(p.s_q, 8) * bh, 1, 128,
               sizeof(float) * (2 * 8 * D + 2 * 32 * PAD + 4 * 2 * 32), p, stream);
   }
   if (e != cudaSuccess || p.s_kv == 0) return e;
   if (tiles_of(p.s_kv, 64) * bk >= sm_count())
-    return run(cross_simt_dkv_kernel<T, D, 8, 8>, tiles_of(p.s_kv, 64) * bk, 1, 256,
+    return run<cross_simt_dkv_kernel<T, D, 8, 8>>(tiles_of(p.s_kv, 64) * bk, 1, 256,
                sizeof(float) * (2 * 64 * D + 2 * 32 * PAD + 2 * 8 * 8 * 32), p, stream);
-  return run(cross_simt_dkv_kernel<T, D, 4, 2>, tiles_of(p.s_kv, 8) * bk, 1, 128,
+  return run<cross_simt_dkv_kernel<T, D, 4, 2>>(tiles_of(p.s_kv, 8) * bk, 1, 128,
              sizeof(float) * (2 * 8 * D + 2 * 32 * PAD + 2 * 4 * 2 * 32), p, stream);
 }
 

@@ -104,7 +104,6 @@ struct RotaryParams {
   int pair_start[CPATTN_MAX_ROTARY_AXES];
   int rotary_pairs;        // pairs that turn (the rest of the features is copied)
   int interleaved, inverse;
-  int token_inner;         // walk order of a block's rows: tokens or heads innermost
   float2 freq[CPATTN_MAX_ROTARY_DIM / 2];   // turns per position, hi + lo
   Span x_span[kMaxPermuteBatch], y_span[kMaxPermuteBatch], pos_span;   // (CPATTN_CHECK builds)
   unsigned int* err;
