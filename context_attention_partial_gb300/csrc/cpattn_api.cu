@@ -101,8 +101,9 @@ int64_t tma_stride(const cpattn_tensor* t, int dim, int64_t dense) {
 }
 
 // 4-D map over a [B, H, S, D] tensor: dims (D, S, H, B), box (128 bytes of D,
-// box_rows rows, 1, 1), 128-byte swizzle, zero fill out of bounds.
-cpattn_status make_tmap(CUtensorMap* m, const cpattn_tensor* t, int box_rows) {
+// box_rows rows, 1, 1), 128-byte swizzle, zero fill out of bounds; with
+// half_rows, 64 bytes of D and no swizzle.
+cpattn_status make_tmap(CUtensorMap* m, const cpattn_tensor* t, int box_rows, bool half_rows = false) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return CPATTN_ERR_CUDA;
   const int eb = elem_bytes(t->dtype);
@@ -113,12 +114,13 @@ cpattn_status make_tmap(CUtensorMap* m, const cpattn_tensor* t, int box_rows) {
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)S, (cuuint64_t)H, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)(ss * eb), (cuuint64_t)(sh * eb),
                                  (cuuint64_t)(sb * eb)};
-  const cuuint32_t box[4] = {(cuuint32_t)(128 / eb), (cuuint32_t)box_rows, 1u, 1u};
+  const cuuint32_t box[4] = {(cuuint32_t)((half_rows ? 64 : 128) / eb), (cuuint32_t)box_rows, 1u, 1u};
   const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   const CUtensorMapDataType dt =
       t->dtype == CPATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   const CUresult r = enc(m, dt, 4, t->data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         half_rows ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
@@ -760,11 +762,12 @@ cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor
   if (p.splits > 0 && cross_few(q, k)) {
     e = cpattn::launch_cross_few(D, p, cs);
   } else if (p.splits > 0 && dt == InDtype::BF16) {
-    CUtensorMap tm_q, tm_k, tm_v;
+    CUtensorMap tm_q, tm_k, tm_v, tm_o;
     if ((st = make_tmap(&tm_q, q, 128)) != CPATTN_OK) return st;
     if ((st = make_tmap(&tm_k, k, 128)) != CPATTN_OK) return st;
     if ((st = make_tmap(&tm_v, v, 128)) != CPATTN_OK) return st;
-    e = cpattn::launch_cross_fwd(D, tm_q, tm_k, tm_v, p, cs);
+    if ((st = make_tmap(&tm_o, out, 32)) != CPATTN_OK) return st;
+    e = cpattn::launch_cross_fwd(D, tm_q, tm_k, tm_v, tm_o, p, cs);
   } else if (p.splits > 0) {
     e = cpattn::launch_cross_simt(dt, D, p, cs);
   }
@@ -812,19 +815,22 @@ cpattn_status cpattn_cross_attention_backward(const cpattn_tensor* q, const cpat
   const InDtype dt = q->dtype == CPATTN_BF16 ? InDtype::BF16 : InDtype::F32;
   const int D = static_cast<int>(q->shape[3]);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  CUtensorMap tm_q, tm_k, tm_v, tm_g;
-  const bool tensor_cores = dt == InDtype::BF16 && rows && keys;
-  if (tensor_cores) {
-    if ((st = make_tmap(&tm_q, q, 128)) != CPATTN_OK) return st;
-    if ((st = make_tmap(&tm_k, k, 128)) != CPATTN_OK) return st;
-    if ((st = make_tmap(&tm_v, v, 128)) != CPATTN_OK) return st;
-    if ((st = make_tmap(&tm_g, dout, 128)) != CPATTN_OK) return st;
-  }
   cudaError_t e = cudaSuccess;
-  if (rows) e = cpattn::launch_cross_delta(dt, D, p, cs);
-  if (e == cudaSuccess)
-    e = tensor_cores ? cpattn::launch_cross_bwd(D, tm_q, tm_k, tm_v, tm_g, p, cross_delta_floats(q), cs)
-                     : cpattn::launch_cross_simt_backward(dt, D, p, cs);
+  if (dt == InDtype::BF16 && rows && keys) {
+    cpattn::CrossBwdMaps m;
+    if ((st = make_tmap(&m.q, q, 128)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&m.k, k, 128)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&m.v, v, 128)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&m.out, out, 128)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&m.dout, dout, 128)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&m.dq, dq, 32, D == 64)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&m.dk, dk, 32)) != CPATTN_OK) return st;
+    if ((st = make_tmap(&m.dv, dv, 32)) != CPATTN_OK) return st;
+    e = cpattn::launch_cross_bwd(D, m, p, cross_delta_floats(q), cs);
+  } else {
+    if (rows) e = cpattn::launch_cross_delta(dt, D, p, cs);
+    if (e == cudaSuccess) e = cpattn::launch_cross_simt_backward(dt, D, p, cs);
+  }
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 

@@ -53,17 +53,21 @@ cudaError_t cross_set_up(K kernel, size_t smem, std::atomic<unsigned long long>&
 }
 
 // bf16 inputs, D 64 or 128, on the tensor cores (s_kv >= 1; the maps' boxes
-// have 128 rows).
+// have 128 rows, the output's 32).
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                             const CUtensorMap& tm_v, const CrossParams& p, cudaStream_t stream);
+                             const CUtensorMap& tm_v, const CUtensorMap& tm_o, const CrossParams& p,
+                             cudaStream_t stream);
 // the same for at most kCrossFewRows query rows a key head (s_q * H / H_kv)
 constexpr int kCrossFewRows = 64;
 cudaError_t launch_cross_few(int head_dim, const CrossParams& p, cudaStream_t stream);
-// its gradient (s_q, s_kv >= 1; delta at the workspace's start, partial sums of
-// dk and dv `partials` floats into it when p.splits > 1)
-cudaError_t launch_cross_bwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                             const CUtensorMap& tm_v, const CUtensorMap& tm_g, const CrossParams& p,
-                             int64_t partials, cudaStream_t stream);
+// its gradient (s_q, s_kv >= 1; the kernels write delta to the workspace's start
+// and, when p.splits > 1, partial sums of dk and dv `partials` floats into it;
+// the outputs' maps have boxes of 32 rows, dq's of 32 columns, dense, at D = 64)
+struct CrossBwdMaps {
+  CUtensorMap q, k, v, out, dout, dq, dk, dv;
+};
+cudaError_t launch_cross_bwd(int head_dim, const CrossBwdMaps& maps, const CrossParams& p, int64_t partials,
+                             cudaStream_t stream);
 // parts of the query axis for key_units 128-key tiles that walk `steps`
 // 128-row query tiles each
 int cross_backward_parts(int64_t key_units, int64_t steps);

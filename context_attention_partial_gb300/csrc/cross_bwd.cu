@@ -16,21 +16,24 @@
 //
 // Roles (12 warps): warps 0-7 elementwise, two warpgroups on the same 128 TMEM
 // lanes taking 64 of the tile's 128 columns each; warp 8 TMA producer, warp 9
-// MMA issuer, warp 10 row statistics (dk/dv kernel).
+// MMA issuer; row statistics by warps 10-11 (dq kernel: lse and delta of the
+// next unit while this one runs, delta also to the workspace) or warp 10.
 // TMEM columns, dq:     S 0 | dP 128 | dQ 256 | dS 384, 448 (two buffers)
 //               dk, dv: S^T 0 | dP^T 128, then P^T and dS^T over it | dV, dK 256..
 // The next step's S is issued as soon as this step's S is in registers, so the
 // exponentials run under dQ (or dV and dK) and the products under the
 // elementwise work.
+// Shared memory holds seven 32 KB tiles at D = 128.  dq: Q, dO, three K and two
+// V tiles -- K_t is held until dQ_t, while S_{t+1} already needs K_{t+1}, so
+// two K tiles would expose every load (3710 cycles a step); a unit's output
+// leaves through its last K tile.  dk, dv: K, V, and five Q / dO tiles in turn
+// (two whole pairs exposed 960 of 3400 cycles a step).
 #include <cuda_bf16.h>
 
 #include <atomic>
 #include <cmath>
 
-#include "cross.cuh"
-#include "ptx.cuh"
-#include "tile_ops.cuh"
-#include "tmem_ops.cuh"
+#include "cross_ops.cuh"
 
 namespace cpattn {
 namespace {
@@ -48,22 +51,22 @@ constexpr unsigned kErrProducer = 1u, kErrMma = 2u, kErrSoftmax = 4u, kErrStats 
 template <int D>
 struct Cfg {
   static constexpr int ROW = D * 2;                    // bytes
-  static constexpr int NKB = ROW / 128;                // 128-byte column blocks
   static constexpr int TILE = kBM * ROW;
   static constexpr int QK = ROW / 32, PV = kBM / 16;   // MMAs over D, over a tile's rows
   static constexpr uint32_t IDESC_S = make_idesc(1, false, kBM, kBM);
   static constexpr uint32_t IDESC_G = make_idesc(1, true, kBM, D);
-  // dq kernel: K, V tiles in a ring, Q and dO of a unit
-  static constexpr int RING = D == 128 ? 4 : 8;
-  static constexpr int DQ_BARS = 2 * RING + 11;
-  static constexpr int STAGING = 8 * 32 * (D / 2) * 2; // 32 rows x D / 2 columns per warp
-  static constexpr int DQ_SMEM = 1024 + (2 + RING) * TILE + STAGING + DQ_BARS * 8 + 16;
-  // dk, dv kernel: K, V tiles, stages of a Q and a dO tile with row statistics
-  static constexpr int STAGES = D == 128 ? 2 : 4;
-  static constexpr int STATS = 2 * kBM * 4;            // lse2, delta of a stage
-  static constexpr int KV_BARS = 4 * STAGES + 7;
-  static constexpr int KV_SMEM = 1024 + (2 + 2 * STAGES) * TILE + STAGES * STATS + KV_BARS * 8 + 16;
+  static constexpr int STATS = 2 * kBM * 4;            // -lse log2e and delta of 128 rows
+  // dq kernel: Q, dO of a unit, rings of K and of V tiles, statistics of two units
+  static constexpr int KR = D == 128 ? 3 : 5, VR = D == 128 ? 2 : 4;
+  static constexpr int DQ_BARS = 2 * KR + 2 * VR + 16;
+  static constexpr int DQ_SMEM = (2 + KR + VR) * TILE + 2 * STATS + DQ_BARS * 8 + 16;
+  // dk, dv kernel: K, V tiles, a ring of Q and dO tiles, statistics of two steps
+  static constexpr int RING = D == 128 ? 5 : 9;
+  static constexpr int KV_BARS = 2 * RING + 11;
+  static constexpr int KV_SMEM = (2 + RING) * TILE + 2 * STATS + KV_BARS * 8 + 16;
+  static constexpr int PART_ROW = D * 4 + 16;          // staged fp32 row, padded against bank conflicts
   static_assert(DQ_SMEM <= 227 * 1024 && KV_SMEM <= 227 * 1024, "shared memory");
+  static_assert(8 * 32 * PART_ROW <= RING * TILE && 8 * 4096 * (D / 64) <= RING * TILE, "staging");
 };
 
 // [rows x D] x [rows x D]^T: both tiles as TMA wrote them, row by row
@@ -95,74 +98,96 @@ __device__ __forceinline__ void mma_cols(uint32_t d, F a_col, uint32_t b_addr, u
   mma_group<C::PV, false>(d, a, b, static_cast<uint32_t>(base >> 32), C::IDESC_G, acc);
 }
 
-template <int D>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int row, int h, int b,
-                                          uint64_t pol) {
-  for (int kb = 0; kb < Cfg<D>::NKB; ++kb)
-    tma_load_4d_hint(dst + kb * kBM * 128, tm, bar, kb * 64, row, h, b, pol);
-}
+// ------------------------------------------------------------------ dq
+struct DqUnit {
+  int b, h, q0, len, tiles;
+};
 
-// A warp's 32 rows x N columns (fp32 in registers, one row per lane) as bf16
-// through its staging area (16-byte chunks XOR-swizzled by row) to rows
-// row0.. of a tensor, columns from c0; rows at or past `rows` are not written.
-template <int N>
-__device__ __forceinline__ void store_rows(const CrossParams& p, const CrossTensor& t, uint8_t* stage,
-                                           const uint32_t (&o)[N], float f, int b, int h, int row0, int rows, int c0,
-                                           uint64_t pol) {
-  constexpr int CH = N / 8;   // chunks of a row
-  const int lane = threadIdx.x % 32;
-  __syncwarp();
-  uint4* srow = reinterpret_cast<uint4*>(stage) + lane * CH;
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    uint32_t x[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = pack_bf16x2(u2f(o[8 * i + 2 * e]) * f, u2f(o[8 * i + 2 * e + 1]) * f);
-    srow[i ^ (lane % CH)] = make_uint4(x[0], x[1], x[2], x[3]);
+// Walks this CTA's units, blockIdx.x, blockIdx.x + gridDim.x, ..., query tile
+// fastest, then head and batch; the grid's size is added digit by digit.
+struct DqWalk {
+  int q, h, b, dq, dh, db, q_tiles;
+  __device__ explicit DqWalk(const CrossParams& p) {
+    q_tiles = ceil_div(p.s_q, kBM);
+    auto split = [&](uint32_t u, int& q_, int& h_, int& b_) {
+      const uint32_t r = u / q_tiles;
+      q_ = static_cast<int>(u - r * q_tiles);
+      b_ = static_cast<int>(r / p.heads);
+      h_ = static_cast<int>(r - b_ * p.heads);
+    };
+    split(blockIdx.x, q, h, b);
+    split(gridDim.x, dq, dh, db);
   }
-  __syncwarp();
-  uint8_t* out = static_cast<uint8_t*>(t.data) + (b * t.s[0] + h * t.s[1]) * 2;
-#pragma unroll
-  for (int it = 0; it < CH; ++it) {
-    const int idx = it * 32 + lane, r = idx / CH, c = idx % CH;
-    if (row0 + r < rows) {
-      const uint4 val = reinterpret_cast<const uint4*>(stage)[r * CH + (c ^ (r % CH))];
-      uint8_t* dst = out + (static_cast<int64_t>(row0 + r) * t.s[2] + c0) * 2 + c * 16;
-      if (CPATTN_IN(t.span, dst, 16, p.err)) st_global_v4_hint(dst, val, pol);
+  __device__ bool more(const CrossParams& p) const { return b < p.batch; }
+  __device__ void step(const CrossParams& p) {
+    q += dq;
+    h += dh;
+    b += db;
+    if (q >= q_tiles) {
+      q -= q_tiles;
+      ++h;
+    }
+    if (h >= p.heads) {
+      h -= p.heads;
+      ++b;
     }
   }
-}
+  __device__ DqUnit unit(const CrossParams& p) const {
+    const int len = cross_length(p, b);
+    return {b, h, q * kBM, len, ceil_div(len, kBM)};
+  }
+  // Moves to the first unit with keys at or after this one.
+  __device__ bool with_keys(const CrossParams& p, DqUnit& w) {
+    for (; more(p); step(p)) {
+      w = unit(p);
+      if (w.tiles > 0) return true;
+    }
+    return false;
+  }
+};
 
-// ------------------------------------------------------------------ dq
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
-                    const __grid_constant__ CrossParams p, const int64_t units) {
+                    const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CrossParams p) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  const uint32_t sQ = smem_addr(smem), sG = sQ + C::TILE, sKV = sG + C::TILE;
-  uint8_t* staging = smem + (2 + C::RING) * C::TILE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::STAGING);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (!tiles_aligned(p, smem)) return;
+  const uint32_t sQ = smem_addr(smem), sG = sQ + C::TILE, sK = sG + C::TILE, sV = sK + C::KR * C::TILE;
+  float* stats = reinterpret_cast<float*>(smem + (2 + C::KR + C::VR) * C::TILE);   // [2][-lse log2e, delta][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stats + 2 * C::STATS / 4);
   const uint32_t bar0 = smem_addr(bars);
-  auto bar_full = [&](int s) { return bar0 + 8u * s; };
-  auto bar_empty = [&](int s) { return bar0 + 8u * (C::RING + s); };
-  const uint32_t B = bar0 + 8u * (2 * C::RING);
+  auto k_full = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto k_empty = [&](uint32_t s) { return bar0 + 8u * (C::KR + s); };
+  auto v_full = [&](uint32_t s) { return bar0 + 8u * (2 * C::KR + s); };
+  auto v_empty = [&](uint32_t s) { return bar0 + 8u * (2 * C::KR + C::VR + s); };
+  const uint32_t B = bar0 + 8u * (2 * C::KR + 2 * C::VR);
   const uint32_t BAR_Q = B, BAR_G = B + 8, BAR_QFREE = B + 16, BAR_GFREE = B + 24, BAR_S = B + 32, BAR_DP = B + 40,
                  BAR_SREAD = B + 48, BAR_DPREAD = B + 56, BAR_DS = B + 64, BAR_DQ = B + 72, BAR_DRAIN = B + 80;
+  auto st_full = [&](uint32_t s) { return B + 88 + 8u * s; };
+  auto st_empty = [&](uint32_t s) { return B + 104 + 8u * s; };
+  const uint32_t BAR_OUT = B + 120;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::DQ_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
   const int lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::RING; ++s) {
-      mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 1);
+    for (int s = 0; s < C::KR; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+    }
+    for (int s = 0; s < C::VR; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
     }
     for (uint32_t x : {BAR_Q, BAR_G, BAR_QFREE, BAR_GFREE, BAR_S, BAR_DP, BAR_DQ, BAR_DRAIN}) mbar_init(x, 1);
-    for (uint32_t x : {BAR_SREAD, BAR_DPREAD, BAR_DS}) mbar_init(x, 8);   // one arrival per elementwise warp
+    for (uint32_t x : {BAR_SREAD, BAR_DPREAD, BAR_DS, BAR_OUT}) mbar_init(x, 8);   // one arrival per elementwise warp
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(st_full(s), 2);    // one arrival per statistics warp
+      mbar_init(st_empty(s), 8);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -172,28 +197,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     tma_prefetch_desc(&tm_g);
+    tma_prefetch_desc(&tm_dq);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  // every wait of a warp is voted on, so its lanes stay together
   auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) {
     const bool r = mbar_wait(bar, parity, abort_flag, p.timeout_ns, p.err, code);
     return __all_sync(0xffffffffu, r) != 0;
-  };
-  const int q_tiles = ceil_div(p.s_q, kBM);
-  struct Unit {
-    int b, h, q0, len, tiles;
-  };
-  auto unit_at = [&](int64_t u) {
-    Unit w;
-    w.q0 = static_cast<int>(u % q_tiles) * kBM;
-    u /= q_tiles;
-    w.h = static_cast<int>(u % p.heads);
-    w.b = static_cast<int>(u / p.heads);
-    w.len = cross_length(p, w.b);
-    w.tiles = ceil_div(w.len, kBM);
-    return w;
   };
 
   if (warp >= 8) {
@@ -201,92 +214,125 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = elect_one();
     if (warp == kWarpProducer) {
       const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
-      int ld = 0, nq = 0, ng = 0;
+      uint32_t ld = 0, nq = 0, ng = 0;   // K tiles (and V tiles) requested, Q and dO tiles
+      uint32_t nv = 0;
       bool ok = p.fault_skip_kv == 0;
-      for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const Unit w = unit_at(u);
+      DqWalk walk(p), ahead(p);
+      DqUnit w, wa;
+      // Q, dO and O two units ahead into L2: the statistics warps read O and dO
+      // one unit ahead, with few loads in flight
+      auto prefetch = [&]() {
+        if (ahead.with_keys(p, wa) && leader) {
+          prefetch_tile<D>(&tm_g, wa.q0, wa.h, wa.b);
+          prefetch_tile<D>(&tm_o, wa.q0, wa.h, wa.b);
+          prefetch_tile<D>(&tm_q, wa.q0, wa.h, wa.b);
+        }
+        __syncwarp();
+        ahead.step(p);
+      };
+      if (ok) prefetch();
+      if (ok) prefetch();
+      while (ok && walk.with_keys(p, w)) {
         const int hk = w.h / (p.heads / p.kv_heads);
-        for (int x = 0; x < 2 * w.tiles && ok; ++x) {
-          const int s = ld % C::RING;
-          ok = wait_all(bar_empty(s), ((ld / C::RING) & 1) ^ 1, kErrProducer);
+        prefetch();
+        for (int j = 0; j < w.tiles && ok; ++j) {
+          ok = wait_all(k_empty(ld % C::KR), ((ld / C::KR) & 1) ^ 1, kErrProducer);
           if (!ok) break;
           if (leader) {
-            mbar_arrive_expect_tx(bar_full(s), C::TILE);
-            load_tile<D>(sKV + s * C::TILE, x % 2 ? &tm_v : &tm_k, bar_full(s), (x / 2) * kBM, hk, w.b, pol_kv);
+            mbar_arrive_expect_tx(k_full(ld % C::KR), C::TILE);
+            load_tile<D>(sK + (ld % C::KR) * C::TILE, &tm_k, k_full(ld % C::KR), j * kBM, hk, w.b, pol_kv);
           }
           __syncwarp();
           ++ld;
-          if (x < 2) {   // Q after the first K tile, dO after the first V tile
-            int& n = x ? ng : nq;
-            ok = wait_all(x ? BAR_GFREE : BAR_QFREE, (n & 1) ^ 1, kErrProducer);
+          if (j == 0) {
+            ok = wait_all(BAR_QFREE, (nq & 1) ^ 1, kErrProducer);
             if (!ok) break;
             if (leader) {
-              mbar_arrive_expect_tx(x ? BAR_G : BAR_Q, C::TILE);
-              load_tile<D>(x ? sG : sQ, x ? &tm_g : &tm_q, x ? BAR_G : BAR_Q, w.q0, w.h, w.b, pol_q);
+              mbar_arrive_expect_tx(BAR_Q, C::TILE);
+              load_tile<D>(sQ, &tm_q, BAR_Q, w.q0, w.h, w.b, pol_q);
             }
             __syncwarp();
-            ++n;
+            ++nq;
+          }
+          ok = wait_all(v_empty(nv % C::VR), ((nv / C::VR) & 1) ^ 1, kErrProducer);
+          if (!ok) break;
+          if (leader) {
+            mbar_arrive_expect_tx(v_full(nv % C::VR), C::TILE);
+            load_tile<D>(sV + (nv % C::VR) * C::TILE, &tm_v, v_full(nv % C::VR), j * kBM, hk, w.b, pol_kv);
+          }
+          __syncwarp();
+          ++nv;
+          if (j == 0) {
+            ok = wait_all(BAR_GFREE, (ng & 1) ^ 1, kErrProducer);
+            if (!ok) break;
+            if (leader) {
+              mbar_arrive_expect_tx(BAR_G, C::TILE);
+              load_tile<D>(sG, &tm_g, BAR_G, w.q0, w.h, w.b, pol_q);
+            }
+            __syncwarp();
+            ++ng;
           }
         }
+        walk.step(p);
       }
       if (!ok && leader) {
         // leave no copy in flight into this CTA's shared memory
-        for (int x = ld > C::RING ? ld - C::RING : 0; x < ld; ++x)
-          mbar_drain(bar_full(x % C::RING), (x / C::RING) & 1, p.timeout_ns);
+        for (uint32_t x = ld > C::KR ? ld - C::KR : 0; x < ld; ++x)
+          mbar_drain(k_full(x % C::KR), (x / C::KR) & 1, p.timeout_ns);
+        for (uint32_t x = nv > C::VR ? nv - C::VR : 0; x < nv; ++x)
+          mbar_drain(v_full(x % C::VR), (x / C::VR) & 1, p.timeout_ns);
         if (nq > 0) mbar_drain(BAR_Q, (nq - 1) & 1, p.timeout_ns);
         if (ng > 0) mbar_drain(BAR_G, (ng - 1) & 1, p.timeout_ns);
       }
       __syncwarp();
     } else if (warp == kWarpMma) {
-      auto next_unit = [&](int64_t& u, Unit& w) {   // the next one with keys
-        for (; u < units; u += gridDim.x) {
-          w = unit_at(u);
-          if (w.tiles > 0) return true;
-        }
-        return false;
-      };
-      int ld = 0, n = 0, it = 0;   // first load of the unit, units, steps over all units
+      uint32_t n = 0, it = 0;   // units and steps so far
       bool ok = true;
-      int64_t u = blockIdx.x;
-      Unit w;
-      bool have = next_unit(u, w);
-      // S and dP of key tile j (loads at and at + 1) of a unit; K's rows past
-      // the last key become zeros first: dS is 0 there, and 0 * NaN is not
-      auto issue_s = [&](const Unit& x, int j, int at) {
-        const int s = at % C::RING;
-        ok = wait_all(bar_full(s), (at / C::RING) & 1, kErrMma);
+      DqWalk walk(p);
+      DqUnit w;
+      bool have = walk.with_keys(p, w);
+      auto ready = [&](bool now, uint32_t bar, uint32_t parity) {   // after a test of the same phase
+        return __all_sync(0xffffffffu, now) || wait_all(bar, parity, kErrMma);
+      };
+      // S and dP of a unit's key tile j, the g-th step over all units
+      auto issue_s = [&](const DqUnit& x, int j, uint32_t g) {
+        const uint32_t s = g % C::KR, ph = (g / C::KR) & 1;
+        ok = ready(mbar_test(k_full(s), ph), k_full(s), ph);
         if (ok && j == 0) ok = wait_all(BAR_Q, n & 1, kErrMma);
         if (!ok) return;
         const int valid = x.len - j * kBM;
-        if (valid < kBM) {
-          uint8_t* kt = smem + (2 + s) * C::TILE;
-          const int per = (kBM - valid) * 8;
-          for (int i = lane; i < per * C::NKB; i += 32) {
-            const int kb = i / per;
-            *reinterpret_cast<uint4*>(kt + kb * kBM * 128 + (valid * 8 + i - kb * per) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
+        if (valid < kBM) zero_tile_rows<D>(smem + (2 + s) * C::TILE, valid);   // (dS is 0 there, and 0 * NaN is not)
         tc_fence_after();
         if (leader) {
-          mma_rows<D>(tmem, sQ, sKV + s * C::TILE);
+          mma_rows<D>(tmem, sQ, sK + s * C::TILE);
           mma_commit(BAR_S);
           if (j + 1 == x.tiles) mma_commit(BAR_QFREE);
         }
         __syncwarp();
       };
-      auto issue_dp = [&](const Unit& x, int j, int at) {
-        const int s = (at + 1) % C::RING;
-        ok = wait_all(bar_full(s), ((at + 1) / C::RING) & 1, kErrMma);
+      auto issue_dp = [&](const DqUnit& x, int j, uint32_t g) {
+        const uint32_t s = g % C::VR, ph = (g / C::VR) & 1;
+        ok = ready(mbar_test(v_full(s), ph), v_full(s), ph);
         if (ok && j == 0) ok = wait_all(BAR_G, n & 1, kErrMma);
         if (!ok) return;
         tc_fence_after();
         if (leader) {
-          mma_rows<D>(tmem + 128, sG, sKV + s * C::TILE);
+          mma_rows<D>(tmem + 128, sG, sV + s * C::TILE);
           mma_commit(BAR_DP);
-          mma_commit(bar_empty(s));
+          mma_commit(v_empty(s));
           if (j + 1 == x.tiles) mma_commit(BAR_GFREE);
+        }
+        __syncwarp();
+      };
+      auto issue_dq = [&](int j, bool last) {
+        ok = wait_all(BAR_DS, it & 1, kErrMma);
+        if (!ok) return;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t s = it % C::KR, ds = tmem + 384 + (it & 1) * 64;
+          mma_cols<D>(tmem + 256, [&](int kk) { return ds + kk * 8; }, sK + s * C::TILE, j > 0);
+          // (a unit's last K tile is given back once its output has left through it)
+          mma_commit(last ? BAR_DQ : k_empty(s));
         }
         __syncwarp();
       };
@@ -296,38 +342,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n;
       }
       while (have && ok) {
-        int64_t un = u + gridDim.x;
-        Unit wn;
-        const bool more_units = next_unit(un, wn);
-        for (int j = 0; j < w.tiles && ok; ++j, ++it) {
-          const bool more = j + 1 < w.tiles;
-          if (more || more_units) {
-            const Unit& x = more ? w : wn;
-            const int jn = more ? j + 1 : 0, at = ld + 2 * j + 2;
-            ok = wait_all(BAR_SREAD, it & 1, kErrMma);
-            if (!ok) break;
-            issue_s(x, jn, at);
-            if (ok) ok = wait_all(BAR_DPREAD, it & 1, kErrMma);
-            if (!ok) break;
-            issue_dp(x, jn, at);
-            if (!ok) break;
-            if (!more) ++n;
-          }
-          ok = wait_all(BAR_DS, it & 1, kErrMma);
+        DqUnit wn;
+        walk.step(p);
+        const bool more_units = walk.with_keys(p, wn);
+        for (int j = 0; j + 1 < w.tiles && ok; ++j, ++it) {
+          ok = wait_all(BAR_SREAD, it & 1, kErrMma);
           if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-            const int s = (ld + 2 * j) % C::RING;
-            const uint32_t ds = tmem + 384 + (it & 1) * 64;
-            mma_cols<D>(tmem + 256, [&](int kk) { return ds + kk * 8; }, sKV + s * C::TILE, j > 0);
-            mma_commit(bar_empty(s));
-            if (!more) mma_commit(BAR_DQ);
-          }
-          __syncwarp();
+          issue_s(w, j + 1, it + 1);
+          if (ok) ok = wait_all(BAR_DPREAD, it & 1, kErrMma);
+          if (!ok) break;
+          issue_dp(w, j + 1, it + 1);
+          if (ok) issue_dq(j, false);
         }
-        ld += 2 * w.tiles;
+        if (!ok) break;
+        // (the unit's last product before the next unit's first: its tiles may
+        // still be on their way)
+        issue_dq(w.tiles - 1, true);
+        ++it;
+        if (ok && more_units) {
+          issue_s(wn, 0, it);
+          if (ok) issue_dp(wn, 0, it);
+          ++n;
+        }
         have = more_units;
-        u = un;
         w = wn;
       }
       if (!ok && leader) {
@@ -336,26 +373,97 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(BAR_DRAIN, 0, p.timeout_ns);
       }
       __syncwarp();
+    } else {
+      // -------------------------------------------------- row statistics
+      // lse and delta = do . o of the unit's rows, 64 rows a warp; D / 8 lanes
+      // a row, eight row groups in flight
+      constexpr int LPR = D / 8, RPI = 32 / LPR, G = 8;
+      const int r_base = (warp - kWarpStats) * 64;
+      const int c = lane % LPR, r_in = lane / LPR;
+      uint32_t n = 0;
+      bool ok = true;
+      DqWalk walk(p);
+      DqUnit w;
+      while (ok && walk.with_keys(p, w)) {
+        ok = wait_all(st_empty(n & 1), ((n >> 1) & 1) ^ 1, kErrStats);
+        if (!ok) break;
+        float* st = stats + (n & 1) * (C::STATS / 4);
+        const int64_t bh = static_cast<int64_t>(w.b) * p.heads + w.h;
+        const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.out.data) + w.b * p.out.s[0] + w.h * p.out.s[1] + c * 8;
+        const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.dout.data) + w.b * p.dout.s[0] + w.h * p.dout.s[1] + c * 8;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 64; i0 += G * RPI) {
+          uint4 x[G], y[G];
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            const int64_t row = w.q0 + r_base + i0 + i * RPI + r_in;
+            x[i] = y[i] = make_uint4(0, 0, 0, 0);
+            if (row < p.s_q) {
+              const __nv_bfloat16 *ox = o + row * p.out.s[2], *gx = g + row * p.dout.s[2];
+              if (CPATTN_IN(p.out.span, ox, 16, p.err)) x[i] = __ldcs(reinterpret_cast<const uint4*>(ox));
+              if (CPATTN_IN(p.dout.span, gx, 16, p.err)) y[i] = *reinterpret_cast<const uint4*>(gx);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            const __nv_bfloat162 *a = reinterpret_cast<const __nv_bfloat162*>(&x[i]),
+                                 *b = reinterpret_cast<const __nv_bfloat162*>(&y[i]);
+            float d = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = __bfloat1622float2(a[e]), h = __bfloat1622float2(b[e]);
+              d = fmaf(f.x, h.x, fmaf(f.y, h.y, d));
+            }
+#pragma unroll
+            for (int s = LPR / 2; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
+            const int r = r_base + i0 + i * RPI + r_in;
+            if (c == 0) {
+              st[kBM + r] = d;
+              float* dst = p.ws + bh * p.s_q + w.q0 + r;
+              if (w.q0 + r < p.s_q && CPATTN_IN(p.ws_span, dst, 4, p.err)) *dst = d;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = r_base + i * 32 + lane;
+          const float* l = static_cast<const float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + (w.q0 + r) * p.lse.s[2];
+          float v = -INFINITY;   // (rows past the end: P = 0)
+          if (w.q0 + r < p.s_q && CPATTN_IN(p.lse.span, l, 4, p.err)) v = -*l * kLog2e;
+          st[r] = v;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(st_full(n & 1));
+        ++n;
+        walk.step(p);
+      }
+      __syncwarp();
     }
   } else {
     regs_increase<kSoftmaxRegs>();
     const int half = warp / 4, quarter = warp % 4;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint64_t pol = l2_policy_evict_first();
-    uint8_t* stage = staging + warp * (C::STAGING / 8);
     const float sl2 = p.scale_log2;
-    int it = 0, n = 0;
+    uint32_t it = 0, n = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const Unit w = unit_at(u);
-      const int row0 = w.q0 + quarter * 32, row = row0 + lane;
-      float neg_lse = -INFINITY, delta = 0.f;   // (rows past the end: P = 0)
-      if (row < p.s_q) {
-        const float* l = static_cast<const float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + row * p.lse.s[2];
-        const float* d = p.ws + (static_cast<int64_t>(w.b) * p.heads + w.h) * p.s_q + row;
-        if (CPATTN_IN(p.lse.span, l, 4, p.err)) neg_lse = -*l * kLog2e;
-        if (CPATTN_IN(p.ws_span, d, 4, p.err)) delta = *d;
+    for (DqWalk walk(p); ok && walk.more(p); walk.step(p)) {
+      const DqUnit w = walk.unit(p);
+      const int row0 = w.q0 + quarter * 32;
+      if (w.tiles == 0) {
+        // a sequence without keys: dq is 0
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dq.data) + w.b * p.dq.s[0] + w.h * p.dq.s[1] +
+                             static_cast<int64_t>(row0 + lane) * p.dq.s[2] + half * (D / 2);
+        for (int i = 0; i < D / 16; ++i)
+          if (row0 + lane < p.s_q && CPATTN_IN(p.dq.span, dst + 8 * i, 16, p.err))
+            *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(0, 0, 0, 0);
+        continue;
       }
+      ok = wait_all(st_full(n & 1), (n >> 1) & 1, kErrSoftmax);
+      if (!ok) break;
+      const float neg_lse = stats[(n & 1) * (C::STATS / 4) + quarter * 32 + lane];
+      const float neg_delta = -stats[(n & 1) * (C::STATS / 4) + kBM + quarter * 32 + lane];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(st_empty(n & 1));
       for (int j = 0; j < w.tiles; ++j, ++it) {
         ok = wait_all(BAR_S, it & 1, kErrSoftmax);
         if (!ok) break;
@@ -379,19 +487,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR_DPREAD);
-        const int valid = w.len - j * kBM - half * 64;   // of this thread's 64 columns
         uint32_t ds[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float x0, x1;
-          fadd2(x0, x1, u2f(g[2 * i]), u2f(g[2 * i + 1]), -delta, -delta);
-          x0 *= u2f(s[2 * i]);
-          x1 *= u2f(s[2 * i + 1]);
-          if (valid < 64) {   // (the same for the whole warpgroup)
-            x0 = 2 * i < valid ? x0 : 0.f;
-            x1 = 2 * i + 1 < valid ? x1 : 0.f;
-          }
+          fadd2(x0, x1, u2f(g[2 * i]), u2f(g[2 * i + 1]), neg_delta, neg_delta);
+          fmul2(x0, x1, x0, x1, u2f(s[2 * i]), u2f(s[2 * i + 1]));
           ds[i] = pack_bf16x2(x0, x1);
+        }
+        const int valid = w.len - j * kBM - half * 64;   // of this thread's 64 columns
+        if (valid < 64) {   // (the same for the whole warpgroup; what was computed there may be NaN)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            ds[i] = 2 * i + 1 < valid ? ds[i] : 2 * i < valid ? ds[i] & 0xFFFFu : 0u;
         }
         tmem_st_x32(lanes + 384 + (it & 1) * 64 + half * 32, ds);
         tmem_wait_st();
@@ -400,21 +508,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(BAR_DS);
       }
       if (!ok) break;
+      ok = wait_all(BAR_DQ, n & 1, kErrSoftmax);
+      if (!ok) break;
+      tc_fence_after();
       uint32_t o[D / 2];
-      if (w.tiles > 0) {
-        ok = wait_all(BAR_DQ, n & 1, kErrSoftmax);
-        if (!ok) break;
-        ++n;
-        tc_fence_after();
-        if constexpr (D == 128)
-          tmem_ld_x64(lanes + 256 + half * 64, o);
-        else
-          tmem_ld_x32(lanes + 256 + half * 32, o);
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 2; ++i) o[i] = 0u;
+      if constexpr (D == 128)
+        tmem_ld_x64(lanes + 256 + half * 64, o);
+      else
+        tmem_ld_x32(lanes + 256 + half * 32, o);
+      // out through the unit's last K tile, which every product has read; the
+      // tile is free once all eight warps' rows have left it
+      const uint32_t slot = (it - 1) % C::KR;
+      store_rows<D / 2>(p, p.dq, &tm_dq, smem + (2 + slot) * C::TILE + warp * (C::TILE / 8), o, p.scale, w.b, w.h, row0,
+                        p.s_q, half * (D / 2));
+      if (lane == 0) {
+        bulk_wait_read();
+        mbar_arrive(BAR_OUT);
       }
-      store_rows<D / 2>(p, p.dq, stage, o, p.scale, w.b, w.h, row0, p.s_q, half * (D / 2), pol);
+      __syncwarp();
+      if (warp == 0) {
+        ok = wait_all(BAR_OUT, n & 1, kErrSoftmax);
+        if (lane == 0) mbar_arrive(k_empty(slot));
+      }
+      ++n;
     }
   }
   tc_fence_before();
@@ -433,47 +549,52 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
+                     const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                      const __grid_constant__ CrossParams p, const int64_t partials) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  const uint32_t sK = smem_addr(smem), sV = sK + C::TILE, sQ = sV + C::TILE;   // stage s: Q, dO at sQ + 2 s TILE
-  uint8_t* stats = smem + (2 + 2 * C::STAGES) * C::TILE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stats + C::STAGES * C::STATS);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (!tiles_aligned(p, smem)) return;
+  const uint32_t sK = smem_addr(smem), sV = sK + C::TILE, sR = sV + C::TILE;
+  uint8_t* ring = smem + 2 * C::TILE;
+  float* stats = reinterpret_cast<float*>(ring + C::RING * C::TILE);   // [2][-lse log2e, -delta][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stats + 2 * C::STATS / 4);
   const uint32_t bar0 = smem_addr(bars);
-  auto bar_full = [&](int s) { return bar0 + 8u * s; };
-  auto bar_empty = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
-  auto bar_stats = [&](int s) { return bar0 + 8u * (2 * C::STAGES + s); };
-  auto bar_stats_empty = [&](int s) { return bar0 + 8u * (3 * C::STAGES + s); };
-  const uint32_t B = bar0 + 8u * (4 * C::STAGES);
+  auto full = [&](uint32_t x) { return bar0 + 8u * (x % C::RING); };
+  auto empty = [&](uint32_t x) { return bar0 + 8u * (C::RING + x % C::RING); };
+  auto phase = [&](uint32_t x) { return (x / C::RING) & 1u; };
+  auto tile = [&](uint32_t x) { return sR + (x % C::RING) * C::TILE; };
+  const uint32_t B = bar0 + 8u * (2 * C::RING);
   const uint32_t BAR_KV = B, BAR_S = B + 8, BAR_DP = B + 16, BAR_SREAD = B + 24, BAR_DS = B + 32, BAR_DONE = B + 40,
                  BAR_DRAIN = B + 48;
+  auto st_full = [&](uint32_t s) { return B + 56 + 8u * s; };
+  auto st_empty = [&](uint32_t s) { return B + 72 + 8u * s; };
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::KV_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
   const int lane = threadIdx.x % 32;
-  const int k_tiles = ceil_div(p.s_kv, kBM), q_tiles = ceil_div(p.s_q, kBM);
-  const int share = p.heads / p.kv_heads;
-  int64_t u = blockIdx.x;
-  const int k0 = static_cast<int>(u % k_tiles) * kBM;
-  u /= k_tiles;
-  const int part = static_cast<int>(u % p.splits);
-  u /= p.splits;
-  const int hk = static_cast<int>(u % p.kv_heads), b = static_cast<int>(u / p.kv_heads);
+  const uint32_t k_tiles = (p.s_kv + kBM - 1) / kBM, q_tiles = (p.s_q + kBM - 1) / kBM;
+  const uint32_t share = p.heads / p.kv_heads;
+  uint32_t u = blockIdx.x, r = u / k_tiles;
+  const int k0 = static_cast<int>(u - r * k_tiles) * kBM;
+  u = r / p.splits;
+  const uint32_t part = r - u * p.splits;
+  const int b = static_cast<int>(u / p.kv_heads), hk = static_cast<int>(u - b * p.kv_heads);
   const int len = cross_length(p, b);
-  const int all = share * q_tiles, per = ceil_div(all, p.splits);
-  const int first = min(part * per, all), steps = k0 < len ? min(per, all - first) : 0;
+  const uint32_t all = share * q_tiles, per = (all + p.splits - 1) / p.splits;
+  const uint32_t first = min(part * per, all), steps = k0 < len ? min(per, all - first) : 0u;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 1);
-      mbar_init(bar_stats(s), 1);
-      mbar_init(bar_stats_empty(s), 8);
+    for (int s = 0; s < C::RING; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
     }
     for (uint32_t x : {BAR_KV, BAR_S, BAR_DP, BAR_DONE, BAR_DRAIN}) mbar_init(x, 1);
     for (uint32_t x : {BAR_SREAD, BAR_DS}) mbar_init(x, 8);   // one arrival per elementwise warp
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(st_full(s), 1);
+      mbar_init(st_empty(s), 8);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -483,14 +604,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     tma_prefetch_desc(&tm_g);
+    tma_prefetch_desc(&tm_dk);
+    tma_prefetch_desc(&tm_dv);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) {
-    const bool r = mbar_wait(bar, parity, abort_flag, p.timeout_ns, p.err, code);
-    return __all_sync(0xffffffffu, r) != 0;
+    const bool ok = mbar_wait(bar, parity, abort_flag, p.timeout_ns, p.err, code);
+    return __all_sync(0xffffffffu, ok) != 0;
   };
 
   if (warp >= 8) {
@@ -499,61 +622,66 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpProducer) {
       const uint64_t pol = l2_policy_evict_last();   // every tile is read again by another CTA
       bool ok = p.fault_skip_kv == 0;
-      int t = 0;
+      uint32_t x = 0;   // Q tile of step t is load 2t, its dO tile load 2t + 1
       if (ok && steps > 0 && leader) {
         mbar_arrive_expect_tx(BAR_KV, 2 * C::TILE);
         load_tile<D>(sK, &tm_k, BAR_KV, k0, hk, b, pol);
         load_tile<D>(sV, &tm_v, BAR_KV, k0, hk, b, pol);
       }
       __syncwarp();
-      for (; t < steps && ok; ++t) {
-        const int s = t % C::STAGES, x = first + t;
-        ok = wait_all(bar_empty(s), ((t / C::STAGES) & 1) ^ 1, kErrProducer);
+      uint32_t g = first / q_tiles, qt = first - g * q_tiles;
+      for (; x < 2 * steps && ok; ++x) {
+        ok = wait_all(empty(x), phase(x) ^ 1, kErrProducer);
         if (!ok) break;
         if (leader) {
-          const int h = hk * share + x / q_tiles, q0 = (x % q_tiles) * kBM;
-          mbar_arrive_expect_tx(bar_full(s), 2 * C::TILE);
-          load_tile<D>(sQ + 2 * s * C::TILE, &tm_q, bar_full(s), q0, h, b, pol);
-          load_tile<D>(sQ + (2 * s + 1) * C::TILE, &tm_g, bar_full(s), q0, h, b, pol);
+          mbar_arrive_expect_tx(full(x), C::TILE);
+          load_tile<D>(tile(x), x % 2 ? &tm_g : &tm_q, full(x), qt * kBM, hk * share + g, b, pol);
         }
         __syncwarp();
+        if (x % 2 == 1 && ++qt == q_tiles) {
+          qt = 0;
+          ++g;
+        }
       }
-      if (!ok && leader && t > 0) {
+      if (!ok && leader && x > 0) {
         // leave no copy in flight into this CTA's shared memory
         mbar_drain(BAR_KV, 0, p.timeout_ns);
-        for (int x = t > C::STAGES ? t - C::STAGES : 0; x < t; ++x)
-          mbar_drain(bar_full(x % C::STAGES), (x / C::STAGES) & 1, p.timeout_ns);
+        for (uint32_t y = x > C::RING ? x - C::RING : 0; y < x; ++y) mbar_drain(full(y), phase(y), p.timeout_ns);
       }
       __syncwarp();
     } else if (warp == kWarpMma) {
       bool ok = true;
-      auto full = [&](int t) { return wait_all(bar_full(t % C::STAGES), (t / C::STAGES) & 1, kErrMma); };
-      auto q_of = [&](int t) { return sQ + 2 * (t % C::STAGES) * C::TILE; };
+      auto ready = [&](bool now, uint32_t bar, uint32_t parity) {   // after a test of the same phase
+        return __all_sync(0xffffffffu, now) || wait_all(bar, parity, kErrMma);
+      };
       if (steps > 0) {
-        ok = wait_all(BAR_KV, 0, kErrMma) && full(0);
+        ok = wait_all(BAR_KV, 0, kErrMma) && wait_all(full(0), 0, kErrMma) && wait_all(full(1), 0, kErrMma);
         if (ok) {
           tc_fence_after();
           if (leader) {
-            mma_rows<D>(tmem, sK, q_of(0));
+            mma_rows<D>(tmem, sK, tile(0));
             mma_commit(BAR_S);
-            mma_rows<D>(tmem + 128, sV, q_of(0) + C::TILE);
+            mma_rows<D>(tmem + 128, sV, tile(1));
             mma_commit(BAR_DP);
           }
           __syncwarp();
         }
       }
-      for (int t = 0; t < steps && ok; ++t) {
+      for (uint32_t t = 0; t < steps && ok; ++t) {
         const bool more = t + 1 < steps;
+        const uint32_t xq = 2 * t + 2, xg = 2 * t + 3;   // the next step's tiles
         if (more) {
-          ok = full(t + 1) && wait_all(BAR_SREAD, t & 1, kErrMma);
+          const bool q_now = mbar_test(full(xq), phase(xq)), s_now = mbar_test(BAR_SREAD, t & 1);
+          ok = ready(q_now, full(xq), phase(xq)) && ready(s_now, BAR_SREAD, t & 1);
           if (!ok) break;
           tc_fence_after();
           if (leader) {
-            mma_rows<D>(tmem, sK, q_of(t + 1));
+            mma_rows<D>(tmem, sK, tile(xq));
             mma_commit(BAR_S);
           }
           __syncwarp();
         }
+        bool g_now = more && mbar_test(full(xg), phase(xg));
         ok = wait_all(BAR_DS, t & 1, kErrMma);
         if (!ok) break;
         tc_fence_after();
@@ -561,17 +689,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 64 of the 128 query columns per warpgroup: P^T in the first half
           // of its dP^T columns, dS^T in the second
           const uint32_t pt = tmem + 128;
-          mma_cols<D>(tmem + 256, [&](int kk) { return pt + (kk / 4) * 64 + (kk % 4) * 8; }, q_of(t) + C::TILE, t > 0);
-          mma_cols<D>(tmem + 256 + D, [&](int kk) { return pt + (kk / 4) * 64 + 32 + (kk % 4) * 8; }, q_of(t), t > 0);
-          mma_commit(bar_empty(t % C::STAGES));
-          if (more) {
-            mma_rows<D>(tmem + 128, sV, q_of(t + 1) + C::TILE);
-            mma_commit(BAR_DP);
-          } else {
-            mma_commit(BAR_DONE);
-          }
+          mma_cols<D>(tmem + 256 + D, [&](int kk) { return pt + (kk / 4) * 64 + 32 + (kk % 4) * 8; }, tile(2 * t), t > 0);
+          mma_commit(empty(2 * t));
+          mma_cols<D>(tmem + 256, [&](int kk) { return pt + (kk / 4) * 64 + (kk % 4) * 8; }, tile(2 * t + 1), t > 0);
+          mma_commit(more ? empty(2 * t + 1) : BAR_DONE);
         }
         __syncwarp();
+        if (more) {
+          ok = ready(g_now, full(xg), phase(xg));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            mma_rows<D>(tmem + 128, sV, tile(xg));
+            mma_commit(BAR_DP);
+          }
+          __syncwarp();
+        }
       }
       if (!ok && leader) {
         // let every MMA already issued finish before TMEM is released
@@ -580,33 +713,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == kWarpStats) {
+      // (the next step's are requested before this step's are handed over)
       bool ok = true;
-      for (int t = 0; t < steps && ok; ++t) {
-        const int s = t % C::STAGES, x = first + t;
-        const int h = hk * share + x / q_tiles, q0 = (x % q_tiles) * kBM;
-        float nl[4], dl[4];
+      uint32_t g = first / q_tiles, qt = first - g * q_tiles;
+      float nl[4], dl[4], nn[4], dn[4];
+      auto fetch = [&](float (&a)[4], float (&d)[4]) {
+        const int h = hk * share + g, q0 = qt * kBM;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = q0 + i * 32 + lane;
-          nl[i] = -INFINITY;   // (rows past the end: P = 0)
-          dl[i] = 0.f;
+          a[i] = INFINITY;   // (rows past the end: P = 0)
+          d[i] = 0.f;
           if (row < p.s_q) {
             const float* l = static_cast<const float*>(p.lse.data) + b * p.lse.s[0] + h * p.lse.s[1] + row * p.lse.s[2];
-            const float* d = p.ws + (static_cast<int64_t>(b) * p.heads + h) * p.s_q + row;
-            if (CPATTN_IN(p.lse.span, l, 4, p.err)) nl[i] = -*l * kLog2e;
-            if (CPATTN_IN(p.ws_span, d, 4, p.err)) dl[i] = -*d;
+            const float* x = p.ws + (static_cast<int64_t>(b) * p.heads + h) * p.s_q + row;
+            if (CPATTN_IN(p.lse.span, l, 4, p.err)) a[i] = *l;
+            if (CPATTN_IN(p.ws_span, x, 4, p.err)) d[i] = *x;
           }
         }
-        ok = wait_all(bar_stats_empty(s), ((t / C::STAGES) & 1) ^ 1, kErrStats);
+        if (++qt == q_tiles) {
+          qt = 0;
+          ++g;
+        }
+      };
+      if (steps > 0) fetch(nl, dl);
+      for (uint32_t t = 0; t < steps && ok; ++t) {
+        if (t + 1 < steps) fetch(nn, dn);
+        ok = wait_all(st_empty(t & 1), ((t >> 1) & 1) ^ 1, kErrStats);
         if (!ok) break;
-        float* st = reinterpret_cast<float*>(stats + s * C::STATS);
+        float* st = stats + (t & 1) * (C::STATS / 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          st[i * 32 + lane] = nl[i];
-          st[kBM + i * 32 + lane] = dl[i];
+          st[i * 32 + lane] = -nl[i] * kLog2e;
+          st[kBM + i * 32 + lane] = -dl[i];
+          nl[i] = nn[i];
+          dl[i] = dn[i];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_stats(s));
+        if (lane == 0) mbar_arrive(st_full(t & 1));
       }
       __syncwarp();
     }
@@ -616,17 +760,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float sl2 = p.scale_log2;
     const int key = k0 + quarter * 32 + lane;
-    const bool ragged = k0 + kBM > len, live = key < len;
+    const bool live = key < len;
     bool ok = true;
-    for (int t = 0; t < steps; ++t) {
-      const int st = t % C::STAGES;
-      const float4* nl = reinterpret_cast<const float4*>(stats + st * C::STATS) + half * 16;
+    for (uint32_t t = 0; t < steps; ++t) {
+      const float4* nl = reinterpret_cast<const float4*>(stats + (t & 1) * (C::STATS / 4)) + half * 16;
       const float4* dl = nl + kBM / 4;
-      ok = wait_all(BAR_S, t & 1, kErrSoftmax);
-      if (ok) ok = wait_all(bar_stats(st), (t / C::STAGES) & 1, kErrSoftmax);
+      ok = wait_all(st_full(t & 1), (t >> 1) & 1, kErrSoftmax);
+      if (ok) ok = wait_all(BAR_S, t & 1, kErrSoftmax);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[64], g[64];
+      uint32_t s[64], g[64], pb[32];
       tmem_ld_x64(lanes + half * 64, s);
       tc_fence_before();
       __syncwarp();
@@ -639,38 +782,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         ffma2(x[2], x[3], u2f(s[4 * i + 2]), u2f(s[4 * i + 3]), sl2, sl2, m.z, m.w);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[4 * i + e] = f2u(ex2_approx(x[e]));
+        pb[2 * i] = pack_bf16x2(u2f(s[4 * i]), u2f(s[4 * i + 1]));
+        pb[2 * i + 1] = pack_bf16x2(u2f(s[4 * i + 2]), u2f(s[4 * i + 3]));
       }
       ok = wait_all(BAR_DP, t & 1, kErrSoftmax);
       if (!ok) break;
       tc_fence_after();
       tmem_ld_x64(lanes + 128 + half * 64, g);
-      uint32_t pb[32], db[32];
+      if (!live) {
+        // a key past the length (its k and v may hold anything): no weight
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pb[i] = 0u;
+      }
+      tmem_st_x32(lanes + 128 + half * 64, pb);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float4 d = dl[i];
         float x[4];
         fadd2(x[0], x[1], u2f(g[4 * i]), u2f(g[4 * i + 1]), d.x, d.y);
         fadd2(x[2], x[3], u2f(g[4 * i + 2]), u2f(g[4 * i + 3]), d.z, d.w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] *= u2f(s[4 * i + e]);
-        pb[2 * i] = pack_bf16x2(u2f(s[4 * i]), u2f(s[4 * i + 1]));
-        pb[2 * i + 1] = pack_bf16x2(u2f(s[4 * i + 2]), u2f(s[4 * i + 3]));
-        db[2 * i] = pack_bf16x2(x[0], x[1]);
-        db[2 * i + 1] = pack_bf16x2(x[2], x[3]);
+        fmul2(x[0], x[1], x[0], x[1], u2f(s[4 * i]), u2f(s[4 * i + 1]));
+        fmul2(x[2], x[3], x[2], x[3], u2f(s[4 * i + 2]), u2f(s[4 * i + 3]));
+        pb[2 * i] = pack_bf16x2(x[0], x[1]);
+        pb[2 * i + 1] = pack_bf16x2(x[2], x[3]);
       }
-      if (ragged && !live) {
-        // a key past the length (its k and v may hold anything): no weight
+      if (!live) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) pb[i] = db[i] = 0u;
+        for (int i = 0; i < 32; ++i) pb[i] = 0u;
       }
-      tmem_st_x32(lanes + 128 + half * 64, pb);
-      tmem_st_x32(lanes + 128 + half * 64 + 32, db);
+      __syncwarp();
+      tmem_st_x32(lanes + 128 + half * 64 + 32, pb);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(BAR_DS);
-        mbar_arrive(bar_stats_empty(st));
+        mbar_arrive(st_empty(t & 1));
       }
     }
     if (ok && steps > 0) {
@@ -678,14 +825,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) tc_fence_after();
     }
     if (ok) {
-      // warpgroup 0 writes dv, warpgroup 1 dk; the Q and dO stages are idle
+      // warpgroup 0 writes dv, warpgroup 1 dk, through the idle ring
       const CrossTensor& t = half ? p.dk : p.dv;
+      const CUtensorMap* tm = half ? &tm_dk : &tm_dv;
       const float f = half ? p.scale : 1.f;
       const bool zero = steps == 0 || !live;
       const int64_t rows = static_cast<int64_t>(p.batch) * p.kv_heads * p.s_kv;
       float* ws = p.ws + partials + (2 * part + (half ? 0 : 1)) * rows * D +
                   ((static_cast<int64_t>(b) * p.kv_heads + hk) * p.s_kv + key) * D;
-      const uint64_t pol = l2_policy_evict_first();
+      uint8_t* row = ring + (warp * 32 + lane) * C::PART_ROW;   // (several parts: a row of fp32 each)
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 64) {
         uint32_t o[64];
@@ -694,17 +842,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 64; ++i) o[i] = zero ? 0u : o[i];
         if (p.splits > 1) {
-          if (key < p.s_kv) {
-            float4* dst = reinterpret_cast<float4*>(ws + c0);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (CPATTN_IN(p.ws_span, dst + i, 16, p.err))
-                dst[i] = make_float4(u2f(o[4 * i]), u2f(o[4 * i + 1]), u2f(o[4 * i + 2]), u2f(o[4 * i + 3]));
-          }
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<uint4*>(row + c0 * 4 + i * 16) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         } else {
-          store_rows<64>(p, t, smem + 2 * C::TILE + warp * 4096, o, f, b, hk, k0 + quarter * 32, p.s_kv, c0, pol);
+          store_rows<64>(p, t, tm, ring + (warp * (D / 64) + c0 / 64) * 4096, o, f, b, hk, k0 + quarter * 32, p.s_kv, c0);
         }
       }
+      if (p.splits > 1 && key < p.s_kv) {
+        // each lane's row leaves by one bulk copy
+        if (CPATTN_IN(p.ws_span, ws, D * 4, p.err)) {
+          fence_proxy_async_smem();
+          bulk_store(ws, smem_addr(row), D * 4);
+          bulk_commit();
+        }
+      }
+      bulk_wait_read();   // (before this CTA's shared memory is given up)
     }
   }
   tc_fence_before();
@@ -758,8 +911,7 @@ cudaError_t set_up(K kernel, int smem, std::atomic<unsigned long long>& ready) {
 }
 
 template <int D>
-cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                         const CUtensorMap& tm_g, const CrossParams& p, int64_t partials, cudaStream_t stream) {
+cudaError_t launch_typed(const CrossBwdMaps& m, const CrossParams& p, int64_t partials, cudaStream_t stream) {
   using C = Cfg<D>;
   static std::atomic<unsigned long long> ready_q{0}, ready_kv{0};
   cudaError_t e = set_up(cross_dq_kernel<D>, C::DQ_SMEM, ready_q);
@@ -767,13 +919,13 @@ cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
   if (e != cudaSuccess) return e;
   const int64_t sms = sm_count();
   const int64_t units = static_cast<int64_t>(p.batch) * p.heads * ((p.s_q + kBM - 1) / kBM);
-  cross_dq_kernel<D><<<static_cast<unsigned>(units < sms ? units : sms), kThreads, C::DQ_SMEM, stream>>>(
-      tm_q, tm_k, tm_v, tm_g, p, units);
   const int64_t ctas = static_cast<int64_t>(p.batch) * p.kv_heads * p.splits * ((p.s_kv + kBM - 1) / kBM);
   const int64_t rows = static_cast<int64_t>(p.batch) * p.kv_heads * p.s_kv, join = (2 * rows * (D / 4) + 255) / 256;
-  if (ctas > 0x7fffffff || join > 0x7fffffff) return cudaErrorInvalidValue;
-  cross_dkv_kernel<D><<<static_cast<unsigned>(ctas), kThreads, C::KV_SMEM, stream>>>(tm_q, tm_k, tm_v, tm_g, p,
-                                                                                       partials);
+  if (units > 0x7fffffff || ctas > 0x7fffffff || join > 0x7fffffff) return cudaErrorInvalidValue;
+  cross_dq_kernel<D><<<static_cast<unsigned>(units < sms ? units : sms), kThreads, C::DQ_SMEM, stream>>>(
+      m.q, m.k, m.v, m.dout, m.out, m.dq, p);
+  cross_dkv_kernel<D><<<static_cast<unsigned>(ctas), kThreads, C::KV_SMEM, stream>>>(m.q, m.k, m.v, m.dout, m.dk, m.dv,
+                                                                                       p, partials);
   if (p.splits > 1) cross_dkv_join_kernel<D><<<static_cast<unsigned>(join), 256, 0, stream>>>(p, partials);
   return cudaGetLastError();
 }
@@ -798,10 +950,9 @@ int cross_backward_parts(int64_t key_units, int64_t steps) {
   return best;
 }
 
-cudaError_t launch_cross_bwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                             const CUtensorMap& tm_g, const CrossParams& p, int64_t partials, cudaStream_t stream) {
-  return head_dim == 64 ? launch_typed<64>(tm_q, tm_k, tm_v, tm_g, p, partials, stream)
-                        : launch_typed<128>(tm_q, tm_k, tm_v, tm_g, p, partials, stream);
+cudaError_t launch_cross_bwd(int head_dim, const CrossBwdMaps& maps, const CrossParams& p, int64_t partials,
+                             cudaStream_t stream) {
+  return head_dim == 64 ? launch_typed<64>(maps, p, partials, stream) : launch_typed<128>(maps, p, partials, stream);
 }
 
 }  // namespace cpattn

@@ -31,10 +31,7 @@
 #include <atomic>
 #include <cmath>
 
-#include "cross.cuh"
-#include "ptx.cuh"
-#include "tile_ops.cuh"
-#include "tmem_ops.cuh"
+#include "cross_ops.cuh"
 
 namespace cpattn {
 namespace {
@@ -53,7 +50,6 @@ constexpr unsigned kErrProducer = 1u, kErrMma = 2u, kErrSoftmax = 4u;
 template <int D>
 struct Cfg {
   static constexpr int ROW = D * 2;                       // bytes
-  static constexpr int NKB = ROW / 128;                   // 128-byte column blocks
   static constexpr int TILE = kBM * ROW;                  // bytes of a Q, K or V tile
   static constexpr int STAGES = D == 128 ? 4 : 8;
   static constexpr int STAGING = 8 * 32 * 128;            // 32 rows x 64 columns bf16 per warp
@@ -73,30 +69,80 @@ struct Unit {
   int tiles, halves;       // key tiles, query tiles with rows
 };
 
-__device__ __forceinline__ Unit unit_at(const CrossParams& p, int64_t u) {
-  const int q_blocks = ceil_div(p.s_q, 2 * kBM);
-  Unit w;
-  w.q0 = static_cast<int>(u % q_blocks) * (2 * kBM);
-  u /= q_blocks;
-  w.part = static_cast<int>(u % p.splits);
-  u /= p.splits;
-  w.h = static_cast<int>(u % p.heads);
-  w.b = static_cast<int>(u / p.heads);
-  const int len = cross_length(p, w.b);
-  const int all = ceil_div(len, kBN), per = ceil_div(all, p.splits);
-  const int t0 = min(w.part * per, all), t1 = min(t0 + per, all);
-  w.k0 = t0 * kBN;
-  w.k1 = min(t1 * kBN, len);
-  w.tiles = t1 - t0;
-  w.halves = p.s_q - w.q0 > kBM ? 2 : 1;
-  return w;
-}
+// Walks this CTA's units, blockIdx.x, blockIdx.x + gridDim.x, ..., query block
+// fastest, then part, head and batch.  A step adds the grid's size digit by
+// digit: divisions at every unit cost some 700 cycles between two units.
+struct UnitWalk {
+  int q, part, h, b;       // digits of the unit
+  int dq, dp, dh, db;      // digits of the grid's size
+  int q_blocks;
+  __device__ void split(const CrossParams& p, uint32_t u, int& q_, int& p_, int& h_, int& b_) const {
+    uint32_t r = u / q_blocks;
+    q_ = static_cast<int>(u - r * q_blocks);
+    u = r / p.splits;
+    p_ = static_cast<int>(r - u * p.splits);
+    b_ = static_cast<int>(u / p.heads);
+    h_ = static_cast<int>(u - b_ * p.heads);
+  }
+  __device__ explicit UnitWalk(const CrossParams& p) {
+    q_blocks = ceil_div(p.s_q, 2 * kBM);
+    split(p, blockIdx.x, q, part, h, b);
+    split(p, gridDim.x, dq, dp, dh, db);
+  }
+  __device__ bool more(const CrossParams& p) const { return b < p.batch; }
+  __device__ void step(const CrossParams& p) {
+    q += dq;
+    part += dp;
+    h += dh;
+    b += db;
+    if (q >= q_blocks) {
+      q -= q_blocks;
+      ++part;
+    }
+    if (part >= p.splits) {
+      part -= p.splits;
+      ++h;
+    }
+    if (h >= p.heads) {
+      h -= p.heads;
+      ++b;
+    }
+  }
+  __device__ Unit unit(const CrossParams& p) const {
+    Unit w;
+    w.b = b;
+    w.h = h;
+    w.part = part;
+    w.q0 = q * (2 * kBM);
+    const int len = cross_length(p, b);
+    const int all = ceil_div(len, kBN);
+    int t0 = 0, t1 = all;
+    if (p.splits > 1) {
+      const int per = ceil_div(all, p.splits);
+      t0 = min(part * per, all);
+      t1 = min(t0 + per, all);
+    }
+    w.k0 = t0 * kBN;
+    w.k1 = min(t1 * kBN, len);
+    w.tiles = t1 - t0;
+    w.halves = p.s_q - w.q0 > kBM ? 2 : 1;
+    return w;
+  }
+  // Moves to the first unit with keys at or after this one.
+  __device__ bool with_keys(const CrossParams& p, Unit& w) {
+    for (; more(p); step(p)) {
+      w = unit(p);
+      if (w.tiles > 0) return true;
+    }
+    return false;
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CrossParams p,
-                     const int64_t units) {
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                     const __grid_constant__ CrossParams p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -138,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_o);
   }
   tc_fence_before();
   __syncthreads();
@@ -154,44 +201,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = elect_one();
     if (warp == kWarpProducer) {
       // ---------------------------------------------------------- producer
+      // K tiles on even stages, V tiles on odd ones: the first K alone, then
+      // V_j and the K tile after it (of the next unit behind a unit's last V)
+      // as one pair on the K stage's barrier, so the MMA warp waits once a
+      // step; the very last V on its own.
+      static_assert(C::STAGES % 2 == 0, "K / V pairs");
       const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
       int ld = 0, nq[2] = {0, 0};
+      UnitWalk walk(p);
+      Unit w;
+      const int share = p.heads / p.kv_heads;
+      bool have = walk.with_keys(p, w);
       bool ok = p.fault_skip_kv == 0;
-      for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const Unit w = unit_at(p, u);
-        const int hk = w.h / (p.heads / p.kv_heads);
-        for (int x = 0; x < 2 * w.tiles && ok; ++x) {
-          const int s = ld % C::STAGES;
-          ok = wait_all(bar_empty(s), ((ld / C::STAGES) & 1) ^ 1, kErrProducer);
-          if (!ok) break;
+      auto load_q = [&](const Unit& x) {   // once the previous unit's last Q K^T is done
+        for (int i = 0; i < x.halves; ++i) {
+          ok = wait_all(bar_qfree(i), (nq[i] & 1) ^ 1, kErrProducer);
+          if (!ok) return;
           if (leader) {
-            mbar_arrive_expect_tx(bar_full(s), C::TILE);
-            for (int kb = 0; kb < C::NKB; ++kb)
-              tma_load_4d_hint(sKV + s * C::TILE + kb * kBN * 128, x % 2 ? &tm_v : &tm_k, bar_full(s), kb * 64,
-                               w.k0 + (x / 2) * kBN, hk, w.b, pol_kv);
+            mbar_arrive_expect_tx(bar_q(i), C::TILE);
+            load_tile<D>(sQ + i * C::TILE, &tm_q, bar_q(i), x.q0 + i * kBM, x.h, x.b, pol_q);
           }
           __syncwarp();
-          ++ld;
-          // (the first K tile is requested before the Q tiles, which wait for
-          // the previous unit's last Q K^T)
-          for (int i = 0; x == 0 && i < w.halves && ok; ++i) {
-            ok = wait_all(bar_qfree(i), (nq[i] & 1) ^ 1, kErrProducer);
-            if (!ok) break;
-            if (leader) {
-              mbar_arrive_expect_tx(bar_q(i), C::TILE);
-              for (int kb = 0; kb < C::NKB; ++kb)
-                tma_load_4d_hint(sQ + i * C::TILE + kb * kBM * 128, &tm_q, bar_q(i), kb * 64, w.q0 + i * kBM, w.h,
-                                 w.b, pol_q);
-            }
-            __syncwarp();
-            ++nq[i];
-          }
+          ++nq[i];
         }
+      };
+      if (have && ok) {
+        if (leader) {
+          mbar_arrive_expect_tx(bar_full(0), C::TILE);
+          load_tile<D>(sKV, &tm_k, bar_full(0), w.k0, w.h / share, w.b, pol_kv);
+        }
+        __syncwarp();
+        ld = 1;
+        load_q(w);
+      }
+      while (have && ok) {
+        Unit wn;
+        walk.step(p);
+        const bool more_units = walk.with_keys(p, wn);
+        // (from HBM the next Q tiles arrived some 2000 cycles after they were wanted)
+        if (more_units && leader)
+          for (int i = 0; i < wn.halves; ++i) prefetch_tile<D>(&tm_q, wn.q0 + i * kBM, wn.h, wn.b);
+        for (int j = 0; j < w.tiles && ok; ++j) {
+          const bool in_unit = j + 1 < w.tiles, more = in_unit || more_units;
+          const int sv = ld % C::STAGES, sk = (ld + 1) % C::STAGES;
+          ok = wait_all(bar_empty(sv), ((ld / C::STAGES) & 1) ^ 1, kErrProducer);
+          if (ok && more) ok = wait_all(bar_empty(sk), (((ld + 1) / C::STAGES) & 1) ^ 1, kErrProducer);
+          if (!ok) break;
+          if (leader) {
+            const uint32_t bar = more ? bar_full(sk) : bar_full(sv);
+            mbar_arrive_expect_tx(bar, (more ? 2 : 1) * C::TILE);
+            load_tile<D>(sKV + sv * C::TILE, &tm_v, bar, w.k0 + j * kBN, w.h / share, w.b, pol_kv);
+            if (in_unit)
+              load_tile<D>(sKV + sk * C::TILE, &tm_k, bar, w.k0 + (j + 1) * kBN, w.h / share, w.b, pol_kv);
+            else if (more)
+              load_tile<D>(sKV + sk * C::TILE, &tm_k, bar, wn.k0, wn.h / share, wn.b, pol_kv);
+          }
+          __syncwarp();
+          ld += more ? 2 : 1;
+        }
+        if (ok && more_units) load_q(wn);
+        have = more_units;
+        w = wn;
       }
       if (!ok && leader) {
         // leave no copy in flight into this CTA's shared memory
-        for (int x = ld > C::STAGES ? ld - C::STAGES : 0; x < ld; ++x)
-          mbar_drain(bar_full(x % C::STAGES), (x / C::STAGES) & 1, p.timeout_ns);
+        for (int x = ld > C::STAGES ? ld - C::STAGES : 0; x < ld; ++x) {
+          if (x % 2 == 0)
+            mbar_drain(bar_full(x % C::STAGES), (x / C::STAGES) & 1, p.timeout_ns);
+          else if (x + 1 >= ld)   // (a last V tile alone)
+            mbar_drain(bar_full(x % C::STAGES), 0, p.timeout_ns);
+        }
         for (int i = 0; i < 2; ++i)
           if (nq[i] > 0) mbar_drain(bar_q(i), (nq[i] - 1) & 1, p.timeout_ns);
       }
@@ -201,49 +280,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024), k_desc = smem_desc_sw128(sKV, 16, 1024);
       const uint64_t v_desc = smem_desc_sw128(sKV, kBN * 128, 1024);
       const uint32_t hi = static_cast<uint32_t>(q_desc >> 32);   // (shared by all: low words hold the address)
-      auto issue_qk = [&](int i, int stage) {
-        uint32_t a[C::QK], b[C::QK];
-#pragma unroll
-        for (int kk = 0; kk < C::QK; ++kk) {
-          const uint32_t off = ((kk / 4) * (kBM * 128) + (kk % 4) * 32) >> 4;
-          a[kk] = static_cast<uint32_t>(q_desc) + ((i * C::TILE) >> 4) + off;
-          b[kk] = static_cast<uint32_t>(k_desc) + ((stage * C::TILE) >> 4) + off;
-        }
-        mma_group<C::QK, true>(tmem + i * kBN, a, b, hi, C::IDESC_QK, 0u);
-      };
-      auto issue_pv = [&](int i, int stage, uint32_t acc) {
-        uint32_t a[C::PV], b[C::PV];
-#pragma unroll
-        for (int kk = 0; kk < C::PV; ++kk) {
-          a[kk] = tmem + i * kBN + kk * 8;
-          b[kk] = static_cast<uint32_t>(v_desc) + ((stage * C::TILE + kk * 16 * 128) >> 4);
-        }
-        mma_group<C::PV, false>(tmem + C::O_COL + i * D, a, b, hi, C::IDESC_PV, acc);
-      };
-      auto next_unit = [&](int64_t& u, Unit& w) {   // the next one with keys
-        for (; u < units; u += gridDim.x) {
-          w = unit_at(p, u);
-          if (w.tiles > 0) return true;
-        }
-        return false;
-      };
-      int ld = 0;                    // load index of the unit's first K tile
-      int nq[2] = {0, 0}, np[2] = {0, 0};
+      // Tests come before the descriptors are built, waits only where a test
+      // failed: a wait costs this warp some 190 cycles beside the softmax
+      // warps of its SM sub-partition, and the tensor pipe's queue is only a
+      // few MMAs deep (four waits a step: 3310 cycles a step instead of 2400).
+      uint32_t g = 0;                // key tiles so far, over all units
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
       bool ok = true;
-      int64_t u = blockIdx.x;
+      UnitWalk walk(p);
       Unit w;
-      bool have = next_unit(u, w);
-      // a unit's first scores, query tile by query tile
-      auto first_qk = [&](const Unit& x, int at) {
-        const int s = at % C::STAGES;
-        ok = ok && wait_all(bar_full(s), (at / C::STAGES) & 1, kErrMma);
+      bool have = walk.with_keys(p, w);
+      // a unit's first scores, query tile by query tile (its K tile is here)
+      auto first_qk = [&](const Unit& x, uint32_t at) {
+        const uint32_t s = at % C::STAGES;
         for (int i = 0; i < x.halves && ok; ++i) {
           ok = wait_all(bar_q(i), nq[i] & 1, kErrMma);
           if (!ok) return;
           ++nq[i];
+          uint32_t a[C::QK], b[C::QK];
+#pragma unroll
+          for (int kk = 0; kk < C::QK; ++kk) {
+            const uint32_t off = ((kk / 4) * (kBM * 128) + (kk % 4) * 32) >> 4;
+            a[kk] = static_cast<uint32_t>(q_desc) + ((i * C::TILE) >> 4) + off;
+            b[kk] = static_cast<uint32_t>(k_desc) + ((s * C::TILE) >> 4) + off;
+          }
           tc_fence_after();
           if (leader) {
-            issue_qk(i, s);
+            mma_group<C::QK, true>(tmem + i * kBN, a, b, hi, C::IDESC_QK, 0u);
             mma_commit(bar_s(i));
             if (x.tiles == 1) mma_commit(bar_qfree(i));
             if (i == x.halves - 1) mma_commit(bar_empty(s));
@@ -251,54 +314,82 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       };
-      if (have) first_qk(w, ld);
+      if (have) {
+        ok = wait_all(bar_full(0), 0, kErrMma);
+        if (ok) first_qk(w, 0);
+      }
       while (have && ok) {
-        int64_t un = u + gridDim.x;
         Unit wn;
-        const bool more_units = next_unit(un, wn);
-        for (int j = 0; j < w.tiles && ok; ++j) {
-          const int lv = ld + 2 * j + 1, sv = lv % C::STAGES;
-          const int lk = ld + 2 * j + 2, sk = lk % C::STAGES;
-          const bool more = j + 1 < w.tiles;
-          ok = wait_all(bar_full(sv), (lv / C::STAGES) & 1, kErrMma);
-          if (ok && more) ok = wait_all(bar_full(sk), (lk / C::STAGES) & 1, kErrMma);
+        walk.step(p);
+        const bool more_units = walk.with_keys(p, wn);
+        for (int j = 0; j < w.tiles; ++j, ++g) {
+          const bool more = j + 1 < w.tiles, two = w.halves == 2;
+          const uint32_t sv = (2 * g + 1) % C::STAGES, lk = 2 * g + 2, sk = lk % C::STAGES;
+          const bool pair = more || more_units;
+          const uint32_t kv_bar = pair ? bar_full(sk) : bar_full(sv), kv_ph = pair ? (lk / C::STAGES) & 1 : 0u;
+          const bool kv_now = mbar_test(kv_bar, kv_ph);
+          const bool p0_now = mbar_test(bar_p(0), np[0] & 1);
+          const uint32_t vb = static_cast<uint32_t>(v_desc) + ((sv * C::TILE) >> 4);
+          const uint32_t kb = static_cast<uint32_t>(k_desc) + ((sk * C::TILE) >> 4);
+          uint32_t vd[C::PV], kd[C::QK], qd[C::QK], pa[C::PV];
+#pragma unroll
+          for (int kk = 0; kk < C::PV; ++kk) {
+            vd[kk] = vb + ((kk * 16 * 128) >> 4);
+            pa[kk] = tmem + kk * 8;
+          }
+#pragma unroll
+          for (int kk = 0; kk < C::QK; ++kk) {
+            const uint32_t off = ((kk / 4) * (kBM * 128) + (kk % 4) * 32) >> 4;
+            kd[kk] = kb + off;
+            qd[kk] = static_cast<uint32_t>(q_desc) + off;
+          }
+          ok = __all_sync(0xffffffffu, kv_now) || wait_all(kv_bar, kv_ph, kErrMma);
           if (!ok) break;
           const int valid = w.k1 - (w.k0 + j * kBN);
-          if (valid < kBN) {
-            // V rows past the last valid key: zero (see above)
-            uint8_t* vt = smem + (2 + sv) * C::TILE;
-            for (int x = lane; x < (kBN - valid) * 8 * C::NKB; x += 32) {
-              const int kb = x / ((kBN - valid) * 8), y = x - kb * ((kBN - valid) * 8);
-              *reinterpret_cast<uint4*>(vt + kb * kBN * 128 + (valid * 8 + y) * 16) = make_uint4(0, 0, 0, 0);
+          if (valid < kBN) zero_tile_rows<D>(smem + (2 + sv) * C::TILE, valid);
+          ok = __all_sync(0xffffffffu, p0_now) || wait_all(bar_p(0), np[0] & 1, kErrMma);
+          if (!ok) break;
+          ++np[0];
+          const bool p1_now = two && mbar_test(bar_p(1), np[1] & 1);
+          tc_fence_after();
+          if (leader) {
+            mma_group<C::PV, false>(tmem + C::O_COL, pa, vd, hi, C::IDESC_PV, j > 0);
+            if (!two) mma_commit(bar_empty(sv));
+            if (more) {
+              mma_group<C::QK, true>(tmem, qd, kd, hi, C::IDESC_QK, 0u);
+              mma_commit(bar_s(0));
+              if (j + 2 == w.tiles) mma_commit(bar_qfree(0));
+              if (!two) mma_commit(bar_empty(sk));
+            } else {
+              mma_commit(bar_o(0));
             }
-            fence_proxy_async_smem();
-            __syncwarp();
           }
-          for (int i = 0; i < w.halves && ok; ++i) {
-            ok = wait_all(bar_p(i), np[i] & 1, kErrMma);
-            if (!ok) break;
-            ++np[i];
-            tc_fence_after();
-            if (leader) {
-              const bool last = i == w.halves - 1;
-              issue_pv(i, sv, j > 0);
-              if (last) mma_commit(bar_empty(sv));
-              if (more) {
-                issue_qk(i, sk);
-                mma_commit(bar_s(i));
-                if (j + 2 == w.tiles) mma_commit(bar_qfree(i));
-                if (last) mma_commit(bar_empty(sk));
-              } else {
-                mma_commit(bar_o(i));
-              }
+          __syncwarp();
+          if (!two) continue;
+#pragma unroll
+          for (int kk = 0; kk < C::PV; ++kk) pa[kk] += kBN;
+#pragma unroll
+          for (int kk = 0; kk < C::QK; ++kk) qd[kk] += C::TILE >> 4;
+          ok = __all_sync(0xffffffffu, p1_now) || wait_all(bar_p(1), np[1] & 1, kErrMma);
+          if (!ok) break;
+          ++np[1];
+          tc_fence_after();
+          if (leader) {
+            mma_group<C::PV, false>(tmem + C::O_COL + D, pa, vd, hi, C::IDESC_PV, j > 0);
+            mma_commit(bar_empty(sv));
+            if (more) {
+              mma_group<C::QK, true>(tmem + kBN, qd, kd, hi, C::IDESC_QK, 0u);
+              mma_commit(bar_s(1));
+              if (j + 2 == w.tiles) mma_commit(bar_qfree(1));
+              mma_commit(bar_empty(sk));
+            } else {
+              mma_commit(bar_o(1));
             }
-            __syncwarp();
           }
+          __syncwarp();
         }
-        ld += 2 * w.tiles;
-        if (ok && more_units) first_qk(wn, ld);
+        if (ok && more_units) first_qk(wn, 2 * g);
         have = more_units;
-        u = un;
         w = wn;
       }
       if (!ok && leader) {
@@ -316,12 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_base + wg * kBN;
     const uint32_t tO = tmem + lane_base + C::O_COL + wg * D;
     const float sl2 = p.scale_log2;
-    const uint64_t pol_out = l2_policy_evict_first();
     uint8_t* stage = staging + warp * 4096;
     int ns = 0, no = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      const Unit w = unit_at(p, u);
+    for (UnitWalk walk(p); ok && walk.more(p); walk.step(p)) {
+      const Unit w = walk.unit(p);
       if (wg >= w.halves) continue;
       const int row0 = w.q0 + wg * kBM + quarter * 32, row = row0 + lane;
       float m = -INFINITY, l = 0.f;
@@ -373,15 +463,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool none = w.tiles == 0;
       const float inv = none ? 0.f : 1.f / l;
       const float lse = none ? -INFINITY : (m + log2f(l)) * kLn2;
+      const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
+      const int64_t at = w.part * n + (static_cast<int64_t>(w.b) * p.heads + w.h) * p.s_q + row;
+      if (row < p.s_q) {
+        float* dst = p.splits > 1
+                         ? p.ws + p.splits * n * D + at
+                         : static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + row * p.lse.s[2];
+        if (CPATTN_IN(p.splits > 1 ? p.ws_span : p.lse.span, dst, 4, p.err)) *dst = lse;
+      }
       if (!none) {
         ok = wait_all(bar_o(wg), no & 1, kErrSoftmax);
         if (!ok) break;
         ++no;
         tc_fence_after();
       }
-      const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
-      const int64_t at = w.part * n + (static_cast<int64_t>(w.b) * p.heads + w.h) * p.s_q + row;
-      uint8_t* out = static_cast<uint8_t*>(p.out.data) + (w.b * p.out.s[0] + w.h * p.out.s[1]) * 2;
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 64) {
         uint32_t o[64];
@@ -403,36 +498,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
-        // the warp's 32 rows pass through its staging area (16-byte chunks
-        // XOR-swizzled by row) and leave as whole 128-byte pieces
-        uint4* srow = reinterpret_cast<uint4*>(stage) + lane * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t x[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = pack_bf16x2(u2f(o[8 * i + 2 * e]) * inv, u2f(o[8 * i + 2 * e + 1]) * inv);
-          srow[i ^ (lane % 8)] = make_uint4(x[0], x[1], x[2], x[3]);
-        }
+        // (the previous store has read the stage)
+        if (lane == 0) bulk_wait_read();
         __syncwarp();
-#pragma unroll
-        for (int it = 0; it < 8; ++it) {
-          const int r = it * 4 + lane / 8, c = lane % 8;
-          if (row0 + r < p.s_q) {
-            const uint4 val = reinterpret_cast<const uint4*>(stage)[r * 8 + (c ^ (r % 8))];
-            uint8_t* dst = out + (static_cast<int64_t>(row0 + r) * p.out.s[2] + c0) * 2 + c * 16;
-            if (CPATTN_IN(p.out.span, dst, 16, p.err)) st_global_v4_hint(dst, val, pol_out);
-          }
-        }
-      }
-      if (row < p.s_q) {
-        float* dst = p.splits > 1
-                         ? p.ws + p.splits * n * D + at
-                         : static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + row * p.lse.s[2];
-        if (CPATTN_IN(p.splits > 1 ? p.ws_span : p.lse.span, dst, 4, p.err)) *dst = lse;
+        store_rows<64>(p, p.out, &tm_o, stage, o, inv, w.b, w.h, row0, p.s_q, c0);
       }
     }
   }
+  if (lane == 0) bulk_wait_read();   // (no store reads this CTA's shared memory any more)
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {
@@ -443,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                         const CrossParams& p, cudaStream_t stream) {
+                         const CUtensorMap& tm_o, const CrossParams& p, cudaStream_t stream) {
   using C = Cfg<D>;
   auto kernel = cross_fwd_kernel<D>;
   // once per device: the register split needs exactly kLaunchRegs at launch
@@ -463,16 +536,18 @@ cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
   }
   const int64_t units = static_cast<int64_t>(p.batch) * p.heads * p.splits * ((p.s_q + 2 * kBM - 1) / (2 * kBM));
   const int64_t sms = sm_count();
-  kernel<<<static_cast<unsigned>(units < sms ? units : sms), kThreads, C::SMEM, stream>>>(tm_q, tm_k, tm_v, p, units);
+  if (units > 0x7fffffff) return cudaErrorInvalidValue;
+  kernel<<<static_cast<unsigned>(units < sms ? units : sms), kThreads, C::SMEM, stream>>>(
+      tm_q, tm_k, tm_v, tm_o, p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                             const CrossParams& p, cudaStream_t stream) {
-  return head_dim == 64 ? launch_typed<64>(tm_q, tm_k, tm_v, p, stream)
-                        : launch_typed<128>(tm_q, tm_k, tm_v, p, stream);
+                             const CUtensorMap& tm_o, const CrossParams& p, cudaStream_t stream) {
+  return head_dim == 64 ? launch_typed<64>(tm_q, tm_k, tm_v, tm_o, p, stream)
+                        : launch_typed<128>(tm_q, tm_k, tm_v, tm_o, p, stream);
 }
 
 }  // namespace cpattn
