@@ -16,8 +16,11 @@
 //
 // Roles (12 warps): warps 0-7 elementwise, two warpgroups on the same 128 TMEM
 // lanes taking 64 of the tile's 128 columns each; warp 8 TMA producer, warp 9
-// MMA issuer; row statistics by warps 10-11 (dq kernel: lse and delta of the
-// next unit while this one runs, delta also to the workspace) or warp 10.
+// MMA issuer; warp 10 row statistics (dk, dv kernel).  The dq kernel forms
+// delta, and writes it to the workspace for the other: each thread from its
+// half row of dO in shared memory and of O, requested a unit ahead.  (By two
+// warps of their own, 64 rows each, it took 17,500 cycles a unit: beside the
+// elementwise warps they get few issue slots.)
 // TMEM columns, dq:     S 0 | dP 128 | dQ 256 | dS 384, 448 (two buffers)
 //               dk, dv: S^T 0 | dP^T 128, then P^T and dS^T over it | dV, dK 256..
 // The next step's S is issued as soon as this step's S is in registers, so the
@@ -56,10 +59,10 @@ struct Cfg {
   static constexpr uint32_t IDESC_S = make_idesc(1, false, kBM, kBM);
   static constexpr uint32_t IDESC_G = make_idesc(1, true, kBM, D);
   static constexpr int STATS = 2 * kBM * 4;            // -lse log2e and delta of 128 rows
-  // dq kernel: Q, dO of a unit, rings of K and of V tiles, statistics of two units
+  // dq kernel: Q, dO of a unit, rings of K and of V tiles, halves of delta
   static constexpr int KR = D == 128 ? 3 : 5, VR = D == 128 ? 2 : 4;
-  static constexpr int DQ_BARS = 2 * KR + 2 * VR + 16;
-  static constexpr int DQ_SMEM = (2 + KR + VR) * TILE + 2 * STATS + DQ_BARS * 8 + 16;
+  static constexpr int DQ_BARS = 2 * KR + 2 * VR + 13;
+  static constexpr int DQ_SMEM = (2 + KR + VR) * TILE + STATS + DQ_BARS * 8 + 16;
   // dk, dv kernel: K, V tiles, a ring of Q and dO tiles, statistics of two steps
   static constexpr int RING = D == 128 ? 5 : 9;
   static constexpr int KV_BARS = 2 * RING + 11;
@@ -155,8 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   if (!tiles_aligned(p, smem)) return;
   const uint32_t sQ = smem_addr(smem), sG = sQ + C::TILE, sK = sG + C::TILE, sV = sK + C::KR * C::TILE;
-  float* stats = reinterpret_cast<float*>(smem + (2 + C::KR + C::VR) * C::TILE);   // [2][-lse log2e, delta][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stats + 2 * C::STATS / 4);
+  float* halves = reinterpret_cast<float*>(smem + (2 + C::KR + C::VR) * C::TILE);   // [2][128] of delta
+  uint64_t* bars = reinterpret_cast<uint64_t*>(halves + C::STATS / 4);
   const uint32_t bar0 = smem_addr(bars);
   auto k_full = [&](uint32_t s) { return bar0 + 8u * s; };
   auto k_empty = [&](uint32_t s) { return bar0 + 8u * (C::KR + s); };
@@ -165,9 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t B = bar0 + 8u * (2 * C::KR + 2 * C::VR);
   const uint32_t BAR_Q = B, BAR_G = B + 8, BAR_QFREE = B + 16, BAR_GFREE = B + 24, BAR_S = B + 32, BAR_DP = B + 40,
                  BAR_SREAD = B + 48, BAR_DPREAD = B + 56, BAR_DS = B + 64, BAR_DQ = B + 72, BAR_DRAIN = B + 80;
-  auto st_full = [&](uint32_t s) { return B + 88 + 8u * s; };
-  auto st_empty = [&](uint32_t s) { return B + 104 + 8u * s; };
-  const uint32_t BAR_OUT = B + 120;
+  const uint32_t BAR_OUT = B + 88, BAR_DELTA = B + 96;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::DQ_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -182,12 +183,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(v_full(s), 1);
       mbar_init(v_empty(s), 1);
     }
-    for (uint32_t x : {BAR_Q, BAR_G, BAR_QFREE, BAR_GFREE, BAR_S, BAR_DP, BAR_DQ, BAR_DRAIN}) mbar_init(x, 1);
-    for (uint32_t x : {BAR_SREAD, BAR_DPREAD, BAR_DS, BAR_OUT}) mbar_init(x, 8);   // one arrival per elementwise warp
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(st_full(s), 2);    // one arrival per statistics warp
-      mbar_init(st_empty(s), 8);
-    }
+    for (uint32_t x : {BAR_Q, BAR_G, BAR_QFREE, BAR_S, BAR_DP, BAR_DQ, BAR_DRAIN}) mbar_init(x, 1);
+    mbar_init(BAR_GFREE, 2);   // the last product with dO, and delta formed
+    for (uint32_t x : {BAR_SREAD, BAR_DPREAD, BAR_DS, BAR_OUT, BAR_DELTA}) mbar_init(x, 8);   // one arrival per elementwise warp
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -219,8 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = p.fault_skip_kv == 0;
       DqWalk walk(p), ahead(p);
       DqUnit w, wa;
-      // Q, dO and O two units ahead into L2: the statistics warps read O and dO
-      // one unit ahead, with few loads in flight
+      // the next unit's Q, dO and O into L2
       auto prefetch = [&]() {
         if (ahead.with_keys(p, wa) && leader) {
           prefetch_tile<D>(&tm_g, wa.q0, wa.h, wa.b);
@@ -230,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ahead.step(p);
       };
-      if (ok) prefetch();
       if (ok) prefetch();
       while (ok && walk.with_keys(p, w)) {
         const int hk = w.h / (p.heads / p.kv_heads);
@@ -373,81 +369,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(BAR_DRAIN, 0, p.timeout_ns);
       }
       __syncwarp();
-    } else {
-      // -------------------------------------------------- row statistics
-      // lse and delta = do . o of the unit's rows, 64 rows a warp; D / 8 lanes
-      // a row, eight row groups in flight
-      constexpr int LPR = D / 8, RPI = 32 / LPR, G = 8;
-      const int r_base = (warp - kWarpStats) * 64;
-      const int c = lane % LPR, r_in = lane / LPR;
-      uint32_t n = 0;
-      bool ok = true;
-      DqWalk walk(p);
-      DqUnit w;
-      while (ok && walk.with_keys(p, w)) {
-        ok = wait_all(st_empty(n & 1), ((n >> 1) & 1) ^ 1, kErrStats);
-        if (!ok) break;
-        float* st = stats + (n & 1) * (C::STATS / 4);
-        const int64_t bh = static_cast<int64_t>(w.b) * p.heads + w.h;
-        const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.out.data) + w.b * p.out.s[0] + w.h * p.out.s[1] + c * 8;
-        const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.dout.data) + w.b * p.dout.s[0] + w.h * p.dout.s[1] + c * 8;
-#pragma unroll 1
-        for (int i0 = 0; i0 < 64; i0 += G * RPI) {
-          uint4 x[G], y[G];
-#pragma unroll
-          for (int i = 0; i < G; ++i) {
-            const int64_t row = w.q0 + r_base + i0 + i * RPI + r_in;
-            x[i] = y[i] = make_uint4(0, 0, 0, 0);
-            if (row < p.s_q) {
-              const __nv_bfloat16 *ox = o + row * p.out.s[2], *gx = g + row * p.dout.s[2];
-              if (CPATTN_IN(p.out.span, ox, 16, p.err)) x[i] = __ldcs(reinterpret_cast<const uint4*>(ox));
-              if (CPATTN_IN(p.dout.span, gx, 16, p.err)) y[i] = *reinterpret_cast<const uint4*>(gx);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < G; ++i) {
-            const __nv_bfloat162 *a = reinterpret_cast<const __nv_bfloat162*>(&x[i]),
-                                 *b = reinterpret_cast<const __nv_bfloat162*>(&y[i]);
-            float d = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = __bfloat1622float2(a[e]), h = __bfloat1622float2(b[e]);
-              d = fmaf(f.x, h.x, fmaf(f.y, h.y, d));
-            }
-#pragma unroll
-            for (int s = LPR / 2; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
-            const int r = r_base + i0 + i * RPI + r_in;
-            if (c == 0) {
-              st[kBM + r] = d;
-              float* dst = p.ws + bh * p.s_q + w.q0 + r;
-              if (w.q0 + r < p.s_q && CPATTN_IN(p.ws_span, dst, 4, p.err)) *dst = d;
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = r_base + i * 32 + lane;
-          const float* l = static_cast<const float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + (w.q0 + r) * p.lse.s[2];
-          float v = -INFINITY;   // (rows past the end: P = 0)
-          if (w.q0 + r < p.s_q && CPATTN_IN(p.lse.span, l, 4, p.err)) v = -*l * kLog2e;
-          st[r] = v;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(st_full(n & 1));
-        ++n;
-        walk.step(p);
-      }
-      __syncwarp();
     }
   } else {
     regs_increase<kSoftmaxRegs>();
     const int half = warp / 4, quarter = warp % 4;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float sl2 = p.scale_log2;
+    // this thread's row and half: 16-byte chunks of O, dO in shared memory
+    constexpr int CH = D / 16;
+    const int r = quarter * 32 + lane;
+    const uint8_t* g_row = smem + C::TILE + (D == 128 ? half * (kBM * 128) : 0) + r * 128;
+    constexpr int kChunk0 = D == 128 ? 0 : CH;   // first chunk of the second half in its 128 bytes
+    uint4 ox[CH];
+    float neg_lse = -INFINITY;   // (rows past the end: P = 0)
+    auto fetch = [&](const DqUnit& x) {
+      const int64_t row = x.q0 + r;
+      neg_lse = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) ox[i] = make_uint4(0, 0, 0, 0);
+      if (row >= p.s_q || x.tiles == 0) return;
+      const float* l = static_cast<const float*>(p.lse.data) + x.b * p.lse.s[0] + x.h * p.lse.s[1] + row * p.lse.s[2];
+      if (CPATTN_IN(p.lse.span, l, 4, p.err)) neg_lse = -*l * kLog2e;
+      const uint4* o = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.out.data) + x.b * p.out.s[0] +
+                                                      x.h * p.out.s[1] + row * p.out.s[2] + half * (D / 2));
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (CPATTN_IN(p.out.span, o + i, 16, p.err)) ox[i] = __ldcs(o + i);
+    };
     uint32_t it = 0, n = 0;
     bool ok = true;
-    for (DqWalk walk(p); ok && walk.more(p); walk.step(p)) {
-      const DqUnit w = walk.unit(p);
+    DqWalk walk(p);
+    DqUnit wn = walk.unit(p);   // (the grid has no more CTAs than units)
+    fetch(wn);
+    while (ok && walk.more(p)) {
+      const DqUnit w = wn;
+      const float nl = neg_lse;
+      float neg_delta = 0.f;
+      walk.step(p);
+      const bool more = walk.more(p);
+      if (more) wn = walk.unit(p);
       const int row0 = w.q0 + quarter * 32;
       if (w.tiles == 0) {
         // a sequence without keys: dq is 0
@@ -456,14 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < D / 16; ++i)
           if (row0 + lane < p.s_q && CPATTN_IN(p.dq.span, dst + 8 * i, 16, p.err))
             *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(0, 0, 0, 0);
+        if (more) fetch(wn);
         continue;
       }
-      ok = wait_all(st_full(n & 1), (n >> 1) & 1, kErrSoftmax);
-      if (!ok) break;
-      const float neg_lse = stats[(n & 1) * (C::STATS / 4) + quarter * 32 + lane];
-      const float neg_delta = -stats[(n & 1) * (C::STATS / 4) + kBM + quarter * 32 + lane];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(st_empty(n & 1));
       for (int j = 0; j < w.tiles; ++j, ++it) {
         ok = wait_all(BAR_S, it & 1, kErrSoftmax);
         if (!ok) break;
@@ -476,9 +431,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float x0, x1;
-          ffma2(x0, x1, u2f(s[2 * i]), u2f(s[2 * i + 1]), sl2, sl2, neg_lse, neg_lse);
+          ffma2(x0, x1, u2f(s[2 * i]), u2f(s[2 * i + 1]), sl2, sl2, nl, nl);
           s[2 * i] = f2u(ex2_approx(x0));
           s[2 * i + 1] = f2u(ex2_approx(x1));
+        }
+        if (j == 0) {
+          // delta of the unit's rows, a half row a thread
+          ok = wait_all(BAR_G, n & 1, kErrSoftmax);
+          if (!ok) break;
+          float d = 0.f;
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const uint4 gx = *reinterpret_cast<const uint4*>(g_row + (((half * kChunk0 + i) ^ (r & 7)) << 4));
+            const uint32_t a[4] = {ox[i].x, ox[i].y, ox[i].z, ox[i].w}, c[4] = {gx.x, gx.y, gx.z, gx.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              d = fmaf(u2f(a[e] << 16), u2f(c[e] << 16), fmaf(u2f(a[e] & 0xFFFF0000u), u2f(c[e] & 0xFFFF0000u), d));
+          }
+          halves[half * kBM + r] = d;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR_DELTA);
+          ok = wait_all(BAR_DELTA, n & 1, kErrSoftmax);
+          if (!ok) break;
+          d = halves[r] + halves[kBM + r];
+          neg_delta = -d;
+          if (threadIdx.x == 0) mbar_arrive(BAR_GFREE);
+          float* dst = p.ws + (static_cast<int64_t>(w.b) * p.heads + w.h) * p.s_q + w.q0 + r;
+          if (half == 0 && w.q0 + r < p.s_q && CPATTN_IN(p.ws_span, dst, 4, p.err)) *dst = d;
         }
         ok = wait_all(BAR_DP, it & 1, kErrSoftmax);
         if (!ok) break;
@@ -508,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(BAR_DS);
       }
       if (!ok) break;
+      if (more) fetch(wn);
       ok = wait_all(BAR_DQ, n & 1, kErrSoftmax);
       if (!ok) break;
       tc_fence_after();
