@@ -93,16 +93,6 @@ def bind(path: str):
                                            vp]
     lib.cpattn_cross_attention_backward.argtypes = [P, P, P, P, P, P, P, ctypes.c_float, P, P, P,
                                                     vp, ctypes.c_size_t, vp]
-    # the same entry points taking descriptors as packed records (bytes): no
-    # ctypes object per tensor
-    b, f32, size = ctypes.c_char_p, ctypes.c_float, ctypes.c_size_t
-    for name, *args in (
-            ("cpattn_rotary", i32, b, b, i32, b, ctypes.c_double, i32, i32, b, vp),
-            ("cpattn_cross_attention", b, b, b, b, f32, b, b, vp, size, vp),
-            ("cpattn_cross_attention_backward", b, b, b, b, b, b, b, f32, b, b, b, vp, size, vp)):
-        setattr(lib, name + "_packed", ctypes.CFUNCTYPE(i32, *args)((name, lib)))
-    for name in ("cpattn_cross_workspace_bytes", "cpattn_cross_backward_workspace_bytes"):
-        setattr(lib, name + "_packed", ctypes.CFUNCTYPE(size, b, b)((name, lib)))
     for name in ("cpattn_cross_workspace_bytes", "cpattn_cross_backward_workspace_bytes"):
         getattr(lib, name).argtypes = [P, P]
         getattr(lib, name).restype = ctypes.c_size_t
@@ -112,6 +102,10 @@ def bind(path: str):
                  "cpattn_ulysses_anything_permute", "cpattn_ulysses_anything_attention",
                  "cpattn_ulysses_permute_batch", "cpattn_ulysses_anything_permute_batch"):
         getattr(lib, name).restype = ctypes.c_int
+    # entry points the binding module calls by address
+    lib.addresses = {name: ctypes.cast(getattr(lib, "cpattn_" + name), vp).value for name in (
+        "rotary", "cross_attention", "cross_workspace_bytes", "cross_attention_backward",
+        "cross_backward_workspace_bytes")}
     return lib
 
 
@@ -136,16 +130,28 @@ _RECORD = [struct.Struct(f"@Pii{n}q{8 * (MAX_DIMS - n)}x{n}q{8 * (MAX_DIMS - n)}
            for n in range(MAX_DIMS + 1)]
 
 
-def record(data_ptr: int, dtype_code: int, shape, stride) -> bytes:
-    """A tensor's descriptor as the bytes of a CTensor."""
+def describe(data_ptr: int, dtype_code: int, shape, stride) -> CTensor:
     n = len(shape)
     if n > MAX_DIMS:
         raise IndexError(f"{n} dimensions: at most {MAX_DIMS}")
-    return _RECORD[n](data_ptr, dtype_code, n, *shape, *stride)
+    return CTensor.from_buffer_copy(_RECORD[n](data_ptr, dtype_code, n, *shape, *stride))
 
 
-def describe(data_ptr: int, dtype_code: int, shape, stride) -> CTensor:
-    return CTensor.from_buffer_copy(record(data_ptr, dtype_code, shape, stride))
+def binding():
+    """The compiled binding module (built with the library).  Raises if it is
+    missing: there is no fallback implementation."""
+    global _binding
+    if _binding is None:
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError(f"the binding module cannot be loaded ({e}): build it with `python -c \"import "
+                              f"__graft_entry__ as g; g.build()\"`") from None
+        _binding = module
+    return _binding
+
+
+_binding = None
 
 
 def check(status: int, what: str):

@@ -8,8 +8,6 @@ kernels; CPU tensors are rejected (there is no CPU path).
 from __future__ import annotations
 
 import ctypes
-import struct
-from contextlib import nullcontext
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
@@ -417,39 +415,22 @@ def prepare_ulysses_anything(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     return call
 
 
-def _on_device(ts, stream: Optional[torch.cuda.Stream]):
-    """Checks that a call's tensors share one CUDA device.  Returns (a context
-    in which that device is the current one, the handle of the stream to use,
-    the stream itself if it is another than the device's current one)."""
-    index = ts[0].get_device()
-    for t in ts:
-        at = t.get_device()
-        if at < 0:
-            raise ValueError("cpattn runs on CUDA tensors only (no CPU path)")
-        if at != index:
-            raise ValueError(f"tensors on cuda:{index} and cuda:{at} in one call")
-    ctx = _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
-    current = torch.cuda.current_stream(index)
+def _handle(stream: Optional[torch.cuda.Stream], t: torch.Tensor) -> Optional[int]:
+    """A given stream's handle for tensors beside t (None: t's device's current stream)."""
     if stream is None:
-        return ctx, current.cuda_stream, None
-    if stream.device_index != index:
-        raise ValueError(f"a stream of cuda:{stream.device_index} for tensors on cuda:{index}")
-    return ctx, stream.cuda_stream, stream if stream != current else None
-
-
-_HERE = nullcontext()
-
-
-def _record(t: torch.Tensor) -> bytes:
-    return _lib.record(t.data_ptr(), _code(t), t.shape, t.stride())
-
-
-def _lengths_record(t: Optional[torch.Tensor]) -> Optional[bytes]:
-    if t is None:
         return None
-    if t.dtype != torch.int32:
-        raise TypeError(f"kv_lengths are int32, not {t.dtype}")
-    return _lib.record(t.data_ptr(), _lib.I32, t.shape, t.stride())
+    if t.is_cuda and stream.device_index != t.get_device():
+        raise ValueError(f"a stream of cuda:{stream.device_index} for tensors on cuda:{t.get_device()}")
+    return stream.cuda_stream
+
+
+def _hand_over(stream: Optional[torch.cuda.Stream], made) -> None:
+    """Memory this call took from the allocator, used on another stream than
+    the one it was taken for, is not given out again before that stream is done."""
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float = 10000.0,
@@ -463,39 +444,25 @@ def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float =
     the gradient.  outs may be xs (in place).  Returns a tensor for a tensor,
     else a list."""
     lib = _lib.load()
-    single = isinstance(xs, torch.Tensor)
-    if single:
-        xs, outs = [xs], None if outs is None else [outs]
+    if isinstance(xs, torch.Tensor):
+        return rotary([xs], positions, axes_dims, theta, interleaved, inverse, None if outs is None else [outs],
+                      stream)[0]
+    status, results = _lib.binding().rotary(lib.addresses["rotary"], xs, positions, axes_dims, theta,
+                                            interleaved, inverse, outs, _handle(stream, positions))
+    check(status, "cpattn_rotary")
     if outs is None:
-        given = (*xs, positions)
-        outs = made = [torch.empty_like(x) for x in xs]   # (keeps a [B,S,H,D] tensor's order)
-    else:
-        outs, made = list(outs), []
-        if len(outs) != len(xs):
-            raise ValueError(f"{len(xs)} tensors but {len(outs)} outputs")
-        given = (*xs, positions, *outs)
-    ctx, handle, other = _on_device(given, stream)
-    n = len(axes_dims)
-    with ctx:
-        check(lib.cpattn_rotary_packed(len(xs), b"".join(map(_record, xs)), _record(positions), n,
-                                       _INTS[min(n, 5)](*axes_dims[:5]), theta, interleaved, inverse,
-                                       b"".join(map(_record, outs)), handle), "cpattn_rotary")
-    if other is not None:
-        for t in made:
-            t.record_stream(other)
-    return outs[0] if single else outs
-
-
-# int32 arrays as bytes, by length (five axes are refused by the library)
-_INTS = [struct.Struct(f"@{n}i").pack for n in range(6)]
+        _hand_over(stream, results)
+    return results
 
 
 def cross_workspace_bytes(q: torch.Tensor, k: torch.Tensor) -> int:
-    return _lib.load().cpattn_cross_workspace_bytes_packed(_record(q), _record(k))
+    return int(_lib.load().cpattn_cross_workspace_bytes(describe(0, _code(q), q.shape, q.stride()),
+                                                        describe(0, _code(k), k.shape, k.stride())))
 
 
 def cross_backward_workspace_bytes(q: torch.Tensor, k: torch.Tensor) -> int:
-    return _lib.load().cpattn_cross_backward_workspace_bytes_packed(_record(q), _record(k))
+    return int(_lib.load().cpattn_cross_backward_workspace_bytes(
+        describe(0, _code(q), q.shape, q.stride()), describe(0, _code(k), k.shape, k.stride())))
 
 
 def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -507,33 +474,13 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     (cpattn_cross_attention): H_kv divides H; kv_lengths (int32 [B]) gives each
     sequence's valid keys, a sequence without any gives (0, -inf).
     Returns (out [B,H,S_q,D] in q's dtype, lse f32 [B,H,S_q])."""
-    lib = _lib.load()
-    ctx, handle, other = _on_device([t for t in (q, k, v, kv_lengths, out, lse, workspace) if t is not None],
-                                    stream)
-    made = []
-    if out is None:
-        out = torch.empty_like(q)
-        made.append(out)
-    if lse is None:
-        lse = torch.empty(q.shape[:3], device=q.device, dtype=torch.float32)
-        made.append(lse)
-    rq, rk = _record(q), _record(k)
-    with ctx:
-        ws_ptr, ws_bytes = None, 0
-        if workspace is None:
-            need = lib.cpattn_cross_workspace_bytes_packed(rq, rk)
-            if need > 0:
-                workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-                made.append(workspace)
-        if workspace is not None:
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
-        check(lib.cpattn_cross_attention_packed(rq, rk, _record(v), _lengths_record(kv_lengths),
-                                                _scale(scale), _record(out), _record(lse), ws_ptr,
-                                                ws_bytes, handle), "cpattn_cross_attention")
-    if other is not None:
-        for t in made:
-            t.record_stream(other)
-    return out, lse
+    at = _lib.load().addresses
+    status, o, l, ws = _lib.binding().cross(at["cross_attention"], at["cross_workspace_bytes"], q, k, v, kv_lengths,
+                                            _scale(scale), out, lse, workspace, _handle(stream, q))
+    check(status, "cpattn_cross_attention")
+    _hand_over(stream, [None if out is not None else o, None if lse is not None else l,
+                        None if workspace is not None else ws])
+    return o, l
 
 
 def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -548,37 +495,14 @@ def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     lse as it returned them, dout the gradient of out.  Returns (dq, dk, dv) in
     the shapes and dtype of q, k, v; rows of dk and dv past a sequence's
     length are 0."""
-    lib = _lib.load()
-    ctx, handle, other = _on_device([t for t in (q, k, v, out, lse, dout, kv_lengths, dq, dk, dv, workspace)
-                                     if t is not None], stream)
-    made = []
-    if dq is None:
-        dq = torch.empty_like(q)
-        made.append(dq)
-    if dk is None:
-        dk = torch.empty_like(k)
-        made.append(dk)
-    if dv is None:
-        dv = torch.empty_like(v)
-        made.append(dv)
-    rq, rk = _record(q), _record(k)
-    with ctx:
-        ws_ptr, ws_bytes = None, 0
-        if workspace is None:
-            need = lib.cpattn_cross_backward_workspace_bytes_packed(rq, rk)
-            if need > 0:
-                workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-                made.append(workspace)
-        if workspace is not None:
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
-        check(lib.cpattn_cross_attention_backward_packed(
-            rq, rk, _record(v), _record(out), _record(lse), _record(dout), _lengths_record(kv_lengths),
-            _scale(scale), _record(dq), _record(dk), _record(dv), ws_ptr, ws_bytes, handle),
-            "cpattn_cross_attention_backward")
-    if other is not None:
-        for t in made:
-            t.record_stream(other)
-    return dq, dk, dv
+    at = _lib.load().addresses
+    status, *grads, ws = _lib.binding().cross_backward(
+        at["cross_attention_backward"], at["cross_backward_workspace_bytes"], q, k, v, out, lse, dout, kv_lengths,
+        _scale(scale), dq, dk, dv, workspace, _handle(stream, q))
+    check(status, "cpattn_cross_attention_backward")
+    _hand_over(stream, [None if given is not None else t
+                        for given, t in zip((dq, dk, dv, workspace), (*grads, ws))])
+    return tuple(grads)
 
 
 def last_device_status(stream: Optional[torch.cuda.Stream] = None) -> int:

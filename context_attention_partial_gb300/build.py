@@ -1,4 +1,5 @@
-"""Builds libcpattn.so in-tree with nvcc for sm_103a.
+"""Builds libcpattn.so in-tree with nvcc for sm_103a, and beside it the
+PyTorch binding module of its newer calls (host C++, csrc/binding.cpp).
 
 One object per translation unit, compiled in parallel, linked with the static
 CUDA runtime (the library resolves the driver's tensor-map encoder at run
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +27,10 @@ SOURCES = ["attn_fwd.cu", "merge_permute.cu", "cpattn_api.cu", "ring_noalloc.cu"
            "cross_bwd.cu", "cross_few.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "tmem_ops.cuh", "tile_ops.cuh", "check.cuh", "cross.cuh", "cross_ops.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+
+
+BINDING_PATH = os.path.join(PKG, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 
 def nvcc() -> str:
@@ -43,8 +49,45 @@ def _stale(lib_path: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def _start_binding(force: bool):
+    """Starts the compiler on the binding module (None if it is up to date)."""
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    deps = [BINDING_SOURCE, os.path.join(ROOT, "include", "cpattn.h"), os.path.abspath(__file__),
+            os.path.join(torch_dir, "version.py")]
+    if not force and os.path.exists(BINDING_PATH):
+        t = os.path.getmtime(BINDING_PATH)
+        if all(os.path.getmtime(d) <= t for d in deps):
+            return None
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    lib, inc = os.path.join(torch_dir, "lib"), os.path.join(torch_dir, "include")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           BINDING_SOURCE, "-o", BINDING_PATH + f".{os.getpid()}.tmp", "-L" + lib, "-Wl,-rpath," + lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish_binding(proc):
+    out, _ = proc.communicate()
+    if proc.returncode != 0:
+        raise RuntimeError("binding.cpp:\n" + out.decode(errors="replace"))
+    os.replace(BINDING_PATH + f".{os.getpid()}.tmp", BINDING_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None, check: bool = False) -> str:
     lib_path = CHECK_LIB_PATH if check else LIB_PATH
+    binding = None if check else _start_binding(force)   # compiles beside the kernels
+    try:
+        return _build_library(lib_path, force, verbose, extra_flags, check)
+    finally:
+        if binding is not None:
+            _finish_binding(binding)
+
+
+def _build_library(lib_path, force, verbose, extra_flags, check) -> str:
     if not force and not _stale(lib_path):
         return lib_path
     build_dir = os.path.join(BUILD_DIR, "check") if check else BUILD_DIR
