@@ -65,40 +65,47 @@ struct Cfg {
   static constexpr int DQ_SMEM = (2 + KR + VR) * TILE + STATS + DQ_BARS * 8 + 16;
   // dk, dv kernel: K, V tiles, a ring of Q and dO tiles, statistics of two steps
   static constexpr int RING = D == 128 ? 5 : 9;
-  static constexpr int KV_BARS = 2 * RING + 11;
+  static constexpr int KV_BARS = 2 * RING + 12;
   static constexpr int KV_SMEM = (2 + RING) * TILE + 2 * STATS + KV_BARS * 8 + 16;
   static constexpr int PART_ROW = D * 4 + 16;          // staged fp32 row, padded against bank conflicts
   static_assert(DQ_SMEM <= 227 * 1024 && KV_SMEM <= 227 * 1024, "shared memory");
   static_assert(8 * 32 * PART_ROW <= RING * TILE && 8 * 4096 * (D / 64) <= RING * TILE, "staging");
 };
 
-// [rows x D] x [rows x D]^T: both tiles as TMA wrote them, row by row
-template <int D>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
-  using C = Cfg<D>;
-  const uint64_t base = smem_desc_sw128(0, 16, 1024);
-  uint32_t a[C::QK], b[C::QK];
-#pragma unroll
-  for (int kk = 0; kk < C::QK; ++kk) {
-    const uint32_t off = ((kk / 4) * (kBM * 128) + (kk % 4) * 32) >> 4;
-    a[kk] = static_cast<uint32_t>(base) + (a_addr >> 4) + off;
-    b[kk] = static_cast<uint32_t>(base) + (b_addr >> 4) + off;
+// A place in a ring of N tiles and the parity of its use, stepped without
+// divisions: the MMA warp gets an issue slot every eight cycles or so beside
+// the elementwise warps, and its instructions between two groups of MMAs are
+// time the tensor pipe waits.
+template <int N>
+struct Place {
+  uint32_t i = 0, ph = 0;
+  __device__ void next() {
+    if (++i == N) {
+      i = 0;
+      ph ^= 1u;
+    }
   }
-  mma_group<C::QK, true>(d, a, b, static_cast<uint32_t>(base >> 32), C::IDESC_S, 0u);
-}
+};
 
-// (+)= A (TMEM, k-step kk at a_col(kk)) x the rows of a tile
-template <int D, typename F>
-__device__ __forceinline__ void mma_cols(uint32_t d, F a_col, uint32_t b_addr, uint32_t acc) {
-  using C = Cfg<D>;
-  const uint64_t base = smem_desc_sw128(0, kBM * 128, 1024);
-  uint32_t a[C::PV], b[C::PV];
+// Low descriptor words of a tile's k-steps: over its columns (the tile's rows
+// times another's), and over its rows (a TMEM operand times the tile).  The
+// high words are one constant; they are built before a group's waits.
+constexpr uint64_t kRowsDesc = (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+constexpr uint64_t kColsDesc = (uint64_t((kBM * 128) >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+                               (uint64_t(2) << 61);
+constexpr uint32_t kDescHi = static_cast<uint32_t>(kRowsDesc >> 32);
+static_assert(kDescHi == static_cast<uint32_t>(kColsDesc >> 32), "one high word");
+
+template <int N>
+__device__ __forceinline__ void rows_desc(uint32_t (&d)[N], uint32_t addr) {
 #pragma unroll
-  for (int kk = 0; kk < C::PV; ++kk) {
-    a[kk] = a_col(kk);
-    b[kk] = static_cast<uint32_t>(base) + ((b_addr + kk * 16 * 128) >> 4);
-  }
-  mma_group<C::PV, false>(d, a, b, static_cast<uint32_t>(base >> 32), C::IDESC_G, acc);
+  for (int kk = 0; kk < N; ++kk)
+    d[kk] = static_cast<uint32_t>(kRowsDesc) + (addr >> 4) + (((kk / 4) * (kBM * 128) + (kk % 4) * 32) >> 4);
+}
+template <int N>
+__device__ __forceinline__ void cols_desc(uint32_t (&d)[N], uint32_t addr) {
+#pragma unroll
+  for (int kk = 0; kk < N; ++kk) d[kk] = static_cast<uint32_t>(kColsDesc) + ((addr + kk * 16 * 128) >> 4);
 }
 
 // ------------------------------------------------------------------ dq
@@ -282,59 +289,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == kWarpMma) {
-      uint32_t n = 0, it = 0;   // units and steps so far
+      uint32_t n = 0, it = 0;              // units and steps so far
+      Place<C::KR> kc, kn;                 // K tile of this step, and of the next S
+      Place<C::VR> vn;                     // V tile of the next dP
       bool ok = true;
       DqWalk walk(p);
       DqUnit w;
       bool have = walk.with_keys(p, w);
+      uint32_t qa[C::QK], ga[C::QK];
+      rows_desc(qa, sQ);
+      rows_desc(ga, sG);
       auto ready = [&](bool now, uint32_t bar, uint32_t parity) {   // after a test of the same phase
         return __all_sync(0xffffffffu, now) || wait_all(bar, parity, kErrMma);
       };
-      // S and dP of a unit's key tile j, the g-th step over all units
-      auto issue_s = [&](const DqUnit& x, int j, uint32_t g) {
-        const uint32_t s = g % C::KR, ph = (g / C::KR) & 1;
-        ok = ready(mbar_test(k_full(s), ph), k_full(s), ph);
+      // S and dP of a unit's key tile j; `read`: wait for the warps to have
+      // read the ones before
+      auto issue_s = [&](const DqUnit& x, int j, bool read) {
+        const bool k_now = mbar_test(k_full(kn.i), kn.ph), r_now = read && mbar_test(BAR_SREAD, it & 1);
+        uint32_t kb[C::QK];
+        rows_desc(kb, sK + kn.i * C::TILE);
+        ok = ready(k_now, k_full(kn.i), kn.ph);
         if (ok && j == 0) ok = wait_all(BAR_Q, n & 1, kErrMma);
-        if (!ok) return;
         const int valid = x.len - j * kBM;
-        if (valid < kBM) zero_tile_rows<D>(smem + (2 + s) * C::TILE, valid);   // (dS is 0 there, and 0 * NaN is not)
+        if (ok && valid < kBM)
+          zero_tile_rows<D>(smem + (2 + kn.i) * C::TILE, valid);   // (dS is 0 there, and 0 * NaN is not)
+        if (ok && read) ok = ready(r_now, BAR_SREAD, it & 1);
+        if (!ok) return;
         tc_fence_after();
         if (leader) {
-          mma_rows<D>(tmem, sQ, sK + s * C::TILE);
+          mma_group<C::QK, true>(tmem, qa, kb, kDescHi, C::IDESC_S, 0u);
           mma_commit(BAR_S);
           if (j + 1 == x.tiles) mma_commit(BAR_QFREE);
         }
         __syncwarp();
+        kn.next();
       };
-      auto issue_dp = [&](const DqUnit& x, int j, uint32_t g) {
-        const uint32_t s = g % C::VR, ph = (g / C::VR) & 1;
-        ok = ready(mbar_test(v_full(s), ph), v_full(s), ph);
+      auto issue_dp = [&](const DqUnit& x, int j, bool read) {
+        const bool v_now = mbar_test(v_full(vn.i), vn.ph), r_now = read && mbar_test(BAR_DPREAD, it & 1);
+        uint32_t vb[C::QK];
+        rows_desc(vb, sV + vn.i * C::TILE);
+        ok = ready(v_now, v_full(vn.i), vn.ph);
         if (ok && j == 0) ok = wait_all(BAR_G, n & 1, kErrMma);
+        if (ok && read) ok = ready(r_now, BAR_DPREAD, it & 1);
         if (!ok) return;
         tc_fence_after();
         if (leader) {
-          mma_rows<D>(tmem + 128, sG, sV + s * C::TILE);
+          mma_group<C::QK, true>(tmem + 128, ga, vb, kDescHi, C::IDESC_S, 0u);
           mma_commit(BAR_DP);
-          mma_commit(v_empty(s));
+          mma_commit(v_empty(vn.i));
           if (j + 1 == x.tiles) mma_commit(BAR_GFREE);
         }
         __syncwarp();
+        vn.next();
       };
       auto issue_dq = [&](int j, bool last) {
-        ok = wait_all(BAR_DS, it & 1, kErrMma);
+        const bool now = mbar_test(BAR_DS, it & 1);
+        uint32_t da[C::PV], kb[C::PV];
+        cols_desc(kb, sK + kc.i * C::TILE);
+#pragma unroll
+        for (int kk = 0; kk < C::PV; ++kk) da[kk] = tmem + 384 + (it & 1) * 64 + kk * 8;
+        ok = ready(now, BAR_DS, it & 1);
         if (!ok) return;
         tc_fence_after();
         if (leader) {
-          const uint32_t s = it % C::KR, ds = tmem + 384 + (it & 1) * 64;
-          mma_cols<D>(tmem + 256, [&](int kk) { return ds + kk * 8; }, sK + s * C::TILE, j > 0);
+          mma_group<C::PV, false>(tmem + 256, da, kb, kDescHi, C::IDESC_G, j > 0);
           // (a unit's last K tile is given back once its output has left through it)
-          mma_commit(last ? BAR_DQ : k_empty(s));
+          mma_commit(last ? BAR_DQ : k_empty(kc.i));
         }
         __syncwarp();
+        kc.next();
       };
       if (have) {
-        issue_s(w, 0, 0);
-        if (ok) issue_dp(w, 0, 0);
+        issue_s(w, 0, false);
+        if (ok) issue_dp(w, 0, false);
         ++n;
       }
       while (have && ok) {
@@ -342,12 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         walk.step(p);
         const bool more_units = walk.with_keys(p, wn);
         for (int j = 0; j + 1 < w.tiles && ok; ++j, ++it) {
-          ok = wait_all(BAR_SREAD, it & 1, kErrMma);
-          if (!ok) break;
-          issue_s(w, j + 1, it + 1);
-          if (ok) ok = wait_all(BAR_DPREAD, it & 1, kErrMma);
-          if (!ok) break;
-          issue_dp(w, j + 1, it + 1);
+          issue_s(w, j + 1, true);
+          if (ok) issue_dp(w, j + 1, true);
           if (ok) issue_dq(j, false);
         }
         if (!ok) break;
@@ -356,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue_dq(w.tiles - 1, true);
         ++it;
         if (ok && more_units) {
-          issue_s(wn, 0, it);
-          if (ok) issue_dp(wn, 0, it);
+          issue_s(wn, 0, false);
+          if (ok) issue_dp(wn, 0, false);
           ++n;
         }
         have = more_units;
@@ -381,29 +404,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint8_t* g_row = smem + C::TILE + (D == 128 ? half * (kBM * 128) : 0) + r * 128;
     constexpr int kChunk0 = D == 128 ? 0 : CH;   // first chunk of the second half in its 128 bytes
     uint4 ox[CH];
-    float neg_lse = -INFINITY;   // (rows past the end: P = 0)
+    float lse = INFINITY;   // (rows past the end: P = 0)
     auto fetch = [&](const DqUnit& x) {
       const int64_t row = x.q0 + r;
-      neg_lse = -INFINITY;
+      lse = INFINITY;
 #pragma unroll
       for (int i = 0; i < CH; ++i) ox[i] = make_uint4(0, 0, 0, 0);
       if (row >= p.s_q || x.tiles == 0) return;
       const float* l = static_cast<const float*>(p.lse.data) + x.b * p.lse.s[0] + x.h * p.lse.s[1] + row * p.lse.s[2];
-      if (CPATTN_IN(p.lse.span, l, 4, p.err)) neg_lse = -*l * kLog2e;
+      if (CPATTN_IN(p.lse.span, l, 4, p.err)) lse = *l;   // (not used before the unit begins: no wait here)
       const uint4* o = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.out.data) + x.b * p.out.s[0] +
                                                       x.h * p.out.s[1] + row * p.out.s[2] + half * (D / 2));
 #pragma unroll
       for (int i = 0; i < CH; ++i)
         if (CPATTN_IN(p.out.span, o + i, 16, p.err)) ox[i] = __ldcs(o + i);
     };
-    uint32_t it = 0, n = 0;
+    uint32_t it = 0, n = 0, slot = 0;
+    // A unit's output leaves through its last K tile (n - 1: the unit before);
+    // the tile is given back once all eight warps' rows have left it, looked
+    // at when the next unit's first scores are done, not waited for.
+    auto give_back = [&]() {
+      if (lane == 0) {
+        bulk_wait_read();
+        mbar_arrive(BAR_OUT);
+      }
+      __syncwarp();
+      bool done = true;
+      if (warp == 0) {
+        done = wait_all(BAR_OUT, (n - 1) & 1, kErrSoftmax);
+        if (lane == 0) mbar_arrive(k_empty(slot));
+      }
+      return done;
+    };
     bool ok = true;
     DqWalk walk(p);
     DqUnit wn = walk.unit(p);   // (the grid has no more CTAs than units)
     fetch(wn);
     while (ok && walk.more(p)) {
       const DqUnit w = wn;
-      const float nl = neg_lse;
+      const float nl = -lse * kLog2e;
       float neg_delta = 0.f;
       walk.step(p);
       const bool more = walk.more(p);
@@ -437,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (j == 0) {
           // delta of the unit's rows, a half row a thread
-          ok = wait_all(BAR_G, n & 1, kErrSoftmax);
+          ok = (n == 0 || give_back()) && wait_all(BAR_G, n & 1, kErrSoftmax);
           if (!ok) break;
           float d = 0.f;
 #pragma unroll
@@ -496,22 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_x64(lanes + 256 + half * 64, o);
       else
         tmem_ld_x32(lanes + 256 + half * 32, o);
-      // out through the unit's last K tile, which every product has read; the
-      // tile is free once all eight warps' rows have left it
-      const uint32_t slot = (it - 1) % C::KR;
+      // (every product has read the unit's last K tile)
+      slot = (it - 1) % C::KR;
       store_rows<D / 2>(p, p.dq, &tm_dq, smem + (2 + slot) * C::TILE + warp * (C::TILE / 8), o, p.scale, w.b, w.h, row0,
                         p.s_q, half * (D / 2));
-      if (lane == 0) {
-        bulk_wait_read();
-        mbar_arrive(BAR_OUT);
-      }
-      __syncwarp();
-      if (warp == 0) {
-        ok = wait_all(BAR_OUT, n & 1, kErrSoftmax);
-        if (lane == 0) mbar_arrive(k_empty(slot));
-      }
       ++n;
     }
+    if (lane == 0) bulk_wait_read();   // (before this CTA's shared memory is given up)
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -545,9 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tile = [&](uint32_t x) { return sR + (x % C::RING) * C::TILE; };
   const uint32_t B = bar0 + 8u * (2 * C::RING);
   const uint32_t BAR_KV = B, BAR_S = B + 8, BAR_DP = B + 16, BAR_SREAD = B + 24, BAR_DS = B + 32, BAR_DONE = B + 40,
-                 BAR_DRAIN = B + 48;
-  auto st_full = [&](uint32_t s) { return B + 56 + 8u * s; };
-  auto st_empty = [&](uint32_t s) { return B + 72 + 8u * s; };
+                 BAR_DRAIN = B + 48, BAR_DS2 = B + 56;
+  auto st_full = [&](uint32_t s) { return B + 64 + 8u * s; };
+  auto st_empty = [&](uint32_t s) { return B + 80 + 8u * s; };
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::KV_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -570,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(empty(s), 1);
     }
     for (uint32_t x : {BAR_KV, BAR_S, BAR_DP, BAR_DONE, BAR_DRAIN}) mbar_init(x, 1);
-    for (uint32_t x : {BAR_SREAD, BAR_DS}) mbar_init(x, 8);   // one arrival per elementwise warp
+    for (uint32_t x : {BAR_SREAD, BAR_DS, BAR_DS2}) mbar_init(x, 8);   // one arrival per elementwise warp
     for (int s = 0; s < 2; ++s) {
       mbar_init(st_full(s), 1);
       mbar_init(st_empty(s), 8);
@@ -634,14 +665,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto ready = [&](bool now, uint32_t bar, uint32_t parity) {   // after a test of the same phase
         return __all_sync(0xffffffffu, now) || wait_all(bar, parity, kErrMma);
       };
+      auto full_at = [&](uint32_t i) { return bar0 + 8u * i; };
+      auto empty_at = [&](uint32_t i) { return bar0 + 8u * (C::RING + i); };
+      Place<C::RING> qc, gc, qn, gn;   // this step's Q and dO tile, and the next step's
+      gc.next();
+      uint32_t ka[C::QK], va[C::QK];
+      rows_desc(ka, sK);
+      rows_desc(va, sV);
       if (steps > 0) {
-        ok = wait_all(BAR_KV, 0, kErrMma) && wait_all(full(0), 0, kErrMma) && wait_all(full(1), 0, kErrMma);
+        uint32_t qb[C::QK], gb[C::QK];
+        rows_desc(qb, sR + qc.i * C::TILE);
+        rows_desc(gb, sR + gc.i * C::TILE);
+        ok = wait_all(BAR_KV, 0, kErrMma) && wait_all(full_at(qc.i), 0, kErrMma) && wait_all(full_at(gc.i), 0, kErrMma);
         if (ok) {
           tc_fence_after();
           if (leader) {
-            mma_rows<D>(tmem, sK, tile(0));
+            mma_group<C::QK, true>(tmem, ka, qb, kDescHi, C::IDESC_S, 0u);
             mma_commit(BAR_S);
-            mma_rows<D>(tmem + 128, sV, tile(1));
+            mma_group<C::QK, true>(tmem + 128, va, gb, kDescHi, C::IDESC_S, 0u);
             mma_commit(BAR_DP);
           }
           __syncwarp();
@@ -649,42 +690,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (uint32_t t = 0; t < steps && ok; ++t) {
         const bool more = t + 1 < steps;
-        const uint32_t xq = 2 * t + 2, xg = 2 * t + 3;   // the next step's tiles
+        qn = gc;
+        qn.next();
+        gn = qn;
+        gn.next();
         if (more) {
-          const bool q_now = mbar_test(full(xq), phase(xq)), s_now = mbar_test(BAR_SREAD, t & 1);
-          ok = ready(q_now, full(xq), phase(xq)) && ready(s_now, BAR_SREAD, t & 1);
+          const bool q_now = mbar_test(full_at(qn.i), qn.ph), s_now = mbar_test(BAR_SREAD, t & 1);
+          uint32_t qb[C::QK];
+          rows_desc(qb, sR + qn.i * C::TILE);
+          ok = ready(q_now, full_at(qn.i), qn.ph) && ready(s_now, BAR_SREAD, t & 1);
           if (!ok) break;
           tc_fence_after();
           if (leader) {
-            mma_rows<D>(tmem, sK, tile(xq));
+            mma_group<C::QK, true>(tmem, ka, qb, kDescHi, C::IDESC_S, 0u);
             mma_commit(BAR_S);
           }
           __syncwarp();
         }
-        bool g_now = more && mbar_test(full(xg), phase(xg));
-        ok = wait_all(BAR_DS, t & 1, kErrMma);
+        // P^T and dS^T arrive in two halves (32 of each warpgroup's 64 query
+        // columns), so the products begin under the second half's arithmetic;
+        // P^T lies in the first half of the warpgroup's dP^T columns, dS^T in
+        // the second.  k-step kk covers query rows 16 kk..: steps 0, 1, 4, 5
+        // belong to the first halves.
+        const bool g_now = more && mbar_test(full_at(gn.i), gn.ph), d_now = mbar_test(BAR_DS, t & 1);
+        uint32_t qb[C::PV], gb[C::PV], nb[C::QK];
+        cols_desc(qb, sR + qc.i * C::TILE);
+        cols_desc(gb, sR + gc.i * C::TILE);
+        rows_desc(nb, sR + gn.i * C::TILE);
+        const uint32_t pt = tmem + 128;
+        auto products = [&](int part) {
+          const int k0 = 2 * part;
+          const uint32_t pa[4] = {pt + 8 * k0, pt + 8 * k0 + 8, pt + 64 + 8 * k0, pt + 64 + 8 * k0 + 8};
+          const uint32_t da[4] = {pa[0] + 32, pa[1] + 32, pa[2] + 32, pa[3] + 32};
+          const uint32_t q4[4] = {qb[k0], qb[k0 + 1], qb[k0 + 4], qb[k0 + 5]};
+          const uint32_t g4[4] = {gb[k0], gb[k0 + 1], gb[k0 + 4], gb[k0 + 5]};
+          mma_group<4, false>(tmem + 256 + D, da, q4, kDescHi, C::IDESC_G, t > 0 || part > 0);
+          if (part == 1) mma_commit(empty_at(qc.i));
+          mma_group<4, false>(tmem + 256, pa, g4, kDescHi, C::IDESC_G, t > 0 || part > 0);
+          if (part == 1) mma_commit(more ? empty_at(gc.i) : BAR_DONE);
+        };
+        if (more) ok = ready(g_now, full_at(gn.i), gn.ph);
+        if (ok) ok = ready(d_now, BAR_DS, t & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) products(0);
+        __syncwarp();
+        ok = ready(mbar_test(BAR_DS2, t & 1), BAR_DS2, t & 1);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          // 64 of the 128 query columns per warpgroup: P^T in the first half
-          // of its dP^T columns, dS^T in the second
-          const uint32_t pt = tmem + 128;
-          mma_cols<D>(tmem + 256 + D, [&](int kk) { return pt + (kk / 4) * 64 + 32 + (kk % 4) * 8; }, tile(2 * t), t > 0);
-          mma_commit(empty(2 * t));
-          mma_cols<D>(tmem + 256, [&](int kk) { return pt + (kk / 4) * 64 + (kk % 4) * 8; }, tile(2 * t + 1), t > 0);
-          mma_commit(more ? empty(2 * t + 1) : BAR_DONE);
-        }
-        __syncwarp();
-        if (more) {
-          ok = ready(g_now, full(xg), phase(xg));
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-            mma_rows<D>(tmem + 128, sV, tile(xg));
+          products(1);
+          if (more) {
+            mma_group<C::QK, true>(tmem + 128, va, nb, kDescHi, C::IDESC_S, 0u);
             mma_commit(BAR_DP);
           }
-          __syncwarp();
         }
+        __syncwarp();
+        qc = qn;
+        gc = gn;
       }
       if (!ok && leader) {
         // let every MMA already issued finish before TMEM is released
@@ -769,36 +832,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       tmem_ld_x64(lanes + 128 + half * 64, g);
-      if (!live) {
-        // a key past the length (its k and v may hold anything): no weight
+      // two halves of the 64 query columns: P^T and dS^T of each over dP^T
 #pragma unroll
-        for (int i = 0; i < 32; ++i) pb[i] = 0u;
-      }
-      tmem_st_x32(lanes + 128 + half * 64, pb);
+      for (int q = 0; q < 2; ++q) {
+        uint32_t px[16], dx[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float4 d = dl[i];
-        float x[4];
-        fadd2(x[0], x[1], u2f(g[4 * i]), u2f(g[4 * i + 1]), d.x, d.y);
-        fadd2(x[2], x[3], u2f(g[4 * i + 2]), u2f(g[4 * i + 3]), d.z, d.w);
-        fmul2(x[0], x[1], x[0], x[1], u2f(s[4 * i]), u2f(s[4 * i + 1]));
-        fmul2(x[2], x[3], x[2], x[3], u2f(s[4 * i + 2]), u2f(s[4 * i + 3]));
-        pb[2 * i] = pack_bf16x2(x[0], x[1]);
-        pb[2 * i + 1] = pack_bf16x2(x[2], x[3]);
-      }
-      if (!live) {
+        for (int i = 0; i < 8; ++i) {
+          const int c = 32 * q + 4 * i;
+          const float4 d = dl[8 * q + i];
+          float x[4];
+          fadd2(x[0], x[1], u2f(g[c]), u2f(g[c + 1]), d.x, d.y);
+          fadd2(x[2], x[3], u2f(g[c + 2]), u2f(g[c + 3]), d.z, d.w);
+          fmul2(x[0], x[1], x[0], x[1], u2f(s[c]), u2f(s[c + 1]));
+          fmul2(x[2], x[3], x[2], x[3], u2f(s[c + 2]), u2f(s[c + 3]));
+          px[2 * i] = pb[16 * q + 2 * i];
+          px[2 * i + 1] = pb[16 * q + 2 * i + 1];
+          dx[2 * i] = pack_bf16x2(x[0], x[1]);
+          dx[2 * i + 1] = pack_bf16x2(x[2], x[3]);
+        }
+        if (!live) {
+          // a key past the length (its k and v may hold anything): no weight
 #pragma unroll
-        for (int i = 0; i < 32; ++i) pb[i] = 0u;
+          for (int i = 0; i < 16; ++i) px[i] = dx[i] = 0u;
+        }
+        __syncwarp();
+        tmem_st_x16(lanes + 128 + half * 64 + q * 16, px);
+        tmem_st_x16(lanes + 128 + half * 64 + 32 + q * 16, dx);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q == 0 ? BAR_DS : BAR_DS2);
       }
-      __syncwarp();
-      tmem_st_x32(lanes + 128 + half * 64 + 32, pb);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(BAR_DS);
-        mbar_arrive(st_empty(t & 1));
-      }
+      if (lane == 0) mbar_arrive(st_empty(t & 1));
     }
     if (ok && steps > 0) {
       ok = wait_all(BAR_DONE, 0, kErrSoftmax);
