@@ -87,6 +87,19 @@ struct Place {
   }
 };
 
+// Sum of eight products of bf16 values, each added in fp32 with one rounding.
+__device__ __forceinline__ float dot_bf16x8(const uint4& a, const uint4& b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  float d = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b16 al, ah, bl, bh;\n\tmov.b32 {al, ah}, %1;\n\tmov.b32 {bl, bh}, %2;\n\t"
+        "fma.rn.f32.bf16 %0, al, bl, %0;\n\tfma.rn.f32.bf16 %0, ah, bh, %0;\n\t}"
+        : "+f"(d)
+        : "r"(x[i]), "r"(y[i]));
+  return d;
+}
+
 // Low descriptor words of a tile's k-steps: over its columns (the tile's rows
 // times another's), and over its rows (a TMEM operand times the tile).  The
 // high words are one constant; they are built before a group's waits.
@@ -398,26 +411,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp / 4, quarter = warp % 4;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float sl2 = p.scale_log2;
-    // this thread's row and half: 16-byte chunks of O, dO in shared memory
-    constexpr int CH = D / 16;
-    const int r = quarter * 32 + lane;
-    const uint8_t* g_row = smem + C::TILE + (D == 128 ? half * (kBM * 128) : 0) + r * 128;
+    // delta's dot products: LPR lanes read a half row's 16-byte chunks, so a
+    // load touches whole 128-byte lines
+    constexpr int CH = D / 16, LPR = CH, RPI = 32 / LPR;   // CH loads cover the warp's 32 rows
+    const int r = quarter * 32 + lane, r_in = quarter * 32 + lane / LPR, c_in = lane % LPR;
+    const uint8_t* g_tile = smem + C::TILE + (D == 128 ? half * (kBM * 128) : 0);
     constexpr int kChunk0 = D == 128 ? 0 : CH;   // first chunk of the second half in its 128 bytes
     uint4 ox[CH];
-    float lse = INFINITY;   // (rows past the end: P = 0)
+    float lse = INFINITY;
     auto fetch = [&](const DqUnit& x) {
-      const int64_t row = x.q0 + r;
-      lse = INFINITY;
-#pragma unroll
-      for (int i = 0; i < CH; ++i) ox[i] = make_uint4(0, 0, 0, 0);
-      if (row >= p.s_q || x.tiles == 0) return;
-      const float* l = static_cast<const float*>(p.lse.data) + x.b * p.lse.s[0] + x.h * p.lse.s[1] + row * p.lse.s[2];
-      if (CPATTN_IN(p.lse.span, l, 4, p.err)) lse = *l;   // (not used before the unit begins: no wait here)
+      if (x.tiles == 0) return;
+      lse = INFINITY;   // (rows past the end: P = 0)
+      const float* l = static_cast<const float*>(p.lse.data) + x.b * p.lse.s[0] + x.h * p.lse.s[1] + (x.q0 + r) * p.lse.s[2];
+      if (x.q0 + r < p.s_q && CPATTN_IN(p.lse.span, l, 4, p.err)) lse = *l;   // (not used before the unit begins: no wait here)
       const uint4* o = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.out.data) + x.b * p.out.s[0] +
-                                                      x.h * p.out.s[1] + row * p.out.s[2] + half * (D / 2));
+                                                      x.h * p.out.s[1] + half * (D / 2)) + c_in;
 #pragma unroll
-      for (int i = 0; i < CH; ++i)
-        if (CPATTN_IN(p.out.span, o + i, 16, p.err)) ox[i] = __ldcs(o + i);
+      for (int i = 0; i < CH; ++i) {
+        const int64_t row = x.q0 + r_in + i * RPI;
+        const uint4* at = o + row * (p.out.s[2] / 8);
+        ox[i] = make_uint4(0, 0, 0, 0);
+        if (row < p.s_q && CPATTN_IN(p.out.span, at, 16, p.err)) ox[i] = __ldcs(at);
+      }
     };
     uint32_t it = 0, n = 0, slot = 0;
     // A unit's output leaves through its last K tile (n - 1: the unit before);
@@ -475,24 +490,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           s[2 * i + 1] = f2u(ex2_approx(x1));
         }
         if (j == 0) {
-          // delta of the unit's rows, a half row a thread
+          // delta of the unit's rows
           ok = (n == 0 || give_back()) && wait_all(BAR_G, n & 1, kErrSoftmax);
           if (!ok) break;
-          float d = 0.f;
 #pragma unroll
           for (int i = 0; i < CH; ++i) {
-            const uint4 gx = *reinterpret_cast<const uint4*>(g_row + (((half * kChunk0 + i) ^ (r & 7)) << 4));
-            const uint32_t a[4] = {ox[i].x, ox[i].y, ox[i].z, ox[i].w}, c[4] = {gx.x, gx.y, gx.z, gx.w};
+            const int row = r_in + i * RPI;
+            const uint4 gx = *reinterpret_cast<const uint4*>(g_tile + row * 128 + (((half * kChunk0 + c_in) ^ (row & 7)) << 4));
+            float e = dot_bf16x8(ox[i], gx);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              d = fmaf(u2f(a[e] << 16), u2f(c[e] << 16), fmaf(u2f(a[e] & 0xFFFF0000u), u2f(c[e] & 0xFFFF0000u), d));
+            for (int x = LPR / 2; x > 0; x >>= 1) e += __shfl_xor_sync(0xffffffffu, e, x);
+            if (c_in == 0) halves[half * kBM + row] = e;
           }
-          halves[half * kBM + r] = d;
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR_DELTA);
           ok = wait_all(BAR_DELTA, n & 1, kErrSoftmax);
           if (!ok) break;
-          d = halves[r] + halves[kBM + r];
+          const float d = halves[r] + halves[kBM + r];
           neg_delta = -d;
           if (threadIdx.x == 0) mbar_arrive(BAR_GFREE);
           float* dst = p.ws + (static_cast<int64_t>(w.b) * p.heads + w.h) * p.s_q + w.q0 + r;
