@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::DQ_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
+  launch_next();
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
   const int lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
@@ -596,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::KV_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
+  launch_next();
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
   const int lane = threadIdx.x % 32;
   const uint32_t k_tiles = (p.s_kv + kBM - 1) / kBM, q_tiles = (p.s_q + kBM - 1) / kBM;
@@ -793,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++g;
         }
       };
+      launch_wait();   // (delta is written; inputs are older than the dq kernel)
       if (steps > 0) fetch(nl, dl);
       for (uint32_t t = 0; t < steps && ok; ++t) {
         if (t + 1 < steps) fetch(nn, dn);
@@ -932,6 +935,7 @@ template <int D>
 __global__ void __launch_bounds__(256) cross_dkv_join_kernel(const __grid_constant__ CrossParams p, const int64_t partials) {
   const int64_t rows = static_cast<int64_t>(p.batch) * p.kv_heads * p.s_kv, n = rows * (D / 4);
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  launch_wait();   // (the parts are written)
   if (i >= 2 * n) return;
   const int which = i >= n;   // 0: dk, 1: dv
   const int64_t at = i - which * n;
@@ -983,24 +987,27 @@ cudaError_t launch_typed(const CrossBwdMaps& m, const CrossParams& p, int64_t pa
   if (units > 0x7fffffff || ctas > 0x7fffffff || join > 0x7fffffff) return cudaErrorInvalidValue;
   cross_dq_kernel<D><<<static_cast<unsigned>(units < sms ? units : sms), kThreads, C::DQ_SMEM, stream>>>(
       m.q, m.k, m.v, m.dout, m.out, m.dq, p);
-  cross_dkv_kernel<D><<<static_cast<unsigned>(ctas), kThreads, C::KV_SMEM, stream>>>(m.q, m.k, m.v, m.dout, m.dk, m.dv,
-                                                                                       p, partials);
-  if (p.splits > 1) cross_dkv_join_kernel<D><<<static_cast<unsigned>(join), 256, 0, stream>>>(p, partials);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_behind(cross_dkv_kernel<D>, dim3(static_cast<unsigned>(ctas)), kThreads, C::KV_SMEM, stream, m.q, m.k, m.v,
+                    m.dout, m.dk, m.dv, p, partials);
+  if (e == cudaSuccess && p.splits > 1)
+    e = launch_behind(cross_dkv_join_kernel<D>, dim3(static_cast<unsigned>(join)), 256, 0, stream, p, partials);
+  return e;
 }
 
 }  // namespace
 
 int cross_backward_parts(int64_t key_units, int64_t steps) {
   // The parts share the GPU as whole CTAs, one per SM at a time: the fewest
-  // query-tile steps over all waves, a CTA's start and end counting as three
-  // steps and a part's share of the join as half a step.
+  // query-tile steps over all waves, a CTA's start and end (its sums leave at
+  // some 28 bytes a cycle) counting as six steps and the join as eight.
+  // (4608 x 512 x 24 heads: 1 part 105 us, 3 parts 108, 2 parts 119 in all.)
   const int64_t sms = sm_count();
   int best = 1;
-  double least = 0;
+  int64_t least = 0;
   for (int parts = 1; parts <= 32 && parts <= steps; ++parts) {
-    const double waves = static_cast<double>((key_units * parts + sms - 1) / sms);
-    const double cost = waves * ((steps + parts - 1) / parts + 3) + (parts > 1 ? 2 + 0.5 * parts : 0);
+    const int64_t waves = (key_units * parts + sms - 1) / sms;
+    const int64_t cost = waves * ((steps + parts - 1) / parts + 6) + (parts > 1 ? 8 : 0);
     if (parts == 1 || cost < least) {
       best = parts;
       least = cost;

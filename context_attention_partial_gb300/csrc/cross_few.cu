@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_consta
   using C = Few<D>;
   constexpr int KG = 4 / MT, KW = kKeys / KG;    // key groups, keys of a warp and stage
   extern __shared__ __align__(1024) uint8_t smem[];
+  launch_next();
   const uint32_t s0 = smem_addr(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int mt = warp % MT, kg = warp / MT;

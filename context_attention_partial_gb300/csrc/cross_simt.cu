@@ -140,6 +140,7 @@ template <typename T, int D, int W, int R, int KS>
 __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constant__ CrossParams p) {
   constexpr int F = D / 32, ROWS = (W / KS) * R, PAD = D + 4;
   extern __shared__ __align__(16) float sm[];
+  launch_next();
   float* sQ = sm;                          // [ROWS][D]
   float* sK = sQ + ROWS * D;               // [32 KS][PAD]
   float* sV = sK + 32 * KS * PAD;
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
   const int lane = threadIdx.x % 32;
   const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  launch_wait();   // (the parts are written)
   if (at >= n) return;
   const float* pl = p.ws + p.splits * n * D + at;
   float top = -INFINITY;
@@ -479,11 +481,14 @@ template <typename T, int D>
 cudaError_t forward_typed(const CrossParams& p, cudaStream_t stream) {
   constexpr int PAD = D + 4;
   const int64_t bh = static_cast<int64_t>(p.batch) * p.heads;
-  // 64 rows a block where that fills the GPU, else 2 rows a block with its
-  // four warps taking every fourth key tile
+  // 64 rows a block where that fills the GPU; else 8, and for one or two
+  // queries 2 rows a block, four warps of each row taking every fourth key tile
   if (tiles_of(p.s_q, 64) * bh >= sm_count())
     return run<cross_simt_kernel<T, D, 8, 8, 1>>(tiles_of(p.s_q, 64) * bh, p.splits, 256,
                sizeof(float) * (64 * D + 2 * 32 * PAD + 8 * 8 * 32), p, stream);
+  if (p.s_q > 2)
+    return run<cross_simt_kernel<T, D, 16, 2, 4>>(tiles_of(p.s_q, 8) * bh, p.splits, 512,
+                                                  sizeof(float) * (8 * D + 2 * 128 * PAD + 16 * 2 * 32), p, stream);
   return run<cross_simt_kernel<T, D, 4, 2, 4>>(tiles_of(p.s_q, 2) * bh, p.splits, 128,
              sizeof(float) * (2 * D + 2 * 128 * PAD + 4 * 2 * 32), p, stream);
 }
@@ -527,15 +532,12 @@ cudaError_t launch_cross_simt_backward(InDtype dt, int head_dim, const CrossPara
 cudaError_t launch_cross_join(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream) {
   const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
   if ((n + 7) / 8 > 0x7fffffff) return cudaErrorInvalidValue;
-  const unsigned blocks = static_cast<unsigned>((n + 7) / 8);
-  if (dt == InDtype::BF16) {
-    if (head_dim == 64) cross_join_kernel<__nv_bfloat16, 64><<<blocks, 256, 0, stream>>>(p);
-    else cross_join_kernel<__nv_bfloat16, 128><<<blocks, 256, 0, stream>>>(p);
-  } else {
-    if (head_dim == 64) cross_join_kernel<float, 64><<<blocks, 256, 0, stream>>>(p);
-    else cross_join_kernel<float, 128><<<blocks, 256, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  const dim3 blocks(static_cast<unsigned>((n + 7) / 8));
+  if (dt == InDtype::BF16)
+    return launch_behind(head_dim == 64 ? cross_join_kernel<__nv_bfloat16, 64> : cross_join_kernel<__nv_bfloat16, 128>,
+                         blocks, 256, 0, stream, p);
+  return launch_behind(head_dim == 64 ? cross_join_kernel<float, 64> : cross_join_kernel<float, 128>, blocks, 256, 0,
+                       stream, p);
 }
 
 cudaError_t launch_cross_delta(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream) {
