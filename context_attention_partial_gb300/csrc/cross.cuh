@@ -30,6 +30,11 @@ struct CrossParams {
   unsigned int* err;                 // device error word
 };
 
+// A value that is the same in every lane, passed through a shuffle so that the
+// compiler knows it: loops and addresses that depend on it then stay in
+// uniform registers (whole warps only).
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Valid keys of batch b: the given length, brought into [0, s_kv].
 __device__ __forceinline__ int cross_length(const CrossParams& p, int b) {
   if (p.lengths == nullptr) return p.s_kv;

@@ -140,6 +140,7 @@ struct DqWalk {
     };
     split(blockIdx.x, q, h, b);
     split(gridDim.x, dq, dh, db);
+    for (int* x : {&q, &h, &b, &dq, &dh, &db}) *x = uniform(*x);
   }
   __device__ bool more(const CrossParams& p) const { return b < p.batch; }
   __device__ void step(const CrossParams& p) {
@@ -156,7 +157,7 @@ struct DqWalk {
     }
   }
   __device__ DqUnit unit(const CrossParams& p) const {
-    const int len = cross_length(p, b);
+    const int len = uniform(cross_length(p, b));
     return {b, h, q * kBM, len, ceil_div(len, kBM)};
   }
   // Moves to the first unit with keys at or after this one.
@@ -601,14 +602,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
   const int lane = threadIdx.x % 32;
   const uint32_t k_tiles = (p.s_kv + kBM - 1) / kBM, q_tiles = (p.s_q + kBM - 1) / kBM;
-  const uint32_t share = p.heads / p.kv_heads;
-  uint32_t u = blockIdx.x, r = u / k_tiles;
-  const int k0 = static_cast<int>(u - r * k_tiles) * kBM;
-  u = r / p.splits;
+  const uint32_t share = uniform(p.heads / p.kv_heads);
+  const uint32_t r = uniform(blockIdx.x / k_tiles), u = uniform(r / p.splits);
+  const int k0 = static_cast<int>(blockIdx.x - r * k_tiles) * kBM;
   const uint32_t part = r - u * p.splits;
-  const int b = static_cast<int>(u / p.kv_heads), hk = static_cast<int>(u - b * p.kv_heads);
-  const int len = cross_length(p, b);
-  const uint32_t all = share * q_tiles, per = (all + p.splits - 1) / p.splits;
+  const int b = uniform(static_cast<int>(u / p.kv_heads)), hk = static_cast<int>(u - b * p.kv_heads);
+  const int len = uniform(cross_length(p, b));
+  const uint32_t all = share * q_tiles, per = uniform((all + p.splits - 1) / p.splits);
   const uint32_t first = min(part * per, all), steps = k0 < len ? min(per, all - first) : 0u;
 
   if (threadIdx.x == 0) {
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_tile<D>(sV, &tm_v, BAR_KV, k0, hk, b, pol);
       }
       __syncwarp();
-      uint32_t g = first / q_tiles, qt = first - g * q_tiles;
+      uint32_t g = uniform(first / q_tiles), qt = first - g * q_tiles;
       for (; x < 2 * steps && ok; ++x) {
         ok = wait_all(empty(x), phase(x) ^ 1, kErrProducer);
         if (!ok) break;
@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kWarpStats) {
       // (the next step's are requested before this step's are handed over)
       bool ok = true;
-      uint32_t g = first / q_tiles, qt = first - g * q_tiles;
+      uint32_t g = uniform(first / q_tiles), qt = first - g * q_tiles;
       float nl[4], dl[4], nn[4], dn[4];
       auto fetch = [&](float (&a)[4], float (&d)[4]) {
         const int h = hk * share + g, q0 = qt * kBM;

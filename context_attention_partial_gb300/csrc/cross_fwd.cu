@@ -88,6 +88,7 @@ struct UnitWalk {
     q_blocks = ceil_div(p.s_q, 2 * kBM);
     split(p, blockIdx.x, q, part, h, b);
     split(p, gridDim.x, dq, dp, dh, db);
+    for (int* x : {&q, &part, &h, &b, &dq, &dp, &dh, &db}) *x = uniform(*x);
   }
   __device__ bool more(const CrossParams& p) const { return b < p.batch; }
   __device__ void step(const CrossParams& p) {
@@ -114,11 +115,11 @@ struct UnitWalk {
     w.h = h;
     w.part = part;
     w.q0 = q * (2 * kBM);
-    const int len = cross_length(p, b);
+    const int len = uniform(cross_length(p, b));
     const int all = ceil_div(len, kBN);
     int t0 = 0, t1 = all;
     if (p.splits > 1) {
-      const int per = ceil_div(all, p.splits);
+      const int per = uniform(ceil_div(all, p.splits));
       t0 = min(part * per, all);
       t1 = min(t0 + per, all);
     }
@@ -215,7 +216,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool have = walk.with_keys(p, w);
       bool ok = p.fault_skip_kv == 0;
       auto load_q = [&](const Unit& x) {   // once the previous unit's last Q K^T is done
-        for (int i = 0; i < x.halves; ++i) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i >= x.halves) break;
           ok = wait_all(bar_qfree(i), (nq[i] & 1) ^ 1, kErrProducer);
           if (!ok) return;
           if (leader) {
@@ -294,7 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a unit's first scores, query tile by query tile (its K tile is here)
       auto first_qk = [&](const Unit& x, uint32_t at) {
         const uint32_t s = at % C::STAGES;
-        for (int i = 0; i < x.halves && ok; ++i) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i >= x.halves) break;
           ok = wait_all(bar_q(i), nq[i] & 1, kErrMma);
           if (!ok) return;
           ++nq[i];
