@@ -380,6 +380,9 @@ cpattn_status cross_shape(const cpattn_tensor* q, const cpattn_tensor* k) {
   if (B > 65535 || H > 65535 || Hk > 65535 || q->shape[2] > (int64_t(1) << 30) ||
       k->shape[2] > (int64_t(1) << 30))
     return CPATTN_ERR_UNSUPPORTED;
+  // (blocks of one launch)
+  if (B * H * ((q->shape[2] + 63) / 64) > 0x7fffffff || B * Hk * ((k->shape[2] + 63) / 64) > 0x7fffffff)
+    return CPATTN_ERR_UNSUPPORTED;
   return CPATTN_OK;
 }
 
@@ -770,7 +773,7 @@ cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor
     if ((st = make_tmap(&tm_o, out, 32)) != CPATTN_OK) return st;
     e = cpattn::launch_cross_fwd(D, tm_q, tm_k, tm_v, tm_o, p, cs);
   } else if (p.splits > 0) {
-    e = cpattn::launch_cross_simt(dt, D, p, cs);
+    e = cpattn::launch_cross_simt(D, p, cs);
   }
   // (no parts: the join writes the empty result)
   if (e == cudaSuccess && p.splits != 1) e = cpattn::launch_cross_join(dt, D, p, cs);
@@ -817,7 +820,9 @@ cpattn_status cpattn_cross_attention_backward(const cpattn_tensor* q, const cpat
   const int D = static_cast<int>(q->shape[3]);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (dt == InDtype::BF16 && rows && keys) {
+  if (!rows || !keys) {
+    e = cpattn::launch_cross_zeros(dt, D, p, cs);
+  } else if (dt == InDtype::BF16) {
     cpattn::CrossBwdMaps m;
     if ((st = make_tmap(&m.q, q, 128)) != CPATTN_OK) return st;
     if ((st = make_tmap(&m.k, k, 128)) != CPATTN_OK) return st;
@@ -829,8 +834,7 @@ cpattn_status cpattn_cross_attention_backward(const cpattn_tensor* q, const cpat
     if ((st = make_tmap(&m.dv, dv, 32)) != CPATTN_OK) return st;
     e = cpattn::launch_cross_bwd(D, m, p, cross_delta_floats(q), cs);
   } else {
-    if (rows) e = cpattn::launch_cross_delta(dt, D, p, cs);
-    if (e == cudaSuccess) e = cpattn::launch_cross_simt_backward(dt, D, p, cs);
+    e = cpattn::launch_cross_simt_backward(D, p, cs);
   }
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }

@@ -103,12 +103,12 @@ cudaError_t launch_cross_bwd(int head_dim, const CrossBwdMaps& maps, const Cross
 // parts of the query axis for key_units 128-key tiles that walk `steps`
 // 128-row query tiles each
 int cross_backward_parts(int64_t key_units, int64_t steps);
-// fp32 inputs (D 64 or 128).
-cudaError_t launch_cross_simt(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream);
-cudaError_t launch_cross_simt_backward(InDtype dt, int head_dim, const CrossParams& p,
-                                       cudaStream_t stream);
-// ws_delta[b][h][i] = sum_d dout o (the row term of the softmax's gradient)
-cudaError_t launch_cross_delta(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream);
+// fp32 inputs (D 64 or 128; s_q, s_kv >= 1); the gradient keeps delta, [B, H, S_q],
+// at the workspace's start.
+cudaError_t launch_cross_simt(int head_dim, const CrossParams& p, cudaStream_t stream);
+cudaError_t launch_cross_simt_backward(int head_dim, const CrossParams& p, cudaStream_t stream);
+// dq, dk, dv = 0 (no queries, or no keys).
+cudaError_t launch_cross_zeros(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream);
 // joins p.splits partial outputs of the workspace into out and lse
 cudaError_t launch_cross_join(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream);
 

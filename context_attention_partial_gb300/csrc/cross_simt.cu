@@ -1,5 +1,5 @@
-// cross_simt.cu -- cross attention and its gradient on the FP32 pipes, the
-// row term of the gradient, and the join of key-split partials.
+// cross_simt.cu -- cross attention of fp32 inputs and its gradient on the FP32
+// pipes (no tf32 rounding), and the join of key-split partials of both types.
 //
 // Forward, per query row i over the first n = length[b] keys:
 //     s_j = scale q_i . k_j,  o = sum_j e^(s_j - m) v_j / l,  lse = m + ln l
@@ -12,11 +12,13 @@
 // and a fixed order, at the price of forming s and do . v twice.
 //
 // Layout: a warp owns R rows (query rows, or keys in the dk/dv kernel), its
-// lanes own one row each of a 32-row tile of the other side for the dot
+// lanes own C rows each of a 32 C-row tile of the other side for the dot
 // products over D, and D / 32 features each for the products over the tile.
 // A tile row is padded by 16 bytes, so both walks are free of bank conflicts.
-// The R rows' values are broadcast reads: R = 8 takes 12 shared-memory
-// wavefronts for 32 FMA instructions, R = 2 serves calls with few rows.
+// The R rows' values are broadcast reads: R = 8, C = 2 takes 16 shared-memory
+// wavefronts for 64 FMA instructions, which the four FP32 pipes issue in 16
+// cycles (C = 1: 12 for 32, bound by shared memory); R = 2, C = 1 serves calls
+// with few rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,19 +32,7 @@ namespace {
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.442695040888963407f;
 
-template <typename T, int D>
-struct Row {
-  static constexpr int FPL = D / 32;                  // features per lane
-  static constexpr int PAD = D + 4;                   // floats of a tile row
-};
-
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
 
 template <typename T, int N>
 __device__ __forceinline__ void store_n(T* p, const float (&f)[N]) {
@@ -82,50 +72,58 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 // rows [row0, row0 + n) of one head into a tile of `rows` padded fp32 rows;
 // rows at or past `end` are zero and not read (they may hold anything).
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void fill_tile(const CrossParams& p, const CrossTensor& t, int b, int h,
                                           int row0, int rows, int end, float* tile, int stride) {
   for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row0 + r < end) {
-      const T* src = static_cast<const T*>(t.data) + b * t.s[0] + h * t.s[1] +
+      const float* src = static_cast<const float*>(t.data) + b * t.s[0] + h * t.s[1] +
                      static_cast<int64_t>(row0 + r) * t.s[2] + c;
-      if (CPATTN_IN(t.span, src, 4 * sizeof(T), p.err)) x = load4(src);
+      if (CPATTN_IN(t.span, src, 16, p.err)) x = load4(src);
     }
     *reinterpret_cast<float4*>(tile + r * stride + c) = x;
   }
 }
 
-// dot products of R broadcast rows (dense, stride D) with this lane's tile row
-template <int D, int R>
-__device__ __forceinline__ void dots(const float* rows, const float* mine, float (&s)[R]) {
+// dot products of R broadcast rows (dense, stride D) with this lane's tile
+// rows, lane, lane + 32, ...
+template <int D, int R, int C>
+__device__ __forceinline__ void dots(const float* rows, const float* tile, float (&s)[R][C]) {
+  const float* mine = tile + (threadIdx.x % 32) * (D + 4);
 #pragma unroll
-  for (int r = 0; r < R; ++r) s[r] = 0.f;
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[r][c] = 0.f;
 #pragma unroll 4
   for (int d = 0; d < D; d += 4) {
-    const float4 k = *reinterpret_cast<const float4*>(mine + d);
+    float4 k[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) k[c] = *reinterpret_cast<const float4*>(mine + c * 32 * (D + 4) + d);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const float4 q = *reinterpret_cast<const float4*>(rows + r * D + d);
-      s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        s[r][c] = fmaf(q.x, k[c].x, fmaf(q.y, k[c].y, fmaf(q.z, k[c].z, fmaf(q.w, k[c].w, s[r][c]))));
     }
   }
 }
 
-// acc[r][f] += sum over the tile's 32 rows j of w[r][j] tile[j][lane's features]
-template <int D, int R>
+// acc[r][f] += sum over the tile's 32 C rows j of w[r][j] tile[j][lane's features]
+template <int D, int R, int C>
 __device__ __forceinline__ void spread(const float* w, const float* tile, float (&acc)[R][D / 32]) {
   constexpr int F = D / 32;
   const int lane = threadIdx.x % 32;
 #pragma unroll 2
-  for (int j = 0; j < 32; j += 4) {
+  for (int j = 0; j < 32 * C; j += 4) {
     float t[4][F];
 #pragma unroll
     for (int u = 0; u < 4; ++u) load_lane<F>(tile + (j + u) * (D + 4) + lane * F, t[u]);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float4 x = *reinterpret_cast<const float4*>(w + r * 32 + j);
+      const float4 x = *reinterpret_cast<const float4*>(w + r * 32 * C + j);
 #pragma unroll
       for (int f = 0; f < F; ++f)
         acc[r][f] = fmaf(x.x, t[0][f], fmaf(x.y, t[1][f], fmaf(x.z, t[2][f], fmaf(x.w, t[3][f], acc[r][f]))));
@@ -135,16 +133,16 @@ __device__ __forceinline__ void spread(const float* w, const float* tile, float 
 
 // ------------------------------------------------------------------ forward
 // W warps as W / KS groups of R query rows; the KS warps of a group take every
-// KS-th 32-key tile and are joined at the end.
-template <typename T, int D, int W, int R, int KS>
+// KS-th 32 C-key tile and are joined at the end.
+template <int D, int W, int R, int C, int KS>
 __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constant__ CrossParams p) {
-  constexpr int F = D / 32, ROWS = (W / KS) * R, PAD = D + 4;
+  constexpr int F = D / 32, ROWS = (W / KS) * R, PAD = D + 4, T1 = 32 * C, TK = T1 * KS;
   extern __shared__ __align__(16) float sm[];
   launch_next();
   float* sQ = sm;                          // [ROWS][D]
-  float* sK = sQ + ROWS * D;               // [32 KS][PAD]
-  float* sV = sK + 32 * KS * PAD;
-  float* sP = sV + 32 * KS * PAD;          // [W][R][32]
+  float* sK = sQ + ROWS * D;               // [TK][PAD]
+  float* sV = sK + TK * PAD;
+  float* sP = sV + TK * PAD;               // [W][R][T1]
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int group = warp / KS, part = warp % KS;
   const int tiles = (p.s_q + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
@@ -152,12 +150,12 @@ __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constan
   const int h = bh % p.heads, b = bh / p.heads;
   const int hk = h / (p.heads / p.kv_heads);
   const int len = cross_length(p, b);
-  // this split's keys: whole tiles of 32 KS, dealt out evenly
-  const int all_tiles = (len + 32 * KS - 1) / (32 * KS);
+  // this split's keys: whole tiles, dealt out evenly
+  const int all_tiles = (len + TK - 1) / TK;
   const int per = (all_tiles + p.splits - 1) / p.splits;
   const int t_begin = min(static_cast<int>(blockIdx.y) * per, all_tiles), t_end = min(t_begin + per, all_tiles);
 
-  fill_tile<T, D>(p, p.q, b, h, row0, ROWS, p.s_q, sQ, D);
+  fill_tile<D>(p, p.q, b, h, row0, ROWS, p.s_q, sQ, D);
   float o[R][F], m[R], l[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -166,29 +164,39 @@ __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constan
 #pragma unroll
     for (int f = 0; f < F; ++f) o[r][f] = 0.f;
   }
-  float* myP = sP + warp * R * 32;
+  float* myP = sP + warp * R * T1;
   for (int t = t_begin; t < t_end; ++t) {
     __syncthreads();
-    fill_tile<T, D>(p, p.k, b, hk, t * 32 * KS, 32 * KS, len, sK, PAD);
-    fill_tile<T, D>(p, p.v, b, hk, t * 32 * KS, 32 * KS, len, sV, PAD);
+    fill_tile<D>(p, p.k, b, hk, t * TK, TK, len, sK, PAD);
+    fill_tile<D>(p, p.v, b, hk, t * TK, TK, len, sV, PAD);
     __syncthreads();
-    const int key = (t * KS + part) * 32 + lane;
-    float s[R];
-    dots<D, R>(sQ + group * R * D, sK + (part * 32 + lane) * PAD, s);
+    const int valid = len - (t * KS + part) * T1 - lane;   // row lane + 32 c is a key where 32 c < valid
+    float s[R][C];
+    dots<D, R, C>(sQ + group * R * D, sK + part * T1 * PAD, s);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float x = key < len ? s[r] * p.scale_log2 : -INFINITY;
+      float x = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        s[r][c] = 32 * c < valid ? s[r][c] * p.scale_log2 : -INFINITY;
+        x = fmaxf(x, s[r][c]);
+      }
       const float top = fmaxf(m[r], warp_max(x));
       const float base = top == -INFINITY ? 0.f : top;
-      const float e = exp2f(x - base), f = exp2f(m[r] - base);
+      const float f = exp2f(m[r] - base);
       m[r] = top;
-      l[r] = fmaf(l[r], f, e);   // (this lane's share of the sum)
+      l[r] *= f;   // (this lane's share of the sum)
 #pragma unroll
-      for (int c = 0; c < F; ++c) o[r][c] *= f;
-      myP[r * 32 + lane] = e;
+      for (int c = 0; c < C; ++c) {
+        const float e = exp2f(s[r][c] - base);
+        l[r] += e;
+        myP[r * T1 + c * 32 + lane] = e;
+      }
+#pragma unroll
+      for (int i = 0; i < F; ++i) o[r][i] *= f;
     }
     __syncwarp();
-    spread<D, R>(myP, sV + part * 32 * PAD, o);
+    spread<D, R, C>(myP, sV + part * T1 * PAD, o);
     __syncwarp();
   }
 #pragma unroll
@@ -247,8 +255,8 @@ __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constan
       if (CPATTN_IN(p.ws_span, dst, 4 * F, p.err)) store_n<float, F>(dst, res);
       if (lane == 0 && CPATTN_IN(p.ws_span, dl, 4, p.err)) *dl = lse;
     } else {
-      T* dst = static_cast<T*>(p.out.data) + b * p.out.s[0] + h * p.out.s[1] + row * p.out.s[2] + lane * F;
-      if (CPATTN_IN(p.out.span, dst, F * sizeof(T), p.err)) store_n<T, F>(dst, res);
+      float* dst = static_cast<float*>(p.out.data) + b * p.out.s[0] + h * p.out.s[1] + row * p.out.s[2] + lane * F;
+      if (CPATTN_IN(p.out.span, dst, 4 * F, p.err)) store_n<float, F>(dst, res);
       float* dl = static_cast<float*>(p.lse.data) + b * p.lse.s[0] + h * p.lse.s[1] + row * p.lse.s[2];
       if (lane == 0 && CPATTN_IN(p.lse.span, dl, 4, p.err)) *dl = lse;
     }
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
 // ------------------------------------------------------------------ gradient
 // delta_i = sum_d do_id o_id, one warp per query row, dense [B, H, S_q] fp32
 // at the workspace's start.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) cross_delta_kernel(const __grid_constant__ CrossParams p) {
   constexpr int PER = D / 4;   // lanes of a row
   const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
@@ -314,9 +322,9 @@ __global__ void __launch_bounds__(256) cross_delta_kernel(const __grid_constant_
   float d = 0.f;
   if (at < n) {
     const int64_t row = at % p.s_q, bh = at / p.s_q, h = bh % p.heads, b = bh / p.heads;
-    const T* o = static_cast<const T*>(p.out.data) + b * p.out.s[0] + h * p.out.s[1] + row * p.out.s[2] + c;
-    const T* g = static_cast<const T*>(p.dout.data) + b * p.dout.s[0] + h * p.dout.s[1] + row * p.dout.s[2] + c;
-    if (CPATTN_IN(p.out.span, o, 4 * sizeof(T), p.err) && CPATTN_IN(p.dout.span, g, 4 * sizeof(T), p.err)) {
+    const float* o = static_cast<const float*>(p.out.data) + b * p.out.s[0] + h * p.out.s[1] + row * p.out.s[2] + c;
+    const float* g = static_cast<const float*>(p.dout.data) + b * p.dout.s[0] + h * p.dout.s[1] + row * p.dout.s[2] + c;
+    if (CPATTN_IN(p.out.span, o, 16, p.err) && CPATTN_IN(p.dout.span, g, 16, p.err)) {
       const float4 x = load4(o), y = load4(g);
       d = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w)));
     }
@@ -327,23 +335,23 @@ __global__ void __launch_bounds__(256) cross_delta_kernel(const __grid_constant_
 }
 
 // dq: a warp owns R query rows and walks the keys.
-template <typename T, int D, int W, int R>
+template <int D, int W, int R, int C>
 __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_constant__ CrossParams p) {
-  constexpr int F = D / 32, ROWS = W * R, PAD = D + 4;
+  constexpr int F = D / 32, ROWS = W * R, PAD = D + 4, T1 = 32 * C;
   extern __shared__ __align__(16) float sm[];
   float* sQ = sm;                          // [ROWS][D]
   float* sG = sQ + ROWS * D;               // [ROWS][D] dout
-  float* sK = sG + ROWS * D;               // [32][PAD]
-  float* sV = sK + 32 * PAD;
-  float* sS = sV + 32 * PAD;               // [W][R][32]
+  float* sK = sG + ROWS * D;               // [T1][PAD]
+  float* sV = sK + T1 * PAD;
+  float* sS = sV + T1 * PAD;               // [W][R][T1]
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int tiles = (p.s_q + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
   const int row0 = (blockIdx.x - bh * tiles) * ROWS;
   const int h = bh % p.heads, b = bh / p.heads;
   const int hk = h / (p.heads / p.kv_heads);
   const int len = cross_length(p, b);
-  fill_tile<T, D>(p, p.q, b, h, row0, ROWS, p.s_q, sQ, D);
-  fill_tile<T, D>(p, p.dout, b, h, row0, ROWS, p.s_q, sG, D);
+  fill_tile<D>(p, p.q, b, h, row0, ROWS, p.s_q, sQ, D);
+  fill_tile<D>(p, p.dout, b, h, row0, ROWS, p.s_q, sG, D);
   float dq[R][F], lse2[R], delta[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -359,22 +367,24 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_cons
 #pragma unroll
     for (int f = 0; f < F; ++f) dq[r][f] = 0.f;
   }
-  float* myS = sS + warp * R * 32;
-  for (int k0 = 0; k0 < len; k0 += 32) {
+  float* myS = sS + warp * R * T1;
+  for (int k0 = 0; k0 < len; k0 += T1) {
     __syncthreads();
-    fill_tile<T, D>(p, p.k, b, hk, k0, 32, len, sK, PAD);
-    fill_tile<T, D>(p, p.v, b, hk, k0, 32, len, sV, PAD);
+    fill_tile<D>(p, p.k, b, hk, k0, T1, len, sK, PAD);
+    fill_tile<D>(p, p.v, b, hk, k0, T1, len, sV, PAD);
     __syncthreads();
-    float s[R], g[R];
-    dots<D, R>(sQ + warp * R * D, sK + lane * PAD, s);
-    dots<D, R>(sG + warp * R * D, sV + lane * PAD, g);
+    float s[R][C], g[R][C];
+    dots<D, R, C>(sQ + warp * R * D, sK, s);
+    dots<D, R, C>(sG + warp * R * D, sV, g);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float e = k0 + lane < len ? exp2f(fmaf(s[r], p.scale_log2, -lse2[r])) : 0.f;
-      myS[r * 32 + lane] = e * (g[r] - delta[r]);
-    }
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const float e = k0 + 32 * c + lane < len ? exp2f(fmaf(s[r][c], p.scale_log2, -lse2[r])) : 0.f;
+        myS[r * T1 + c * 32 + lane] = e * (g[r][c] - delta[r]);
+      }
     __syncwarp();
-    spread<D, R>(myS, sK, dq);
+    spread<D, R, C>(myS, sK, dq);
     __syncwarp();
   }
 #pragma unroll
@@ -384,23 +394,23 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_cons
     float res[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) res[f] = dq[r][f] * p.scale;
-    T* dst = static_cast<T*>(p.dq.data) + b * p.dq.s[0] + h * p.dq.s[1] + row * p.dq.s[2] + lane * F;
-    if (CPATTN_IN(p.dq.span, dst, F * sizeof(T), p.err)) store_n<T, F>(dst, res);
+    float* dst = static_cast<float*>(p.dq.data) + b * p.dq.s[0] + h * p.dq.s[1] + row * p.dq.s[2] + lane * F;
+    if (CPATTN_IN(p.dq.span, dst, 4 * F, p.err)) store_n<float, F>(dst, res);
   }
 }
 
 // dk, dv: a warp owns R keys and walks the query rows of every query head
 // that shares the key head.
-template <typename T, int D, int W, int R>
+template <int D, int W, int R, int C>
 __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_constant__ CrossParams p) {
-  constexpr int F = D / 32, KEYS = W * R, PAD = D + 4;
+  constexpr int F = D / 32, KEYS = W * R, PAD = D + 4, T1 = 32 * C;
   extern __shared__ __align__(16) float sm[];
   float* sK = sm;                          // [KEYS][D]
   float* sV = sK + KEYS * D;
-  float* sQ = sV + KEYS * D;               // [32][PAD]
-  float* sG = sQ + 32 * PAD;
-  float* sS = sG + 32 * PAD;               // [W][R][32] ds
-  float* sP = sS + W * R * 32;             // [W][R][32] p
+  float* sQ = sV + KEYS * D;               // [T1][PAD]
+  float* sG = sQ + T1 * PAD;
+  float* sS = sG + T1 * PAD;               // [W][R][T1] ds
+  float* sP = sS + W * R * T1;             // [W][R][T1] p
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int tiles = (p.s_kv + KEYS - 1) / KEYS, bk = blockIdx.x / tiles;
   const int key0 = (blockIdx.x - bk * tiles) * KEYS;
@@ -412,38 +422,45 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int f = 0; f < F; ++f) dk[r][f] = dv[r][f] = 0.f;
-  float* myS = sS + warp * R * 32;
-  float* myP = sP + warp * R * 32;
+  float* myS = sS + warp * R * T1;
+  float* myP = sP + warp * R * T1;
   if (key0 < len) {
-    fill_tile<T, D>(p, p.k, b, hk, key0, KEYS, len, sK, D);
-    fill_tile<T, D>(p, p.v, b, hk, key0, KEYS, len, sV, D);
+    fill_tile<D>(p, p.k, b, hk, key0, KEYS, len, sK, D);
+    fill_tile<D>(p, p.v, b, hk, key0, KEYS, len, sV, D);
     for (int g = 0; g < share; ++g) {
       const int h = hk * share + g;
-      for (int i0 = 0; i0 < p.s_q; i0 += 32) {
+      for (int i0 = 0; i0 < p.s_q; i0 += T1) {
         __syncthreads();
-        fill_tile<T, D>(p, p.q, b, h, i0, 32, p.s_q, sQ, PAD);
-        fill_tile<T, D>(p, p.dout, b, h, i0, 32, p.s_q, sG, PAD);
+        fill_tile<D>(p, p.q, b, h, i0, T1, p.s_q, sQ, PAD);
+        fill_tile<D>(p, p.dout, b, h, i0, T1, p.s_q, sG, PAD);
         __syncthreads();
-        const int row = i0 + lane;
-        float lse2 = INFINITY, delta = 0.f;
-        if (row < p.s_q) {
-          const float* l = static_cast<const float*>(p.lse.data) + b * p.lse.s[0] + h * p.lse.s[1] + row * p.lse.s[2];
-          const float* d = p.ws + (static_cast<int64_t>(b) * p.heads + h) * p.s_q + row;
-          if (CPATTN_IN(p.lse.span, l, 4, p.err)) lse2 = *l * kLog2e;
-          if (CPATTN_IN(p.ws_span, d, 4, p.err)) delta = *d;
-        }
-        float s[R], e[R];
-        dots<D, R>(sK + warp * R * D, sQ + lane * PAD, s);
-        dots<D, R>(sV + warp * R * D, sG + lane * PAD, e);
+        float lse2[C], delta[C];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float pr = key0 + warp * R + r < len ? exp2f(fmaf(s[r], p.scale_log2, -lse2)) : 0.f;
-          myP[r * 32 + lane] = pr;
-          myS[r * 32 + lane] = pr * (e[r] - delta);
+        for (int c = 0; c < C; ++c) {
+          const int row = i0 + 32 * c + lane;
+          lse2[c] = INFINITY;
+          delta[c] = 0.f;
+          if (row < p.s_q) {
+            const float* l = static_cast<const float*>(p.lse.data) + b * p.lse.s[0] + h * p.lse.s[1] + row * p.lse.s[2];
+            const float* d = p.ws + (static_cast<int64_t>(b) * p.heads + h) * p.s_q + row;
+            if (CPATTN_IN(p.lse.span, l, 4, p.err)) lse2[c] = *l * kLog2e;
+            if (CPATTN_IN(p.ws_span, d, 4, p.err)) delta[c] = *d;
+          }
         }
+        float s[R][C], e[R][C];
+        dots<D, R, C>(sK + warp * R * D, sQ, s);
+        dots<D, R, C>(sV + warp * R * D, sG, e);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const float pr = key0 + warp * R + r < len ? exp2f(fmaf(s[r][c], p.scale_log2, -lse2[c])) : 0.f;
+            myP[r * T1 + c * 32 + lane] = pr;
+            myS[r * T1 + c * 32 + lane] = pr * (e[r][c] - delta[c]);
+          }
         __syncwarp();
-        spread<D, R>(myP, sG, dv);
-        spread<D, R>(myS, sQ, dk);
+        spread<D, R, C>(myP, sG, dv);
+        spread<D, R, C>(myS, sQ, dk);
         __syncwarp();
       }
     }
@@ -455,13 +472,25 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
     float res[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) res[f] = dk[r][f] * p.scale;
-    T* d1 = static_cast<T*>(p.dk.data) + b * p.dk.s[0] + hk * p.dk.s[1] + key * p.dk.s[2] + lane * F;
-    T* d2 = static_cast<T*>(p.dv.data) + b * p.dv.s[0] + hk * p.dv.s[1] + key * p.dv.s[2] + lane * F;
-    if (CPATTN_IN(p.dk.span, d1, F * sizeof(T), p.err)) store_n<T, F>(d1, res);
+    float* d1 = static_cast<float*>(p.dk.data) + b * p.dk.s[0] + hk * p.dk.s[1] + key * p.dk.s[2] + lane * F;
+    float* d2 = static_cast<float*>(p.dv.data) + b * p.dv.s[0] + hk * p.dv.s[1] + key * p.dv.s[2] + lane * F;
+    if (CPATTN_IN(p.dk.span, d1, 4 * F, p.err)) store_n<float, F>(d1, res);
 #pragma unroll
     for (int f = 0; f < F; ++f) res[f] = dv[r][f];
-    if (CPATTN_IN(p.dv.span, d2, F * sizeof(T), p.err)) store_n<T, F>(d2, res);
+    if (CPATTN_IN(p.dv.span, d2, 4 * F, p.err)) store_n<float, F>(d2, res);
   }
+}
+
+// A gradient without terms (no queries, or no keys): zeros.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_zero_kernel(const CrossTensor t, int batch, int heads, int rows, unsigned int* err) {
+  constexpr int PER = D * sizeof(T) / 16;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t at = i / PER;
+  const int64_t row = at % rows, h = at / rows % heads, b = at / rows / heads;
+  if (b >= batch) return;
+  T* dst = static_cast<T*>(t.data) + b * t.s[0] + h * t.s[1] + row * t.s[2] + (i % PER) * (16 / sizeof(T));
+  if (CPATTN_IN(t.span, dst, 16, err)) *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
 }
 
 // (one instantiation, so one set-up record, per kernel)
@@ -477,56 +506,77 @@ cudaError_t run(int64_t blocks, int splits, int threads, size_t smem, const Cros
 
 int64_t tiles_of(int rows, int per) { return (rows + per - 1) / per; }
 
-template <typename T, int D>
+template <int D>
 cudaError_t forward_typed(const CrossParams& p, cudaStream_t stream) {
   constexpr int PAD = D + 4;
   const int64_t bh = static_cast<int64_t>(p.batch) * p.heads;
   // 64 rows a block where that fills the GPU; else 8, and for one or two
   // queries 2 rows a block, four warps of each row taking every fourth key tile
   if (tiles_of(p.s_q, 64) * bh >= sm_count())
-    return run<cross_simt_kernel<T, D, 8, 8, 1>>(tiles_of(p.s_q, 64) * bh, p.splits, 256,
-               sizeof(float) * (64 * D + 2 * 32 * PAD + 8 * 8 * 32), p, stream);
+    return run<cross_simt_kernel<D, 8, 8, 2, 1>>(tiles_of(p.s_q, 64) * bh, p.splits, 256,
+                                                        sizeof(float) * (64 * D + 2 * 64 * PAD + 8 * 8 * 64), p, stream);
   if (p.s_q > 2)
-    return run<cross_simt_kernel<T, D, 16, 2, 4>>(tiles_of(p.s_q, 8) * bh, p.splits, 512,
-                                                  sizeof(float) * (8 * D + 2 * 128 * PAD + 16 * 2 * 32), p, stream);
-  return run<cross_simt_kernel<T, D, 4, 2, 4>>(tiles_of(p.s_q, 2) * bh, p.splits, 128,
-             sizeof(float) * (2 * D + 2 * 128 * PAD + 4 * 2 * 32), p, stream);
+    return run<cross_simt_kernel<D, 16, 2, 1, 4>>(tiles_of(p.s_q, 8) * bh, p.splits, 512,
+                                                         sizeof(float) * (8 * D + 2 * 128 * PAD + 16 * 2 * 32), p, stream);
+  return run<cross_simt_kernel<D, 4, 2, 1, 4>>(tiles_of(p.s_q, 2) * bh, p.splits, 128,
+                                                      sizeof(float) * (2 * D + 2 * 128 * PAD + 4 * 2 * 32), p, stream);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t backward_typed(const CrossParams& p, cudaStream_t stream) {
   constexpr int PAD = D + 4;
   const int64_t bh = static_cast<int64_t>(p.batch) * p.heads;
   const int64_t bk = static_cast<int64_t>(p.batch) * p.kv_heads;
-  cudaError_t e = cudaSuccess;
-  if (p.s_q > 0) {
-    if (tiles_of(p.s_q, 64) * bh >= sm_count())
-      e = run<cross_simt_dq_kernel<T, D, 8, 8>>(tiles_of(p.s_q, 64) * bh, 1, 256,
-              sizeof(float) * (2 * 64 * D + 2 * 32 * PAD + 8 * 8 * 32), p, stream);
-    else
-      e = run<cross_simt_dq_kernel<T, D, 4, 2>>(tiles_of(p.s_q, 8) * bh, 1, 128,
-              sizeof(float) * (2 * 8 * D + 2 * 32 * PAD + 4 * 2 * 32), p, stream);
-  }
-  if (e != cudaSuccess || p.s_kv == 0) return e;
+  const int64_t n = bh * p.s_q * (D / 4);
+  if ((n + 255) / 256 > 0x7fffffff) return cudaErrorInvalidValue;
+  cross_delta_kernel<D><<<static_cast<unsigned>((n + 255) / 256), 256, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (tiles_of(p.s_q, 64) * bh >= sm_count())
+    e = run<cross_simt_dq_kernel<D, 8, 8, 2>>(tiles_of(p.s_q, 64) * bh, 1, 256,
+                                                     sizeof(float) * (2 * 64 * D + 2 * 64 * PAD + 8 * 8 * 64), p, stream);
+  else
+    e = run<cross_simt_dq_kernel<D, 4, 2, 1>>(tiles_of(p.s_q, 8) * bh, 1, 128,
+                                                     sizeof(float) * (2 * 8 * D + 2 * 32 * PAD + 4 * 2 * 32), p, stream);
+  if (e != cudaSuccess) return e;
   if (tiles_of(p.s_kv, 64) * bk >= sm_count())
-    return run<cross_simt_dkv_kernel<T, D, 8, 8>>(tiles_of(p.s_kv, 64) * bk, 1, 256,
-               sizeof(float) * (2 * 64 * D + 2 * 32 * PAD + 2 * 8 * 8 * 32), p, stream);
-  return run<cross_simt_dkv_kernel<T, D, 4, 2>>(tiles_of(p.s_kv, 8) * bk, 1, 128,
-             sizeof(float) * (2 * 8 * D + 2 * 32 * PAD + 2 * 4 * 2 * 32), p, stream);
+    return run<cross_simt_dkv_kernel<D, 8, 8, 2>>(
+        tiles_of(p.s_kv, 64) * bk, 1, 256, sizeof(float) * (2 * 64 * D + 2 * 64 * PAD + 2 * 8 * 8 * 64), p, stream);
+  return run<cross_simt_dkv_kernel<D, 4, 2, 1>>(tiles_of(p.s_kv, 8) * bk, 1, 128,
+                                                       sizeof(float) * (2 * 8 * D + 2 * 32 * PAD + 2 * 4 * 2 * 32), p,
+                                                       stream);
+}
+
+template <typename T, int D>
+cudaError_t zero_typed(const CrossParams& p, const CrossTensor& t, int heads, int rows, cudaStream_t stream) {
+  const int64_t n = static_cast<int64_t>(p.batch) * heads * rows * (D * sizeof(T) / 16);
+  if (n == 0) return cudaSuccess;
+  if ((n + 255) / 256 > 0x7fffffff) return cudaErrorInvalidValue;
+  cross_zero_kernel<T, D><<<static_cast<unsigned>((n + 255) / 256), 256, 0, stream>>>(t, p.batch, heads, rows, p.err);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t zeros_typed(const CrossParams& p, cudaStream_t stream) {
+  cudaError_t e = zero_typed<T, D>(p, p.dq, p.heads, p.s_q, stream);
+  if (e == cudaSuccess) e = zero_typed<T, D>(p, p.dk, p.kv_heads, p.s_kv, stream);
+  return e == cudaSuccess ? zero_typed<T, D>(p, p.dv, p.kv_heads, p.s_kv, stream) : e;
 }
 
 }  // namespace
 
-cudaError_t launch_cross_simt(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream) {
-  if (dt == InDtype::BF16)
-    return head_dim == 64 ? forward_typed<__nv_bfloat16, 64>(p, stream) : forward_typed<__nv_bfloat16, 128>(p, stream);
-  return head_dim == 64 ? forward_typed<float, 64>(p, stream) : forward_typed<float, 128>(p, stream);
+cudaError_t launch_cross_simt(int head_dim, const CrossParams& p, cudaStream_t stream) {
+  return head_dim == 64 ? forward_typed<64>(p, stream) : forward_typed<128>(p, stream);
 }
 
-cudaError_t launch_cross_simt_backward(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream) {
+cudaError_t launch_cross_simt_backward(int head_dim, const CrossParams& p, cudaStream_t stream) {
+  return head_dim == 64 ? backward_typed<64>(p, stream) : backward_typed<128>(p, stream);
+}
+
+cudaError_t launch_cross_zeros(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream) {
   if (dt == InDtype::BF16)
-    return head_dim == 64 ? backward_typed<__nv_bfloat16, 64>(p, stream) : backward_typed<__nv_bfloat16, 128>(p, stream);
-  return head_dim == 64 ? backward_typed<float, 64>(p, stream) : backward_typed<float, 128>(p, stream);
+    return head_dim == 64 ? zeros_typed<__nv_bfloat16, 64>(p, stream) : zeros_typed<__nv_bfloat16, 128>(p, stream);
+  return head_dim == 64 ? zeros_typed<float, 64>(p, stream) : zeros_typed<float, 128>(p, stream);
 }
 
 cudaError_t launch_cross_join(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream) {
@@ -538,20 +588,6 @@ cudaError_t launch_cross_join(InDtype dt, int head_dim, const CrossParams& p, cu
                          blocks, 256, 0, stream, p);
   return launch_behind(head_dim == 64 ? cross_join_kernel<float, 64> : cross_join_kernel<float, 128>, blocks, 256, 0,
                        stream, p);
-}
-
-cudaError_t launch_cross_delta(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream) {
-  const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q * (head_dim / 4);
-  if ((n + 255) / 256 > 0x7fffffff) return cudaErrorInvalidValue;
-  const unsigned blocks = static_cast<unsigned>((n + 255) / 256);
-  if (dt == InDtype::BF16) {
-    if (head_dim == 64) cross_delta_kernel<__nv_bfloat16, 64><<<blocks, 256, 0, stream>>>(p);
-    else cross_delta_kernel<__nv_bfloat16, 128><<<blocks, 256, 0, stream>>>(p);
-  } else {
-    if (head_dim == 64) cross_delta_kernel<float, 64><<<blocks, 256, 0, stream>>>(p);
-    else cross_delta_kernel<float, 128><<<blocks, 256, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
 }
 
 }  // namespace cpattn
