@@ -397,7 +397,7 @@ bool cross_few(const cpattn_tensor* q, const cpattn_tensor* k) {
 // SM (5 parts 64 us, 9 to 24 parts 66-70 us at 64 key heads x 16384 keys), each
 // with 256 keys or more; for 256-row units of the tensor-core kernel
 // one per SM, each with four 128-key tiles or more; for fp32's blocks of few
-// rows likewise, each with 512 keys or more.
+// rows likewise, each with 128 keys or more.
 int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
   const int64_t bh = q->shape[0] * q->shape[1], sm = cpattn::sm_count();
   if (bh == 0 || q->shape[2] == 0 || k->shape[2] == 0) return 1;
@@ -410,7 +410,7 @@ int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
     int64_t units = (q->shape[2] + 255) / 256 * bh;
     if (q->dtype != CPATTN_BF16)
       units = (q->shape[2] + 63) / 64 * bh >= sm ? sm : q->shape[2] > 2 ? (q->shape[2] + 7) / 8 * bh : bh;
-    most = (k->shape[2] + 511) / 512;
+    most = q->dtype == CPATTN_BF16 ? (k->shape[2] + 511) / 512 : (k->shape[2] + 127) / 128;
     want = sm / units;
   }
   const int64_t s = want < most ? want : most;

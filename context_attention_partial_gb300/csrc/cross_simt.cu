@@ -25,6 +25,7 @@
 #include <cmath>
 
 #include "cross.cuh"
+#include "ptx.cuh"
 
 namespace cpattn {
 namespace {
@@ -70,20 +71,27 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// rows [row0, row0 + n) of one head into a tile of `rows` padded fp32 rows;
-// rows at or past `end` are zero and not read (they may hold anything).
+// 16 bytes to shared memory, or zeros without a read.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool read) {
+  const int n = read ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Waits for all but the newest group of this thread's copies.
+__device__ __forceinline__ void copies_wait_older() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// Requests rows [row0, row0 + rows) of one head into a tile of padded rows;
+// rows at or past `end` become zero and are not read (they may hold anything).
 template <int D>
 __device__ __forceinline__ void fill_tile(const CrossParams& p, const CrossTensor& t, int b, int h,
                                           int row0, int rows, int end, float* tile, int stride) {
+  const float* head = static_cast<const float*>(t.data) + b * t.s[0] + h * t.s[1];
   for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x) {
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row0 + r < end) {
-      const float* src = static_cast<const float*>(t.data) + b * t.s[0] + h * t.s[1] +
-                     static_cast<int64_t>(row0 + r) * t.s[2] + c;
-      if (CPATTN_IN(t.span, src, 16, p.err)) x = load4(src);
-    }
-    *reinterpret_cast<float4*>(tile + r * stride + c) = x;
+    const float* src = head + static_cast<int64_t>(row0 + r) * t.s[2] + c;
+    const bool read = row0 + r < end && CPATTN_IN(t.span, src, 16, p.err);
+    copy16(tile + r * stride + c, read ? src : head, read);
   }
 }
 
@@ -140,9 +148,8 @@ __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constan
   extern __shared__ __align__(16) float sm[];
   launch_next();
   float* sQ = sm;                          // [ROWS][D]
-  float* sK = sQ + ROWS * D;               // [TK][PAD]
-  float* sV = sK + TK * PAD;
-  float* sP = sV + TK * PAD;               // [W][R][T1]
+  float* sKV = sQ + ROWS * D;              // two stages of K and V, [TK][PAD] each
+  float* sP = sKV + 4 * TK * PAD;          // [W][R][T1]
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int group = warp / KS, part = warp % KS;
   const int tiles = (p.s_q + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
@@ -165,11 +172,21 @@ __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constan
     for (int f = 0; f < F; ++f) o[r][f] = 0.f;
   }
   float* myP = sP + warp * R * T1;
+  auto request = [&](int t) {
+    if (t < t_end) {
+      float* stage = sKV + ((t - t_begin) & 1) * 2 * TK * PAD;
+      fill_tile<D>(p, p.k, b, hk, t * TK, TK, len, stage, PAD);
+      fill_tile<D>(p, p.v, b, hk, t * TK, TK, len, stage + TK * PAD, PAD);
+    }
+    copies_commit();
+  };
+  request(t_begin);   // (with the query rows)
   for (int t = t_begin; t < t_end; ++t) {
+    request(t + 1);
+    copies_wait_older();
     __syncthreads();
-    fill_tile<D>(p, p.k, b, hk, t * TK, TK, len, sK, PAD);
-    fill_tile<D>(p, p.v, b, hk, t * TK, TK, len, sV, PAD);
-    __syncthreads();
+    const float* sK = sKV + ((t - t_begin) & 1) * 2 * TK * PAD;
+    const float* sV = sK + TK * PAD;
     const int valid = len - (t * KS + part) * T1 - lane;   // row lane + 32 c is a key where 32 c < valid
     float s[R][C];
     dots<D, R, C>(sQ + group * R * D, sK + part * T1 * PAD, s);
@@ -197,14 +214,15 @@ __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constan
     }
     __syncwarp();
     spread<D, R, C>(myP, sV + part * T1 * PAD, o);
-    __syncwarp();
+    __syncthreads();   // (this stage may be filled again)
   }
+  copies_wait_all();
 #pragma unroll
   for (int r = 0; r < R; ++r) l[r] = warp_sum(l[r]);
   if constexpr (KS > 1) {
     // join the group's KS parts through shared memory (K and V are done with)
     __syncthreads();
-    float* so = sK;                        // [W][R][D]
+    float* so = sKV;                       // [W][R][D]
     float* sml = sP;                       // [W][R][2]
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -341,9 +359,8 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_cons
   extern __shared__ __align__(16) float sm[];
   float* sQ = sm;                          // [ROWS][D]
   float* sG = sQ + ROWS * D;               // [ROWS][D] dout
-  float* sK = sG + ROWS * D;               // [T1][PAD]
-  float* sV = sK + T1 * PAD;
-  float* sS = sV + T1 * PAD;               // [W][R][T1]
+  float* sKV = sG + ROWS * D;              // two stages of K and V, [T1][PAD] each
+  float* sS = sKV + 4 * T1 * PAD;          // [W][R][T1]
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int tiles = (p.s_q + ROWS - 1) / ROWS, bh = blockIdx.x / tiles;
   const int row0 = (blockIdx.x - bh * tiles) * ROWS;
@@ -368,11 +385,21 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_cons
     for (int f = 0; f < F; ++f) dq[r][f] = 0.f;
   }
   float* myS = sS + warp * R * T1;
+  auto request = [&](int k0) {
+    if (k0 < len) {
+      float* stage = sKV + ((k0 / T1) & 1) * 2 * T1 * PAD;
+      fill_tile<D>(p, p.k, b, hk, k0, T1, len, stage, PAD);
+      fill_tile<D>(p, p.v, b, hk, k0, T1, len, stage + T1 * PAD, PAD);
+    }
+    copies_commit();
+  };
+  request(0);   // (with the query rows)
   for (int k0 = 0; k0 < len; k0 += T1) {
+    request(k0 + T1);
+    copies_wait_older();
     __syncthreads();
-    fill_tile<D>(p, p.k, b, hk, k0, T1, len, sK, PAD);
-    fill_tile<D>(p, p.v, b, hk, k0, T1, len, sV, PAD);
-    __syncthreads();
+    const float* sK = sKV + ((k0 / T1) & 1) * 2 * T1 * PAD;
+    const float* sV = sK + T1 * PAD;
     float s[R][C], g[R][C];
     dots<D, R, C>(sQ + warp * R * D, sK, s);
     dots<D, R, C>(sG + warp * R * D, sV, g);
@@ -385,8 +412,9 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_cons
       }
     __syncwarp();
     spread<D, R, C>(myS, sK, dq);
-    __syncwarp();
+    __syncthreads();   // (this stage may be filled again)
   }
+  copies_wait_all();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int row = row0 + warp * R + r;
@@ -407,9 +435,8 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
   extern __shared__ __align__(16) float sm[];
   float* sK = sm;                          // [KEYS][D]
   float* sV = sK + KEYS * D;
-  float* sQ = sV + KEYS * D;               // [T1][PAD]
-  float* sG = sQ + T1 * PAD;
-  float* sS = sG + T1 * PAD;               // [W][R][T1] ds
+  float* sQG = sV + KEYS * D;              // two stages of Q and dO, [T1][PAD] each
+  float* sS = sQG + 4 * T1 * PAD;          // [W][R][T1] ds
   float* sP = sS + W * R * T1;             // [W][R][T1] p
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int tiles = (p.s_kv + KEYS - 1) / KEYS, bk = blockIdx.x / tiles;
@@ -427,43 +454,55 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
   if (key0 < len) {
     fill_tile<D>(p, p.k, b, hk, key0, KEYS, len, sK, D);
     fill_tile<D>(p, p.v, b, hk, key0, KEYS, len, sV, D);
-    for (int g = 0; g < share; ++g) {
-      const int h = hk * share + g;
-      for (int i0 = 0; i0 < p.s_q; i0 += T1) {
-        __syncthreads();
-        fill_tile<D>(p, p.q, b, h, i0, T1, p.s_q, sQ, PAD);
-        fill_tile<D>(p, p.dout, b, h, i0, T1, p.s_q, sG, PAD);
-        __syncthreads();
-        float lse2[C], delta[C];
+    // steps: the query tiles of one head after the other
+    const int tiles_q = (p.s_q + T1 - 1) / T1, steps = share * tiles_q;
+    auto request = [&](int x) {
+      if (x < steps) {
+        float* stage = sQG + (x & 1) * 2 * T1 * PAD;
+        const int g = x / tiles_q, i0 = (x - g * tiles_q) * T1, h = hk * share + g;
+        fill_tile<D>(p, p.q, b, h, i0, T1, p.s_q, stage, PAD);
+        fill_tile<D>(p, p.dout, b, h, i0, T1, p.s_q, stage + T1 * PAD, PAD);
+      }
+      copies_commit();
+    };
+    request(0);   // (with the keys and values)
+    for (int x = 0; x < steps; ++x) {
+      request(x + 1);
+      const int g = x / tiles_q, i0 = (x - g * tiles_q) * T1, h = hk * share + g;
+      float lse2[C], delta[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int row = i0 + 32 * c + lane;
+        lse2[c] = INFINITY;
+        delta[c] = 0.f;
+        if (row < p.s_q) {
+          const float* l = static_cast<const float*>(p.lse.data) + b * p.lse.s[0] + h * p.lse.s[1] + row * p.lse.s[2];
+          const float* d = p.ws + (static_cast<int64_t>(b) * p.heads + h) * p.s_q + row;
+          if (CPATTN_IN(p.lse.span, l, 4, p.err)) lse2[c] = *l * kLog2e;
+          if (CPATTN_IN(p.ws_span, d, 4, p.err)) delta[c] = *d;
+        }
+      }
+      copies_wait_older();
+      __syncthreads();
+      const float* sQ = sQG + (x & 1) * 2 * T1 * PAD;
+      const float* sG = sQ + T1 * PAD;
+      float s[R][C], e[R][C];
+      dots<D, R, C>(sK + warp * R * D, sQ, s);
+      dots<D, R, C>(sV + warp * R * D, sG, e);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const int row = i0 + 32 * c + lane;
-          lse2[c] = INFINITY;
-          delta[c] = 0.f;
-          if (row < p.s_q) {
-            const float* l = static_cast<const float*>(p.lse.data) + b * p.lse.s[0] + h * p.lse.s[1] + row * p.lse.s[2];
-            const float* d = p.ws + (static_cast<int64_t>(b) * p.heads + h) * p.s_q + row;
-            if (CPATTN_IN(p.lse.span, l, 4, p.err)) lse2[c] = *l * kLog2e;
-            if (CPATTN_IN(p.ws_span, d, 4, p.err)) delta[c] = *d;
-          }
+          const float pr = key0 + warp * R + r < len ? exp2f(fmaf(s[r][c], p.scale_log2, -lse2[c])) : 0.f;
+          myP[r * T1 + c * 32 + lane] = pr;
+          myS[r * T1 + c * 32 + lane] = pr * (e[r][c] - delta[c]);
         }
-        float s[R][C], e[R][C];
-        dots<D, R, C>(sK + warp * R * D, sQ, s);
-        dots<D, R, C>(sV + warp * R * D, sG, e);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const float pr = key0 + warp * R + r < len ? exp2f(fmaf(s[r][c], p.scale_log2, -lse2[c])) : 0.f;
-            myP[r * T1 + c * 32 + lane] = pr;
-            myS[r * T1 + c * 32 + lane] = pr * (e[r][c] - delta[c]);
-          }
-        __syncwarp();
-        spread<D, R, C>(myP, sG, dv);
-        spread<D, R, C>(myS, sQ, dk);
-        __syncwarp();
-      }
+      __syncwarp();
+      spread<D, R, C>(myP, sG, dv);
+      spread<D, R, C>(myS, sQ, dk);
+      __syncthreads();   // (this stage may be filled again)
     }
+    copies_wait_all();
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -506,25 +545,30 @@ cudaError_t run(int64_t blocks, int splits, int threads, size_t smem, const Cros
 
 int64_t tiles_of(int rows, int per) { return (rows + per - 1) / per; }
 
+// Shared memory of the kernels in floats: the rows a block owns, two stages of
+// two tiles, the warps' weights.
+constexpr size_t simt_smem(int D, int rows, int tile, int weights) {
+  return sizeof(float) * (static_cast<size_t>(rows) * D + 4 * tile * (D + 4) + weights);
+}
+
 template <int D>
 cudaError_t forward_typed(const CrossParams& p, cudaStream_t stream) {
-  constexpr int PAD = D + 4;
   const int64_t bh = static_cast<int64_t>(p.batch) * p.heads;
-  // 64 rows a block where that fills the GPU; else 8, and for one or two
-  // queries 2 rows a block, four warps of each row taking every fourth key tile
+  // 64 rows a block where that fills the GPU; else 8 or 16, and for one or two
+  // queries 2 rows a block, the KS warps of each row taking every KS-th tile
+  constexpr int KS = D == 64 ? 4 : 2;
   if (tiles_of(p.s_q, 64) * bh >= sm_count())
     return run<cross_simt_kernel<D, 8, 8, 2, 1>>(tiles_of(p.s_q, 64) * bh, p.splits, 256,
-                                                        sizeof(float) * (64 * D + 2 * 64 * PAD + 8 * 8 * 64), p, stream);
+                                                 simt_smem(D, 64, 64, 8 * 8 * 64), p, stream);
   if (p.s_q > 2)
-    return run<cross_simt_kernel<D, 16, 2, 1, 4>>(tiles_of(p.s_q, 8) * bh, p.splits, 512,
-                                                         sizeof(float) * (8 * D + 2 * 128 * PAD + 16 * 2 * 32), p, stream);
-  return run<cross_simt_kernel<D, 4, 2, 1, 4>>(tiles_of(p.s_q, 2) * bh, p.splits, 128,
-                                                      sizeof(float) * (2 * D + 2 * 128 * PAD + 4 * 2 * 32), p, stream);
+    return run<cross_simt_kernel<D, 16, 2, 1, KS>>(tiles_of(p.s_q, 32 / KS) * bh, p.splits, 512,
+                                                   simt_smem(D, 32 / KS, 32 * KS, 16 * 2 * 32), p, stream);
+  return run<cross_simt_kernel<D, KS, 2, 1, KS>>(tiles_of(p.s_q, 2) * bh, p.splits, 32 * KS,
+                                                 simt_smem(D, 2, 32 * KS, KS * 2 * 32), p, stream);
 }
 
 template <int D>
 cudaError_t backward_typed(const CrossParams& p, cudaStream_t stream) {
-  constexpr int PAD = D + 4;
   const int64_t bh = static_cast<int64_t>(p.batch) * p.heads;
   const int64_t bk = static_cast<int64_t>(p.batch) * p.kv_heads;
   const int64_t n = bh * p.s_q * (D / 4);
@@ -533,18 +577,20 @@ cudaError_t backward_typed(const CrossParams& p, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (tiles_of(p.s_q, 64) * bh >= sm_count())
-    e = run<cross_simt_dq_kernel<D, 8, 8, 2>>(tiles_of(p.s_q, 64) * bh, 1, 256,
-                                                     sizeof(float) * (2 * 64 * D + 2 * 64 * PAD + 8 * 8 * 64), p, stream);
+    e = run<cross_simt_dq_kernel<D, 8, 8, 2>>(tiles_of(p.s_q, 64) * bh, 1, 256, simt_smem(D, 128, 64, 8 * 8 * 64), p,
+                                              stream);
   else
-    e = run<cross_simt_dq_kernel<D, 4, 2, 1>>(tiles_of(p.s_q, 8) * bh, 1, 128,
-                                                     sizeof(float) * (2 * 8 * D + 2 * 32 * PAD + 4 * 2 * 32), p, stream);
+    e = run<cross_simt_dq_kernel<D, 4, 2, 1>>(tiles_of(p.s_q, 8) * bh, 1, 128, simt_smem(D, 16, 32, 4 * 2 * 32), p,
+                                              stream);
   if (e != cudaSuccess) return e;
-  if (tiles_of(p.s_kv, 64) * bk >= sm_count())
-    return run<cross_simt_dkv_kernel<D, 8, 8, 2>>(
-        tiles_of(p.s_kv, 64) * bk, 1, 256, sizeof(float) * (2 * 64 * D + 2 * 64 * PAD + 2 * 8 * 8 * 64), p, stream);
+  // 32 keys a block, two blocks an SM: with 64 keys, 192 blocks took two rounds
+  // of 152 SMs (24 heads x 512 keys x 1024 queries)
+  constexpr int C = D == 64 ? 2 : 1;   // (shared memory)
+  if (tiles_of(p.s_kv, 32) * bk >= sm_count())
+    return run<cross_simt_dkv_kernel<D, 4, 8, C>>(tiles_of(p.s_kv, 32) * bk, 1, 128,
+                                                  simt_smem(D, 64, 32 * C, 2 * 4 * 8 * 32 * C), p, stream);
   return run<cross_simt_dkv_kernel<D, 4, 2, 1>>(tiles_of(p.s_kv, 8) * bk, 1, 128,
-                                                       sizeof(float) * (2 * 8 * D + 2 * 32 * PAD + 2 * 4 * 2 * 32), p,
-                                                       stream);
+                                                simt_smem(D, 16, 32, 2 * 4 * 2 * 32), p, stream);
 }
 
 template <typename T, int D>
