@@ -57,33 +57,6 @@ cudaError_t cross_set_up(K kernel, size_t smem, std::atomic<unsigned long long>&
   return e;
 }
 
-// Launches a kernel that may start while the one before it in the stream still
-// runs: it calls launch_wait() before it touches what that kernel writes, and
-// every block of it does, so it never completes before that kernel.  (Saves
-// the launch and the start of each block, some 3 us.)
-template <typename... Params, typename... Args>
-cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
-                          const Args&... args) {
-  cudaLaunchConfig_t config = {};
-  config.gridDim = grid;
-  config.blockDim = dim3(threads);
-  config.dynamicSmemBytes = smem;
-  config.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = &attr;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, kernel, args...);
-}
-#ifdef __CUDACC__
-// Waits until the kernel before this one has completed (nothing to wait for
-// when it was launched the ordinary way).
-__device__ __forceinline__ void launch_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the kernel behind this one start (once every block has called it).
-__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-#endif
-
 // bf16 inputs, D 64 or 128, on the tensor cores (s_kv >= 1; the maps' boxes
 // have 128 rows, the output's 32).
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,

@@ -157,8 +157,9 @@ struct DqWalk {
     }
   }
   __device__ DqUnit unit(const CrossParams& p) const {
+    // (one key has all the weight whatever q is: dq is 0, as without keys)
     const int len = uniform(cross_length(p, b));
-    return {b, h, q * kBM, len, ceil_div(len, kBM)};
+    return {b, h, q * kBM, len, len > 1 ? ceil_div(len, kBM) : 0};
   }
   // Moves to the first unit with keys at or after this one.
   __device__ bool with_keys(const CrossParams& p, DqUnit& w) {
@@ -193,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::DQ_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  launch_next();
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
   const int lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
@@ -222,6 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  launch_wait();
+  launch_next();
   const uint32_t tmem = *tmem_holder;
   // every wait of a warp is voted on, so its lanes stay together
   auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) {
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (more) wn = walk.unit(p);
       const int row0 = w.q0 + quarter * 32;
       if (w.tiles == 0) {
-        // a sequence without keys: dq is 0
+        // a sequence without keys, or with one: dq is 0
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.dq.data) + w.b * p.dq.s[0] + w.h * p.dq.s[1] +
                              static_cast<int64_t>(row0 + lane) * p.dq.s[2] + half * (D / 2);
         for (int i = 0; i < D / 16; ++i)
@@ -598,7 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::KV_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  launch_next();
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
   const int lane = threadIdx.x % 32;
   const uint32_t k_tiles = (p.s_kv + kBM - 1) / kBM, q_tiles = (p.s_q + kBM - 1) / kBM;
@@ -795,7 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++g;
         }
       };
-      launch_wait();   // (delta is written; inputs are older than the dq kernel)
+      launch_wait();   // (delta is written; everything older than the dq kernel was when this one started)
+      launch_next();
       if (steps > 0) fetch(nl, dl);
       for (uint32_t t = 0; t < steps && ok; ++t) {
         if (t + 1 < steps) fetch(nn, dn);
@@ -891,7 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CrossTensor& t = half ? p.dk : p.dv;
       const CUtensorMap* tm = half ? &tm_dk : &tm_dv;
       const float f = half ? p.scale : 1.f;
-      const bool zero = steps == 0 || !live;
+      // (dk is 0 where one key has all the weight; delta was not formed there)
+      const bool zero = steps == 0 || !live || (half == 1 && len == 1);
       const int64_t rows = static_cast<int64_t>(p.batch) * p.kv_heads * p.s_kv;
       float* ws = p.ws + partials + (2 * part + (half ? 0 : 1)) * rows * D +
                   ((static_cast<int64_t>(b) * p.kv_heads + hk) * p.s_kv + key) * D;
@@ -936,6 +939,7 @@ __global__ void __launch_bounds__(256) cross_dkv_join_kernel(const __grid_consta
   const int64_t rows = static_cast<int64_t>(p.batch) * p.kv_heads * p.s_kv, n = rows * (D / 4);
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   launch_wait();   // (the parts are written)
+  launch_next();
   if (i >= 2 * n) return;
   const int which = i >= n;   // 0: dk, 1: dv
   const int64_t at = i - which * n;
@@ -985,9 +989,9 @@ cudaError_t launch_typed(const CrossBwdMaps& m, const CrossParams& p, int64_t pa
   const int64_t ctas = static_cast<int64_t>(p.batch) * p.kv_heads * p.splits * ((p.s_kv + kBM - 1) / kBM);
   const int64_t rows = static_cast<int64_t>(p.batch) * p.kv_heads * p.s_kv, join = (2 * rows * (D / 4) + 255) / 256;
   if (units > 0x7fffffff || ctas > 0x7fffffff || join > 0x7fffffff) return cudaErrorInvalidValue;
-  cross_dq_kernel<D><<<static_cast<unsigned>(units < sms ? units : sms), kThreads, C::DQ_SMEM, stream>>>(
-      m.q, m.k, m.v, m.dout, m.out, m.dq, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_behind(cross_dq_kernel<D>, dim3(static_cast<unsigned>(units < sms ? units : sms)), kThreads, C::DQ_SMEM,
+                    stream, m.q, m.k, m.v, m.dout, m.out, m.dq, p);
+  if (e != cudaSuccess) return e;
   e = launch_behind(cross_dkv_kernel<D>, dim3(static_cast<unsigned>(ctas)), kThreads, C::KV_SMEM, stream, m.q, m.k, m.v,
                     m.dout, m.dk, m.dv, p, partials);
   if (e == cudaSuccess && p.splits > 1)

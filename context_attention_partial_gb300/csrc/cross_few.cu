@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_consta
   using C = Few<D>;
   constexpr int KG = 4 / MT, KW = kKeys / KG;    // key groups, keys of a warp and stage
   extern __shared__ __align__(1024) uint8_t smem[];
+  launch_wait();
   launch_next();
   const uint32_t s0 = smem_addr(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -277,8 +278,7 @@ cudaError_t launch_tiles(const CrossParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(p.batch) * p.kv_heads;
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  kernel<<<dim3(static_cast<unsigned>(units), p.splits), kThreads, C::SMEM, stream>>>(p);
-  return cudaGetLastError();
+  return launch_behind(kernel, dim3(static_cast<unsigned>(units), p.splits), kThreads, C::SMEM, stream, p);
 }
 
 template <int D>

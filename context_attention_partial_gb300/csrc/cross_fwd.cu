@@ -162,7 +162,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
-  launch_next();
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
   const int lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
@@ -191,6 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  launch_wait();
+  launch_next();
   const uint32_t tmem = *tmem_holder;
   // every wait of a warp is voted on, so its lanes stay together
   auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) {
@@ -543,9 +544,8 @@ cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
   const int64_t units = static_cast<int64_t>(p.batch) * p.heads * p.splits * ((p.s_q + 2 * kBM - 1) / (2 * kBM));
   const int64_t sms = sm_count();
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  kernel<<<static_cast<unsigned>(units < sms ? units : sms), kThreads, C::SMEM, stream>>>(
-      tm_q, tm_k, tm_v, tm_o, p);
-  return cudaGetLastError();
+  return launch_behind(kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)), kThreads, C::SMEM, stream, tm_q,
+                       tm_k, tm_v, tm_o, p);
 }
 
 }  // namespace

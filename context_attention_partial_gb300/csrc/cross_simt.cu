@@ -146,6 +146,7 @@ template <int D, int W, int R, int C, int KS>
 __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constant__ CrossParams p) {
   constexpr int F = D / 32, ROWS = (W / KS) * R, PAD = D + 4, T1 = 32 * C, TK = T1 * KS;
   extern __shared__ __align__(16) float sm[];
+  launch_wait();
   launch_next();
   float* sQ = sm;                          // [ROWS][D]
   float* sKV = sQ + ROWS * D;              // two stages of K and V, [TK][PAD] each
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
   const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
   launch_wait();   // (the parts are written)
+  launch_next();
   if (at >= n) return;
   const float* pl = p.ws + p.splits * n * D + at;
   float top = -INFINITY;
@@ -338,6 +340,8 @@ __global__ void __launch_bounds__(256) cross_delta_kernel(const __grid_constant_
   const int64_t at = i / PER;
   const int c = static_cast<int>(i % PER) * 4;
   float d = 0.f;
+  launch_wait();
+  launch_next();
   if (at < n) {
     const int64_t row = at % p.s_q, bh = at / p.s_q, h = bh % p.heads, b = bh / p.heads;
     const float* o = static_cast<const float*>(p.out.data) + b * p.out.s[0] + h * p.out.s[1] + row * p.out.s[2] + c;
@@ -357,6 +361,8 @@ template <int D, int W, int R, int C>
 __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_constant__ CrossParams p) {
   constexpr int F = D / 32, ROWS = W * R, PAD = D + 4, T1 = 32 * C;
   extern __shared__ __align__(16) float sm[];
+  launch_wait();
+  launch_next();
   float* sQ = sm;                          // [ROWS][D]
   float* sG = sQ + ROWS * D;               // [ROWS][D] dout
   float* sKV = sG + ROWS * D;              // two stages of K and V, [T1][PAD] each
@@ -408,7 +414,8 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_cons
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const float e = k0 + 32 * c + lane < len ? exp2f(fmaf(s[r][c], p.scale_log2, -lse2[r])) : 0.f;
-        myS[r * T1 + c * 32 + lane] = e * (g[r][c] - delta[r]);
+        // (one key has all the weight whatever q is)
+        myS[r * T1 + c * 32 + lane] = len > 1 ? e * (g[r][c] - delta[r]) : 0.f;
       }
     __syncwarp();
     spread<D, R, C>(myS, sK, dq);
@@ -433,6 +440,8 @@ template <int D, int W, int R, int C>
 __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_constant__ CrossParams p) {
   constexpr int F = D / 32, KEYS = W * R, PAD = D + 4, T1 = 32 * C;
   extern __shared__ __align__(16) float sm[];
+  launch_wait();
+  launch_next();
   float* sK = sm;                          // [KEYS][D]
   float* sV = sK + KEYS * D;
   float* sQG = sV + KEYS * D;              // two stages of Q and dO, [T1][PAD] each
@@ -495,7 +504,7 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
         for (int c = 0; c < C; ++c) {
           const float pr = key0 + warp * R + r < len ? exp2f(fmaf(s[r][c], p.scale_log2, -lse2[c])) : 0.f;
           myP[r * T1 + c * 32 + lane] = pr;
-          myS[r * T1 + c * 32 + lane] = pr * (e[r][c] - delta[c]);
+          myS[r * T1 + c * 32 + lane] = len > 1 ? pr * (e[r][c] - delta[c]) : 0.f;   // (as in the dq kernel)
         }
       __syncwarp();
       spread<D, R, C>(myP, sG, dv);
@@ -527,6 +536,8 @@ __global__ void __launch_bounds__(256) cross_zero_kernel(const CrossTensor t, in
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t at = i / PER;
   const int64_t row = at % rows, h = at / rows % heads, b = at / rows / heads;
+  launch_wait();
+  launch_next();
   if (b >= batch) return;
   T* dst = static_cast<T*>(t.data) + b * t.s[0] + h * t.s[1] + row * t.s[2] + (i % PER) * (16 / sizeof(T));
   if (CPATTN_IN(t.span, dst, 16, err)) *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
@@ -539,8 +550,7 @@ cudaError_t run(int64_t blocks, int splits, int threads, size_t smem, const Cros
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const cudaError_t e = cross_set_up(kernel, smem, ready);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(static_cast<unsigned>(blocks), splits), threads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_behind(kernel, dim3(static_cast<unsigned>(blocks), splits), threads, smem, stream, p);
 }
 
 int64_t tiles_of(int rows, int per) { return (rows + per - 1) / per; }
@@ -573,8 +583,7 @@ cudaError_t backward_typed(const CrossParams& p, cudaStream_t stream) {
   const int64_t bk = static_cast<int64_t>(p.batch) * p.kv_heads;
   const int64_t n = bh * p.s_q * (D / 4);
   if ((n + 255) / 256 > 0x7fffffff) return cudaErrorInvalidValue;
-  cross_delta_kernel<D><<<static_cast<unsigned>((n + 255) / 256), 256, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_behind(cross_delta_kernel<D>, dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream, p);
   if (e != cudaSuccess) return e;
   if (tiles_of(p.s_q, 64) * bh >= sm_count())
     e = run<cross_simt_dq_kernel<D, 8, 8, 2>>(tiles_of(p.s_q, 64) * bh, 1, 256, simt_smem(D, 128, 64, 8 * 8 * 64), p,
@@ -598,8 +607,8 @@ cudaError_t zero_typed(const CrossParams& p, const CrossTensor& t, int heads, in
   const int64_t n = static_cast<int64_t>(p.batch) * heads * rows * (D * sizeof(T) / 16);
   if (n == 0) return cudaSuccess;
   if ((n + 255) / 256 > 0x7fffffff) return cudaErrorInvalidValue;
-  cross_zero_kernel<T, D><<<static_cast<unsigned>((n + 255) / 256), 256, 0, stream>>>(t, p.batch, heads, rows, p.err);
-  return cudaGetLastError();
+  return launch_behind(cross_zero_kernel<T, D>, dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream, t, p.batch,
+                       heads, rows, p.err);
 }
 
 template <typename T, int D>

@@ -110,6 +110,35 @@ struct RotaryParams {
 };
 cudaError_t launch_rotary(InDtype dt, const RotaryParams& p, cudaStream_t stream);
 
+// Launches a kernel that may start while the one before it in the stream still
+// runs, whoever launched that.  Every block of it calls launch_wait() before it
+// touches memory that an earlier kernel writes or reads -- so it never
+// completes before that kernel -- and launch_next() after that, so a kernel
+// behind it only starts once everything before it has completed.  (Hides the
+// launch and the start of the blocks, 2 to 4 us a kernel.)
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                          const Args&... args) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, args...);
+}
+#ifdef __CUDACC__
+// Waits until the kernel before this one has completed (nothing to wait for
+// when it was launched the ordinary way).
+__device__ __forceinline__ void launch_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the kernel behind this one start (once every block has called it).
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 // Error word helpers (defined with the device symbol).
 cudaError_t read_and_clear_device_error(unsigned int* value, cudaStream_t stream);
 // Device address of the error word on the current device (nullptr on

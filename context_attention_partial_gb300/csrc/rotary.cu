@@ -88,6 +88,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   const int b = blockIdx.x / kp.token_tiles;
   const int token = (blockIdx.x - b * kp.token_tiles) * kp.tile_tokens + t;
   const bool active = t < kp.tile_tokens && token < p.seq;
+  launch_wait();
+  launch_next();
 
   float c[NC], s[NC];
   int partner[N];
@@ -203,13 +205,8 @@ cudaError_t launch_typed(const RotaryParams& p, cudaStream_t stream) {
   for (int a = 0; a < p.axes; ++a) whole = whole && p.axis_dim[a] % (2 * Vec<T>::N) == 0;
   const size_t stage = p.interleaved ? 0 : static_cast<size_t>(kRowsInFlight) * kp.tile_tokens * p.head_dim * sizeof(T);
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(groups));
-  if (p.interleaved)
-    rotary_kernel<T, 0><<<grid, kThreads, stage, stream>>>(kp);
-  else if (whole)
-    rotary_kernel<T, 1><<<grid, kThreads, stage, stream>>>(kp);
-  else
-    rotary_kernel<T, 2><<<grid, kThreads, stage, stream>>>(kp);
-  return cudaGetLastError();
+  return launch_behind(p.interleaved ? rotary_kernel<T, 0> : whole ? rotary_kernel<T, 1> : rotary_kernel<T, 2>, grid,
+                       kThreads, stage, stream, kp);
 }
 
 }  // namespace

@@ -331,7 +331,8 @@ size_t cpattn_cross_workspace_bytes(const cpattn_tensor* q, const cpattn_tensor*
  *   dout [B, H, S_q, D]: the gradient of out, q's dtype;
  *   dq [B, H, S_q, D], dk, dv [B, H_kv, S_kv, D]: written, q's dtype.  dk and
  *     dv sum over the query heads that share a key head; rows past a sequence's
- *     length get 0, and dq is 0 for a sequence without keys.
+ *     length get 0; dq is 0 for a sequence without keys, dq and dk are exactly 0
+ *     for one with a single key.
  * Every sum has one owner and a fixed order: equal calls give equal bits.
  *   workspace: at least cpattn_cross_backward_workspace_bytes(q, k) bytes,
  *     16-byte aligned.

@@ -152,6 +152,20 @@ def test_cross_empty_axes(dtype):
     assert cp.last_device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M", [1, 150])
+def test_cross_single_key_has_no_score_gradient(dtype, M):
+    """One key takes all the weight whatever q and k are: dq and dk are 0, to the bit."""
+    for keys, lengths in ((1, None), (200, (1, 1)), (1, (1, 0))):
+        q, k, v, dout, n = make(2, 4, 2, M, keys, 128, dtype, lengths, seed=9)
+        out, lse = cp.cross_attention(q, k, v, kv_lengths=n)
+        dq, dk, dv = cp.cross_attention_backward(q, k, v, out, lse, dout, kv_lengths=n)
+        assert torch.all(dq == 0) and torch.all(dk == 0)
+        want = plain.cross(q, k, v, lengths, dout=dout)
+        check("out", out, want)
+        check("dv", dv, want)
+
+
 def test_cross_gradient_against_differences():
     """fp32 central differences of sum(dout out) in a few directions."""
     B, H, Hk, M, N, D = 2, 4, 2, 9, 21, 64
