@@ -387,15 +387,19 @@ cpattn_status cross_shape(const cpattn_tensor* q, const cpattn_tensor* k) {
 }
 
 // Few query rows a key head: bf16 calls that the key and value read bounds.
+// Up to 32 rows the few-rows kernel is as fast as the tensor-core kernel or
+// faster; up to 64 only where many query heads share the key head, since the
+// other one reads it for each of them (figures in cross_few.cu).
 bool cross_few(const cpattn_tensor* q, const cpattn_tensor* k) {
-  return q->dtype == CPATTN_BF16 && k->shape[1] > 0 &&
-         q->shape[2] * (q->shape[1] / k->shape[1]) <= cpattn::kCrossFewRows;
+  if (q->dtype != CPATTN_BF16 || k->shape[1] == 0) return false;
+  const int64_t share = q->shape[1] / k->shape[1], rows = q->shape[2] * share;
+  return rows <= 32 || (rows <= 64 && share >= 8);
 }
 
 // Parts of the key axis of a forward call: 1 where the query rows fill the
 // GPU, else as many as keep it full: for few rows one round of two CTAs per
-// SM (5 parts 64 us, 9 to 24 parts 66-70 us at 64 key heads x 16384 keys), each
-// with 256 keys or more; for 256-row units of the tensor-core kernel
+// SM (64 key heads x 16384 keys: 4 parts 83 us, 5 parts 109, 9 parts 85, 19
+// parts 91), each with 512 keys or more; for 256-row units of the tensor-core kernel
 // one per SM, each with four 128-key tiles or more; for fp32's blocks of few
 // rows likewise, each with 128 keys or more.
 int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
@@ -404,8 +408,8 @@ int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
   int64_t most, want;
   if (cross_few(q, k)) {
     const int64_t units = q->shape[0] * k->shape[1];
-    most = (k->shape[2] + 255) / 256;
-    want = (2 * sm + units - 1) / units;
+    most = (k->shape[2] + 511) / 512;
+    want = 2 * sm / units;
   } else {
     int64_t units = (q->shape[2] + 255) / 256 * bh;
     if (q->dtype != CPATTN_BF16)

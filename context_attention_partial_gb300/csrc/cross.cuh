@@ -62,8 +62,7 @@ cudaError_t cross_set_up(K kernel, size_t smem, std::atomic<unsigned long long>&
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                              const CUtensorMap& tm_v, const CUtensorMap& tm_o, const CrossParams& p,
                              cudaStream_t stream);
-// the same for at most kCrossFewRows query rows a key head (s_q * H / H_kv)
-constexpr int kCrossFewRows = 64;
+// the same for at most 64 query rows a key head (s_q * H / H_kv)
 cudaError_t launch_cross_few(int head_dim, const CrossParams& p, cudaStream_t stream);
 // its gradient (s_q, s_kv >= 1; the kernels write delta to the workspace's start
 // and, when p.splits > 1, partial sums of dk and dv `partials` floats into it;

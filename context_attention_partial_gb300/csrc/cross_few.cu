@@ -15,6 +15,12 @@
 // tile would be 7/8 padding, and its accumulators' way through TMEM is longer
 // than the whole product.  P is rounded to bf16 for its product with V, sums
 // and outputs of parts are fp32.
+//
+// Against the tensor-core kernel, which reads a key head once per query head
+// (head size 128; us, this kernel / that one): 8 sequences x 8 key heads x 4096
+// keys, 4 query heads each: 4 queries 29 / 81, 8 queries 31 / 81; 4 x 16 heads
+// x 4096 keys, not shared: 16 queries 29 / 30, 32 queries 32 / 31; 64 queries
+// x 4608 keys x 24 heads 28 / 21; 16 queries x 4 query heads x 1024 keys 16 / 14.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,8 +34,9 @@ namespace cpattn {
 namespace {
 
 constexpr int kKeys = 64;       // of a stage
-constexpr int kThreads = 128;
 constexpr float kLn2 = 0.693147180559945309f;
+
+constexpr int kThreads = 128;
 
 template <int D>
 struct Few {

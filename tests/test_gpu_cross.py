@@ -77,6 +77,8 @@ CASES = [
     (3, 5, 5, 1, 9001, 128, (9001, 0, 4096)),
     (1, 32, 2, 4, 5000, 128, None),                   # 64 rows share a key head
     (1, 6, 1, 11, 3001, 64, (2050,)),                 # 66 rows
+    (2, 16, 2, 7, 2500, 128, (2500, 1200)),           # 56 rows, many query heads a key head
+    (2, 3, 3, 31, 1500, 128, None),                   # 31 rows of one head
 ]
 
 
