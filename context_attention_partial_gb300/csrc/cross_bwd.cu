@@ -497,15 +497,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           // delta of the unit's rows
           ok = (n == 0 || give_back()) && wait_all(BAR_G, n & 1, kErrSoftmax);
           if (!ok) break;
+          float e[CH];
 #pragma unroll
           for (int i = 0; i < CH; ++i) {
             const int row = r_in + i * RPI;
             const uint4 gx = *reinterpret_cast<const uint4*>(g_tile + row * 128 + (((half * kChunk0 + c_in) ^ (row & 7)) << 4));
-            float e = dot_bf16x8(ox[i], gx);
-#pragma unroll
-            for (int x = LPR / 2; x > 0; x >>= 1) e += __shfl_xor_sync(0xffffffffu, e, x);
-            if (c_in == 0) halves[half * kBM + row] = e;
+            e[i] = dot_bf16x8(ox[i], gx);
           }
+          // LPR rows' sums over LPR lanes, each lane left with one row's
+          // (LPR - 1 shuffles; one sum after the other took 1800 cycles)
+#pragma unroll
+          for (int x = LPR / 2; x > 0; x >>= 1) {
+            const bool up = (c_in & x) != 0;
+#pragma unroll
+            for (int i = 0; i < x; ++i) {
+              const float give = up ? e[i] : e[i + x];
+              e[i] = (up ? e[i + x] : e[i]) + __shfl_xor_sync(0xffffffffu, give, x);
+            }
+          }
+          halves[half * kBM + r_in + c_in * RPI] = e[0];
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR_DELTA);
           ok = wait_all(BAR_DELTA, n & 1, kErrSoftmax);
