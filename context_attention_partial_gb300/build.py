@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG, "libcpattn.so")
 CHECK_LIB_PATH = os.path.join(PKG, "libcpattn_check.so")
 SOURCES = ["attn_fwd.cu", "merge_permute.cu", "cpattn_api.cu", "ring_noalloc.cu",
            "rotary.cu", "cross_simt.cu", "cross_fwd.cu",
-           "cross_bwd.cu", "cross_few.cu"]
+           "cross_bwd.cu", "cross_few.cu", "cross_f32.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "tmem_ops.cuh", "tile_ops.cuh", "check.cuh", "cross.cuh", "cross_ops.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

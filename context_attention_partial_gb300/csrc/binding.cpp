@@ -93,7 +93,11 @@ struct Call {
     if (!ok) return Tensor();
     if (o != Py_None) {
       const Tensor* t = tensor(o);
-      return t ? *t : Tensor();
+      if (t && !t->is_contiguous()) {
+        PyErr_SetString(PyExc_ValueError, "a workspace is contiguous");
+        ok = false;
+      }
+      return ok ? *t : Tensor();
     }
     return need > 0 ? at::empty({static_cast<int64_t>(need)}, at::TensorOptions().device(at::kCUDA, device).dtype(at::kByte))
                     : Tensor();

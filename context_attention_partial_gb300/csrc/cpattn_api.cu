@@ -400,8 +400,8 @@ bool cross_few(const cpattn_tensor* q, const cpattn_tensor* k) {
 // GPU, else as many as keep it full: for few rows one round of two CTAs per
 // SM (64 key heads x 16384 keys: 4 parts 83 us, 5 parts 109, 9 parts 85, 19
 // parts 91), each with 512 keys or more; for 256-row units of the tensor-core kernel
-// one per SM, each with four 128-key tiles or more; for fp32's blocks of few
-// rows likewise, each with 128 keys or more.
+// one per SM, each with four 128-key tiles or more; for fp32's blocks
+// likewise, each with 128 keys or more.
 int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
   const int64_t bh = q->shape[0] * q->shape[1], sm = cpattn::sm_count();
   if (bh == 0 || q->shape[2] == 0 || k->shape[2] == 0) return 1;
@@ -413,7 +413,7 @@ int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
   } else {
     int64_t units = (q->shape[2] + 255) / 256 * bh;
     if (q->dtype != CPATTN_BF16)
-      units = (q->shape[2] + 63) / 64 * bh >= sm ? sm : q->shape[2] > 2 ? (q->shape[2] + 7) / 8 * bh : bh;
+      units = cpattn::cross_f32_rows((q->shape[2] + 63) / 64 * bh) ? (q->shape[2] + 63) / 64 * bh : q->shape[2] > 2 ? (q->shape[2] + 7) / 8 * bh : bh;
     most = q->dtype == CPATTN_BF16 ? (k->shape[2] + 511) / 512 : (k->shape[2] + 127) / 128;
     want = sm / units;
   }
@@ -427,10 +427,13 @@ size_t cross_workspace(const cpattn_tensor* q, const cpattn_tensor* k) {
   return splits > 1 && rows > 0 ? static_cast<size_t>(splits) * rows * (q->shape[3] + 1) * 4 : 0;
 }
 
-// Parts of the query axis for dk and dv (bf16; fp32: 1).
+// Parts of the query axis for dk and dv.
 int cross_parts(const cpattn_tensor* q, const cpattn_tensor* k) {
   const int64_t rows = q->shape[0] * q->shape[1] * q->shape[2], keys = k->shape[0] * k->shape[1] * k->shape[2];
-  if (q->dtype != CPATTN_BF16 || rows == 0 || keys == 0) return 1;
+  if (rows == 0 || keys == 0) return 1;
+  if (q->dtype != CPATTN_BF16)
+    return cpattn::cross_f32_parts(k->shape[0] * k->shape[1] * ((k->shape[2] + 63) / 64),
+                                   q->shape[1] / k->shape[1] * ((q->shape[2] + 63) / 64));
   return cpattn::cross_backward_parts(k->shape[0] * k->shape[1] * ((k->shape[2] + 127) / 128),
                                       q->shape[1] / k->shape[1] * ((q->shape[2] + 127) / 128));
 }
@@ -838,7 +841,7 @@ cpattn_status cpattn_cross_attention_backward(const cpattn_tensor* q, const cpat
     if ((st = make_tmap(&m.dv, dv, 32)) != CPATTN_OK) return st;
     e = cpattn::launch_cross_bwd(D, m, p, cross_delta_floats(q), cs);
   } else {
-    e = cpattn::launch_cross_simt_backward(D, p, cs);
+    e = cpattn::launch_cross_simt_backward(D, p, cross_delta_floats(q), cs);
   }
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }

@@ -57,6 +57,17 @@ cudaError_t cross_set_up(K kernel, size_t smem, std::atomic<unsigned long long>&
   return e;
 }
 
+// Launches `kernel` on blocks x splits blocks (one instantiation, so one set-up
+// record, per kernel).
+template <auto kernel, typename... Args>
+cudaError_t cross_run(int64_t blocks, int splits, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+  static std::atomic<unsigned long long> ready{0};
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const cudaError_t e = cross_set_up(kernel, smem, ready);
+  if (e != cudaSuccess) return e;
+  return launch_behind(kernel, dim3(static_cast<unsigned>(blocks), splits), threads, smem, stream, args...);
+}
+
 // bf16 inputs, D 64 or 128, on the tensor cores (s_kv >= 1; the maps' boxes
 // have 128 rows, the output's 32).
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
@@ -76,9 +87,23 @@ cudaError_t launch_cross_bwd(int head_dim, const CrossBwdMaps& maps, const Cross
 // 128-row query tiles each
 int cross_backward_parts(int64_t key_units, int64_t steps);
 // fp32 inputs (D 64 or 128; s_q, s_kv >= 1); the gradient keeps delta, [B, H, S_q],
-// at the workspace's start.
+// at the workspace's start, and, when p.splits > 1, partial sums of dk and dv
+// `partials` floats into it.
 cudaError_t launch_cross_simt(int head_dim, const CrossParams& p, cudaStream_t stream);
-cudaError_t launch_cross_simt_backward(int head_dim, const CrossParams& p, cudaStream_t stream);
+cudaError_t launch_cross_simt_backward(int head_dim, const CrossParams& p, int64_t partials, cudaStream_t stream);
+// whether fp32 calls with that many 64-row query blocks, or 64 x 64 tiles of dk
+// and dv, take 64-row blocks
+bool cross_f32_rows(int64_t blocks);
+bool cross_f32_keys(int64_t tiles);
+// parts of the query axis for key_units 64-key tiles that walk `steps` 64-row
+// query tiles each
+int cross_f32_parts(int64_t key_units, int64_t steps);
+// the same in 64-row blocks, for calls with many rows (dq takes no splits)
+cudaError_t launch_cross_f32(int head_dim, const CrossParams& p, cudaStream_t stream);
+cudaError_t launch_cross_f32_dq(int head_dim, const CrossParams& p, cudaStream_t stream);
+cudaError_t launch_cross_f32_dkv(int head_dim, const CrossParams& p, int64_t partials, cudaStream_t stream);
+// adds up p.splits partial sums of dk and dv
+cudaError_t launch_cross_dkv_join(InDtype dt, int head_dim, const CrossParams& p, int64_t partials, cudaStream_t stream);
 // dq, dk, dv = 0 (no queries, or no keys).
 cudaError_t launch_cross_zeros(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream);
 // joins p.splits partial outputs of the workspace into out and lse

@@ -942,34 +942,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
 }
-
-// Sums the parts of dk and dv in their order: one thread per four values.
-template <int D>
-__global__ void __launch_bounds__(256) cross_dkv_join_kernel(const __grid_constant__ CrossParams p, const int64_t partials) {
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.kv_heads * p.s_kv, n = rows * (D / 4);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  launch_wait();   // (the parts are written)
-  launch_next();
-  if (i >= 2 * n) return;
-  const int which = i >= n;   // 0: dk, 1: dv
-  const int64_t at = i - which * n;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* src = reinterpret_cast<const float4*>(p.ws + partials) + which * n + at;
-#pragma unroll 4
-  for (int x = 0; x < p.splits; ++x) {
-    const float4* s = src + 2 * x * n;
-    if (!CPATTN_IN(p.ws_span, s, 16, p.err)) continue;
-    const float4 v = *s;
-    sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
-  }
-  const float f = which ? 1.f : p.scale;
-  const CrossTensor& t = which ? p.dv : p.dk;
-  const int64_t row = at / (D / 4), key = row % p.s_kv, bh = row / p.s_kv, h = bh % p.kv_heads, b = bh / p.kv_heads;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(t.data) + b * t.s[0] + h * t.s[1] + key * t.s[2] + (at % (D / 4)) * 4;
-  if (CPATTN_IN(t.span, dst, 8, p.err))
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
-}
-
 // Once per device and kernel: the register split needs exactly kLaunchRegs at
 // launch (refused otherwise), and the shared-memory limit is raised.
 template <typename K>
@@ -997,16 +969,13 @@ cudaError_t launch_typed(const CrossBwdMaps& m, const CrossParams& p, int64_t pa
   const int64_t sms = sm_count();
   const int64_t units = static_cast<int64_t>(p.batch) * p.heads * ((p.s_q + kBM - 1) / kBM);
   const int64_t ctas = static_cast<int64_t>(p.batch) * p.kv_heads * p.splits * ((p.s_kv + kBM - 1) / kBM);
-  const int64_t rows = static_cast<int64_t>(p.batch) * p.kv_heads * p.s_kv, join = (2 * rows * (D / 4) + 255) / 256;
-  if (units > 0x7fffffff || ctas > 0x7fffffff || join > 0x7fffffff) return cudaErrorInvalidValue;
+  if (units > 0x7fffffff || ctas > 0x7fffffff) return cudaErrorInvalidValue;
   e = launch_behind(cross_dq_kernel<D>, dim3(static_cast<unsigned>(units < sms ? units : sms)), kThreads, C::DQ_SMEM,
                     stream, m.q, m.k, m.v, m.dout, m.out, m.dq, p);
   if (e != cudaSuccess) return e;
   e = launch_behind(cross_dkv_kernel<D>, dim3(static_cast<unsigned>(ctas)), kThreads, C::KV_SMEM, stream, m.q, m.k, m.v,
                     m.dout, m.dk, m.dv, p, partials);
-  if (e == cudaSuccess && p.splits > 1)
-    e = launch_behind(cross_dkv_join_kernel<D>, dim3(static_cast<unsigned>(join)), 256, 0, stream, p, partials);
-  return e;
+  return e == cudaSuccess && p.splits > 1 ? launch_cross_dkv_join(InDtype::BF16, D, p, partials, stream) : e;
 }
 
 }  // namespace

@@ -11,14 +11,13 @@
 // owning query rows (dq), one owning keys (dk, dv): every sum has one owner
 // and a fixed order, at the price of forming s and do . v twice.
 //
-// Layout: a warp owns R rows (query rows, or keys in the dk/dv kernel), its
+// Layout, for calls of fewer rows than cross_f32.cu takes: a warp owns R rows (query rows, or keys in the dk/dv kernel), its
 // lanes own C rows each of a 32 C-row tile of the other side for the dot
 // products over D, and D / 32 features each for the products over the tile.
 // A tile row is padded by 16 bytes, so both walks are free of bank conflicts.
-// The R rows' values are broadcast reads: R = 8, C = 2 takes 16 shared-memory
-// wavefronts for 64 FMA instructions, which the four FP32 pipes issue in 16
-// cycles (C = 1: 12 for 32, bound by shared memory); R = 2, C = 1 serves calls
-// with few rows.
+// R = 2, C = 1: the blocks are small, so few rows make many of them; what
+// bounds them is shared memory and the latency of a short walk (one query x 500
+// keys x 16 heads 12.8 us, its gradient 46).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -529,6 +528,34 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
   }
 }
 
+
+// Sums the parts of dk and dv in their order: one thread per four values.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_dkv_join_kernel(const __grid_constant__ CrossParams p, const int64_t partials) {
+  const int64_t rows = static_cast<int64_t>(p.batch) * p.kv_heads * p.s_kv, n = rows * (D / 4);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  launch_wait();   // (the parts are written)
+  launch_next();
+  if (i >= 2 * n) return;
+  const int which = i >= n;   // 0: dk, 1: dv
+  const int64_t at = i - which * n;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* src = reinterpret_cast<const float4*>(p.ws + partials) + which * n + at;
+#pragma unroll 4
+  for (int x = 0; x < p.splits; ++x) {
+    const float4* s = src + 2 * x * n;
+    if (!CPATTN_IN(p.ws_span, s, 16, p.err)) continue;
+    const float4 v = *s;
+    sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+  }
+  const float f = which ? 1.f : p.scale;
+  const CrossTensor& t = which ? p.dv : p.dk;
+  const int64_t row = at / (D / 4), key = row % p.s_kv, bh = row / p.s_kv, h = bh % p.kv_heads, b = bh / p.kv_heads;
+  T* dst = static_cast<T*>(t.data) + b * t.s[0] + h * t.s[1] + key * t.s[2] + (at % (D / 4)) * 4;
+  const float res[4] = {sum.x * f, sum.y * f, sum.z * f, sum.w * f};
+  if (CPATTN_IN(t.span, dst, 4 * sizeof(T), p.err)) store_n<T, 4>(dst, res);
+}
+
 // A gradient without terms (no queries, or no keys): zeros.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) cross_zero_kernel(const CrossTensor t, int batch, int heads, int rows, unsigned int* err) {
@@ -543,16 +570,6 @@ __global__ void __launch_bounds__(256) cross_zero_kernel(const CrossTensor t, in
   if (CPATTN_IN(t.span, dst, 16, err)) *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
 }
 
-// (one instantiation, so one set-up record, per kernel)
-template <auto kernel>
-cudaError_t run(int64_t blocks, int splits, int threads, size_t smem, const CrossParams& p, cudaStream_t stream) {
-  static std::atomic<unsigned long long> ready{0};
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const cudaError_t e = cross_set_up(kernel, smem, ready);
-  if (e != cudaSuccess) return e;
-  return launch_behind(kernel, dim3(static_cast<unsigned>(blocks), splits), threads, smem, stream, p);
-}
-
 int64_t tiles_of(int rows, int per) { return (rows + per - 1) / per; }
 
 // Shared memory of the kernels in floats: the rows a block owns, two stages of
@@ -561,45 +578,43 @@ constexpr size_t simt_smem(int D, int rows, int tile, int weights) {
   return sizeof(float) * (static_cast<size_t>(rows) * D + 4 * tile * (D + 4) + weights);
 }
 
+
 template <int D>
 cudaError_t forward_typed(const CrossParams& p, cudaStream_t stream) {
   const int64_t bh = static_cast<int64_t>(p.batch) * p.heads;
-  // 64 rows a block where that fills the GPU; else 8 or 16, and for one or two
-  // queries 2 rows a block, the KS warps of each row taking every KS-th tile
+  if (cross_f32_rows(tiles_of(p.s_q, 64) * bh)) return launch_cross_f32(D, p, stream);
+  // 8 or 16 rows a block, and for one or two queries 2, the KS warps of each
+  // row taking every KS-th tile
   constexpr int KS = D == 64 ? 4 : 2;
-  if (tiles_of(p.s_q, 64) * bh >= sm_count())
-    return run<cross_simt_kernel<D, 8, 8, 2, 1>>(tiles_of(p.s_q, 64) * bh, p.splits, 256,
-                                                 simt_smem(D, 64, 64, 8 * 8 * 64), p, stream);
   if (p.s_q > 2)
-    return run<cross_simt_kernel<D, 16, 2, 1, KS>>(tiles_of(p.s_q, 32 / KS) * bh, p.splits, 512,
-                                                   simt_smem(D, 32 / KS, 32 * KS, 16 * 2 * 32), p, stream);
-  return run<cross_simt_kernel<D, KS, 2, 1, KS>>(tiles_of(p.s_q, 2) * bh, p.splits, 32 * KS,
-                                                 simt_smem(D, 2, 32 * KS, KS * 2 * 32), p, stream);
+    return cross_run<cross_simt_kernel<D, 16, 2, 1, KS>>(tiles_of(p.s_q, 32 / KS) * bh, p.splits, 512,
+                                                         simt_smem(D, 32 / KS, 32 * KS, 16 * 2 * 32), stream, p);
+  return cross_run<cross_simt_kernel<D, KS, 2, 1, KS>>(tiles_of(p.s_q, 2) * bh, p.splits, 32 * KS,
+                                                       simt_smem(D, 2, 32 * KS, KS * 2 * 32), stream, p);
 }
 
 template <int D>
-cudaError_t backward_typed(const CrossParams& p, cudaStream_t stream) {
+cudaError_t backward_typed(const CrossParams& p, int64_t partials, cudaStream_t stream) {
   const int64_t bh = static_cast<int64_t>(p.batch) * p.heads;
   const int64_t bk = static_cast<int64_t>(p.batch) * p.kv_heads;
   const int64_t n = bh * p.s_q * (D / 4);
   if ((n + 255) / 256 > 0x7fffffff) return cudaErrorInvalidValue;
   cudaError_t e = launch_behind(cross_delta_kernel<D>, dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream, p);
   if (e != cudaSuccess) return e;
-  if (tiles_of(p.s_q, 64) * bh >= sm_count())
-    e = run<cross_simt_dq_kernel<D, 8, 8, 2>>(tiles_of(p.s_q, 64) * bh, 1, 256, simt_smem(D, 128, 64, 8 * 8 * 64), p,
-                                              stream);
+  // (dq takes no splits: 64-row blocks from a quarter of the SMs; 32 blocks x
+  // 100 keys at D = 64: 26 us without, 30 with)
+  if (tiles_of(p.s_q, 64) * bh * 4 >= sm_count())
+    e = launch_cross_f32_dq(D, p, stream);
   else
-    e = run<cross_simt_dq_kernel<D, 4, 2, 1>>(tiles_of(p.s_q, 8) * bh, 1, 128, simt_smem(D, 16, 32, 4 * 2 * 32), p,
-                                              stream);
+    e = cross_run<cross_simt_dq_kernel<D, 4, 2, 1>>(tiles_of(p.s_q, 8) * bh, 1, 128, simt_smem(D, 16, 32, 4 * 2 * 32),
+                                                    stream, p);
   if (e != cudaSuccess) return e;
-  // 32 keys a block, two blocks an SM: with 64 keys, 192 blocks took two rounds
-  // of 152 SMs (24 heads x 512 keys x 1024 queries)
-  constexpr int C = D == 64 ? 2 : 1;   // (shared memory)
-  if (tiles_of(p.s_kv, 32) * bk >= sm_count())
-    return run<cross_simt_dkv_kernel<D, 4, 8, C>>(tiles_of(p.s_kv, 32) * bk, 1, 128,
-                                                  simt_smem(D, 64, 32 * C, 2 * 4 * 8 * 32 * C), p, stream);
-  return run<cross_simt_dkv_kernel<D, 4, 2, 1>>(tiles_of(p.s_kv, 8) * bk, 1, 128,
-                                                simt_smem(D, 16, 32, 2 * 4 * 2 * 32), p, stream);
+  if (cross_f32_keys(tiles_of(p.s_kv, 64) * bk * tiles_of(p.s_q, 64) * (p.heads / p.kv_heads))) {
+    e = launch_cross_f32_dkv(D, p, partials, stream);
+    return e == cudaSuccess && p.splits > 1 ? launch_cross_dkv_join(InDtype::F32, D, p, partials, stream) : e;
+  }
+  return cross_run<cross_simt_dkv_kernel<D, 4, 2, 1>>(tiles_of(p.s_kv, 8) * bk, 1, 128,
+                                                      simt_smem(D, 16, 32, 2 * 4 * 2 * 32), stream, p);
 }
 
 template <typename T, int D>
@@ -624,8 +639,47 @@ cudaError_t launch_cross_simt(int head_dim, const CrossParams& p, cudaStream_t s
   return head_dim == 64 ? forward_typed<64>(p, stream) : forward_typed<128>(p, stream);
 }
 
-cudaError_t launch_cross_simt_backward(int head_dim, const CrossParams& p, cudaStream_t stream) {
-  return head_dim == 64 ? backward_typed<64>(p, stream) : backward_typed<128>(p, stream);
+cudaError_t launch_cross_simt_backward(int head_dim, const CrossParams& p, int64_t partials, cudaStream_t stream) {
+  return head_dim == 64 ? backward_typed<64>(p, partials, stream) : backward_typed<128>(p, partials, stream);
+}
+
+// Against the kernels of this file, us, this / 64-row blocks.  Forward, 512
+// keys x 8 heads at D = 128: 64 queries 24.1 / 24.1 (8 blocks: this kernel),
+// 128 queries 39 / 21, 512 queries 77 / 36; 128 queries x 100 keys x 16 heads
+// at D = 64 11.0 / 12.0.  Gradient (dk, dv), 100 keys as before (64 tiles) 26 /
+// 41, 256 x 512 x 2 heads (64 tiles) 75 / 61, 128 x 512 x 8 heads (128 tiles)
+// 99 / 92, 300 x 256 x 16 heads at D = 64 (320 tiles) 84 / 76.
+bool cross_f32_rows(int64_t blocks) { return blocks * 8 >= sm_count(); }
+bool cross_f32_keys(int64_t tiles) { return tiles * 2 >= sm_count(); }
+
+int cross_f32_parts(int64_t key_units, int64_t steps) {
+  if (!cross_f32_keys(key_units * steps)) return 1;
+  // as cross_backward_parts: a block's start and end count as one step, the
+  // join as one
+  const int64_t sms = sm_count();
+  int best = 1;
+  int64_t least = 0;
+  for (int parts = 1; parts <= 32 && parts <= steps; ++parts) {
+    const int64_t waves = (key_units * parts + sms - 1) / sms;
+    const int64_t cost = waves * ((steps + parts - 1) / parts + 1) + (parts > 1 ? 1 : 0);
+    if (parts == 1 || cost < least) {
+      best = parts;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_cross_dkv_join(InDtype dt, int head_dim, const CrossParams& p, int64_t partials,
+                                  cudaStream_t stream) {
+  const int64_t blocks = (2 * static_cast<int64_t>(p.batch) * p.kv_heads * p.s_kv * (head_dim / 4) + 255) / 256;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if (dt == InDtype::BF16)
+    return launch_behind(head_dim == 64 ? cross_dkv_join_kernel<__nv_bfloat16, 64> : cross_dkv_join_kernel<__nv_bfloat16, 128>,
+                         grid, 256, 0, stream, p, partials);
+  return launch_behind(head_dim == 64 ? cross_dkv_join_kernel<float, 64> : cross_dkv_join_kernel<float, 128>, grid, 256, 0,
+                       stream, p, partials);
 }
 
 cudaError_t launch_cross_zeros(InDtype dt, int head_dim, const CrossParams& p, cudaStream_t stream) {

@@ -88,6 +88,21 @@ def test_cross_matches_plain(case, dtype):
     run(case, dtype)
 
 
+MANY = [
+    (2, 12, 4, 515, 300, 128, (300, 161)),            # rows that fill the GPU, shared heads
+    (4, 16, 16, 190, 257, 64, (0, 1, 128, 257)),
+    (3, 20, 5, 200, 64, 128, (64, 33, 5)),
+    (1, 40, 40, 256, 129, 64, (-3,)),
+    (1, 3, 3, 1500, 1030, 64, None),                  # few key tiles: dk, dv in parts
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "x".join(map(str, c[:6])) + ("r" if c[6] else ""))
+def test_cross_many_rows(case, dtype):
+    run(case, dtype, layout="bshd", seed=2)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 def test_cross_layouts_and_scale(dtype):
     run((2, 6, 3, 70, 150, 64, (150, 90)), dtype, layout="bshd", scale=0.3, seed=3)
@@ -252,6 +267,44 @@ def test_cross_streams_and_graphs(M):
     assert cp.last_device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_cross_captured_across_two_streams(dtype):
+    """A captured graph that forks (a key side and a query side on two streams)
+    and joins: every kernel waits for both of the kernels it depends on."""
+    q, k, v, dout, n = make(2, 8, 2, 200, 700, 128, dtype, (700, 333), seed=35, poison=False)
+    pos = torch.arange(700, device=DEV).float()[:, None]
+
+    def step(side):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            rk = cp.rotary(k * 2, pos, (128,))
+        rq = cp.rotary(q * 2, pos[:200], (128,))
+        main.wait_stream(side)
+        out, lse = cp.cross_attention(rq, rk, v, kv_lengths=n)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            grads = cp.cross_attention_backward(rq, rk, v, out, lse, dout, kv_lengths=n)
+        y = cp.rotary(out, pos[:200], (128,))
+        main.wait_stream(side)
+        return (rk, out, lse, y, *grads, cp.rotary(grads[0], pos[:200], (128,), inverse=True))
+
+    side = torch.cuda.Stream()
+    want = step(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(side)
+    for _ in range(3):
+        for t in got:
+            t.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert cp.last_device_status() == 0
+
+
 def test_cross_workspace_given_and_refused():
     q, k, v, dout, _ = make(1, 2, 2, 1, 6000, 128, BF)
     need = cp.cross_workspace_bytes(q, k)
@@ -263,6 +316,8 @@ def test_cross_workspace_given_and_refused():
     with pytest.raises(cp.CpattnError) as e:
         cp.cross_attention(q, k, v, workspace=guard[: need - 16])
     assert e.value.name == "CPATTN_ERR_WORKSPACE"
+    with pytest.raises(ValueError, match="contiguous"):    # fewer bytes than it seems to have
+        cp.cross_attention(q, k, v, workspace=torch.zeros(1, dtype=torch.uint8, device=DEV).expand(need))
     need = cp.cross_backward_workspace_bytes(q, k)
     guard = torch.full((need + 64,), 0x5A, dtype=torch.uint8, device=DEV)
     cp.cross_attention_backward(q, k, v, *want, dout, workspace=guard[:need])

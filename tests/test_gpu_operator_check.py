@@ -55,6 +55,8 @@ CASES = [
     (1, 2, 2, 257, 513, 128, (500,)),
     (2, 8, 2, 1, 5001, 128, (5001, 3000)),
     (1, 24, 24, 1000, 301, 64, None),
+    (2, 8, 2, 900, 333, 128, (333, 70)),
+    (1, 3, 3, 1500, 1030, 64, None),
 ]
 
 
