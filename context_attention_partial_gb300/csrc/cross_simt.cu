@@ -11,9 +11,10 @@
 // owning query rows (dq), one owning keys (dk, dv): every sum has one owner
 // and a fixed order, at the price of forming s and do . v twice.
 //
-// Layout, for calls of fewer rows than cross_f32.cu takes: a warp owns R rows (query rows, or keys in the dk/dv kernel), its
-// lanes own C rows each of a 32 C-row tile of the other side for the dot
-// products over D, and D / 32 features each for the products over the tile.
+// Layout, for calls of fewer rows than cross_f32.cu takes: a warp owns R rows
+// (query rows, or keys in the dk/dv kernel), its lanes own C rows each of a 32
+// C-row tile of the other side for the dot products over D, and D / 32 features
+// each for the products over the tile.
 // A tile row is padded by 16 bytes, so both walks are free of bank conflicts.
 // R = 2, C = 1: the blocks are small, so few rows make many of them; what
 // bounds them is shared memory and the latency of a short walk (one query x 500
