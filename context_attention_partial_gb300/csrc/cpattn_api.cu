@@ -397,34 +397,44 @@ bool cross_few(const cpattn_tensor* q, const cpattn_tensor* k) {
 }
 
 // Parts of the key axis of a forward call: 1 where the query rows fill the
-// GPU, else as many as keep it full: for few rows one round of two CTAs per
-// SM (64 key heads x 16384 keys: 4 parts 83 us, 5 parts 109, 9 parts 85, 19
-// parts 91), each with 512 keys or more; for 256-row units of the tensor-core kernel
-// one per SM, each with four 128-key tiles or more; for fp32's blocks
-// likewise, each with 128 keys or more.
+// GPU, else as many as keep it full.  For few rows one round of two CTAs per SM
+// (64 key heads x 16384 keys: 4 parts 79 us, 8 parts 82, 16 parts 95), each with
+// 192 keys or more (2 key heads x 6000 keys: 8 parts 11.4 us, 16 parts 10.5, 32
+// parts 9.0, 128 parts 9.8), above 8 parts whole clusters; two clusters and
+// their join gain on one only past some 8000 keys (8 key heads: 4096 keys 9.0 us
+// with one, 10.9 with two; 8192 14.9 / 15.2; 16384 25.0 / 22.1).  For 256-row
+// units of the tensor-core kernel one per SM, each with four 128-key tiles or
+// more; for fp32's blocks likewise, each with 128 keys or more.
 int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
   const int64_t bh = q->shape[0] * q->shape[1], sm = cpattn::sm_count();
   if (bh == 0 || q->shape[2] == 0 || k->shape[2] == 0) return 1;
   int64_t most, want;
   if (cross_few(q, k)) {
     const int64_t units = q->shape[0] * k->shape[1];
-    most = (k->shape[2] + 511) / 512;
+    most = (k->shape[2] + 191) / 192;
     want = 2 * sm / units;
   } else {
     int64_t units = (q->shape[2] + 255) / 256 * bh;
-    if (q->dtype != CPATTN_BF16)
-      units = cpattn::cross_f32_rows((q->shape[2] + 63) / 64 * bh) ? (q->shape[2] + 63) / 64 * bh : q->shape[2] > 2 ? (q->shape[2] + 7) / 8 * bh : bh;
+    if (q->dtype != CPATTN_BF16) {
+      units = (q->shape[2] + 63) / 64 * bh;
+      if (!cpattn::cross_f32_rows(units)) units = q->shape[2] > 2 ? (q->shape[2] + 7) / 8 * bh : bh;
+    }
     most = q->dtype == CPATTN_BF16 ? (k->shape[2] + 511) / 512 : (k->shape[2] + 127) / 128;
     want = sm / units;
   }
-  const int64_t s = want < most ? want : most;
+  int64_t s = want < most ? want : most;
+  if (cross_few(q, k) && s > cpattn::kCrossCluster) {
+    s -= s % cpattn::kCrossCluster;
+    if (s < 3 * cpattn::kCrossCluster && k->shape[2] <= 8192) s = cpattn::kCrossCluster;
+  }
   return s > 1 ? static_cast<int>(s < 65535 ? s : 65535) : 1;
 }
 
 size_t cross_workspace(const cpattn_tensor* q, const cpattn_tensor* k) {
   const int64_t rows = q->shape[0] * q->shape[1] * q->shape[2];
   const int splits = cross_splits(q, k);
-  return splits > 1 && rows > 0 ? static_cast<size_t>(splits) * rows * (q->shape[3] + 1) * 4 : 0;
+  const int parts = cross_few(q, k) ? splits / cpattn::kCrossCluster : splits;
+  return parts > 1 && rows > 0 ? static_cast<size_t>(parts) * rows * (q->shape[3] + 1) * 4 : 0;
 }
 
 // Parts of the query axis for dk and dv.
@@ -770,8 +780,11 @@ cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   p.splits = p.s_kv > 0 ? cross_splits(q, k) : 0;
+  bool join = p.splits != 1;   // (no parts: the join writes the empty result)
   if (p.splits > 0 && cross_few(q, k)) {
     e = cpattn::launch_cross_few(D, p, cs);
+    p.splits /= cpattn::kCrossCluster;   // (parts in the workspace)
+    join = p.splits > 1;
   } else if (p.splits > 0 && dt == InDtype::BF16) {
     CUtensorMap tm_q, tm_k, tm_v, tm_o;
     if ((st = make_tmap(&tm_q, q, 128)) != CPATTN_OK) return st;
@@ -782,8 +795,7 @@ cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor
   } else if (p.splits > 0) {
     e = cpattn::launch_cross_simt(D, p, cs);
   }
-  // (no parts: the join writes the empty result)
-  if (e == cudaSuccess && p.splits != 1) e = cpattn::launch_cross_join(dt, D, p, cs);
+  if (e == cudaSuccess && join) e = cpattn::launch_cross_join(dt, D, p, cs);
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
 

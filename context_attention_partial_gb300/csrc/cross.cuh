@@ -73,7 +73,10 @@ cudaError_t cross_run(int64_t blocks, int splits, int threads, size_t smem, cuda
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                              const CUtensorMap& tm_v, const CUtensorMap& tm_o, const CrossParams& p,
                              cudaStream_t stream);
-// the same for at most 64 query rows a key head (s_q * H / H_kv)
+// the same for at most 64 query rows a key head (s_q * H / H_kv); p.splits up
+// to kCrossCluster, or a multiple of it: then the workspace gets
+// p.splits / kCrossCluster parts to join
+constexpr int kCrossCluster = 8;
 cudaError_t launch_cross_few(int head_dim, const CrossParams& p, cudaStream_t stream);
 // its gradient (s_q, s_kv >= 1; the kernels write delta to the workspace's start
 // and, when p.splits > 1, partial sums of dk and dv `partials` floats into it;

@@ -4,8 +4,10 @@
 // Mathematics as in cross_fwd.cu; the rows are the S_q queries of every query
 // head that shares a key head (at most 64), so each key and value is read once
 // per key head.  What bounds it is that read: 4 D bytes a key.  The key axis
-// is split over CTAs until the GPU is full, and the parts are joined by their
-// lse (cross_simt.cu).
+// is split over CTAs until the GPU is full.  8 parts (or fewer, where that is
+// enough) are a cluster and join in its shared memory; the results of several
+// clusters go to the workspace and are joined by their lse in a second kernel
+// (cross_simt.cu).
 //
 // A CTA of 4 warps walks its keys in stages of 64, three or more stages in
 // flight by 16-byte asynchronous copies (rows past the length are zero-filled
@@ -44,7 +46,7 @@ struct Few {
   static constexpr int CH = ROW / 16;                     // 16-byte chunks of a row
   static constexpr int STAGES = D == 128 ? 3 : 4;
   static constexpr int STAGE = 2 * kKeys * ROW;           // K and V
-  static constexpr int JOIN = 4 * 16 * (D + 4) * 4 + 4 * 16 * 8;
+  static constexpr int JOIN = 4 * 16 * (D + 4) * 4 + 2 * 4 * 16 * 8;
   static constexpr int SMEM = STAGES * STAGE > JOIN ? STAGES * STAGE : JOIN;
 };
 
@@ -235,34 +237,70 @@ __global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_consta
     if (lane % 4 == 0) sm[r] = make_float2(m[i], l[i]);
   }
   __syncthreads();
-  const int64_t n_rows = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
+  // the key groups of this block: their sums over group 0's, (m, l) to sj
+  float2* sj = sm + 4 * 16;
   for (int i = threadIdx.x; i < MT * 16 * (D / 4); i += kThreads) {
     const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-    if (r >= rows) break;
-    const int tile = r / 16, in_tile = r % 16;
     float top = -INFINITY;
 #pragma unroll
-    for (int g = 0; g < KG; ++g) top = fmaxf(top, sm[(g * MT + tile) * 16 + in_tile].x);
+    for (int g = 0; g < KG; ++g) top = fmaxf(top, sm[g * MT * 16 + r].x);
     const float base = top == -INFINITY ? 0.f : top;
     float total = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int g = 0; g < KG; ++g) {
-      const int at = (g * MT + tile) * 16 + in_tile;
+      const int at = g * MT * 16 + r;
       const float w = ex2_approx(sm[at].x - base);
       const float4 x = *reinterpret_cast<const float4*>(so + at * (D + 4) + d);
       total = fmaf(w, sm[at].y, total);
       sum = make_float4(fmaf(w, x.x, sum.x), fmaf(w, x.y, sum.y), fmaf(w, x.z, sum.z), fmaf(w, x.w, sum.w));
     }
-    const bool none = tiles == 0;
+    *reinterpret_cast<float4*>(so + r * (D + 4) + d) = sum;
+    if (d == 0) sj[r] = make_float2(top, total);
+  }
+  // the blocks of a cluster share out the rows
+  const int parts = min(p.splits, kCrossCluster), rank = blockIdx.y % parts, cluster = blockIdx.y / parts;
+  const bool clustered = parts > 1;
+  if (clustered) cluster_sync(); else __syncthreads();
+  const int64_t n_rows = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
+  for (int i = rank * kThreads + threadIdx.x; i < MT * 16 * (D / 4); i += kThreads * parts) {
+    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+    if (r >= rows) break;
+    float top, total;
+    float4 sum;
+    if (!clustered) {
+      top = sj[r].x;
+      total = sj[r].y;
+      sum = *reinterpret_cast<const float4*>(so + r * (D + 4) + d);
+    } else {
+      float2 ml[kCrossCluster];
+      top = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kCrossCluster; ++x) {
+        ml[x] = x < parts ? cluster_load2(cluster_addr(smem_addr(sj + r), x)) : make_float2(-INFINITY, 0.f);
+        top = fmaxf(top, ml[x].x);
+      }
+      const float base = top == -INFINITY ? 0.f : top;
+      total = 0.f;
+      sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kCrossCluster; ++x) {
+        if (x >= parts) continue;
+        const float w = ex2_approx(ml[x].x - base);
+        const float4 y = cluster_load4(cluster_addr(smem_addr(so + r * (D + 4) + d), x));
+        total = fmaf(w, ml[x].y, total);
+        sum = make_float4(fmaf(w, y.x, sum.x), fmaf(w, y.y, sum.y), fmaf(w, y.z, sum.z), fmaf(w, y.w, sum.w));
+      }
+    }
+    const bool none = cluster * parts * per >= all;   // (no keys in this cluster's parts)
     const float inv = none ? 0.f : 1.f / total;
     sum = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
     const float lse = none ? -INFINITY : (top + log2f(total)) * kLn2;
     const int qi = r / share, h = hk * share + r % share;
-    if (p.splits > 1) {
-      const int64_t at = blockIdx.y * n_rows + (static_cast<int64_t>(b) * p.heads + h) * p.s_q + qi;
+    if (p.splits > parts) {
+      const int64_t at = cluster * n_rows + (static_cast<int64_t>(b) * p.heads + h) * p.s_q + qi;
       float* dst = p.ws + at * D + d;
-      float* dl = p.ws + p.splits * n_rows * D + at;
+      float* dl = p.ws + p.splits / parts * n_rows * D + at;
       if (!none && CPATTN_IN(p.ws_span, dst, 16, p.err)) *reinterpret_cast<float4*>(dst) = sum;
       if (d == 0 && CPATTN_IN(p.ws_span, dl, 4, p.err)) *dl = lse;
     } else {
@@ -274,6 +312,7 @@ __global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_consta
       if (d == 0 && CPATTN_IN(p.lse.span, dl, 4, p.err)) *dl = lse;
     }
   }
+  if (clustered) cluster_sync();   // (shared memory stays until every block has read it)
 }
 
 template <int D, int MT>
@@ -285,7 +324,8 @@ cudaError_t launch_tiles(const CrossParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(p.batch) * p.kv_heads;
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_behind(kernel, dim3(static_cast<unsigned>(units), p.splits), kThreads, C::SMEM, stream, p);
+  return launch_behind_clustered(kernel, dim3(static_cast<unsigned>(units), p.splits),
+                                 p.splits < kCrossCluster ? p.splits : kCrossCluster, kThreads, C::SMEM, stream, p);
 }
 
 template <int D>
