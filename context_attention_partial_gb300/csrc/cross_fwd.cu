@@ -139,7 +139,12 @@ struct UnitWalk {
   }
 };
 
-template <int D>
+// PAIR: the two query tiles are the same one (S_q <= 128), its key tiles
+// alternate between them, each with sums of its own, and the warps of the first
+// take the second's over at the end; a CTA has one unit.  A lone tile's products
+// and exponentials wait for one another (some 2600 cycles a key tile); two
+// chains fill each other's waits.
+template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -335,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool pair = more || more_units;
           const uint32_t kv_bar = pair ? bar_full(sk) : bar_full(sv), kv_ph = pair ? (lk / C::STAGES) & 1 : 0u;
           const bool kv_now = mbar_test(kv_bar, kv_ph);
-          const bool p0_now = mbar_test(bar_p(0), np[0] & 1);
+          const bool p0_now = !PAIR && mbar_test(bar_p(0), np[0] & 1);
           const uint32_t vb = static_cast<uint32_t>(v_desc) + ((sv * C::TILE) >> 4);
           const uint32_t kb = static_cast<uint32_t>(k_desc) + ((sk * C::TILE) >> 4);
           uint32_t vd[C::PV], kd[C::QK], qd[C::QK], pa[C::PV];
@@ -354,6 +359,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const int valid = w.k1 - (w.k0 + j * kBN);
           if (valid < kBN) zero_tile_rows<D>(smem + (2 + sv) * C::TILE, valid);
+          if constexpr (PAIR) {
+            const int i = j & 1;
+            if (more && leader) {
+              // (S_1-i's last P V was issued a step ago)
+              tc_fence_after();
+              mma_group<C::QK, true>(tmem + (i ^ 1) * kBN, qd, kd, hi, C::IDESC_QK, 0u);
+              mma_commit(bar_s(i ^ 1));
+              if (j + 2 == w.tiles) mma_commit(bar_qfree(0));
+              mma_commit(bar_empty(sk));
+            }
+            __syncwarp();
+            ok = wait_all(bar_p(i), np[i] & 1, kErrMma);
+            if (!ok) break;
+            ++np[i];
+#pragma unroll
+            for (int kk = 0; kk < C::PV; ++kk) pa[kk] += i * kBN;
+            tc_fence_after();
+            if (leader) {
+              mma_group<C::PV, false>(tmem + C::O_COL + i * D, pa, vd, hi, C::IDESC_PV, j > 1);
+              mma_commit(bar_empty(sv));
+              if (j + 2 >= w.tiles) mma_commit(bar_o(i));
+            }
+            __syncwarp();
+            continue;
+          }
           ok = __all_sync(0xffffffffu, p0_now) || wait_all(bar_p(0), np[0] & 1, kErrMma);
           if (!ok) break;
           ++np[0];
@@ -415,14 +445,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_base + C::O_COL + wg * D;
     const float sl2 = p.scale_log2;
     uint8_t* stage = staging + warp * 4096;
+    float4* pair_o = reinterpret_cast<float4*>(smem + 2 * C::TILE);   // PAIR: [128][D / 4], over the K and V tiles
+    float2* pair_ml = reinterpret_cast<float2*>(smem + 4 * C::TILE);  // [128]
+    static_assert(kBM * D * 4 <= 2 * C::TILE && C::STAGES > 2, "the second tile's O");
     int ns = 0, no = 0;
     bool ok = true;
     for (UnitWalk walk(p); ok && walk.more(p); walk.step(p)) {
       const Unit w = walk.unit(p);
-      if (wg >= w.halves) continue;
-      const int row0 = w.q0 + wg * kBM + quarter * 32, row = row0 + lane;
+      if (!PAIR && wg >= w.halves) continue;
+      const int row0 = w.q0 + (PAIR ? 0 : wg * kBM) + quarter * 32, row = row0 + lane;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < w.tiles; ++j) {
+      const int first = PAIR ? wg : 0;
+      for (int j = first; j < w.tiles; j += PAIR ? 2 : 1) {
         ok = wait_all(bar_s(wg), ns & 1, kErrSoftmax);
         if (!ok) break;
         ++ns;
@@ -439,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float top = row_max * sl2;
         float factor = 1.f;
         bool raise = false;
-        if (j == 0) {
+        if (j == first) {
           m = top;
         } else if (top > m + kRescaleThreshold) {
           factor = ex2_approx(m - top);
@@ -466,8 +500,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p(wg));
       }
-      if (!ok) break;
+      if (!PAIR && !ok) break;
       const bool none = w.tiles == 0;
+      if constexpr (PAIR) {
+        // the second tile's O (unnormalised), m and l to shared memory, whose K
+        // and V tiles all products have read
+        for (int i = 0; i <= wg && ok; ++i)
+          if (w.tiles > i) ok = wait_all(bar_o(i), 0, kErrSoftmax);
+        tc_fence_after();
+        if (wg == 1 && ok && w.tiles > 1) {
+          const int r = quarter * 32 + lane;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 64) {
+            uint32_t o[64];
+            tmem_ld_x64(tO + c0, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pair_o[r * (D / 4) + c0 / 4 + (i ^ (r & 7))] =
+                  make_float4(u2f(o[4 * i]), u2f(o[4 * i + 1]), u2f(o[4 * i + 2]), u2f(o[4 * i + 3]));
+          }
+          pair_ml[r] = make_float2(m, l);
+        }
+        // (all 8 warps come here, whether their waits ran out or not: a CTA has one unit)
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (!ok || wg == 1) break;
+      }
+      float own = 1.f, other = 0.f;   // weights of the two sums
+      if (PAIR && w.tiles > 1) {
+        const float2 ml = pair_ml[quarter * 32 + lane];
+        const float top = fmaxf(m, ml.x);
+        own = ex2_approx(m - top);
+        other = ex2_approx(ml.x - top);
+        l = l * own + ml.y * other;
+        m = top;
+      }
       const float inv = none ? 0.f : 1.f / l;
       const float lse = none ? -INFINITY : (m + log2f(l)) * kLn2;
       const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
@@ -478,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + row * p.lse.s[2];
         if (CPATTN_IN(p.splits > 1 ? p.ws_span : p.lse.span, dst, 4, p.err)) *dst = lse;
       }
-      if (!none) {
+      if (!PAIR && !none) {
         ok = wait_all(bar_o(wg), no & 1, kErrSoftmax);
         if (!ok) break;
         ++no;
@@ -493,15 +559,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 64; ++i) o[i] = 0u;
         } else {
           tmem_ld_x64(tO + c0, o);
+          if (PAIR && w.tiles > 1) {
+            const int r = quarter * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float4 x = pair_o[r * (D / 4) + c0 / 4 + (i ^ (r & 7))];
+              o[4 * i] = f2u(u2f(o[4 * i]) * own + x.x * other);
+              o[4 * i + 1] = f2u(u2f(o[4 * i + 1]) * own + x.y * other);
+              o[4 * i + 2] = f2u(u2f(o[4 * i + 2]) * own + x.z * other);
+              o[4 * i + 3] = f2u(u2f(o[4 * i + 3]) * own + x.w * other);
+            }
+          }
         }
         if (p.splits > 1) {
-          if (row < p.s_q && !none) {   // (a part without keys is not read)
-            float4* dst = reinterpret_cast<float4*>(p.ws + at * D + c0);
+          // through the stage, so that lines leave whole (a part without keys is not read)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (CPATTN_IN(p.ws_span, dst + i, 16, p.err))
-                dst[i] = make_float4(u2f(o[4 * i]) * inv, u2f(o[4 * i + 1]) * inv, u2f(o[4 * i + 2]) * inv,
-                                     u2f(o[4 * i + 3]) * inv);
+          for (int half = 0; half < 2 && !none; ++half) {
+            float4* st = reinterpret_cast<float4*>(stage);   // [32 rows][32 columns], chunks swizzled
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t* x = o + half * 32 + 4 * i;
+              st[lane * 8 + (i ^ (lane & 7))] =
+                  make_float4(u2f(x[0]) * inv, u2f(x[1]) * inv, u2f(x[2]) * inv, u2f(x[3]) * inv);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = i * 4 + lane / 8, c = lane % 8;
+              float4* dst = reinterpret_cast<float4*>(p.ws + (at + r - lane) * D + c0 + half * 32) + c;
+              if (row0 + r < p.s_q && CPATTN_IN(p.ws_span, dst, 16, p.err)) *dst = st[r * 8 + (c ^ (r & 7))];
+            }
+            __syncwarp();
           }
           continue;
         }
@@ -521,11 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool PAIR>
 cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                          const CUtensorMap& tm_o, const CrossParams& p, cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kernel = cross_fwd_kernel<D>;
+  auto kernel = cross_fwd_kernel<D, PAIR>;
   // once per device: the register split needs exactly kLaunchRegs at launch
   // (refused otherwise), and the shared-memory limit is raised
   static std::atomic<unsigned long long> ready{0};
@@ -544,7 +632,7 @@ cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
   const int64_t units = static_cast<int64_t>(p.batch) * p.heads * p.splits * ((p.s_q + 2 * kBM - 1) / (2 * kBM));
   const int64_t sms = sm_count();
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_behind(kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)), kThreads, C::SMEM, stream, tm_q,
+  return launch_behind(kernel, dim3(static_cast<unsigned>(PAIR || units < sms ? units : sms)), kThreads, C::SMEM, stream, tm_q,
                        tm_k, tm_v, tm_o, p);
 }
 
@@ -552,8 +640,13 @@ cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
 
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const CUtensorMap& tm_o, const CrossParams& p, cudaStream_t stream) {
-  return head_dim == 64 ? launch_typed<64>(tm_q, tm_k, tm_v, tm_o, p, stream)
-                        : launch_typed<128>(tm_q, tm_k, tm_v, tm_o, p, stream);
+  // one wave of a single query tile each: two sums a tile
+  const int64_t units = static_cast<int64_t>(p.batch) * p.heads * p.splits;
+  if (p.s_q <= kBM && units <= sm_count())
+    return head_dim == 64 ? launch_typed<64, true>(tm_q, tm_k, tm_v, tm_o, p, stream)
+                          : launch_typed<128, true>(tm_q, tm_k, tm_v, tm_o, p, stream);
+  return head_dim == 64 ? launch_typed<64, false>(tm_q, tm_k, tm_v, tm_o, p, stream)
+                        : launch_typed<128, false>(tm_q, tm_k, tm_v, tm_o, p, stream);
 }
 
 }  // namespace cpattn

@@ -94,6 +94,9 @@ MANY = [
     (3, 20, 5, 200, 64, 128, (64, 33, 5)),
     (1, 40, 40, 256, 129, 64, (-3,)),
     (1, 3, 3, 1500, 1030, 64, None),                  # few key tiles: dk, dv in parts
+    (3, 2, 2, 100, 1100, 128, (1100, 130, 0)),        # one query tile, its keys in parts of 1 to 5 tiles
+    (1, 4, 2, 128, 2049, 64, (2049,)),
+    (2, 3, 1, 77, 4481, 128, (4481, 3000)),
 ]
 
 

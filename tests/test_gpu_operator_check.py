@@ -56,6 +56,7 @@ CASES = [
     (2, 8, 2, 1, 5001, 128, (5001, 3000)),
     (1, 24, 24, 1000, 301, 64, None),
     (2, 8, 2, 900, 333, 128, (333, 70)),
+    (2, 2, 2, 100, 2500, 128, (2500, 1030)),
     (1, 3, 3, 1500, 1030, 64, None),
 ]
 

@@ -14,13 +14,13 @@ TIMEOUT = 9
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("queries", [300, 100])
-def test_stalled_producers_time_out_and_recover(d, queries):
+@pytest.mark.parametrize("queries,keys", [(300, 333), (100, 333), (100, 1300)])
+def test_stalled_producers_time_out_and_recover(d, queries, keys):
     lib = cp.load_library()
     g = torch.Generator("cpu").manual_seed(71)
     q, k, v, dout = (torch.randn(2, 3, s, d, generator=g).to(torch.bfloat16).to(DEV)
-                     for s in (queries, 333, 333, queries))
-    lengths = torch.tensor((333, 140), dtype=torch.int32, device=DEV)
+                     for s in (queries, keys, keys, queries))
+    lengths = torch.tensor((keys, 140), dtype=torch.int32, device=DEV)
     out, lse = cp.cross_attention(q, k, v, kv_lengths=lengths)
     grads = cp.cross_attention_backward(q, k, v, out, lse, dout, kv_lengths=lengths)
     assert cp.last_device_status() == 0
@@ -41,6 +41,6 @@ def test_stalled_producers_time_out_and_recover(d, queries):
     for a, b in zip(cp.cross_attention_backward(q, k, v, out, lse, dout, kv_lengths=lengths), grads):
         assert torch.equal(a, b)
     assert cp.last_device_status() == 0
-    want = plain.cross(q, k, v, (333, 140), dout=dout)
+    want = plain.cross(q, k, v, (keys, 140), dout=dout)
     for name, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
         assert plain.worst(got, *want[name]) <= 1.0
