@@ -403,29 +403,36 @@ bool cross_few(const cpattn_tensor* q, const cpattn_tensor* k) {
 // parts 9.0, 128 parts 9.8), above 8 parts whole clusters; two clusters and
 // their join gain on one only past some 8000 keys (8 key heads: 4096 keys 9.0 us
 // with one, 10.9 with two; 8192 14.9 / 15.2; 16384 25.0 / 22.1).  For 256-row
-// units of the tensor-core kernel one per SM, each with four 128-key tiles or
-// more; for fp32's blocks likewise, each with 128 keys or more.
+// units of the tensor-core kernel one per SM, each with 256 keys or more and
+// none below 1024 keys (256 queries x 8 heads, D = 128: 1024 keys 15.1 us with
+// one part, 13.1 with 4, 14.6 with 8; 512 x 512 x 8 heads at D = 64 8.4 with one,
+// 9.6 with 4); for fp32's blocks likewise, each with 128 keys or more.
 int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
   const int64_t bh = q->shape[0] * q->shape[1], sm = cpattn::sm_count();
   if (bh == 0 || q->shape[2] == 0 || k->shape[2] == 0) return 1;
-  int64_t most, want;
+  int64_t most, want, units;
   if (cross_few(q, k)) {
-    const int64_t units = q->shape[0] * k->shape[1];
+    units = q->shape[0] * k->shape[1];
     most = (k->shape[2] + 191) / 192;
     want = 2 * sm / units;
   } else {
-    int64_t units = (q->shape[2] + 255) / 256 * bh;
+    units = (q->shape[2] + 255) / 256 * bh;
     if (q->dtype != CPATTN_BF16) {
       units = (q->shape[2] + 63) / 64 * bh;
       if (!cpattn::cross_f32_rows(units)) units = q->shape[2] > 2 ? (q->shape[2] + 7) / 8 * bh : bh;
     }
-    most = q->dtype == CPATTN_BF16 ? (k->shape[2] + 511) / 512 : (k->shape[2] + 127) / 128;
+    most = q->dtype != CPATTN_BF16 ? (k->shape[2] + 127) / 128 : k->shape[2] < 1024 ? 1 : (k->shape[2] + 255) / 256;
     want = sm / units;
   }
   int64_t s = want < most ? want : most;
-  if (cross_few(q, k) && s > cpattn::kCrossCluster) {
+  if (q->dtype == CPATTN_BF16 && s > cpattn::kCrossCluster) {
     s -= s % cpattn::kCrossCluster;
     if (s < 3 * cpattn::kCrossCluster && k->shape[2] <= 8192) s = cpattn::kCrossCluster;
+  }
+  // clusters of one block an SM leave some SMs of a processing cluster free
+  if (q->dtype == CPATTN_BF16 && !cross_few(q, k)) {
+    static const int room[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};   // SMs of 152 that clusters of s can take
+    while (s > 1 && units * s * 152 > sm * room[s < 8 ? s : 8]) s -= s > 8 ? 8 : 1;
   }
   return s > 1 ? static_cast<int>(s < 65535 ? s : 65535) : 1;
 }
@@ -433,7 +440,7 @@ int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
 size_t cross_workspace(const cpattn_tensor* q, const cpattn_tensor* k) {
   const int64_t rows = q->shape[0] * q->shape[1] * q->shape[2];
   const int splits = cross_splits(q, k);
-  const int parts = cross_few(q, k) ? splits / cpattn::kCrossCluster : splits;
+  const int parts = q->dtype == CPATTN_BF16 ? splits / cpattn::kCrossCluster : splits;
   return parts > 1 && rows > 0 ? static_cast<size_t>(parts) * rows * (q->shape[3] + 1) * 4 : 0;
 }
 
@@ -783,8 +790,6 @@ cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor
   bool join = p.splits != 1;   // (no parts: the join writes the empty result)
   if (p.splits > 0 && cross_few(q, k)) {
     e = cpattn::launch_cross_few(D, p, cs);
-    p.splits /= cpattn::kCrossCluster;   // (parts in the workspace)
-    join = p.splits > 1;
   } else if (p.splits > 0 && dt == InDtype::BF16) {
     CUtensorMap tm_q, tm_k, tm_v, tm_o;
     if ((st = make_tmap(&tm_q, q, 128)) != CPATTN_OK) return st;
@@ -794,6 +799,10 @@ cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor
     e = cpattn::launch_cross_fwd(D, tm_q, tm_k, tm_v, tm_o, p, cs);
   } else if (p.splits > 0) {
     e = cpattn::launch_cross_simt(D, p, cs);
+  }
+  if (dt == InDtype::BF16 && p.splits > 0) {   // (a cluster has joined its parts)
+    p.splits /= cpattn::kCrossCluster;
+    join = p.splits > 1;
   }
   if (e == cudaSuccess && join) e = cpattn::launch_cross_join(dt, D, p, cs);
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;

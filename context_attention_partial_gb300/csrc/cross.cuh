@@ -68,15 +68,16 @@ cudaError_t cross_run(int64_t blocks, int splits, int threads, size_t smem, cuda
   return launch_behind(kernel, dim3(static_cast<unsigned>(blocks), splits), threads, smem, stream, args...);
 }
 
+// Blocks of a cluster, at most.  bf16 forward calls have p.splits up to it, or a
+// multiple of it: a cluster joins its parts itself, and the workspace gets
+// p.splits / kCrossCluster parts to join.
+constexpr int kCrossCluster = 8;
 // bf16 inputs, D 64 or 128, on the tensor cores (s_kv >= 1; the maps' boxes
 // have 128 rows, the output's 32).
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                              const CUtensorMap& tm_v, const CUtensorMap& tm_o, const CrossParams& p,
                              cudaStream_t stream);
-// the same for at most 64 query rows a key head (s_q * H / H_kv); p.splits up
-// to kCrossCluster, or a multiple of it: then the workspace gets
-// p.splits / kCrossCluster parts to join
-constexpr int kCrossCluster = 8;
+// the same for at most 64 query rows a key head (s_q * H / H_kv)
 cudaError_t launch_cross_few(int head_dim, const CrossParams& p, cudaStream_t stream);
 // its gradient (s_q, s_kv >= 1; the kernels write delta to the workspace's start
 // and, when p.splits > 1, partial sums of dk and dv `partials` floats into it;

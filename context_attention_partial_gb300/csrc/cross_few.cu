@@ -325,7 +325,7 @@ cudaError_t launch_tiles(const CrossParams& p, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(p.batch) * p.kv_heads;
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_behind_clustered(kernel, dim3(static_cast<unsigned>(units), p.splits),
-                                 p.splits < kCrossCluster ? p.splits : kCrossCluster, kThreads, C::SMEM, stream, p);
+                                 dim3(1, p.splits < kCrossCluster ? p.splits : kCrossCluster), kThreads, C::SMEM, stream, p);
 }
 
 template <int D>

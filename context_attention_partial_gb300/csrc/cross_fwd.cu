@@ -24,8 +24,11 @@
 // Keys past a length share their tile with valid ones: their scores are
 // masked in registers, and their V rows are overwritten with zeros in shared
 // memory before P V reads them (0 * NaN would not be 0).
-// A unit may also be one part of the key axis (few queries): its normalised
-// fp32 output and lse go to the workspace and are joined by a second kernel.
+// A unit may also be one part of the key axis (few queries): up to 8 parts are a
+// cluster and join their fp32 rows in its shared memory (by way of the workspace
+// and a second kernel this took 6 of 18 us at 77 queries x 4481 keys x 32 heads,
+// 4 parts); the results of several clusters go to the workspace and are joined
+// by that kernel.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -44,7 +47,7 @@ constexpr int kSoftmaxRegs = 208, kControlRegs = 88;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
-constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.442695040888963407f;
 constexpr unsigned kErrProducer = 1u, kErrMma = 2u, kErrSoftmax = 4u;
 
 template <int D>
@@ -69,18 +72,18 @@ struct Unit {
   int tiles, halves;       // key tiles, query tiles with rows
 };
 
-// Walks this CTA's units, blockIdx.x, blockIdx.x + gridDim.x, ..., query block
-// fastest, then part, head and batch.  A step adds the grid's size digit by
+// Walks this CTA's units, blockIdx.x, blockIdx.x + gridDim.x, ..., part fastest
+// (a cluster has one unit's), then query block, head and batch.  A step adds the grid's size digit by
 // digit: divisions at every unit cost some 700 cycles between two units.
 struct UnitWalk {
   int q, part, h, b;       // digits of the unit
   int dq, dp, dh, db;      // digits of the grid's size
   int q_blocks;
   __device__ void split(const CrossParams& p, uint32_t u, int& q_, int& p_, int& h_, int& b_) const {
-    uint32_t r = u / q_blocks;
-    q_ = static_cast<int>(u - r * q_blocks);
-    u = r / p.splits;
-    p_ = static_cast<int>(r - u * p.splits);
+    uint32_t r = u / p.splits;
+    p_ = static_cast<int>(u - r * p.splits);
+    u = r / q_blocks;
+    q_ = static_cast<int>(r - u * q_blocks);
     b_ = static_cast<int>(u / p.heads);
     h_ = static_cast<int>(u - b_ * p.heads);
   }
@@ -96,12 +99,12 @@ struct UnitWalk {
     part += dp;
     h += dh;
     b += db;
-    if (q >= q_blocks) {
-      q -= q_blocks;
-      ++part;
-    }
     if (part >= p.splits) {
       part -= p.splits;
+      ++q;
+    }
+    if (q >= q_blocks) {
+      q -= q_blocks;
       ++h;
     }
     if (h >= p.heads) {
@@ -138,6 +141,93 @@ struct UnitWalk {
     return false;
   }
 };
+
+// Joins the rows of a cluster's parts (256 threads of every block; the block's
+// other threads meet the two cluster barriers): every block takes some of the
+// rows, four 16-byte chunks a thread at a time.  Results of several clusters go
+// to the workspace.  `weights`: [9][256] floats of this block's own.
+template <int D>
+__device__ __forceinline__ void join_cluster(const CrossParams& p, const float4* part_o, const float* part_lse,
+                                             float* weights) {
+  const int parts = min(p.splits, kCrossCluster);
+  const Unit w = UnitWalk(p).unit(p);
+  const int rank = w.part % parts, cluster = w.part / parts, rows = min(p.s_q - w.q0, 2 * kBM);
+  cluster_sync();
+  // a row's weights, and the lse of its whole, where one of this block's threads
+  // below takes the row
+  const int t = threadIdx.x;
+  if (t < rows && t * (D / 4) / 256 % parts == rank) {
+    float lse[kCrossCluster], top = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int x = 0; x < kCrossCluster; ++x) {
+      lse[x] = x < parts ? cluster_load(cluster_addr(smem_addr(part_lse + t), x)) : -INFINITY;
+      top = fmaxf(top, lse[x]);
+    }
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int x = 0; x < kCrossCluster; ++x) {
+      lse[x] = ex2_approx((lse[x] - base) * kLog2e);
+      total += lse[x];
+    }
+    const bool none = total == 0.f;
+    const float inv = none ? 0.f : 1.f / total;
+#pragma unroll
+    for (int x = 0; x < kCrossCluster; ++x)
+      if (x < parts) weights[x * 256 + t] = lse[x] * inv;
+    weights[8 * 256 + t] = none ? -INFINITY : base + log2f(total) * kLn2;
+  }
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+  const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
+  constexpr int U = 4;
+  const int items = rows * (D / 4), step = parts * 256;
+  for (int i0 = rank * 256 + t; i0 < items; i0 += U * step) {
+    float4 sum[U];
+    int at[U], r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = min(i0 + u * step, items - 1);
+      r[u] = i / (D / 4);
+      at[u] = r[u] * (D / 4) + (i % (D / 4) ^ (r[u] & 7));
+      sum[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 4
+    for (int x = 0; x < parts; ++x) {
+      float4 y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * step < items) y[u] = cluster_load4(cluster_addr(smem_addr(part_o + at[u]), x));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float f = weights[x * 256 + r[u]];
+        if (f != 0.f && i0 + u * step < items)   // (a part without keys has written no row)
+          sum[u] = make_float4(fmaf(f, y[u].x, sum[u].x), fmaf(f, y[u].y, sum[u].y), fmaf(f, y[u].z, sum[u].z),
+                               fmaf(f, y[u].w, sum[u].w));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * step >= items) break;
+      const int c = (i0 + u * step) % (D / 4);
+      const int64_t row = w.q0 + r[u];
+      if (p.splits > parts) {
+        const int64_t place = cluster * n + (static_cast<int64_t>(w.b) * p.heads + w.h) * p.s_q + row;
+        float4* dst = reinterpret_cast<float4*>(p.ws + place * D) + c;
+        float* dl = p.ws + p.splits / parts * n * D + place;
+        if (CPATTN_IN(p.ws_span, dst, 16, p.err)) *dst = sum[u];
+        if (c == 0 && CPATTN_IN(p.ws_span, dl, 4, p.err)) *dl = weights[8 * 256 + r[u]];
+      } else {
+        __nv_bfloat16* dst =
+            static_cast<__nv_bfloat16*>(p.out.data) + w.b * p.out.s[0] + w.h * p.out.s[1] + row * p.out.s[2] + c * 4;
+        float* dl = static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + row * p.lse.s[2];
+        if (CPATTN_IN(p.out.span, dst, 8, p.err))
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(pack_bf16x2(sum[u].x, sum[u].y), pack_bf16x2(sum[u].z, sum[u].w));
+        if (c == 0 && CPATTN_IN(p.lse.span, dl, 4, p.err)) *dl = weights[8 * 256 + r[u]];
+      }
+    }
+  }
+  cluster_sync();   // (shared memory stays until every block has read it)
+}
 
 // PAIR: the two query tiles are the same one (S_q <= 128), its key tiles
 // alternate between them, each with sums of its own, and the warps of the first
@@ -445,9 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_base + C::O_COL + wg * D;
     const float sl2 = p.scale_log2;
     uint8_t* stage = staging + warp * 4096;
-    float4* pair_o = reinterpret_cast<float4*>(smem + 2 * C::TILE);   // PAIR: [128][D / 4], over the K and V tiles
-    float2* pair_ml = reinterpret_cast<float2*>(smem + 4 * C::TILE);  // [128]
-    static_assert(kBM * D * 4 <= 2 * C::TILE && C::STAGES > 2, "the second tile's O");
+    // rows of a split, and before that PAIR's second O, over the K and V tiles;
+    // their lse over the Q tiles
+    float4* part_o = reinterpret_cast<float4*>(smem + 2 * C::TILE);   // [256][D / 4], chunks swizzled
+    float* part_lse = reinterpret_cast<float*>(smem);                 // [256]
+    float2* pair_ml = reinterpret_cast<float2*>(smem + C::TILE);      // [128]
+    static_assert(2 * kBM * D * 4 <= C::STAGES * C::TILE && 4096 + 9 * 1024 <= 2 * C::TILE, "a split's rows");
     int ns = 0, no = 0;
     bool ok = true;
     for (UnitWalk walk(p); ok && walk.more(p); walk.step(p)) {
@@ -516,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_x64(tO + c0, o);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              pair_o[r * (D / 4) + c0 / 4 + (i ^ (r & 7))] =
+              part_o[r * (D / 4) + c0 / 4 + (i ^ (r & 7))] =
                   make_float4(u2f(o[4 * i]), u2f(o[4 * i + 1]), u2f(o[4 * i + 2]), u2f(o[4 * i + 3]));
           }
           pair_ml[r] = make_float2(m, l);
@@ -536,19 +629,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float inv = none ? 0.f : 1.f / l;
       const float lse = none ? -INFINITY : (m + log2f(l)) * kLn2;
-      const int64_t n = static_cast<int64_t>(p.batch) * p.heads * p.s_q;
-      const int64_t at = w.part * n + (static_cast<int64_t>(w.b) * p.heads + w.h) * p.s_q + row;
-      if (row < p.s_q) {
-        float* dst = p.splits > 1
-                         ? p.ws + p.splits * n * D + at
-                         : static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + row * p.lse.s[2];
-        if (CPATTN_IN(p.splits > 1 ? p.ws_span : p.lse.span, dst, 4, p.err)) *dst = lse;
-      }
       if (!PAIR && !none) {
         ok = wait_all(bar_o(wg), no & 1, kErrSoftmax);
+        // (a split's rows go where the other tile's products read K and V)
+        if (ok && p.splits > 1 && w.halves == 2) ok = wait_all(bar_o(wg ^ 1), 0, kErrSoftmax);
         if (!ok) break;
         ++no;
         tc_fence_after();
+      }
+      if (p.splits > 1) {
+        if (row < p.s_q) part_lse[(PAIR ? 0 : wg * kBM) + quarter * 32 + lane] = lse;
+      } else if (row < p.s_q) {
+        float* dst = static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + row * p.lse.s[2];
+        if (CPATTN_IN(p.lse.span, dst, 4, p.err)) *dst = lse;
       }
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 64) {
@@ -563,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = quarter * 32 + lane;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float4 x = pair_o[r * (D / 4) + c0 / 4 + (i ^ (r & 7))];
+              const float4 x = part_o[r * (D / 4) + c0 / 4 + (i ^ (r & 7))];
               o[4 * i] = f2u(u2f(o[4 * i]) * own + x.x * other);
               o[4 * i + 1] = f2u(u2f(o[4 * i + 1]) * own + x.y * other);
               o[4 * i + 2] = f2u(u2f(o[4 * i + 2]) * own + x.z * other);
@@ -572,25 +665,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (p.splits > 1) {
-          // through the stage, so that lines leave whole (a part without keys is not read)
+          const int r = (PAIR ? 0 : wg * kBM) + quarter * 32 + lane;
 #pragma unroll
-          for (int half = 0; half < 2 && !none; ++half) {
-            float4* st = reinterpret_cast<float4*>(stage);   // [32 rows][32 columns], chunks swizzled
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t* x = o + half * 32 + 4 * i;
-              st[lane * 8 + (i ^ (lane & 7))] =
-                  make_float4(u2f(x[0]) * inv, u2f(x[1]) * inv, u2f(x[2]) * inv, u2f(x[3]) * inv);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = i * 4 + lane / 8, c = lane % 8;
-              float4* dst = reinterpret_cast<float4*>(p.ws + (at + r - lane) * D + c0 + half * 32) + c;
-              if (row0 + r < p.s_q && CPATTN_IN(p.ws_span, dst, 16, p.err)) *dst = st[r * 8 + (c ^ (r & 7))];
-            }
-            __syncwarp();
-          }
+          for (int i = 0; i < 16; ++i)
+            part_o[r * (D / 4) + c0 / 4 + (i ^ (r & 7))] = make_float4(
+                u2f(o[4 * i]) * inv, u2f(o[4 * i + 1]) * inv, u2f(o[4 * i + 2]) * inv, u2f(o[4 * i + 3]) * inv);
           continue;
         }
         // (the previous store has read the stage)
@@ -599,6 +678,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         store_rows<64>(p, p.out, &tm_o, stage, o, inv, w.b, w.h, row0, p.s_q, c0);
       }
     }
+    if (p.splits > 1) join_cluster<D>(p, part_o, part_lse, reinterpret_cast<float*>(smem + 4096));
+  }
+  if (p.splits > 1 && warp >= 8) {   // (as join_cluster)
+    cluster_sync();
+    cluster_sync();
   }
   if (lane == 0) bulk_wait_read();   // (no store reads this CTA's shared memory any more)
   tc_fence_before();
@@ -632,8 +716,9 @@ cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
   const int64_t units = static_cast<int64_t>(p.batch) * p.heads * p.splits * ((p.s_q + 2 * kBM - 1) / (2 * kBM));
   const int64_t sms = sm_count();
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_behind(kernel, dim3(static_cast<unsigned>(PAIR || units < sms ? units : sms)), kThreads, C::SMEM, stream, tm_q,
-                       tm_k, tm_v, tm_o, p);
+  const dim3 grid(static_cast<unsigned>(PAIR || p.splits > 1 || units < sms ? units : sms));
+  const unsigned cluster = p.splits < kCrossCluster ? p.splits : kCrossCluster;
+  return launch_behind_clustered(kernel, grid, dim3(cluster), kThreads, C::SMEM, stream, tm_q, tm_k, tm_v, tm_o, p);
 }
 
 }  // namespace

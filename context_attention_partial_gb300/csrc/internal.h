@@ -116,9 +116,8 @@ cudaError_t launch_rotary(InDtype dt, const RotaryParams& p, cudaStream_t stream
 // completes before that kernel -- and launch_next() after that, so a kernel
 // behind it only starts once everything before it has completed.  (Hides the
 // launch and the start of the blocks, 2 to 4 us a kernel.)
-// cluster_y: blocks of a cluster along y.
 template <typename... Params, typename... Args>
-cudaError_t launch_behind_clustered(void (*kernel)(Params...), dim3 grid, unsigned cluster_y, unsigned threads,
+cudaError_t launch_behind_clustered(void (*kernel)(Params...), dim3 grid, dim3 cluster, unsigned threads,
                                     size_t smem, cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t config = {};
   config.gridDim = grid;
@@ -129,16 +128,17 @@ cudaError_t launch_behind_clustered(void (*kernel)(Params...), dim3 grid, unsign
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = attr[1].val.clusterDim.z = 1;
-  attr[1].val.clusterDim.y = cluster_y;
+  attr[1].val.clusterDim.x = cluster.x;
+  attr[1].val.clusterDim.y = cluster.y;
+  attr[1].val.clusterDim.z = cluster.z;
   config.attrs = attr;
-  config.numAttrs = cluster_y > 1 ? 2 : 1;
+  config.numAttrs = cluster.x * cluster.y * cluster.z > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&config, kernel, args...);
 }
 template <typename... Params, typename... Args>
 cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                           const Args&... args) {
-  return launch_behind_clustered(kernel, grid, 1, threads, smem, stream, args...);
+  return launch_behind_clustered(kernel, grid, dim3(1), threads, smem, stream, args...);
 }
 #ifdef __CUDACC__
 // Waits until the kernel before this one has completed (nothing to wait for
