@@ -75,13 +75,15 @@ struct Unit {
 // Walks this CTA's units, blockIdx.x, blockIdx.x + gridDim.x, ..., part fastest
 // (a cluster has one unit's), then query block, head and batch.  A step adds the grid's size digit by
 // digit: divisions at every unit cost some 700 cycles between two units.
+template <bool SPLIT>   // false: one part
 struct UnitWalk {
   int q, part, h, b;       // digits of the unit
   int dq, dp, dh, db;      // digits of the grid's size
   int q_blocks;
   __device__ void split(const CrossParams& p, uint32_t u, int& q_, int& p_, int& h_, int& b_) const {
-    uint32_t r = u / p.splits;
-    p_ = static_cast<int>(u - r * p.splits);
+    const uint32_t splits = SPLIT ? p.splits : 1;
+    uint32_t r = u / splits;
+    p_ = static_cast<int>(u - r * splits);
     u = r / q_blocks;
     q_ = static_cast<int>(r - u * q_blocks);
     b_ = static_cast<int>(u / p.heads);
@@ -96,10 +98,10 @@ struct UnitWalk {
   __device__ bool more(const CrossParams& p) const { return b < p.batch; }
   __device__ void step(const CrossParams& p) {
     q += dq;
-    part += dp;
+    if (SPLIT) part += dp;
     h += dh;
     b += db;
-    if (part >= p.splits) {
+    if (SPLIT && part >= p.splits) {
       part -= p.splits;
       ++q;
     }
@@ -121,7 +123,7 @@ struct UnitWalk {
     const int len = uniform(cross_length(p, b));
     const int all = ceil_div(len, kBN);
     int t0 = 0, t1 = all;
-    if (p.splits > 1) {
+    if (SPLIT) {
       const int per = uniform(ceil_div(all, p.splits));
       t0 = min(part * per, all);
       t1 = min(t0 + per, all);
@@ -150,7 +152,7 @@ template <int D>
 __device__ __forceinline__ void join_cluster(const CrossParams& p, const float4* part_o, const float* part_lse,
                                              float* weights) {
   const int parts = min(p.splits, kCrossCluster);
-  const Unit w = UnitWalk(p).unit(p);
+  const Unit w = UnitWalk<true>(p).unit(p);
   const int rank = w.part % parts, cluster = w.part / parts, rows = min(p.s_q - w.q0, 2 * kBM);
   cluster_sync();
   // a row's weights, and the lse of its whole, where one of this block's threads
@@ -234,12 +236,14 @@ __device__ __forceinline__ void join_cluster(const CrossParams& p, const float4*
 // take the second's over at the end; a CTA has one unit.  A lone tile's products
 // and exponentials wait for one another (some 2600 cycles a key tile); two
 // chains fill each other's waits.
-template <int D, bool PAIR>
+// SPLIT: parts of the key axis (one, with PAIR, where the units fill the GPU).
+template <int D, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                      const __grid_constant__ CrossParams p) {
   using C = Cfg<D>;
+  const bool split = SPLIT && p.splits > 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t sQ = smem_addr(smem), sKV = sQ + 2 * C::TILE;
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       static_assert(C::STAGES % 2 == 0, "K / V pairs");
       const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
       int ld = 0, nq[2] = {0, 0};
-      UnitWalk walk(p);
+      UnitWalk<SPLIT> walk(p);
       Unit w;
       const int share = p.heads / p.kv_heads;
       bool have = walk.with_keys(p, w);
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;                // key tiles so far, over all units
       uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
       bool ok = true;
-      UnitWalk walk(p);
+      UnitWalk<SPLIT> walk(p);
       Unit w;
       bool have = walk.with_keys(p, w);
       // a unit's first scores, query tile by query tile (its K tile is here)
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(2 * kBM * D * 4 <= C::STAGES * C::TILE && 4096 + 9 * 1024 <= 2 * C::TILE, "a split's rows");
     int ns = 0, no = 0;
     bool ok = true;
-    for (UnitWalk walk(p); ok && walk.more(p); walk.step(p)) {
+    for (UnitWalk<SPLIT> walk(p); ok && walk.more(p); walk.step(p)) {
       const Unit w = walk.unit(p);
       if (!PAIR && wg >= w.halves) continue;
       const int row0 = w.q0 + (PAIR ? 0 : wg * kBM) + quarter * 32, row = row0 + lane;
@@ -632,12 +636,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!PAIR && !none) {
         ok = wait_all(bar_o(wg), no & 1, kErrSoftmax);
         // (a split's rows go where the other tile's products read K and V)
-        if (ok && p.splits > 1 && w.halves == 2) ok = wait_all(bar_o(wg ^ 1), 0, kErrSoftmax);
+        if (ok && split && w.halves == 2) ok = wait_all(bar_o(wg ^ 1), 0, kErrSoftmax);
         if (!ok) break;
         ++no;
         tc_fence_after();
       }
-      if (p.splits > 1) {
+      if (split) {
         if (row < p.s_q) part_lse[(PAIR ? 0 : wg * kBM) + quarter * 32 + lane] = lse;
       } else if (row < p.s_q) {
         float* dst = static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + w.h * p.lse.s[1] + row * p.lse.s[2];
@@ -664,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (p.splits > 1) {
+        if (split) {
           const int r = (PAIR ? 0 : wg * kBM) + quarter * 32 + lane;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -678,9 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         store_rows<64>(p, p.out, &tm_o, stage, o, inv, w.b, w.h, row0, p.s_q, c0);
       }
     }
-    if (p.splits > 1) join_cluster<D>(p, part_o, part_lse, reinterpret_cast<float*>(smem + 4096));
+    if (split) join_cluster<D>(p, part_o, part_lse, reinterpret_cast<float*>(smem + 4096));
   }
-  if (p.splits > 1 && warp >= 8) {   // (as join_cluster)
+  if (split && warp >= 8) {   // (as join_cluster)
     cluster_sync();
     cluster_sync();
   }
@@ -693,11 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool SPLIT>
 cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                          const CUtensorMap& tm_o, const CrossParams& p, cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kernel = cross_fwd_kernel<D, PAIR>;
+  auto kernel = cross_fwd_kernel<D, PAIR, SPLIT>;
   // once per device: the register split needs exactly kLaunchRegs at launch
   // (refused otherwise), and the shared-memory limit is raised
   static std::atomic<unsigned long long> ready{0};
@@ -728,10 +732,14 @@ cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtens
   // one wave of a single query tile each: two sums a tile
   const int64_t units = static_cast<int64_t>(p.batch) * p.heads * p.splits;
   if (p.s_q <= kBM && units <= sm_count())
-    return head_dim == 64 ? launch_typed<64, true>(tm_q, tm_k, tm_v, tm_o, p, stream)
-                          : launch_typed<128, true>(tm_q, tm_k, tm_v, tm_o, p, stream);
-  return head_dim == 64 ? launch_typed<64, false>(tm_q, tm_k, tm_v, tm_o, p, stream)
-                        : launch_typed<128, false>(tm_q, tm_k, tm_v, tm_o, p, stream);
+    return head_dim == 64 ? launch_typed<64, true, true>(tm_q, tm_k, tm_v, tm_o, p, stream)
+                          : launch_typed<128, true, true>(tm_q, tm_k, tm_v, tm_o, p, stream);
+  // (the code of splits costs calls without 3 %: 4608 x 512 x 24 heads 27.0 us, not 26.3)
+  if (p.splits > 1)
+    return head_dim == 64 ? launch_typed<64, false, true>(tm_q, tm_k, tm_v, tm_o, p, stream)
+                          : launch_typed<128, false, true>(tm_q, tm_k, tm_v, tm_o, p, stream);
+  return head_dim == 64 ? launch_typed<64, false, false>(tm_q, tm_k, tm_v, tm_o, p, stream)
+                        : launch_typed<128, false, false>(tm_q, tm_k, tm_v, tm_o, p, stream);
 }
 
 }  // namespace cpattn
