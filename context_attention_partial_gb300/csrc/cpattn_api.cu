@@ -429,11 +429,13 @@ int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
     s -= s % cpattn::kCrossCluster;
     if (s < 3 * cpattn::kCrossCluster && k->shape[2] <= 8192) s = cpattn::kCrossCluster;
   }
-  // clusters of one block an SM leave some SMs of a processing cluster free
-  if (q->dtype == CPATTN_BF16 && !cross_few(q, k)) {
-    static const int room[9] = {0, 152, 152, 138, 144, 140, 138, 105, 120};   // SMs of 152 that clusters of s can take
-    while (s > 1 && units * s * 152 > sm * room[s < 8 ? s : 8]) s -= s > 8 ? 8 : 1;
-  }
+  // what is left of an SM group (GPC) stays free: blocks that clusters of s of
+  // them find room for at once, one block an SM and two, of 152 and 304; a second
+  // round of clusters costs up to half (40 key heads x 8192 keys: 6 parts 28.7
+  // us, 7 parts 41.1)
+  static const int room[2][9] = {{0, 152, 152, 138, 144, 140, 138, 105, 120}, {0, 304, 304, 291, 296, 290, 276, 266, 288}};
+  if (q->dtype == CPATTN_BF16)
+    while (s > 1 && units * s * 152 > sm * room[cross_few(q, k)][s < 8 ? s : 8]) s -= s > 8 ? 8 : 1;
   return s > 1 ? static_cast<int>(s < 65535 ? s : 65535) : 1;
 }
 
