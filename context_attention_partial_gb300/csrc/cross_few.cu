@@ -20,9 +20,12 @@
 //
 // Against the tensor-core kernel, which reads a key head once per query head
 // (head size 128; us, this kernel / that one): 8 sequences x 8 key heads x 4096
-// keys, 4 query heads each: 4 queries 29 / 81, 8 queries 31 / 81; 4 x 16 heads
-// x 4096 keys, not shared: 16 queries 29 / 30, 32 queries 32 / 31; 64 queries
-// x 4608 keys x 24 heads 28 / 21; 16 queries x 4 query heads x 1024 keys 16 / 14.
+// keys, 4 query heads each, 8 queries 28 / 81; 4 x 16 heads x 4096 keys, not
+// shared, 48 queries 40 / 29; 24 heads x 4608 keys: 32 queries 18.7 / 17.6, 64
+// queries 27 / 18; 4 key heads x 1024 keys, 4 query heads each: 8 queries 8.1 /
+// 8.9, 16 queries 10.4 / 9.0; 8 heads x 2000 keys at D = 64, 32 queries 7.0 / 9.3;
+// 2 x 2 key heads x 2500 keys, 8 query heads each, 7 queries 12.4 / 12.9.
+// One query of 32 heads on 8, 8 sequences of up to 16384 keys: 302 MB in 56 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

