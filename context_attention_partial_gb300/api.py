@@ -441,8 +441,8 @@ def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float =
     positions: f32 [S,A] or [B,S,A]; axes_dims: the features of each axis (even, sum
     at most D, the rest is copied).  interleaved: pairs (2i, 2i+1) of an
     axis' features, else (i, i + d/2).  inverse: turns back, which is also
-    the gradient.  outs may be xs (in place).  Returns a tensor for a tensor,
-    else a list."""
+    the gradient (no autograd graph is recorded).  outs may be xs (in place).
+    Returns a tensor for a tensor, else a list."""
     lib = _lib.load()
     if isinstance(xs, torch.Tensor):
         return rotary([xs], positions, axes_dims, theta, interleaved, inverse, None if outs is None else [outs],
@@ -472,7 +472,8 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                     stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention of q [B,H,S_q,D] to an encoder's states k, v [B,H_kv,S_kv,D]
     (cpattn_cross_attention): H_kv divides H; kv_lengths (int32 [B]) gives each
-    sequence's valid keys, a sequence without any gives (0, -inf).
+    sequence's valid keys, a sequence without any gives (0, -inf).  No autograd
+    graph is recorded: ``cross_attention_backward`` is its gradient.
     Returns (out [B,H,S_q,D] in q's dtype, lse f32 [B,H,S_q])."""
     at = _lib.load().addresses
     status, o, l, ws = _lib.binding().cross(at["cross_attention"], at["cross_workspace_bytes"], q, k, v, kv_lengths,
