@@ -96,13 +96,27 @@ __global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_consta
   using C = Few<D>;
   constexpr int KG = 4 / MT, KW = kKeys / KG;    // key groups, keys of a warp and stage
   extern __shared__ __align__(1024) uint8_t smem[];
-  launch_wait();
-  launch_next();
   const uint32_t s0 = smem_addr(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int mt = warp % MT, kg = warp / MT;
   const int share = p.heads / p.kv_heads, rows = p.s_q * share;
   const int hk = blockIdx.x % p.kv_heads, b = blockIdx.x / p.kv_heads;
+  {
+    // the first stages, while the kernel before this one ends (where every key is
+    // valid: lengths are not known yet); 36 key heads x 8192 keys, one query, 27.8
+    // us without, 26.4 with
+    const int first = min(static_cast<int>(blockIdx.y) * ceil_div(ceil_div(p.s_kv, kKeys), p.splits) * kKeys, p.s_kv);
+    constexpr int LINES = C::ROW / 128;
+    const int rows = p.lengths == nullptr ? min(p.s_kv - first, (C::STAGES - 1) * kKeys) : 0;
+    for (int i = threadIdx.x; i < rows * LINES; i += kThreads) {
+      const int64_t key = first + i / LINES;
+      const int col = i % LINES * 64;
+      prefetch_l2(static_cast<const __nv_bfloat16*>(p.k.data) + b * p.k.s[0] + hk * p.k.s[1] + key * p.k.s[2] + col);
+      prefetch_l2(static_cast<const __nv_bfloat16*>(p.v.data) + b * p.v.s[0] + hk * p.v.s[1] + key * p.v.s[2] + col);
+    }
+  }
+  launch_wait();
+  launch_next();
   const int len = cross_length(p, b);
   const int all = ceil_div(len, kKeys), per = ceil_div(all, p.splits);
   const int t0 = min(static_cast<int>(blockIdx.y) * per, all), tiles = min(per, all - t0);

@@ -144,6 +144,9 @@ cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, unsigned threads
 // Waits until the kernel before this one has completed (nothing to wait for
 // when it was launched the ordinary way).
 __device__ __forceinline__ void launch_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Asks for a line in L2, also before launch_wait(): no value is read, and what an
+// earlier kernel still writes there it writes in L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // Lets the kernel behind this one start (once every block has called it).
 __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 #endif
