@@ -424,15 +424,6 @@ def _handle(stream: Optional[torch.cuda.Stream], t: torch.Tensor) -> Optional[in
     return stream.cuda_stream
 
 
-def _hand_over(stream: Optional[torch.cuda.Stream], made) -> None:
-    """Memory this call took from the allocator, used on another stream than
-    the one it was taken for, is not given out again before that stream is done."""
-    if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-
-
 def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float = 10000.0,
            interleaved: bool = True, inverse: bool = False, outs=None,
            stream: Optional[torch.cuda.Stream] = None) -> Union[torch.Tensor, list]:
@@ -450,8 +441,6 @@ def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float =
     status, results = _lib.binding().rotary(lib.addresses["rotary"], xs, positions, axes_dims, theta,
                                             interleaved, inverse, outs, _handle(stream, positions))
     check(status, "cpattn_rotary")
-    if outs is None:
-        _hand_over(stream, results)
     return results
 
 
@@ -476,11 +465,9 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     graph is recorded: ``cross_attention_backward`` is its gradient.
     Returns (out [B,H,S_q,D] in q's dtype, lse f32 [B,H,S_q])."""
     at = _lib.load().addresses
-    status, o, l, ws = _lib.binding().cross(at["cross_attention"], at["cross_workspace_bytes"], q, k, v, kv_lengths,
+    status, o, l = _lib.binding().cross(at["cross_attention"], at["cross_workspace_bytes"], q, k, v, kv_lengths,
                                             _scale(scale), out, lse, workspace, _handle(stream, q))
     check(status, "cpattn_cross_attention")
-    _hand_over(stream, [None if out is not None else o, None if lse is not None else l,
-                        None if workspace is not None else ws])
     return o, l
 
 
@@ -497,12 +484,10 @@ def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     the shapes and dtype of q, k, v; rows of dk and dv past a sequence's
     length are 0."""
     at = _lib.load().addresses
-    status, *grads, ws = _lib.binding().cross_backward(
+    status, *grads = _lib.binding().cross_backward(
         at["cross_attention_backward"], at["cross_backward_workspace_bytes"], q, k, v, out, lse, dout, kv_lengths,
         _scale(scale), dq, dk, dv, workspace, _handle(stream, q))
     check(status, "cpattn_cross_attention_backward")
-    _hand_over(stream, [None if given is not None else t
-                        for given, t in zip((dq, dk, dv, workspace), (*grads, ws))])
     return tuple(grads)
 
 

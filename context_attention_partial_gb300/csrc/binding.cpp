@@ -14,8 +14,11 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+
+#include <optional>
 
 #include "../../include/cpattn.h"
 
@@ -27,6 +30,32 @@ using at::Tensor;
 struct Call {
   int device = -1;
   bool ok = true;   // false: a Python error is set
+  // while the call allocates and launches: its device, and its stream where that
+  // is not the device's current one (then `caller`)
+  std::optional<c10::cuda::CUDAGuard> device_guard;
+  std::optional<c10::cuda::CUDAStreamGuard> stream_guard;
+  std::optional<c10::cuda::CUDAStream> caller;
+  void* stream = nullptr;
+
+  // Makes the given stream (None: the device's current one) the current one, so
+  // that what the call allocates is that stream's memory: a block that the caller's
+  // stream has freed may still be read there by work not yet done.
+  void enter(PyObject* given) {
+    const auto index = static_cast<c10::DeviceIndex>(device);
+    device_guard.emplace(index);
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(index);
+    stream = given == Py_None ? static_cast<void*>(current.stream()) : PyLong_AsVoidPtr(given);
+    if (stream == static_cast<void*>(current.stream())) return;
+    caller = current;
+    stream_guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), index));
+  }
+
+  // A result that this call allocated: not given out again, once it is released,
+  // before what the caller's stream does with it is done.
+  Tensor made(Tensor t) const {
+    if (caller) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *caller);
+    return t;
+  }
 
   const Tensor* tensor(PyObject* o) {
     if (!ok) return nullptr;
@@ -84,12 +113,8 @@ struct Call {
     }
     // (like empty_like, without its two passes through the dispatcher)
     if (like.is_non_overlapping_and_dense())
-      return Tensor(at::detail::empty_strided_cuda(like.sizes(), like.strides(), like.scalar_type(), like.device()));
-    return at::empty_like(like);
-  }
-
-  void* stream(PyObject* o) const {
-    return o == Py_None ? static_cast<void*>(c10::cuda::getCurrentCUDAStream(device).stream()) : PyLong_AsVoidPtr(o);
+      return made(Tensor(at::detail::empty_strided_cuda(like.sizes(), like.strides(), like.scalar_type(), like.device())));
+    return made(at::empty_like(like));
   }
 
   Tensor fresh(at::IntArrayRef sizes, at::ScalarType type) const {
@@ -185,7 +210,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t count) {
   }
   call.input(a[2], &pos);
   if (!call.ok) return nullptr;
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(call.device));
+  call.enter(a[8]);
   Owned list(PyList_New(n));
   if (!list) return nullptr;
   for (Py_ssize_t i = 0; i < n; ++i) {
@@ -196,17 +221,16 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t count) {
     if (!o) return nullptr;
     PyList_SET_ITEM(list.get(), i, o);
   }
-  void* stream = call.stream(a[8]);
   cpattn_status st;
   Py_BEGIN_ALLOW_THREADS
-  st = fn(static_cast<int>(n), x, &pos, static_cast<int>(n_axes), dims, theta, interleaved, inverse, y, stream);
+  st = fn(static_cast<int>(n), x, &pos, static_cast<int>(n_axes), dims, theta, interleaved, inverse, y, call.stream);
   Py_END_ALLOW_THREADS
   return Py_BuildValue("iN", static_cast<int>(st), list.release());
   END_HANDLE_TH_ERRORS
 }
 
 // cross(entry, workspace_bytes entry, q, k, v, kv_lengths | None, scale, out | None, lse | None,
-//       workspace | None, stream | None) -> (status, out, lse, workspace | None)
+//       workspace | None, stream | None) -> (status, out, lse)
 PyObject* cross(PyObject*, PyObject* const* a, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   if (!arguments(count, 11)) return nullptr;
@@ -224,7 +248,7 @@ PyObject* cross(PyObject*, PyObject* const* a, Py_ssize_t count) {
   call.input(a[4], &v);
   if (a[5] != Py_None) call.input(a[5], &n, true);
   if (!call.ok) return nullptr;
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(call.device));
+  call.enter(a[10]);
   const Tensor out = call.output(a[7], *tq);
   if (call.ok) call.describe(out, &o);
   Tensor lse;
@@ -234,26 +258,25 @@ PyObject* cross(PyObject*, PyObject* const* a, Py_ssize_t count) {
       if (t) lse = *t;
     } else {
       const auto sizes = tq->sizes();
-      lse = call.fresh(sizes.slice(0, sizes.size() < 3 ? sizes.size() : 3), at::kFloat);
+      lse = call.made(call.fresh(sizes.slice(0, sizes.size() < 3 ? sizes.size() : 3), at::kFloat));
     }
   }
   if (call.ok) call.describe(lse, &l);
   const Tensor ws = call.workspace(a[9], call.ok && a[9] == Py_None ? bytes(&q, &k) : 0);
   if (!call.ok) return nullptr;
-  void* stream = call.stream(a[10]);
   void* ws_ptr = ws.defined() ? ws.data_ptr() : nullptr;
   const size_t ws_bytes = ws.defined() ? static_cast<size_t>(ws.nbytes()) : 0;
   cpattn_status st;
   Py_BEGIN_ALLOW_THREADS
-  st = fn(&q, &k, &v, a[5] != Py_None ? &n : nullptr, scale, &o, &l, ws_ptr, ws_bytes, stream);
+  st = fn(&q, &k, &v, a[5] != Py_None ? &n : nullptr, scale, &o, &l, ws_ptr, ws_bytes, call.stream);
   Py_END_ALLOW_THREADS
-  return Py_BuildValue("iNNN", static_cast<int>(st), wrap(out), wrap(lse), wrap(ws));
+  return Py_BuildValue("iNN", static_cast<int>(st), wrap(out), wrap(lse));
   END_HANDLE_TH_ERRORS
 }
 
 // cross_backward(entry, workspace_bytes entry, q, k, v, out, lse, dout, kv_lengths | None, scale,
 //                dq | None, dk | None, dv | None, workspace | None, stream | None)
-//   -> (status, dq, dk, dv, workspace | None)
+//   -> (status, dq, dk, dv)
 PyObject* cross_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   if (!arguments(count, 15)) return nullptr;
@@ -274,7 +297,7 @@ PyObject* cross_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   }
   if (a[8] != Py_None) call.input(a[8], &n, true);
   if (!call.ok) return nullptr;
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(call.device));
+  call.enter(a[14]);
   Tensor out[3];
   for (int i = 0; i < 3 && call.ok; ++i) {
     out[i] = call.output(a[10 + i], *t[i]);
@@ -282,15 +305,14 @@ PyObject* cross_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   }
   const Tensor ws = call.workspace(a[13], call.ok && a[13] == Py_None ? bytes(&in[0], &in[1]) : 0);
   if (!call.ok) return nullptr;
-  void* stream = call.stream(a[14]);
   void* ws_ptr = ws.defined() ? ws.data_ptr() : nullptr;
   const size_t ws_bytes = ws.defined() ? static_cast<size_t>(ws.nbytes()) : 0;
   cpattn_status st;
   Py_BEGIN_ALLOW_THREADS
   st = fn(&in[0], &in[1], &in[2], &in[3], &in[4], &in[5], a[8] != Py_None ? &n : nullptr, scale, &grad[0], &grad[1],
-          &grad[2], ws_ptr, ws_bytes, stream);
+          &grad[2], ws_ptr, ws_bytes, call.stream);
   Py_END_ALLOW_THREADS
-  return Py_BuildValue("iNNNN", static_cast<int>(st), wrap(out[0]), wrap(out[1]), wrap(out[2]), wrap(ws));
+  return Py_BuildValue("iNNN", static_cast<int>(st), wrap(out[0]), wrap(out[1]), wrap(out[2]));
   END_HANDLE_TH_ERRORS
 }
 
