@@ -36,6 +36,19 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
     return s.cuda_stream
 
 
+def _empty(shape, device, dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """Memory for a call that runs on ``stream`` (None: the current one).  It is
+    that stream's: a block that the caller's stream has freed may still be read
+    there by work not yet done.  And it is not given out again before the
+    caller's stream is done with it."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, device=device, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, device=device, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _scale(scale: Optional[float]) -> float:
     return 0.0 if scale is None else float(scale)
 
@@ -48,9 +61,9 @@ def partial(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[f
     lib = _lib.load()
     B, H, S, D = q.shape
     if out is None:
-        out = torch.empty(B, H, S, D, device=q.device, dtype=torch.float32)
+        out = _empty((B, H, S, D), q.device, torch.float32, stream)
     if lse is None:
-        lse = torch.empty(B, H, S, device=q.device, dtype=torch.float32)
+        lse = _empty((B, H, S), q.device, torch.float32, stream)
     dq, dk, dv, do, dl = _desc(q), _desc(k), _desc(v), _desc(out), _desc(lse)
     check(lib.cpattn_partial(dq, dk, dv, _scale(scale), do, dl, _stream_handle(stream)),
           "cpattn_partial")
@@ -84,12 +97,12 @@ def ring(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ring_degree: int = 1
     lib = _lib.load()
     B, H, S, D = q.shape
     if out is None:
-        out = torch.empty(B, H, S, D, device=q.device, dtype=q.dtype)
+        out = _empty((B, H, S, D), q.device, q.dtype, stream)
     if lse is None:
-        lse = torch.empty(B, H, S, device=q.device, dtype=torch.float32)
+        lse = _empty((B, H, S), q.device, torch.float32, stream)
     need = ring_workspace_bytes(q, ring_degree)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        workspace = _empty(need, q.device, torch.uint8, stream)
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     dq, dk, dv, do, dl = _desc(q), _desc(k), _desc(v), _desc(out), _desc(lse)
@@ -114,12 +127,12 @@ def prepare_ring(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ring_degree:
     lib = _lib.load()
     B, H, S, D = q.shape
     if out is None:
-        out = torch.empty(B, H, S, D, device=q.device, dtype=q.dtype)
+        out = _empty((B, H, S, D), q.device, q.dtype, stream)
     if lse is None:
-        lse = torch.empty(B, H, S, device=q.device, dtype=torch.float32)
+        lse = _empty((B, H, S), q.device, torch.float32, stream)
     need = ring_workspace_bytes(q, ring_degree)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        workspace = _empty(need, q.device, torch.uint8, stream)
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     fn = lib.cpattn_ring_causal if causal else lib.cpattn_ring
@@ -148,9 +161,9 @@ def ring_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ring_degree:
     lib = _lib.load()
     B, H, S, D = q.shape
     if out is None:
-        out = torch.empty(B, H, S, D, device=q.device, dtype=q.dtype)
+        out = _empty((B, H, S, D), q.device, q.dtype, stream)
     if lse is None:
-        lse = torch.empty(B, H, S, device=q.device, dtype=torch.float32)
+        lse = _empty((B, H, S), q.device, torch.float32, stream)
     dq, dk, dv, do, dl = _desc(q), _desc(k), _desc(v), _desc(out), _desc(lse)
     check(lib.cpattn_ring_noalloc(dq, dk, dv, _scale(scale), int(ring_degree),
                                   int(bool(ring_anything)), do, dl, _stream_handle(stream)),
@@ -170,10 +183,10 @@ def ulysses_permute(x: torch.Tensor, degree: int, direction: int,
     if out is None:
         if direction == 1:
             B, S, H, D = x.shape
-            out = torch.empty(degree, B, S, H // max(degree, 1), D, device=x.device, dtype=x.dtype)
+            out = _empty((degree, B, S, H // max(degree, 1), D), x.device, x.dtype, stream)
         else:
             G, B, S, Hg, D = x.shape
-            out = torch.empty(B, S, G * Hg, D, device=x.device, dtype=x.dtype)
+            out = _empty((B, S, G * Hg, D), x.device, x.dtype, stream)
     dx, dy = _desc(x), _desc(out)
     check(lib.cpattn_ulysses_permute(dx, int(degree), int(direction), dy, _stream_handle(stream)),
           "cpattn_ulysses_permute")
@@ -197,11 +210,10 @@ def ulysses_permute_batch(xs, degree: int, direction: int, outs=None,
         if outs[i] is None:
             if direction == 1:
                 B, S, H, D = x.shape
-                outs[i] = torch.empty(degree, B, S, H // max(degree, 1), D, device=x.device,
-                                      dtype=x.dtype)
+                outs[i] = _empty((degree, B, S, H // max(degree, 1), D), x.device, x.dtype, stream)
             else:
                 G, B, S, Hg, D = x.shape
-                outs[i] = torch.empty(B, S, G * Hg, D, device=x.device, dtype=x.dtype)
+                outs[i] = _empty((B, S, G * Hg, D), x.device, x.dtype, stream)
     check(lib.cpattn_ulysses_permute_batch(len(xs), _descs(xs), int(degree), int(direction),
                                            _descs(outs), _stream_handle(stream)),
           "cpattn_ulysses_permute_batch")
@@ -235,7 +247,7 @@ def unified_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ulysses
     def buf(name, shape, dtype):
         t = bufs.get(name)
         if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-            t = torch.empty(shape, device=q.device, dtype=dtype)
+            t = _empty(shape, q.device, dtype, stream)
             bufs[name] = t
         return t
 
@@ -266,9 +278,9 @@ def prepare_unified(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ulysses_d
     B, S, H, D = q.shape
     G, R = int(ulysses_degree), int(ring_degree)
     gshape = (G, B, S, H // max(G, 1), D)
-    qg, kg, vg, og = (torch.empty(gshape, device=q.device, dtype=q.dtype) for _ in range(4))
-    lse = torch.empty(G * B, H // G, S, device=q.device, dtype=torch.float32)
-    out = torch.empty(B, S, H, D, device=q.device, dtype=q.dtype)
+    qg, kg, vg, og = (_empty(gshape, q.device, q.dtype, stream) for _ in range(4))
+    lse = _empty((G * B, H // G, S), q.device, torch.float32, stream)
+    out = _empty((B, S, H, D), q.device, q.dtype, stream)
     h = _stream_handle(stream)
     fwd = (3, _descs((q, k, v)), G, 1, _descs((qg, kg, vg)), h)
     inner = prepare_ring(grouped_as_bhsd(qg), grouped_as_bhsd(kg), grouped_as_bhsd(vg), R, False,
@@ -308,12 +320,12 @@ def ulysses_anything_permute(x: torch.Tensor, degree: int, direction: int,
     if out is None:
         if direction == 1:
             B, S, H, D = x.shape
-            out = torch.empty(G, B, S, -(-H // max(G, 1)), D, device=x.device, dtype=x.dtype)
+            out = _empty((G, B, S, -(-H // max(G, 1)), D), x.device, x.dtype, stream)
         else:
             if heads is None:
                 raise ValueError("the inverse regroup needs heads (or out)")
             _, B, S, _, D = x.shape
-            out = torch.empty(B, S, int(heads), D, device=x.device, dtype=x.dtype)
+            out = _empty((B, S, int(heads), D), x.device, x.dtype, stream)
     dx, dy = _desc(x), _desc(out)
     check(lib.cpattn_ulysses_anything_permute(dx, G, int(direction), dy, _stream_handle(stream)),
           "cpattn_ulysses_anything_permute")
@@ -332,13 +344,12 @@ def ulysses_anything_permute_batch(xs, degree: int, direction: int, heads: Optio
         if outs[i] is None:
             if direction == 1:
                 B, S, H, D = x.shape
-                outs[i] = torch.empty(G, B, S, -(-H // max(G, 1)), D, device=x.device,
-                                      dtype=x.dtype)
+                outs[i] = _empty((G, B, S, -(-H // max(G, 1)), D), x.device, x.dtype, stream)
             else:
                 if heads is None:
                     raise ValueError("the inverse regroup needs heads (or outs)")
                 _, B, S, _, D = x.shape
-                outs[i] = torch.empty(B, S, int(heads), D, device=x.device, dtype=x.dtype)
+                outs[i] = _empty((B, S, int(heads), D), x.device, x.dtype, stream)
     check(lib.cpattn_ulysses_anything_permute_batch(len(xs), _descs(xs), G, int(direction),
                                                     _descs(outs), _stream_handle(stream)),
           "cpattn_ulysses_anything_permute_batch")
@@ -365,7 +376,7 @@ def ulysses_anything_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     def buf(name, shape, dtype):
         t = bufs.get(name)
         if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-            t = torch.empty(shape, device=q.device, dtype=dtype)
+            t = _empty(shape, q.device, dtype, stream)
             bufs[name] = t
         return t
 
@@ -395,9 +406,9 @@ def prepare_ulysses_anything(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     G = int(degree)
     hm = -(-H // max(G, 1))
     gshape = (G, B, S, hm, D)
-    qg, kg, vg, og = (torch.empty(gshape, device=q.device, dtype=q.dtype) for _ in range(4))
-    lse = torch.empty(G, B, hm, S, device=q.device, dtype=torch.float32)
-    out = torch.empty(B, S, H, D, device=q.device, dtype=q.dtype)
+    qg, kg, vg, og = (_empty(gshape, q.device, q.dtype, stream) for _ in range(4))
+    lse = _empty((G, B, hm, S), q.device, torch.float32, stream)
+    out = _empty((B, S, H, D), q.device, q.dtype, stream)
     h = _stream_handle(stream)
     fwd = (3, _descs((q, k, v)), G, 1, _descs((qg, kg, vg)), h)
     attn = (_desc(qg), _desc(kg), _desc(vg), _scale(scale), H, int(bool(causal)), _desc(og),

@@ -132,3 +132,51 @@ def test_a_call_leaves_the_current_stream_as_it_was(make):
     torch.cuda.synchronize()
     for a, b, c in zip(got, same, named):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def older_calls():
+    """The attention, merge and regroup calls by name, each on tensors of its own."""
+    q, k, v = (normal(7 + i, 1, 4, 1024, 64) for i in range(3))
+    x = normal(10, 1, 1024, 4, 64)
+    grouped = cp.ulysses_permute(x, 2, 1)
+    uneven = cp.ulysses_anything_permute(x, 3, 1).zero_()
+    cp.ulysses_anything_permute(x, 3, 1, out=uneven)
+
+    def prepared(make, s):
+        call = make(s)
+        call()
+        return [call.out]
+
+    return {
+        "partial": lambda s: list(cp.partial(q, k, v, stream=s)),
+        "ring": lambda s: list(cp.ring(q, k, v, 2, stream=s)),
+        "ring_noalloc": lambda s: list(cp.ring_noalloc(q, k, v, 2, stream=s)),
+        "prepare_ring": lambda s: prepared(lambda s: cp.prepare_ring(q, k, v, 2, stream=s), s),
+        "permute": lambda s: [cp.ulysses_permute(x, 2, 1, stream=s), cp.ulysses_permute(grouped, 2, -1, stream=s)],
+        "permute_batch": lambda s: cp.ulysses_permute_batch([x, x], 2, 1, stream=s),
+        "unified": lambda s: list(cp.unified_attention(x, x, x, 2, 2, stream=s)),
+        "prepare_unified": lambda s: prepared(lambda s: cp.prepare_unified(x, x, x, 2, 2, stream=s), s),
+        "anything_permute": lambda s: [cp.ulysses_anything_permute(uneven, 3, -1, heads=4, stream=s)],
+        "anything_permute_batch": lambda s: cp.ulysses_anything_permute_batch([uneven, uneven], 3, -1, heads=4, stream=s),
+        "anything": lambda s: [cp.ulysses_anything_attention(x, x, x, 3, stream=s)[0]],
+        "prepare_anything": lambda s: prepared(lambda s: cp.prepare_ulysses_anything(x, x, x, 3, stream=s), s),
+    }
+
+
+OLDER = ("partial", "ring", "ring_noalloc", "prepare_ring", "permute", "permute_batch", "unified", "prepare_unified",
+         "anything_permute", "anything_permute_batch", "anything", "prepare_anything")
+
+
+@pytest.mark.parametrize("name", OLDER)
+def test_older_calls_results_are_not_the_current_streams_freed_blocks(name):
+    test_results_are_not_the_current_streams_freed_blocks(lambda: older_calls()[name])
+
+
+@pytest.mark.parametrize("name", OLDER)
+def test_older_calls_read_a_freed_temporary_to_its_end(name):
+    test_a_freed_temporary_is_read_to_its_end(lambda: older_calls()[name])
+
+
+@pytest.mark.parametrize("name", OLDER)
+def test_older_calls_read_a_released_result_to_its_end(name):
+    test_a_released_result_is_read_to_its_end(lambda: older_calls()[name])
