@@ -601,11 +601,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // (the previous P V completed before these scores: one issue order)
         if (__any_sync(0xffffffffu, raise)) rescale_o<D>(tO, factor);
+        // (only scores of -inf so far: their exponentials are 0, not of -inf + inf)
+        const float base = m == -INFINITY ? 0.f : -m;
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kBN / 2; ++i) {
           float x0, x1;
-          ffma2(x0, x1, u2f(s[2 * i]), u2f(s[2 * i + 1]), sl2, sl2, -m, -m);
+          ffma2(x0, x1, u2f(s[2 * i]), u2f(s[2 * i + 1]), sl2, sl2, base, base);
           const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
           const int a = 2 * (i & 1);
           fadd2(acc[a], acc[a + 1], acc[a], acc[a + 1], e0, e1);
@@ -646,9 +648,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float own = 1.f, other = 0.f;   // weights of the two sums
       if (PAIR && w.tiles > 1) {
         const float2 ml = pair_ml[quarter * 32 + lane];
-        const float top = fmaxf(m, ml.x);
-        own = ex2_approx(m - top);
-        other = ex2_approx(ml.x - top);
+        const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
+        own = ex2_approx(m - base);
+        other = ex2_approx(ml.x - base);
         l = l * own + ml.y * other;
         m = top;
       }
