@@ -851,7 +851,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key = k0 + quarter * 32 + lane;
     const bool live = key < len;
     bool ok = true;
+    uint32_t qt = first % q_tiles;
     for (uint32_t t = 0; t < steps; ++t) {
+      const int rows = p.s_q - static_cast<int>(qt) * kBM - half * 64;   // of this thread's 64 query columns
+      if (++qt == q_tiles) qt = 0;
       const float4* nl = reinterpret_cast<const float4*>(stats + (t & 1) * (C::STATS / 4)) + half * 16;
       const float4* dl = nl + kBM / 4;
       ok = wait_all(st_full(t & 1), (t >> 1) & 1, kErrSoftmax);
@@ -900,6 +903,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           // a key past the length (its k and v may hold anything): no weight
 #pragma unroll
           for (int i = 0; i < 16; ++i) px[i] = dx[i] = 0u;
+        }
+        if (rows < 64) {
+          // (the same for the whole warpgroup) rows past the end: their scores are
+          // 0 k_j, and 0 * inf is not 0
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = 32 * q + 2 * i;
+            const uint32_t keep = c + 1 < rows ? 0xFFFFFFFFu : c < rows ? 0xFFFFu : 0u;
+            px[i] &= keep;
+            dx[i] &= keep;
+          }
         }
         __syncwarp();
         tmem_st_x16(lanes + 128 + half * 64 + q * 16, px);

@@ -503,9 +503,11 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-          const float pr = key0 + warp * R + r < len ? exp2f(fmaf(s[r][c], p.scale_log2, -lse2[c])) : 0.f;
+          // (rows past the end: 0 k_j need not be 0)
+          const bool on = key0 + warp * R + r < len && i0 + 32 * c + lane < p.s_q;
+          const float pr = on ? exp2f(fmaf(s[r][c], p.scale_log2, -lse2[c])) : 0.f;
           myP[r * T1 + c * 32 + lane] = pr;
-          myS[r * T1 + c * 32 + lane] = len > 1 ? pr * (e[r][c] - delta[c]) : 0.f;   // (as in the dq kernel)
+          myS[r * T1 + c * 32 + lane] = on && len > 1 ? pr * (e[r][c] - delta[c]) : 0.f;   // (as in the dq kernel)
         }
       __syncwarp();
       spread<D, R, C>(myP, sG, dv);

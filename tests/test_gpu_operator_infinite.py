@@ -109,3 +109,23 @@ def test_keys_at_minus_infinity_have_no_weight(case, kind, dtype):
     assert cp.last_device_status() == 0
     assert ratio(out, want["out"]) <= 1.0
     assert ratio(lse, want["lse"]) <= 1.0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["inf", "overflow"])
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_gradient_with_keys_at_minus_infinity(case, kind, dtype):
+    """dk and dv of such a key are 0 where no row gives it weight, also when the
+    last tile of queries is not full.  (dq's feature 0 is 0 * inf, or past bf16.)"""
+    sizes, dead, lengths = whole(case)
+    q, k, v, dout, rows = inputs(kind, *sizes, dtype, dead, seed=2)
+    want = expected(q, k, v, dout, rows, dead, lengths)
+    n = lengths_of(lengths)
+    out, lse = cp.cross_attention(q, k, v, kv_lengths=n)
+    dq, dk, dv = cp.cross_attention_backward(q, k, v, out, lse, dout, kv_lengths=n)
+    assert cp.last_device_status() == 0
+    assert ratio(dq, want["dq"], skip_first=True) <= 1.0
+    assert ratio(dk, want["dk"]) <= 1.0
+    assert ratio(dv, want["dv"]) <= 1.0
+    if kind == "inf":
+        assert torch.all(dk[:, :, dead] == 0) and torch.all(dv[:, :, dead] == 0)
