@@ -2,6 +2,7 @@
 // (not part of the public ABI).
 #pragma once
 #include <atomic>
+#include <cmath>
 
 #include "internal.h"
 
@@ -41,6 +42,12 @@ __device__ __forceinline__ int cross_length(const CrossParams& p, int b) {
   const int32_t* at = p.lengths + b;
   const int n = CPATTN_IN(p.lengths_span, at, 4, p.err) ? *at : 0;
   return max(0, min(n, p.s_kv));
+}
+
+// A row's lse in base 2, as the gradients subtract it.  A row whose scores are all
+// -inf has lse -inf and no weights: against +inf its exponentials are 0.
+__device__ __forceinline__ float cross_lse2(float lse) {
+  return lse == -INFINITY ? INFINITY : lse * 1.442695040888963407f;
 }
 
 // Raises a kernel's dynamic shared-memory limit once per device (bit d of

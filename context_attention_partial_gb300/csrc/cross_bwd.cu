@@ -51,7 +51,6 @@ constexpr int kLaunchRegs = 168;    // 65536 / 384, rounded down to 8
 constexpr int kSoftmaxRegs = 208, kControlRegs = 88;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
-constexpr float kLog2e = 1.442695040888963407f;
 constexpr unsigned kErrProducer = 1u, kErrMma = 2u, kErrSoftmax = 4u, kErrStats = 8u;
 
 template <int D>
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fetch(wn);
     while (ok && walk.more(p)) {
       const DqUnit w = wn;
-      const float nl = -lse * kLog2e;
+      const float nl = -cross_lse2(lse);
       float neg_delta = 0.f;
       walk.step(p);
       const bool more = walk.more(p);
@@ -833,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* st = stats + (t & 1) * (C::STATS / 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          st[i * 32 + lane] = -nl[i] * kLog2e;
+          st[i * 32 + lane] = -cross_lse2(nl[i]);
           st[kBM + i * 32 + lane] = -dl[i];
           nl[i] = nn[i];
           dl[i] = dn[i];

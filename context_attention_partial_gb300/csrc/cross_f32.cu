@@ -33,7 +33,6 @@ namespace {
 constexpr int kOwn = 64;         // rows a block owns
 constexpr int kThreads = 256;
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr float kLog2e = 1.442695040888963407f;
 
 // This lane's row of 4 and column of 8 in a warp's tile (see above).
 __device__ __forceinline__ int lane_row() { return (threadIdx.x & 1) | ((threadIdx.x >> 1) & 2); }
@@ -357,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_f32_dq_kernel
     stat[i] = scores ? INFINITY : 0.f;   // (rows past the end: p = 0)
     if (row < p.s_q) {
       const float* at = scores ? lse_at(p.lse, b, h, row) : p.ws + static_cast<int64_t>(bh) * p.s_q + row;
-      if (CPATTN_IN(scores ? p.lse.span : p.ws_span, at, 4, p.err)) stat[i] = scores ? *at * kLog2e : *at;
+      if (CPATTN_IN(scores ? p.lse.span : p.ws_span, at, 4, p.err)) stat[i] = scores ? cross_lse2(*at) : *at;
     }
 #pragma unroll
     for (int f = 0; f < F; ++f) dq[i][f] = 0.f;
@@ -459,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
         if (row < p.s_q) {
           const float* at =
               scores ? lse_at(p.lse, b, h, row) : p.ws + (static_cast<int64_t>(b) * p.heads + h) * p.s_q + row;
-          if (CPATTN_IN(scores ? p.lse.span : p.ws_span, at, 4, p.err)) stat[j] = scores ? *at * kLog2e : *at;
+          if (CPATTN_IN(scores ? p.lse.span : p.ws_span, at, 4, p.err)) stat[j] = scores ? cross_lse2(*at) : *at;
         }
       }
       copies_wait_older();

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_consta
         sum = make_float4(fmaf(w, y.x, sum.x), fmaf(w, y.y, sum.y), fmaf(w, y.z, sum.z), fmaf(w, y.w, sum.w));
       }
     }
-    const bool none = cluster * parts * per >= all;   // (no keys in this cluster's parts)
+    const bool none = total == 0.f;   // (no keys in this cluster's parts, or scores of -inf only)
     const float inv = none ? 0.f : 1.f / total;
     sum = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
     const float lse = none ? -INFINITY : (top + log2f(total)) * kLn2;

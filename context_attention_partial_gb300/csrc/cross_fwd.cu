@@ -654,7 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * own + ml.y * other;
         m = top;
       }
-      const float inv = none ? 0.f : 1.f / l;
+      // (l is 0 where every score is -inf: no key has weight, as without keys)
+      const float inv = none || l == 0.f ? 0.f : 1.f / l;
       const float lse = none ? -INFINITY : (m + log2f(l)) * kLn2;
       if (!PAIR && !none) {
         ok = wait_all(bar_o(wg), no & 1, kErrSoftmax);

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_cons
     if (row < p.s_q) {
       const float* l = static_cast<const float*>(p.lse.data) + b * p.lse.s[0] + h * p.lse.s[1] + row * p.lse.s[2];
       const float* d = p.ws + static_cast<int64_t>(bh) * p.s_q + row;
-      if (CPATTN_IN(p.lse.span, l, 4, p.err)) lse2[r] = *l * kLog2e;
+      if (CPATTN_IN(p.lse.span, l, 4, p.err)) lse2[r] = cross_lse2(*l);
       if (CPATTN_IN(p.ws_span, d, 4, p.err)) delta[r] = *d;
     }
 #pragma unroll
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
         if (row < p.s_q) {
           const float* l = static_cast<const float*>(p.lse.data) + b * p.lse.s[0] + h * p.lse.s[1] + row * p.lse.s[2];
           const float* d = p.ws + (static_cast<int64_t>(b) * p.heads + h) * p.s_q + row;
-          if (CPATTN_IN(p.lse.span, l, 4, p.err)) lse2[c] = *l * kLog2e;
+          if (CPATTN_IN(p.lse.span, l, 4, p.err)) lse2[c] = cross_lse2(*l);
           if (CPATTN_IN(p.ws_span, d, 4, p.err)) delta[c] = *d;
         }
       }

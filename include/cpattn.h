@@ -303,7 +303,7 @@ cpattn_status cpattn_rotary(int n, const cpattn_tensor* x, const cpattn_tensor* 
  * length:
  *   out = softmax(scale q k^T) v over the first kv_lengths[b] keys, lse its
  *   natural log-sum-exp; a sequence without keys gives (0, -inf), the identity
- *   of cpattn_merge.
+ *   of cpattn_merge, and so does a row whose scores are all -inf.
  *   q [B, H, S_q, D], k, v [B, H_kv, S_kv, D]: bf16 or f32, D = 64 or 128;
  *     H % H_kv == 0 (else CPATTN_ERR_DIVISIBILITY): query heads h_kv * H / H_kv
  *     and following share key head h_kv.  S_kv may be 0.
@@ -332,7 +332,7 @@ size_t cpattn_cross_workspace_bytes(const cpattn_tensor* q, const cpattn_tensor*
  *   dq [B, H, S_q, D], dk, dv [B, H_kv, S_kv, D]: written, q's dtype.  dk and
  *     dv sum over the query heads that share a key head; rows past a sequence's
  *     length get 0; dq is 0 for a sequence without keys, dq and dk are exactly 0
- *     for one with a single key.
+ *     for one with a single key.  A row with lse -inf has no weights.
  * Every sum has one owner and a fixed order: equal calls give equal bits.
  *   workspace: at least cpattn_cross_backward_workspace_bytes(q, k) bytes,
  *     16-byte aligned.

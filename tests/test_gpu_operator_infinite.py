@@ -129,3 +129,28 @@ def test_gradient_with_keys_at_minus_infinity(case, kind, dtype):
     assert ratio(dv, want["dv"]) <= 1.0
     if kind == "inf":
         assert torch.all(dk[:, :, dead] == 0) and torch.all(dv[:, :, dead] == 0)
+
+
+# S_q, S_kv, D: the few-rows kernel, one chain and two, key parts (cluster and
+# workspace), 64-row and small fp32 blocks
+ALL = [(1, 5, 64), (3, 700, 128), (1, 9000, 128), (40, 130, 64), (77, 4481, 64), (130, 128, 128), (300, 300, 128), (1000, 200, 64)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["inf", "overflow"])
+@pytest.mark.parametrize("M,N,D", ALL)
+def test_rows_without_a_finite_score_are_rows_without_keys(M, N, D, kind, dtype):
+    """(0, -inf) forward, and no part in any gradient."""
+    dead = slice(0, N)
+    q, k, v, dout, rows = inputs(kind, 1, 4, 2, M, N, D, dtype, dead, seed=3)
+    want = expected(q, k, v, dout, rows, dead, None)
+    out, lse = cp.cross_attention(q, k, v)
+    dq, dk, dv = cp.cross_attention_backward(q, k, v, out, lse, dout)
+    assert cp.last_device_status() == 0
+    assert torch.all(out[:, :, rows] == 0) and torch.all(lse[:, :, rows] == -math.inf)
+    assert ratio(out, want["out"]) <= 1.0 and ratio(lse, want["lse"]) <= 1.0
+    assert torch.all(dq[:, :, rows, 1:] == 0)
+    assert ratio(dq, want["dq"], skip_first=True) <= 1.0
+    assert ratio(dk, want["dk"]) <= 1.0 and ratio(dv, want["dv"]) <= 1.0
+    if kind == "overflow":
+        assert torch.all(dq[:, :, rows] == 0)
