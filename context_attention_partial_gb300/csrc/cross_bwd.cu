@@ -665,6 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  // The copies and the first S and dP may run under the dq kernel.  What follows
+  // them needs its delta, and the limit of a wait must not count the time that
+  // kernel still takes: every warp waits for its end (launch_wait) before its
+  // first wait for something behind the statistics.
   auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) {
     const bool ok = mbar_wait(bar, parity, abort_flag, p.timeout_ns, p.err, code);
     return __all_sync(0xffffffffu, ok) != 0;
@@ -685,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       uint32_t g = uniform(first / q_tiles), qt = first - g * q_tiles;
       for (; x < 2 * steps && ok; ++x) {
+        if (x == C::RING) launch_wait();
         ok = wait_all(empty(x), phase(x) ^ 1, kErrProducer);
         if (!ok) break;
         if (leader) {
@@ -731,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
+      launch_wait();
       for (uint32_t t = 0; t < steps && ok; ++t) {
         const bool more = t + 1 < steps;
         qn = gc;
@@ -851,6 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool live = key < len;
     bool ok = true;
     uint32_t qt = first % q_tiles;
+    launch_wait();
     for (uint32_t t = 0; t < steps; ++t) {
       const int rows = p.s_q - static_cast<int>(qt) * kBM - half * 64;   // of this thread's 64 query columns
       if (++qt == q_tiles) qt = 0;
