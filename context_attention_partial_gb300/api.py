@@ -472,8 +472,8 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                     stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention of q [B,H,S_q,D] to an encoder's states k, v [B,H_kv,S_kv,D]
     (cpattn_cross_attention): H_kv divides H; kv_lengths (int32 [B]) gives each
-    sequence's valid keys, a sequence without any gives (0, -inf).  No autograd
-    graph is recorded: ``cross_attention_backward`` is its gradient.
+    sequence's valid keys, a sequence without any gives (0, -inf).  Inputs may be
+    broadcast views (they are copied for the call).  No autograd graph is recorded: ``cross_attention_backward`` is its gradient.
     Returns (out [B,H,S_q,D] in q's dtype, lse f32 [B,H,S_q])."""
     at = _lib.load().addresses
     status, o, l = _lib.binding().cross(at["cross_attention"], at["cross_workspace_bytes"], q, k, v, kv_lengths,
@@ -491,7 +491,8 @@ def cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
                              stream: Optional[torch.cuda.Stream] = None
                              ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Gradient of ``cross_attention`` (cpattn_cross_attention_backward): out and
-    lse as it returned them, dout the gradient of out.  Returns (dq, dk, dv) in
+    lse as it returned them, dout the gradient of out (a broadcast view like that of
+    ``out.sum()`` too).  Returns (dq, dk, dv) in
     the shapes and dtype of q, k, v; rows of dk and dv past a sequence's
     length are 0."""
     at = _lib.load().addresses

@@ -12,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDACachingAllocator.h>
@@ -77,6 +78,27 @@ struct Call {
     return ok ? &t : nullptr;
   }
 
+  // An input for kernels that read each element from a place of its own: a
+  // broadcast view (the gradient that out.sum() sends back, a prompt expanded over a
+  // guided pair) is copied into one, on the call's stream (so after enter()).
+  const Tensor* dense(const Tensor* t) {
+    bool broadcast = false;
+    for (int64_t i = 0; i < t->dim(); ++i) broadcast = broadcast || (t->size(i) > 1 && t->stride(i) == 0);
+    return broadcast ? copy(*t) : t;
+  }
+  // For kernels that read broadcast rows, heads and batches where they are.
+  const Tensor* dense_rows(const Tensor* t) {
+    const int64_t n = t->dim();
+    return n > 0 && t->size(n - 1) > 1 && t->stride(n - 1) == 0 ? copy(*t) : t;
+  }
+  const Tensor* copy(const Tensor& t) {
+    const at::NoGradGuard no_grad;
+    copies[n_copies] = t.contiguous();
+    return &copies[n_copies++];
+  }
+  Tensor copies[7];   // of the at most seven inputs of a call
+  int n_copies = 0;
+
   void describe(const Tensor& t, cpattn_tensor* d, bool lengths = false) {
     if (!ok) return;
     const auto type = t.scalar_type();
@@ -98,10 +120,6 @@ struct Call {
       d->shape[i] = i < d->ndim ? t.size(i) : 0;
       d->stride[i] = i < d->ndim ? t.stride(i) : 0;
     }
-  }
-
-  void input(PyObject* o, cpattn_tensor* d, bool lengths = false) {
-    if (const Tensor* t = tensor(o)) describe(*t, d, lengths);
   }
 
   // A given output, or a new one like `like` (keeping a [B, S, H, D] tensor's order).
@@ -204,13 +222,13 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t count) {
   Call call;
   cpattn_tensor x[CPATTN_MAX_PERMUTE_BATCH], y[CPATTN_MAX_PERMUTE_BATCH], pos;
   const Tensor* in[CPATTN_MAX_PERMUTE_BATCH];
-  for (Py_ssize_t i = 0; i < n; ++i) {
-    in[i] = call.tensor(PySequence_Fast_GET_ITEM(xs.get(), i));
-    if (in[i]) call.describe(*in[i], &x[i]);
-  }
-  call.input(a[2], &pos);
+  for (Py_ssize_t i = 0; i < n; ++i) in[i] = call.tensor(PySequence_Fast_GET_ITEM(xs.get(), i));
+  const Tensor* positions = call.tensor(a[2]);
   if (!call.ok) return nullptr;
   call.enter(a[8]);
+  for (Py_ssize_t i = 0; i < n; ++i) call.describe(*call.dense_rows(in[i]), &x[i]);
+  call.describe(*positions, &pos);
+  if (!call.ok) return nullptr;
   Owned list(PyList_New(n));
   if (!list) return nullptr;
   for (Py_ssize_t i = 0; i < n; ++i) {
@@ -243,12 +261,16 @@ PyObject* cross(PyObject*, PyObject* const* a, Py_ssize_t count) {
   Call call;
   cpattn_tensor q, k, v, n, o, l;
   const Tensor* tq = call.tensor(a[2]);
-  if (tq) call.describe(*tq, &q);
-  call.input(a[3], &k);
-  call.input(a[4], &v);
-  if (a[5] != Py_None) call.input(a[5], &n, true);
+  const Tensor* tk = call.tensor(a[3]);
+  const Tensor* tv = call.tensor(a[4]);
+  const Tensor* tn = a[5] != Py_None ? call.tensor(a[5]) : nullptr;
   if (!call.ok) return nullptr;
   call.enter(a[10]);
+  call.describe(*call.dense(tq), &q);
+  call.describe(*call.dense(tk), &k);
+  call.describe(*call.dense(tv), &v);
+  if (tn) call.describe(*call.dense(tn), &n, true);
+  if (!call.ok) return nullptr;
   const Tensor out = call.output(a[7], *tq);
   if (call.ok) call.describe(out, &o);
   Tensor lse;
@@ -268,7 +290,7 @@ PyObject* cross(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const size_t ws_bytes = ws.defined() ? static_cast<size_t>(ws.nbytes()) : 0;
   cpattn_status st;
   Py_BEGIN_ALLOW_THREADS
-  st = fn(&q, &k, &v, a[5] != Py_None ? &n : nullptr, scale, &o, &l, ws_ptr, ws_bytes, call.stream);
+  st = fn(&q, &k, &v, tn ? &n : nullptr, scale, &o, &l, ws_ptr, ws_bytes, call.stream);
   Py_END_ALLOW_THREADS
   return Py_BuildValue("iNN", static_cast<int>(st), wrap(out), wrap(lse));
   END_HANDLE_TH_ERRORS
@@ -289,15 +311,14 @@ PyObject* cross_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (PyErr_Occurred()) return nullptr;
   Call call;
   cpattn_tensor in[6], n, grad[3];
-  const Tensor* t[3] = {};
-  for (int i = 0; i < 6; ++i) {
-    const Tensor* x = call.tensor(a[2 + i]);
-    if (x) call.describe(*x, &in[i]);
-    if (i < 3) t[i] = x;
-  }
-  if (a[8] != Py_None) call.input(a[8], &n, true);
+  const Tensor* t[6];
+  for (int i = 0; i < 6; ++i) t[i] = call.tensor(a[2 + i]);
+  const Tensor* tn = a[8] != Py_None ? call.tensor(a[8]) : nullptr;
   if (!call.ok) return nullptr;
   call.enter(a[14]);
+  for (int i = 0; i < 6; ++i) call.describe(*call.dense(t[i]), &in[i]);
+  if (tn) call.describe(*call.dense(tn), &n, true);
+  if (!call.ok) return nullptr;
   Tensor out[3];
   for (int i = 0; i < 3 && call.ok; ++i) {
     out[i] = call.output(a[10 + i], *t[i]);
@@ -309,7 +330,7 @@ PyObject* cross_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const size_t ws_bytes = ws.defined() ? static_cast<size_t>(ws.nbytes()) : 0;
   cpattn_status st;
   Py_BEGIN_ALLOW_THREADS
-  st = fn(&in[0], &in[1], &in[2], &in[3], &in[4], &in[5], a[8] != Py_None ? &n : nullptr, scale, &grad[0], &grad[1],
+  st = fn(&in[0], &in[1], &in[2], &in[3], &in[4], &in[5], tn ? &n : nullptr, scale, &grad[0], &grad[1],
           &grad[2], ws_ptr, ws_bytes, call.stream);
   Py_END_ALLOW_THREADS
   return Py_BuildValue("iNNN", static_cast<int>(st), wrap(out[0]), wrap(out[1]), wrap(out[2]));

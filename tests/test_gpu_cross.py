@@ -371,3 +371,47 @@ def test_cross_attention_merges_with_other_partials():
         vv = torch.cat([v[i:i + 1, :, :cut], v[i:i + 1, :, 100:]], 2)
         value, tol = plain.cross(q[i:i + 1], kk, vv)["out"]
         assert plain.worst(a[i:i + 1], value, 3 * tol) <= 1.0
+
+
+def broadcast_inputs(dtype, B, H, Hk, M, N, D):
+    """q, k, v, dout with extents that walk on the spot, and their dense copies."""
+    g = torch.Generator("cpu").manual_seed(60)
+    q = torch.randn(1, H, M, D, generator=g).to(dtype).to(DEV).expand(B, H, M, D)            # one query block
+    k = torch.randn(1, Hk, N, D, generator=g).to(dtype).to(DEV).expand(B, Hk, N, D)          # one prompt for all
+    v = torch.randn(B, 1, N, D, generator=g).to(dtype).to(DEV).expand(B, Hk, N, D)
+    dout = torch.full((), 0.5, dtype=dtype, device=DEV).expand(B, H, M, D)                   # of (out / 2).sum()
+    return (q, k, v, dout), tuple(t.contiguous() for t in (q, k, v, dout))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("sizes", [(2, 4, 2, 150, 77, 64), (3, 2, 2, 1, 700, 128), (2, 4, 4, 90, 3000, 64)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_cross_broadcast_inputs(sizes, dtype):
+    """Broadcast inputs give what their dense copies give, also on another stream
+    and captured; a broadcast output is refused."""
+    B = sizes[0]
+    views, dense = broadcast_inputs(dtype, *sizes)
+    n = torch.full((1,), sizes[4] - 3, dtype=torch.int32, device=DEV)
+    out, lse = cp.cross_attention(*dense[:3], kv_lengths=n.expand(B).contiguous())
+    want = (out, lse, *cp.cross_attention_backward(*dense[:3], out, lse, dense[3], kv_lengths=n.expand(B).contiguous()))
+
+    def step(stream=None):
+        o, l = cp.cross_attention(*views[:3], kv_lengths=n.expand(B), stream=stream)
+        return (o, l, *cp.cross_attention_backward(*views[:3], o, l, views[3], kv_lengths=n.expand(B), stream=stream))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = [step(), step(s)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got.append(step())
+    graph.replay()
+    torch.cuda.synchronize()
+    for result in got:
+        for a, b in zip(result, want):
+            assert a.shape == b.shape and torch.equal(a, b)
+    with pytest.raises(cp.CpattnError) as e:
+        cp.cross_attention(*dense[:3], out=dense[0][:1].expand_as(dense[0]))
+    assert e.value.name == "CPATTN_ERR_LAYOUT"
+    assert cp.last_device_status() == 0

@@ -144,3 +144,15 @@ def test_rotary_captured_and_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(out, -want)
     assert cp.last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_rotary_gradient_of_a_sum(interleaved, dtype):
+    """The gradient that (w y).sum() sends back is one value for every element."""
+    pos = grid_positions(1, 3, 11)
+    dy = torch.full((), 0.75, dtype=dtype, device=DEV).expand(2, 3, 33, 64)
+    want = cp.rotary(dy.contiguous(), pos, (16, 24, 24), interleaved=interleaved, inverse=True)
+    got = cp.rotary(dy, pos, (16, 24, 24), interleaved=interleaved, inverse=True)
+    assert got.shape == dy.shape and torch.equal(got, want)
+    check(dy, got, pos, (16, 24, 24), interleaved=interleaved, inverse=True)
