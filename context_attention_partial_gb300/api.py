@@ -446,13 +446,13 @@ def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float =
     the gradient (no autograd graph is recorded).  outs may be xs (in place).
     Returns a tensor for a tensor, else a list."""
     lib = _lib.load()
-    if isinstance(xs, torch.Tensor):
-        return rotary([xs], positions, axes_dims, theta, interleaved, inverse, None if outs is None else [outs],
-                      stream)[0]
+    single = isinstance(xs, torch.Tensor)
+    if single:
+        xs, outs = [xs], None if outs is None else [outs]
     status, results = _lib.binding().rotary(lib.addresses["rotary"], xs, positions, axes_dims, theta,
                                             interleaved, inverse, outs, _handle(stream, positions))
     check(status, "cpattn_rotary")
-    return results
+    return results[0] if single else results
 
 
 def cross_workspace_bytes(q: torch.Tensor, k: torch.Tensor) -> int:

@@ -78,6 +78,20 @@ struct Call {
     return ok ? &t : nullptr;
   }
 
+  // An input.  No autograd graph is recorded, so one that asks for a gradient is
+  // worth a warning where graphs are recorded (not inside no_grad(), nor in the
+  // forward or backward of an autograd.Function that calls this).
+  const Tensor* input(PyObject* o) {
+    const Tensor* t = tensor(o);
+    if (t && t->requires_grad() && at::GradMode::is_enabled() &&
+        PyErr_WarnEx(PyExc_UserWarning,
+                     "cpattn records no autograd graph: the result is detached from an input that requires a gradient "
+                     "(call the gradient entry points, under torch.no_grad() or in a torch.autograd.Function)",
+                     2) < 0)
+      ok = false;
+    return ok ? t : nullptr;
+  }
+
   // An input for kernels that read each element from a place of its own: a
   // broadcast view (the gradient that out.sum() sends back, a prompt expanded over a
   // guided pair) is copied into one, on the call's stream (so after enter()).
@@ -222,8 +236,8 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t count) {
   Call call;
   cpattn_tensor x[CPATTN_MAX_PERMUTE_BATCH], y[CPATTN_MAX_PERMUTE_BATCH], pos;
   const Tensor* in[CPATTN_MAX_PERMUTE_BATCH];
-  for (Py_ssize_t i = 0; i < n; ++i) in[i] = call.tensor(PySequence_Fast_GET_ITEM(xs.get(), i));
-  const Tensor* positions = call.tensor(a[2]);
+  for (Py_ssize_t i = 0; i < n; ++i) in[i] = call.input(PySequence_Fast_GET_ITEM(xs.get(), i));
+  const Tensor* positions = call.input(a[2]);
   if (!call.ok) return nullptr;
   call.enter(a[8]);
   for (Py_ssize_t i = 0; i < n; ++i) call.describe(*call.dense_rows(in[i]), &x[i]);
@@ -260,9 +274,9 @@ PyObject* cross(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (PyErr_Occurred()) return nullptr;
   Call call;
   cpattn_tensor q, k, v, n, o, l;
-  const Tensor* tq = call.tensor(a[2]);
-  const Tensor* tk = call.tensor(a[3]);
-  const Tensor* tv = call.tensor(a[4]);
+  const Tensor* tq = call.input(a[2]);
+  const Tensor* tk = call.input(a[3]);
+  const Tensor* tv = call.input(a[4]);
   const Tensor* tn = a[5] != Py_None ? call.tensor(a[5]) : nullptr;
   if (!call.ok) return nullptr;
   call.enter(a[10]);
@@ -312,7 +326,7 @@ PyObject* cross_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   Call call;
   cpattn_tensor in[6], n, grad[3];
   const Tensor* t[6];
-  for (int i = 0; i < 6; ++i) t[i] = call.tensor(a[2 + i]);
+  for (int i = 0; i < 6; ++i) t[i] = call.input(a[2 + i]);
   const Tensor* tn = a[8] != Py_None ? call.tensor(a[8]) : nullptr;
   if (!call.ok) return nullptr;
   call.enter(a[14]);
