@@ -12,8 +12,13 @@
 // at position 100,000.  Frequencies therefore come from the host as two
 // floats, in turns per position (theta^(-2i/d) / 2 pi in fp64, split hi + lo);
 // pos * hi is taken exactly as a product and its fused remainder, whole turns
-// are dropped from the product (exact), and sincospif sees the rest: the
-// angle's error is below 2^-24 turns at any position fp32 can hold exactly.
+// are dropped from the product (exact), and sincospif sees the rest.  With theta
+// >= 1 and |pos| <= 2^24 that is at most 2^21.4 turns, and off by
+//     2^-25.6   the frequency, 2^-47 of the turns
+//   + 2^-26     the sum of remainder and pos * lo, below half a turn
+//   + 2^-25     the sum of both with the product, below one turn
+// or 2^-23.9 turns in all (2^-24.6 is the largest found).  Past 2^24 the first two
+// grow with the position: 2^-23.4 found at 2^27, 2^-20.4 at 2^30.
 // (fp64 sines would cost 29 us at 4608 tokens on this GPU's FP64 units.)
 //
 // What bounds it: HBM, each tensor read and written once.  A thread keeps one

@@ -289,8 +289,9 @@ size_t cpattn_ring_noalloc_max_workspace_bytes(void);
  *     (i, i + axis_dims[a] / 2).
  *   inverse: 0, or 1 for the turn by the negative angle: the gradient with
  *     respect to x, and the way back.
- * Angles are formed in two-float arithmetic: exact to fp32 at any position
- * that fp32 holds exactly.  y[i] may be x[i] itself (same data and strides);
+ * Angles are formed in two-float arithmetic: off by less than 2^-23 turns (7.5e-7
+ * radians) at positions of up to 2^24 in magnitude, theta >= 1; past that the error
+ * grows with the position, as it does with a theta below 1.  y[i] may be x[i] itself (same data and strides);
  * otherwise no element of an output may be an element of another buffer of
  * the call.  B, S or every H_i = 0 is a no-op.
  */

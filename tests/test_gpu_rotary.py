@@ -156,3 +156,25 @@ def test_rotary_gradient_of_a_sum(interleaved, dtype):
     got = cp.rotary(dy, pos, (16, 24, 24), interleaved=interleaved, inverse=True)
     assert got.shape == dy.shape and torch.equal(got, want)
     check(dy, got, pos, (16, 24, 24), interleaved=interleaved, inverse=True)
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("theta", [1.0, 1.5, 1e4, 1e7])
+@pytest.mark.parametrize("axes", [(64,), (128,), (256,), (22, 20, 22)])
+def test_rotary_angles_up_to_two_to_the_24(axes, theta, interleaved):
+    """The header's bound: 2^-23 turns at positions of up to 2^24 in magnitude.
+    With it, cos and sin of two steps, two products and a sum:
+    (2 pi 2^-23 + 2 * 2^-24 + 3 * 2^-24) / 2^-24 < 18 of the pair's magnitudes."""
+    g = torch.Generator("cpu").manual_seed(12)
+    D = max(64, sum(axes) + 2)
+    D += -D % 8
+    S = 64
+    x = normal(13, 1, 2, S, D, dtype=torch.float32)
+    pos = ((torch.rand(S, len(axes), generator=g) * 2 - 1) * 2 ** 24)
+    pos[:4] = torch.tensor([2.0 ** 24, -(2.0 ** 24), 2.0 ** 24 - 1, 0.0]).view(4, 1)
+    pos = pos.to(DEV)
+    if D > 256:
+        x, D = x[..., :256].contiguous(), 256
+    y = cp.rotary(x, pos, axes, theta=theta, interleaved=interleaved)
+    want, mag = plain.rotary(x, pos, axes, theta=theta, interleaved=interleaved)
+    assert plain.worst(y, want, 18 * 2.0 ** -24 * mag) <= 1.0

@@ -156,3 +156,33 @@ def test_python_binding_refusals():
         cp.cross_attention(q, q, q)
     with pytest.raises(ValueError):
         cp.cross_attention_backward(q, q, q, q, torch.zeros(1, 1, 4), q)
+
+
+@pytest.mark.parametrize("theta", [1.0, 1.5, 100.0, 1e4, 1e7])
+@pytest.mark.parametrize("d", [64, 256])
+def test_rotary_angle_arithmetic(d, theta):
+    """The kernel's angle step by step on the host, in exact fractions where fp32
+    rounds: within the header's 2^-23 turns at positions of up to 2^24."""
+    import math
+    import random
+    from decimal import Decimal, getcontext
+
+    import numpy as np
+    f32 = np.float32
+    getcontext().prec = 50
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937511")
+    rate, rng = -2.0 / d * math.log(theta), random.Random(1)
+    step, f, worst = math.exp(rate), 0.0, Decimal(0)
+    for i in range(d // 2):
+        f = 0.15915494309189535 * math.exp(i * rate) if i % 8 == 0 else f * step
+        hi_w = f32(f)
+        lo_w = f32(f - float(hi_w))
+        exact = (Decimal(-2 * i) / d * Decimal(theta).ln()).exp() / two_pi
+        for pos in [f32(2.0 ** 24), f32(2.0 ** 24 - 1)] + [f32(rng.uniform(-2.0 ** 24, 2.0 ** 24)) for _ in range(8)]:
+            product = float(pos) * float(hi_w)                 # (48 bits: exact in fp64)
+            hi = f32(product)
+            lo = f32(Decimal(float(pos)) * Decimal(float(lo_w)) + Decimal(product - float(hi)))
+            turns = f32(f32(hi - np.rint(hi)) + lo)
+            off = Decimal(float(turns)) - Decimal(float(pos)) * exact
+            worst = max(worst, abs(off - off.to_integral_value()))
+    assert worst < Decimal(2) ** -23
