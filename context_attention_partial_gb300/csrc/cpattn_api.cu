@@ -748,13 +748,13 @@ cpattn_status cpattn_rotary(int n, const cpattn_tensor* x, const cpattn_tensor* 
   for (int a = 0; a < axes; ++a) {
     p.axis_dim[a] = axis_dims[a];
     p.pair_start[a] = j;
-    // theta^(-2i/d) / 2 pi: every eighth of its own, the seven behind it by repeated
-    // products (an exponential costs some 15 ns of host time).  Relative error
-    // below 2^-48 (1 + i / d log theta), as what hi + lo leave out: 2^-48.
+    // theta^(-2i/d) / 2 pi: every sixteenth of its own, those behind it by repeated
+    // products (an exponential costs some 15 ns of host time): relative error
+    // below 2^-47 and 2^-51 of |log| of the power; hi + lo leave out 2^-48
     const double rate = -2.0 / axis_dims[a] * std::log(theta), step = std::exp(rate);
-    double f = 0.0;
+    double f = 0.15915494309189535;
     for (int i = 0; i < axis_dims[a] / 2; ++i, f *= step) {
-      if (i % 8 == 0) f = 0.15915494309189535 * std::exp(i * rate);
+      if (i > 0 && i % 16 == 0) f = 0.15915494309189535 * std::exp(i * rate);
       const float hi = static_cast<float>(f);
       p.freq[j++] = make_float2(hi, static_cast<float>(f - hi));
     }

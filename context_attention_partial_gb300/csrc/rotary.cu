@@ -14,10 +14,10 @@
 // pos * hi is taken exactly as a product and its fused remainder, whole turns
 // are dropped from the product (exact), and sincospif sees the rest.  With theta
 // >= 1 and |pos| <= 2^24 that is at most 2^21.4 turns, and off by
-//     2^-25.6   the frequency, 2^-47 of the turns
+//     2^-25.0   the frequency, 1.5 * 2^-47 of the turns
 //   + 2^-26     the sum of remainder and pos * lo, below half a turn
 //   + 2^-25     the sum of both with the product, below one turn
-// or 2^-23.9 turns in all (2^-24.6 is the largest found).  Past 2^24 the first two
+// or 2^-23.6 turns in all (2^-24.6 is the largest found).  Past 2^24 the first two
 // grow with the position: 2^-23.4 found at 2^27, 2^-20.4 at 2^30.
 // (fp64 sines would cost 29 us at 4608 tokens on this GPU's FP64 units.)
 //

@@ -174,7 +174,7 @@ def test_rotary_angle_arithmetic(d, theta):
     rate, rng = -2.0 / d * math.log(theta), random.Random(1)
     step, f, worst = math.exp(rate), 0.0, Decimal(0)
     for i in range(d // 2):
-        f = 0.15915494309189535 * math.exp(i * rate) if i % 8 == 0 else f * step
+        f = 0.15915494309189535 * math.exp(i * rate) if i % 16 == 0 else f * step
         hi_w = f32(f)
         lo_w = f32(f - float(hi_w))
         exact = (Decimal(-2 * i) / d * Decimal(theta).ln()).exp() / two_pi
