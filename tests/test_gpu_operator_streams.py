@@ -180,3 +180,28 @@ def test_older_calls_read_a_freed_temporary_to_its_end(name):
 @pytest.mark.parametrize("name", OLDER)
 def test_older_calls_read_a_released_result_to_its_end(name):
     test_a_released_result_is_read_to_its_end(lambda: older_calls()[name])
+
+
+@pytest.mark.parametrize("make", [rotary_call, cross_call, split_call, grad_call], ids=lambda f: f.__name__)
+def test_a_named_stream_inside_a_capture(make):
+    """A captured graph that forks to the call's stream and joins it again; what the
+    call allocates is the graph's own, and results may be released in it."""
+    call, side = make(), torch.cuda.Stream()
+    want = call(None)
+    call(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        call(side)                              # (released at once)
+        got = call(side)
+        main.wait_stream(side)
+        kept = [t.clone() for t in got]
+    for _ in range(2):
+        for t in kept:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(kept, want))
+    assert cp.last_device_status() == 0
