@@ -43,8 +43,9 @@ def split_call():
 
 def grad_call():
     q, k, v = normal(3, 1, 8, 2048, 128), normal(4, 1, 8, 1024, 128), normal(5, 1, 8, 1024, 128)
+    dout = normal(6, 1, 8, 2048, 128)
     out, lse = cp.cross_attention(q, k, v)
-    return lambda s: list(cp.cross_attention_backward(q, k, v, out, lse, normal(6, 1, 8, 2048, 128), stream=s))
+    return lambda s: list(cp.cross_attention_backward(q, k, v, out, lse, dout, stream=s))
 
 
 CALLS = [rotary_call, rotary_call_one_given, cross_call, split_call, grad_call]
