@@ -396,6 +396,24 @@ bool cross_few(const cpattn_tensor* q, const cpattn_tensor* k) {
   return rows <= 32 || (rows <= 64 && share >= 8);
 }
 
+// Blocks that clusters of `size` of them find room for at once: what is left of an
+// SM group (GPC) stays free, and how many SMs a group has differs between chips.
+// Asked once per device.  Found on one of 152 SMs, sizes 2 to 8: 152 138 144 140 138
+// 105 120 with one block an SM, 304 291 296 290 276 266 288 with two.
+int cluster_room(bool few, int size) {
+  static std::atomic<int> known[64][2][cpattn::kCrossCluster + 1];   // (0: not asked yet)
+  int dev = 0;
+  const bool place = cudaGetDevice(&dev) == cudaSuccess && dev < 64;
+  if (place) {
+    const int n = known[dev][few][size].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+  }
+  const int clusters = few ? cpattn::cross_few_clusters(size) : cpattn::cross_fwd_clusters(size);
+  if (clusters <= 0) return cpattn::sm_count() * (few ? 2 : 1);   // (no device: any split is as good)
+  if (place) known[dev][few][size].store(clusters * size, std::memory_order_relaxed);
+  return clusters * size;
+}
+
 // Parts of the key axis of a forward call: 1 where the query rows fill the
 // GPU, else as many as keep it full.  For few rows one round of two CTAs per SM
 // (64 key heads x 16384 keys: 4 parts 79 us, 8 parts 82, 16 parts 95), each with
@@ -429,13 +447,10 @@ int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
     s -= s % cpattn::kCrossCluster;
     if (s < 3 * cpattn::kCrossCluster && k->shape[2] <= 8192) s = cpattn::kCrossCluster;
   }
-  // what is left of an SM group (GPC) stays free: blocks that clusters of s of
-  // them find room for at once, one block an SM and two, of 152 and 304; a second
-  // round of clusters costs up to half (40 key heads x 8192 keys: 6 parts 28.7
-  // us, 7 parts 41.1)
-  static const int room[2][9] = {{0, 152, 152, 138, 144, 140, 138, 105, 120}, {0, 304, 304, 291, 296, 290, 276, 266, 288}};
+  // a second round of clusters costs up to half (40 key heads x 8192 keys: 6 parts
+  // 28.7 us, 7 parts 41.1)
   if (q->dtype == CPATTN_BF16)
-    while (s > 1 && units * s * 152 > sm * room[cross_few(q, k)][s < 8 ? s : 8]) s -= s > 8 ? 8 : 1;
+    while (s > 1 && units * s > cluster_room(cross_few(q, k), static_cast<int>(s < 8 ? s : 8))) s -= s > 8 ? 8 : 1;
   return s > 1 ? static_cast<int>(s < 65535 ? s : 65535) : 1;
 }
 

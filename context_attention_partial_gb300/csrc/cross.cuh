@@ -75,6 +75,36 @@ cudaError_t cross_run(int64_t blocks, int splits, int threads, size_t smem, cuda
   return launch_behind(kernel, dim3(static_cast<unsigned>(blocks), splits), threads, smem, stream, args...);
 }
 
+// Clusters of `size` blocks of a kernel that the idle current device holds at
+// once; -1 if that cannot be asked (no device).
+template <typename... Params>
+int cross_clusters(void (*kernel)(Params...), dim3 cluster, int threads, size_t smem) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  cudaLaunchConfig_t config = {};
+  config.gridDim = cluster;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster.x;
+  attr.val.clusterDim.y = cluster.y;
+  attr.val.clusterDim.z = cluster.z;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &config) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  return n;
+}
+// The same for the two bf16 forward kernels at D = 128 (one block an SM, and two).
+int cross_fwd_clusters(int size);
+int cross_few_clusters(int size);
+
 // Blocks of a cluster, at most.  bf16 forward calls have p.splits up to it, or a
 // multiple of it: a cluster joins its parts itself, and the workspace gets
 // p.splits / kCrossCluster parts to join.

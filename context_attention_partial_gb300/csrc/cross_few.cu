@@ -354,6 +354,10 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t stream) {
 
 }  // namespace
 
+int cross_few_clusters(int size) {
+  return cross_clusters(cross_few_kernel<128, 1>, dim3(1, size), kThreads, Few<128>::SMEM);
+}
+
 cudaError_t launch_cross_few(int head_dim, const CrossParams& p, cudaStream_t stream) {
   return head_dim == 64 ? launch_typed<64>(p, stream) : launch_typed<128>(p, stream);
 }

@@ -751,6 +751,10 @@ cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
 
 }  // namespace
 
+int cross_fwd_clusters(int size) {
+  return cross_clusters(cross_fwd_kernel<128, false, true>, dim3(size), kThreads, Cfg<128>::SMEM);
+}
+
 cudaError_t launch_cross_fwd(int head_dim, const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const CUtensorMap& tm_o, const CrossParams& p, cudaStream_t stream) {
   // one wave of a single query tile each: two sums a tile
