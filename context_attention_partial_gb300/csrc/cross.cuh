@@ -51,14 +51,21 @@ __device__ __forceinline__ float cross_lse2(float lse) {
 }
 
 // Raises a kernel's dynamic shared-memory limit once per device (bit d of
-// `ready`: device d is set up; the call costs about 5 us of host time).
+// `ready`: device d is set up; the call costs about 5 us of host time).  A kernel
+// that splits its registers between its warps needs exactly `regs` at launch and
+// is refused otherwise.
 template <typename K>
-cudaError_t cross_set_up(K kernel, size_t smem, std::atomic<unsigned long long>& ready) {
+cudaError_t cross_set_up(K kernel, size_t smem, std::atomic<unsigned long long>& ready, int regs = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (bit != 0 && (ready.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  if (regs > 0) {
+    cudaFuncAttributes attr;
+    if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
+    if (attr.numRegs != regs) return cudaErrorInvalidConfiguration;
+  }
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_acq_rel);
   return e;

@@ -979,29 +979,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
 }
-// Once per device and kernel: the register split needs exactly kLaunchRegs at
-// launch (refused otherwise), and the shared-memory limit is raised.
-template <typename K>
-cudaError_t set_up(K kernel, int smem, std::atomic<unsigned long long>& ready) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (bit != 0 && (ready.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
-  cudaFuncAttributes attr;
-  if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
-  if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-  ready.fetch_or(bit, std::memory_order_acq_rel);
-  return cudaSuccess;
-}
-
 template <int D>
 cudaError_t launch_typed(const CrossBwdMaps& m, const CrossParams& p, int64_t partials, cudaStream_t stream) {
   using C = Cfg<D>;
   static std::atomic<unsigned long long> ready_q{0}, ready_kv{0};
-  cudaError_t e = set_up(cross_dq_kernel<D>, C::DQ_SMEM, ready_q);
-  if (e == cudaSuccess) e = set_up(cross_dkv_kernel<D>, C::KV_SMEM, ready_kv);
+  cudaError_t e = cross_set_up(cross_dq_kernel<D>, C::DQ_SMEM, ready_q, kLaunchRegs);
+  if (e == cudaSuccess) e = cross_set_up(cross_dkv_kernel<D>, C::KV_SMEM, ready_kv, kLaunchRegs);
   if (e != cudaSuccess) return e;
   const int64_t sms = sm_count();
   const int64_t units = static_cast<int64_t>(p.batch) * p.heads * ((p.s_q + kBM - 1) / kBM);

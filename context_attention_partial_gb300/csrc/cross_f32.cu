@@ -145,16 +145,6 @@ __device__ __forceinline__ void spread(const float* w, const float* tile, int n,
   }
 }
 
-// 16 bytes to shared memory, or zeros without a read.
-__device__ __forceinline__ void copy16(float* dst, const float* src, bool read) {
-  const int n = read ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// Waits for all but the newest group of this thread's copies.
-__device__ __forceinline__ void copies_wait_older() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
-
 // Requests rows [row0, row0 + ROWS) of one head into a tile of padded rows;
 // rows at or past `end` become zero and are not read (they may hold anything).
 template <int D, int ROWS>
@@ -168,7 +158,7 @@ __device__ __forceinline__ void fill_tile(const CrossParams& p, const CrossTenso
 #pragma unroll 4
   for (int r = 0; r < ROWS; r += STEP) {
     const bool read = row0 + r0 + r < end && CPATTN_IN(t.span, src, 16, p.err);
-    copy16(dst, read ? src : head, read);
+    copy16(smem_addr(dst), read ? src : head, read);
     src += STEP * t.s[2];
     dst += STEP * (D + 4);
   }
@@ -228,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_f32_kernel(co
 #pragma unroll
     for (int f = 0; f < F; ++f) o[i][f] = 0.f;
   }
-  copies_wait_older();
+  copies_wait<1>();
   __syncthreads();
   for (int k0 = begin; k0 < end; k0 += kTileF) {
     const int valid = min(end - k0, kTileF), col = part * 32 + lc;   // this lane's keys: col + 8 j
@@ -266,10 +256,10 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_f32_kernel(co
 #pragma unroll
       for (int x = 0; x < F; ++x) o[i][x] *= f;
     }
-    copies_wait_older();
+    copies_wait<1>();
     __syncthreads();   // (P and V are there)
     spread<D, kWF>(sP + mine * kWF, sV + (part * 8 + lc) * F, (valid + 3) & ~3, o);
-    copies_wait_all();
+    copies_wait<0>();
     __syncthreads();   // (the next K is there, P and V are done with)
     if (k0 + kTileF < end) {
       if (OVER) fill_tile<D, kTileF>(p, p.k, b, hk, k0 + kTileF, end, sK);
@@ -277,12 +267,12 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_f32_kernel(co
       fill_tile<D, kTileF>(p, p.v, b, hk, k0 + kTileF, end, sV);
       copies_commit();
       if (OVER) {
-        copies_wait_older();
+        copies_wait<1>();
         __syncthreads();
       }
     }
   }
-  copies_wait_all();
+  copies_wait<0>();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     l[i] = row_sum(l[i]);
@@ -363,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_f32_dq_kernel
   }
   for (int k0 = 0; k0 < len; k0 += kTile) {
     request(k0 + kTile);
-    copies_wait_older();
+    copies_wait<1>();
     __syncthreads();
     const float* sK = sKV + ((k0 / kTile) & 1) * 2 * kTile * PAD;
     const int valid = min(len - k0, kTile), col = half * 32 + lc;
@@ -393,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1) cross_f32_dq_kernel
     spread<D, kW>(sS + mine * kW, sK + ((warp >> 1) * 8 + lc) * F, (valid + 3) & ~3, dq);
     __syncthreads();   // (this stage may be filled again)
   }
-  copies_wait_all();
+  copies_wait<0>();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = row0 + mine + 4 * i;
@@ -461,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
           if (CPATTN_IN(scores ? p.lse.span : p.ws_span, at, 4, p.err)) stat[j] = scores ? cross_lse2(*at) : *at;
         }
       }
-      copies_wait_older();
+      copies_wait<1>();
       __syncthreads();
       const float* sQ = sQG + ((x - x0) & 1) * 2 * kTile * PAD;
       const float* sG = sQ + kTile * PAD;
@@ -499,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
       spread<D, kW>(sS + mine * kW, sQ + ((warp >> 1) * 8 + lc) * F, n, dk);
       __syncthreads();   // (this stage may be filled again)
     }
-    copies_wait_all();
+    copies_wait<0>();
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

@@ -53,16 +53,6 @@ struct Few {
   static constexpr int SMEM = STAGES * STAGE > JOIN ? STAGES * STAGE : JOIN;
 };
 
-// 16 bytes to shared memory, or zeros without a read
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool read) {
-  const int n = read ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -137,8 +127,8 @@ __global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_consta
         const char* kp = kg_ptr + static_cast<int64_t>(key) * p.k.s[2] * 2;
         const char* vp = vg_ptr + static_cast<int64_t>(key) * p.v.s[2] * 2;
         const bool in = key < k_end;
-        copy16(dst + at, in ? kp : kg_ptr, in && CPATTN_IN(p.k.span, kp, 16, p.err));
-        copy16(dst + kKeys * C::ROW + at, in ? vp : vg_ptr, in && CPATTN_IN(p.v.span, vp, 16, p.err));
+        copy16<true>(dst + at, in ? kp : kg_ptr, in && CPATTN_IN(p.k.span, kp, 16, p.err));
+        copy16<true>(dst + kKeys * C::ROW + at, in ? vp : vg_ptr, in && CPATTN_IN(p.v.span, vp, 16, p.err));
       }
     }
     copies_commit();

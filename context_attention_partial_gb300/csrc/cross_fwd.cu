@@ -726,21 +726,9 @@ cudaError_t launch_typed(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
                          const CUtensorMap& tm_o, const CrossParams& p, cudaStream_t stream) {
   using C = Cfg<D>;
   auto kernel = cross_fwd_kernel<D, PAIR, SPLIT>;
-  // once per device: the register split needs exactly kLaunchRegs at launch
-  // (refused otherwise), and the shared-memory limit is raised
   static std::atomic<unsigned long long> ready{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = cross_set_up(kernel, C::SMEM, ready, kLaunchRegs);
   if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (bit == 0 || (ready.load(std::memory_order_acquire) & bit) == 0) {
-    cudaFuncAttributes attr;
-    if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
-    if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess)
-      return e;
-    ready.fetch_or(bit, std::memory_order_acq_rel);
-  }
   const int64_t units = static_cast<int64_t>(p.batch) * p.heads * p.splits * ((p.s_q + 2 * kBM - 1) / (2 * kBM));
   const int64_t sms = sm_count();
   if (units > 0x7fffffff) return cudaErrorInvalidValue;

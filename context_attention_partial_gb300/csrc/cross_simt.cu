@@ -72,16 +72,6 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// 16 bytes to shared memory, or zeros without a read.
-__device__ __forceinline__ void copy16(float* dst, const float* src, bool read) {
-  const int n = read ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// Waits for all but the newest group of this thread's copies.
-__device__ __forceinline__ void copies_wait_older() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
-
 // Requests rows [row0, row0 + rows) of one head into a tile of padded rows;
 // rows at or past `end` become zero and are not read (they may hold anything).
 template <int D>
@@ -92,7 +82,7 @@ __device__ __forceinline__ void fill_tile(const CrossParams& p, const CrossTenso
     const int r = i / (D / 4), c = (i % (D / 4)) * 4;
     const float* src = head + static_cast<int64_t>(row0 + r) * t.s[2] + c;
     const bool read = row0 + r < end && CPATTN_IN(t.span, src, 16, p.err);
-    copy16(tile + r * stride + c, read ? src : head, read);
+    copy16(smem_addr(tile + r * stride + c), read ? src : head, read);
   }
 }
 
@@ -185,7 +175,7 @@ __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constan
   request(t_begin);   // (with the query rows)
   for (int t = t_begin; t < t_end; ++t) {
     request(t + 1);
-    copies_wait_older();
+    copies_wait<1>();
     __syncthreads();
     const float* sK = sKV + ((t - t_begin) & 1) * 2 * TK * PAD;
     const float* sV = sK + TK * PAD;
@@ -218,7 +208,7 @@ __global__ void __launch_bounds__(W * 32) cross_simt_kernel(const __grid_constan
     spread<D, R, C>(myP, sV + part * T1 * PAD, o);
     __syncthreads();   // (this stage may be filled again)
   }
-  copies_wait_all();
+  copies_wait<0>();
 #pragma unroll
   for (int r = 0; r < R; ++r) l[r] = warp_sum(l[r]);
   if constexpr (KS > 1) {
@@ -403,7 +393,7 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_cons
   request(0);   // (with the query rows)
   for (int k0 = 0; k0 < len; k0 += T1) {
     request(k0 + T1);
-    copies_wait_older();
+    copies_wait<1>();
     __syncthreads();
     const float* sK = sKV + ((k0 / T1) & 1) * 2 * T1 * PAD;
     const float* sV = sK + T1 * PAD;
@@ -422,7 +412,7 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dq_kernel(const __grid_cons
     spread<D, R, C>(myS, sK, dq);
     __syncthreads();   // (this stage may be filled again)
   }
-  copies_wait_all();
+  copies_wait<0>();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int row = row0 + warp * R + r;
@@ -492,7 +482,7 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
           if (CPATTN_IN(p.ws_span, d, 4, p.err)) delta[c] = *d;
         }
       }
-      copies_wait_older();
+      copies_wait<1>();
       __syncthreads();
       const float* sQ = sQG + (x & 1) * 2 * T1 * PAD;
       const float* sG = sQ + T1 * PAD;
@@ -514,7 +504,7 @@ __global__ void __launch_bounds__(W * 32) cross_simt_dkv_kernel(const __grid_con
       spread<D, R, C>(myS, sQ, dk);
       __syncthreads();   // (this stage may be filled again)
     }
-    copies_wait_all();
+    copies_wait<0>();
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
