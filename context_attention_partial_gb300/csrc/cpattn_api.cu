@@ -437,7 +437,7 @@ int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
     units = (q->shape[2] + 255) / 256 * bh;
     if (q->dtype != CPATTN_BF16) {
       units = (q->shape[2] + 63) / 64 * bh;
-      if (!cpattn::cross_f32_rows(units)) units = q->shape[2] > 2 ? (q->shape[2] + 7) / 8 * bh : bh;
+      if (!cpattn::cross_f32_rows(units, k->shape[2] * k->shape[3])) units = q->shape[2] > 2 ? (q->shape[2] + 7) / 8 * bh : bh;
     }
     most = q->dtype != CPATTN_BF16 ? (k->shape[2] + 127) / 128 : k->shape[2] < 1024 ? 1 : (k->shape[2] + 255) / 256;
     want = sm / units;

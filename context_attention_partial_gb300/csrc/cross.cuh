@@ -139,9 +139,9 @@ int cross_backward_parts(int64_t key_units, int64_t steps);
 // `partials` floats into it.
 cudaError_t launch_cross_simt(int head_dim, const CrossParams& p, cudaStream_t stream);
 cudaError_t launch_cross_simt_backward(int head_dim, const CrossParams& p, int64_t partials, cudaStream_t stream);
-// whether fp32 calls with that many 64-row query blocks, or 64 x 64 tiles of dk
-// and dv, take 64-row blocks
-bool cross_f32_rows(int64_t blocks);
+// whether fp32 calls with that many 64-row query blocks, which walk `values`
+// elements of a key head (S_kv D), or 64 x 64 tiles of dk and dv, take 64-row blocks
+bool cross_f32_rows(int64_t blocks, int64_t values);
 bool cross_f32_keys(int64_t tiles);
 // parts of the query axis for key_units 64-key tiles that walk `steps` 64-row
 // query tiles each

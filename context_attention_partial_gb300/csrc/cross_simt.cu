@@ -576,7 +576,7 @@ constexpr size_t simt_smem(int D, int rows, int tile, int weights) {
 template <int D>
 cudaError_t forward_typed(const CrossParams& p, cudaStream_t stream) {
   const int64_t bh = static_cast<int64_t>(p.batch) * p.heads;
-  if (cross_f32_rows(tiles_of(p.s_q, 64) * bh)) return launch_cross_f32(D, p, stream);
+  if (cross_f32_rows(tiles_of(p.s_q, 64) * bh, static_cast<int64_t>(p.s_kv) * D)) return launch_cross_f32(D, p, stream);
   // 8 or 16 rows a block, and for one or two queries 2, the KS warps of each
   // row taking every KS-th tile
   constexpr int KS = D == 64 ? 4 : 2;
@@ -637,13 +637,16 @@ cudaError_t launch_cross_simt_backward(int head_dim, const CrossParams& p, int64
   return head_dim == 64 ? backward_typed<64>(p, partials, stream) : backward_typed<128>(p, partials, stream);
 }
 
-// Against the kernels of this file, us, this / 64-row blocks.  Forward, 512
-// keys x 8 heads at D = 128: 64 queries 24.1 / 24.1 (8 blocks: this kernel),
-// 128 queries 39 / 21, 512 queries 77 / 36; 128 queries x 100 keys x 16 heads
-// at D = 64 11.0 / 12.0.  Gradient (dk, dv), 100 keys as before (64 tiles) 26 /
-// 41, 256 x 512 x 2 heads (64 tiles) 75 / 61, 128 x 512 x 8 heads (128 tiles)
+// Against the kernels of this file, us, this / 64-row blocks.  Forward, 8 heads at
+// D = 128: 64 queries (8 blocks) x 512 keys 23.7 / 20.7, 128 queries (16 blocks) x
+// 512 keys 38.6 / 21.0, x 1500 keys 109.6 / 36.3, x 100 keys 11.9 / 16.3; at D = 64
+// x 512 keys 14.2 / 15.2, x 1500 keys 36.2 / 23.7; 512 queries x 512 keys at D = 128
+// 77 / 36.  Gradient (dk, dv), 128 queries x 100 keys x 16 heads at D = 64 (64 tiles)
+// 26 / 41, 256 x 512 x 2 heads (64 tiles) 75 / 61, 128 x 512 x 8 heads (128 tiles)
 // 99 / 92, 300 x 256 x 16 heads at D = 64 (320 tiles) 84 / 76.
-bool cross_f32_rows(int64_t blocks) { return blocks * 8 >= sm_count(); }
+bool cross_f32_rows(int64_t blocks, int64_t values) {
+  return blocks * 8 >= sm_count() || (blocks * 16 >= sm_count() && values >= 512 * 128);
+}
 bool cross_f32_keys(int64_t tiles) { return tiles * 2 >= sm_count(); }
 
 int cross_f32_parts(int64_t key_units, int64_t steps) {
