@@ -18,7 +18,7 @@
 // A tile row is padded by 16 bytes, so both walks are free of bank conflicts.
 // R = 2, C = 1: the blocks are small, so few rows make many of them; what
 // bounds them is shared memory and the latency of a short walk (one query x 500
-// keys x 16 heads 12.8 us, its gradient 46; 256 queries x 77 keys x 4 heads at
+// keys x 16 heads 10.7 us, its gradient 52; 256 queries x 77 keys x 4 heads at
 // D = 64 6.9, host-bound).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

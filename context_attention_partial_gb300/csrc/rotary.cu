@@ -21,12 +21,13 @@
 // grow with the position: 2^-23.4 found at 2^27, 2^-20.4 at 2^30.
 // (fp64 sines would cost 29 us at 4608 tokens on this GPU's FP64 units.)
 //
-// What bounds it: HBM, each tensor read and written once.  A thread keeps one
-// 16-byte column of one token for a group of heads of all tensors, so its
-// cosines and sines are formed once and stay in registers, and walks the heads
-// with four rows in flight.  Back to back, q and k of 24 heads, bf16, D = 128:
-// 32768 tokens (806 MB) 123 us, 6.5 TB/s; 4608 tokens (113 MB) 22.8 us, 5.0 TB/s,
-// alone 18.7 (the launch before still writes its output back).
+// A thread keeps one 16-byte column of one token for a group of heads of all
+// tensors, so its cosines and sines are formed once and stay in registers, and
+// walks the heads with four rows in flight.  Back to back, q and k of 24 heads,
+// bf16, D = 128: 32768 tokens (806 MB) 123 us, 6.5 TB/s, bound by HBM; 4608 tokens
+// (113 MB, [B, S, H, D]) 22.9 us, 4.9 TB/s, where HBM would take 16.7.  The short
+// call is not bound by HBM: its 576 blocks start and end together, and a thread has
+// no load in flight between one group of four rows and the next.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -315,7 +315,10 @@ cpattn_status cpattn_rotary(int n, const cpattn_tensor* x, const cpattn_tensor* 
  *   workspace: at least cpattn_cross_workspace_bytes(q, k) bytes, 16-byte
  *     aligned, NULL if that is 0: partial outputs of a key axis that is split
  *     (few queries) and joined.  Calls that may overlap need their own.
- * fp32 inputs are computed in fp32 (no tf32 rounding).  Strides of extents
+ * fp32 inputs are computed in fp32 (no tf32 rounding).  bf16 inputs: scores, sums
+ * and lse are fp32; each weight exp(s - max) is rounded to bf16 once for its product
+ * with v, and out once: out is off by up to 2^-8 (|out| + sum_j p_j |v_j|), some
+ * 2.3e-3 of out's size for normal inputs.  Strides of extents
  * above 1 must be positive; outputs may not overlap any other buffer.
  * B * H * S_q = 0 is a no-op.
  */
@@ -334,7 +337,10 @@ size_t cpattn_cross_workspace_bytes(const cpattn_tensor* q, const cpattn_tensor*
  *     dv sum over the query heads that share a key head; rows past a sequence's
  *     length get 0; dq is 0 for a sequence without keys, dq and dk are exactly 0
  *     for one with a single key.  A row with lse -inf has no weights.
- * Every sum has one owner and a fixed order: equal calls give equal bits.
+ * Every sum has one owner and a fixed order: equal calls give equal bits.  bf16
+ * inputs: p and ds are rounded to bf16 once each for their products, the results
+ * once, and delta = sum(dout * out) uses out as it was rounded: some 2.4e-3 of
+ * the gradients' size for normal inputs, up to 3.2e-3 with few keys.
  *   workspace: at least cpattn_cross_backward_workspace_bytes(q, k) bytes,
  *     16-byte aligned.
  * Other arguments, layouts and errors as cpattn_cross_attention.  S_q = 0

@@ -79,3 +79,27 @@ def test_an_autograd_function_around_the_calls():
     pair = lambda t: t.unflatten(-1, (32, 2)).sum(-1, keepdim=True).expand(*t.shape[:-1], 32, 2).flatten(-2)
     limit = pair(tol) + plain.rotary_tolerance(turned, mag, torch.float32) + 2.0 ** -24 * pair(value.abs())
     assert plain.worst(leaves[0].grad, turned, limit) <= 1.0
+
+
+def test_readme_blocks_run_as_they_stand():
+    """The README's Python blocks, with tensors of the kind it names."""
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    assert len(blocks) >= 2
+    g = torch.Generator("cpu").manual_seed(91)
+    bf = lambda h, s: torch.randn(2, h, s, 128, generator=g).bfloat16().to(DEV)
+    have = dict(cp=cp, q=bf(4, 90), k=bf(4, 90), v=bf(4, 90), text_k=bf(2, 77), text_v=bf(2, 77), dy=bf(4, 90),
+                positions=torch.rand(90, 3, generator=g).to(DEV) * 30, n=torch.tensor([77, 20], dtype=torch.int32, device=DEV))
+    for block in blocks:
+        names = dict(have)
+        exec(block, names)
+        assert names["y"].shape == have["q"].shape and torch.isfinite(names["y"].float()).all()
+        if "dq" in names:
+            want = plain.cross(names["rq"], names["text_k"], names["text_v"], (77, 20), dout=names["dy"])
+            for name, got in (("out", names["y"]), ("lse", names["lse"]), ("dq", names["drq"]), ("dk", names["dk"]),
+                              ("dv", names["dv"])):
+                assert plain.worst(got, *want[name]) <= 1.0
+            turned, mag = plain.rotary(names["drq"], names["positions"], (16, 56, 56), inverse=True)
+            assert plain.worst(names["dq"], turned, plain.rotary_tolerance(turned, mag, torch.bfloat16)) <= 1.0
