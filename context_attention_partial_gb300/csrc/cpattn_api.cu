@@ -409,8 +409,8 @@ int cluster_room(bool few, int size) {
     if (n > 0) return n;
   }
   const int clusters = few ? cpattn::cross_few_clusters(size) : cpattn::cross_fwd_clusters(size);
-  if (clusters <= 0) return cpattn::sm_count() * (few ? 2 : 1);   // (no device: any split is as good)
-  if (place) known[dev][few][size].store(clusters * size, std::memory_order_relaxed);
+  if (clusters < 0) return cpattn::sm_count() * (few ? 2 : 1);   // (no device: any split is as good)
+  if (place && clusters > 0) known[dev][few][size].store(clusters * size, std::memory_order_relaxed);
   return clusters * size;
 }
 
@@ -437,7 +437,8 @@ int cross_splits(const cpattn_tensor* q, const cpattn_tensor* k) {
     units = (q->shape[2] + 255) / 256 * bh;
     if (q->dtype != CPATTN_BF16) {
       units = (q->shape[2] + 63) / 64 * bh;
-      if (!cpattn::cross_f32_rows(units, k->shape[2] * k->shape[3])) units = q->shape[2] > 2 ? (q->shape[2] + 7) / 8 * bh : bh;
+      if (!cpattn::cross_f32_rows(units, k->shape[2] * k->shape[3]))
+        units = q->shape[2] > 2 ? (q->shape[2] + 7) / 8 * bh : bh;
     }
     most = q->dtype != CPATTN_BF16 ? (k->shape[2] + 127) / 128 : k->shape[2] < 1024 ? 1 : (k->shape[2] + 255) / 256;
     want = sm / units;
