@@ -455,14 +455,18 @@ def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float =
     return results[0] if single else results
 
 
+def _cross_bytes(entry, q: torch.Tensor, k: torch.Tensor) -> int:
+    """A workspace's size on q's device: key parts depend on its SMs."""
+    with torch.cuda.device(q.device if q.is_cuda else -1):
+        return int(entry(describe(0, _code(q), q.shape, q.stride()), describe(0, _code(k), k.shape, k.stride())))
+
+
 def cross_workspace_bytes(q: torch.Tensor, k: torch.Tensor) -> int:
-    return int(_lib.load().cpattn_cross_workspace_bytes(describe(0, _code(q), q.shape, q.stride()),
-                                                        describe(0, _code(k), k.shape, k.stride())))
+    return _cross_bytes(_lib.load().cpattn_cross_workspace_bytes, q, k)
 
 
 def cross_backward_workspace_bytes(q: torch.Tensor, k: torch.Tensor) -> int:
-    return int(_lib.load().cpattn_cross_backward_workspace_bytes(
-        describe(0, _code(q), q.shape, q.stride()), describe(0, _code(k), k.shape, k.stride())))
+    return _cross_bytes(_lib.load().cpattn_cross_backward_workspace_bytes, q, k)
 
 
 def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -473,7 +477,8 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Attention of q [B,H,S_q,D] to an encoder's states k, v [B,H_kv,S_kv,D]
     (cpattn_cross_attention): H_kv divides H; kv_lengths (int32 [B]) gives each
     sequence's valid keys, a sequence without any gives (0, -inf).  Inputs may be
-    broadcast views (they are copied for the call).  No autograd graph is recorded: ``cross_attention_backward`` is its gradient.
+    broadcast views (they are copied for the call).  No autograd graph is
+    recorded: ``cross_attention_backward`` is its gradient.
     Returns (out [B,H,S_q,D] in q's dtype, lse f32 [B,H,S_q])."""
     at = _lib.load().addresses
     status, o, l = _lib.binding().cross(at["cross_attention"], at["cross_workspace_bytes"], q, k, v, kv_lengths,

@@ -326,7 +326,8 @@ cpattn_status cpattn_cross_attention(const cpattn_tensor* q, const cpattn_tensor
                                      const cpattn_tensor* v, const cpattn_tensor* kv_lengths,
                                      float scale, cpattn_tensor* out, cpattn_tensor* lse,
                                      void* workspace, size_t workspace_bytes, void* stream);
-/* 0 also for a descriptor that the call would refuse. */
+/* For the current device, like the call.  0 also for a descriptor that the call
+ * would refuse. */
 size_t cpattn_cross_workspace_bytes(const cpattn_tensor* q, const cpattn_tensor* k);
 
 /*

@@ -186,3 +186,12 @@ def test_rotary_angle_arithmetic(d, theta):
             off = Decimal(float(turns)) - Decimal(float(pos)) * exact
             worst = max(worst, abs(off - off.to_integral_value()))
     assert worst < Decimal(2) ** -23
+
+
+def test_workspace_sizes_without_a_device():
+    """The sizes need no GPU and no CUDA tensor: shapes say all."""
+    q, k = torch.zeros(1, 2, 1, 128).bfloat16(), torch.zeros(1, 2, 9000, 128).bfloat16()
+    assert cp.cross_workspace_bytes(q, k) == cp.load_library().cpattn_cross_workspace_bytes(
+        t((1, 2, 1, 128)), t((1, 2, 9000, 128))) > 0
+    assert cp.cross_backward_workspace_bytes(q, k) >= 2 * 4
+    assert cp.cross_workspace_bytes(torch.empty(1, 2, 1, 96, device="meta").bfloat16(), k) == 0
