@@ -56,11 +56,12 @@ class OracleError(ValueError):
 
 
 def build(force: bool = False) -> str:
-    """Compile the C oracle with gcc (IEEE double, OpenMP)."""
+    """Compile the C oracle with gcc (IEEE double, every product rounded: the same
+    results on machines whose compiler would fuse them; OpenMP)."""
     if force or not os.path.exists(_LIB_PATH) or (
-            os.path.getmtime(_LIB_PATH) < os.path.getmtime(_SRC)):
+            os.path.getmtime(_LIB_PATH) < max(map(os.path.getmtime, (_SRC, __file__)))):
         tmp = _LIB_PATH + f".{os.getpid()}.tmp"
-        subprocess.run(["gcc", "-O2", "-fopenmp", "-fPIC", "-shared",
+        subprocess.run(["gcc", "-O2", "-ffp-contract=off", "-fopenmp", "-fPIC", "-shared",
                         "-fno-fast-math", "-Wall", "-o", tmp, _SRC, "-lm"],
                        check=True)
         os.replace(tmp, _LIB_PATH)
@@ -122,7 +123,7 @@ def compile_variant(source_text: str, out_path: str) -> str:
     src = out_path + ".c"
     with open(src, "w") as f:
         f.write(source_text)
-    subprocess.run(["gcc", "-O2", "-fopenmp", "-fPIC", "-shared", "-fno-fast-math",
+    subprocess.run(["gcc", "-O2", "-ffp-contract=off", "-fopenmp", "-fPIC", "-shared", "-fno-fast-math",
                     "-o", out_path, src, "-lm"], check=True)
     return out_path
 
