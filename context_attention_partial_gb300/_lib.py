@@ -30,6 +30,8 @@ EXPORTS = (
     "cpattn_ulysses_anything_permute_batch", "cpattn_is_check_build", "cpattn_set_check_shrink",
     "cpattn_rotary", "cpattn_cross_attention", "cpattn_cross_workspace_bytes",
     "cpattn_cross_attention_backward", "cpattn_cross_backward_workspace_bytes",
+    "cpattn_norm_rotary", "cpattn_norm_rotary_backward", "cpattn_norm_rotary_backward_workspace_bytes",
+    "cpattn_cache_append", "cpattn_cache_attention", "cpattn_cache_attention_workspace_bytes",
 )
 
 
@@ -93,10 +95,21 @@ def bind(path: str):
                                            vp]
     lib.cpattn_cross_attention_backward.argtypes = [P, P, P, P, P, P, P, ctypes.c_float, P, P, P,
                                                     vp, ctypes.c_size_t, vp]
+    axes = [i32, ctypes.POINTER(ctypes.c_int32), ctypes.c_double, i32]   # axes, axis_dims, theta, interleaved
+    lib.cpattn_norm_rotary.argtypes = [i32, P, P, ctypes.c_float, P, *axes, P, vp]
+    lib.cpattn_norm_rotary_backward.argtypes = [i32, P, P, ctypes.c_float, P, *axes, P, P, P, vp,
+                                                ctypes.c_size_t, vp]
+    lib.cpattn_norm_rotary_backward_workspace_bytes.argtypes = [i32, P]
+    lib.cpattn_norm_rotary_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.cpattn_cache_append.argtypes = [P, P, P, P, P, ctypes.c_float, P, *axes, P, P, P, P, P, P, vp]
+    lib.cpattn_cache_attention.argtypes = [P] * 7 + [ctypes.c_float, P, P, vp, ctypes.c_size_t, vp]
+    lib.cpattn_cache_attention_workspace_bytes.argtypes = [P, P, P]
+    lib.cpattn_cache_attention_workspace_bytes.restype = ctypes.c_size_t
     for name in ("cpattn_cross_workspace_bytes", "cpattn_cross_backward_workspace_bytes"):
         getattr(lib, name).argtypes = [P, P]
         getattr(lib, name).restype = ctypes.c_size_t
-    for name in ("cpattn_rotary", "cpattn_cross_attention", "cpattn_cross_attention_backward",
+    for name in ("cpattn_norm_rotary", "cpattn_norm_rotary_backward", "cpattn_cache_append",
+                 "cpattn_cache_attention", "cpattn_rotary", "cpattn_cross_attention", "cpattn_cross_attention_backward",
                  "cpattn_partial", "cpattn_merge", "cpattn_ring", "cpattn_ulysses_permute",
                  "cpattn_last_device_status", "cpattn_ring_noalloc", "cpattn_ring_causal",
                  "cpattn_ulysses_anything_permute", "cpattn_ulysses_anything_attention",
@@ -105,7 +118,9 @@ def bind(path: str):
     # entry points the binding module calls by address
     lib.addresses = {name: ctypes.cast(getattr(lib, "cpattn_" + name), vp).value for name in (
         "rotary", "cross_attention", "cross_workspace_bytes", "cross_attention_backward",
-        "cross_backward_workspace_bytes")}
+        "cross_backward_workspace_bytes", "norm_rotary", "norm_rotary_backward",
+        "norm_rotary_backward_workspace_bytes", "cache_append", "cache_attention",
+        "cache_attention_workspace_bytes")}
     return lib
 
 

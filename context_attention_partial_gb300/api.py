@@ -455,6 +455,106 @@ def rotary(xs, positions: torch.Tensor, axes_dims: Sequence[int], theta: float =
     return results[0] if single else results
 
 
+def norm_rotary(xs, weights, positions: torch.Tensor, axes_dims: Sequence[int], eps: float = 1e-6,
+                theta: float = 10000.0, interleaved: bool = True, outs=None,
+                stream: Optional[torch.cuda.Stream] = None) -> Union[torch.Tensor, list]:
+    """Norms of each head, then rotary positions, in one pass (cpattn_norm_rotary) on a
+    tensor or up to 4 tensors [B,H_i,S,D]: x / sqrt(mean(x^2) + eps) * weight, turned as
+    ``rotary`` turns.  weights: None (ones), or a tensor [D] for each of xs (float32 or
+    bfloat16); the other arguments as in ``rotary``.  outs may be xs (in place).  No
+    autograd graph is recorded: ``norm_rotary_backward`` is its gradient.
+    Returns a tensor for a tensor, else a list."""
+    lib = _lib.load()
+    single = isinstance(xs, torch.Tensor)
+    if single:
+        xs, weights, outs = ([t] if t is not None else None for t in (xs, weights, outs))
+    status, results, *_ = _lib.binding().norm_rotary(lib.addresses["norm_rotary"], xs, weights, eps, positions, axes_dims,
+                                                     theta, interleaved, outs, _handle(stream, positions))
+    check(status, "cpattn_norm_rotary")
+    return results[0] if single else results
+
+
+def norm_rotary_backward_workspace_bytes(xs) -> int:
+    """The workspace's size on the device of xs (a tensor or a list): its parts depend
+    on the device's SMs."""
+    xs = [xs] if isinstance(xs, torch.Tensor) else xs
+    descs = (_lib.CTensor * len(xs))(*(describe(0, _code(x), x.shape, x.stride()) for x in xs))
+    with torch.cuda.device(xs[0].device if xs[0].is_cuda else -1):
+        return int(_lib.load().cpattn_norm_rotary_backward_workspace_bytes(len(xs), descs))
+
+
+def norm_rotary_backward(xs, weights, positions: torch.Tensor, axes_dims: Sequence[int], dys, eps: float = 1e-6,
+                         theta: float = 10000.0, interleaved: bool = True, dxs=None, dweights=None,
+                         workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Gradient of ``norm_rotary`` (cpattn_norm_rotary_backward): its arguments, and dys,
+    the gradients of its results.  Returns (dxs, dweights): a tensor or list each like xs
+    and weights (dweights None if weights is); a weight's gradient is summed over every
+    token and head, in its type.  dxs may be xs or dys (in place)."""
+    at = _lib.load().addresses
+    single = isinstance(xs, torch.Tensor)
+    if single:
+        xs, weights, dys, dxs, dweights = ([t] if t is not None else None for t in (xs, weights, dys, dxs, dweights))
+    status, dx, dw = _lib.binding().norm_rotary_backward(
+        at["norm_rotary_backward"], at["norm_rotary_backward_workspace_bytes"], xs, weights, eps, positions, axes_dims,
+        theta, interleaved, dys, dxs, dweights, workspace, _handle(stream, positions))
+    check(status, "cpattn_norm_rotary_backward")
+    return (dx[0], dw[0] if dw is not None else None) if single else (dx, dw)
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,
+                 page_table: torch.Tensor, lengths: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                 axes_dims: Sequence[int] = (), q: Optional[torch.Tensor] = None,
+                 counts: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                 q_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, theta: float = 10000.0,
+                 interleaved: bool = True, q_out: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """A step's keys and values k, v [B,H_kv,S,D] to a paged cache, in place, and its
+    queries q [B,H,S,D], in one launch (cpattn_cache_append).  key_pages, value_pages
+    [P,H_kv,R,D] (R rows a page, 16 to 1024, a power of two); page_table int32 [B,W]:
+    the token at place j of sequence b is row j % R of page page_table[b, j // R];
+    lengths int32 [B]: tokens of each sequence before this step's; counts int32 [B]: how
+    many of the S tokens a sequence has (None: all).  k and q are normed with weight and
+    q_weight [D] as ``norm_rotary`` does (None: no norm) and turned to positions f32
+    [S,A] or [B,S,A] as ``rotary`` does (None: not turned); v is copied.  Tokens from
+    counts[b] on are not written.  Returns the queries (q_out may be q), or None."""
+    lib = _lib.load()
+    status, out = _lib.binding().cache_append(
+        lib.addresses["cache_append"], k, v, key_pages, value_pages, page_table, lengths, positions, axes_dims, q, counts,
+        weight, q_weight, eps, theta, interleaved, q_out, _handle(stream, k))
+    check(status, "cpattn_cache_append")
+    return out
+
+
+def cache_attention_workspace_bytes(q: torch.Tensor, key_pages: torch.Tensor, page_table: torch.Tensor) -> int:
+    """The workspace's size on q's device: key parts depend on its SMs."""
+    with torch.cuda.device(q.device if q.is_cuda else -1):
+        return int(_lib.load().cpattn_cache_attention_workspace_bytes(
+            *(describe(0, code, x.shape, x.stride()) for x, code in
+              ((q, _code(q)), (key_pages, _code(key_pages)), (page_table, _lib.I32)))))
+
+
+def cache_attention(q: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor, page_table: torch.Tensor,
+                    lengths: torch.Tensor, parents: Optional[torch.Tensor] = None,
+                    counts: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of a step's queries q [B,H,S,D] to their sequences' paged caches, which
+    hold the step's keys and values already (cpattn_cache_attention; the cache and
+    counts as in ``cache_append``, lengths the same tensor as there).  Query i sees the
+    lengths[b] cached tokens and, of the step's own, a chain's up to i (parents None),
+    or in a tree of drafts i, parents[b,i], and so on up (int32 [B,S], S at most 256,
+    -1: none).  H_kv divides H.  Queries from counts[b] on give (0, -inf).  No autograd
+    graph is recorded, and there is no gradient.
+    Returns (out [B,H,S,D] in q's dtype, lse f32 [B,H,S])."""
+    at = _lib.load().addresses
+    status, o, l = _lib.binding().cache_attention(
+        at["cache_attention"], at["cache_attention_workspace_bytes"], q, key_pages, value_pages, page_table, lengths,
+        parents, counts, _scale(scale), out, lse, workspace, _handle(stream, q))
+    check(status, "cpattn_cache_attention")
+    return o, l
+
+
 def _cross_bytes(entry, q: torch.Tensor, k: torch.Tensor) -> int:
     """A workspace's size on q's device: key parts depend on its SMs."""
     with torch.cuda.device(q.device if q.is_cuda else -1):
@@ -523,4 +623,6 @@ __all__ = ["partial", "merge", "ring", "ring_workspace_bytes", "ring_noalloc", "
            "ring_noalloc_max_workspace_bytes", "ulysses_permute", "unified_attention",
            "ulysses_attention", "grouped_as_bhsd", "last_device_status", "set_wait_timeout_ns",
            "rotary", "cross_attention", "cross_attention_backward", "cross_workspace_bytes",
-           "cross_backward_workspace_bytes", "CpattnError"]
+           "cross_backward_workspace_bytes", "norm_rotary", "norm_rotary_backward",
+           "norm_rotary_backward_workspace_bytes", "cache_append", "cache_attention",
+           "cache_attention_workspace_bytes", "CpattnError"]

@@ -1,0 +1,442 @@
+// cache.cuh -- the paged key / value cache: where a sequence's tokens are, and the
+// parameters of the attention to it (not part of the public ABI).
+#pragma once
+#include "cross.cuh"
+#include "internal.h"
+#include "tile_ops.cuh"
+
+namespace cpattn {
+
+struct CachePlace {
+  int64_t page;
+  int row;
+  bool valid;
+};
+
+// Tokens of sequence b before this call's, brought into [0, width * page size], and
+// its new ones, into [0, most].
+__device__ __forceinline__ int cache_length(const PageTable& c, int b, unsigned int* err) {
+  const int32_t* at = c.lengths + b;
+  const int n = CPATTN_IN(c.lengths_span, at, 4, err) ? *at : 0;
+  const int64_t room = static_cast<int64_t>(c.width) << c.shift;
+  return max(0, static_cast<int>(min(static_cast<int64_t>(n), room)));
+}
+__device__ __forceinline__ int cache_count(const PageTable& c, int b, int most, unsigned int* err) {
+  if (c.counts == nullptr) return most;
+  const int32_t* at = c.counts + b;
+  const int n = CPATTN_IN(c.counts_span, at, 4, err) ? *at : 0;
+  return max(0, min(n, most));
+}
+
+// The page of place `at` (a key's number within its sequence) of sequence b; -1, and
+// the error word says so, where the table has none that the pool has.
+__device__ __forceinline__ int cache_page(const PageTable& c, int b, int64_t at, unsigned int* err) {
+  const int64_t i = at >> c.shift;
+  int page = -1;
+  if (i < c.width) {
+    const int32_t* from = c.table + b * c.stride + i;
+    if (CPATTN_IN(c.table_span, from, 4, err)) page = *from;
+  }
+  if (page >= 0 && page < c.pages) return page;
+  atomicOr(err, kErrBounds);
+  return -1;
+}
+
+// Where new token i of sequence b goes (not valid: nowhere).
+__device__ __forceinline__ CachePlace cache_place(const PageTable& c, int b, int i, int most, unsigned int* err) {
+  CachePlace p = {0, 0, false};
+  if (i >= cache_count(c, b, most, err)) return p;
+  const int64_t at = static_cast<int64_t>(cache_length(c, b, err)) + i;
+  const int page = cache_page(c, b, at, err);
+  if (page < 0) return p;
+  p.page = page;
+  p.row = static_cast<int>(at & ((1 << c.shift) - 1));
+  p.valid = true;
+  return p;
+}
+
+// ------------------------------------------------------------- attention
+// S_q new tokens of each sequence against its cache, which holds them already, in
+// the places behind lengths[b].  A row is a (token, query head) pair of those that
+// share a key head, row = token * share + head % share; a row tile is R of them.
+struct CacheParams {
+  CrossTensor q, out, lse;    // [B, H, S_q, D], lse [B, H, S_q]
+  CrossTensor k, v;           // pages: strides (page, head, row of the page)
+  PageTable cache;
+  const int32_t* parents;     // [B, S_q], rows `parents_stride` apart, or nullptr: a chain
+  int64_t parents_stride;
+  Span parents_span;
+  float* ws;                  // parts of units, see CacheWalk
+  Span ws_span;
+  int batch, heads, kv_heads, s_q;
+  int row_tiles;              // of a key head
+  int split;                  // whether units are split over blocks (see CacheWalk)
+  float scale_log2;           // softmax scale times log2(e)
+  unsigned long long timeout_ns;
+  int fault_skip_kv;          // testing: the producer issues no copies
+  unsigned int* err;
+};
+
+// Key tiles that a block takes at least before another one shares its work.
+constexpr int kCacheMinTiles = 3;
+// Units a block above which none are split: then a round of whole units is at most
+// an eighth of the call, and the tables that a split needs would be long.
+constexpr int kCacheWholeUnits = 8;
+
+// A piece of work: key tiles t0 .. t1 of row tile rt of (b, hk), which has `tiles`.
+struct CachePiece {
+  int b, hk, rt;
+  int t0, t1, tiles;
+  int len, count;             // the sequence's cached and new tokens
+  __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// Deals the key tiles out to the blocks, evenly, whatever the lengths are.  All (row
+// tile, key head) units of all sequences stand in a line, b slowest, then row tile,
+// then key head; block c takes the c-th of `blocks` equal stretches of the line's key
+// tiles, so its pieces are the end of a unit, whole units, and the beginning of one.
+// A piece that is not a whole unit goes to the workspace: slot 0 of the block if it
+// begins inside its unit, slot 1 if it only ends there; the join kernel finds a
+// unit's parts by the same arithmetic.  Not split: whole units, c, c + blocks, ...
+// R: rows of a row tile, KT: keys of a key tile.  Whole warps.
+template <int R, int KT>
+struct CacheWalk {
+  long long total, pos, end;  // tiles of the line; of this block: the next, one past the last
+  long long base;             // of pair x: its first
+  int blocks, x, pairs;       // pair: (b, row tile)
+
+  // Key tiles of pair x.
+  __device__ static int tiles_of(const CacheParams& p, int x, int* len, int* count) {
+    const int b = x / p.row_tiles, rt = x - b * p.row_tiles, share = p.heads / p.kv_heads;
+    const int n = cache_count(p.cache, b, p.s_q, p.err);
+    *len = cache_length(p.cache, b, p.err);
+    *count = n;
+    const int first = rt * R / share;
+    if (first >= n) return 0;   // (no row has a token)
+    // a chain's rows see nothing past their last token
+    const int last = p.parents != nullptr ? n - 1 : min(n - 1, (rt * R + R - 1) / share);
+    return (*len + last + KT) / KT;
+  }
+  __device__ static long long warp_sum(long long v) {
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+  }
+  __device__ long long begin_of(long long c) const { return total * c / blocks; }
+  // Moves x and base to the pair that holds tile `at` of the line (at < total).
+  __device__ void find(const CacheParams& p, long long at) {
+    const int lane = threadIdx.x % 32;
+    base = 0;
+    for (int x0 = 0; x0 < pairs; x0 += 32) {
+      int len, count;
+      const long long w = x0 + lane < pairs ? static_cast<long long>(tiles_of(p, x0 + lane, &len, &count)) * p.kv_heads : 0;
+      long long sum = w;
+#pragma unroll
+      for (int m = 1; m < 32; m *= 2) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, m);
+        if (lane >= m) sum += y;
+      }
+      const unsigned behind = __ballot_sync(0xffffffffu, at < base + sum);
+      if (behind != 0) {
+        const int i = __ffs(behind) - 1;
+        x = x0 + i;
+        base += __shfl_sync(0xffffffffu, sum - w, i);
+        return;
+      }
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    x = pairs;
+  }
+  __device__ void measure(const CacheParams& p, int most) {   // total and blocks
+    pairs = p.batch * p.row_tiles;
+    total = 0;
+    for (int i = threadIdx.x % 32; i < pairs; i += 32) {
+      int len, count;
+      total += static_cast<long long>(tiles_of(p, i, &len, &count)) * p.kv_heads;
+    }
+    total = warp_sum(total);
+    const long long most_blocks = (total + kCacheMinTiles - 1) / kCacheMinTiles;
+    blocks = static_cast<int>(most_blocks < 1 ? 1 : most_blocks < most ? most_blocks : most);
+  }
+  __device__ void start(const CacheParams& p) {
+    pos = end = base = 0;
+    if (p.split) {
+      measure(p, gridDim.x);
+      if (blockIdx.x >= blocks || total == 0) return;
+      pos = begin_of(blockIdx.x);
+      end = begin_of(blockIdx.x + 1);
+      find(p, pos);
+    } else {
+      pos = blockIdx.x;
+      end = static_cast<long long>(p.batch) * p.row_tiles * p.kv_heads;
+    }
+  }
+  // The next piece with keys; false: no more.
+  __device__ bool next(const CacheParams& p, CachePiece& w) {
+    while (pos < end) {
+      if (!p.split) {
+        w.hk = static_cast<int>(pos % p.kv_heads);
+        x = static_cast<int>(pos / p.kv_heads);
+        pos += gridDim.x;
+        w.tiles = tiles_of(p, x, &w.len, &w.count);
+        if (w.tiles == 0) continue;
+        w.t0 = 0;
+        w.t1 = w.tiles;
+      } else {
+        w.tiles = tiles_of(p, x, &w.len, &w.count);
+        const long long off = pos - base, all = static_cast<long long>(w.tiles) * p.kv_heads;
+        if (off >= all) {
+          base += all;
+          ++x;
+          continue;
+        }
+        w.hk = static_cast<int>(off / w.tiles);
+        w.t0 = static_cast<int>(off - static_cast<long long>(w.hk) * w.tiles);
+        const long long left = end - pos;
+        w.t1 = left < w.tiles - w.t0 ? w.t0 + static_cast<int>(left) : w.tiles;
+        pos += w.t1 - w.t0;
+      }
+      w.b = x / p.row_tiles;
+      w.rt = x - w.b * p.row_tiles;
+      return true;
+    }
+    return false;
+  }
+};
+
+// A unit without keys: (0, -inf) for its rows that exist.  All threads of the block,
+// which share the units without keys out by their number.
+template <typename T, int R, int KT, int D>
+__device__ __forceinline__ void cache_empty_units(const CacheParams& p) {
+  const int share = p.heads / p.kv_heads, rows = p.s_q * share;
+  const int64_t units = static_cast<int64_t>(p.batch) * p.row_tiles * p.kv_heads;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int x = static_cast<int>(u / p.kv_heads), hk = static_cast<int>(u % p.kv_heads);
+    int len, count;
+    if (CacheWalk<R, KT>::tiles_of(p, x, &len, &count) != 0) continue;
+    const int b = x / p.row_tiles, rt = x - b * p.row_tiles;
+    constexpr int C = D * sizeof(T) / 16;
+    for (int i = threadIdx.x; i < R * C; i += blockDim.x) {
+      const int row = rt * R + i / C;
+      if (row >= rows) break;
+      const int token = row / share, h = hk * share + row % share;
+      T* dst = static_cast<T*>(p.out.data) + b * p.out.s[0] + h * p.out.s[1] + token * p.out.s[2] + i % C * (16 / sizeof(T));
+      if (CPATTN_IN(p.out.span, dst, 16, p.err)) *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+      float* dl = static_cast<float*>(p.lse.data) + b * p.lse.s[0] + h * p.lse.s[1] + token * p.lse.s[2];
+      if (i % C == 0 && CPATTN_IN(p.lse.span, dl, 4, p.err)) *dl = -INFINITY;
+    }
+  }
+}
+
+// A tree's paths: `words` [R][kTreeWords], bit j of row r's: draft j is the row's token
+// or above it.  A parent that is not before its draft is none (so a walk ends).
+// `parents`: S_q ints of shared memory, loaded.  Thread t of `threads` takes rows t, ...
+constexpr int kTreeWords = CPATTN_MAX_TREE / 32;
+template <int R>
+__device__ __forceinline__ void tree_paths(const CacheParams& p, const int* parents, int rt, int t, int threads,
+                                           uint32_t* words) {
+  const int share = p.heads / p.kv_heads;
+  for (int r = t; r < R; r += threads) {
+    uint32_t bits[kTreeWords] = {};
+    int j = (rt * R + r) / share;
+    if (j >= p.s_q) j = -1;
+    while (j >= 0) {
+#pragma unroll
+      for (int w = 0; w < kTreeWords; ++w)
+        if (j / 32 == w) bits[w] |= 1u << (j % 32);
+      const int up = parents[j];
+      j = up < j ? up : -1;
+    }
+#pragma unroll
+    for (int w = 0; w < kTreeWords; ++w) words[r * kTreeWords + w] = bits[w];
+  }
+}
+
+// What a row sees of the keys start .. start + 63, as bits.  len: the sequence's
+// cached tokens; i: the row's token (below its count).
+__device__ __forceinline__ unsigned long long low_bits(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+__device__ __forceinline__ unsigned long long chain_window(int len, int i, int start) { return low_bits(len + i + 1 - start); }
+__device__ __forceinline__ unsigned long long tree_window(const uint32_t* words, int len, int start) {
+  const int cached = len - start;   // of the window
+  if (cached >= 64) return ~0ull;
+  auto word64 = [&](int w) {        // drafts 32 w .. 32 w + 63
+    const unsigned long long lo = w < kTreeWords ? words[w] : 0u, hi = w + 1 < kTreeWords ? words[w + 1] : 0u;
+    return lo | hi << 32;
+  };
+  if (cached >= 0) return low_bits(cached) | (cached == 0 ? word64(0) : word64(0) << cached);
+  const int j = -cached, w = j / 32, o = j % 32;
+  unsigned long long bits = word64(w) >> o;
+  if (o != 0 && w + 2 < kTreeWords) bits |= static_cast<unsigned long long>(words[w + 2]) << (64 - o);
+  return bits;
+}
+
+// Eight bf16 values: those that are not finite become 0; whether there were any.
+__device__ __forceinline__ bool clear_unfinite(uint4* at) {
+  uint4 v = *at;
+  uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = (x[i] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u, hi = (x[i] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+    found |= (lo | hi) != 0;
+    x[i] &= ~(lo | hi);
+  }
+  if (found) *at = v;
+  return found;
+}
+// Four fp32 values likewise.
+__device__ __forceinline__ bool clear_unfinite(float4* at) {
+  float4 v = *at;
+  float* x = reinterpret_cast<float*>(&v);
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (!isfinite(x[i])) {
+      x[i] = 0.f;
+      found = true;
+    }
+  if (found) *at = v;
+  return found;
+}
+
+// Adds to features d .. d + 3 of a row of token i the values that are not finite, of
+// the drafts with keys k0 .. k1 - 1 that it sees (paths: its path, nullptr for a chain).
+template <typename T>
+__device__ __noinline__ void add_unfinite(const CacheParams& p, const CachePiece& w, int i, const uint32_t* path, int k0,
+                                          int k1, int d, float4& sum) {
+  for (int key = max(k0, w.len); key < k1; ++key) {
+    const int j = key - w.len;
+    if (path != nullptr ? !((path[j / 32] >> (j % 32)) & 1u) : j > i) continue;
+    const int page = cache_page(p.cache, w.b, key, p.err);
+    if (page < 0) continue;
+    const T* from = static_cast<const T*>(p.v.data) + page * p.v.s[0] + w.hk * p.v.s[1] +
+                    (key & ((1 << p.cache.shift) - 1)) * p.v.s[2] + d;
+    if (!CPATTN_IN(p.v.span, from, 4 * sizeof(T), p.err)) continue;
+    float* x = reinterpret_cast<float*>(&sum);
+    for (int e = 0; e < 4; ++e) {
+      const float v = static_cast<float>(from[e]);
+      if (!isfinite(v)) x[e] += v;
+    }
+  }
+}
+
+// Four features of a row's result: sum / l and, with feature 0, m ln2 + ln l; (0, -inf)
+// where no key had weight.
+template <typename T>
+__device__ __forceinline__ void cache_write_row(const CacheParams& p, int b, int h, int token, int d, float4 sum, float m,
+                                                float l) {
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
+  if (none) sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  T* dst = static_cast<T*>(p.out.data) + b * p.out.s[0] + h * p.out.s[1] + token * p.out.s[2] + d;
+  if (CPATTN_IN(p.out.span, dst, 4 * sizeof(T), p.err)) {
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4*>(dst) = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+    else
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+  }
+  if (d != 0) return;
+  float* dl = static_cast<float*>(p.lse.data) + b * p.lse.s[0] + h * p.lse.s[1] + token * p.lse.s[2];
+  if (CPATTN_IN(p.lse.span, dl, 4, p.err)) *dl = none ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+}
+
+// Joins the parts of split units (see CacheWalk).  O and (m, l), m in base 2, as a
+// block left them: [block][slot][R][D] floats, then [block][slot][R] pairs.
+// `most`: blocks of the attention's launch.
+template <int R, int KT, int D, typename T>
+__global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ CacheParams p, int most) {
+  __shared__ long long range[3];
+  __shared__ int parts[2];
+  __shared__ int unit[2];
+  launch_wait();
+  launch_next();
+  const int hk = blockIdx.x % p.kv_heads, x = blockIdx.x / p.kv_heads;
+  if (threadIdx.x < 32) {
+    CacheWalk<R, KT> w;
+    w.measure(p, most);
+    // tiles of the pairs before x
+    long long before = 0;
+    for (int i = threadIdx.x; i < x; i += 32) {
+      int len, count;
+      before += static_cast<long long>(CacheWalk<R, KT>::tiles_of(p, i, &len, &count)) * p.kv_heads;
+    }
+    before = CacheWalk<R, KT>::warp_sum(before);
+    int len, count;
+    const int tiles = CacheWalk<R, KT>::tiles_of(p, x, &len, &count);
+    const long long u0 = before + static_cast<long long>(hk) * tiles, u1 = u0 + tiles;
+    if (threadIdx.x == 0) {
+      int c0 = 0, c1 = 0;
+      if (tiles > 0) {
+        c0 = static_cast<int>(u0 * w.blocks / w.total);
+        while (c0 + 1 < w.blocks && w.begin_of(c0 + 1) <= u0) ++c0;
+        while (c0 > 0 && w.begin_of(c0) > u0) --c0;
+        c1 = c0;
+        while (c1 + 1 < w.blocks && w.begin_of(c1 + 1) < u1) ++c1;
+      }
+      parts[0] = c0;
+      parts[1] = c1;
+      range[0] = u0;
+      range[1] = w.total;
+      unit[0] = w.blocks;
+      // (block c0 begins inside the unit only if the one before it ends there: not so)
+    }
+  }
+  __syncthreads();
+  const int c0 = parts[0], c1 = parts[1];
+  if (c0 == c1) return;   // (written by its block)
+  const int share = p.heads / p.kv_heads, rows = p.s_q * share;
+  const int b = x / p.row_tiles, rt = x - b * p.row_tiles;
+  const long long u0 = range[0], total = range[1];
+  const float2* ml = reinterpret_cast<const float2*>(p.ws + static_cast<int64_t>(most) * 2 * R * D);
+  // (slot 1: the block's range begins at or before the unit)
+  auto slot = [&](int c) { return static_cast<int64_t>(c) * 2 + (total * c / unit[0] > u0 ? 0 : 1); };
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < R * (D / 4); i += 256 * gridDim.y) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    const int row = rt * R + r;
+    if (row >= rows) break;
+    float top = -INFINITY;
+    for (int c = c0; c <= c1; ++c) {
+      const float2* at = ml + slot(c) * R + r;
+      if (CPATTN_IN(p.ws_span, at, 8, p.err)) top = fmaxf(top, at->x);
+    }
+    const float base = top == -INFINITY ? 0.f : top;
+    float l = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const int64_t s = slot(c);
+      const float2* at = ml + s * R + r;
+      const float4* o = reinterpret_cast<const float4*>(p.ws + (s * R + r) * D + d);
+      if (!CPATTN_IN(p.ws_span, at, 8, p.err) || !CPATTN_IN(p.ws_span, o, 16, p.err)) continue;
+      const float2 a = *at;
+      const float4 y = *o;
+      const float f = exp2f(a.x - base);
+      if (a.y == 0.f) continue;   // (no key of this part)
+      l = fmaf(f, a.y, l);
+      sum = make_float4(fmaf(f, y.x, sum.x), fmaf(f, y.y, sum.y), fmaf(f, y.z, sum.z), fmaf(f, y.w, sum.w));
+    }
+    const int token = row / share, h = hk * share + row % share;
+    cache_write_row<T>(p, b, h, token, d, sum, top, l);
+  }
+}
+
+
+// Launches the join behind an attention of `most` blocks.
+template <int R, int KT, int D, typename T>
+cudaError_t cache_join(const CacheParams& p, int most, cudaStream_t stream) {
+  const int64_t units = static_cast<int64_t>(p.batch) * p.row_tiles * p.kv_heads;
+  const int y = R * (D / 4) / 256;   // an item a thread
+  return launch_behind(cache_join_kernel<R, KT, D, T>, dim3(static_cast<unsigned>(units), y > 1 ? y : 1), 256, 0, stream, p,
+                       most);
+}
+
+// bf16 inputs, row tiles of 16, 32 or 64 rows, on `blocks` blocks
+cudaError_t launch_cache_few(int head_dim, int rows, const CacheParams& p, int blocks, cudaStream_t stream);
+// fp32 inputs, row tiles of kCacheF32Rows
+constexpr int kCacheF32Rows = 16, kCacheF32Keys = 32;
+cudaError_t launch_cache_f32(int head_dim, const CacheParams& p, int blocks, cudaStream_t stream);
+
+}  // namespace cpattn

@@ -16,21 +16,15 @@
 #include <cstring>
 #include <mutex>
 
+#include "args.h"
 #include "cross.cuh"
 #include "internal.h"
 
-namespace {
-
-using cpattn::InDtype;
+namespace cpattn {
 
 std::atomic<unsigned long long> g_timeout_ns{2000000000ull};
 std::atomic<int> g_fault_skip_kv{0};
 std::atomic<long long> g_check_shrink{0};   // testing: output extents shrunk by this many bytes
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
   static std::once_flag once;
@@ -46,59 +40,11 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-int elem_bytes(int32_t dtype) { return dtype == CPATTN_BF16 ? 2 : 4; }
+}  // namespace cpattn
 
-bool dtype_known(int32_t dtype) { return dtype == CPATTN_F32 || dtype == CPATTN_BF16; }
+namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Inner stride 1; other strides of extent>1 dims are multiples of 16 bytes
-// and non-negative; data 16-byte aligned.
-bool layout_ok(const cpattn_tensor* t) {
-  if (t->ndim < 1) return false;
-  if (t->shape[t->ndim - 1] > 1 && t->stride[t->ndim - 1] != 1) return false;
-  if (!aligned16(t->data)) return false;
-  const int eb = elem_bytes(t->dtype);
-  for (int i = 0; i < t->ndim - 1; ++i) {
-    if (t->stride[i] < 0) return false;
-    if (t->shape[i] > 1 && (t->stride[i] * eb) % 16 != 0) return false;
-  }
-  return true;
-}
-
-bool shape_ok(const cpattn_tensor* t, int ndim) {
-  if (t->ndim != ndim) return false;
-  for (int i = 0; i < ndim; ++i)
-    if (t->shape[i] < 0) return false;
-  return true;
-}
-
-// Bytes from a tensor's data pointer to the end of its last element (0 if
-// it has none), less `shrink` (the bounds-check testing hook).
-uint64_t extent_bytes(const cpattn_tensor* t, long long shrink = 0) {
-  int64_t last = 0;
-  for (int i = 0; i < t->ndim; ++i) {
-    if (t->shape[i] == 0) return 0;
-    last += (t->shape[i] - 1) * t->stride[i];
-  }
-  const int64_t bytes = (last + 1) * elem_bytes(t->dtype) - shrink;
-  return bytes > 0 ? static_cast<uint64_t>(bytes) : 0;
-}
-
-bool contiguous(const cpattn_tensor* t) {
-  int64_t expect = 1;
-  for (int i = t->ndim - 1; i >= 0; --i) {
-    if (t->shape[i] > 1 && t->stride[i] != expect) return false;
-    expect *= t->shape[i];
-  }
-  return true;
-}
-
-// Stride of a dimension as the TMA map sees it: dims of extent 1 get the
-// dense stride so that every stride stays a positive multiple of 16 bytes.
-int64_t tma_stride(const cpattn_tensor* t, int dim, int64_t dense) {
-  return t->shape[dim] > 1 ? t->stride[dim] : dense;
-}
+using namespace cpattn;
 
 // 4-D map over a [B, H, S, D] tensor: dims (D, S, H, B), box (128 bytes of D,
 // box_rows rows, 1, 1), 128-byte swizzle, zero fill out of bounds; with
@@ -341,27 +287,6 @@ cpattn_status permute_batch(int n, const cpattn_tensor* x, int degree, int dir, 
   const cudaError_t e =
       anything ? cpattn::launch_permute_anything(p, stream) : cpattn::launch_permute(p, stream);
   return e == cudaSuccess ? CPATTN_OK : CPATTN_ERR_CUDA;
-}
-
-// layout_ok, and no extent above 1 walks on the spot (broadcast views).
-bool layout_distinct(const cpattn_tensor* t) {
-  if (!layout_ok(t)) return false;
-  for (int i = 0; i < t->ndim; ++i)
-    if (t->shape[i] > 1 && t->stride[i] <= 0) return false;
-  return true;
-}
-
-bool lse_layout_ok(const cpattn_tensor* t) {
-  if (reinterpret_cast<uintptr_t>(t->data) & 3u) return false;
-  for (int i = 0; i < 3; ++i)
-    if (t->shape[i] > 1 && t->stride[i] <= 0) return false;
-  return t->shape[2] <= 1 || t->stride[2] == 1;
-}
-
-bool same_shape(const cpattn_tensor* a, const cpattn_tensor* b, int ndim) {
-  for (int i = 0; i < ndim; ++i)
-    if (a->shape[i] != b->shape[i]) return false;
-  return true;
 }
 
 cpattn::CrossTensor cross_tensor(const cpattn_tensor* t, long long shrink = 0) {
@@ -755,27 +680,10 @@ cpattn_status cpattn_rotary(int n, const cpattn_tensor* x, const cpattn_tensor* 
   p.pos_ss = positions->stride[pa - 1];
   p.pos_sa = positions->stride[pa];
   p.pos_span = {positions->data, extent_bytes(positions)};
-  p.axes = axes;
   p.interleaved = interleaved != 0;
   p.inverse = inverse != 0;
   p.err = cpattn::device_error_word();
-  if (!(theta > 0.0) || !std::isfinite(theta)) theta = 10000.0;
-  int j = 0;
-  for (int a = 0; a < axes; ++a) {
-    p.axis_dim[a] = axis_dims[a];
-    p.pair_start[a] = j;
-    // theta^(-2i/d) / 2 pi: every sixteenth of its own, those behind it by repeated
-    // products (an exponential costs some 15 ns of host time): relative error
-    // below 2^-47 and 2^-51 of |log| of the power; hi + lo leave out 2^-48
-    const double rate = -2.0 / axis_dims[a] * std::log(theta), step = std::exp(rate);
-    double f = 0.15915494309189535;
-    for (int i = 0; i < axis_dims[a] / 2; ++i, f *= step) {
-      if (i > 0 && i % 16 == 0) f = 0.15915494309189535 * std::exp(i * rate);
-      const float hi = static_cast<float>(f);
-      p.freq[j++] = make_float2(hi, static_cast<float>(f - hi));
-    }
-  }
-  p.rotary_pairs = j;
+  fill_turns(p, axes, axis_dims, theta);
   const InDtype dt = x[0].dtype == CPATTN_BF16 ? InDtype::BF16 : InDtype::F32;
   return cpattn::launch_rotary(dt, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CPATTN_OK
                                                                                        : CPATTN_ERR_CUDA;

@@ -110,6 +110,59 @@ struct RotaryParams {
 };
 cudaError_t launch_rotary(InDtype dt, const RotaryParams& p, cudaStream_t stream);
 
+// Norms of each head and rotary positions, and new tokens' way to a paged cache:
+// up to kMaxPermuteBatch tensors of one dtype, batch, sequence and head size (head
+// counts may differ).
+struct NormTensor {
+  const void* x;
+  const void* dy;          // backward: the gradient of y
+  void* y;                 // forward: the result; backward: dx
+  const void* w;           // [D] weights, or nullptr: ones
+  void* dw;                // backward: [D], or nullptr
+  int64_t x_s[3], dy_s[3]; // strides (b, h, s) in elements
+  int64_t y_s[3];          // the same, or (page, h, row of the page) of a paged result
+  int norm, turn, paged;   // 0 / 1
+  Span x_span, dy_span, y_span, w_span, dw_span;   // (CPATTN_CHECK builds)
+};
+// Where a cache's tokens are: page table[b][place / page size], row place % page size.
+struct PageTable {
+  const int32_t* table;    // [B, width], rows `stride` apart
+  const int32_t* lengths;  // [B] tokens before this call's
+  const int32_t* counts;   // [B] new tokens, or nullptr: all of them
+  int64_t stride;
+  int width, shift;        // page size: 1 << shift
+  int pages;               // of the pool
+  Span table_span, lengths_span, counts_span;
+};
+struct NormParams {
+  int n;
+  NormTensor t[kMaxPermuteBatch];
+  int head_start[kMaxPermuteBatch + 1];   // first head of tensor i in the count over all tensors
+  int head_group;          // heads (over all tensors) a block takes (set at launch)
+  int batch, seq, head_dim;
+  int w_f32;               // weights: 1 f32, 0 bf16
+  float eps;
+  const float* pos;
+  int64_t pos_sb, pos_ss, pos_sa;
+  int axes;
+  int axis_dim[CPATTN_MAX_ROTARY_AXES];
+  int pair_start[CPATTN_MAX_ROTARY_AXES];
+  int rotary_pairs;        // pairs that turn (none: no rotation)
+  int interleaved;
+  float2 freq[CPATTN_MAX_ROTARY_DIM / 2];   // turns per position, hi + lo
+  Span pos_span;
+  PageTable cache;         // where tensors are paged
+  float* ws;               // backward: [parts][n][D] sums of dw
+  int parts;
+  Span ws_span;
+  unsigned int* err;
+};
+cudaError_t launch_norm_rotary(InDtype dt, const NormParams& p, cudaStream_t stream);
+// its gradient; p.parts = norm_backward_parts(...)
+cudaError_t launch_norm_backward(InDtype dt, const NormParams& p, cudaStream_t stream);
+// partial sums of dw for `tokens` tokens in all of `heads` heads in all
+int norm_backward_parts(InDtype dt, int head_dim, int64_t tokens, int64_t heads);
+
 // Launches a kernel that may start while the one before it in the stream still
 // runs, whoever launched that.  Every block of it calls launch_wait() before it
 // touches memory that an earlier kernel writes or reads -- so it never

@@ -62,10 +62,12 @@ typedef enum {
   CPATTN_ERR_WORKSPACE = 7,     /* workspace missing or too small */
   CPATTN_ERR_CUDA = 8,          /* a CUDA runtime call failed */
   CPATTN_ERR_TIMEOUT = 9,       /* a device-side wait ran out of time */
-  CPATTN_ERR_BOUNDS = 10        /* a device-side bounds check failed (check builds only) */
+  CPATTN_ERR_BOUNDS = 10        /* a page number outside the pool; in check builds any
+                                   failed device-side bounds check */
 } cpattn_status;
 
-/* CPATTN_I32 is the type of kv_lengths only. */
+/* CPATTN_I32 is the type of kv_lengths and of a paged cache's table, lengths, counts
+ * and parents only. */
 typedef enum { CPATTN_F32 = 0, CPATTN_BF16 = 1, CPATTN_I32 = 2 } cpattn_dtype;
 
 #define CPATTN_MAX_DIMS 5
@@ -356,14 +358,143 @@ cpattn_status cpattn_cross_attention_backward(const cpattn_tensor* q, const cpat
                                               size_t workspace_bytes, void* stream);
 size_t cpattn_cross_backward_workspace_bytes(const cpattn_tensor* q, const cpattn_tensor* k);
 
+/*
+ * cpattn_norm_rotary -- norms of each head and rotary positions in the same pass,
+ * on queries and keys before any of the attentions above:
+ *   y = Turn(x r w),  r = 1 / sqrt(sum_d x_d^2 / D + eps) for each token and head,
+ *   with Turn as in cpattn_rotary; D counts all features, turned or not.
+ *   x, y, positions, axes, axis_dims, theta, interleaved: as cpattn_rotary.
+ *   weights: NULL (ones), or an array of n descriptors [D], f32 or bf16 (one type
+ *     for all n), inner stride 1: weights[i] belongs to x[i].
+ *   eps: not a number, below 0 or infinite selects 1e-6.
+ * Everything is computed in fp32 and rounded once.  Squares are summed in fp32: a
+ * row's sum must stay below 3.4e38 (|x| up to 1e18).  B, S or every H_i = 0 is a
+ * no-op.
+ */
+cpattn_status cpattn_norm_rotary(int n, const cpattn_tensor* x, const cpattn_tensor* weights,
+                                 float eps, const cpattn_tensor* positions, int axes,
+                                 const int32_t* axis_dims, double theta, int interleaved,
+                                 cpattn_tensor* y, void* stream);
+
+/*
+ * cpattn_norm_rotary_backward -- the gradient of cpattn_norm_rotary:
+ *   x, weights and what follows: as the forward call took them; dy[i]: the gradient
+ *     of y[i] (shape and dtype of x[i]).
+ *   dx[i]: written, shape and dtype of x[i]; may be x[i] or dy[i] itself.
+ *   dweights: NULL if weights is, else n descriptors [D] of the weights' type:
+ *     written, summed in fp32 over every token and head of x[i] and rounded once.
+ *   workspace: at least cpattn_norm_rotary_backward_workspace_bytes(n, x) bytes,
+ *     16-byte aligned, if weights is not NULL.  Calls that may overlap need their own.
+ * Every sum has one owner and a fixed order: equal calls give equal bits.  No rows:
+ * dweights are 0.
+ */
+cpattn_status cpattn_norm_rotary_backward(int n, const cpattn_tensor* x,
+                                          const cpattn_tensor* weights, float eps,
+                                          const cpattn_tensor* positions, int axes,
+                                          const int32_t* axis_dims, double theta,
+                                          int interleaved, const cpattn_tensor* dy,
+                                          cpattn_tensor* dx, cpattn_tensor* dweights,
+                                          void* workspace, size_t workspace_bytes,
+                                          void* stream);
+/* For the current device, like the call.  0 also for descriptors that the call
+ * would refuse. */
+size_t cpattn_norm_rotary_backward_workspace_bytes(int n, const cpattn_tensor* x);
+
+#define CPATTN_MIN_PAGE 16
+#define CPATTN_MAX_PAGE 1024
+#define CPATTN_MAX_TREE 256
+
+/*
+ * A paged cache of keys and values, for the two calls below:
+ *   key_pages, value_pages [P, H_kv, R, D], of one dtype: P pages of R tokens; R a
+ *     power of two from CPATTN_MIN_PAGE to CPATTN_MAX_PAGE (else
+ *     CPATTN_ERR_UNSUPPORTED).  Any strides that the conventions above allow, so
+ *     pages [P, R, H_kv, D] are given as their [P, H_kv, R, D] view.
+ *   page_table i32 [B, W], rows of inner stride 1: the token at place j of sequence b
+ *     is row j % R of page page_table[b][j / R].  W R <= 2^30.
+ *   lengths i32 [B], contiguous: tokens of each sequence before this step's, brought
+ *     into [0, W R].
+ *   counts: NULL (all S), or i32 [B], contiguous: how many of the step's S tokens a
+ *     sequence has, the first ones; brought into [0, S].
+ * Table entries are read only for places that the call uses; pages may be shared
+ * between sequences where they are only read.  A place past the table's width, or a
+ * page number outside [0, P), is an error that the kernels meet: nothing outside the
+ * pool is touched, the token is not written (its key and value are read as zeros),
+ * and cpattn_last_device_status reports CPATTN_ERR_BOUNDS.
+ */
+
+/*
+ * cpattn_cache_append -- a step's new keys and values to their pages, with a norm and
+ * rotary positions on the way, and the step's queries in the same launch:
+ *   key_pages   at place lengths[b] + s  =  Turn(norm(k[b, :, s]))
+ *   value_pages at place lengths[b] + s  =  v[b, :, s]
+ *   q_out[b, :, s]                       =  Turn(norm(q[b, :, s]))
+ *   k, v [B, H_kv, S, D], q [B, H, S, D] (NULL, with q_out: no queries): the pages'
+ *     dtype, bf16 or f32; D as cpattn_rotary.  q_out may be q itself.
+ *   k_weight, q_weight [D], f32 or bf16 (one type): norm as in cpattn_norm_rotary;
+ *     NULL: no norm.
+ *   positions: f32 [S, axes] or [B, S, axes], with axes, axis_dims, theta and
+ *     interleaved as in cpattn_rotary; NULL: nothing turns.
+ * Tokens from counts[b] on are not written (q_out has all S).  No two tokens of a call
+ * may have the same place in the pool.  B, S or every head count 0 is a no-op.
+ */
+cpattn_status cpattn_cache_append(const cpattn_tensor* q, const cpattn_tensor* k,
+                                  const cpattn_tensor* v, const cpattn_tensor* q_weight,
+                                  const cpattn_tensor* k_weight, float eps,
+                                  const cpattn_tensor* positions, int axes,
+                                  const int32_t* axis_dims, double theta, int interleaved,
+                                  cpattn_tensor* key_pages, cpattn_tensor* value_pages,
+                                  const cpattn_tensor* page_table, const cpattn_tensor* lengths,
+                                  const cpattn_tensor* counts, cpattn_tensor* q_out,
+                                  void* stream);
+
+/*
+ * cpattn_cache_attention -- attention of a step's queries to their sequences' paged
+ * caches, which hold the step's keys and values already (cpattn_cache_append): one
+ * new token, a chain of them (the next piece of a prompt), or a tree of drafts.
+ *   Query i of sequence b sees the keys at places 0 .. lengths[b] - 1 and, of those
+ *   behind them, places lengths[b] + j for j = i and every j above it:
+ *     parents NULL: a chain, j <= i;
+ *     parents i32 [B, S], rows of inner stride 1, S <= CPATTN_MAX_TREE: j = parents[i],
+ *       its parent, and so on; a parent that is negative or not before its draft is
+ *       none (the draft follows the cached tokens).
+ *   out = softmax(scale q k^T) v over these, lse its natural log-sum-exp; queries from
+ *   counts[b] on, and rows whose scores are all -inf, give (0, -inf).
+ *   q, out [B, H, S, D], bf16 or f32, D = 64 or 128; lse [B, H, S] f32; H % H_kv == 0
+ *     (else CPATTN_ERR_DIVISIBILITY): query heads h_kv * H / H_kv and following share
+ *     key head h_kv.  S <= 2^24.
+ *   workspace: at least cpattn_cache_attention_workspace_bytes(...) bytes, 16-byte
+ *     aligned, NULL if that is 0: parts of key axes that are split and joined.  Calls
+ *     that may overlap need their own.
+ * Places that no query of a sequence sees are not used and may hold anything; a draft
+ * that is not above a query has no part in its result, NaN and infinities included.
+ * fp32 inputs are computed in fp32.  bf16 inputs: scores, sums and lse are fp32; each
+ * weight exp(s - max) is rounded to bf16 once for its product with v, and out once (the
+ * bound is cpattn_cross_attention's).  Equal calls give equal bits.  Strides of
+ * extents above 1 must be positive; outputs may not overlap any other buffer.
+ * B * H * S = 0 is a no-op.
+ */
+cpattn_status cpattn_cache_attention(const cpattn_tensor* q, const cpattn_tensor* key_pages,
+                                     const cpattn_tensor* value_pages,
+                                     const cpattn_tensor* page_table,
+                                     const cpattn_tensor* lengths, const cpattn_tensor* counts,
+                                     const cpattn_tensor* parents, float scale,
+                                     cpattn_tensor* out, cpattn_tensor* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+/* For the current device, like the call.  0 also for descriptors that the call would
+ * refuse. */
+size_t cpattn_cache_attention_workspace_bytes(const cpattn_tensor* q,
+                                             const cpattn_tensor* key_pages,
+                                             const cpattn_tensor* page_table);
+
 /* Human-readable name of a status code (static storage). */
 const char* cpattn_status_string(cpattn_status status);
 
 /*
  * cpattn_last_device_status -- synchronises `stream`, then reads and clears
  * the device error word that kernel-side waits set when they time out.
- * Returns CPATTN_OK, CPATTN_ERR_TIMEOUT, CPATTN_ERR_BOUNDS (check builds;
- * reported first when both happened), or CPATTN_ERR_CUDA if the
+ * Returns CPATTN_OK, CPATTN_ERR_TIMEOUT, CPATTN_ERR_BOUNDS (a bad page number, or
+ * check builds; reported first when both happened), or CPATTN_ERR_CUDA if the
  * synchronisation itself failed.
  */
 cpattn_status cpattn_last_device_status(void* stream);
