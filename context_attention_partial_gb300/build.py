@@ -25,7 +25,7 @@ CHECK_LIB_PATH = os.path.join(PKG, "libcpattn_check.so")
 SOURCES = ["attn_fwd.cu", "merge_permute.cu", "cpattn_api.cu", "ring_noalloc.cu",
            "rotary.cu", "cross_simt.cu", "cross_fwd.cu",
            "cross_bwd.cu", "cross_few.cu", "cross_f32.cu", "norm_rotary.cu", "cache_api.cu",
-           "cache_few.cu", "cache_f32.cu"]
+           "cache_few.cu", "cache_f32.cu", "cache_fwd.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "tmem_ops.cuh", "tile_ops.cuh", "check.cuh", "cross.cuh", "cross_ops.cuh",
            "args.h", "rotary_turns.cuh", "cache.cuh", "mma_ops.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

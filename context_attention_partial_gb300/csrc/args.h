@@ -26,6 +26,11 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 // The driver's encoder, looked up once (nullptr without a driver).
 EncodeTiledFn encode_fn();
 
+// 4-D map over a [B, H, S, D] tensor: dims (D, S, H, B), box (128 bytes of D,
+// box_rows rows, 1, 1), 128-byte swizzle, zero fill out of bounds; with
+// half_rows, 64 bytes of D and no swizzle.
+cpattn_status make_tmap(CUtensorMap* m, const cpattn_tensor* t, int box_rows, bool half_rows = false);
+
 inline int elem_bytes(int32_t dtype) { return dtype == CPATTN_BF16 ? 2 : 4; }
 
 inline bool dtype_known(int32_t dtype) { return dtype == CPATTN_F32 || dtype == CPATTN_BF16; }

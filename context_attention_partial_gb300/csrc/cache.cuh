@@ -58,7 +58,10 @@ __device__ __forceinline__ CachePlace cache_place(const PageTable& c, int b, int
 // ------------------------------------------------------------- attention
 // S_q new tokens of each sequence against its cache, which holds them already, in
 // the places behind lengths[b].  A row is a (token, query head) pair of those that
-// share a key head, row = token * share + head % share; a row tile is R of them.
+// share a key head, row = token * share + head % share; a row tile is `tile_rows` of
+// them.  Where it is kept they have R places: place r holds row (r / 128) * half_rows
+// + r % 128 of the tile, if r % 128 < half_rows (the tensor cores' tiles have 128
+// rows, of which whole tokens fill some).
 struct CacheParams {
   CrossTensor q, out, lse;    // [B, H, S_q, D], lse [B, H, S_q]
   CrossTensor k, v;           // pages: strides (page, head, row of the page)
@@ -70,6 +73,7 @@ struct CacheParams {
   Span ws_span;
   int batch, heads, kv_heads, s_q;
   int row_tiles;              // of a key head
+  int tile_rows, half_rows;   // rows of a row tile, and of each 128 places of its storage
   int split;                  // whether units are split over blocks (see CacheWalk)
   float scale_log2;           // softmax scale times log2(e)
   unsigned long long timeout_ns;
@@ -77,8 +81,14 @@ struct CacheParams {
   unsigned int* err;
 };
 
+// Row of (b, hk, rt)'s place r, or -1.
+__device__ __forceinline__ int cache_row(const CacheParams& p, int rt, int r) {
+  const int x = r % 128, row = rt * p.tile_rows + r / 128 * p.half_rows + x;
+  return x < p.half_rows && row < p.s_q * (p.heads / p.kv_heads) ? row : -1;
+}
+
 // Key tiles that a block takes at least before another one shares its work.
-constexpr int kCacheMinTiles = 3;
+constexpr int cache_min_tiles(int keys) { return keys >= 128 ? 2 : 3; }
 // Units a block above which none are split: then a round of whole units is at most
 // an eighth of the call, and the tables that a split needs would be long.
 constexpr int kCacheWholeUnits = 8;
@@ -111,10 +121,10 @@ struct CacheWalk {
     const int n = cache_count(p.cache, b, p.s_q, p.err);
     *len = cache_length(p.cache, b, p.err);
     *count = n;
-    const int first = rt * R / share;
+    const int first = rt * p.tile_rows / share;
     if (first >= n) return 0;   // (no row has a token)
     // a chain's rows see nothing past their last token
-    const int last = p.parents != nullptr ? n - 1 : min(n - 1, (rt * R + R - 1) / share);
+    const int last = p.parents != nullptr ? n - 1 : min(n - 1, (rt * p.tile_rows + p.tile_rows - 1) / share);
     return (*len + last + KT) / KT;
   }
   __device__ static long long warp_sum(long long v) {
@@ -155,7 +165,7 @@ struct CacheWalk {
       total += static_cast<long long>(tiles_of(p, i, &len, &count)) * p.kv_heads;
     }
     total = warp_sum(total);
-    const long long most_blocks = (total + kCacheMinTiles - 1) / kCacheMinTiles;
+    const long long most_blocks = (total + cache_min_tiles(KT) - 1) / cache_min_tiles(KT);
     blocks = static_cast<int>(most_blocks < 1 ? 1 : most_blocks < most ? most_blocks : most);
   }
   __device__ void start(const CacheParams& p) {
@@ -208,7 +218,7 @@ struct CacheWalk {
 // which share the units without keys out by their number.
 template <typename T, int R, int KT, int D>
 __device__ __forceinline__ void cache_empty_units(const CacheParams& p) {
-  const int share = p.heads / p.kv_heads, rows = p.s_q * share;
+  const int share = p.heads / p.kv_heads;
   const int64_t units = static_cast<int64_t>(p.batch) * p.row_tiles * p.kv_heads;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int x = static_cast<int>(u / p.kv_heads), hk = static_cast<int>(u % p.kv_heads);
@@ -217,8 +227,8 @@ __device__ __forceinline__ void cache_empty_units(const CacheParams& p) {
     const int b = x / p.row_tiles, rt = x - b * p.row_tiles;
     constexpr int C = D * sizeof(T) / 16;
     for (int i = threadIdx.x; i < R * C; i += blockDim.x) {
-      const int row = rt * R + i / C;
-      if (row >= rows) break;
+      const int row = cache_row(p, rt, i / C);
+      if (row < 0) continue;
       const int token = row / share, h = hk * share + row % share;
       T* dst = static_cast<T*>(p.out.data) + b * p.out.s[0] + h * p.out.s[1] + token * p.out.s[2] + i % C * (16 / sizeof(T));
       if (CPATTN_IN(p.out.span, dst, 16, p.err)) *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
@@ -238,8 +248,8 @@ __device__ __forceinline__ void tree_paths(const CacheParams& p, const int* pare
   const int share = p.heads / p.kv_heads;
   for (int r = t; r < R; r += threads) {
     uint32_t bits[kTreeWords] = {};
-    int j = (rt * R + r) / share;
-    if (j >= p.s_q) j = -1;
+    const int row = cache_row(p, rt, r);
+    int j = row < 0 ? -1 : row / share;
     while (j >= 0) {
 #pragma unroll
       for (int w = 0; w < kTreeWords; ++w)
@@ -348,9 +358,8 @@ __device__ __forceinline__ void cache_write_row(const CacheParams& p, int b, int
 // `most`: blocks of the attention's launch.
 template <int R, int KT, int D, typename T>
 __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ CacheParams p, int most) {
-  __shared__ long long range[3];
-  __shared__ int parts[2];
-  __shared__ int unit[2];
+  __shared__ long long range[2];
+  __shared__ int parts[4];
   launch_wait();
   launch_next();
   const int hk = blockIdx.x % p.kv_heads, x = blockIdx.x / p.kv_heads;
@@ -380,25 +389,27 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
       parts[1] = c1;
       range[0] = u0;
       range[1] = w.total;
-      unit[0] = w.blocks;
-      // (block c0 begins inside the unit only if the one before it ends there: not so)
+      parts[2] = w.blocks;
+      parts[3] = count;
     }
   }
   __syncthreads();
   const int c0 = parts[0], c1 = parts[1];
   if (c0 == c1) return;   // (written by its block)
-  const int share = p.heads / p.kv_heads, rows = p.s_q * share;
+  const int share = p.heads / p.kv_heads, blocks = parts[2], count = parts[3];
   const int b = x / p.row_tiles, rt = x - b * p.row_tiles;
   const long long u0 = range[0], total = range[1];
   const float2* ml = reinterpret_cast<const float2*>(p.ws + static_cast<int64_t>(most) * 2 * R * D);
   // (slot 1: the block's range begins at or before the unit)
-  auto slot = [&](int c) { return static_cast<int64_t>(c) * 2 + (total * c / unit[0] > u0 ? 0 : 1); };
+  auto slot = [&](int c) { return static_cast<int64_t>(c) * 2 + (total * c / blocks > u0 ? 0 : 1); };
   for (int i = blockIdx.y * 256 + threadIdx.x; i < R * (D / 4); i += 256 * gridDim.y) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
-    const int row = rt * R + r;
-    if (row >= rows) break;
+    const int row = cache_row(p, rt, r);
+    if (row < 0) continue;
+    const int token = row / share, h = hk * share + row % share;
+    const int last = token < count ? c1 : c0 - 1;   // (no parts for a row without a token)
     float top = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
+    for (int c = c0; c <= last; ++c) {
       const float2* at = ml + slot(c) * R + r;
       if (CPATTN_IN(p.ws_span, at, 8, p.err)) top = fmaxf(top, at->x);
     }
@@ -406,7 +417,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
     float l = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
+    for (int c = c0; c <= last; ++c) {
       const int64_t s = slot(c);
       const float2* at = ml + s * R + r;
       const float4* o = reinterpret_cast<const float4*>(p.ws + (s * R + r) * D + d);
@@ -418,7 +429,6 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
       l = fmaf(f, a.y, l);
       sum = make_float4(fmaf(f, y.x, sum.x), fmaf(f, y.y, sum.y), fmaf(f, y.z, sum.z), fmaf(f, y.w, sum.w));
     }
-    const int token = row / share, h = hk * share + row % share;
     cache_write_row<T>(p, b, h, token, d, sum, top, l);
   }
 }
@@ -435,6 +445,12 @@ cudaError_t cache_join(const CacheParams& p, int most, cudaStream_t stream) {
 
 // bf16 inputs, row tiles of 16, 32 or 64 rows, on `blocks` blocks
 cudaError_t launch_cache_few(int head_dim, int rows, const CacheParams& p, int blocks, cudaStream_t stream);
+// bf16 inputs, row tiles of 128 places (one tile of the tensor cores) or 256 (two)
+struct CacheMaps {
+  CUtensorMap q, k, v;   // boxes of 64 features: q's of half_rows rows, pages' of `box` rows
+};
+cudaError_t launch_cache_fwd(int head_dim, int places, const CacheMaps& maps, const CacheParams& p, int blocks,
+                             cudaStream_t stream);
 // fp32 inputs, row tiles of kCacheF32Rows
 constexpr int kCacheF32Rows = 16, kCacheF32Keys = 32;
 cudaError_t launch_cache_f32(int head_dim, const CacheParams& p, int blocks, cudaStream_t stream);

@@ -190,7 +190,8 @@ cpattn_status cache_common(const cpattn_tensor* key_pages, const cpattn_tensor* 
 // How an attention to a cache is run; the same for every cache of these sizes, whatever
 // its lengths are.
 struct CachePlan {
-  int rows, keys;        // of a row tile, of a key tile
+  int places, keys;      // of a row tile (see CacheParams), keys of a key tile
+  int tile_rows, half_rows;
   int row_tiles;         // of a key head
   int blocks, split;     // see CacheWalk
   size_t workspace;
@@ -210,27 +211,58 @@ cpattn_status cache_shape(const cpattn_tensor* q, const cpattn_tensor* key_pages
   return CPATTN_OK;
 }
 
+// Whether a bf16 call goes to the tensor cores' 128-row tiles.
+bool cache_many(const cpattn_tensor* q, const cpattn_tensor* key_pages) {
+  const int64_t share = q->shape[1] / key_pages->shape[1], rows = q->shape[2] * share;
+  return rows > 32 && share <= 128 && key_pages->shape[0] > 0;
+}
+
+// Queries as the tensor cores' tiles take them: dims (D, H, S, B), boxes of 64 features,
+// the heads that share a key head, and `tokens` tokens.
+cpattn_status query_map(CUtensorMap* m, const cpattn_tensor* q, int share, int tokens) {
+  const EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return CPATTN_ERR_CUDA;
+  const int64_t B = q->shape[0], H = q->shape[1], S = q->shape[2], D = q->shape[3];
+  const int64_t sh = tma_stride(q, 1, D), ss = tma_stride(q, 2, D), sb = tma_stride(q, 0, D);
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)S, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)(sh * 2), (cuuint64_t)(ss * 2), (cuuint64_t)(sb * 2)};
+  const cuuint32_t box[4] = {64u, (cuuint32_t)share, (cuuint32_t)tokens, 1u}, step[4] = {1u, 1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, q->data, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? CPATTN_OK
+             : CPATTN_ERR_CUDA;
+}
+
 CachePlan cache_plan(const cpattn_tensor* q, const cpattn_tensor* key_pages, const cpattn_tensor* page_table) {
   CachePlan c = {};
   const int64_t B = q->shape[0], H = q->shape[1], S = q->shape[2], D = q->shape[3], Hk = key_pages->shape[1];
   if (B * H * S == 0) return c;
   const int64_t rows = S * (H / Hk);
-  int64_t slots;
+  int64_t slots = 2 * static_cast<int64_t>(sm_count());
   if (q->dtype == CPATTN_F32) {
-    c.rows = kCacheF32Rows;
+    c.places = kCacheF32Rows;
     c.keys = kCacheF32Keys;
+  } else if (cache_many(q, key_pages)) {
+    // whole tokens of up to 128 rows, in one or two tiles of the tensor cores
+    c.half_rows = static_cast<int>(128 / (H / Hk) * (H / Hk));
+    c.places = rows <= c.half_rows ? 128 : 256;
+    c.tile_rows = c.places / 128 * c.half_rows;
+    c.keys = 128;
+    slots = sm_count();
   } else {
-    c.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    c.places = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     c.keys = 64;
   }
-  slots = 2 * static_cast<int64_t>(sm_count());
-  c.row_tiles = static_cast<int>((rows + c.rows - 1) / c.rows);
+  if (c.tile_rows == 0) c.tile_rows = c.half_rows = c.places;
+  c.row_tiles = static_cast<int>((rows + c.tile_rows - 1) / c.tile_rows);
   const int64_t units = B * c.row_tiles * Hk;
   const int64_t most = (page_table->shape[1] * key_pages->shape[2] + S + c.keys - 1) / c.keys;   // tiles of a unit
-  c.split = most > kCacheMinTiles && units < kCacheWholeUnits * slots;
-  const int64_t want = c.split ? (units * most + kCacheMinTiles - 1) / kCacheMinTiles : units;
+  const int64_t least = cache_min_tiles(c.keys);
+  c.split = most > least && units < kCacheWholeUnits * slots;
+  const int64_t want = c.split ? (units * most + least - 1) / least : units;
   c.blocks = static_cast<int>(want < slots ? want : slots);
-  c.workspace = c.split ? static_cast<size_t>(c.blocks) * 2 * c.rows * (D + 2) * 4 : 0;
+  c.workspace = c.split ? static_cast<size_t>(c.blocks) * 2 * c.places * (D + 2) * 4 : 0;
   return c;
 }
 
@@ -418,6 +450,8 @@ cpattn_status cpattn_cache_attention(const cpattn_tensor* q, const cpattn_tensor
   p.kv_heads = static_cast<int>(key_pages->shape[1]);
   p.s_q = static_cast<int>(S);
   p.row_tiles = plan.row_tiles;
+  p.tile_rows = plan.tile_rows;
+  p.half_rows = plan.half_rows;
   p.split = plan.split;
   if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt(static_cast<float>(D));
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
@@ -427,7 +461,13 @@ cpattn_status cpattn_cache_attention(const cpattn_tensor* q, const cpattn_tensor
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int head_dim = static_cast<int>(D);
   if (q->dtype == CPATTN_F32) return status_of(launch_cache_f32(head_dim, p, plan.blocks, cs));
-  return status_of(launch_cache_few(head_dim, plan.rows, p, plan.blocks, cs));
+  if (!cache_many(q, key_pages)) return status_of(launch_cache_few(head_dim, plan.places, p, plan.blocks, cs));
+  const int share = static_cast<int>(H / key_pages->shape[1]), page = static_cast<int>(key_pages->shape[2]);
+  CacheMaps m;
+  if ((st = query_map(&m.q, q, share, 128 / share)) != CPATTN_OK) return st;
+  if ((st = make_tmap(&m.k, key_pages, page < 128 ? page : 128)) != CPATTN_OK) return st;
+  if ((st = make_tmap(&m.v, value_pages, page < 128 ? page : 128)) != CPATTN_OK) return st;
+  return status_of(launch_cache_fwd(head_dim, plan.places, m, p, plan.blocks, cs));
 }
 
 }  // extern "C"

@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
     const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1);   // (a piece's slot)
     for (int i = threadIdx.x; i < R * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-      const int row = w.rt * R + r;
-      if (row >= rows) break;
+      const int row = cache_row(p, w.rt, r);
+      if (row < 0) continue;
       float top = -INFINITY;
 #pragma unroll
       for (int g = 0; g < KG; ++g) top = fmaxf(top, sm[g * R + r].x);

@@ -1,0 +1,697 @@
+// cache_fwd.cu -- attention of many rows (wide trees, pieces of prompts) to a paged
+// cache, bf16, on the tensor cores.
+//
+// Mathematics as in cache_few.cu.  P is rounded to bf16 for its product with V (the
+// tensor cores' operand type; l keeps the fp32 values), and the output once.
+//
+// What bounds it: with 256 rows a key head or more the products (4 D operations a row
+// and key), below that the read of the keys and values.  Blocks are persistent, one an
+// SM, and walk pieces of the line of all key tiles (CacheWalk): the next piece's
+// queries and keys are fetched and its first Q K^T is issued while this piece's last
+// softmax, P V and output are under way.
+//
+// Roles (12 warps): warps 0-7 softmax and output, one thread per row of a 128-row query
+// tile and warpgroup; warp 8 TMA producer; warp 9 MMA issuer; warps 10-11 clean the
+// value tiles that hold drafts.  TMEM: S_0 | S_1 | O_0 | O_1, P over S's first columns.
+// Shared memory: the two Q tiles, a ring of K / V tiles, an output staging area and the
+// paths of a tree's drafts per softmax warp.
+//
+// Rows.  A query tile is whole tokens, each with every query head that shares the key
+// head: a TMA box [tokens][heads][64 features].  PAIR: a unit has one query tile, its
+// key tiles alternate between the two sums, which are joined at the end of a piece:
+// a lone tile's products and exponentials would wait for one another.  Otherwise a
+// unit has two query tiles, which read the same keys.
+//
+// Keys.  A 128-key tile is up to eight pages' boxes, each asked for by a lane of the
+// producer.  Scores of keys that a row does not see are masked in registers, by the
+// bits of its path.  Value rows behind the last key are zeroed in shared memory, and so
+// are a draft's values that are not finite (see cache_few.cu), by warps 10 and 11.
+#include <cmath>
+
+#include "cache.cuh"
+#include "cross_ops.cuh"
+
+namespace cpattn {
+namespace {
+
+constexpr int kBM = 128, kBN = 128;
+constexpr int kThreads = 384;
+constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10;
+constexpr int kLaunchRegs = 168;    // 65536 / 384, rounded down to 8
+constexpr int kSoftmaxRegs = 208, kControlRegs = 88;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= kThreads * kLaunchRegs,
+              "register split exceeds the launch allocation");
+constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
+constexpr unsigned kErrProducer = 1u, kErrMma = 2u, kErrSoftmax = 4u, kErrClean = 8u;
+
+template <int D>
+struct Cfg {
+  static constexpr int ROW = D * 2;                       // bytes
+  static constexpr int TILE = kBM * ROW;                  // bytes of a Q, K or V tile
+  static constexpr int STAGES = D == 128 ? 4 : 8;
+  static constexpr int STAGING = 8 * 32 * 64;             // 32 rows x 64 bytes per warp
+  static constexpr int PATHS = 8 * 32 * kTreeWords * 4;   // a path per row
+  static constexpr int SUMS = 2 * kBM * 8;                // PAIR: m and l of both sums
+  static constexpr int BARS = 2 * STAGES + 13;
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + STAGING + PATHS + SUMS + BARS * 8 + 48;
+  static constexpr int QK = ROW / 32, PV = kBN / 16;      // MMAs of a tile product
+  static constexpr int KB = ROW / 128;                    // 128-byte column blocks
+  static constexpr int O_COL = 2 * kBN;
+  static constexpr uint32_t IDESC_QK = make_idesc(1, false, kBM, kBN);
+  static constexpr uint32_t IDESC_PV = make_idesc(1, true, kBM, D);
+  static_assert(O_COL + 2 * D <= 512, "TMEM");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// All 256 softmax threads meet and vote.
+__device__ __forceinline__ bool vote_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.aligned.pred q, 1, 256, p;\n\tselp.u32 %0, 1, "
+      "0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// Largest of the scores whose bits are set; the others are set to -inf in place.
+__device__ __forceinline__ float masked_bits_max(uint32_t (&s)[128], const unsigned long long (&seen)[2]) {
+  float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 128; ++i) {
+    if (!((seen[i / 64] >> (i % 64)) & 1)) s[i] = f2u(-INFINITY);
+    mx[i & 1] = fmaxf(mx[i & 1], u2f(s[i]));
+  }
+  return fmaxf(mx[0], mx[1]);
+}
+
+// A piece and what its roles derive from it.
+struct Work : CachePiece {
+  int k0, k1;     // its keys
+  int n;          // its key tiles
+  int halves;     // query tiles with rows
+  __device__ bool drafts(int j) const { return k0 + (j + 1) * kBN > len; }   // key tile j holds some
+};
+
+template <bool PAIR>
+struct Walk : CacheWalk<PAIR ? 128 : 256, kBN> {
+  __device__ bool step(const CacheParams& p, Work& w) {
+    if (!this->next(p, w)) return false;
+    w.k0 = w.t0 * kBN;
+    w.k1 = min(w.len + w.count, w.t1 * kBN);
+    w.n = w.t1 - w.t0;
+    const int share = p.heads / p.kv_heads;
+    w.halves = !PAIR && (w.rt * p.tile_rows + p.half_rows) / share < w.count ? 2 : 1;
+    return true;
+  }
+};
+
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CacheParams p) {
+  using C = Cfg<D>;
+  constexpr int R = PAIR ? 128 : 256;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sQ = smem_addr(smem), sKV = sQ + 2 * C::TILE;
+  uint8_t* staging = smem + (2 + C::STAGES) * C::TILE;
+  uint32_t* all_paths = reinterpret_cast<uint32_t*>(staging + C::STAGING);
+  float2* sums = reinterpret_cast<float2*>(staging + C::STAGING + C::PATHS);   // [2][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::STAGING + C::PATHS + C::SUMS);
+  const uint32_t bar0 = smem_addr(bars);
+  auto bar_full = [&](int s) { return bar0 + 8u * s; };
+  auto bar_empty = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+  auto bar_q = [&](int i) { return bar0 + 8u * (2 * C::STAGES + i); };          // Q tile arrived
+  auto bar_qfree = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 2 + i); };  // its last Q K^T is done
+  auto bar_s = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 4 + i); };      // scores ready
+  auto bar_p = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 6 + i); };      // P written
+  auto bar_o = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 8 + i); };      // O of a piece ready
+  const uint32_t bar_drain = bar0 + 8u * (2 * C::STAGES + 10);
+  const uint32_t bar_dirty = bar0 + 8u * (2 * C::STAGES + 11);                  // a value tile with drafts arrived
+  const uint32_t bar_clean = bar0 + 8u * (2 * C::STAGES + 12);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  // pieces with values that are not finite, by the piece's number
+  volatile int* unclean = reinterpret_cast<volatile int*>(tmem_holder + 2);     // [8]
+
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
+  const int lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_q(i), 1);
+      mbar_init(bar_qfree(i), 1);
+      mbar_init(bar_s(i), 1);
+      mbar_init(bar_p(i), 4);   // one arrival per softmax warp
+      mbar_init(bar_o(i), 1);
+    }
+    mbar_init(bar_drain, 1);
+    mbar_init(bar_dirty, 1);
+    mbar_init(bar_clean, 2);
+    *abort_flag = 0;
+    for (int i = 0; i < 8; ++i) unclean[i] = -1;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(smem_addr(tmem_holder), 512);
+  if (warp == kWarpProducer && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  launch_wait();
+  launch_next();
+  const uint32_t tmem = *tmem_holder;
+  const int share = p.heads / p.kv_heads;
+  // every wait of a warp is voted on, so its lanes stay together
+  auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) {
+    const bool r = mbar_wait(bar, parity, abort_flag, p.timeout_ns, p.err, code);
+    return __all_sync(0xffffffffu, r) != 0;
+  };
+
+  if (warp >= 8) {
+    regs_decrease<kControlRegs>();
+    const bool leader = elect_one();
+    Walk<PAIR> walk;
+    walk.start(p);
+    Work w;
+    bool have = walk.step(p, w);
+    if (warp == kWarpProducer) {
+      // ---------------------------------------------------------- producer
+      // K tiles on even stages, V tiles on odd ones: the first K alone, then
+      // V_j and the K tile after it (of the next piece behind a piece's last V)
+      // as one pair on the K stage's barrier, so the MMA warp waits once a
+      // step; the very last V on its own.  Lanes 0-15 ask for a value tile's pages,
+      // lanes 16-31 for a key tile's.
+      static_assert(C::STAGES % 2 == 0, "K / V pairs");
+      const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
+      const int box = min(1 << p.cache.shift, kBN), kb = lane % C::KB, part = lane % 16 / C::KB;
+      const uint32_t q_bytes = static_cast<uint32_t>(p.half_rows) * C::ROW;
+      int ld = 0, nq[2] = {0, 0};
+      bool ok = p.fault_skip_kv == 0;
+      // boxes of key tile j of piece x; this lane's box's page
+      auto boxes = [&](const Work& x, int j) { return ceil_div(min(kBN, x.k1 - (x.k0 + j * kBN)), box); };
+      auto page_of = [&](const Work& x, int j, int n) {
+        return part < n ? cache_page(p.cache, x.b, x.k0 + j * kBN + part * box, p.err) : -1;
+      };
+      auto ask = [&](const CUtensorMap* tm, int stage, uint32_t bar, const Work& x, int j, int n, int page) {
+        if (part < n)   // (a page that is not in the pool: zeros)
+          tma_load_4d_hint(sKV + stage * C::TILE + kb * kBN * 128 + part * box * 128, tm, bar, kb * 64,
+                           (x.k0 + j * kBN + part * box) & ((1 << p.cache.shift) - 1), x.hk, page, pol_kv);
+      };
+      auto load_q = [&](const Work& x) {   // once the previous piece's last Q K^T is done
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i >= x.halves) break;
+          ok = wait_all(bar_qfree(i), (nq[i] & 1) ^ 1, kErrProducer);
+          if (!ok) return;
+          if (leader) {
+            mbar_arrive_expect_tx(bar_q(i), q_bytes);
+            const int token = (x.rt * p.tile_rows + i * p.half_rows) / share;
+#pragma unroll
+            for (int c = 0; c < C::KB; ++c)
+              tma_load_4d_hint(sQ + i * C::TILE + c * kBM * 128, &tm_q, bar_q(i), c * 64, x.hk * share, token, x.b, pol_q);
+          }
+          __syncwarp();
+          ++nq[i];
+        }
+      };
+      if (have && ok) {
+        const int n = boxes(w, 0), page = page_of(w, 0, n);
+        if (leader) mbar_arrive_expect_tx(bar_full(0), n * box * C::ROW);
+        __syncwarp();
+        if (lane < 16) ask(&tm_k, 0, bar_full(0), w, 0, n, page);
+        __syncwarp();
+        ld = 1;
+        load_q(w);
+      }
+      while (have && ok) {
+        Work wn;
+        const bool more_units = walk.step(p, wn);
+        // (the next Q tiles into L2 while this piece runs)
+        if (more_units && leader)
+          for (int i = 0; i < wn.halves; ++i)
+#pragma unroll
+            for (int c = 0; c < C::KB; ++c)
+              tma_prefetch_l2_4d(&tm_q, c * 64, wn.hk * share, (wn.rt * p.tile_rows + i * p.half_rows) / share, wn.b);
+        for (int j = 0; j < w.n && ok; ++j) {
+          const bool in_unit = j + 1 < w.n, more = in_unit || more_units;
+          const int sv = ld % C::STAGES, sk = (ld + 1) % C::STAGES;
+          const Work& kw = in_unit ? w : wn;
+          const int kj = in_unit ? j + 1 : 0;
+          const int nv = boxes(w, j), nk = more ? boxes(kw, kj) : 0;
+          const int page = lane < 16 ? page_of(w, j, nv) : more ? page_of(kw, kj, nk) : -1;
+          ok = wait_all(bar_empty(sv), ((ld / C::STAGES) & 1) ^ 1, kErrProducer);
+          if (ok && more) ok = wait_all(bar_empty(sk), (((ld + 1) / C::STAGES) & 1) ^ 1, kErrProducer);
+          if (!ok) break;
+          const uint32_t bar = more ? bar_full(sk) : bar_full(sv);
+          if (leader) mbar_arrive_expect_tx(bar, (nv + nk) * box * C::ROW);
+          __syncwarp();
+          if (lane < 16)
+            ask(&tm_v, sv, bar, w, j, nv, page);
+          else
+            ask(&tm_k, sk, bar, kw, kj, nk, page);
+          __syncwarp();
+          ld += more ? 2 : 1;
+        }
+        if (ok && more_units) load_q(wn);
+        have = more_units;
+        w = wn;
+      }
+      if (!ok && leader) {
+        // leave no copy in flight into this CTA's shared memory
+        for (int x = ld > C::STAGES ? ld - C::STAGES : 0; x < ld; ++x) {
+          if (x % 2 == 0)
+            mbar_drain(bar_full(x % C::STAGES), (x / C::STAGES) & 1, p.timeout_ns);
+          else if (x + 1 >= ld)   // (a last V tile alone)
+            mbar_drain(bar_full(x % C::STAGES), 0, p.timeout_ns);
+        }
+        for (int i = 0; i < 2; ++i)
+          if (nq[i] > 0) mbar_drain(bar_q(i), (nq[i] - 1) & 1, p.timeout_ns);
+      }
+      __syncwarp();
+    } else if (warp == kWarpMma) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024), k_desc = smem_desc_sw128(sKV, 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(sKV, kBN * 128, 1024);
+      const uint32_t hi = static_cast<uint32_t>(q_desc >> 32);   // (shared by all: low words hold the address)
+      // (tests come before the descriptors are built, waits only where a test failed)
+      uint32_t g = 0;                // key tiles so far, over all pieces
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, nc = 0;
+      bool ok = true;
+      // a piece's first scores, query tile by query tile (its K tile is here)
+      auto first_qk = [&](const Work& x, uint32_t at) {
+        const uint32_t s = at % C::STAGES;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i >= x.halves) break;
+          ok = wait_all(bar_q(i), nq[i] & 1, kErrMma);
+          if (!ok) return;
+          ++nq[i];
+          uint32_t a[C::QK], b[C::QK];
+#pragma unroll
+          for (int kk = 0; kk < C::QK; ++kk) {
+            const uint32_t off = ((kk / 4) * (kBM * 128) + (kk % 4) * 32) >> 4;
+            a[kk] = static_cast<uint32_t>(q_desc) + ((i * C::TILE) >> 4) + off;
+            b[kk] = static_cast<uint32_t>(k_desc) + ((s * C::TILE) >> 4) + off;
+          }
+          tc_fence_after();
+          if (leader) {
+            mma_group<C::QK, true>(tmem + i * kBN, a, b, hi, C::IDESC_QK, 0u);
+            mma_commit(bar_s(i));
+            if (x.n == 1) mma_commit(bar_qfree(i));
+            if (i == x.halves - 1) mma_commit(bar_empty(s));
+          }
+          __syncwarp();
+        }
+      };
+      if (have) {
+        ok = wait_all(bar_full(0), 0, kErrMma);
+        if (ok) first_qk(w, 0);
+      }
+      while (have && ok) {
+        Work wn;
+        const bool more_units = walk.step(p, wn);
+        for (int j = 0; j < w.n; ++j, ++g) {
+          const bool more = j + 1 < w.n, two = w.halves == 2;
+          const uint32_t sv = (2 * g + 1) % C::STAGES, lk = 2 * g + 2, sk = lk % C::STAGES;
+          const bool pair = more || more_units;
+          const uint32_t kv_bar = pair ? bar_full(sk) : bar_full(sv), kv_ph = pair ? (lk / C::STAGES) & 1 : 0u;
+          const bool kv_now = mbar_test(kv_bar, kv_ph);
+          const bool p0_now = !PAIR && mbar_test(bar_p(0), np[0] & 1);
+          const uint32_t vb = static_cast<uint32_t>(v_desc) + ((sv * C::TILE) >> 4);
+          const uint32_t kb = static_cast<uint32_t>(k_desc) + ((sk * C::TILE) >> 4);
+          uint32_t vd[C::PV], kd[C::QK], qd[C::QK], pa[C::PV];
+#pragma unroll
+          for (int kk = 0; kk < C::PV; ++kk) {
+            vd[kk] = vb + ((kk * 16 * 128) >> 4);
+            pa[kk] = tmem + kk * 8;
+          }
+#pragma unroll
+          for (int kk = 0; kk < C::QK; ++kk) {
+            const uint32_t off = ((kk / 4) * (kBM * 128) + (kk % 4) * 32) >> 4;
+            kd[kk] = kb + off;
+            qd[kk] = static_cast<uint32_t>(q_desc) + off;
+          }
+          ok = __all_sync(0xffffffffu, kv_now) || wait_all(kv_bar, kv_ph, kErrMma);
+          if (!ok) break;
+          const bool dirty = w.drafts(j);
+          if (dirty) {
+            if (leader) mbar_arrive(bar_dirty);
+            __syncwarp();
+          }
+          // before the tile's first P V
+          auto cleaned = [&]() {
+            if (!dirty) return true;
+            const bool r = wait_all(bar_clean, nc & 1, kErrMma);
+            ++nc;
+            return r;
+          };
+          if constexpr (PAIR) {
+            const int i = j & 1;
+            if (more && leader) {
+              // (S_1-i's last P V was issued a step ago)
+              tc_fence_after();
+              mma_group<C::QK, true>(tmem + (i ^ 1) * kBN, qd, kd, hi, C::IDESC_QK, 0u);
+              mma_commit(bar_s(i ^ 1));
+              if (j + 2 == w.n) mma_commit(bar_qfree(0));
+              mma_commit(bar_empty(sk));
+            }
+            __syncwarp();
+            ok = cleaned() && wait_all(bar_p(i), np[i] & 1, kErrMma);
+            if (!ok) break;
+            ++np[i];
+#pragma unroll
+            for (int kk = 0; kk < C::PV; ++kk) pa[kk] += i * kBN;
+            tc_fence_after();
+            if (leader) {
+              mma_group<C::PV, false>(tmem + C::O_COL + i * D, pa, vd, hi, C::IDESC_PV, j > 1);
+              mma_commit(bar_empty(sv));
+              if (j + 2 >= w.n) mma_commit(bar_o(i));
+            }
+            __syncwarp();
+            continue;
+          }
+          ok = __all_sync(0xffffffffu, p0_now) || wait_all(bar_p(0), np[0] & 1, kErrMma);
+          if (!ok || !(ok = cleaned())) break;
+          ++np[0];
+          const bool p1_now = two && mbar_test(bar_p(1), np[1] & 1);
+          tc_fence_after();
+          if (leader) {
+            mma_group<C::PV, false>(tmem + C::O_COL, pa, vd, hi, C::IDESC_PV, j > 0);
+            if (!two) mma_commit(bar_empty(sv));
+            if (more) {
+              mma_group<C::QK, true>(tmem, qd, kd, hi, C::IDESC_QK, 0u);
+              mma_commit(bar_s(0));
+              if (j + 2 == w.n) mma_commit(bar_qfree(0));
+              if (!two) mma_commit(bar_empty(sk));
+            } else {
+              mma_commit(bar_o(0));
+            }
+          }
+          __syncwarp();
+          if (!two) continue;
+#pragma unroll
+          for (int kk = 0; kk < C::PV; ++kk) pa[kk] += kBN;
+#pragma unroll
+          for (int kk = 0; kk < C::QK; ++kk) qd[kk] += C::TILE >> 4;
+          ok = __all_sync(0xffffffffu, p1_now) || wait_all(bar_p(1), np[1] & 1, kErrMma);
+          if (!ok) break;
+          ++np[1];
+          tc_fence_after();
+          if (leader) {
+            mma_group<C::PV, false>(tmem + C::O_COL + D, pa, vd, hi, C::IDESC_PV, j > 0);
+            mma_commit(bar_empty(sv));
+            if (more) {
+              mma_group<C::QK, true>(tmem + kBN, qd, kd, hi, C::IDESC_QK, 0u);
+              mma_commit(bar_s(1));
+              if (j + 2 == w.n) mma_commit(bar_qfree(1));
+              mma_commit(bar_empty(sk));
+            } else {
+              mma_commit(bar_o(1));
+            }
+          }
+          __syncwarp();
+        }
+        if (ok && more_units) first_qk(wn, 2 * g);
+        have = more_units;
+        w = wn;
+      }
+      if (!ok && leader) {
+        // let every MMA already issued finish before TMEM is released
+        mma_commit(bar_drain);
+        mbar_drain(bar_drain, 0, p.timeout_ns);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------- cleaners
+      const int half = warp - kWarpClean;
+      uint32_t g = 0, nd = 0;
+      int number = 0;
+      for (bool ok = true; have && ok; have = walk.step(p, w), ++number) {
+        for (int j = 0; j < w.n && ok; ++j, ++g) {
+          if (!w.drafts(j)) continue;
+          ok = wait_all(bar_dirty, nd & 1, kErrClean);
+          if (!ok) break;
+          ++nd;
+          const int start = w.k0 + j * kBN, valid = min(kBN, w.k1 - start);
+          const int from = w.count > 1 ? max(0, w.len - start) : valid;   // (a lone draft: its rows see it)
+          uint8_t* tile = smem + (2 + (2 * g + 1) % C::STAGES) * C::TILE;
+          bool found = false;
+#pragma unroll 4
+          for (int i = from * 8 + half * 32 + lane; i < kBN * 8; i += 64) {
+#pragma unroll
+            for (int c = 0; c < C::KB; ++c) {
+              uint4* at = reinterpret_cast<uint4*>(tile + c * kBN * 128 + i * 16);
+              if (i >= valid * 8)
+                *at = make_uint4(0, 0, 0, 0);
+              else
+                found |= clear_unfinite(at);
+            }
+          }
+          if (found) unclean[number % 8] = number;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (leader) mbar_arrive(bar_clean);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------- softmax, output
+    regs_increase<kSoftmaxRegs>();
+    const int wg = warp / 4, quarter = warp % 4;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_base + wg * kBN;
+    const uint32_t tO = tmem + lane_base + C::O_COL;   // (of the first sum)
+    const float sl2 = p.scale_log2;
+    uint8_t* stage = staging + warp * 2048;
+    uint32_t* path = all_paths + threadIdx.x * kTreeWords;
+    const int x = quarter * 32 + lane;                 // this thread's row of its query tile
+    int ns = 0, no[2] = {0, 0};
+    bool ok = true;
+    Walk<PAIR> walk;
+    walk.start(p);
+    Work w;
+    for (int number = 0; ok && walk.step(p, w); ++number) {
+      const bool whole = w.whole(), mine = PAIR || wg < w.halves;
+      const int place = (PAIR ? 0 : wg * kBM) + x, row = cache_row(p, w.rt, place);
+      const int token = row < 0 ? p.s_q : row / share;
+      const bool live = token < w.count;
+      float m = -INFINITY, l = 0.f;
+      if (mine && p.parents != nullptr) {
+        uint32_t bits[kTreeWords] = {};
+        int j = live ? token : -1;
+        while (j >= 0) {
+#pragma unroll
+          for (int c = 0; c < kTreeWords; ++c)
+            if (j / 32 == c) bits[c] |= 1u << (j % 32);
+          const int32_t* from = p.parents + w.b * p.parents_stride + j;
+          const int up = CPATTN_IN(p.parents_span, from, 4, p.err) ? *from : -1;
+          j = up < j ? up : -1;
+        }
+#pragma unroll
+        for (int c = 0; c < kTreeWords; ++c) path[c] = bits[c];
+      }
+      const int first = PAIR ? wg : 0;
+      for (int j = first; mine && j < w.n; j += PAIR ? 2 : 1) {
+        ok = wait_all(bar_s(wg), ns & 1, kErrSoftmax);
+        if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        uint32_t s[kBN];
+        float row_max;
+        if (!w.drafts(j)) {
+          tmem_ld_max_x128(tS, s, row_max);
+        } else {
+          const int start = w.k0 + j * kBN;
+          tmem_ld_x128(tS, s);
+          if (p.parents == nullptr) {
+            row_max = masked_row_max<kBN>(s, live ? w.len + token + 1 - start : 0);
+          } else {
+            unsigned long long seen[2] = {0ull, 0ull};
+            if (live) {
+              seen[0] = tree_window(path, w.len, start);
+              seen[1] = tree_window(path, w.len, start + 64);
+            }
+            row_max = masked_bits_max(s, seen);
+          }
+        }
+        const float top = row_max * sl2;
+        float factor = 1.f;
+        bool raise = false;
+        if (j == first) {
+          m = top;
+        } else if (top > m + kRescaleThreshold) {
+          factor = ex2_approx(m - top);
+          m = top;
+          l *= factor;
+          raise = true;
+        }
+        // (the previous P V completed before these scores: one issue order)
+        if (__any_sync(0xffffffffu, raise)) rescale_o<D>(tO + wg * D, factor);
+        // (only scores of -inf so far: their exponentials are 0, not of -inf + inf)
+        const float base = m == -INFINITY ? 0.f : -m;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kBN / 2; ++i) {
+          float x0, x1;
+          ffma2(x0, x1, u2f(s[2 * i]), u2f(s[2 * i + 1]), sl2, sl2, base, base);
+          const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+          const int a = 2 * (i & 1);
+          fadd2(acc[a], acc[a + 1], acc[a], acc[a + 1], e0, e1);
+          s[i] = pack_bf16x2(e0, e1);
+        }
+        tmem_st_x64(tS, *reinterpret_cast<uint32_t(*)[64]>(&s[0]));
+        l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p(wg));
+      }
+      if (ok && mine) {
+        for (int i = 0; i < (PAIR ? 2 : 1); ++i) {
+          const int o = PAIR ? i : wg;
+          if (PAIR && w.n <= i) continue;
+          ok = ok && wait_all(bar_o(o), no[i] & 1, kErrSoftmax);
+          ++no[i];
+        }
+      }
+      float own = 1.f, other = 0.f;     // weights of the first sum and the second
+      if constexpr (PAIR) {
+        sums[wg * kBM + x] = make_float2(m, l);
+        ok = vote_all(ok);
+        const float2 a = sums[x], b = sums[kBM + x];
+        m = fmaxf(a.x, b.x);
+        const float base = m == -INFINITY ? 0.f : m;
+        own = ex2_approx(a.x - base);
+        other = w.n > 1 ? ex2_approx(b.x - base) : 0.f;
+        l = a.y * own + b.y * other;
+      }
+      if (!ok) break;
+      tc_fence_after();
+      // every value that follows is this thread's row's; rows without a token: (0, -inf)
+      // (l is 0 where every score is -inf, too: no key has weight)
+      const bool none = !live || l == 0.f;
+      const float inv = none ? 0.f : whole ? 1.f / l : 1.f;
+      const bool add = !none && w.count > 1 && unclean[number % 8] == number;
+      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * R;
+      const int h = w.hk * share + (row < 0 ? 0 : row % share);
+      if (!PAIR || wg == 0) {
+        if (!whole) {
+          float2* dl = reinterpret_cast<float2*>(p.ws + static_cast<int64_t>(gridDim.x) * 2 * R * D) + part + place;
+          if (live && mine && CPATTN_IN(p.ws_span, dl, 8, p.err)) *dl = make_float2(m, l);
+        } else if (row >= 0) {
+          float* dl = static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + h * p.lse.s[1] + token * p.lse.s[2];
+          if (CPATTN_IN(p.lse.span, dl, 4, p.err)) *dl = none ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+        }
+      }
+      // 64 bytes of each of the warp's rows at a time through its stage: 32 features of
+      // a whole unit's result (bf16), 16 of a part's (fp32, not divided by l)
+      const int c_begin = PAIR ? wg * (D / 2) : 0, c_end = PAIR ? c_begin + D / 2 : D;
+      const uint32_t t_first = tO + (PAIR ? 0 : wg * D);
+      __syncwarp();
+#pragma unroll 1
+      for (int c0 = c_begin; c0 < c_end && (whole || mine); c0 += 32) {
+        uint32_t o[32];
+        if (mine) {
+          tmem_ld_x32(t_first + c0, o);
+          if (PAIR && w.n > 1) {
+            uint32_t o2[32];
+            tmem_ld_x32(tO + D + c0, o2);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * own + u2f(o2[i]) * other);
+          }
+        }
+        if (add) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            float4 v = make_float4(u2f(o[i]), u2f(o[i + 1]), u2f(o[i + 2]), u2f(o[i + 3]));
+            add_unfinite<__nv_bfloat16>(p, w, token, p.parents != nullptr ? path : nullptr, w.k0, w.k1, c0 + i, v);
+            o[i] = f2u(v.x);
+            o[i + 1] = f2u(v.y);
+            o[i + 2] = f2u(v.z);
+            o[i + 3] = f2u(v.w);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = none ? 0u : f2u(u2f(o[i]) * inv);
+        uint4* srow = reinterpret_cast<uint4*>(stage) + lane * 4;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (whole && half == 1) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 v;
+            if (whole)
+              v = make_uint4(pack_bf16x2(u2f(o[8 * i]), u2f(o[8 * i + 1])), pack_bf16x2(u2f(o[8 * i + 2]), u2f(o[8 * i + 3])),
+                             pack_bf16x2(u2f(o[8 * i + 4]), u2f(o[8 * i + 5])),
+                             pack_bf16x2(u2f(o[8 * i + 6]), u2f(o[8 * i + 7])));
+            else
+              v = make_uint4(o[16 * half + 4 * i], o[16 * half + 4 * i + 1], o[16 * half + 4 * i + 2], o[16 * half + 4 * i + 3]);
+            srow[i ^ ((lane >> 1) & 3)] = v;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int r = it * 8 + lane / 4, c = lane % 4;   // (row of the warp, 16-byte chunk)
+            const uint4 v = reinterpret_cast<const uint4*>(stage)[r * 4 + (c ^ ((r >> 1) & 3))];
+            const int pl = place - lane + r;
+            const int rw = cache_row(p, w.rt, pl);
+            if (rw < 0) continue;
+            const int tk = rw / share;
+            if (whole) {
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out.data) + w.b * p.out.s[0] +
+                                   (w.hk * share + rw - tk * share) * p.out.s[1] + tk * p.out.s[2] + c0 + c * 8;
+              if (CPATTN_IN(p.out.span, dst, 16, p.err)) *reinterpret_cast<uint4*>(dst) = v;
+            } else if (tk < w.count) {
+              float* dst = p.ws + (part + pl) * D + c0 + half * 16 + c * 4;
+              if (CPATTN_IN(p.ws_span, dst, 16, p.err)) *reinterpret_cast<uint4*>(dst) = v;
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if constexpr (PAIR) {
+        // (the other group's sum has been read, and so have m and l)
+        tc_fence_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  cache_empty_units<__nv_bfloat16, R, kBN, D>(p);
+}
+
+template <int D, bool PAIR>
+cudaError_t launch_typed(const CacheMaps& m, const CacheParams& p, int blocks, cudaStream_t stream) {
+  auto kernel = cache_fwd_kernel<D, PAIR>;
+  static std::atomic<unsigned long long> ready{0};
+  cudaError_t e = cross_set_up(kernel, Cfg<D>::SMEM, ready, kLaunchRegs);
+  if (e != cudaSuccess) return e;
+  e = launch_behind(kernel, dim3(blocks), kThreads, Cfg<D>::SMEM, stream, m.q, m.k, m.v, p);
+  if (e != cudaSuccess || !p.split) return e;
+  return cache_join<PAIR ? 128 : 256, kBN, D, __nv_bfloat16>(p, blocks, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_fwd(int head_dim, int places, const CacheMaps& maps, const CacheParams& p, int blocks,
+                             cudaStream_t stream) {
+  if (head_dim == 64)
+    return places == 128 ? launch_typed<64, true>(maps, p, blocks, stream) : launch_typed<64, false>(maps, p, blocks, stream);
+  return places == 128 ? launch_typed<128, true>(maps, p, blocks, stream) : launch_typed<128, false>(maps, p, blocks, stream);
+}
+
+}  // namespace cpattn

@@ -40,16 +40,7 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-}  // namespace cpattn
-
-namespace {
-
-using namespace cpattn;
-
-// 4-D map over a [B, H, S, D] tensor: dims (D, S, H, B), box (128 bytes of D,
-// box_rows rows, 1, 1), 128-byte swizzle, zero fill out of bounds; with
-// half_rows, 64 bytes of D and no swizzle.
-cpattn_status make_tmap(CUtensorMap* m, const cpattn_tensor* t, int box_rows, bool half_rows = false) {
+cpattn_status make_tmap(CUtensorMap* m, const cpattn_tensor* t, int box_rows, bool half_rows) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return CPATTN_ERR_CUDA;
   const int eb = elem_bytes(t->dtype);
@@ -70,6 +61,12 @@ cpattn_status make_tmap(CUtensorMap* m, const cpattn_tensor* t, int box_rows, bo
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? CPATTN_OK : CPATTN_ERR_CUDA;
 }
+
+}  // namespace cpattn
+
+namespace {
+
+using namespace cpattn;
 
 // Key partition of the ring (plain: S/R each; Ring Anything: the first
 // S mod R chunks one longer).
