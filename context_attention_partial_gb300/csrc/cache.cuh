@@ -106,8 +106,8 @@ struct CachePiece {
 // then key head; block c takes the c-th of `blocks` equal stretches of the line's key
 // tiles, so its pieces are the end of a unit, whole units, and the beginning of one.
 // A piece that is not a whole unit goes to the workspace: slot 0 of the block if it
-// begins inside its unit, slot 1 if it only ends there; the join kernel finds a
-// unit's parts by the same arithmetic.  Not split: whole units, c, c + blocks, ...
+// begins inside its unit, slot 1 if it only ends there; the blocks that begin and end
+// a unit note themselves for the join kernel.  Not split: whole units, c, c + blocks, ...
 // R: rows of a row tile, KT: keys of a key tile.  Whole warps.
 template <int R, int KT>
 struct CacheWalk {
@@ -157,21 +157,18 @@ struct CacheWalk {
     }
     x = pairs;
   }
-  __device__ void measure(const CacheParams& p, int most) {   // total and blocks
-    pairs = p.batch * p.row_tiles;
-    total = 0;
-    for (int i = threadIdx.x % 32; i < pairs; i += 32) {
-      int len, count;
-      total += static_cast<long long>(tiles_of(p, i, &len, &count)) * p.kv_heads;
-    }
-    total = warp_sum(total);
-    const long long most_blocks = (total + cache_min_tiles(KT) - 1) / cache_min_tiles(KT);
-    blocks = static_cast<int>(most_blocks < 1 ? 1 : most_blocks < most ? most_blocks : most);
-  }
   __device__ void start(const CacheParams& p) {
     pos = end = base = 0;
+    pairs = p.batch * p.row_tiles;
     if (p.split) {
-      measure(p, gridDim.x);
+      total = 0;
+      for (int i = threadIdx.x % 32; i < pairs; i += 32) {
+        int len, count;
+        total += static_cast<long long>(tiles_of(p, i, &len, &count)) * p.kv_heads;
+      }
+      total = warp_sum(total);
+      const long long most = (total + cache_min_tiles(KT) - 1) / cache_min_tiles(KT);
+      blocks = static_cast<int>(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
       if (blockIdx.x >= blocks || total == 0) return;
       pos = begin_of(blockIdx.x);
       end = begin_of(blockIdx.x + 1);
@@ -214,6 +211,21 @@ struct CacheWalk {
   }
 };
 
+// First and last block of every unit, behind the parts in the workspace.
+template <int R, int D>
+__device__ __forceinline__ int2* cache_unit_blocks(const CacheParams& p, int most) {
+  return reinterpret_cast<int2*>(p.ws + static_cast<int64_t>(most) * 2 * R * (D + 2));
+}
+// Notes for the join that this block begins or ends the piece's unit (one thread).
+template <int R, int D>
+__device__ __forceinline__ void cache_note_unit(const CacheParams& p, const CachePiece& w) {
+  if (!p.split) return;
+  int2* at = cache_unit_blocks<R, D>(p, gridDim.x) + (static_cast<int64_t>(w.b) * p.row_tiles + w.rt) * p.kv_heads + w.hk;
+  if (!CPATTN_IN(p.ws_span, at, 8, p.err)) return;
+  if (w.t0 == 0) at->x = blockIdx.x;
+  if (w.t1 == w.tiles) at->y = blockIdx.x;
+}
+
 // A unit without keys: (0, -inf) for its rows that exist.  All threads of the block,
 // which share the units without keys out by their number.
 template <typename T, int R, int KT, int D>
@@ -225,6 +237,10 @@ __device__ __forceinline__ void cache_empty_units(const CacheParams& p) {
     int len, count;
     if (CacheWalk<R, KT>::tiles_of(p, x, &len, &count) != 0) continue;
     const int b = x / p.row_tiles, rt = x - b * p.row_tiles;
+    if (p.split && threadIdx.x == 0) {   // (nothing to join)
+      int2* at = cache_unit_blocks<R, D>(p, gridDim.x) + u;
+      if (CPATTN_IN(p.ws_span, at, 8, p.err)) *at = make_int2(0, 0);
+    }
     constexpr int C = D * sizeof(T) / 16;
     for (int i = threadIdx.x; i < R * C; i += blockDim.x) {
       const int row = cache_row(p, rt, i / C);
@@ -354,54 +370,25 @@ __device__ __forceinline__ void cache_write_row(const CacheParams& p, int b, int
 }
 
 // Joins the parts of split units (see CacheWalk).  O and (m, l), m in base 2, as a
-// block left them: [block][slot][R][D] floats, then [block][slot][R] pairs.
-// `most`: blocks of the attention's launch.
+// block left them: [block][slot][R][D] floats, then [block][slot][R] pairs, then each
+// unit's first and last block.  `most`: blocks of the attention's launch.
 template <int R, int KT, int D, typename T>
 __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ CacheParams p, int most) {
-  __shared__ long long range[2];
-  __shared__ int parts[4];
   launch_wait();
   launch_next();
+  const int2* at_unit = cache_unit_blocks<R, D>(p, most) + blockIdx.x;
+  int2 blocks = make_int2(0, 0);
+  if (CPATTN_IN(p.ws_span, at_unit, 8, p.err)) blocks = *at_unit;
+  const int c0 = blocks.x, c1 = blocks.y;
+  // (written by its block; or, behind a wait that ran out, not noted)
+  if (c0 < 0 || c0 >= c1 || c1 >= most) return;
   const int hk = blockIdx.x % p.kv_heads, x = blockIdx.x / p.kv_heads;
-  if (threadIdx.x < 32) {
-    CacheWalk<R, KT> w;
-    w.measure(p, most);
-    // tiles of the pairs before x
-    long long before = 0;
-    for (int i = threadIdx.x; i < x; i += 32) {
-      int len, count;
-      before += static_cast<long long>(CacheWalk<R, KT>::tiles_of(p, i, &len, &count)) * p.kv_heads;
-    }
-    before = CacheWalk<R, KT>::warp_sum(before);
-    int len, count;
-    const int tiles = CacheWalk<R, KT>::tiles_of(p, x, &len, &count);
-    const long long u0 = before + static_cast<long long>(hk) * tiles, u1 = u0 + tiles;
-    if (threadIdx.x == 0) {
-      int c0 = 0, c1 = 0;
-      if (tiles > 0) {
-        c0 = static_cast<int>(u0 * w.blocks / w.total);
-        while (c0 + 1 < w.blocks && w.begin_of(c0 + 1) <= u0) ++c0;
-        while (c0 > 0 && w.begin_of(c0) > u0) --c0;
-        c1 = c0;
-        while (c1 + 1 < w.blocks && w.begin_of(c1 + 1) < u1) ++c1;
-      }
-      parts[0] = c0;
-      parts[1] = c1;
-      range[0] = u0;
-      range[1] = w.total;
-      parts[2] = w.blocks;
-      parts[3] = count;
-    }
-  }
-  __syncthreads();
-  const int c0 = parts[0], c1 = parts[1];
-  if (c0 == c1) return;   // (written by its block)
-  const int share = p.heads / p.kv_heads, blocks = parts[2], count = parts[3];
+  const int share = p.heads / p.kv_heads;
   const int b = x / p.row_tiles, rt = x - b * p.row_tiles;
-  const long long u0 = range[0], total = range[1];
+  const int count = cache_count(p.cache, b, p.s_q, p.err);
   const float2* ml = reinterpret_cast<const float2*>(p.ws + static_cast<int64_t>(most) * 2 * R * D);
-  // (slot 1: the block's range begins at or before the unit)
-  auto slot = [&](int c) { return static_cast<int64_t>(c) * 2 + (total * c / blocks > u0 ? 0 : 1); };
+  // (the first block only ends in the unit's tiles, the others begin in them)
+  auto slot = [&](int c) { return static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0); };
   for (int i = blockIdx.y * 256 + threadIdx.x; i < R * (D / 4); i += 256 * gridDim.y) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     const int row = cache_row(p, rt, r);

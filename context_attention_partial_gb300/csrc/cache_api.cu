@@ -262,7 +262,7 @@ CachePlan cache_plan(const cpattn_tensor* q, const cpattn_tensor* key_pages, con
   c.split = most > least && units < kCacheWholeUnits * slots;
   const int64_t want = c.split ? (units * most + least - 1) / least : units;
   c.blocks = static_cast<int>(want < slots ? want : slots);
-  c.workspace = c.split ? static_cast<size_t>(c.blocks) * 2 * c.places * (D + 2) * 4 : 0;
+  c.workspace = c.split ? static_cast<size_t>(c.blocks) * 2 * c.places * (D + 2) * 4 + units * 8 : 0;
   return c;
 }
 

@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kThreads) cache_f32_kernel(const __grid_consta
   walk.start(p);
   CachePiece w;
   while (walk.next(p, w)) {
+    if (threadIdx.x == 0) cache_note_unit<R, D>(p, w);
     const int k_begin = w.t0 * kKeys, k_end = min(w.len + w.count, w.t1 * kKeys), tiles = w.t1 - w.t0;
     auto load = [&](int t) {
       if (t < tiles) {

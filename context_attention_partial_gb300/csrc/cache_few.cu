@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
   walk.start(p);
   CachePiece w;
   while (walk.next(p, w)) {
+    if (threadIdx.x == 0) cache_note_unit<R, D>(p, w);
     const int k_begin = w.t0 * kKeys, k_end = min(w.len + w.count, w.t1 * kKeys), tiles = w.t1 - w.t0;
     // page numbers of a stage, at most four
     auto pages = [&](int t, int (&pg)[4]) {

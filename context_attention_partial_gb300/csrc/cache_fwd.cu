@@ -52,8 +52,9 @@ struct Cfg {
   static constexpr int STAGING = 8 * 32 * 64;             // 32 rows x 64 bytes per warp
   static constexpr int PATHS = 8 * 32 * kTreeWords * 4;   // a path per row
   static constexpr int SUMS = 2 * kBM * 8;                // PAIR: m and l of both sums
+  static constexpr int WALKS = 12 * 192;                  // a warp's walk and pieces
   static constexpr int BARS = 2 * STAGES + 13;
-  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + STAGING + PATHS + SUMS + BARS * 8 + 48;
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + STAGING + PATHS + SUMS + WALKS + BARS * 8 + 48;
   static constexpr int QK = ROW / 32, PV = kBN / 16;      // MMAs of a tile product
   static constexpr int KB = ROW / 128;                    // 128-byte column blocks
   static constexpr int O_COL = 2 * kBN;
@@ -75,35 +76,54 @@ __device__ __forceinline__ bool vote_all(bool ok) {
   return r != 0;
 }
 
-// Largest of the scores whose bits are set; the others are set to -inf in place.
-__device__ __forceinline__ float masked_bits_max(uint32_t (&s)[128], const unsigned long long (&seen)[2]) {
-  float mx[2] = {-INFINITY, -INFINITY};
+// Sets the scores 32 C .. 32 C + 31 whose bits are not set to -inf.
+template <int C>
+__device__ __forceinline__ void mask_scores(uint32_t (&s)[128], uint32_t seen) {
 #pragma unroll
-  for (int i = 0; i < 128; ++i) {
-    if (!((seen[i / 64] >> (i % 64)) & 1)) s[i] = f2u(-INFINITY);
-    mx[i & 1] = fmaxf(mx[i & 1], u2f(s[i]));
-  }
-  return fmaxf(mx[0], mx[1]);
+  for (int i = 0; i < 32; ++i)
+    if (!((seen >> i) & 1u)) s[32 * C + i] = f2u(-INFINITY);
 }
 
 // A piece and what its roles derive from it.
 struct Work : CachePiece {
   int k0, k1;     // its keys
   int n;          // its key tiles
+  int drafts;     // the first of them that holds drafts
   int halves;     // query tiles with rows
-  __device__ bool drafts(int j) const { return k0 + (j + 1) * kBN > len; }   // key tile j holds some
 };
 
+// A warp's walk, this piece and the next: in shared memory, since the registers hold
+// tiles and descriptors (every lane writes the same).
 template <bool PAIR>
-struct Walk : CacheWalk<PAIR ? 128 : 256, kBN> {
-  __device__ bool step(const CacheParams& p, Work& w) {
-    if (!this->next(p, w)) return false;
-    w.k0 = w.t0 * kBN;
-    w.k1 = min(w.len + w.count, w.t1 * kBN);
-    w.n = w.t1 - w.t0;
-    const int share = p.heads / p.kv_heads;
-    w.halves = !PAIR && (w.rt * p.tile_rows + p.half_rows) / share < w.count ? 2 : 1;
-    return true;
+struct Walk {
+  CacheWalk<PAIR ? 128 : 256, kBN> walk;
+  Work piece[2];
+
+  __device__ void start(const CacheParams& p) {
+    CacheWalk<PAIR ? 128 : 256, kBN> first;
+    first.start(p);
+    walk = first;
+    __syncwarp();
+  }
+  // The next piece to piece[slot]; false: no more.
+  __device__ bool step(const CacheParams& p, int slot) {
+    __syncwarp();
+    CacheWalk<PAIR ? 128 : 256, kBN> at = walk;
+    Work w;
+    const bool more = at.next(p, w);
+    if (more) {
+      w.k0 = w.t0 * kBN;
+      w.k1 = min(w.len + w.count, w.t1 * kBN);
+      w.n = w.t1 - w.t0;
+      w.drafts = max(0, w.len - w.k0) / kBN;
+      const int share = p.heads / p.kv_heads;
+      w.halves = !PAIR && (w.rt * p.tile_rows + p.half_rows) / share < w.count ? 2 : 1;
+    }
+    __syncwarp();
+    walk = at;
+    if (more) piece[slot] = w;
+    __syncwarp();
+    return more;
   }
 };
 
@@ -119,7 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* staging = smem + (2 + C::STAGES) * C::TILE;
   uint32_t* all_paths = reinterpret_cast<uint32_t*>(staging + C::STAGING);
   float2* sums = reinterpret_cast<float2*>(staging + C::STAGING + C::PATHS);   // [2][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + C::STAGING + C::PATHS + C::SUMS);
+  uint8_t* walks = staging + C::STAGING + C::PATHS + C::SUMS;
+  static_assert(sizeof(Walk<PAIR>) <= 192, "a warp's walk");
+  uint64_t* bars = reinterpret_cast<uint64_t*>(walks + C::WALKS);
   const uint32_t bar0 = smem_addr(bars);
   auto bar_full = [&](int s) { return bar0 + 8u * s; };
   auto bar_empty = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
@@ -176,13 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, r) != 0;
   };
 
+  Walk<PAIR>& walk = *reinterpret_cast<Walk<PAIR>*>(walks + warp * 192);
+
   if (warp >= 8) {
     regs_decrease<kControlRegs>();
     const bool leader = elect_one();
-    Walk<PAIR> walk;
     walk.start(p);
-    Work w;
-    bool have = walk.step(p, w);
+    bool have = walk.step(p, 0);
     if (warp == kWarpProducer) {
       // ---------------------------------------------------------- producer
       // K tiles on even stages, V tiles on odd ones: the first K alone, then
@@ -224,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (have && ok) {
+        const Work& w = walk.piece[0];
         const int n = boxes(w, 0), page = page_of(w, 0, n);
         if (leader) mbar_arrive_expect_tx(bar_full(0), n * box * C::ROW);
         __syncwarp();
@@ -232,9 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ld = 1;
         load_q(w);
       }
-      while (have && ok) {
-        Work wn;
-        const bool more_units = walk.step(p, wn);
+      for (int number = 0; have && ok; ++number) {
+        const Work &w = walk.piece[number & 1], &wn = walk.piece[(number & 1) ^ 1];
+        const bool more_units = walk.step(p, (number & 1) ^ 1);
         // (the next Q tiles into L2 while this piece runs)
         if (more_units && leader)
           for (int i = 0; i < wn.halves; ++i)
@@ -263,7 +286,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && more_units) load_q(wn);
         have = more_units;
-        w = wn;
       }
       if (!ok && leader) {
         // leave no copy in flight into this CTA's shared memory
@@ -314,13 +336,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (have) {
         ok = wait_all(bar_full(0), 0, kErrMma);
-        if (ok) first_qk(w, 0);
+        if (ok) first_qk(walk.piece[0], 0);
       }
-      while (have && ok) {
-        Work wn;
-        const bool more_units = walk.step(p, wn);
-        for (int j = 0; j < w.n; ++j, ++g) {
-          const bool more = j + 1 < w.n, two = w.halves == 2;
+      for (int number = 0; have && ok; ++number) {
+        const bool more_units = walk.step(p, (number & 1) ^ 1);
+        const int n = walk.piece[number & 1].n, drafts = walk.piece[number & 1].drafts;
+        const bool two = walk.piece[number & 1].halves == 2;
+        for (int j = 0; j < n; ++j, ++g) {
+          const bool more = j + 1 < n;
           const uint32_t sv = (2 * g + 1) % C::STAGES, lk = 2 * g + 2, sk = lk % C::STAGES;
           const bool pair = more || more_units;
           const uint32_t kv_bar = pair ? bar_full(sk) : bar_full(sv), kv_ph = pair ? (lk / C::STAGES) & 1 : 0u;
@@ -342,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ok = __all_sync(0xffffffffu, kv_now) || wait_all(kv_bar, kv_ph, kErrMma);
           if (!ok) break;
-          const bool dirty = w.drafts(j);
+          const bool dirty = j >= drafts;
           if (dirty) {
             if (leader) mbar_arrive(bar_dirty);
             __syncwarp();
@@ -361,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
               mma_group<C::QK, true>(tmem + (i ^ 1) * kBN, qd, kd, hi, C::IDESC_QK, 0u);
               mma_commit(bar_s(i ^ 1));
-              if (j + 2 == w.n) mma_commit(bar_qfree(0));
+              if (j + 2 == n) mma_commit(bar_qfree(0));
               mma_commit(bar_empty(sk));
             }
             __syncwarp();
@@ -374,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader) {
               mma_group<C::PV, false>(tmem + C::O_COL + i * D, pa, vd, hi, C::IDESC_PV, j > 1);
               mma_commit(bar_empty(sv));
-              if (j + 2 >= w.n) mma_commit(bar_o(i));
+              if (j + 2 >= n) mma_commit(bar_o(i));
             }
             __syncwarp();
             continue;
@@ -390,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) {
               mma_group<C::QK, true>(tmem, qd, kd, hi, C::IDESC_QK, 0u);
               mma_commit(bar_s(0));
-              if (j + 2 == w.n) mma_commit(bar_qfree(0));
+              if (j + 2 == n) mma_commit(bar_qfree(0));
               if (!two) mma_commit(bar_empty(sk));
             } else {
               mma_commit(bar_o(0));
@@ -412,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) {
               mma_group<C::QK, true>(tmem + kBN, qd, kd, hi, C::IDESC_QK, 0u);
               mma_commit(bar_s(1));
-              if (j + 2 == w.n) mma_commit(bar_qfree(1));
+              if (j + 2 == n) mma_commit(bar_qfree(1));
               mma_commit(bar_empty(sk));
             } else {
               mma_commit(bar_o(1));
@@ -420,9 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (ok && more_units) first_qk(wn, 2 * g);
+        if (ok && more_units) first_qk(walk.piece[(number & 1) ^ 1], 2 * g);
         have = more_units;
-        w = wn;
       }
       if (!ok && leader) {
         // let every MMA already issued finish before TMEM is released
@@ -434,10 +456,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------- cleaners
       const int half = warp - kWarpClean;
       uint32_t g = 0, nd = 0;
+      const Work& w = walk.piece[0];
       int number = 0;
-      for (bool ok = true; have && ok; have = walk.step(p, w), ++number) {
-        for (int j = 0; j < w.n && ok; ++j, ++g) {
-          if (!w.drafts(j)) continue;
+      for (bool ok = true; have && ok; have = walk.step(p, 0), ++number) {
+        if (half == 0 && leader) cache_note_unit<R, D>(p, w);
+        g += min(w.drafts, w.n);
+        for (int j = w.drafts; j < w.n && ok; ++j, ++g) {
           ok = wait_all(bar_dirty, nd & 1, kErrClean);
           if (!ok) break;
           ++nd;
@@ -476,28 +500,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = quarter * 32 + lane;                 // this thread's row of its query tile
     int ns = 0, no[2] = {0, 0};
     bool ok = true;
-    Walk<PAIR> walk;
+    const Work& w = walk.piece[0];
     walk.start(p);
-    Work w;
-    for (int number = 0; ok && walk.step(p, w); ++number) {
-      const bool whole = w.whole(), mine = PAIR || wg < w.halves;
-      const int place = (PAIR ? 0 : wg * kBM) + x, row = cache_row(p, w.rt, place);
-      const int token = row < 0 ? p.s_q : row / share;
-      const bool live = token < w.count;
+    for (int number = 0; ok && walk.step(p, 0); ++number) {
+      const bool mine = PAIR || wg < w.halves;
+      const int place = (PAIR ? 0 : wg * kBM) + x;
       float m = -INFINITY, l = 0.f;
       if (mine && p.parents != nullptr) {
-        uint32_t bits[kTreeWords] = {};
-        int j = live ? token : -1;
-        while (j >= 0) {
 #pragma unroll
-          for (int c = 0; c < kTreeWords; ++c)
-            if (j / 32 == c) bits[c] |= 1u << (j % 32);
+        for (int c = 0; c < kTreeWords; ++c) path[c] = 0u;
+        const int row = cache_row(p, w.rt, place);
+        int j = row < 0 || row / share >= w.count ? -1 : row / share;
+        while (j >= 0) {
+          path[j / 32] |= 1u << (j % 32);
           const int32_t* from = p.parents + w.b * p.parents_stride + j;
           const int up = CPATTN_IN(p.parents_span, from, 4, p.err) ? *from : -1;
           j = up < j ? up : -1;
         }
-#pragma unroll
-        for (int c = 0; c < kTreeWords; ++c) path[c] = bits[c];
       }
       const int first = PAIR ? wg : 0;
       for (int j = first; mine && j < w.n; j += PAIR ? 2 : 1) {
@@ -507,21 +526,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t s[kBN];
         float row_max;
-        if (!w.drafts(j)) {
+        if (j < w.drafts) {
           tmem_ld_max_x128(tS, s, row_max);
         } else {
-          const int start = w.k0 + j * kBN;
           tmem_ld_x128(tS, s);
-          if (p.parents == nullptr) {
-            row_max = masked_row_max<kBN>(s, live ? w.len + token + 1 - start : 0);
-          } else {
-            unsigned long long seen[2] = {0ull, 0ull};
-            if (live) {
-              seen[0] = tree_window(path, w.len, start);
-              seen[1] = tree_window(path, w.len, start + 64);
-            }
-            row_max = masked_bits_max(s, seen);
-          }
+          const int start = w.k0 + j * kBN, row = cache_row(p, w.rt, place), token = row < 0 ? p.s_q : row / share;
+          const bool live = token < w.count;
+          // what the row sees of 32 keys at a time (seldom: the last tile or two of a unit)
+          auto seen = [&](int at) -> uint32_t {
+            if (!live) return 0u;
+            return static_cast<uint32_t>(p.parents == nullptr ? chain_window(w.len, token, at) : tree_window(path, w.len, at));
+          };
+          mask_scores<0>(s, seen(start));
+          mask_scores<1>(s, seen(start + 32));
+          mask_scores<2>(s, seen(start + 64));
+          mask_scores<3>(s, seen(start + 96));
+          row_max = masked_row_max<kBN>(s, kBN);
         }
         const float top = row_max * sl2;
         float factor = 1.f;
@@ -555,6 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p(wg));
       }
+      const bool whole = w.whole();
+      const int row = cache_row(p, w.rt, place), token = row < 0 ? p.s_q : row / share;
+      const bool live = token < w.count;
       if (ok && mine) {
         for (int i = 0; i < (PAIR ? 2 : 1); ++i) {
           const int o = PAIR ? i : wg;
