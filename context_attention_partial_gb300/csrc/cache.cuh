@@ -103,50 +103,58 @@ struct CachePiece {
 
 // Deals the key tiles out to the blocks, evenly, whatever the lengths are.  All (row
 // tile, key head) units of all sequences stand in a line, b slowest, then row tile,
-// then key head; block c takes the c-th of `blocks` equal stretches of the line's key
-// tiles, so its pieces are the end of a unit, whole units, and the beginning of one.
-// A piece that is not a whole unit goes to the workspace: slot 0 of the block if it
-// begins inside its unit, slot 1 if it only ends there; the blocks that begin and end
-// a unit note themselves for the join kernel.  Not split: whole units, c, c + blocks, ...
-// R: rows of a row tile, KT: keys of a key tile.  Whole warps.
-template <int R, int KT>
+// then key head; block c takes the c-th of `blocks` stretches of the line's key tiles
+// (equal, but for one tile), so its pieces are the end of a unit, whole units, and the
+// beginning of one.  A piece that is not a whole unit goes to the workspace: slot 0 of
+// the block if it begins inside its unit, slot 1 if it only ends there; the blocks
+// that begin and end a unit note themselves for the join kernel.  Not split: whole
+// units, c, c + blocks, ...
+// KT: keys of a key tile.  A split line has less than 2^31 tiles.  Whole warps.
+template <int KT>
 struct CacheWalk {
-  long long total, pos, end;  // tiles of the line; of this block: the next, one past the last
-  long long base;             // of pair x: its first
-  int blocks, x, pairs;       // pair: (b, row tile)
+  int pos, end;    // tiles of the line (not split: units): the next, one past the last
+  int base, x;     // pair (b, row tile) that holds the next; its first tile
 
   // Key tiles of pair x.
   __device__ static int tiles_of(const CacheParams& p, int x, int* len, int* count) {
-    const int b = x / p.row_tiles, rt = x - b * p.row_tiles, share = p.heads / p.kv_heads;
-    const int n = cache_count(p.cache, b, p.s_q, p.err);
+    const int b = x / p.row_tiles, first = (x - b * p.row_tiles) * p.tile_rows, share = p.heads / p.kv_heads;
     *len = cache_length(p.cache, b, p.err);
-    *count = n;
-    const int first = rt * p.tile_rows / share;
-    if (first >= n) return 0;   // (no row has a token)
+    *count = cache_count(p.cache, b, p.s_q, p.err);
+    if (first / share >= *count) return 0;   // (no row has a token)
     // a chain's rows see nothing past their last token
-    const int last = p.parents != nullptr ? n - 1 : min(n - 1, (rt * p.tile_rows + p.tile_rows - 1) / share);
+    const int last = p.parents != nullptr ? *count - 1 : min(*count - 1, (first + p.tile_rows - 1) / share);
     return (*len + last + KT) / KT;
   }
-  __device__ static long long warp_sum(long long v) {
-#pragma unroll
-    for (int m = 16; m > 0; m /= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
-    return v;
-  }
-  __device__ long long begin_of(long long c) const { return total * c / blocks; }
-  // Moves x and base to the pair that holds tile `at` of the line (at < total).
-  __device__ void find(const CacheParams& p, long long at) {
-    const int lane = threadIdx.x % 32;
-    base = 0;
+  __device__ void start(const CacheParams& p) {
+    pos = blockIdx.x;
+    end = p.batch * p.row_tiles * p.kv_heads;
+    base = x = 0;
+    if (!p.split) return;
+    const int lane = threadIdx.x % 32, pairs = p.batch * p.row_tiles;
+    unsigned total = 0;
     for (int x0 = 0; x0 < pairs; x0 += 32) {
       int len, count;
-      const long long w = x0 + lane < pairs ? static_cast<long long>(tiles_of(p, x0 + lane, &len, &count)) * p.kv_heads : 0;
-      long long sum = w;
+      total += __reduce_add_sync(
+          0xffffffffu, x0 + lane < pairs ? static_cast<unsigned>(tiles_of(p, x0 + lane, &len, &count) * p.kv_heads) : 0u);
+    }
+    unsigned blocks = (total + cache_min_tiles(KT) - 1) / cache_min_tiles(KT);
+    blocks = blocks < gridDim.x ? blocks : gridDim.x;
+    pos = end = 0;
+    if (blockIdx.x >= blocks) return;
+    const unsigned each = total / blocks, more = total - each * blocks;
+    pos = blockIdx.x * each + min(blockIdx.x, more);
+    end = pos + each + (blockIdx.x < more ? 1 : 0);
+    // the pair that holds pos
+    for (int x0 = 0; x0 < pairs; x0 += 32) {
+      int len, count;
+      const int w = x0 + lane < pairs ? tiles_of(p, x0 + lane, &len, &count) * p.kv_heads : 0;
+      int sum = w;
 #pragma unroll
       for (int m = 1; m < 32; m *= 2) {
-        const long long y = __shfl_up_sync(0xffffffffu, sum, m);
+        const int y = __shfl_up_sync(0xffffffffu, sum, m);
         if (lane >= m) sum += y;
       }
-      const unsigned behind = __ballot_sync(0xffffffffu, at < base + sum);
+      const unsigned behind = __ballot_sync(0xffffffffu, pos < base + sum);
       if (behind != 0) {
         const int i = __ffs(behind) - 1;
         x = x0 + i;
@@ -155,35 +163,13 @@ struct CacheWalk {
       }
       base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    x = pairs;
-  }
-  __device__ void start(const CacheParams& p) {
-    pos = end = base = 0;
-    pairs = p.batch * p.row_tiles;
-    if (p.split) {
-      total = 0;
-      for (int i = threadIdx.x % 32; i < pairs; i += 32) {
-        int len, count;
-        total += static_cast<long long>(tiles_of(p, i, &len, &count)) * p.kv_heads;
-      }
-      total = warp_sum(total);
-      const long long most = (total + cache_min_tiles(KT) - 1) / cache_min_tiles(KT);
-      blocks = static_cast<int>(most < 1 ? 1 : most < gridDim.x ? most : gridDim.x);
-      if (blockIdx.x >= blocks || total == 0) return;
-      pos = begin_of(blockIdx.x);
-      end = begin_of(blockIdx.x + 1);
-      find(p, pos);
-    } else {
-      pos = blockIdx.x;
-      end = static_cast<long long>(p.batch) * p.row_tiles * p.kv_heads;
-    }
   }
   // The next piece with keys; false: no more.
   __device__ bool next(const CacheParams& p, CachePiece& w) {
     while (pos < end) {
       if (!p.split) {
-        w.hk = static_cast<int>(pos % p.kv_heads);
-        x = static_cast<int>(pos / p.kv_heads);
+        x = pos / p.kv_heads;
+        w.hk = pos - x * p.kv_heads;
         pos += gridDim.x;
         w.tiles = tiles_of(p, x, &w.len, &w.count);
         if (w.tiles == 0) continue;
@@ -191,16 +177,15 @@ struct CacheWalk {
         w.t1 = w.tiles;
       } else {
         w.tiles = tiles_of(p, x, &w.len, &w.count);
-        const long long off = pos - base, all = static_cast<long long>(w.tiles) * p.kv_heads;
+        const int off = pos - base, all = w.tiles * p.kv_heads;
         if (off >= all) {
           base += all;
           ++x;
           continue;
         }
-        w.hk = static_cast<int>(off / w.tiles);
-        w.t0 = static_cast<int>(off - static_cast<long long>(w.hk) * w.tiles);
-        const long long left = end - pos;
-        w.t1 = left < w.tiles - w.t0 ? w.t0 + static_cast<int>(left) : w.tiles;
+        w.hk = off / w.tiles;
+        w.t0 = off - w.hk * w.tiles;
+        w.t1 = min(w.t0 + end - pos, w.tiles);
         pos += w.t1 - w.t0;
       }
       w.b = x / p.row_tiles;
@@ -226,23 +211,23 @@ __device__ __forceinline__ void cache_note_unit(const CacheParams& p, const Cach
   if (w.t1 == w.tiles) at->y = blockIdx.x;
 }
 
-// A unit without keys: (0, -inf) for its rows that exist.  All threads of the block,
-// which share the units without keys out by their number.
+// Units without keys: (0, -inf) for their rows that exist.  The blocks share the units
+// out by their number; thread t of `threads` of a block.
 template <typename T, int R, int KT, int D>
-__device__ __forceinline__ void cache_empty_units(const CacheParams& p) {
+__device__ __forceinline__ void cache_empty_units(const CacheParams& p, int t, int threads) {
   const int share = p.heads / p.kv_heads;
   const int64_t units = static_cast<int64_t>(p.batch) * p.row_tiles * p.kv_heads;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int x = static_cast<int>(u / p.kv_heads), hk = static_cast<int>(u % p.kv_heads);
     int len, count;
-    if (CacheWalk<R, KT>::tiles_of(p, x, &len, &count) != 0) continue;
+    if (CacheWalk<KT>::tiles_of(p, x, &len, &count) != 0) continue;
     const int b = x / p.row_tiles, rt = x - b * p.row_tiles;
-    if (p.split && threadIdx.x == 0) {   // (nothing to join)
+    if (p.split && t == 0) {   // (nothing to join)
       int2* at = cache_unit_blocks<R, D>(p, gridDim.x) + u;
       if (CPATTN_IN(p.ws_span, at, 8, p.err)) *at = make_int2(0, 0);
     }
     constexpr int C = D * sizeof(T) / 16;
-    for (int i = threadIdx.x; i < R * C; i += blockDim.x) {
+    for (int i = t; i < R * C; i += threads) {
       const int row = cache_row(p, rt, i / C);
       if (row < 0) continue;
       const int token = row / share, h = hk * share + row % share;
@@ -369,11 +354,38 @@ __device__ __forceinline__ void cache_write_row(const CacheParams& p, int b, int
   if (CPATTN_IN(p.lse.span, dl, 4, p.err)) *dl = none ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 
-// Joins the parts of split units (see CacheWalk).  O and (m, l), m in base 2, as a
-// block left them: [block][slot][R][D] floats, then [block][slot][R] pairs, then each
-// unit's first and last block.  `most`: blocks of the attention's launch.
-template <int R, int KT, int D, typename T>
-__global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ CacheParams p, int most) {
+// Where the workspace has features d .. d + 3 of place r of a part ([part][D / 4][R][4]:
+// neighbouring places are neighbours in memory), and its m (base 2) and l.  Parts: two
+// slots of each of the attention's `most` blocks.
+template <int R, int D>
+__device__ __forceinline__ float4* cache_part(const CacheParams& p, int64_t part, int r, int d) {
+  return reinterpret_cast<float4*>(p.ws + part * R * D) + (d / 4) * R + r;
+}
+template <int R, int D>
+__device__ __forceinline__ float2* cache_part_sums(const CacheParams& p, int most, int64_t part, int r) {
+  return reinterpret_cast<float2*>(p.ws + static_cast<int64_t>(most) * 2 * R * D) + part * R + r;
+}
+template <int R, int D>
+__device__ __forceinline__ void cache_write_part(const CacheParams& p, int64_t part, int r, int d, float4 sum, float m,
+                                                 float l) {
+  float4* dst = cache_part<R, D>(p, part, r, d);
+  float2* dl = cache_part_sums<R, D>(p, gridDim.x, part, r);
+  if (CPATTN_IN(p.ws_span, dst, 16, p.err)) *dst = sum;
+  if (d == 0 && CPATTN_IN(p.ws_span, dl, 8, p.err)) *dl = make_float2(m, l);
+}
+
+// Joins the parts of split units (see CacheWalk).  An item is 16 features of a row;
+// G threads share an item's parts out, so that all of them are on the way at once,
+// and meet in shared memory.  `most`: blocks of the attention's launch.
+constexpr int kJoinThreads = 256;
+template <int R, int D, typename T, int G>
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheParams p, int most) {
+  constexpr int I = kJoinThreads / G;   // items of a block
+  __shared__ float part_sums[G][16][I];
+  __shared__ float2 part_ml[G][I];
+  const int item = threadIdx.x % I, g = threadIdx.x / I;
+  const int hk = blockIdx.x % p.kv_heads, x = blockIdx.x / p.kv_heads;
+  const int share = p.heads / p.kv_heads, b = x / p.row_tiles, rt = x - b * p.row_tiles;
   launch_wait();
   launch_next();
   const int2* at_unit = cache_unit_blocks<R, D>(p, most) + blockIdx.x;
@@ -382,52 +394,81 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__
   const int c0 = blocks.x, c1 = blocks.y;
   // (written by its block; or, behind a wait that ran out, not noted)
   if (c0 < 0 || c0 >= c1 || c1 >= most) return;
-  const int hk = blockIdx.x % p.kv_heads, x = blockIdx.x / p.kv_heads;
-  const int share = p.heads / p.kv_heads;
-  const int b = x / p.row_tiles, rt = x - b * p.row_tiles;
   const int count = cache_count(p.cache, b, p.s_q, p.err);
-  const float2* ml = reinterpret_cast<const float2*>(p.ws + static_cast<int64_t>(most) * 2 * R * D);
-  // (the first block only ends in the unit's tiles, the others begin in them)
-  auto slot = [&](int c) { return static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0); };
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < R * (D / 4); i += 256 * gridDim.y) {
-    const int r = i / (D / 4), d = i % (D / 4) * 4;
+  {
+    const int i = blockIdx.y * I + item, r = i % R, d = i / R * 16;
     const int row = cache_row(p, rt, r);
-    if (row < 0) continue;
-    const int token = row / share, h = hk * share + row % share;
-    const int last = token < count ? c1 : c0 - 1;   // (no parts for a row without a token)
-    float top = -INFINITY;
-    for (int c = c0; c <= last; ++c) {
-      const float2* at = ml + slot(c) * R + r;
-      if (CPATTN_IN(p.ws_span, at, 8, p.err)) top = fmaxf(top, at->x);
+    float m = -INFINITY, l = 0.f;
+    float4 sum[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row >= 0 && d < D && row / share < count)   // (no parts for a row without a token)
+#pragma unroll 2
+      for (int c = c0 + g; c <= c1; c += G) {
+        // (the first block only ends in the unit's tiles, the others begin in them)
+        const int64_t part = static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0);
+        const float2* at = cache_part_sums<R, D>(p, most, part, r);
+        const float2 a = CPATTN_IN(p.ws_span, at, 8, p.err) ? *at : make_float2(-INFINITY, 0.f);
+        float4 y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4* o = cache_part<R, D>(p, part, r, d + 4 * e);
+          y[e] = CPATTN_IN(p.ws_span, o, 16, p.err) ? *o : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (a.y == 0.f) continue;   // (no key of this part)
+        const float top = fmaxf(m, a.x), base = top == -INFINITY ? 0.f : top;
+        const float f0 = ex2_approx(m - base), f1 = ex2_approx(a.x - base);
+        m = top;
+        l = l * f0 + a.y * f1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sum[e] = make_float4(sum[e].x * f0 + y[e].x * f1, sum[e].y * f0 + y[e].y * f1, sum[e].z * f0 + y[e].z * f1,
+                               sum[e].w * f0 + y[e].w * f1);
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      part_sums[g][4 * e][item] = sum[e].x;
+      part_sums[g][4 * e + 1][item] = sum[e].y;
+      part_sums[g][4 * e + 2][item] = sum[e].z;
+      part_sums[g][4 * e + 3][item] = sum[e].w;
     }
-    const float base = top == -INFINITY ? 0.f : top;
+    part_ml[g][item] = make_float2(m, l);
+  }
+  __syncthreads();
+  // four threads an item, four features each
+  for (int t = threadIdx.x; t < I * 4; t += kJoinThreads) {
+    const int it = t / 4, i = blockIdx.y * I + it, r = i % R, e = t % 4 * 4, d = i / R * 16 + e;
+    const int row = cache_row(p, rt, r);
+    if (row < 0 || d >= D) continue;
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < G; ++k) m = fmaxf(m, part_ml[k][it].x);
+    const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = c0; c <= last; ++c) {
-      const int64_t s = slot(c);
-      const float2* at = ml + s * R + r;
-      const float4* o = reinterpret_cast<const float4*>(p.ws + (s * R + r) * D + d);
-      if (!CPATTN_IN(p.ws_span, at, 8, p.err) || !CPATTN_IN(p.ws_span, o, 16, p.err)) continue;
-      const float2 a = *at;
-      const float4 y = *o;
-      const float f = exp2f(a.x - base);
-      if (a.y == 0.f) continue;   // (no key of this part)
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      const float2 a = part_ml[k][it];
+      if (a.y == 0.f) continue;
+      const float f = ex2_approx(a.x - base);
       l = fmaf(f, a.y, l);
-      sum = make_float4(fmaf(f, y.x, sum.x), fmaf(f, y.y, sum.y), fmaf(f, y.z, sum.z), fmaf(f, y.w, sum.w));
+      sum = make_float4(fmaf(f, part_sums[k][e][it], sum.x), fmaf(f, part_sums[k][e + 1][it], sum.y),
+                        fmaf(f, part_sums[k][e + 2][it], sum.z), fmaf(f, part_sums[k][e + 3][it], sum.w));
     }
-    cache_write_row<T>(p, b, h, token, d, sum, top, l);
+    cache_write_row<T>(p, b, hk * share + row % share, row / share, d, sum, m, l);
   }
 }
 
-
 // Launches the join behind an attention of `most` blocks.
-template <int R, int KT, int D, typename T>
+template <int R, int D, typename T>
 cudaError_t cache_join(const CacheParams& p, int most, cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(p.batch) * p.row_tiles * p.kv_heads;
-  const int y = R * (D / 4) / 256;   // an item a thread
-  return launch_behind(cache_join_kernel<R, KT, D, T>, dim3(static_cast<unsigned>(units), y > 1 ? y : 1), 256, 0, stream, p,
-                       most);
+  const int units = p.batch * p.row_tiles * p.kv_heads, parts = most / units + 1;
+  const int g = parts <= 2 ? 2 : parts <= 4 ? 4 : 8, items = kJoinThreads / g;
+  const dim3 grid(units, (R * (D / 16) + items - 1) / items);
+  return launch_behind(g == 2   ? cache_join_kernel<R, D, T, 2>
+                       : g == 4 ? cache_join_kernel<R, D, T, 4>
+                                : cache_join_kernel<R, D, T, 8>,
+                       grid, kJoinThreads, 0, stream, p, most);
 }
 
 // bf16 inputs, row tiles of 16, 32 or 64 rows, on `blocks` blocks

@@ -206,7 +206,7 @@ cpattn_status cache_shape(const cpattn_tensor* q, const cpattn_tensor* key_pages
   if (D != 64 && D != 128) return CPATTN_ERR_UNSUPPORTED;
   if (B > 65535 || H > 65535 || Hk > 65535 || S > (int64_t(1) << 24)) return CPATTN_ERR_UNSUPPORTED;
   // (row numbers, and blocks of the join's launch)
-  if (S * H > (int64_t(1) << 30) || B * Hk * ((Hk > 0 ? S * (H / Hk) : 0) / 16 + 1) > 0x7fffffff)
+  if (S * H > (int64_t(1) << 30) || B * Hk * ((Hk > 0 ? S * (H / Hk) : 0) / 16 + 1) > 0x7fff0000)
     return CPATTN_ERR_UNSUPPORTED;
   return CPATTN_OK;
 }
@@ -259,7 +259,7 @@ CachePlan cache_plan(const cpattn_tensor* q, const cpattn_tensor* key_pages, con
   const int64_t units = B * c.row_tiles * Hk;
   const int64_t most = (page_table->shape[1] * key_pages->shape[2] + S + c.keys - 1) / c.keys;   // tiles of a unit
   const int64_t least = cache_min_tiles(c.keys);
-  c.split = most > least && units < kCacheWholeUnits * slots;
+  c.split = most > least && units < kCacheWholeUnits * slots && units * most < 0x7fffffff;
   const int64_t want = c.split ? (units * most + least - 1) / least : units;
   c.blocks = static_cast<int>(want < slots ? want : slots);
   c.workspace = c.split ? static_cast<size_t>(c.blocks) * 2 * c.places * (D + 2) * 4 + units * 8 : 0;

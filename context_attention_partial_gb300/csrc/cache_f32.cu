@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) cache_f32_kernel(const __grid_consta
   const int share = p.heads / p.kv_heads, rows = p.s_q * share;
   launch_wait();
   launch_next();
-  CacheWalk<R, kKeys> walk;
+  CacheWalk<kKeys> walk;
   walk.start(p);
   CachePiece w;
   while (walk.next(p, w)) {
@@ -173,32 +173,28 @@ __global__ void __launch_bounds__(kThreads) cache_f32_kernel(const __grid_consta
     }
     copies_wait<0>();
     if (row < rows) {
-      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * R + r;
+      const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1);
       const int h = w.hk * share + row % share;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const int d = g * 4 + i * 32;
         if (unclean && token < w.count)
           add_unfinite<float>(p, w, token, p.parents != nullptr ? paths + r * kTreeWords : nullptr, k_begin, k_end, d, o[i]);
-        if (w.whole()) {
+        if (w.whole())
           cache_write_row<float>(p, w.b, h, token, d, o[i], m, l);
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.ws + part * D + d);
-          float2* dl = reinterpret_cast<float2*>(p.ws + static_cast<int64_t>(gridDim.x) * 2 * R * D) + part;
-          if (CPATTN_IN(p.ws_span, dst, 16, p.err)) *dst = o[i];
-          if (d == 0 && CPATTN_IN(p.ws_span, dl, 8, p.err)) *dl = make_float2(m, l);
-        }
+        else
+          cache_write_part<R, D>(p, part, r, d, o[i], m, l);
       }
     }
   }
-  cache_empty_units<float, R, kKeys, D>(p);
+  cache_empty_units<float, R, kKeys, D>(p, threadIdx.x, kThreads);
 }
 
 template <int D>
 cudaError_t launch_typed(const CacheParams& p, int blocks, cudaStream_t stream) {
   const cudaError_t e = cross_run<cache_f32_kernel<D>>(blocks, 1, kThreads, Cfg<D>::SMEM, stream, p);
   if (e != cudaSuccess || !p.split) return e;
-  return cache_join<R, kKeys, D, float>(p, blocks, stream);
+  return cache_join<R, D, float>(p, blocks, stream);
 }
 
 }  // namespace

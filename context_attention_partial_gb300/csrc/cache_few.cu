@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
   constexpr int RSTEP = kThreads / C::CH;
   launch_wait();
   launch_next();
-  CacheWalk<R, kKeys> walk;
+  CacheWalk<kKeys> walk;
   walk.start(p);
   CachePiece w;
   while (walk.next(p, w)) {
@@ -253,8 +253,10 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
     }
     __syncthreads();
     const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1);   // (a piece's slot)
+    const bool whole = w.whole();
     for (int i = threadIdx.x; i < R * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+      // (rows of the result, or neighbouring places of a part, by neighbouring threads)
+      const int r = whole ? i / (D / 4) : i % R, d = (whole ? i % (D / 4) : i / R) * 4;
       const int row = cache_row(p, w.rt, r);
       if (row < 0) continue;
       float top = -INFINITY;
@@ -274,17 +276,13 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
       const int t = row / share, h = w.hk * share + row % share;
       if (unclean && t < w.count)
         add_unfinite<__nv_bfloat16>(p, w, t, p.parents != nullptr ? paths + r * kTreeWords : nullptr, k_begin, k_end, d, sum);
-      if (w.whole()) {
+      if (whole)
         cache_write_row<__nv_bfloat16>(p, w.b, h, t, d, sum, top, total);
-      } else {
-        float4* dst = reinterpret_cast<float4*>(p.ws + (part * R + r) * D + d);
-        float2* dl = reinterpret_cast<float2*>(p.ws + static_cast<int64_t>(gridDim.x) * 2 * R * D) + part * R + r;
-        if (CPATTN_IN(p.ws_span, dst, 16, p.err)) *dst = sum;
-        if (d == 0 && CPATTN_IN(p.ws_span, dl, 8, p.err)) *dl = make_float2(top, total);
-      }
+      else
+        cache_write_part<R, D>(p, part, r, d, sum, top, total);
     }
   }
-  cache_empty_units<__nv_bfloat16, R, kKeys, D>(p);
+  cache_empty_units<__nv_bfloat16, R, kKeys, D>(p, threadIdx.x, kThreads);
 }
 
 template <int D, int MT>
@@ -293,7 +291,7 @@ cudaError_t launch_tiles(const CacheParams& params, int blocks, cudaStream_t str
   CacheParams p = params;
   cudaError_t e = cross_run<cache_few_kernel<D, MT>>(blocks, 1, kThreads, C::SMEM, stream, p);
   if (e != cudaSuccess || !p.split) return e;
-  return cache_join<C::R, kKeys, D, __nv_bfloat16>(p, blocks, stream);
+  return cache_join<C::R, D, __nv_bfloat16>(p, blocks, stream);
 }
 
 }  // namespace

@@ -96,11 +96,11 @@ struct Work : CachePiece {
 // tiles and descriptors (every lane writes the same).
 template <bool PAIR>
 struct Walk {
-  CacheWalk<PAIR ? 128 : 256, kBN> walk;
+  CacheWalk<kBN> walk;
   Work piece[2];
 
   __device__ void start(const CacheParams& p) {
-    CacheWalk<PAIR ? 128 : 256, kBN> first;
+    CacheWalk<kBN> first;
     first.start(p);
     walk = first;
     __syncwarp();
@@ -108,7 +108,7 @@ struct Walk {
   // The next piece to piece[slot]; false: no more.
   __device__ bool step(const CacheParams& p, int slot) {
     __syncwarp();
-    CacheWalk<PAIR ? 128 : 256, kBN> at = walk;
+    CacheWalk<kBN> at = walk;
     Work w;
     const bool more = at.next(p, w);
     if (more) {
@@ -455,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ------------------------------------------------------------- cleaners
       const int half = warp - kWarpClean;
+      cache_empty_units<__nv_bfloat16, R, kBN, D>(p, half * 32 + lane, 64);
       uint32_t g = 0, nd = 0;
       const Work& w = walk.piece[0];
       int number = 0;
@@ -506,18 +507,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = PAIR || wg < w.halves;
       const int place = (PAIR ? 0 : wg * kBM) + x;
       float m = -INFINITY, l = 0.f;
-      if (mine && p.parents != nullptr) {
+      if (mine && p.parents != nullptr) {   // (this warp's copy, on its way until the first drafts)
+        for (int i = lane; i < p.s_q; i += 32) {
+          const int32_t* from = p.parents + w.b * p.parents_stride + i;
+          copy4(smem_addr(stage) + i * 4, from, CPATTN_IN(p.parents_span, from, 4, p.err));
+        }
+        copies_commit();
+      }
+      bool paths = false;
+      auto make_path = [&](int at) {   // the row's path, up from draft `at`
+        paths = true;
+        copies_wait<0>();
+        __syncwarp();
 #pragma unroll
         for (int c = 0; c < kTreeWords; ++c) path[c] = 0u;
-        const int row = cache_row(p, w.rt, place);
-        int j = row < 0 || row / share >= w.count ? -1 : row / share;
-        while (j >= 0) {
-          path[j / 32] |= 1u << (j % 32);
-          const int32_t* from = p.parents + w.b * p.parents_stride + j;
-          const int up = CPATTN_IN(p.parents_span, from, 4, p.err) ? *from : -1;
-          j = up < j ? up : -1;
+        while (at >= 0) {
+          path[at / 32] |= 1u << (at % 32);
+          const int up = reinterpret_cast<const int*>(stage)[at];
+          at = up < at ? up : -1;
         }
-      }
+        __syncwarp();
+      };
       const int first = PAIR ? wg : 0;
       for (int j = first; mine && j < w.n; j += PAIR ? 2 : 1) {
         ok = wait_all(bar_s(wg), ns & 1, kErrSoftmax);
@@ -532,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_x128(tS, s);
           const int start = w.k0 + j * kBN, row = cache_row(p, w.rt, place), token = row < 0 ? p.s_q : row / share;
           const bool live = token < w.count;
+          if (p.parents != nullptr && !paths) make_path(live ? token : -1);
           // what the row sees of 32 keys at a time (seldom: the last tile or two of a unit)
           auto seen = [&](int at) -> uint32_t {
             if (!live) return 0u;
@@ -599,84 +610,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       tc_fence_after();
-      // every value that follows is this thread's row's; rows without a token: (0, -inf)
-      // (l is 0 where every score is -inf, too: no key has weight)
-      const bool none = !live || l == 0.f;
-      const float inv = none ? 0.f : whole ? 1.f / l : 1.f;
-      const bool add = !none && w.count > 1 && unclean[number % 8] == number;
-      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * R;
-      const int h = w.hk * share + (row < 0 ? 0 : row % share);
-      if (!PAIR || wg == 0) {
-        if (!whole) {
-          float2* dl = reinterpret_cast<float2*>(p.ws + static_cast<int64_t>(gridDim.x) * 2 * R * D) + part + place;
-          if (live && mine && CPATTN_IN(p.ws_span, dl, 8, p.err)) *dl = make_float2(m, l);
-        } else if (row >= 0) {
-          float* dl = static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + h * p.lse.s[1] + token * p.lse.s[2];
+      const bool add = live && w.count > 1 && unclean[number % 8] == number;
+      // (PAIR: the drafts may have been the other group's; the stage is written below)
+      if (mine && p.parents != nullptr && !paths) make_path(live ? token : -1);
+      // features of the row, 32 at a time, from tensor memory
+      const int c_begin = PAIR ? wg * (D / 2) : 0, c_end = PAIR ? c_begin + D / 2 : D;
+      auto features = [&](int c0, uint32_t (&o)[32]) {
+        tmem_ld_x32(tO + (PAIR ? 0 : wg * D) + c0, o);
+        if (PAIR && w.n > 1) {
+          uint32_t o2[32];
+          tmem_ld_x32(tO + D + c0, o2);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * own + u2f(o2[i]) * other);
+        }
+        if (__any_sync(0xffffffffu, add)) {
+#pragma unroll 1
+          for (int i = 0; i < 32 && add; i += 4) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            add_unfinite<__nv_bfloat16>(p, w, token, p.parents != nullptr ? path : nullptr, w.k0, w.k1, c0 + i, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e / 4 * 4 == i) o[e] = f2u(u2f(o[e]) + (e % 4 == 0 ? v.x : e % 4 == 1 ? v.y : e % 4 == 2 ? v.z : v.w));
+          }
+          __syncwarp();
+        }
+      };
+      if (!whole) {
+        // not divided by l: a part for the join
+        const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1);
+#pragma unroll 1
+        for (int c0 = c_begin; c0 < c_end && mine; c0 += 32) {
+          uint32_t o[32];
+          features(c0, o);
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              cache_write_part<R, D>(p, part, place, c0 + i,
+                                     make_float4(u2f(o[i]), u2f(o[i + 1]), u2f(o[i + 2]), u2f(o[i + 3])), m, l);
+          }
+          __syncwarp();
+        }
+      } else {
+        // rows without a token, or all of whose scores are -inf: (0, -inf)
+        const bool none = !live || l == 0.f;
+        const float inv = none ? 0.f : 1.f / l;
+        if ((!PAIR || wg == 0) && row >= 0) {
+          float* dl = static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + (w.hk * share + row % share) * p.lse.s[1] +
+                      token * p.lse.s[2];
           if (CPATTN_IN(p.lse.span, dl, 4, p.err)) *dl = none ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
         }
-      }
-      // 64 bytes of each of the warp's rows at a time through its stage: 32 features of
-      // a whole unit's result (bf16), 16 of a part's (fp32, not divided by l)
-      const int c_begin = PAIR ? wg * (D / 2) : 0, c_end = PAIR ? c_begin + D / 2 : D;
-      const uint32_t t_first = tO + (PAIR ? 0 : wg * D);
-      __syncwarp();
+        // through the warp's stage, 64 bytes of each of its rows at a time: the lane's
+        // four rows there, and its 16 bytes of them
+        int64_t to[4];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const int rw = cache_row(p, w.rt, place - lane + it * 8 + lane / 4), tk = rw / share;
+          to[it] = rw < 0 ? -1 : w.b * p.out.s[0] + (w.hk * share + rw - tk * share) * p.out.s[1] + tk * p.out.s[2] + lane % 4 * 8;
+        }
+        __syncwarp();
 #pragma unroll 1
-      for (int c0 = c_begin; c0 < c_end && (whole || mine); c0 += 32) {
-        uint32_t o[32];
-        if (mine) {
-          tmem_ld_x32(t_first + c0, o);
-          if (PAIR && w.n > 1) {
-            uint32_t o2[32];
-            tmem_ld_x32(tO + D + c0, o2);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * own + u2f(o2[i]) * other);
-          }
-        }
-        if (add) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float4 v = make_float4(u2f(o[i]), u2f(o[i + 1]), u2f(o[i + 2]), u2f(o[i + 3]));
-            add_unfinite<__nv_bfloat16>(p, w, token, p.parents != nullptr ? path : nullptr, w.k0, w.k1, c0 + i, v);
-            o[i] = f2u(v.x);
-            o[i + 1] = f2u(v.y);
-            o[i + 2] = f2u(v.z);
-            o[i + 3] = f2u(v.w);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = none ? 0u : f2u(u2f(o[i]) * inv);
-        uint4* srow = reinterpret_cast<uint4*>(stage) + lane * 4;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (whole && half == 1) break;
+        for (int c0 = c_begin; c0 < c_end; c0 += 32) {
+          uint32_t o[32];
+          if (mine) features(c0, o);
+          uint4* srow = reinterpret_cast<uint4*>(stage) + lane * 4;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint4 v;
-            if (whole)
-              v = make_uint4(pack_bf16x2(u2f(o[8 * i]), u2f(o[8 * i + 1])), pack_bf16x2(u2f(o[8 * i + 2]), u2f(o[8 * i + 3])),
-                             pack_bf16x2(u2f(o[8 * i + 4]), u2f(o[8 * i + 5])),
-                             pack_bf16x2(u2f(o[8 * i + 6]), u2f(o[8 * i + 7])));
-            else
-              v = make_uint4(o[16 * half + 4 * i], o[16 * half + 4 * i + 1], o[16 * half + 4 * i + 2], o[16 * half + 4 * i + 3]);
-            srow[i ^ ((lane >> 1) & 3)] = v;
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = none ? 0u : pack_bf16x2(u2f(o[8 * i + 2 * e]) * inv, u2f(o[8 * i + 2 * e + 1]) * inv);
+            srow[i ^ ((lane >> 1) & 3)] = make_uint4(v[0], v[1], v[2], v[3]);
           }
           __syncwarp();
 #pragma unroll
           for (int it = 0; it < 4; ++it) {
-            const int r = it * 8 + lane / 4, c = lane % 4;   // (row of the warp, 16-byte chunk)
-            const uint4 v = reinterpret_cast<const uint4*>(stage)[r * 4 + (c ^ ((r >> 1) & 3))];
-            const int pl = place - lane + r;
-            const int rw = cache_row(p, w.rt, pl);
-            if (rw < 0) continue;
-            const int tk = rw / share;
-            if (whole) {
-              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out.data) + w.b * p.out.s[0] +
-                                   (w.hk * share + rw - tk * share) * p.out.s[1] + tk * p.out.s[2] + c0 + c * 8;
-              if (CPATTN_IN(p.out.span, dst, 16, p.err)) *reinterpret_cast<uint4*>(dst) = v;
-            } else if (tk < w.count) {
-              float* dst = p.ws + (part + pl) * D + c0 + half * 16 + c * 4;
-              if (CPATTN_IN(p.ws_span, dst, 16, p.err)) *reinterpret_cast<uint4*>(dst) = v;
-            }
+            const int r = it * 8 + lane / 4;
+            const uint4 v = reinterpret_cast<const uint4*>(stage)[r * 4 + (lane % 4 ^ ((r >> 1) & 3))];
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out.data) + to[it] + c0;
+            if (to[it] >= 0 && CPATTN_IN(p.out.span, dst, 16, p.err)) *reinterpret_cast<uint4*>(dst) = v;
           }
           __syncwarp();
         }
@@ -694,7 +705,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  cache_empty_units<__nv_bfloat16, R, kBN, D>(p);
 }
 
 template <int D, bool PAIR>
@@ -705,7 +715,7 @@ cudaError_t launch_typed(const CacheMaps& m, const CacheParams& p, int blocks, c
   if (e != cudaSuccess) return e;
   e = launch_behind(kernel, dim3(blocks), kThreads, Cfg<D>::SMEM, stream, m.q, m.k, m.v, p);
   if (e != cudaSuccess || !p.split) return e;
-  return cache_join<PAIR ? 128 : 256, kBN, D, __nv_bfloat16>(p, blocks, stream);
+  return cache_join<PAIR ? 128 : 256, D, __nv_bfloat16>(p, blocks, stream);
 }
 
 }  // namespace
