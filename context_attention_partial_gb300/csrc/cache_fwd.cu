@@ -11,9 +11,9 @@
 // softmax, P V and output are under way.
 //
 // Roles (12 warps): warps 0-7 softmax and output, one thread per row of a 128-row query
-// tile and warpgroup; warp 8 TMA producer; warp 9 MMA issuer; warps 10-11 clean the
-// value tiles that hold drafts.  TMEM: S_0 | S_1 | O_0 | O_1, P over S's first columns.
-// Shared memory: the two Q tiles, a ring of K / V tiles, an output staging area and the
+// tile and warpgroup; warp 8 TMA producer; warp 9 MMA issuer; warp 10 cleans the value
+// tiles that hold drafts; warp 11 finds the block's pieces and announces them.  TMEM:
+// S_0 | S_1 | O_0 | O_1, P over S's first columns.  Shared memory: the two Q tiles, a ring of K / V tiles, an output staging area and the
 // paths of a tree's drafts per softmax warp.
 //
 // Rows.  A query tile is whole tokens, each with every query head that shares the key
@@ -25,7 +25,7 @@
 // Keys.  A 128-key tile is up to eight pages' boxes, each asked for by a lane of the
 // producer.  Scores of keys that a row does not see are masked in registers, by the
 // bits of its path.  Value rows behind the last key are zeroed in shared memory, and so
-// are a draft's values that are not finite (see cache_few.cu), by warps 10 and 11.
+// are a draft's values that are not finite (see cache_few.cu), by warp 10.
 #include <cmath>
 
 #include "cache.cuh"
@@ -36,13 +36,14 @@ namespace {
 
 constexpr int kBM = 128, kBN = 128;
 constexpr int kThreads = 384;
-constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10;
+constexpr int kWarpProducer = 8, kWarpMma = 9, kWarpClean = 10, kWarpWalk = 11;
+constexpr int kPieces = 4;          // announced ahead
 constexpr int kLaunchRegs = 168;    // 65536 / 384, rounded down to 8
 constexpr int kSoftmaxRegs = 208, kControlRegs = 88;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays below 2^8
-constexpr unsigned kErrProducer = 1u, kErrMma = 2u, kErrSoftmax = 4u, kErrClean = 8u;
+constexpr unsigned kErrProducer = 1u, kErrMma = 2u, kErrSoftmax = 4u, kErrClean = 8u, kErrWalk = 0x10u;
 
 template <int D>
 struct Cfg {
@@ -52,9 +53,9 @@ struct Cfg {
   static constexpr int STAGING = 8 * 32 * 64;             // 32 rows x 64 bytes per warp
   static constexpr int PATHS = 8 * 32 * kTreeWords * 4;   // a path per row
   static constexpr int SUMS = 2 * kBM * 8;                // PAIR: m and l of both sums
-  static constexpr int WALKS = 12 * 192;                  // a warp's walk and pieces
-  static constexpr int BARS = 2 * STAGES + 13;
-  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + STAGING + PATHS + SUMS + WALKS + BARS * 8 + 48;
+  static constexpr int PIECES = kPieces * 64;
+  static constexpr int BARS = 2 * STAGES + 13 + 2 * kPieces;
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + STAGING + PATHS + SUMS + PIECES + BARS * 8 + 48;
   static constexpr int QK = ROW / 32, PV = kBN / 16;      // MMAs of a tile product
   static constexpr int KB = ROW / 128;                    // 128-byte column blocks
   static constexpr int O_COL = 2 * kBN;
@@ -92,40 +93,22 @@ struct Work : CachePiece {
   int halves;     // query tiles with rows
 };
 
-// A warp's walk, this piece and the next: in shared memory, since the registers hold
-// tiles and descriptors (every lane writes the same).
+// The next piece of a block's walk (n = 0: no more).
 template <bool PAIR>
-struct Walk {
-  CacheWalk<kBN> walk;
-  Work piece[2];
-
-  __device__ void start(const CacheParams& p) {
-    CacheWalk<kBN> first;
-    first.start(p);
-    walk = first;
-    __syncwarp();
+__device__ __forceinline__ Work next_work(const CacheParams& p, CacheWalk<kBN>& walk) {
+  Work w;
+  if (!walk.next(p, w)) {
+    w.n = 0;
+    return w;
   }
-  // The next piece to piece[slot]; false: no more.
-  __device__ bool step(const CacheParams& p, int slot) {
-    __syncwarp();
-    CacheWalk<kBN> at = walk;
-    Work w;
-    const bool more = at.next(p, w);
-    if (more) {
-      w.k0 = w.t0 * kBN;
-      w.k1 = min(w.len + w.count, w.t1 * kBN);
-      w.n = w.t1 - w.t0;
-      w.drafts = max(0, w.len - w.k0) / kBN;
-      const int share = p.heads / p.kv_heads;
-      w.halves = !PAIR && (w.rt * p.tile_rows + p.half_rows) / share < w.count ? 2 : 1;
-    }
-    __syncwarp();
-    walk = at;
-    if (more) piece[slot] = w;
-    __syncwarp();
-    return more;
-  }
-};
+  w.k0 = w.t0 * kBN;
+  w.k1 = min(w.len + w.count, w.t1 * kBN);
+  w.n = w.t1 - w.t0;
+  w.drafts = max(0, w.len - w.k0) / kBN;
+  const int share = p.heads / p.kv_heads;
+  w.halves = !PAIR && (w.rt * p.tile_rows + p.half_rows) / share < w.count ? 2 : 1;
+  return w;
+}
 
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -139,9 +122,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* staging = smem + (2 + C::STAGES) * C::TILE;
   uint32_t* all_paths = reinterpret_cast<uint32_t*>(staging + C::STAGING);
   float2* sums = reinterpret_cast<float2*>(staging + C::STAGING + C::PATHS);   // [2][128]
-  uint8_t* walks = staging + C::STAGING + C::PATHS + C::SUMS;
-  static_assert(sizeof(Walk<PAIR>) <= 192, "a warp's walk");
-  uint64_t* bars = reinterpret_cast<uint64_t*>(walks + C::WALKS);
+  Work* pieces = reinterpret_cast<Work*>(staging + C::STAGING + C::PATHS + C::SUMS);
+  static_assert(sizeof(Work) <= 64, "a piece");
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(pieces) + C::PIECES);
   const uint32_t bar0 = smem_addr(bars);
   auto bar_full = [&](int s) { return bar0 + 8u * s; };
   auto bar_empty = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
@@ -153,6 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_drain = bar0 + 8u * (2 * C::STAGES + 10);
   const uint32_t bar_dirty = bar0 + 8u * (2 * C::STAGES + 11);                  // a value tile with drafts arrived
   const uint32_t bar_clean = bar0 + 8u * (2 * C::STAGES + 12);
+  auto bar_piece = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 13 + i); };           // announced
+  auto bar_done = [&](int i) { return bar0 + 8u * (2 * C::STAGES + 13 + kPieces + i); };  // its output is written
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   // pieces with values that are not finite, by the piece's number
@@ -174,7 +159,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar_drain, 1);
     mbar_init(bar_dirty, 1);
-    mbar_init(bar_clean, 2);
+    mbar_init(bar_clean, 1);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(bar_piece(i), 1);
+      mbar_init(bar_done(i), 9);   // softmax warps, cleaner
+    }
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) unclean[i] = -1;
     fence_mbar_init();
@@ -198,13 +187,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, r) != 0;
   };
 
-  Walk<PAIR>& walk = *reinterpret_cast<Walk<PAIR>*>(walks + warp * 192);
+  // Piece `number` of this block, once announced; false: no more, or a wait ran out (ok).
+  auto take = [&](int number, bool& ok, unsigned code) {
+    ok = wait_all(bar_piece(number % kPieces), (number / kPieces) & 1, code);
+    return ok && pieces[number % kPieces].n != 0;
+  };
 
   if (warp >= 8) {
     regs_decrease<kControlRegs>();
     const bool leader = elect_one();
-    walk.start(p);
-    bool have = walk.step(p, 0);
     if (warp == kWarpProducer) {
       // ---------------------------------------------------------- producer
       // K tiles on even stages, V tiles on odd ones: the first K alone, then
@@ -217,7 +208,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int box = min(1 << p.cache.shift, kBN), kb = lane % C::KB, part = lane % 16 / C::KB;
       const uint32_t q_bytes = static_cast<uint32_t>(p.half_rows) * C::ROW;
       int ld = 0, nq[2] = {0, 0};
-      bool ok = p.fault_skip_kv == 0;
+      bool ok = true;
+      bool have = take(0, ok, kErrProducer);
+      ok = ok && p.fault_skip_kv == 0;
       // boxes of key tile j of piece x; this lane's box's page
       auto boxes = [&](const Work& x, int j) { return ceil_div(min(kBN, x.k1 - (x.k0 + j * kBN)), box); };
       auto page_of = [&](const Work& x, int j, int n) {
@@ -246,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (have && ok) {
-        const Work& w = walk.piece[0];
+        const Work& w = pieces[0];
         const int n = boxes(w, 0), page = page_of(w, 0, n);
         if (leader) mbar_arrive_expect_tx(bar_full(0), n * box * C::ROW);
         __syncwarp();
@@ -256,8 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_q(w);
       }
       for (int number = 0; have && ok; ++number) {
-        const Work &w = walk.piece[number & 1], &wn = walk.piece[(number & 1) ^ 1];
-        const bool more_units = walk.step(p, (number & 1) ^ 1);
+        const Work &w = pieces[number % kPieces], &wn = pieces[(number + 1) % kPieces];
+        const bool more_units = take(number + 1, ok, kErrProducer);
+        if (!ok) break;
         // (the next Q tiles into L2 while this piece runs)
         if (more_units && leader)
           for (int i = 0; i < wn.halves; ++i)
@@ -308,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t g = 0;                // key tiles so far, over all pieces
       uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, nc = 0;
       bool ok = true;
+      bool have = take(0, ok, kErrMma);
       // a piece's first scores, query tile by query tile (its K tile is here)
       auto first_qk = [&](const Work& x, uint32_t at) {
         const uint32_t s = at % C::STAGES;
@@ -336,12 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (have) {
         ok = wait_all(bar_full(0), 0, kErrMma);
-        if (ok) first_qk(walk.piece[0], 0);
+        if (ok) first_qk(pieces[0], 0);
       }
       for (int number = 0; have && ok; ++number) {
-        const bool more_units = walk.step(p, (number & 1) ^ 1);
-        const int n = walk.piece[number & 1].n, drafts = walk.piece[number & 1].drafts;
-        const bool two = walk.piece[number & 1].halves == 2;
+        const bool more_units = take(number + 1, ok, kErrMma);
+        if (!ok) break;
+        const int n = pieces[number % kPieces].n, drafts = pieces[number % kPieces].drafts;
+        const bool two = pieces[number % kPieces].halves == 2;
         for (int j = 0; j < n; ++j, ++g) {
           const bool more = j + 1 < n;
           const uint32_t sv = (2 * g + 1) % C::STAGES, lk = 2 * g + 2, sk = lk % C::STAGES;
@@ -443,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (ok && more_units) first_qk(walk.piece[(number & 1) ^ 1], 2 * g);
+        if (ok && more_units) first_qk(pieces[(number + 1) % kPieces], 2 * g);
         have = more_units;
       }
       if (!ok && leader) {
@@ -452,17 +448,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(bar_drain, 0, p.timeout_ns);
       }
       __syncwarp();
-    } else {
-      // ------------------------------------------------------------- cleaners
-      const int half = warp - kWarpClean;
-      cache_empty_units<__nv_bfloat16, R, kBN, D>(p, half * 32 + lane, 64);
+    } else if (warp == kWarpWalk) {
+      // ----------------------------------------------------------- the walk
+      // (one warp's: the others would each fetch its instructions, at the start of a
+      // launch from HBM)
+      CacheWalk<kBN> walk;
+      walk.start(p);
+      for (int number = 0;; ++number) {
+        const Work w = next_work<PAIR>(p, walk);
+        if (number >= kPieces && !wait_all(bar_done(number % kPieces), (number / kPieces - 1) & 1, kErrWalk)) break;
+        if (leader) {
+          if (w.n != 0) cache_note_unit<R, D>(p, w);
+          pieces[number % kPieces] = w;
+          mbar_arrive(bar_piece(number % kPieces));
+        }
+        __syncwarp();
+        if (w.n == 0) break;
+      }
+      cache_empty_units<__nv_bfloat16, R, kBN, D>(p, lane, 32);
+    } else if (warp == kWarpClean) {
+      // -------------------------------------------------------------- cleaner
       uint32_t g = 0, nd = 0;
-      const Work& w = walk.piece[0];
-      int number = 0;
-      for (bool ok = true; have && ok; have = walk.step(p, 0), ++number) {
-        if (half == 0 && leader) cache_note_unit<R, D>(p, w);
-        g += min(w.drafts, w.n);
-        for (int j = w.drafts; j < w.n && ok; ++j, ++g) {
+      bool ok = true;
+      for (int number = 0; ok && take(number, ok, kErrClean); ++number) {
+        const Work& w = pieces[number % kPieces];
+        const int n = w.n;
+        g += min(w.drafts, n);
+        for (int j = w.drafts; j < n; ++j, ++g) {
           ok = wait_all(bar_dirty, nd & 1, kErrClean);
           if (!ok) break;
           ++nd;
@@ -471,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* tile = smem + (2 + (2 * g + 1) % C::STAGES) * C::TILE;
           bool found = false;
 #pragma unroll 4
-          for (int i = from * 8 + half * 32 + lane; i < kBN * 8; i += 64) {
+          for (int i = from * 8 + lane; i < kBN * 8; i += 32) {
 #pragma unroll
             for (int c = 0; c < C::KB; ++c) {
               uint4* at = reinterpret_cast<uint4*>(tile + c * kBN * 128 + i * 16);
@@ -486,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (leader) mbar_arrive(bar_clean);
         }
+        if (leader) mbar_arrive(bar_done(number % kPieces));
       }
     }
   } else {
@@ -501,9 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = quarter * 32 + lane;                 // this thread's row of its query tile
     int ns = 0, no[2] = {0, 0};
     bool ok = true;
-    const Work& w = walk.piece[0];
-    walk.start(p);
-    for (int number = 0; ok && walk.step(p, 0); ++number) {
+    for (int number = 0;; ++number) {
+      const bool have = take(number, ok, kErrSoftmax);
+      // (the two groups stay together, also when a wait has run out)
+      if (PAIR) ok = vote_all(ok);
+      if (!ok || !have) break;
+      const Work& w = pieces[number % kPieces];
       const bool mine = PAIR || wg < w.halves;
       const int place = (PAIR ? 0 : wg * kBM) + x;
       float m = -INFINITY, l = 0.f;
@@ -697,6 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         asm volatile("bar.sync 1, 256;" ::: "memory");
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_done(number % kPieces));
     }
   }
   tc_fence_before();
