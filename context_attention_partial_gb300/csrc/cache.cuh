@@ -81,6 +81,20 @@ struct CacheParams {
   unsigned int* err;
 };
 
+// Asks for what a call reads first -- lengths, counts, the table's beginning, parents --
+// while the kernel before it ends (launch_wait() follows; no value is read).
+__device__ __forceinline__ void cache_prefetch(const CacheParams& p) {
+  auto lines = [&](const int32_t* from, int64_t n) {
+    if (from == nullptr) return;
+    const int64_t bytes = min(n * 4, static_cast<int64_t>(blockDim.x) * 128);
+    if (threadIdx.x * 128 < bytes) prefetch_l2(reinterpret_cast<const char*>(from) + threadIdx.x * 128);
+  };
+  lines(p.cache.lengths, p.batch);
+  lines(p.cache.counts, p.batch);
+  lines(p.cache.table, (p.batch - 1) * p.cache.stride + p.cache.width);
+  lines(p.parents, p.parents != nullptr ? (p.batch - 1) * p.parents_stride + p.s_q : 0);
+}
+
 // Row of (b, hk, rt)'s place r, or -1.
 __device__ __forceinline__ int cache_row(const CacheParams& p, int rt, int r) {
   const int x = r % 128, row = rt * p.tile_rows + r / 128 * p.half_rows + x;

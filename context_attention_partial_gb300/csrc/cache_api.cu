@@ -339,11 +339,12 @@ cpattn_status cpattn_cache_append(const cpattn_tensor* q, const cpattn_tensor* k
   if (!k || !v || (q && !q_out)) return CPATTN_ERR_NULL;
   NormParams p;
   std::memset(&p, 0, sizeof(p));
+  // (queries first: where the keys go takes a while to find)
   cpattn_tensor in[3];
-  in[0] = *k;
-  in[1] = *v;
-  if (q) in[2] = *q;
-  const int n = q ? 3 : 2;
+  const int n = q ? 3 : 2, key = n - 2;
+  if (q) in[0] = *q;
+  in[key] = *k;
+  in[key + 1] = *v;
   int64_t B, S, D, heads;
   cpattn_status st = norm_shapes(n, in, &B, &S, &D, &heads);
   if (st != CPATTN_OK) return st;
@@ -353,31 +354,38 @@ cpattn_status cpattn_cache_append(const cpattn_tensor* q, const cpattn_tensor* k
   if ((st = cache_common(key_pages, value_pages, page_table, lengths, counts, k->dtype, B, k->shape[1], D, run,
                          &p.cache)) != CPATTN_OK)
     return st;
-  const cpattn_tensor* weights[3] = {k_weight, nullptr, q ? q_weight : nullptr};
-  cpattn_tensor* out[3] = {key_pages, value_pages, q_out};
+  const cpattn_tensor* weights[3] = {};
+  cpattn_tensor* out[3] = {};
+  if (q) {
+    weights[0] = q_weight;
+    out[0] = q_out;
+  }
+  weights[key] = k_weight;
+  out[key] = key_pages;
+  out[key + 1] = value_pages;
   const long long shrink = g_check_shrink.load();
   for (int i = 0; i < n; ++i) {
     NormTensor& t = p.t[i];
     if (weights[i]) {
       // (of one type, so that one kernel reads them)
-      if (i == 2 && k_weight && q_weight->dtype != k_weight->dtype) return CPATTN_ERR_DTYPE;
+      if (i < key && k_weight && q_weight->dtype != k_weight->dtype) return CPATTN_ERR_DTYPE;
       if ((st = norm_weight(weights[i], weights[i]->dtype, D)) != CPATTN_OK) return st;
       t.w = weights[i]->data;
       t.w_span = {t.w, extent_bytes(weights[i])};
       p.w_f32 = weights[i]->dtype == CPATTN_F32;
       t.norm = 1;
     }
-    t.turn = i != 1 && positions;
-    t.paged = i < 2;
+    t.turn = i <= key && positions;
+    t.paged = i >= key;
     p.head_start[i + 1] = p.head_start[i] + static_cast<int>(in[i].shape[1]);
-    if (i == 2) {
+    if (!t.paged) {
       if (q_out->dtype != q->dtype) return CPATTN_ERR_DTYPE;
       if (!shape_ok(q_out, 4) || !same_shape(q, q_out, 4)) return CPATTN_ERR_SHAPE;
     }
     if (B * S * in[i].shape[1] == 0) continue;
-    if (!in[i].data || (i == 2 && !q_out->data)) return CPATTN_ERR_NULL;
-    if (!layout_ok(&in[i]) || (i == 2 && !layout_distinct(q_out))) return CPATTN_ERR_LAYOUT;
-    if (i == 2 && q->data == q_out->data && !same_place(q, q_out)) return CPATTN_ERR_LAYOUT;
+    if (!in[i].data || (!t.paged && !q_out->data)) return CPATTN_ERR_NULL;
+    if (!layout_ok(&in[i]) || (!t.paged && !layout_distinct(q_out))) return CPATTN_ERR_LAYOUT;
+    if (!t.paged && q->data == q_out->data && !same_place(q, q_out)) return CPATTN_ERR_LAYOUT;
     t.x = in[i].data;
     t.y = out[i]->data;
     strides(&in[i], t.x_s);

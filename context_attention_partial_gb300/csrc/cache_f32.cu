@@ -2,8 +2,8 @@
 // computed in fp32 (no tf32 rounding).
 //
 // Mathematics as in cache_few.cu.  A block of 128 threads takes 16 rows (tokens of the
-// query heads that share a key head) and walks its keys in tiles of 32, two in flight
-// by asynchronous copies.  Scores: a thread has one row and every eighth key; P V: the
+// query heads that share a key head) and walks its keys in tiles of 32, the next one in flight by asynchronous
+// copies.  Scores: a thread has one row and every eighth key; P V: the
 // same row, and every eighth group of four features; the eight threads of a row share
 // its maximum and sum by shuffles, and its weights through shared memory.  Rows of
 // shared memory are D + 4 floats, so that eight neighbouring rows use all banks.
@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kThreads) cache_f32_kernel(const __grid_consta
   int* parents = reinterpret_cast<int*>(paths + R * kTreeWords);
   const int r = threadIdx.x / 8, g = threadIdx.x % 8;   // this thread's row, and place in it
   const int share = p.heads / p.kv_heads, rows = p.s_q * share;
+  cache_prefetch(p);
   launch_wait();
   launch_next();
   CacheWalk<kKeys> walk;
@@ -60,23 +61,37 @@ __global__ void __launch_bounds__(kThreads) cache_f32_kernel(const __grid_consta
   while (walk.next(p, w)) {
     if (threadIdx.x == 0) cache_note_unit<R, D>(p, w);
     const int k_begin = w.t0 * kKeys, k_end = min(w.len + w.count, w.t1 * kKeys), tiles = w.t1 - w.t0;
+    // page numbers of a tile, at most two, read while the tile before it is asked for
+    auto pages = [&](int t, int (&pg)[2]) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int key = k_begin + t * kKeys + (j << p.cache.shift);
+        pg[j] = t < tiles && (j << p.cache.shift) < kKeys && key < k_end ? cache_page(p.cache, w.b, key, p.err) : -1;
+      }
+    };
+    int pg[2];
+    pages(0, pg);
     auto load = [&](int t) {
       if (t < tiles) {
         float* dst = shared + (t % C::STAGES) * C::STAGE;
+        const float* kbase = static_cast<const float*>(p.k.data) + w.hk * p.k.s[1];
+        const float* vbase = static_cast<const float*>(p.v.data) + w.hk * p.v.s[1];
+#pragma unroll 4
         for (int i = threadIdx.x; i < kKeys * C::CH; i += kThreads) {
           const int kr = i / C::CH, d = i % C::CH * 4, key = k_begin + t * kKeys + kr;
-          const int64_t page = key < k_end ? cache_page(p.cache, w.b, key, p.err) : -1;
+          const int64_t page = (kr >> p.cache.shift) == 0 ? pg[0] : pg[1];
           const int at_row = key & ((1 << p.cache.shift) - 1);
-          const float* kbase = static_cast<const float*>(p.k.data);
-          const float* vbase = static_cast<const float*>(p.v.data);
-          const float* kp = kbase + page * p.k.s[0] + w.hk * p.k.s[1] + at_row * p.k.s[2] + d;
-          const float* vp = vbase + page * p.v.s[0] + w.hk * p.v.s[1] + at_row * p.v.s[2] + d;
-          const bool in = page >= 0;
-          copy16(smem_addr(dst + kr * C::ROW + d), in ? static_cast<const void*>(kp) : p.q.data, in && CPATTN_IN(p.k.span, kp, 16, p.err));
-          copy16(smem_addr(dst + (kKeys + kr) * C::ROW + d), in ? static_cast<const void*>(vp) : p.q.data, in && CPATTN_IN(p.v.span, vp, 16, p.err));
+          const float* kp = kbase + page * p.k.s[0] + at_row * p.k.s[2] + d;
+          const float* vp = vbase + page * p.v.s[0] + at_row * p.v.s[2] + d;
+          const bool in = key < k_end && page >= 0;
+          copy16<true>(smem_addr(dst + kr * C::ROW + d), in ? static_cast<const void*>(kp) : p.q.data,
+                       in && CPATTN_IN(p.k.span, kp, 16, p.err));
+          copy16<true>(smem_addr(dst + (kKeys + kr) * C::ROW + d), in ? static_cast<const void*>(vp) : p.q.data,
+                       in && CPATTN_IN(p.v.span, vp, 16, p.err));
         }
       }
       copies_commit();
+      pages(t + 1, pg);
     };
     __syncthreads();   // (the piece before has read its rows and paths)
     load(0);

@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
   const int share = p.heads / p.kv_heads, rows = p.s_q * share;
   const int c = threadIdx.x % C::CH, r_first = threadIdx.x / C::CH;
   constexpr int RSTEP = kThreads / C::CH;
+  cache_prefetch(p);
   launch_wait();
   launch_next();
   CacheWalk<kKeys> walk;

@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  cache_prefetch(p);
   launch_wait();
   launch_next();
   const uint32_t tmem = *tmem_holder;

@@ -42,6 +42,15 @@ __device__ __forceinline__ uint4 repack(const float (&f)[4], float) {
                     __float_as_uint(f[3]));
 }
 
+// Cosine and sine of a pair with frequency w (turns per position, hi + lo) at `pos`.
+__device__ __forceinline__ float2 rotary_turn(float pos, float2 w) {
+  const float hi = __fmul_rn(pos, w.x);
+  const float lo = fmaf(pos, w.y, fmaf(pos, w.x, -hi));
+  float2 cs;
+  sincospif(2.f * ((hi - rintf(hi)) + lo), &cs.y, &cs.x);
+  return cs;
+}
+
 // Cosines and sines of vector v's features at (b, token), and the features that
 // are turned (bit e).  PAIRING 0: interleaved, a turn per pair.  Halves (1, 2): a
 // turn per feature, s with the sign that its partner, feature partner[e], is
@@ -72,11 +81,9 @@ __device__ __forceinline__ unsigned load_turns(const P& p, int v, int b, int tok
       }
       if (active) {
         const float* src = p.pos + b * p.pos_sb + token * p.pos_ss + axis * p.pos_sa;
-        const float pos = CPATTN_IN(p.pos_span, src, 4, p.err) ? *src : 0.f;
-        const float2 w = p.freq[pair];   // turns per position, hi + lo
-        const float hi = __fmul_rn(pos, w.x);
-        const float lo = fmaf(pos, w.y, fmaf(pos, w.x, -hi));
-        sincospif(2.f * ((hi - rintf(hi)) + lo), &s[e], &c[e]);
+        const float2 cs = rotary_turn(CPATTN_IN(p.pos_span, src, 4, p.err) ? *src : 0.f, p.freq[pair]);
+        c[e] = cs.x;
+        s[e] = cs.y;
         // (sign: what this feature's partner is multiplied with)
         if (inverse != (PAIRING != 0 && !upper)) s[e] = -s[e];
       }
