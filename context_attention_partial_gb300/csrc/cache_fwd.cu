@@ -53,7 +53,7 @@ struct Cfg {
   static constexpr int STAGING = 8 * 32 * 64;             // 32 rows x 64 bytes per warp
   static constexpr int PATHS = 8 * 32 * kTreeWords * 4;   // a path per row
   static constexpr int SUMS = 2 * kBM * 8;                // PAIR: m and l of both sums
-  static constexpr int PIECES = kPieces * 64;
+  static constexpr int PIECES = (kPieces + 1) * 64;
   static constexpr int BARS = 2 * STAGES + 13 + 2 * kPieces;
   static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + STAGING + PATHS + SUMS + PIECES + BARS * 8 + 48;
   static constexpr int QK = ROW / 32, PV = kBN / 16;      // MMAs of a tile product
@@ -167,6 +167,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) unclean[i] = -1;
     fence_mbar_init();
+    // the piece of nothing that the softmax warps begin with
+    Work nothing = {};
+    nothing.n = PAIR ? 2 : 1;   // (a tile for each group)
+    nothing.drafts = nothing.halves = 2;
+    pieces[kPieces] = nothing;
+    mbar_arrive(bar_s(0));
+    mbar_arrive(bar_s(1));
   }
   if (warp == kWarpMma) tmem_alloc(smem_addr(tmem_holder), 512);
   if (warp == kWarpProducer && lane == 0) {
@@ -178,8 +185,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   cache_prefetch(p);
-  launch_wait();
-  launch_next();
   const uint32_t tmem = *tmem_holder;
   const int share = p.heads / p.kv_heads;
   // every wait of a warp is voted on, so its lanes stay together
@@ -195,6 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= 8) {
+    launch_wait();
+    launch_next();
     regs_decrease<kControlRegs>();
     const bool leader = elect_one();
     if (warp == kWarpProducer) {
@@ -203,9 +210,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V_j and the K tile after it (of the next piece behind a piece's last V)
       // as one pair on the K stage's barrier, so the MMA warp waits once a
       // step; the very last V on its own.  Lanes 0-15 ask for a value tile's pages,
-      // lanes 16-31 for a key tile's.
+      // lanes 16-31 for a key tile's.  Keys that one row tile reads leave L2 first, so
+      // that tables, parts and instructions stay (trees of 27 drafts x 8192 keys: 40.0
+      // us, 43.6 when they are kept).
       static_assert(C::STAGES % 2 == 0, "K / V pairs");
-      const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
+      const uint64_t pol_q = l2_policy_evict_first(), pol_kv =
+          p.row_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
       const int box = min(1 << p.cache.shift, kBN), kb = lane % C::KB, part = lane % 16 / C::KB;
       const uint32_t q_bytes = static_cast<uint32_t>(p.half_rows) * C::ROW;
       int ld = 0, nq[2] = {0, 0};
@@ -301,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t hi = static_cast<uint32_t>(q_desc >> 32);   // (shared by all: low words hold the address)
       // (tests come before the descriptors are built, waits only where a test failed)
       uint32_t g = 0;                // key tiles so far, over all pieces
-      uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, nc = 0;
+      uint32_t nq[2] = {0, 0}, np[2] = {1, 1}, nc = 0;
       bool ok = true;
       bool have = take(0, ok, kErrMma);
       // a piece's first scores, query tile by query tile (its K tile is here)
@@ -331,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (have) {
-        ok = wait_all(bar_full(0), 0, kErrMma);
+        // (tensor memory is free once the piece of nothing is through)
+        ok = wait_all(bar_p(0), 0, kErrMma) && wait_all(bar_p(1), 0, kErrMma) && wait_all(bar_full(0), 0, kErrMma);
         if (ok) first_qk(pieces[0], 0);
       }
       for (int number = 0; have && ok; ++number) {
@@ -515,16 +526,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = quarter * 32 + lane;                 // this thread's row of its query tile
     int ns = 0, no[2] = {0, 0};
     bool ok = true;
-    for (int number = 0;; ++number) {
-      const bool have = take(number, ok, kErrSoftmax);
-      // (the two groups stay together, also when a wait has run out)
-      if (PAIR) ok = vote_all(ok);
-      if (!ok || !have) break;
-      const Work& w = pieces[number % kPieces];
+    // First a piece of nothing: a tile of whatever tensor memory holds, of which nothing
+    // is kept.  A launch finds this loop's instructions in HBM, and so they arrive while
+    // the kernel before this one ends and the first keys are on their way.
+    for (int number = -1;; ++number) {
+      if (number >= 0) {
+        const bool have = take(number, ok, kErrSoftmax);
+        // (the two groups stay together, also when a wait has run out)
+        if (PAIR) ok = vote_all(ok);
+        if (!ok || !have) break;
+      }
+      const Work& w = pieces[number >= 0 ? number % kPieces : kPieces];
       const bool mine = PAIR || wg < w.halves;
       const int place = (PAIR ? 0 : wg * kBM) + x;
       float m = -INFINITY, l = 0.f;
-      if (mine && p.parents != nullptr) {   // (this warp's copy, on its way until the first drafts)
+      if (number >= 0 && mine && p.parents != nullptr) {   // (this warp's copy, on its way until the first drafts)
         for (int i = lane; i < p.s_q; i += 32) {
           const int32_t* from = p.parents + w.b * p.parents_stride + i;
           copy4(smem_addr(stage) + i * 4, from, CPATTN_IN(p.parents_span, from, 4, p.err));
@@ -602,6 +618,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p(wg));
+      }
+      if (number < 0) {
+        launch_wait();
+        if (PAIR) ok = vote_all(ok);
+        if (!ok) break;
+        continue;
       }
       const bool whole = w.whole();
       const int row = cache_row(p, w.rt, place), token = row < 0 ? p.s_q : row / share;
