@@ -102,7 +102,10 @@ __device__ __forceinline__ int cache_row(const CacheParams& p, int rt, int r) {
 }
 
 // Key tiles that a block takes at least before another one shares its work.
-constexpr int cache_min_tiles(int keys) { return keys >= 128 ? 2 : 3; }
+// (8 key heads x 1000 keys, one token, tiles of 64: at least 2 tiles 11.6 us, 3 tiles
+// 15.2, 6 tiles 18.0; fp32 tiles of 32: 13 rows a key head x 700 keys 18.0 with 2 or 3,
+// 21.8 with 5, one row x 3000 keys 18.5 with 3, 22.6 with 1)
+constexpr int cache_min_tiles(int keys) { return keys >= 64 ? 2 : 3; }
 // Units a block above which none are split: then a round of whole units is at most
 // an eighth of the call, and the tables that a split needs would be long.
 constexpr int kCacheWholeUnits = 8;
@@ -112,6 +115,7 @@ struct CachePiece {
   int b, hk, rt;
   int t0, t1, tiles;
   int len, count;             // the sequence's cached and new tokens
+  int open;                   // keys before it are seen by every row that has a token
   __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
@@ -204,6 +208,7 @@ struct CacheWalk {
       }
       w.b = x / p.row_tiles;
       w.rt = x - w.b * p.row_tiles;
+      w.open = w.len + (p.parents != nullptr ? 0 : w.rt * p.tile_rows / (p.heads / p.kv_heads) + 1);
       return true;
     }
     return false;
@@ -327,11 +332,11 @@ __device__ __forceinline__ bool clear_unfinite(float4* at) {
 }
 
 // Adds to features d .. d + 3 of a row of token i the values that are not finite, of
-// the drafts with keys k0 .. k1 - 1 that it sees (paths: its path, nullptr for a chain).
+// the keys k0 .. k1 - 1 from w.open on that it sees (paths: its path, nullptr for a chain).
 template <typename T>
 __device__ __noinline__ void add_unfinite(const CacheParams& p, const CachePiece& w, int i, const uint32_t* path, int k0,
                                           int k1, int d, float4& sum) {
-  for (int key = max(k0, w.len); key < k1; ++key) {
+  for (int key = max(k0, w.open); key < k1; ++key) {
     const int j = key - w.len;
     if (path != nullptr ? !((path[j / 32] >> (j % 32)) & 1u) : j > i) continue;
     const int page = cache_page(p.cache, w.b, key, p.err);
@@ -408,7 +413,6 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   const int c0 = blocks.x, c1 = blocks.y;
   // (written by its block; or, behind a wait that ran out, not noted)
   if (c0 < 0 || c0 >= c1 || c1 >= most) return;
-  const int count = cache_count(p.cache, b, p.s_q, p.err);
   {
     const int i = blockIdx.y * I + item, r = i % R, d = i / R * 16;
     const int row = cache_row(p, rt, r);
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     float4 sum[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row >= 0 && d < D && row / share < count)   // (no parts for a row without a token)
+    if (row >= 0 && d < D)
 #pragma unroll 2
       for (int c = c0 + g; c <= c1; c += G) {
         // (the first block only ends in the unit's tiles, the others begin in them)

@@ -124,12 +124,12 @@ __global__ void __launch_bounds__(kThreads) cache_f32_kernel(const __grid_consta
       const float* sK = shared + (t % C::STAGES) * C::STAGE;
       float* sV = shared + (t % C::STAGES) * C::STAGE + kKeys * C::ROW;
       const int start = k_begin + t * kKeys;
-      const bool drafts = start + kKeys > w.len;
+      const bool drafts = start + kKeys > w.open;
       if (drafts && w.count > 1) {     // (values that are not finite: as in cache_few.cu)
         bool found = false;
         for (int i = threadIdx.x; i < kKeys * C::CH; i += kThreads) {
           const int kr = i / C::CH;
-          if (start + kr >= w.len && start + kr < k_end)
+          if (start + kr >= w.open && start + kr < k_end)
             found |= clear_unfinite(reinterpret_cast<float4*>(sV + kr * C::ROW + i % C::CH * 4));
         }
         unclean |= __syncthreads_or(found);
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) cache_f32_kernel(const __grid_consta
 template <int D>
 cudaError_t launch_typed(const CacheParams& p, int blocks, cudaStream_t stream) {
   const cudaError_t e = cross_run<cache_f32_kernel<D>>(blocks, 1, kThreads, Cfg<D>::SMEM, stream, p);
-  if (e != cudaSuccess || !p.split) return e;
+    if (e != cudaSuccess || !p.split) return e;
   return cache_join<R, D, float>(p, blocks, stream);
 }
 

@@ -89,7 +89,7 @@ __device__ __forceinline__ void mask_scores(uint32_t (&s)[128], uint32_t seen) {
 struct Work : CachePiece {
   int k0, k1;     // its keys
   int n;          // its key tiles
-  int drafts;     // the first of them that holds drafts
+  int drafts;     // the first of them with keys that not every row sees
   int halves;     // query tiles with rows
 };
 
@@ -104,7 +104,7 @@ __device__ __forceinline__ Work next_work(const CacheParams& p, CacheWalk<kBN>& 
   w.k0 = w.t0 * kBN;
   w.k1 = min(w.len + w.count, w.t1 * kBN);
   w.n = w.t1 - w.t0;
-  w.drafts = max(0, w.len - w.k0) / kBN;
+  w.drafts = max(0, w.open - w.k0) / kBN;
   const int share = p.heads / p.kv_heads;
   w.halves = !PAIR && (w.rt * p.tile_rows + p.half_rows) / share < w.count ? 2 : 1;
   return w;
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++nd;
           const int start = w.k0 + j * kBN, valid = min(kBN, w.k1 - start);
-          const int from = w.count > 1 ? max(0, w.len - start) : valid;   // (a lone draft: its rows see it)
+          const int from = w.count > 1 ? max(0, w.open - start) : valid;   // (a lone draft: its rows see it)
           uint8_t* tile = smem + (2 + (2 * g + 1) % C::STAGES) * C::TILE;
           bool found = false;
 #pragma unroll 4
@@ -675,17 +675,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (!whole) {
-        // not divided by l: a part for the join
+        // not divided by l: a part for the join (rows without a token: only that l is 0)
         const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1);
+        if (!PAIR || wg == 0) {
+          float2* dl = cache_part_sums<R, D>(p, gridDim.x, part, place);
+          if (CPATTN_IN(p.ws_span, dl, 8, p.err)) *dl = live ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+        }
 #pragma unroll 1
         for (int c0 = c_begin; c0 < c_end && mine; c0 += 32) {
           uint32_t o[32];
           features(c0, o);
           if (live) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              cache_write_part<R, D>(p, part, place, c0 + i,
-                                     make_float4(u2f(o[i]), u2f(o[i + 1]), u2f(o[i + 2]), u2f(o[i + 3])), m, l);
+            for (int i = 0; i < 32; i += 4) {
+              float4* dst = cache_part<R, D>(p, part, place, c0 + i);
+              if (CPATTN_IN(p.ws_span, dst, 16, p.err))
+                *dst = make_float4(u2f(o[i]), u2f(o[i + 1]), u2f(o[i + 2]), u2f(o[i + 3]));
+            }
           }
           __syncwarp();
         }
@@ -755,7 +761,7 @@ cudaError_t launch_typed(const CacheMaps& m, const CacheParams& p, int blocks, c
   cudaError_t e = cross_set_up(kernel, Cfg<D>::SMEM, ready, kLaunchRegs);
   if (e != cudaSuccess) return e;
   e = launch_behind(kernel, dim3(blocks), kThreads, Cfg<D>::SMEM, stream, m.q, m.k, m.v, p);
-  if (e != cudaSuccess || !p.split) return e;
+    if (e != cudaSuccess || !p.split) return e;
   return cache_join<PAIR ? 128 : 256, D, __nv_bfloat16>(p, blocks, stream);
 }
 

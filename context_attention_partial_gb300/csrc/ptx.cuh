@@ -51,6 +51,13 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool read)
   else
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+// The same (with the rest of the line) and an L2 cache policy.
+__device__ __forceinline__ void copy16_hint(uint32_t dst, const void* src, bool read, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::128B [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(read ? 16 : 0), "l"(policy)
+               : "memory");
+}
+// 4 bytes.
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool read) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(read ? 4 : 0) : "memory");
 }
