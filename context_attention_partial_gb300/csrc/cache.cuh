@@ -132,6 +132,7 @@ template <int KT>
 struct CacheWalk {
   int pos, end;    // tiles of the line (not split: units): the next, one past the last
   int base, x;     // pair (b, row tile) that holds the next; its first tile
+  int tiles, len, count;   // of the pair
 
   // Key tiles of pair x.
   __device__ static int tiles_of(const CacheParams& p, int x, int* len, int* count) {
@@ -146,12 +147,11 @@ struct CacheWalk {
   __device__ void start(const CacheParams& p) {
     pos = blockIdx.x;
     end = p.batch * p.row_tiles * p.kv_heads;
-    base = x = 0;
+    base = x = tiles = len = count = 0;
     if (!p.split) return;
     const int lane = threadIdx.x % 32, pairs = p.batch * p.row_tiles;
     unsigned total = 0;
     for (int x0 = 0; x0 < pairs; x0 += 32) {
-      int len, count;
       total += __reduce_add_sync(
           0xffffffffu, x0 + lane < pairs ? static_cast<unsigned>(tiles_of(p, x0 + lane, &len, &count) * p.kv_heads) : 0u);
     }
@@ -164,8 +164,9 @@ struct CacheWalk {
     end = pos + each + (blockIdx.x < more ? 1 : 0);
     // the pair that holds pos
     for (int x0 = 0; x0 < pairs; x0 += 32) {
-      int len, count;
-      const int w = x0 + lane < pairs ? tiles_of(p, x0 + lane, &len, &count) * p.kv_heads : 0;
+      tiles = len = count = 0;
+      if (x0 + lane < pairs) tiles = tiles_of(p, x0 + lane, &len, &count);
+      const int w = tiles * p.kv_heads;
       int sum = w;
 #pragma unroll
       for (int m = 1; m < 32; m *= 2) {
@@ -177,6 +178,9 @@ struct CacheWalk {
         const int i = __ffs(behind) - 1;
         x = x0 + i;
         base += __shfl_sync(0xffffffffu, sum - w, i);
+        tiles = __shfl_sync(0xffffffffu, tiles, i);
+        len = __shfl_sync(0xffffffffu, len, i);
+        count = __shfl_sync(0xffffffffu, count, i);
         return;
       }
       base += __shfl_sync(0xffffffffu, sum, 31);
@@ -189,23 +193,26 @@ struct CacheWalk {
         x = pos / p.kv_heads;
         w.hk = pos - x * p.kv_heads;
         pos += gridDim.x;
-        w.tiles = tiles_of(p, x, &w.len, &w.count);
-        if (w.tiles == 0) continue;
+        tiles = tiles_of(p, x, &len, &count);
+        if (tiles == 0) continue;
         w.t0 = 0;
-        w.t1 = w.tiles;
+        w.t1 = tiles;
       } else {
-        w.tiles = tiles_of(p, x, &w.len, &w.count);
-        const int off = pos - base, all = w.tiles * p.kv_heads;
+        const int off = pos - base, all = tiles * p.kv_heads;
         if (off >= all) {
           base += all;
           ++x;
+          tiles = tiles_of(p, x, &len, &count);
           continue;
         }
-        w.hk = off / w.tiles;
-        w.t0 = off - w.hk * w.tiles;
-        w.t1 = min(w.t0 + end - pos, w.tiles);
+        w.hk = off / tiles;
+        w.t0 = off - w.hk * tiles;
+        w.t1 = min(w.t0 + end - pos, tiles);
         pos += w.t1 - w.t0;
       }
+      w.tiles = tiles;
+      w.len = len;
+      w.count = count;
       w.b = x / p.row_tiles;
       w.rt = x - w.b * p.row_tiles;
       w.open = w.len + (p.parents != nullptr ? 0 : w.rt * p.tile_rows / (p.heads / p.kv_heads) + 1);

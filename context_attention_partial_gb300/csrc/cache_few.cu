@@ -14,8 +14,8 @@
 // blocks an SM.
 //
 // A block of 4 warps walks its keys in stages of 64, three or more in flight by
-// 16-byte asynchronous copies, each from its page; the page numbers of a stage are
-// read while the one before it is asked for.  MT = 1, 2 or 4 tiles of 16 rows; the
+// 16-byte asynchronous copies, each from its page; a warp holds 32 page numbers and has
+// the next 32 on their way.  MT = 1, 2 or 4 tiles of 16 rows; the
 // 4 / MT warps of a row tile share a stage's keys and are joined at the end.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -71,26 +71,29 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
   while (walk.next(p, w)) {
     if (threadIdx.x == 0) cache_note_unit<R, D>(p, w);
     const int k_begin = w.t0 * kKeys, k_end = min(w.len + w.count, w.t1 * kKeys), tiles = w.t1 - w.t0;
-    // page numbers of a stage, at most four
-    auto pages = [&](int t, int (&pg)[4]) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int key = k_begin + t * kKeys + (j << p.cache.shift);
-        pg[j] = t < tiles && (j << p.cache.shift) < kKeys && key < k_end ? cache_page(p.cache, w.b, key, p.err) : -1;
-      }
+    // page numbers, 32 at a time, a lane each; the next 32 are read ahead
+    const int entry0 = k_begin >> p.cache.shift, in_page = k_begin & ((1 << p.cache.shift) - 1);
+    auto read_pages = [&](int window) {
+      const int key = (entry0 + window * 32 + lane) << p.cache.shift;
+      return key < k_end ? cache_page(p.cache, w.b, key, p.err) : -1;
     };
+    int window = 0, here = read_pages(0), ahead = read_pages(1);
     // this thread's copies of a stage: chunk c of rows r_first, r_first + RSTEP, ...
     const char* kbase = static_cast<const char*>(p.k.data) + w.hk * p.k.s[1] * 2 + c * 16;
     const char* vbase = static_cast<const char*>(p.v.data) + w.hk * p.v.s[1] * 2 + c * 16;
-    int pg[4];
-    pages(0, pg);
     auto load = [&](int t) {
       if (t < tiles) {
+        // (a stage's pages are of one window: both begin at multiples of a stage's pages)
+        if ((in_page + t * kKeys) >> p.cache.shift >> 5 != window) {
+          ++window;
+          here = ahead;
+          ahead = read_pages(window + 1);
+        }
         const uint32_t dst = s0 + (t % C::STAGES) * C::STAGE;
 #pragma unroll
         for (int i = 0; i < kKeys / RSTEP; ++i) {
-          const int r = r_first + i * RSTEP, key = k_begin + t * kKeys + r, j = r >> p.cache.shift;
-          const int64_t page = j == 0 ? pg[0] : j == 1 ? pg[1] : j == 2 ? pg[2] : pg[3];
+          const int r = r_first + i * RSTEP, key = k_begin + t * kKeys + r;
+          const int64_t page = __shfl_sync(0xffffffffu, here, (in_page + t * kKeys + r) >> p.cache.shift & 31);
           const int at_row = key & ((1 << p.cache.shift) - 1);
           const uint32_t at = r * C::ROW + ((c ^ (r & 7)) << 4);
           const char* kp = kbase + (page * p.k.s[0] + at_row * p.k.s[2]) * 2;
@@ -101,7 +104,6 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
         }
       }
       copies_commit();
-      pages(t + 1, pg);
     };
     __syncthreads();   // (the piece before has read its rows, paths and sums)
 #pragma unroll
