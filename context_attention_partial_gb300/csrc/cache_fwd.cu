@@ -110,6 +110,19 @@ __device__ __forceinline__ Work next_work(const CacheParams& p, CacheWalk<kBN>& 
   return w;
 }
 
+// Rows of a query tile as tokens and heads: row x is token x / share, head x % share of
+// the tile's (x < 128, so 16 bits of the quotient's factor are exact).
+struct Rows {
+  int share, tokens, factor;   // heads, tokens of a tile
+  __device__ explicit Rows(const CacheParams& p)
+      : share(p.heads / p.kv_heads), tokens(p.half_rows / share), factor((65535 + share) / share) {}
+  // Row x's token counted from the tile's, or -1: none.
+  __device__ int token(int x) const {
+    const int t = (x * factor) >> 16;
+    return t < tokens ? t : -1;
+  }
+};
+
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -186,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   cache_prefetch(p);
   const uint32_t tmem = *tmem_holder;
-  const int share = p.heads / p.kv_heads;
+  const Rows rows(p);
+  const int share = rows.share;
   // every wait of a warp is voted on, so its lanes stay together
   auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) {
     const bool r = mbar_wait(bar, parity, abort_flag, p.timeout_ns, p.err, code);
@@ -240,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) return;
           if (leader) {
             mbar_arrive_expect_tx(bar_q(i), q_bytes);
-            const int token = (x.rt * p.tile_rows + i * p.half_rows) / share;
+            const int token = (x.rt * (PAIR ? 1 : 2) + i) * rows.tokens;
 #pragma unroll
             for (int c = 0; c < C::KB; ++c)
               tma_load_4d_hint(sQ + i * C::TILE + c * kBM * 128, &tm_q, bar_q(i), c * 64, x.hk * share, token, x.b, pol_q);
@@ -268,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < wn.halves; ++i)
 #pragma unroll
             for (int c = 0; c < C::KB; ++c)
-              tma_prefetch_l2_4d(&tm_q, c * 64, wn.hk * share, (wn.rt * p.tile_rows + i * p.half_rows) / share, wn.b);
+              tma_prefetch_l2_4d(&tm_q, c * 64, wn.hk * share, (wn.rt * (PAIR ? 1 : 2) + i) * rows.tokens, wn.b);
         for (int j = 0; j < w.n && ok; ++j) {
           const bool in_unit = j + 1 < w.n, more = in_unit || more_units;
           const int sv = ld % C::STAGES, sk = (ld + 1) % C::STAGES;
@@ -493,18 +507,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int start = w.k0 + j * kBN, valid = min(kBN, w.k1 - start);
           const int from = w.count > 1 ? max(0, w.open - start) : valid;   // (a lone draft: its rows see it)
           uint8_t* tile = smem + (2 + (2 * g + 1) % C::STAGES) * C::TILE;
-          bool found = false;
+          // (a value times 0 is not 0 where it is not finite)
+          __nv_bfloat162 zero = __float2bfloat162_rn(0.f), acc[2] = {zero, zero};
 #pragma unroll 4
-          for (int i = from * 8 + lane; i < kBN * 8; i += 32) {
+          for (int i = from * 8 + lane; i < valid * 8; i += 32)
 #pragma unroll
             for (int c = 0; c < C::KB; ++c) {
-              uint4* at = reinterpret_cast<uint4*>(tile + c * kBN * 128 + i * 16);
-              if (i >= valid * 8)
-                *at = make_uint4(0, 0, 0, 0);
-              else
-                found |= clear_unfinite(at);
+              const uint4 v = *reinterpret_cast<const uint4*>(tile + c * kBN * 128 + i * 16);
+              const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[e % 2] = __hfma2(x[e], zero, acc[e % 2]);
             }
+          const float2 sum = __bfloat1622float2(__hadd2(acc[0], acc[1]));
+          const bool found = !(sum.x + sum.y == 0.f);
+          if (__any_sync(0xffffffffu, found)) {
+#pragma unroll 1
+            for (int i = from * 8 + lane; i < valid * 8; i += 32)
+              for (int c = 0; c < C::KB; ++c) clear_unfinite(reinterpret_cast<uint4*>(tile + c * kBN * 128 + i * 16));
           }
+#pragma unroll 4
+          for (int i = valid * 8 + lane; i < kBN * 8; i += 32)
+#pragma unroll
+            for (int c = 0; c < C::KB; ++c) *reinterpret_cast<uint4*>(tile + c * kBN * 128 + i * 16) = make_uint4(0, 0, 0, 0);
           if (found) unclean[number % 8] = number;
           fence_proxy_async_smem();
           __syncwarp();
@@ -524,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stage = staging + warp * 2048;
     uint32_t* path = all_paths + threadIdx.x * kTreeWords;
     const int x = quarter * 32 + lane;                 // this thread's row of its query tile
+    const int row_token = rows.token(x);
     int ns = 0, no[2] = {0, 0};
     bool ok = true;
     // First a piece of nothing: a tile of whatever tensor memory holds, of which nothing
@@ -539,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Work& w = pieces[number >= 0 ? number % kPieces : kPieces];
       const bool mine = PAIR || wg < w.halves;
       const int place = (PAIR ? 0 : wg * kBM) + x;
+      const int first_token = (PAIR ? w.rt : w.rt * 2 + wg) * rows.tokens;   // of the query tile
       float m = -INFINITY, l = 0.f;
       if (number >= 0 && mine && p.parents != nullptr) {   // (this warp's copy, on its way until the first drafts)
         for (int i = lane; i < p.s_q; i += 32) {
@@ -573,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_max_x128(tS, s, row_max);
         } else {
           tmem_ld_x128(tS, s);
-          const int start = w.k0 + j * kBN, row = cache_row(p, w.rt, place), token = row < 0 ? p.s_q : row / share;
-          const bool live = token < w.count;
+          const int start = w.k0 + j * kBN, token = first_token + row_token;
+          const bool live = row_token >= 0 && token < w.count;
           if (p.parents != nullptr && !paths) make_path(live ? token : -1);
           // what the row sees of 32 keys at a time (seldom: the last tile or two of a unit)
           auto seen = [&](int at) -> uint32_t {
@@ -626,8 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const bool whole = w.whole();
-      const int row = cache_row(p, w.rt, place), token = row < 0 ? p.s_q : row / share;
-      const bool live = token < w.count;
+      const int token = first_token + row_token;
+      const bool live = row_token >= 0 && token < w.count;
       if (ok && mine) {
         for (int i = 0; i < (PAIR ? 2 : 1); ++i) {
           const int o = PAIR ? i : wg;
@@ -699,18 +725,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rows without a token, or all of whose scores are -inf: (0, -inf)
         const bool none = !live || l == 0.f;
         const float inv = none ? 0.f : 1.f / l;
-        if ((!PAIR || wg == 0) && row >= 0) {
-          float* dl = static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] + (w.hk * share + row % share) * p.lse.s[1] +
-                      token * p.lse.s[2];
+        if ((!PAIR || wg == 0) && row_token >= 0 && token < p.s_q) {
+          float* dl = static_cast<float*>(p.lse.data) + w.b * p.lse.s[0] +
+                      (w.hk * share + x - row_token * share) * p.lse.s[1] + token * p.lse.s[2];
           if (CPATTN_IN(p.lse.span, dl, 4, p.err)) *dl = none ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
         }
         // through the warp's stage, 64 bytes of each of its rows at a time: the lane's
         // four rows there, and its 16 bytes of them
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out.data) + w.b * p.out.s[0] +
+                                   w.hk * share * p.out.s[1] + first_token * p.out.s[2] + lane % 4 * 8;
         int64_t to[4];
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-          const int rw = cache_row(p, w.rt, place - lane + it * 8 + lane / 4), tk = rw / share;
-          to[it] = rw < 0 ? -1 : w.b * p.out.s[0] + (w.hk * share + rw - tk * share) * p.out.s[1] + tk * p.out.s[2] + lane % 4 * 8;
+          const int r = quarter * 32 + it * 8 + lane / 4, t = rows.token(r);
+          to[it] = t < 0 || first_token + t >= p.s_q ? -1 : (r - t * share) * p.out.s[1] + t * p.out.s[2];
         }
         __syncwarp();
 #pragma unroll 1
@@ -731,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int it = 0; it < 4; ++it) {
             const int r = it * 8 + lane / 4;
             const uint4 v = reinterpret_cast<const uint4*>(stage)[r * 4 + (lane % 4 ^ ((r >> 1) & 3))];
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out.data) + to[it] + c0;
+            __nv_bfloat16* dst = out + to[it] + c0;
             if (to[it] >= 0 && CPATTN_IN(p.out.span, dst, 16, p.err)) *reinterpret_cast<uint4*>(dst) = v;
           }
           __syncwarp();
