@@ -496,7 +496,7 @@ cudaError_t cache_join(const CacheParams& p, int most, cudaStream_t stream) {
                        grid, kJoinThreads, 0, stream, p, most);
 }
 
-// bf16 inputs, row tiles of 16, 32 or 64 rows, on `blocks` blocks
+// bf16 inputs, row tiles of 16 or 64 rows, on `blocks` blocks
 cudaError_t launch_cache_few(int head_dim, int rows, const CacheParams& p, int blocks, cudaStream_t stream);
 // bf16 inputs, row tiles of 128 places (one tile of the tensor cores) or 256 (two)
 struct CacheMaps {

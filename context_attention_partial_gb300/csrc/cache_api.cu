@@ -211,10 +211,15 @@ cpattn_status cache_shape(const cpattn_tensor* q, const cpattn_tensor* key_pages
   return CPATTN_OK;
 }
 
-// Whether a bf16 call goes to the tensor cores' 128-row tiles.
+// Whether a bf16 call goes to the tensor cores' 128-row tiles: more than 16 rows a key
+// head (us, cache_few.cu's kernel / the tensor cores': 8 sequences x 8 key heads x 8192
+// keys, D = 128: 16 rows 51.8 / 52.6, 24 rows 57.9 / 52.8, 64 rows 79.8 / 54.3; one
+// sequence of 1000 keys: 4 rows 10.5 / 11.6, 16 rows 11.8 / 12.3, 24 rows 13.0 / 12.5;
+// 4 x 24 heads x 4000 keys, D = 64: 1 row 28.7 / 30.9, 16 rows 31.8 / 32.9, 24 rows
+// 36.3 / 33.1).  A token's rows have to fit a tile.
 bool cache_many(const cpattn_tensor* q, const cpattn_tensor* key_pages) {
   const int64_t share = q->shape[1] / key_pages->shape[1], rows = q->shape[2] * share;
-  return rows > 32 && share <= 128 && key_pages->shape[0] > 0;
+  return rows > 16 && share <= 128 && key_pages->shape[0] > 0;
 }
 
 // Queries as the tensor cores' tiles take them: dims (D, H, S, B), boxes of 64 features,
@@ -251,7 +256,7 @@ CachePlan cache_plan(const cpattn_tensor* q, const cpattn_tensor* key_pages, con
     c.keys = 128;
     slots = sm_count();
   } else {
-    c.places = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    c.places = rows <= 16 ? 16 : 64;
     c.keys = 64;
   }
   if (c.tile_rows == 0) c.tile_rows = c.half_rows = c.places;

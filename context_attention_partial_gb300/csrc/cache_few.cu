@@ -15,8 +15,9 @@
 //
 // A block of 4 warps walks its keys in stages of 64, three or more in flight by
 // 16-byte asynchronous copies, each from its page; a warp holds 32 page numbers and has
-// the next 32 on their way.  MT = 1, 2 or 4 tiles of 16 rows; the
-// 4 / MT warps of a row tile share a stage's keys and are joined at the end.
+// the next 32 on their way.  MT = 1 tile of 16 rows, whose 4 warps share a stage's keys
+// and are joined at the end, or 4 (more than 128 query heads a key head, which the
+// tensor cores' tiles do not hold), a warp each.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -304,10 +305,8 @@ cudaError_t launch_tiles(const CacheParams& params, int blocks, cudaStream_t str
 
 cudaError_t launch_cache_few(int head_dim, int rows, const CacheParams& p, int blocks, cudaStream_t stream) {
   if (head_dim == 64)
-    return rows == 16 ? launch_tiles<64, 1>(p, blocks, stream)
-                      : rows == 32 ? launch_tiles<64, 2>(p, blocks, stream) : launch_tiles<64, 4>(p, blocks, stream);
-  return rows == 16 ? launch_tiles<128, 1>(p, blocks, stream)
-                    : rows == 32 ? launch_tiles<128, 2>(p, blocks, stream) : launch_tiles<128, 4>(p, blocks, stream);
+    return rows == 16 ? launch_tiles<64, 1>(p, blocks, stream) : launch_tiles<64, 4>(p, blocks, stream);
+  return rows == 16 ? launch_tiles<128, 1>(p, blocks, stream) : launch_tiles<128, 4>(p, blocks, stream);
 }
 
 }  // namespace cpattn

@@ -207,6 +207,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, r) != 0;
   };
 
+  // The same for a wait that is over only when some key tiles are: at 50 us a tile.
+  auto wait_long = [&](uint32_t bar, uint32_t parity, long long tiles, unsigned code) {
+    const bool r = mbar_wait(bar, parity, abort_flag, p.timeout_ns + tiles * 50000, p.err, code);
+    return __all_sync(0xffffffffu, r) != 0;
+  };
   // Piece `number` of this block, once announced; false: no more, or a wait ran out (ok).
   auto take = [&](int number, bool& ok, unsigned code) {
     ok = wait_all(bar_piece(number % kPieces), (number / kPieces) & 1, code);
@@ -482,7 +487,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       walk.start(p);
       for (int number = 0;; ++number) {
         const Work w = next_work<PAIR>(p, walk);
-        if (number >= kPieces && !wait_all(bar_done(number % kPieces), (number / kPieces - 1) & 1, kErrWalk)) break;
+        if (number >= kPieces) {
+          // (some pieces may have to end, which takes as long as their tiles)
+          long long tiles = 0;
+          for (int i = 0; i < kPieces; ++i) tiles += pieces[i].n;
+          if (!wait_long(bar_done(number % kPieces), (number / kPieces - 1) & 1, tiles, kErrWalk)) break;
+        }
         if (leader) {
           if (w.n != 0) cache_note_unit<R, D>(p, w);
           pieces[number % kPieces] = w;
@@ -501,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = w.n;
         g += min(w.drafts, n);
         for (int j = w.drafts; j < n; ++j, ++g) {
-          ok = wait_all(bar_dirty, nd & 1, kErrClean);
+          ok = wait_long(bar_dirty, nd & 1, j + kPieces, kErrClean);
           if (!ok) break;
           ++nd;
           const int start = w.k0 + j * kBN, valid = min(kBN, w.k1 - start);
