@@ -101,11 +101,12 @@ __device__ __forceinline__ int cache_row(const CacheParams& p, int rt, int r) {
   return x < p.half_rows && row < p.s_q * (p.heads / p.kv_heads) ? row : -1;
 }
 
-// Key tiles that a block takes at least before another one shares its work.
-// (8 key heads x 1000 keys, one token, tiles of 64: at least 2 tiles 11.6 us, 3 tiles
-// 15.2, 6 tiles 18.0; fp32 tiles of 32: 13 rows a key head x 700 keys 18.0 with 2 or 3,
-// 21.8 with 5, one row x 3000 keys 18.5 with 3, 22.6 with 1)
-constexpr int cache_min_tiles(int keys) { return keys >= 64 ? 2 : 3; }
+// Key tiles that a block takes at least before another one shares its work, for row
+// tiles of `places` and key tiles of `keys` (us; tiles of 64 keys, one token, 8 key
+// heads x 1000 keys: at least 2 tiles 11.6, 3 tiles 15.2, 6 tiles 18.0; fp32, tiles of
+// 32: 16 rows x 3000 keys 18.2 with 3, 20.7 with 1; 64 rows x 700 keys 20.4 with 3,
+// 15.7 with 1).
+constexpr int cache_min_tiles(int places, int keys) { return keys >= 64 ? 2 : places > 16 ? 1 : 3; }
 // Units a block above which none are split: then a round of whole units is at most
 // an eighth of the call, and the tables that a split needs would be long.
 constexpr int kCacheWholeUnits = 8;
@@ -119,20 +120,29 @@ struct CachePiece {
   __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
+// What the beginning and end of a unit cost, in key tiles (us with 0 and with this: tiles
+// of 128 keys, 2048 tokens from an empty cache 96.1 / 48.8, trees of 27 x 8192 keys 38.8
+// / 37.3; of 64, 8 sequences of 1000 keys 15.7 / 13.9; of 32 13 fp32 rows 24.9 / 20.6).
+constexpr int cache_unit_cost(int keys) { return keys >= 128 ? 3 : keys >= 64 ? 2 : 1; }
+
 // Deals the key tiles out to the blocks, evenly, whatever the lengths are.  All (row
 // tile, key head) units of all sequences stand in a line, b slowest, then row tile,
-// then key head; block c takes the c-th of `blocks` stretches of the line's key tiles
-// (equal, but for one tile), so its pieces are the end of a unit, whole units, and the
+// then key head, and each is its key tiles and some that stand for its beginning and
+// end; block c takes the c-th of `blocks` stretches of the line's tiles (equal, but for
+// one), so its pieces are the end of a unit, whole units, and the
 // beginning of one.  A piece that is not a whole unit goes to the workspace: slot 0 of
 // the block if it begins inside its unit, slot 1 if it only ends there; the blocks
 // that begin and end a unit note themselves for the join kernel.  Not split: whole
 // units, c, c + blocks, ...
-// KT: keys of a key tile.  A split line has less than 2^31 tiles.  Whole warps.
-template <int KT>
+// R: places of a row tile, KT: keys of a key tile.  A split line has less than 2^31 tiles.  Whole warps.
+template <int R, int KT>
 struct CacheWalk {
   int pos, end;    // tiles of the line (not split: units): the next, one past the last
   int base, x;     // pair (b, row tile) that holds the next; its first tile
   int tiles, len, count;   // of the pair
+
+  // A unit's length in the line.
+  __device__ static int length(int tiles) { return tiles > 0 ? tiles + cache_unit_cost(KT) : 0; }
 
   // Key tiles of pair x.
   __device__ static int tiles_of(const CacheParams& p, int x, int* len, int* count) {
@@ -153,9 +163,9 @@ struct CacheWalk {
     unsigned total = 0;
     for (int x0 = 0; x0 < pairs; x0 += 32) {
       total += __reduce_add_sync(
-          0xffffffffu, x0 + lane < pairs ? static_cast<unsigned>(tiles_of(p, x0 + lane, &len, &count) * p.kv_heads) : 0u);
+          0xffffffffu, x0 + lane < pairs ? static_cast<unsigned>(length(tiles_of(p, x0 + lane, &len, &count)) * p.kv_heads) : 0u);
     }
-    unsigned blocks = (total + cache_min_tiles(KT) - 1) / cache_min_tiles(KT);
+    unsigned blocks = (total + cache_min_tiles(R, KT) - 1) / cache_min_tiles(R, KT);
     blocks = blocks < gridDim.x ? blocks : gridDim.x;
     pos = end = 0;
     if (blockIdx.x >= blocks) return;
@@ -166,7 +176,7 @@ struct CacheWalk {
     for (int x0 = 0; x0 < pairs; x0 += 32) {
       tiles = len = count = 0;
       if (x0 + lane < pairs) tiles = tiles_of(p, x0 + lane, &len, &count);
-      const int w = tiles * p.kv_heads;
+      const int w = length(tiles) * p.kv_heads;
       int sum = w;
 #pragma unroll
       for (int m = 1; m < 32; m *= 2) {
@@ -198,17 +208,18 @@ struct CacheWalk {
         w.t0 = 0;
         w.t1 = tiles;
       } else {
-        const int off = pos - base, all = tiles * p.kv_heads;
+        const int off = pos - base, unit = length(tiles), all = unit * p.kv_heads;
         if (off >= all) {
           base += all;
           ++x;
           tiles = tiles_of(p, x, &len, &count);
           continue;
         }
-        w.hk = off / tiles;
-        w.t0 = off - w.hk * tiles;
+        w.hk = off / unit;
+        w.t0 = off - w.hk * unit;
         w.t1 = min(w.t0 + end - pos, tiles);
-        pos += w.t1 - w.t0;
+        pos += unit - w.t0;            // (beyond the end, if the piece ends there)
+        if (w.t0 >= tiles) continue;   // (what stands for the unit's end)
       }
       w.tiles = tiles;
       w.len = len;
@@ -246,7 +257,7 @@ __device__ __forceinline__ void cache_empty_units(const CacheParams& p, int t, i
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int x = static_cast<int>(u / p.kv_heads), hk = static_cast<int>(u % p.kv_heads);
     int len, count;
-    if (CacheWalk<KT>::tiles_of(p, x, &len, &count) != 0) continue;
+    if (CacheWalk<R, KT>::tiles_of(p, x, &len, &count) != 0) continue;
     const int b = x / p.row_tiles, rt = x - b * p.row_tiles;
     if (p.split && t == 0) {   // (nothing to join)
       int2* at = cache_unit_blocks<R, D>(p, gridDim.x) + u;
@@ -504,8 +515,8 @@ struct CacheMaps {
 };
 cudaError_t launch_cache_fwd(int head_dim, int places, const CacheMaps& maps, const CacheParams& p, int blocks,
                              cudaStream_t stream);
-// fp32 inputs, row tiles of kCacheF32Rows
-constexpr int kCacheF32Rows = 16, kCacheF32Keys = 32;
-cudaError_t launch_cache_f32(int head_dim, const CacheParams& p, int blocks, cudaStream_t stream);
+// fp32 inputs, row tiles of 16 or 64 rows
+constexpr int kCacheF32Keys = 32;
+cudaError_t launch_cache_f32(int head_dim, int rows, const CacheParams& p, int blocks, cudaStream_t stream);
 
 }  // namespace cpattn

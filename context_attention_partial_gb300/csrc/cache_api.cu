@@ -246,7 +246,7 @@ CachePlan cache_plan(const cpattn_tensor* q, const cpattn_tensor* key_pages, con
   const int64_t rows = S * (H / Hk);
   int64_t slots = 2 * static_cast<int64_t>(sm_count());
   if (q->dtype == CPATTN_F32) {
-    c.places = kCacheF32Rows;
+    c.places = rows <= 16 ? 16 : 64;
     c.keys = kCacheF32Keys;
   } else if (cache_many(q, key_pages)) {
     // whole tokens of up to 128 rows, in one or two tiles of the tensor cores
@@ -262,10 +262,10 @@ CachePlan cache_plan(const cpattn_tensor* q, const cpattn_tensor* key_pages, con
   if (c.tile_rows == 0) c.tile_rows = c.half_rows = c.places;
   c.row_tiles = static_cast<int>((rows + c.tile_rows - 1) / c.tile_rows);
   const int64_t units = B * c.row_tiles * Hk;
-  const int64_t most = (page_table->shape[1] * key_pages->shape[2] + S + c.keys - 1) / c.keys;   // tiles of a unit
-  const int64_t least = cache_min_tiles(c.keys);
-  c.split = most > least && units < kCacheWholeUnits * slots && units * most < 0x7fffffff;
-  const int64_t want = c.split ? (units * most + least - 1) / least : units;
+  const int64_t most = (page_table->shape[1] * key_pages->shape[2] + S + c.keys - 1) / c.keys;   // key tiles of a unit
+  const int64_t least = cache_min_tiles(c.places, c.keys);
+  c.split = most > least && units < kCacheWholeUnits * slots && units * (most + cache_unit_cost(c.keys)) < 0x7fffffff;
+  const int64_t want = c.split ? (units * (most + cache_unit_cost(c.keys)) + least - 1) / least : units;
   c.blocks = static_cast<int>(want < slots ? want : slots);
   c.workspace = c.split ? static_cast<size_t>(c.blocks) * 2 * c.places * (D + 2) * 4 + units * 8 : 0;
   return c;
@@ -473,7 +473,7 @@ cpattn_status cpattn_cache_attention(const cpattn_tensor* q, const cpattn_tensor
   p.err = device_error_word();
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int head_dim = static_cast<int>(D);
-  if (q->dtype == CPATTN_F32) return status_of(launch_cache_f32(head_dim, p, plan.blocks, cs));
+  if (q->dtype == CPATTN_F32) return status_of(launch_cache_f32(head_dim, plan.places, p, plan.blocks, cs));
   if (!cache_many(q, key_pages)) return status_of(launch_cache_few(head_dim, plan.places, p, plan.blocks, cs));
   const int share = static_cast<int>(H / key_pages->shape[1]), page = static_cast<int>(key_pages->shape[2]);
   CacheMaps m;

@@ -1,12 +1,14 @@
 // cache_f32.cu -- attention of new tokens to a paged cache of fp32 keys and values,
 // computed in fp32 (no tf32 rounding).
 //
-// Mathematics as in cache_few.cu.  A block of 128 threads takes 16 rows (tokens of the
-// query heads that share a key head) and walks its keys in tiles of 32, the next one in flight by asynchronous
-// copies.  Scores: a thread has one row and every eighth key; P V: the
-// same row, and every eighth group of four features; the eight threads of a row share
-// its maximum and sum by shuffles, and its weights through shared memory.  Rows of
-// shared memory are D + 4 floats, so that eight neighbouring rows use all banks.
+// Mathematics as in cache_few.cu.  A block of 128 threads takes 16 RT rows (tokens of
+// the query heads that share a key head) and walks its keys in tiles of 32, the next
+// one in flight by asynchronous copies.  Scores: a thread has RT rows, 16 apart, and
+// every eighth key; P V: the same rows, and every eighth group of four features; the
+// eight threads of a row share its maximum and sum by shuffles, and its weights through
+// shared memory.  Rows of shared memory are D + 4 floats, so that eight neighbouring
+// rows use all banks.  What bounds it is shared memory's reads: RT + 4 a thread for 4 RT
+// products of four features, so RT = 4 where there are more than 16 rows.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -18,10 +20,11 @@ namespace cpattn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int R = kCacheF32Rows, kKeys = kCacheF32Keys;
+constexpr int kKeys = kCacheF32Keys;
 
-template <int D>
+template <int D, int RT>
 struct Cfg {
+  static constexpr int R = 16 * RT;
   static constexpr int ROW = D + 4;                      // floats of a staged row
   static constexpr int CH = D / 4;                       // 16-byte chunks of a row
   static constexpr int STAGES = 2;
@@ -42,20 +45,21 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-template <int D>
+template <int D, int RT>
 __global__ void __launch_bounds__(kThreads) cache_f32_kernel(const __grid_constant__ CacheParams p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, RT>;
+  constexpr int R = C::R;
   extern __shared__ __align__(16) float shared[];
   float* sQ = shared + C::Q;
   float* sP = shared + C::P;
   uint32_t* paths = reinterpret_cast<uint32_t*>(shared + C::PATHS);
   int* parents = reinterpret_cast<int*>(paths + R * kTreeWords);
-  const int r = threadIdx.x / 8, g = threadIdx.x % 8;   // this thread's row, and place in it
+  const int r = threadIdx.x / 8, g = threadIdx.x % 8;   // this thread's first row, and place in its rows
   const int share = p.heads / p.kv_heads, rows = p.s_q * share;
   cache_prefetch(p);
   launch_wait();
   launch_next();
-  CacheWalk<kKeys> walk;
+  CacheWalk<R, kKeys> walk;
   walk.start(p);
   CachePiece w;
   while (walk.next(p, w)) {
@@ -110,11 +114,17 @@ __global__ void __launch_bounds__(kThreads) cache_f32_kernel(const __grid_consta
     }
     __syncthreads();
     if (p.parents != nullptr) tree_paths<R>(p, parents, w.rt, threadIdx.x, kThreads, paths);
-    const int row = w.rt * R + r, token = row / share;
-    float m = -INFINITY, l = 0.f;
-    float4 o[D / 32];
+    int token[RT];
+    float m[RT], l[RT];
+    float4 o[RT][D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < RT; ++i) {
+      token[i] = (w.rt * R + r + 16 * i) / share;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     bool unclean = false;
 
     for (int t = 0; t < tiles; ++t) {
@@ -134,88 +144,107 @@ __global__ void __launch_bounds__(kThreads) cache_f32_kernel(const __grid_consta
         }
         unclean |= __syncthreads_or(found);
       }
-      float s[kKeys / 8];
+      float s[RT][kKeys / 8];
 #pragma unroll
-      for (int j = 0; j < kKeys / 8; ++j) s[j] = 0.f;
-#pragma unroll 8
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < kKeys / 8; ++j) s[i][j] = 0.f;
+#pragma unroll 4
       for (int d = 0; d < D; d += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(sQ + r * C::ROW + d);
+        float4 k[kKeys / 8];
+#pragma unroll
+        for (int j = 0; j < kKeys / 8; ++j) k[j] = *reinterpret_cast<const float4*>(sK + (g + 8 * j) * C::ROW + d);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float4 q = *reinterpret_cast<const float4*>(sQ + (r + 16 * i) * C::ROW + d);
+#pragma unroll
+          for (int j = 0; j < kKeys / 8; ++j)
+            s[i][j] = fmaf(q.x, k[j].x, fmaf(q.y, k[j].y, fmaf(q.z, k[j].z, fmaf(q.w, k[j].w, s[i][j]))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        unsigned long long seen = 0ull;
+        if (token[i] < w.count)
+          seen = !drafts ? ~0ull
+                 : p.parents == nullptr ? chain_window(w.len, token[i], start)
+                                        : tree_window(paths + (r + 16 * i) * kTreeWords, w.len, start);
+        float top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < kKeys / 8; ++j) {
-          const float4 k = *reinterpret_cast<const float4*>(sK + (g + 8 * j) * C::ROW + d);
-          s[j] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[j]))));
+          s[i][j] = (seen >> (g + 8 * j)) & 1 ? s[i][j] * p.scale_log2 : -INFINITY;
+          top = fmaxf(top, s[i][j]);
         }
-      }
-      unsigned long long seen = 0ull;
-      if (token < w.count)
-        seen = !drafts ? ~0ull
-               : p.parents == nullptr ? chain_window(w.len, token, start) : tree_window(paths + r * kTreeWords, w.len, start);
-      float top = -INFINITY;
+        top = fmaxf(m[i], row_max(top));
+        const float base = top == -INFINITY ? 0.f : top, f = exp2f(m[i] - base);
+        m[i] = top;
+        float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < kKeys / 8; ++j) {
-        s[j] = (seen >> (g + 8 * j)) & 1 ? s[j] * p.scale_log2 : -INFINITY;
-        top = fmaxf(top, s[j]);
-      }
-      top = fmaxf(m, row_max(top));
-      const float base = top == -INFINITY ? 0.f : top;
-      const float f = exp2f(m - base);
-      m = top;
-      float sum = 0.f;
+        for (int j = 0; j < kKeys / 8; ++j) {
+          s[i][j] = exp2f(s[i][j] - base);
+          sum += s[i][j];
+          sP[(r + 16 * i) * (kKeys + 4) + g + 8 * j] = s[i][j];
+        }
+        l[i] = fmaf(l[i], f, row_sum(sum));
 #pragma unroll
-      for (int j = 0; j < kKeys / 8; ++j) {
-        s[j] = exp2f(s[j] - base);
-        sum += s[j];
-        sP[r * (kKeys + 4) + g + 8 * j] = s[j];
+        for (int c = 0; c < D / 32; ++c) o[i][c] = make_float4(o[i][c].x * f, o[i][c].y * f, o[i][c].z * f, o[i][c].w * f);
       }
-      l = fmaf(l, f, row_sum(sum));
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = make_float4(o[i].x * f, o[i].y * f, o[i].z * f, o[i].w * f);
       __syncwarp();                    // (a row's threads are of one warp)
-#pragma unroll 4
+#pragma unroll 2
       for (int k = 0; k < kKeys; k += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(sP + r * (kKeys + 4) + k);
+        float4 x[RT];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f4 = e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w;
+        for (int i = 0; i < RT; ++i) x[i] = *reinterpret_cast<const float4*>(sP + (r + 16 * i) * (kKeys + 4) + k);
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(sV + (k + e) * C::ROW + g * 4 + i * 32);
-            o[i] = make_float4(fmaf(f4, v.x, o[i].x), fmaf(f4, v.y, o[i].y), fmaf(f4, v.z, o[i].z), fmaf(f4, v.w, o[i].w));
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const float4 v = *reinterpret_cast<const float4*>(sV + (k + e) * C::ROW + g * 4 + c * 32);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              const float f = e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w;
+              o[i][c] = make_float4(fmaf(f, v.x, o[i][c].x), fmaf(f, v.y, o[i][c].y), fmaf(f, v.z, o[i][c].z),
+                                    fmaf(f, v.w, o[i][c].w));
+            }
           }
-        }
       }
       __syncthreads();                 // tile t is free
     }
     copies_wait<0>();
-    if (row < rows) {
-      const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1);
-      const int h = w.hk * share + row % share;
+    const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int d = g * 4 + i * 32;
-        if (unclean && token < w.count)
-          add_unfinite<float>(p, w, token, p.parents != nullptr ? paths + r * kTreeWords : nullptr, k_begin, k_end, d, o[i]);
+    for (int i = 0; i < RT; ++i) {
+      const int row = w.rt * R + r + 16 * i, h = w.hk * share + row - token[i] * share;
+      if (row >= rows) continue;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const int d = g * 4 + c * 32;
+        float4 sum = o[i][c];
+        if (unclean && token[i] < w.count)
+          add_unfinite<float>(p, w, token[i], p.parents != nullptr ? paths + (r + 16 * i) * kTreeWords : nullptr, k_begin,
+                              k_end, d, sum);
         if (w.whole())
-          cache_write_row<float>(p, w.b, h, token, d, o[i], m, l);
+          cache_write_row<float>(p, w.b, h, token[i], d, sum, m[i], l[i]);
         else
-          cache_write_part<R, D>(p, part, r, d, o[i], m, l);
+          cache_write_part<R, D>(p, part, r + 16 * i, d, sum, m[i], l[i]);
       }
     }
   }
   cache_empty_units<float, R, kKeys, D>(p, threadIdx.x, kThreads);
 }
 
-template <int D>
+template <int D, int RT>
 cudaError_t launch_typed(const CacheParams& p, int blocks, cudaStream_t stream) {
-  const cudaError_t e = cross_run<cache_f32_kernel<D>>(blocks, 1, kThreads, Cfg<D>::SMEM, stream, p);
-    if (e != cudaSuccess || !p.split) return e;
-  return cache_join<R, D, float>(p, blocks, stream);
+  const cudaError_t e = cross_run<cache_f32_kernel<D, RT>>(blocks, 1, kThreads, Cfg<D, RT>::SMEM, stream, p);
+  if (e != cudaSuccess || !p.split) return e;
+  return cache_join<16 * RT, D, float>(p, blocks, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_f32(int head_dim, const CacheParams& p, int blocks, cudaStream_t stream) {
-  return head_dim == 64 ? launch_typed<64>(p, blocks, stream) : launch_typed<128>(p, blocks, stream);
+cudaError_t launch_cache_f32(int head_dim, int rows, const CacheParams& p, int blocks, cudaStream_t stream) {
+  if (head_dim == 64) return rows == 16 ? launch_typed<64, 1>(p, blocks, stream) : launch_typed<64, 4>(p, blocks, stream);
+  return rows == 16 ? launch_typed<128, 1>(p, blocks, stream) : launch_typed<128, 4>(p, blocks, stream);
 }
 
 }  // namespace cpattn

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
   // (keys that one row tile reads leave L2 first: 8 sequences x 16384 keys 58.1 us, 61.0
   // when they are kept)
   const uint64_t policy = p.row_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-  CacheWalk<kKeys> walk;
+  CacheWalk<R, kKeys> walk;
   walk.start(p);
   CachePiece w;
   while (walk.next(p, w)) {

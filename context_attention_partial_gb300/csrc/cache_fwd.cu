@@ -95,7 +95,7 @@ struct Work : CachePiece {
 
 // The next piece of a block's walk (n = 0: no more).
 template <bool PAIR>
-__device__ __forceinline__ Work next_work(const CacheParams& p, CacheWalk<kBN>& walk) {
+__device__ __forceinline__ Work next_work(const CacheParams& p, CacheWalk<PAIR ? 128 : 256, kBN>& walk) {
   Work w;
   if (!walk.next(p, w)) {
     w.n = 0;
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------- the walk
       // (one warp's: the others would each fetch its instructions, at the start of a
       // launch from HBM)
-      CacheWalk<kBN> walk;
+      CacheWalk<PAIR ? 128 : 256, kBN> walk;
       walk.start(p);
       for (int number = 0;; ++number) {
         const Work w = next_work<PAIR>(p, walk);

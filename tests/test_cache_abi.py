@@ -258,56 +258,54 @@ def test_workspace_sizes_without_a_device():
     assert cp.cache_attention_workspace_bytes(q, pages, table[:, :1]) == 0
 
 
-def walk(tiles, kv_heads, blocks, min_tiles=3):
+def walk(tiles, kv_heads, blocks, cost, min_tiles=3):
     """The split of the key tiles over blocks as the kernels do it: per block its pieces
-    (unit, first tile, last tile, tiles of the unit)."""
+    (unit, first tile, last tile, tiles of the unit).  A unit's place in the line is its
+    tiles and `cost` that stand for its beginning and end."""
     line = [n for n in tiles for _ in range(kv_heads)]
-    total = sum(line)
-    used = max(1, min(blocks, -(-total // min_tiles)))
-    begin = lambda c: total * c // used
+    total = sum(n + cost for n in line if n)
+    used = min(blocks, -(-total // min_tiles))
     pieces = []
     for c in range(used):
-        pos, end, mine = begin(c), begin(c + 1), []
-        base = 0
+        each, more = total // used, total % used
+        pos = c * each + min(c, more)
+        end, mine, base = pos + each + (c < more), [], 0
         for u, n in enumerate(line):
             lo, hi = max(pos, base), min(end, base + n)
             if lo < hi:
                 mine.append((u, lo - base, hi - base, n))
-            base += n
+            base += n + cost if n else 0
         pieces.append(mine)
     return pieces
 
 
+@pytest.mark.parametrize("cost", [0, 1, 3])
 @pytest.mark.parametrize("tiles,kv_heads,blocks", [([5], 1, 304), ([1000], 1, 304), ([7, 0, 300, 1], 3, 304),
-                                                   ([0, 0], 2, 10), ([64] * 20, 8, 304), ([1, 2, 3], 5, 4)])
-def test_parts_of_a_unit_have_slots_of_their_own(tiles, kv_heads, blocks):
-    """Every tile is taken once, a block has at most one piece for each of its two slots, and
-    the join finds the same parts."""
-    pieces = walk(tiles, kv_heads, blocks)
+                                                   ([0, 0], 2, 10), ([64] * 20, 8, 304), ([1, 2, 3], 5, 4), ([1] * 40, 2, 30)])
+def test_parts_of_a_unit_have_slots_of_their_own(tiles, kv_heads, blocks, cost):
+    """Every tile is taken once, a block has at most one piece for each of its two slots, and a
+    unit's parts are slot 1 of the block that begins it and slot 0 of all behind it up to the
+    one that ends it, as the join takes them."""
+    pieces = walk(tiles, kv_heads, blocks, cost)
     line = [n for n in tiles for _ in range(kv_heads)]
-    total, used = sum(line), len(pieces)
-    begin = lambda c: total * c // used
     taken = [[0] * n for n in line]
+    first, last, parts = {}, {}, {}
     for c, mine in enumerate(pieces):
         slots = []
         for u, lo, hi, n in mine:
             for i in range(lo, hi):
                 taken[u][i] += 1
+            if lo == 0:
+                first[u] = c
+            if hi == n:
+                last[u] = c
             if (lo, hi) != (0, n):
                 slots.append(0 if lo > 0 else 1)
+                parts.setdefault(u, []).append((c, slots[-1]))
         assert len(slots) == len(set(slots))
     assert all(x == 1 for unit in taken for x in unit)
-    base = 0
     for u, n in enumerate(line):
-        want = [(c, 0 if lo > 0 else 1) for c, mine in enumerate(pieces) for v, lo, hi, _ in mine if v == u]
-        if n:
-            c0 = base * used // total
-            while c0 + 1 < used and begin(c0 + 1) <= base:
-                c0 += 1
-            while c0 > 0 and begin(c0) > base:
-                c0 -= 1
-            c1 = c0
-            while c1 + 1 < used and begin(c1 + 1) < base + n:
-                c1 += 1
-            assert [(c, 0 if begin(c) > base else 1) for c in range(c0, c1 + 1)] == want
-        base += n
+        if n and first[u] != last[u]:
+            assert parts[u] == [(c, 1 if c == first[u] else 0) for c in range(first[u], last[u] + 1)]
+        else:
+            assert u not in parts
