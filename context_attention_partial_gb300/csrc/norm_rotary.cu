@@ -18,9 +18,9 @@
 // short one waits for its first instructions, which also come from HBM, so the code is
 // kept short, and a block's sines and cosines are formed in one loop, to shared memory.
 //
-// Measured: q and k of 24 heads, bf16, D = 128, 4608 tokens (113 MB) 21.4 us, 5.3 TB/s;
+// Measured: q and k of 24 heads, bf16, D = 128, 4608 tokens (113 MB) 23.6 us, 4.8 TB/s;
 // the gradient at 32768 tokens (1.21 GB) 187 us, 6.5 TB/s; four prompts of up to 4001
-// tokens, 48 heads, to a cache (336 MB) 59 us, 5.7 TB/s.
+// tokens, 48 heads, to a cache (336 MB) 57 us, 5.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -264,7 +264,8 @@ __device__ __forceinline__ bool next_tensor(const NormParams& p, int head0, int 
 }
 
 template <typename T, int PAIRING, int L, int V>
-__global__ void __launch_bounds__(kThreads, V == 1 && PAIRING != 0 ? 5 : 4) norm_rotary_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kThreads, V == 1 && PAIRING != 0 ? 5 : 4)
+    norm_rotary_kernel(const __grid_constant__ NormParams p) {
   using S = Shape<T, L, V, 1>;
   constexpr int N = S::N, P = S::P, U = S::U;
   constexpr int64_t es = sizeof(T);
@@ -359,7 +360,11 @@ __global__ void __launch_bounds__(kThreads, V == 1 && PAIRING != 0 ? 5 : 4) norm
       for (int e = 0; e < N; e += 2) {
         const int f = lane[i] ? (at.l + i * L) * N + e : 0;
         wc[i][e / 2] = mul(pack2(w[f], w[f + 1]), vec[i].c[e / 2]);
-        ws[i][e / 2] = lane[i] ? mul(pack2(w[vec[i].partner[e]], w[vec[i].partner[e + 1]]), vec[i].s[e / 2]) : 0;
+        ws[i][e / 2] = 0;
+        if (lane[i])   // (0 for a feature that does not turn, whatever its weight is)
+          ws[i][e / 2] = mul(pack2((vec[i].turned >> e) & 1u ? w[vec[i].partner[e]] : 0.f,
+                                   (vec[i].turned >> (e + 1)) & 1u ? w[vec[i].partner[e + 1]] : 0.f),
+                             vec[i].s[e / 2]);
       }
     }
     if (t.paged && !placed) {
@@ -638,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_backward_kernel(const __grid
 __global__ void __launch_bounds__(256) norm_weight_kernel(const __grid_constant__ NormParams p) {
   __shared__ float sums[32][9];
   const int col = blockIdx.x * 8 + threadIdx.x % 8, y = threadIdx.x / 8;
-  const int all = p.n * p.head_dim; 
+  const int all = p.n * p.head_dim;
   launch_wait();
   launch_next();
   float sum = 0.f;

@@ -165,6 +165,24 @@ def test_extreme_rows(dtype):
                            cp.norm_rotary(x[:, :, 5:], None, pos[:3], (64,)))
 
 
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_an_infinite_weight_of_a_feature_that_does_not_turn(dtype, interleaved):
+    """It is that feature's alone: infinite of x's sign there, every other feature as ever."""
+    axes, D = (6, 4), 24   # (10 features turn: some vectors in part)
+    x, = tensors(2, (3,), 9, D, dtype, 5)
+    pos = positions(2, 9, axes, False, 6)
+    w, = weights(1, D, F32, 7)
+    for f in (10, 11, 17):
+        bad = w.clone()
+        bad[f] = float("inf")
+        got = cp.norm_rotary(x, bad, pos, axes, interleaved=interleaved)
+        want = cp.norm_rotary(x, w, pos, axes, interleaved=interleaved)
+        others = [i for i in range(D) if i != f]
+        assert torch.equal(got[..., others], want[..., others])
+        assert torch.equal(got[..., f].float(), x[..., f].float().sign() * float("inf"))
+
+
 def test_no_rows():
     w = torch.ones(64, device=DEV)
     for shape in ((0, 2, 5, 64), (1, 0, 5, 64), (1, 2, 0, 64)):
