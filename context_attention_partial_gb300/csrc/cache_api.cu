@@ -399,6 +399,7 @@ cpattn_status cpattn_cache_append(const cpattn_tensor* q, const cpattn_tensor* k
     t.y_span = {out[i]->data, extent_bytes(out[i], shrink)};
   }
   if (!run) return CPATTN_OK;
+  if (key_pages->data == value_pages->data && key_pages->data) return CPATTN_ERR_LAYOUT;   // (two writers)
   p.n = n;
   p.batch = static_cast<int>(B);
   p.seq = static_cast<int>(S);

@@ -436,7 +436,9 @@ size_t cpattn_norm_rotary_backward_workspace_bytes(int n, const cpattn_tensor* x
  *   positions: f32 [S, axes] or [B, S, axes], with axes, axis_dims, theta and
  *     interleaved as in cpattn_rotary; NULL: nothing turns.
  * Tokens from counts[b] on are not written (q_out has all S).  No two tokens of a call
- * may have the same place in the pool.  B, S or every head count 0 is a no-op.
+ * may have the same place in the pool, and but for q_out and q no element of an output
+ * or of the pages may be an element of another buffer of the call.  B, S or every head
+ * count 0 is a no-op.
  */
 cpattn_status cpattn_cache_append(const cpattn_tensor* q, const cpattn_tensor* k,
                                   const cpattn_tensor* v, const cpattn_tensor* q_weight,

@@ -190,6 +190,7 @@ def test_append_validation():
     assert append(pos=t((3, 1), F32), axes=(63,)) == SHAPE
     assert append(pos=t((3, 1), F32), axes=()) == SHAPE
     assert append(k=t((2, 2, 3, 12)), kp=t((9, 2, 16, 12))) == UNSUP
+    assert append(vp=t((9, 2, 16, 64))) == LAYOUT                  # keys and values in one place
     e = t((2, 2, 0, 64), data=0)
     assert append(k=e, v=e) == OK
 
