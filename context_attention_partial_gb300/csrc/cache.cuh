@@ -129,12 +129,12 @@ constexpr int cache_unit_cost(int keys) { return keys >= 128 ? 3 : keys >= 64 ? 
 // tile, key head) units of all sequences stand in a line, b slowest, then row tile,
 // then key head, and each is its key tiles and some that stand for its beginning and
 // end; block c takes the c-th of `blocks` stretches of the line's tiles (equal, but for
-// one), so its pieces are the end of a unit, whole units, and the
-// beginning of one.  A piece that is not a whole unit goes to the workspace: slot 0 of
-// the block if it begins inside its unit, slot 1 if it only ends there; the blocks
-// that begin and end a unit note themselves for the join kernel.  Not split: whole
-// units, c, c + blocks, ...
-// R: places of a row tile, KT: keys of a key tile.  A split line has less than 2^31 tiles.  Whole warps.
+// one), so its pieces are the end of a unit, whole units, and the beginning of one.  A
+// piece that is not a whole unit goes to the workspace: slot 0 of the block if it begins
+// inside its unit, slot 1 if it only ends there; the blocks that begin and end a unit
+// note themselves for the join kernel.  Not split: whole units, c, c + blocks, ...
+// R: places of a row tile, KT: keys of a key tile.  A split line has less than 2^31
+// tiles.  Whole warps.
 template <int R, int KT>
 struct CacheWalk {
   int pos, end;    // tiles of the line (not split: units): the next, one past the last
@@ -252,6 +252,7 @@ __device__ __forceinline__ void cache_note_unit(const CacheParams& p, const Cach
 // out by their number; thread t of `threads` of a block.
 template <typename T, int R, int KT, int D>
 __device__ __forceinline__ void cache_empty_units(const CacheParams& p, int t, int threads) {
+  if (p.cache.counts == nullptr) return;   // (every sequence has new tokens)
   const int share = p.heads / p.kv_heads;
   const int64_t units = static_cast<int64_t>(p.batch) * p.row_tiles * p.kv_heads;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -415,6 +416,12 @@ __device__ __forceinline__ void cache_write_part(const CacheParams& p, int64_t p
 // G threads share an item's parts out, so that all of them are on the way at once,
 // and meet in shared memory.  `most`: blocks of the attention's launch.
 constexpr int kJoinThreads = 256;
+// 2^x: fp32 results take the accurate one.
+template <typename T>
+__device__ __forceinline__ float power2(float x) {
+  if constexpr (sizeof(T) == 4) return exp2f(x);
+  return ex2_approx(x);
+}
 template <int R, int D, typename T, int G>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheParams p, int most) {
   constexpr int I = kJoinThreads / G;   // items of a block
@@ -453,7 +460,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
         }
         if (a.y == 0.f) continue;   // (no key of this part)
         const float top = fmaxf(m, a.x), base = top == -INFINITY ? 0.f : top;
-        const float f0 = ex2_approx(m - base), f1 = ex2_approx(a.x - base);
+        const float f0 = power2<T>(m - base), f1 = power2<T>(a.x - base);
         m = top;
         l = l * f0 + a.y * f1;
 #pragma unroll
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     for (int k = 0; k < G; ++k) {
       const float2 a = part_ml[k][it];
       if (a.y == 0.f) continue;
-      const float f = ex2_approx(a.x - base);
+      const float f = power2<T>(a.x - base);
       l = fmaf(f, a.y, l);
       sum = make_float4(fmaf(f, part_sums[k][e][it], sum.x), fmaf(f, part_sums[k][e + 1][it], sum.y),
                         fmaf(f, part_sums[k][e + 2][it], sum.z), fmaf(f, part_sums[k][e + 3][it], sum.w));

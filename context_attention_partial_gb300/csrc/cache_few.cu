@@ -293,11 +293,10 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
 }
 
 template <int D, int MT>
-cudaError_t launch_tiles(const CacheParams& params, int blocks, cudaStream_t stream) {
+cudaError_t launch_tiles(const CacheParams& p, int blocks, cudaStream_t stream) {
   using C = Few<D, MT>;
-  CacheParams p = params;
-  cudaError_t e = cross_run<cache_few_kernel<D, MT>>(blocks, 1, kThreads, C::SMEM, stream, p);
-    if (e != cudaSuccess || !p.split) return e;
+  const cudaError_t e = cross_run<cache_few_kernel<D, MT>>(blocks, 1, kThreads, C::SMEM, stream, p);
+  if (e != cudaSuccess || !p.split) return e;
   return cache_join<C::R, D, __nv_bfloat16>(p, blocks, stream);
 }
 

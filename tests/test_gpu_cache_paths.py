@@ -420,6 +420,34 @@ def test_many_sequences(H, S, dtype):
     assert torch.all(out[none] == 0) and torch.all(lse[none] == -math.inf)
 
 
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("S", [1, 3])
+def test_norm_and_append_of_many_sequences(S, interleaved):
+    """Sequences shorter than a block's tokens: one token each, and three."""
+    B, D = 5000, 64
+    x, k = randn(B, 2, S, D, dtype=BF, seed=1), randn(B, 1, S, D, dtype=BF, seed=2)
+    pos = torch.randint(0, 4000, (B, S, 1), generator=torch.Generator().manual_seed(3)).float().to(DEV)
+    w = 1 + 0.1 * randn(D, dtype=BF, seed=4)
+    kw = dict(interleaved=interleaved)
+    check(cp.norm_rotary(x, w, pos, (D,), **kw), C.norm_rotary(x, w, pos, (D,), **kw))
+    dx, dw = cp.norm_rotary_backward(x, w, pos, (D,), x, **kw)
+    a, b = C.norm_rotary_backward(x, w, pos, (D,), x, **kw)
+    check(dx, a)
+    check(dw, b)
+    pools = [torch.zeros(B, 1, 16, D, dtype=BF, device=DEV) for _ in range(2)]
+    table = torch.randperm(B, generator=torch.Generator().manual_seed(5)).view(B, 1).to(torch.int32).to(DEV)
+    at = torch.randint(0, 13, (B,), generator=torch.Generator().manual_seed(6)).to(torch.int32).to(DEV)
+    q = cp.cache_append(k, k, *pools, table, at, positions=pos, axes_dims=(D,), q=x, weight=w, q_weight=w, **kw)
+    check(q, C.norm_rotary(x, w, pos, (D,), **kw))
+    rows = at.long()[:, None] + torch.arange(S, device=DEV)
+    got = [p[table.long(), 0, rows].unsqueeze(1) for p in pools]
+    check(got[0], C.norm_rotary(k, w, pos, (D,), **kw))
+    assert torch.equal(got[1], k)
+    for p in pools:
+        p[table.long(), 0, rows] = 0
+        assert torch.all(p == 0)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("S", [1, 33, 150])
 def test_views_of_fused_projections(S, dtype):
