@@ -576,27 +576,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int place = (PAIR ? 0 : wg * kBM) + x;
       const int first_token = (PAIR ? w.rt : w.rt * 2 + wg) * rows.tokens;   // of the query tile
       float m = -INFINITY, l = 0.f;
-      if (number >= 0 && mine && p.parents != nullptr) {   // (this warp's copy, on its way until the first drafts)
+      if (mine && p.parents != nullptr && w.drafts < w.n) {
+        // the rows' paths, up from their drafts (this warp's copy of the parents)
         for (int i = lane; i < p.s_q; i += 32) {
           const int32_t* from = p.parents + w.b * p.parents_stride + i;
           copy4(smem_addr(stage) + i * 4, from, CPATTN_IN(p.parents_span, from, 4, p.err));
         }
         copies_commit();
-      }
-      bool paths = false;
-      auto make_path = [&](int at) {   // the row's path, up from draft `at`
-        paths = true;
+#pragma unroll
+        for (int c = 0; c < kTreeWords; c += 4) *reinterpret_cast<uint4*>(path + c) = make_uint4(0u, 0u, 0u, 0u);
         copies_wait<0>();
         __syncwarp();
-#pragma unroll
-        for (int c = 0; c < kTreeWords; ++c) path[c] = 0u;
-        while (at >= 0) {
-          path[at / 32] |= 1u << (at % 32);
-          const int up = reinterpret_cast<const int*>(stage)[at];
-          at = up < at ? up : -1;
+        const int token = first_token + row_token;
+        uint32_t bits = 0u;
+        for (int at = row_token >= 0 && token < w.count ? token : -1; at >= 0;) {
+          int up = reinterpret_cast<const int*>(stage)[at];
+          up = up < at ? up : -1;
+          bits |= 1u << (at % 32);
+          if (up >> 5 != at >> 5) {   // (none above, or in the word before)
+            path[at / 32] = bits;
+            bits = 0u;
+          }
+          at = up;
         }
         __syncwarp();
-      };
+      }
       const int first = PAIR ? wg : 0;
       for (int j = first; mine && j < w.n; j += PAIR ? 2 : 1) {
         ok = wait_all(bar_s(wg), ns & 1, kErrSoftmax);
@@ -611,7 +615,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_x128(tS, s);
           const int start = w.k0 + j * kBN, token = first_token + row_token;
           const bool live = row_token >= 0 && token < w.count;
-          if (p.parents != nullptr && !paths) make_path(live ? token : -1);
           // what the row sees of 32 keys at a time (seldom: the last tile or two of a unit)
           auto seen = [&](int at) -> uint32_t {
             if (!live) return 0u;
@@ -686,8 +689,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const bool add = live && w.count > 1 && unclean[number % 8] == number;
-      // (PAIR: the drafts may have been the other group's; the stage is written below)
-      if (mine && p.parents != nullptr && !paths) make_path(live ? token : -1);
       // features of the row, 32 at a time, from tensor memory
       const int c_begin = PAIR ? wg * (D / 2) : 0, c_end = PAIR ? c_begin + D / 2 : D;
       auto features = [&](int c0, uint32_t (&o)[32]) {
