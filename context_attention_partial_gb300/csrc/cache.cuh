@@ -416,6 +416,10 @@ __device__ __forceinline__ void cache_write_part(const CacheParams& p, int64_t p
 // G threads share an item's parts out, so that all of them are on the way at once,
 // and meet in shared memory.  `most`: blocks of the attention's launch.
 constexpr int kJoinThreads = 256;
+// Items an SM from which a thread has an item's parts to itself (us, from 1024 / never:
+// 1024 new tokens x 17408 keys 176.9 / 178.5, 2048 tokens from an empty cache 47.8 / 49.1;
+// from 300: trees of 27 x 8192 keys 40.0, 36.6 from 1024).
+constexpr int64_t kJoinItems = 1024;
 // 2^x: fp32 results take the accurate one.
 template <typename T>
 __device__ __forceinline__ float power2(float x) {
@@ -468,14 +472,22 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
           sum[e] = make_float4(sum[e].x * f0 + y[e].x * f1, sum[e].y * f0 + y[e].y * f1, sum[e].z * f0 + y[e].z * f1,
                                sum[e].w * f0 + y[e].w * f1);
       }
+    if constexpr (G == 1) {
+      if (row >= 0 && d < D)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      part_sums[g][4 * e][item] = sum[e].x;
-      part_sums[g][4 * e + 1][item] = sum[e].y;
-      part_sums[g][4 * e + 2][item] = sum[e].z;
-      part_sums[g][4 * e + 3][item] = sum[e].w;
+        for (int e = 0; e < 4; ++e)
+          cache_write_row<T>(p, b, hk * share + row % share, row / share, d + 4 * e, sum[e], m, l);
+      return;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        part_sums[g][4 * e][item] = sum[e].x;
+        part_sums[g][4 * e + 1][item] = sum[e].y;
+        part_sums[g][4 * e + 2][item] = sum[e].z;
+        part_sums[g][4 * e + 3][item] = sum[e].w;
+      }
+      part_ml[g][item] = make_float2(m, l);
     }
-    part_ml[g][item] = make_float2(m, l);
   }
   __syncthreads();
   // four threads an item, four features each
@@ -506,9 +518,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
 template <int R, int D, typename T>
 cudaError_t cache_join(const CacheParams& p, int most, cudaStream_t stream) {
   const int units = p.batch * p.row_tiles * p.kv_heads, parts = most / units + 1;
-  const int g = parts <= 2 ? 2 : parts <= 4 ? 4 : 8, items = kJoinThreads / g;
+  const int64_t all = static_cast<int64_t>(units) * R * (D / 16);
+  const int g = all >= kJoinItems * sm_count() ? 1 : parts <= 2 ? 2 : parts <= 4 ? 4 : 8, items = kJoinThreads / g;
   const dim3 grid(units, (R * (D / 16) + items - 1) / items);
-  return launch_behind(g == 2   ? cache_join_kernel<R, D, T, 2>
+  return launch_behind(g == 1   ? cache_join_kernel<R, D, T, 1>
+                       : g == 2 ? cache_join_kernel<R, D, T, 2>
                        : g == 4 ? cache_join_kernel<R, D, T, 4>
                                 : cache_join_kernel<R, D, T, 8>,
                        grid, kJoinThreads, 0, stream, p, most);

@@ -173,6 +173,14 @@ def test_attention(case, kind, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", [(16, 8, 700, 128, 64, (900, 35), (700, 641)), (24, 8, 900, 64, 32, (33, 2000), None)],
+                         ids=lambda c: "x".join(map(str, c[:5])))
+def test_attention_of_many_units_over_many_blocks(case, dtype):
+    """So many rows, of units that blocks share, that one thread joins all parts of an item."""
+    test_attention(case, "chain", dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("S", [1, 2, 31, 100])
 @pytest.mark.parametrize("H,Hk", [(4, 4), (8, 2), (5, 1)])
 def test_attention_at_tile_borders(H, Hk, S, dtype):
