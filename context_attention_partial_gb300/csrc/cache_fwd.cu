@@ -22,8 +22,8 @@
 // a lone tile's products and exponentials would wait for one another.  Otherwise a
 // unit has two query tiles, which read the same keys.
 //
-// Keys.  A 128-key tile is up to eight pages' boxes, each asked for by a lane of the
-// producer.  Scores of keys that a row does not see are masked in registers, by the
+// Keys.  A 128-key tile is up to eight pages' boxes; the producer's lanes hold 32 page
+// numbers and have the next 32 on their way.  Scores of keys that a row does not see are masked in registers, by the
 // bits of its path.  Value rows behind the last key are zeroed in shared memory, and so
 // are a draft's values that are not finite (see cache_few.cu), by warp 10.
 #include <cmath>
@@ -228,28 +228,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       // K tiles on even stages, V tiles on odd ones: the first K alone, then
       // V_j and the K tile after it (of the next piece behind a piece's last V)
       // as one pair on the K stage's barrier, so the MMA warp waits once a
-      // step; the very last V on its own.  Lanes 0-15 ask for a value tile's pages,
-      // lanes 16-31 for a key tile's.  Keys that one row tile reads leave L2 first, so
+      // step; the very last V on its own.  Keys that one row tile reads leave L2 first, so
       // that tables, parts and instructions stay (trees of 27 drafts x 8192 keys: 40.0
       // us, 43.6 when they are kept).
       static_assert(C::STAGES % 2 == 0, "K / V pairs");
       const uint64_t pol_q = l2_policy_evict_first(), pol_kv =
           p.row_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-      const int box = min(1 << p.cache.shift, kBN), kb = lane % C::KB, part = lane % 16 / C::KB;
+      const int box = min(1 << p.cache.shift, kBN);
       const uint32_t q_bytes = static_cast<uint32_t>(p.half_rows) * C::ROW;
       int ld = 0, nq[2] = {0, 0};
       bool ok = true;
       bool have = take(0, ok, kErrProducer);
       ok = ok && p.fault_skip_kv == 0;
-      // boxes of key tile j of piece x; this lane's box's page
-      auto boxes = [&](const Work& x, int j) { return ceil_div(min(kBN, x.k1 - (x.k0 + j * kBN)), box); };
-      auto page_of = [&](const Work& x, int j, int n) {
-        return part < n ? cache_page(p.cache, x.b, x.k0 + j * kBN + part * box, p.err) : -1;
+      // Pages of a piece's keys, 32 at a time, a lane each (-1: none, or not in the pool);
+      // a tile's are of one window, since both begin at multiples of a tile's pages.
+      auto read_pages = [&](const Work& x, int window) {
+        const int key = ((x.k0 >> p.cache.shift) + window * 32 + lane) << p.cache.shift;
+        return key < x.k1 ? cache_page(p.cache, x.b, key, p.err) : -1;
       };
-      auto ask = [&](const CUtensorMap* tm, int stage, uint32_t bar, const Work& x, int j, int n, int page) {
-        if (part < n)   // (a page that is not in the pool: zeros)
+      // where the first one of key tile j is among the piece's
+      auto entry = [&](const Work& x, int j) { return ((x.k0 + j * kBN) >> p.cache.shift) - (x.k0 >> p.cache.shift); };
+      // boxes of key tile j of piece x
+      auto boxes = [&](const Work& x, int j) { return ceil_div(min(kBN, x.k1 - (x.k0 + j * kBN)), box); };
+      // `n` boxes of key tile j of piece x, a lane each, their pages in lanes `from` on (us,
+      // wide trees with pages of 128, 64, 32, 16 rows: 70, 70, 76, 95, by one lane in turn 72,
+      // 77, 82, 95).  A page that is not in the pool: zeros.
+      const int part = lane / C::KB, kb = lane % C::KB;
+      auto ask = [&](const CUtensorMap* tm, int stage, uint32_t bar, const Work& x, int j, int n, int pages, int from) {
+        const int page = __shfl_sync(0xffffffffu, pages, from + part);
+        if (part < n)
           tma_load_4d_hint(sKV + stage * C::TILE + kb * kBN * 128 + part * box * 128, tm, bar, kb * 64,
-                           (x.k0 + j * kBN + part * box) & ((1 << p.cache.shift) - 1), x.hk, page, pol_kv);
+                           (x.k0 + j * kBN) & ((1 << p.cache.shift) - 1), x.hk, page, pol_kv);
+        __syncwarp();
       };
       auto load_q = [&](const Work& x) {   // once the previous piece's last Q K^T is done
 #pragma unroll
@@ -268,13 +278,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nq[i];
         }
       };
+      // the key tile that is asked for next, j of a piece: its window, and the one behind it
+      int here = -1, ahead = -1, window = 0;
       if (have && ok) {
         const Work& w = pieces[0];
-        const int n = boxes(w, 0), page = page_of(w, 0, n);
+        here = read_pages(w, 0);
+        const int n = boxes(w, 0);
         if (leader) mbar_arrive_expect_tx(bar_full(0), n * box * C::ROW);
         __syncwarp();
-        if (lane < 16) ask(&tm_k, 0, bar_full(0), w, 0, n, page);
-        __syncwarp();
+        ask(&tm_k, 0, bar_full(0), w, 0, n, here, 0);
+        ahead = read_pages(w, 1);
         ld = 1;
         load_q(w);
       }
@@ -288,24 +301,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < C::KB; ++c)
               tma_prefetch_l2_4d(&tm_q, c * 64, wn.hk * share, (wn.rt * (PAIR ? 1 : 2) + i) * rows.tokens, wn.b);
+        const int first = more_units ? read_pages(wn, 0) : -1;   // (used behind this piece's last tile)
         for (int j = 0; j < w.n && ok; ++j) {
           const bool in_unit = j + 1 < w.n, more = in_unit || more_units;
           const int sv = ld % C::STAGES, sk = (ld + 1) % C::STAGES;
           const Work& kw = in_unit ? w : wn;
           const int kj = in_unit ? j + 1 : 0;
           const int nv = boxes(w, j), nk = more ? boxes(kw, kj) : 0;
-          const int page = lane < 16 ? page_of(w, j, nv) : more ? page_of(kw, kj, nk) : -1;
+          // (the values' pages are those of the keys before)
+          const int v_pages = here, v_from = entry(w, j) & 31;
+          if (in_unit) {
+            if (entry(w, kj) >> 5 != window) {
+              ++window;
+              here = ahead;
+              ahead = read_pages(w, window + 1);
+            }
+          } else {
+            window = 0;
+            here = first;
+            ahead = more ? read_pages(wn, 1) : -1;
+          }
           ok = wait_all(bar_empty(sv), ((ld / C::STAGES) & 1) ^ 1, kErrProducer);
           if (ok && more) ok = wait_all(bar_empty(sk), (((ld + 1) / C::STAGES) & 1) ^ 1, kErrProducer);
           if (!ok) break;
           const uint32_t bar = more ? bar_full(sk) : bar_full(sv);
           if (leader) mbar_arrive_expect_tx(bar, (nv + nk) * box * C::ROW);
           __syncwarp();
-          if (lane < 16)
-            ask(&tm_v, sv, bar, w, j, nv, page);
-          else
-            ask(&tm_k, sk, bar, kw, kj, nk, page);
-          __syncwarp();
+          ask(&tm_v, sv, bar, w, j, nv, v_pages, v_from);
+          if (more) ask(&tm_k, sk, bar, kw, kj, nk, here, entry(kw, kj) & 31);
           ld += more ? 2 : 1;
         }
         if (ok && more_units) load_q(wn);
