@@ -28,18 +28,22 @@ __device__ __forceinline__ int cache_count(const PageTable& c, int b, int most, 
   return max(0, min(n, most));
 }
 
-// The page of place `at` (a key's number within its sequence) of sequence b; -1, and
-// the error word says so, where the table has none that the pool has.
-__device__ __forceinline__ int cache_page(const PageTable& c, int b, int64_t at, unsigned int* err) {
+// What the table has for place `at` (a key's number within its sequence) of sequence b,
+// not looked at, so that the load need not have ended; and the page that this is: -1, and
+// the error word says so, where the pool has no such page.
+__device__ __forceinline__ int cache_entry(const PageTable& c, int b, int64_t at, unsigned int* err) {
   const int64_t i = at >> c.shift;
-  int page = -1;
-  if (i < c.width) {
-    const int32_t* from = c.table + b * c.stride + i;
-    if (CPATTN_IN(c.table_span, from, 4, err)) page = *from;
-  }
-  if (page >= 0 && page < c.pages) return page;
+  if (i >= c.width) return -1;
+  const int32_t* from = c.table + b * c.stride + i;
+  return CPATTN_IN(c.table_span, from, 4, err) ? *from : -1;
+}
+__device__ __forceinline__ int cache_checked(const PageTable& c, int entry, unsigned int* err) {
+  if (entry >= 0 && entry < c.pages) return entry;
   atomicOr(err, kErrBounds);
   return -1;
+}
+__device__ __forceinline__ int cache_page(const PageTable& c, int b, int64_t at, unsigned int* err) {
+  return cache_checked(c, cache_entry(c, b, at, err), err);
 }
 
 // Where new token i of sequence b goes (not valid: nowhere).

@@ -72,13 +72,18 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
   while (walk.next(p, w)) {
     if (threadIdx.x == 0) cache_note_unit<R, D>(p, w);
     const int k_begin = w.t0 * kKeys, k_end = min(w.len + w.count, w.t1 * kKeys), tiles = w.t1 - w.t0;
-    // page numbers, 32 at a time, a lane each; the next 32 are read ahead
+    // page numbers, 32 at a time, a lane each; the next 32 are read ahead, and checked
+    // when their turn comes
     const int entry0 = k_begin >> p.cache.shift, in_page = k_begin & ((1 << p.cache.shift) - 1);
+    auto key_of = [&](int window) { return (entry0 + window * 32 + lane) << p.cache.shift; };
     auto read_pages = [&](int window) {
-      const int key = (entry0 + window * 32 + lane) << p.cache.shift;
-      return key < k_end ? cache_page(p.cache, w.b, key, p.err) : -1;
+      return key_of(window) < k_end ? cache_entry(p.cache, w.b, key_of(window), p.err) : -1;
     };
-    int window = 0, here = read_pages(0), ahead = read_pages(1);
+    auto checked = [&](int window, int entry) {
+      return key_of(window) < k_end ? cache_checked(p.cache, entry, p.err) : -1;
+    };
+    const int first = read_pages(0);
+    int window = 0, ahead = read_pages(1), here = checked(0, first);
     // this thread's copies of a stage: chunk c of rows r_first, r_first + RSTEP, ...
     const char* kbase = static_cast<const char*>(p.k.data) + w.hk * p.k.s[1] * 2 + c * 16;
     const char* vbase = static_cast<const char*>(p.v.data) + w.hk * p.v.s[1] * 2 + c * 16;
@@ -87,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) cache_few_kernel(const __grid_consta
         // (a stage's pages are of one window: both begin at multiples of a stage's pages)
         if ((in_page + t * kKeys) >> p.cache.shift >> 5 != window) {
           ++window;
-          here = ahead;
+          here = checked(window, ahead);
           ahead = read_pages(window + 1);
         }
         const uint32_t dst = s0 + (t % C::STAGES) * C::STAGE;

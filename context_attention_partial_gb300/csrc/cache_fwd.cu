@@ -240,11 +240,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       bool have = take(0, ok, kErrProducer);
       ok = ok && p.fault_skip_kv == 0;
-      // Pages of a piece's keys, 32 at a time, a lane each (-1: none, or not in the pool);
-      // a tile's are of one window, since both begin at multiples of a tile's pages.
+      // Pages of a piece's keys, 32 at a time, a lane each; a tile's are of one window, since
+      // both begin at multiples of a tile's pages.  They are read a window ahead, and checked
+      // when their turn comes (-1: no key, or not in the pool).
+      auto key_of = [&](const Work& x, int window) {
+        return ((x.k0 >> p.cache.shift) + window * 32 + lane) << p.cache.shift;
+      };
       auto read_pages = [&](const Work& x, int window) {
-        const int key = ((x.k0 >> p.cache.shift) + window * 32 + lane) << p.cache.shift;
-        return key < x.k1 ? cache_page(p.cache, x.b, key, p.err) : -1;
+        const int key = key_of(x, window);
+        return key < x.k1 ? cache_entry(p.cache, x.b, key, p.err) : -1;
+      };
+      auto checked = [&](const Work& x, int window, int entry) {
+        return key_of(x, window) < x.k1 ? cache_checked(p.cache, entry, p.err) : -1;
       };
       // where the first one of key tile j is among the piece's
       auto entry = [&](const Work& x, int j) { return ((x.k0 + j * kBN) >> p.cache.shift) - (x.k0 >> p.cache.shift); };
@@ -282,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int here = -1, ahead = -1, window = 0;
       if (have && ok) {
         const Work& w = pieces[0];
-        here = read_pages(w, 0);
+        here = checked(w, 0, read_pages(w, 0));
         const int n = boxes(w, 0);
         if (leader) mbar_arrive_expect_tx(bar_full(0), n * box * C::ROW);
         __syncwarp();
@@ -313,12 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (in_unit) {
             if (entry(w, kj) >> 5 != window) {
               ++window;
-              here = ahead;
+              here = checked(w, window, ahead);
               ahead = read_pages(w, window + 1);
             }
           } else {
             window = 0;
-            here = first;
+            here = more ? checked(wn, 0, first) : -1;
             ahead = more ? read_pages(wn, 1) : -1;
           }
           ok = wait_all(bar_empty(sv), ((ld / C::STAGES) & 1) ^ 1, kErrProducer);
