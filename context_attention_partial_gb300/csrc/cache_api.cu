@@ -244,7 +244,9 @@ CachePlan cache_plan(const cpattn_tensor* q, const cpattn_tensor* key_pages, con
   const int64_t B = q->shape[0], H = q->shape[1], S = q->shape[2], D = q->shape[3], Hk = key_pages->shape[1];
   if (B * H * S == 0) return c;
   const int64_t rows = S * (H / Hk);
-  int64_t slots = 2 * static_cast<int64_t>(sm_count());
+  // (blocks of an SM: bf16 with D = 64 has room for three; us, three / two: 4 sequences x
+  // 24 key heads x 16384 keys, one row 66.1 / 77.2, 16 rows in pages of 16 69.5 / 79.8)
+  int64_t slots = (q->dtype == CPATTN_BF16 && D == 64 ? 3 : 2) * static_cast<int64_t>(sm_count());
   if (q->dtype == CPATTN_F32) {
     c.places = rows <= 16 ? 16 : 64;
     c.keys = kCacheF32Keys;

@@ -11,7 +11,7 @@
 // What bounds it is the read of the keys and values, 4 D bytes a key, once per key
 // head: the rows of a tile are the tokens of every query head that shares it.  The
 // key tiles of all sequences are dealt out evenly over the blocks (CacheWalk), two
-// blocks an SM.
+// blocks an SM (D = 64: three).
 //
 // A block of 4 warps walks its keys in stages of 64, three or more in flight by
 // 16-byte asynchronous copies, each from its page; a warp holds 32 page numbers and has
