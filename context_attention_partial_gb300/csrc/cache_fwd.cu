@@ -13,8 +13,8 @@
 // Roles (12 warps): warps 0-7 softmax and output, one thread per row of a 128-row query
 // tile and warpgroup; warp 8 TMA producer; warp 9 MMA issuer; warp 10 cleans the value
 // tiles that hold drafts; warp 11 finds the block's pieces and announces them.  TMEM:
-// S_0 | S_1 | O_0 | O_1, P over S's first columns.  Shared memory: the two Q tiles, a ring of K / V tiles, an output staging area and the
-// paths of a tree's drafts per softmax warp.
+// S_0 | S_1 | O_0 | O_1, P over S's first columns.  Shared memory: the two Q tiles, a ring
+// of K / V tiles, an output staging area and the paths of a tree's drafts per softmax warp.
 //
 // Rows.  A query tile is whole tokens, each with every query head that shares the key
 // head: a TMA box [tokens][heads][64 features].  PAIR: a unit has one query tile, its
@@ -23,9 +23,15 @@
 // unit has two query tiles, which read the same keys.
 //
 // Keys.  A 128-key tile is up to eight pages' boxes; the producer's lanes hold 32 page
-// numbers and have the next 32 on their way.  Scores of keys that a row does not see are masked in registers, by the
-// bits of its path.  Value rows behind the last key are zeroed in shared memory, and so
-// are a draft's values that are not finite (see cache_few.cu), by warp 10.
+// numbers and have the next 32 on their way.  Scores of keys that a row does not see are
+// masked in registers, by the bits of its path.  Value rows behind the last key are
+// zeroed in shared memory, and so are a draft's values that are not finite (see
+// cache_few.cu), by warp 10.
+//
+// Measured, with the join: trees of 27 drafts, 8 sequences of up to 8192 keys, 32 heads on
+// 8, D = 128 (155 MB) 36.5 us, of which the join 6.3; trees of 64, 4 sequences of 16384
+// keys, 24 heads, D = 64 (406 MB) 70 us, 5.8 TB/s; 1024 new tokens behind 16384, 32 heads
+// on 8, D = 128 (283 GFLOP) 175 us, 1620 TFLOP/s, in longer runs 190 under the power cap.
 #include <cmath>
 
 #include "cache.cuh"
@@ -258,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // boxes of key tile j of piece x
       auto boxes = [&](const Work& x, int j) { return ceil_div(min(kBN, x.k1 - (x.k0 + j * kBN)), box); };
       // `n` boxes of key tile j of piece x, a lane each, their pages in lanes `from` on (us,
-      // wide trees with pages of 128, 64, 32, 16 rows: 70, 70, 76, 95, by one lane in turn 72,
-      // 77, 82, 95).  A page that is not in the pool: zeros.
+      // wide trees with pages of 128, 64, 16 rows: 70, 70, 95, by one lane in turn 73, 77,
+      // 95).  A page that is not in the pool: zeros.
       const int part = lane / C::KB, kb = lane % C::KB;
       auto ask = [&](const CUtensorMap* tm, int stage, uint32_t bar, const Work& x, int j, int n, int pages, int from) {
         const int page = __shfl_sync(0xffffffffu, pages, from + part);
