@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_q(w);
       }
       for (int number = 0; have && ok; ++number) {
-        const Work &w = pieces[number % kPieces], &wn = pieces[(number + 1) % kPieces];
         const bool more_units = take(number + 1, ok, kErrProducer);
         if (!ok) break;
+        const Work w = pieces[number % kPieces], wn = pieces[(number + 1) % kPieces];
         // (the next Q tiles into L2 while this piece runs)
         if (more_units && leader)
           for (int i = 0; i < wn.halves; ++i)
@@ -318,9 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < w.n && ok; ++j) {
           const bool in_unit = j + 1 < w.n, more = in_unit || more_units;
           const int sv = ld % C::STAGES, sk = (ld + 1) % C::STAGES;
-          const Work& kw = in_unit ? w : wn;
           const int kj = in_unit ? j + 1 : 0;
-          const int nv = boxes(w, j), nk = more ? boxes(kw, kj) : 0;
+          const int nv = boxes(w, j), nk = in_unit ? boxes(w, kj) : more ? boxes(wn, 0) : 0;
           // (the values' pages are those of the keys before)
           const int v_pages = here, v_from = entry(w, j) & 31;
           if (in_unit) {
@@ -341,7 +340,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (leader) mbar_arrive_expect_tx(bar, (nv + nk) * box * C::ROW);
           __syncwarp();
           ask(&tm_v, sv, bar, w, j, nv, v_pages, v_from);
-          if (more) ask(&tm_k, sk, bar, kw, kj, nk, here, entry(kw, kj) & 31);
+          if (in_unit)
+            ask(&tm_k, sk, bar, w, kj, nk, here, entry(w, kj) & 31);
+          else if (more)
+            ask(&tm_k, sk, bar, wn, 0, nk, here, 0);
           ld += more ? 2 : 1;
         }
         if (ok && more_units) load_q(wn);
