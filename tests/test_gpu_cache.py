@@ -288,6 +288,34 @@ def test_bad_pages(H, dtype):
     check(lse, want[1])
 
 
+@pytest.mark.parametrize("page", [16, 32, 256])
+@pytest.mark.parametrize("H,Hk,S,D", [(24, 24, 40, 64), (32, 16, 30, 128), (24, 24, 3, 64), (16, 16, 2, 128)])
+def test_pieces_of_many_pages(H, Hk, S, D, page):
+    """A block walks more pages than it holds numbers of; one of them, far from the piece's
+    beginning, is not in the pool."""
+    lengths = [2500, 1, 2047, 1300, 2300, 700, 1900, 2222]
+    cache = C.Cache(lengths, None, S, Hk, D, page, BF, DEV, 21, "prhd")
+    q = randn(len(lengths), H, S, D, dtype=BF, seed=22)
+    out, lse = cp.cache_attention(q, cache.key_pages, cache.value_pages, cache.table, cache.lengths_t)
+    assert cp.last_device_status() == OK
+    want = C.attend(q, cache.k, cache.v, cache.lengths, cache.counts)
+    check(out, want[0])
+    check(lse, want[1])
+    table = cache.table.clone()
+    bad = ((0, 2100 // page), (4, 1200 // page))
+    for b, i in bad:
+        table[b, i] = cache.key_pages.shape[0] + b
+    out, lse = cp.cache_attention(q, cache.key_pages, cache.value_pages, table, cache.lengths_t)
+    assert cp.last_device_status() == BOUNDS and cp.last_device_status() == OK
+    k, v = [x.clone() for x in cache.k], [x.clone() for x in cache.v]
+    for b, i in bad:
+        k[b][:, page * i:page * (i + 1)] = 0
+        v[b][:, page * i:page * (i + 1)] = 0
+    want = C.attend(q, k, v, cache.lengths, cache.counts)
+    check(out, want[0])
+    check(lse, want[1])
+
+
 def test_counts_and_lengths_out_of_range():
     cache = C.Cache([20, 20], None, 4, 2, 64, 16, BF, DEV, 7)
     q = randn(2, 4, 4, 64, dtype=BF, seed=14)
