@@ -430,6 +430,19 @@ __device__ __forceinline__ float power2(float x) {
   if constexpr (sizeof(T) == 4) return exp2f(x);
   return ex2_approx(x);
 }
+// The factor f for x, sums of one part.  Where it is 0 (the part's maximum is far below
+// another's, or it has no weight at all) only values that are not finite are left of x, as
+// they are: add_unfinite has put them there for rows that see them, and so they reach the
+// result wherever the border of two parts lies, while 0 times an infinity would be NaN.
+template <int N>
+__device__ __forceinline__ float join_factor(float4 (&x)[N], float f) {
+  if (f != 0.f) return f;
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    x[e] = make_float4(isfinite(x[e].x) ? 0.f : x[e].x, isfinite(x[e].y) ? 0.f : x[e].y, isfinite(x[e].z) ? 0.f : x[e].z,
+                       isfinite(x[e].w) ? 0.f : x[e].w);
+  return 1.f;
+}
 template <int R, int D, typename T, int G>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheParams p, int most) {
   constexpr int I = kJoinThreads / G;   // items of a block
@@ -466,15 +479,15 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
           const float4* o = cache_part<R, D>(p, part, r, d + 4 * e);
           y[e] = CPATTN_IN(p.ws_span, o, 16, p.err) ? *o : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (a.y == 0.f) continue;   // (no key of this part)
         const float top = fmaxf(m, a.x), base = top == -INFINITY ? 0.f : top;
         const float f0 = power2<T>(m - base), f1 = power2<T>(a.x - base);
         m = top;
         l = l * f0 + a.y * f1;
+        const float g0 = join_factor(sum, f0), g1 = join_factor(y, f1);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          sum[e] = make_float4(sum[e].x * f0 + y[e].x * f1, sum[e].y * f0 + y[e].y * f1, sum[e].z * f0 + y[e].z * f1,
-                               sum[e].w * f0 + y[e].w * f1);
+          sum[e] = make_float4(sum[e].x * g0 + y[e].x * g1, sum[e].y * g0 + y[e].y * g1, sum[e].z * g0 + y[e].z * g1,
+                               sum[e].w * g0 + y[e].w * g1);
       }
     if constexpr (G == 1) {
       if (row >= 0 && d < D)
@@ -508,11 +521,10 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
 #pragma unroll
     for (int k = 0; k < G; ++k) {
       const float2 a = part_ml[k][it];
-      if (a.y == 0.f) continue;
-      const float f = power2<T>(a.x - base);
+      float4 y[1] = {make_float4(part_sums[k][e][it], part_sums[k][e + 1][it], part_sums[k][e + 2][it], part_sums[k][e + 3][it])};
+      const float f = power2<T>(a.x - base), g = join_factor(y, f);
       l = fmaf(f, a.y, l);
-      sum = make_float4(fmaf(f, part_sums[k][e][it], sum.x), fmaf(f, part_sums[k][e + 1][it], sum.y),
-                        fmaf(f, part_sums[k][e + 2][it], sum.z), fmaf(f, part_sums[k][e + 3][it], sum.w));
+      sum = make_float4(fmaf(g, y[0].x, sum.x), fmaf(g, y[0].y, sum.y), fmaf(g, y[0].z, sum.z), fmaf(g, y[0].w, sum.w));
     }
     cache_write_row<T>(p, b, hk * share + row % share, row / share, d, sum, m, l);
   }

@@ -470,6 +470,9 @@ cpattn_status cpattn_cache_append(const cpattn_tensor* q, const cpattn_tensor* k
  *     that may overlap need their own.
  * Places that no query of a sequence sees are not used and may hold anything; a draft
  * that is not above a query has no part in its result, NaN and infinities included.
+ * An infinite value that a query sees makes its feature infinite (NaN beside one of the
+ * other sign).  Where its weight is below 2^-126 of the row's largest it may give NaN
+ * instead (0 times an infinity), unless it is one of several drafts of a tree.
  * fp32 inputs are computed in fp32.  bf16 inputs: scores, sums and lse are fp32; each
  * weight exp(s - max) is rounded to bf16 once for its product with v, and out once (the
  * bound is cpattn_cross_attention's).  Equal calls give equal bits.  Strides of
