@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar_dirty, 1);
     mbar_init(bar_clean, 1);
     for (int i = 0; i < kPieces; ++i) {
+      pieces[i].n = 0;
       mbar_init(bar_piece(i), 1);
       mbar_init(bar_done(i), 9);   // softmax warps, cleaner
     }
@@ -218,9 +219,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool r = mbar_wait(bar, parity, abort_flag, p.timeout_ns + tiles * 50000, p.err, code);
     return __all_sync(0xffffffffu, r) != 0;
   };
-  // Piece `number` of this block, once announced; false: no more, or a wait ran out (ok).
+  // Key tiles of piece `number`'s place in the ring.  (The walk may be writing the next
+  // piece there: then the one before has ended, and either number will do.)
+  auto tiles_at = [&](int number) -> int { return *const_cast<const volatile int*>(&pieces[number % kPieces].n); };
+  // Of all pieces announced and not known to have ended: a role with nothing to do in some
+  // runs ahead of the others, and then waits for them.
+  auto tiles_ahead = [&]() {
+    long long tiles = 0;
+    for (int i = 0; i < kPieces; ++i) tiles += tiles_at(i);
+    return tiles;
+  };
+  // Piece `number` of this block, once announced, which is when piece number - kPieces has
+  // ended; false: no more, or a wait ran out (ok).
   auto take = [&](int number, bool& ok, unsigned code) {
-    ok = wait_all(bar_piece(number % kPieces), (number / kPieces) & 1, code);
+    ok = wait_long(bar_piece(number % kPieces), (number / kPieces) & 1, tiles_at(number), code);
     return ok && pieces[number % kPieces].n != 0;
   };
 
@@ -525,12 +537,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       walk.start(p);
       for (int number = 0;; ++number) {
         const Work w = next_work<PAIR>(p, walk);
-        if (number >= kPieces) {
-          // (some pieces may have to end, which takes as long as their tiles)
-          long long tiles = 0;
-          for (int i = 0; i < kPieces; ++i) tiles += pieces[i].n;
-          if (!wait_long(bar_done(number % kPieces), (number / kPieces - 1) & 1, tiles, kErrWalk)) break;
-        }
+        // (some pieces may have to end, which takes as long as their tiles)
+        if (number >= kPieces &&
+            !wait_long(bar_done(number % kPieces), (number / kPieces - 1) & 1, tiles_ahead(), kErrWalk))
+          break;
         if (leader) {
           if (w.n != 0) cache_note_unit<R, D>(p, w);
           pieces[number % kPieces] = w;
@@ -549,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = w.n;
         g += min(w.drafts, n);
         for (int j = w.drafts; j < n; ++j, ++g) {
-          ok = wait_long(bar_dirty, nd & 1, j + kPieces, kErrClean);
+          ok = wait_long(bar_dirty, nd & 1, tiles_ahead(), kErrClean);
           if (!ok) break;
           ++nd;
           const int start = w.k0 + j * kBN, valid = min(kBN, w.k1 - start);
@@ -598,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = quarter * 32 + lane;                 // this thread's row of its query tile
     const int row_token = rows.token(x);
     int ns = 0, no[2] = {0, 0};
-    bool ok = true;
+    bool ok = true, ahead = false;
     // First a piece of nothing: a tile of whatever tensor memory holds, of which nothing
     // is kept.  A launch finds this loop's instructions in HBM, and so they arrive while
     // the kernel before this one ends and the first keys are on their way.
@@ -640,6 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       const int first = PAIR ? wg : 0;
+      // (the second group has no part in pieces with one query tile, and is ahead of them)
+      if (ahead && mine) wait_long(bar_s(wg), ns & 1, tiles_ahead(), kErrSoftmax);
+      ahead = !mine;
       for (int j = first; mine && j < w.n; j += PAIR ? 2 : 1) {
         ok = wait_all(bar_s(wg), ns & 1, kErrSoftmax);
         if (!ok) break;
