@@ -489,7 +489,8 @@ def norm_rotary_backward(xs, weights, positions: torch.Tensor, axes_dims: Sequen
     """Gradient of ``norm_rotary`` (cpattn_norm_rotary_backward): its arguments, and dys,
     the gradients of its results.  Returns (dxs, dweights): a tensor or list each like xs
     and weights (dweights None if weights is); a weight's gradient is summed over every
-    token and head, in its type.  dxs may be xs or dys (in place)."""
+    token and head, in its type.  dxs may be xs or dys (in place); dweights are refused
+    without weights."""
     at = _lib.load().addresses
     single = isinstance(xs, torch.Tensor)
     if single:
@@ -516,7 +517,8 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, key_pages: torch.Tensor, valu
     many of the S tokens a sequence has (None: all).  k and q are normed with weight and
     q_weight [D] as ``norm_rotary`` does (None: no norm) and turned to positions f32
     [S,A] or [B,S,A] as ``rotary`` does (None: not turned); v is copied.  Tokens from
-    counts[b] on are not written.  Returns the queries (q_out may be q), or None."""
+    counts[b] on are not written.  Returns the queries (q_out may be q, and is refused
+    without one), or None."""
     lib = _lib.load()
     status, out = _lib.binding().cache_append(
         lib.addresses["cache_append"], k, v, key_pages, value_pages, page_table, lengths, positions, axes_dims, q, counts,

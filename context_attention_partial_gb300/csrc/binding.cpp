@@ -427,7 +427,9 @@ PyObject* norm(PyObject* const* a, bool backward) {
   if (given_out != Py_None && !sequence_of(outs, n, "outputs")) return nullptr;
   Owned dys(backward ? PySequence_Fast(r[0], "dys is a sequence of tensors") : nullptr);
   if (backward && !sequence_of(dys, n, "gradients")) return nullptr;
-  PyObject* const given_dw = backward && weighted ? r[2] : Py_None;
+  PyObject* const given_dw = backward ? r[2] : Py_None;
+  if (!weighted && given_dw != Py_None)   // (nothing would write them)
+    return Py_BuildValue("iOO", static_cast<int>(CPATTN_ERR_NULL), Py_None, Py_None);
   Owned dws(given_dw != Py_None ? PySequence_Fast(given_dw, "dweights is a sequence of tensors") : nullptr);
   if (given_dw != Py_None && !sequence_of(dws, n, "gradients of weights")) return nullptr;
   const float eps = static_cast<float>(PyFloat_AsDouble(a[3 + b]));
@@ -526,6 +528,8 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t count) {
                               cpattn_tensor*, cpattn_tensor*, const cpattn_tensor*, const cpattn_tensor*,
                               const cpattn_tensor*, cpattn_tensor*, void*);
   const Fn fn = reinterpret_cast<Fn>(PyLong_AsVoidPtr(a[0]));
+  if (a[9] == Py_None && a[16] != Py_None)   // (nothing would write q_out)
+    return Py_BuildValue("iO", static_cast<int>(CPATTN_ERR_NULL), Py_None);
   const Axes axes(a[8]);
   if (!axes.ok) return nullptr;
   if (axes.shape_error) return Py_BuildValue("iO", static_cast<int>(CPATTN_ERR_SHAPE), Py_None);

@@ -308,7 +308,7 @@ cpattn_status cpattn_norm_rotary_backward(int n, const cpattn_tensor* x, const c
   bool run = false;
   cpattn_status st = norm_common(n, x, weights, eps, positions, axes, axis_dims, theta, interleaved, dx, &p, &run);
   if (st != CPATTN_OK) return st;
-  if (!dy || (weights && !dweights)) return CPATTN_ERR_NULL;
+  if (!dy || !weights != !dweights) return CPATTN_ERR_NULL;
   const int64_t B = p.batch, S = p.seq, D = p.head_dim;
   const long long shrink = g_check_shrink.load();
   for (int i = 0; i < n; ++i) {
@@ -344,7 +344,7 @@ cpattn_status cpattn_cache_append(const cpattn_tensor* q, const cpattn_tensor* k
                                   int interleaved, cpattn_tensor* key_pages, cpattn_tensor* value_pages,
                                   const cpattn_tensor* page_table, const cpattn_tensor* lengths,
                                   const cpattn_tensor* counts, cpattn_tensor* q_out, void* stream) {
-  if (!k || !v || (q && !q_out)) return CPATTN_ERR_NULL;
+  if (!k || !v || !q != !q_out) return CPATTN_ERR_NULL;
   NormParams p;
   std::memset(&p, 0, sizeof(p));
   // (queries first: where the keys go takes a while to find)
