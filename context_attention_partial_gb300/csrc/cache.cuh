@@ -111,8 +111,14 @@ __device__ __forceinline__ int cache_row(const CacheParams& p, int rt, int r) {
 // 32: 16 rows x 3000 keys 18.2 with 3, 20.7 with 1; 64 rows x 700 keys 20.4 with 3,
 // 15.7 with 1).
 constexpr int cache_min_tiles(int places, int keys) { return keys >= 64 ? 2 : places > 16 ? 1 : 3; }
-// Units a block above which none are split: then a round of whole units is at most
-// an eighth of the call, and the tables that a split needs would be long.
+// Units a block from which none are split: every block walks over all pairs of sequence
+// and row tile to find its stretch, and a split needs tables of the units.  Of equal units
+// a round is then at most an eighth of the call; but they are dealt out by number, whatever
+// their lengths are, and with unequal ones the busiest block sets the time.  Measured on
+// both sides, 8 key heads (us, those of the bytes in brackets; split / whole): one token,
+// lengths spread by their logarithm over 100 to 16384, 303 sequences 587 (590) / 304 895
+// (590); one of 32768 keys among others of 1000, 303 218 (203) / 512 737 (329); all of
+// 3100, 300 564 (563) / 512 928 (960); trees of 27, spread, 151 309 (259) / 152 435 (259).
 constexpr int kCacheWholeUnits = 8;
 
 // A piece of work: key tiles t0 .. t1 of row tile rt of (b, hk), which has `tiles`.
@@ -420,9 +426,10 @@ __device__ __forceinline__ void cache_write_part(const CacheParams& p, int64_t p
 // G threads share an item's parts out, so that all of them are on the way at once,
 // and meet in shared memory.  `most`: blocks of the attention's launch.
 constexpr int kJoinThreads = 256;
-// Items an SM from which a thread has an item's parts to itself (us, from 1024 / never:
-// 1024 new tokens x 17408 keys 176.9 / 178.5, 2048 tokens from an empty cache 47.8 / 49.1;
-// from 300: trees of 27 x 8192 keys 40.0, 36.6 from 1024).
+// Items an SM from which a thread has an item's parts to itself (us, from 1024 / never, best
+// and median of three runs in turn: 1024 new tokens x 17408 keys 177.7, 184.3 / 178.6, 185.8,
+// 2048 tokens from an empty cache 47.8, 51.3 / 49.0, 54.2; from 300: trees of 27 x 8192 keys
+// 40.0, 36.6 from 1024).
 constexpr int64_t kJoinItems = 1024;
 // 2^x: fp32 results take the accurate one.
 template <typename T>

@@ -10,8 +10,10 @@
 // rows use all banks.  What bounds it is shared memory's reads: RT + 4 a thread for 4 RT
 // products of four features, so RT = 4 where there are more than 16 rows.
 //
-// Measured: 13 drafts of 3 sequences of up to 700 keys, 8 heads on 2, D = 64, 15.7 us,
-// which is two launches' starts, a few key tiles and the join in series.
+// Measured: 13 drafts of 3 sequences of up to 700 keys, 8 heads on 2, D = 64, 15.5 to 17
+// us (14.0 in a replayed graph), which is two launches' starts, a few key tiles and the
+// join in series; 32 tokens of 3 sequences of up to 4000 keys, 16 heads on 4, D = 64 64 us,
+// 14 TFLOP/s; 512 tokens behind 4096, 8 heads on 2, D = 128 257 us, 36 TFLOP/s.
 #include <cuda_runtime.h>
 
 #include <cmath>

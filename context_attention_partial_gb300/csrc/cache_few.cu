@@ -13,15 +13,16 @@
 // key tiles of all sequences are dealt out evenly over the blocks (CacheWalk), two
 // blocks an SM (D = 64: three).
 //
-// A block of 4 warps walks its keys in stages of 64, three or more in flight by
-// 16-byte asynchronous copies, each from its page; a warp holds 32 page numbers and has
-// the next 32 on their way.  MT = 1 tile of 16 rows, whose 4 warps share a stage's keys
+// A block of 4 warps walks its keys in stages of 64, two of them (D = 64: three) on their
+// way by 16-byte asynchronous copies while one is read, each row from its page; a warp
+// holds 32 page numbers and has the next 32 on their way.  MT = 1 tile of 16 rows, whose 4 warps share a stage's keys
 // and are joined at the end, or 4 (more than 128 query heads a key head, which the
 // tensor cores' tiles do not hold), a warp each.
 //
 // Measured, both launches: single tokens of 8 sequences of up to 16384 keys, 32 heads on
-// 8, D = 128 (302 MB) 54 us, 5.6 TB/s; of 4 sequences of 16384 keys, 24 heads, D = 64
-// (403 MB) 66 us, 6.1 TB/s; of one sequence of 1000 keys 10.2 us.
+// 8, D = 128 (302 MB) 53 us, 5.7 TB/s; of 4 sequences of 16384 keys, 24 heads, D = 64
+// (403 MB) 66 us, 6.1 TB/s; of one sequence of 1000 keys 9.7 to 11 us, 8.6 in
+// a replayed graph.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

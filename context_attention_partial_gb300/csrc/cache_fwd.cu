@@ -29,9 +29,9 @@
 // cache_few.cu), by warp 10.
 //
 // Measured, with the join: trees of 27 drafts, 8 sequences of up to 8192 keys, 32 heads on
-// 8, D = 128 (155 MB) 36.5 us, of which the join 6.3; trees of 64, 4 sequences of 16384
+// 8, D = 128 (155 MB) 36.8 us, of which the join 6.3; trees of 64, 4 sequences of 16384
 // keys, 24 heads, D = 64 (406 MB) 70 us, 5.8 TB/s; 1024 new tokens behind 16384, 32 heads
-// on 8, D = 128 (283 GFLOP) 175 us, 1620 TFLOP/s, in longer runs 190 under the power cap.
+// on 8, D = 128 (283 GFLOP) 178 us, 1590 TFLOP/s, in longer runs 184 to 192 under the power cap.
 #include <cmath>
 
 #include "cache.cuh"
@@ -851,7 +851,7 @@ cudaError_t launch_typed(const CacheMaps& m, const CacheParams& p, int blocks, c
   cudaError_t e = cross_set_up(kernel, Cfg<D>::SMEM, ready, kLaunchRegs);
   if (e != cudaSuccess) return e;
   e = launch_behind(kernel, dim3(blocks), kThreads, Cfg<D>::SMEM, stream, m.q, m.k, m.v, p);
-    if (e != cudaSuccess || !p.split) return e;
+  if (e != cudaSuccess || !p.split) return e;
   return cache_join<PAIR ? 128 : 256, D, __nv_bfloat16>(p, blocks, stream);
 }
 

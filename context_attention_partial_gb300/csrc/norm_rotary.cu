@@ -18,9 +18,10 @@
 // short one waits for its first instructions, which also come from HBM, so the code is
 // kept short, and a block's sines and cosines are formed in one loop, to shared memory.
 //
-// Measured: q and k of 24 heads, bf16, D = 128, 4608 tokens (113 MB) 23.6 us, 4.8 TB/s;
-// the gradient at 32768 tokens (1.21 GB) 187 us, 6.5 TB/s; four prompts of up to 4001
-// tokens, 48 heads, to a cache (336 MB) 57 us, 5.9 TB/s.
+// Measured: q and k of 24 heads, bf16, D = 128, 4608 tokens (113 MB) 21.4 us, 5.3 TB/s, in runs
+// of 60 calls, 23.8 in shorter ones; the gradient at 32768 tokens (1.21 GB) 187 us, 6.5 TB/s,
+// in fp32 (2.42 GB) 357 us, 6.8 TB/s; four prompts of up to 4001 tokens, 48 heads, to a cache
+// (336 MB) 58 to 59 us, 5.7 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -86,8 +87,8 @@ __device__ __forceinline__ uint4 from_pairs(const f2 (&x)[2], float) {
   return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
 }
 
-// How a kernel lays a block out: rows of L lanes, V vectors a lane, U rows at a time, P
-// such steps of each input on their way.
+// How a kernel lays a block out: rows of L lanes, V vectors a lane, U rows at a time, and a
+// ring of P such steps of each input, of which P - 1 are on their way.
 template <typename T, int L, int V, int INPUTS>
 struct Shape {
   static constexpr int N = Vec<T>::N;
@@ -676,8 +677,8 @@ int lanes(InDtype dt, int head_dim) {
 }
 
 // Blocks of an SM, forward (registers: see the kernels' launch bounds; interleaved pairs
-// with 4 blocks and 5: 4608 tokens x 48 heads 21.4 and 23.6 us; halves, 16004 tokens x
-// 48 heads to a cache: 61.7 and 58.8).
+// with 4 blocks and 5, in turn three times, runs of 60 calls: 4608 tokens x 48 heads 21.3 and
+// 23.5 us; halves, 16004 tokens x 48 heads to a cache: 67.0 and 59.1; no run 0.3 off).
 int blocks_of_sm(InDtype dt, const NormParams& p) {
   return p.interleaved || p.rotary_pairs == 0 || (dt == InDtype::F32 && p.head_dim > 128) ? 4 : 5;
 }

@@ -1,6 +1,7 @@
-// rotary_turns.cuh -- what the kernels that turn features to positions share:
-// 16-byte vectors of a row, and a thread's cosines and sines (the angles'
-// arithmetic and its error: rotary.cu).
+// rotary_turns.cuh -- what turns features to positions: the size of a row's vectors and a
+// pair's cosine and sine (the angles' arithmetic and its error: rotary.cu), which rotary.cu
+// and norm_rotary.cu use; vectors in fp32 and a thread's turns in registers, which rotary.cu
+// does (norm_rotary.cu has packed pairs, and a block's turns in shared memory).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

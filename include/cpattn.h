@@ -473,6 +473,12 @@ cpattn_status cpattn_cache_append(const cpattn_tensor* q, const cpattn_tensor* k
  * An infinite value that a query sees makes its feature infinite (NaN beside one of the
  * other sign).  Where its weight is below 2^-126 of the row's largest it may give NaN
  * instead (0 times an infinity), unless it is one of several drafts of a tree.
+ * Work is shared out evenly, whatever the lengths are, while a call has fewer than 8
+ * units (a row tile of one key head of a sequence) for each block that runs at once: fp32,
+ * and bf16 with at most 16 rows a key head, have tiles of 16 or 64 rows and 2 blocks an SM
+ * (bf16 with D = 64: 3); bf16 with more rows 128 or 256 and one.  From there on units are
+ * dealt out whole: measured 1.5 to 2.2 times the time of their bytes where the lengths of
+ * a batch are far apart, which two smaller calls do not take.
  * fp32 inputs are computed in fp32.  bf16 inputs: scores, sums and lse are fp32; each
  * weight exp(s - max) is rounded to bf16 once for its product with v, and out once (the
  * bound is cpattn_cross_attention's).  Equal calls give equal bits.  Strides of
